@@ -507,6 +507,99 @@ int moe_backward_e4m3(moe_ctx* ctx, const void* dO, const void* X, const void* W
                       float* dlogits, float* dW_r, void* ws, size_t ws_bytes, moe_stream_t stream);
 
 /*
+ * Around the layer.  The calls below serve the pre-norm block that holds the layer; the pages describe none of
+ * them, they are additions of this library.
+ *
+ * moe_add_rmsnorm — residual addition, root-mean-square norm and, optionally, the normed rows as e4m3 codes with
+ * their scales, in the layouts the FP8 forwards read.  For every row t of T and column j of d:
+ *
+ *   h[t,j] = residual[t,j] + x[t,j]          rounded to the residual stream's type (bf16, or fp32 with
+ *                                            residual_fp32 != 0); x == NULL: h = residual
+ *   rstd[t] = 1 / sqrt(mean_j h[t,j]^2 + eps)
+ *   y[t,j]  = h[t,j] * rstd[t] * weight[j]   in fp32, stored as bf16
+ *
+ * q_form 0: no codes.  1: scales [T] fp32 = max_j |y[t,j]| / 448 (1 for a zero row), q [T,d] = e4m3(y / scale).
+ * 2: scales [T][moe_mx_sf_cols(d)] bytes and q as moe_quantize_rows_mx.  Both quantize the fp32 y (not its bf16
+ * rounding) by the rules of moe_quantize_rows_e4m3 / moe_quantize_rows_mx.
+ *
+ * x [T,d] bf16; weight [d] bf16, or fp32 with weight_fp32 != 0; h has the stream's type, y is bf16.  Row strides
+ * (ld_*, in elements, >= d) are free; columns are contiguous.  h may be the residual itself and y may be x (every
+ * element is read before it is written).  NULL allowed: x, h (when x is NULL), rstd, and y (when codes are asked
+ * for).  1 <= d <= 16384 and any T >= 0 (T = 0 does nothing); d a multiple of 64 and rows 16-byte aligned with codes,
+ * else any alignment of the type (vector accesses need d % 8 == 0 and 16-byte aligned rows).  eps >= 0.
+ * Squares are summed in fp32: |h| up to about 1e18.  MOE_ERR_INVALID_ARG on a violated rule.
+ */
+int moe_add_rmsnorm(moe_ctx* ctx, const void* x, long long ld_x, const void* residual, long long ld_residual,
+                    int residual_fp32, const void* weight, int weight_fp32, long long T, int d, float eps, void* h,
+                    long long ld_h, void* y, long long ld_y, float* rstd, int q_form, void* q, void* scales,
+                    moe_stream_t stream);
+
+/*
+ * moe_add_rmsnorm_backward — the gradients of moe_add_rmsnorm for an upstream gradient dy of y and, along the residual
+ * stream, dh of h (NULL: none).  With xhat = h rstd:
+ *
+ *   dresidual[t,j] = dx[t,j] = dh[t,j] + rstd[t] (weight[j] dy[t,j] - xhat[t,j] mean_i(weight[i] dy[t,i] xhat[t,i]))
+ *   dweight[j] = sum_t dy[t,j] xhat[t,j]
+ *
+ * dy, dx bf16; h, dh, dresidual of the stream's type; rstd as the forward wrote it; dweight [d] fp32.  dx and
+ * dresidual hold the same values in two types: either may be NULL.  dx or dresidual may be dh or dy.  Shape and
+ * alignment rules as the forward without codes.  T = 0 sets dweight to zero.  ws: caller-owned, 256-byte aligned, at
+ * least moe_add_rmsnorm_workspace_bytes(T, d) bytes (0 on a bad shape).  Sums run in a fixed order.
+ */
+size_t moe_add_rmsnorm_workspace_bytes(long long T, int d);
+int moe_add_rmsnorm_backward(moe_ctx* ctx, const void* dy, long long ld_dy, const void* h, long long ld_h,
+                             int residual_fp32, const void* weight, int weight_fp32, const float* rstd, const void* dh,
+                             long long ld_dh, long long T, int d, void* dx, long long ld_dx, void* dresidual,
+                             long long ld_dresidual, float* dweight, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * moe_balance_loss — the router's balance loss and z loss over the sequences of a packed batch, the per-expert counts
+ * and, with dlogits, the gradient of the logits, in one pass over them.  Sequence b holds the tokens
+ * [seq_offsets[b], seq_offsets[b+1]) (seq_offsets NULL: one sequence, B = 1); a token with mask[t] == 0 does not
+ * count (mask NULL: all count).  With n_b the counted tokens of sequence b, n their sum, B' the sequences with
+ * n_b > 0, p[t] = softmax(logits[t]) and lse[t] = log sum_e exp(logits[t,e]):
+ *
+ *   counts[b,e] = #{(t, k) in b : topk_ids[t,k] = e},  probs[b,e] = 1/n_b sum_{t in b} p[t,e]  (0 for n_b = 0)
+ *   loss[1] = 1/B' sum_b sum_e E counts[b,e] / (K n_b) probs[b,e]
+ *   loss[2] = 1/n sum_t lse[t]^2
+ *   loss[0] = balance_coef loss[1] + z_coef loss[2]
+ *   dlogits[t,e] = dloss * d loss[0] / d logits[t,e]  (0 for a token that does not count)
+ *
+ * (the counts are constants of the gradient).  dloss: a device scalar, NULL for 1.  A balanced load has
+ * loss[1] = 1.  A logit may be -infinity (its probability is 0); a token with none above that adds to the counts
+ * alone.  No counted token: losses, probabilities and gradients are 0.
+ * logits, dlogits [T,E] fp32; topk_ids [T,K] int32 (an id outside [0, E) records MOE_DEV_BAD_EXPERT and is not
+ * counted); mask [T] bytes; seq_offsets [B+1] int32 (not from 0 to T without falling: MOE_DEV_BAD_OFFSETS, the
+ * results are then undefined); counts [B,E] int32, probs [B,E] fp32, loss [3] fp32.  1 <= E <= 1024, 1 <= K <= E,
+ * T * K and B * E below 2^31, T = 0 allowed.  ws: caller-owned, 256-byte aligned, at least
+ * moe_balance_loss_workspace_bytes(T, E, B) bytes (0 on bad sizes).  One cooperative launch (grid barriers bounded by
+ * moe_set_wait_timeout; one that gives up records MOE_DEV_TIMEOUT).  Sums run in a fixed order.
+ */
+size_t moe_balance_loss_workspace_bytes(long long T, int E, int B);
+int moe_balance_loss(moe_ctx* ctx, const float* logits, const int32_t* topk_ids, const uint8_t* mask,
+                     const int32_t* seq_offsets, long long T, int E, int K, int B, float balance_coef, float z_coef,
+                     const float* dloss, float* loss, int32_t* counts, float* probs, float* dlogits, void* ws,
+                     size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * moe_router_backward — carries an additional gradient of the router logits (a loss on them, such as
+ * moe_balance_loss) on to the layer's input and the router's weight; moe_backward has its own:
+ *
+ *   dX[t,i]   = dX_in[t,i] + sum_e dlogits[t,e] W_r[i,e]        (bf16; dX_in NULL: 0)
+ *   dW_r[i,e] = dW_r_in[i,e] + sum_t X[t,i] dlogits[t,e]        (fp32; dW_r_in NULL: 0)
+ *
+ * dlogits [T,E] fp32 enters the first product rounded to bf16 and the second as a bf16 high part plus the bf16
+ * rounding of the rest (as in moe_backward); fp32 accumulation.  X, dX_in, dX [T,d], W_r [d,E] bf16; dW_r_in, dW_r
+ * [d,E] fp32; an output may be its own input.  dX or dW_r may be NULL (that product is skipped).  T <= 65536 (0
+ * allowed), d a multiple of 64, E a multiple of 8 up to 1024, 16-byte aligned.  ws: caller-owned, 256-byte aligned,
+ * at least moe_router_backward_workspace_bytes(T, d, E) bytes (0 on bad sizes).
+ */
+size_t moe_router_backward_workspace_bytes(int T, int d, int E);
+int moe_router_backward(moe_ctx* ctx, const float* dlogits, const void* X, const void* W_r, int T, int d, int E,
+                        const void* dX_in, const float* dW_r_in, void* dX, float* dW_r, void* ws, size_t ws_bytes,
+                        moe_stream_t stream);
+
+/*
  * Per-kernel timing (tracing).  With profiling enabled, every kernel the
  * library launches is bracketed by a CUDA event pair on its stream (events
  * come from a pool created by the first moe_profile_enable).  moe_profile_read

@@ -14,6 +14,7 @@ index) are readings of a rule the pages state only in words; the brute-force
 pin checks the oracle against that reading, not against the pages' own
 (absent) algorithm listing.
 """
+from . import block_oracle  # noqa: F401
 from .moe_oracle import (  # noqa: F401
     Routing,
     bf16_bits_to_f64,

@@ -32,7 +32,9 @@ EXPORTS = (
     "moe_expert_capacity", "moe_test_gemm_varlen_k_dual", "moe_test_gemm_varlen_m_dual",
     "moe_mx_sf_cols", "moe_mx_weight_sf_bytes", "moe_mx_act_sf_bytes", "moe_quantize_rows_mx",
     "moe_quantize_weights_mx", "moe_grouped_gemm_fwd_mx", "moe_quantize_bwd_weights_mx", "moe_backward_mx",
-    "moe_mx_dw_ws_bytes",
+    "moe_mx_dw_ws_bytes", "moe_add_rmsnorm", "moe_add_rmsnorm_workspace_bytes", "moe_add_rmsnorm_backward",
+    "moe_balance_loss", "moe_balance_loss_workspace_bytes", "moe_router_backward",
+    "moe_router_backward_workspace_bytes",
 )
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA, MOE_ERR_DEVICE, MOE_ERR_DEVICE_TIMEOUT = range(6)
@@ -43,6 +45,7 @@ _P = ctypes.c_void_p
 _I = ctypes.c_int
 _LL = ctypes.c_longlong
 _SZ = ctypes.c_size_t
+_F = ctypes.c_float
 
 
 def lib() -> ctypes.CDLL:
@@ -107,6 +110,17 @@ def lib() -> ctypes.CDLL:
         L.moe_backward_mx.argtypes = [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _LL, _P, _P,
                                       _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _P, _P, _P, _P,
                                       _SZ, _P, _SZ, _P]
+        L.moe_add_rmsnorm.argtypes = [_P, _P, _LL, _P, _LL, _I, _P, _I, _LL, _I, _F, _P, _LL, _P, _LL, _P, _I, _P, _P, _P]
+        L.moe_add_rmsnorm_workspace_bytes.argtypes = [_LL, _I]
+        L.moe_add_rmsnorm_workspace_bytes.restype = _SZ
+        L.moe_add_rmsnorm_backward.argtypes = [_P, _P, _LL, _P, _LL, _I, _P, _I, _P, _P, _LL, _LL, _I, _P, _LL, _P, _LL,
+                                               _P, _P, _SZ, _P]
+        L.moe_balance_loss_workspace_bytes.argtypes = [_LL, _I, _I]
+        L.moe_balance_loss_workspace_bytes.restype = _SZ
+        L.moe_balance_loss.argtypes = [_P, _P, _P, _P, _P, _LL, _I, _I, _I, _F, _F, _P, _P, _P, _P, _P, _P, _SZ, _P]
+        L.moe_router_backward_workspace_bytes.argtypes = [_I, _I, _I]
+        L.moe_router_backward_workspace_bytes.restype = _SZ
+        L.moe_router_backward.argtypes = [_P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P, _P, _SZ, _P]
         L.moe_profile_enable.argtypes = [_P, _I]
         L.moe_profile_read.argtypes = [_P, _I, ctypes.c_char_p, ctypes.POINTER(ctypes.c_double),
                                        ctypes.POINTER(_LL), ctypes.POINTER(_I)]
@@ -435,6 +449,161 @@ def moe_backward_e4m3(ctx, dO, X, W_r, W_gate, W_up, W_down, Wgu_q, wgu_scale, W
         _ptr(HUq, torch.uint8), _ptr(hu_scale, f32), _ptr(dOq, torch.uint8), _ptr(do_scale, f32), _ptr(dX, bf),
         _ptr(dW_gate), _ptr(dW_up), _ptr(dW_down), dw_fp32, _ptr(dS, f32), _ptr(dlogits, f32), _ptr(dW_r, f32), wp,
         wb, _stream(stream)))
+
+
+# ------------------------------------------------------------------ around the layer
+
+
+def _rows(ctx, t: torch.Tensor | None, shape, dtype, name):
+    """(pointer, row stride) of a [T, d] tensor whose columns are contiguous; (None, 0) for None."""
+    if t is None:
+        return None, 0
+    if t.dtype != dtype or t.get_device() != ctx.device or t.shape != shape:
+        raise ValueError(f"{name} must be a {tuple(shape)} {dtype} tensor on CUDA device {ctx.device}, got "
+                         f"{tuple(t.shape)} {t.dtype} on {t.device}")
+    ld, one = t.stride()
+    if (one != 1 and shape[1] > 1) or (ld < shape[1] and shape[0] > 1):
+        raise ValueError(f"{name} must have contiguous columns and rows that do not overlap, got strides {t.stride()}")
+    return t.data_ptr(), max(ld, shape[1])
+
+
+def _flat(ctx, t: torch.Tensor | None, shape, dtype, name):
+    """Pointer of a contiguous tensor of the given shape; None for None."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.get_device() != ctx.device or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {tuple(shape)} {dtype} tensor on CUDA device {ctx.device}, got "
+                         f"{tuple(t.shape)} {t.dtype} on {t.device}")
+    return t.data_ptr()
+
+
+def _scratch(ctx, ws: torch.Tensor):
+    """(pointer, bytes) of a workspace."""
+    if ws.get_device() != ctx.device or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous tensor on CUDA device {ctx.device}")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _stream_type(t: torch.Tensor, name):
+    """1 for an fp32 tensor, 0 for bf16."""
+    if t.dtype == torch.float32:
+        return 1
+    if t.dtype == torch.bfloat16:
+        return 0
+    raise ValueError(f"{name} must be bf16 or fp32, got {t.dtype}")
+
+
+def moe_add_rmsnorm(ctx, x, residual, weight, eps, h, y, rstd=None, q=None, scales=None, stream=None):
+    """h = residual + x, y = rmsnorm(h) * weight (bf16) and, with ``q`` and ``scales``, y's e4m3 codes: ``scales`` fp32
+    [T] gives one scale a row (the per-row FP8 forward), uint8 [T, mx_sf_cols(d)] one power of two for 32 columns
+    (the block-scaled forward).  ``residual`` and ``h`` are bf16 or fp32, ``weight`` bf16 or fp32; 2-D tensors may
+    have any row stride.  ``x`` None: no addition (``h`` may then be None); ``y`` may be None when codes are
+    written; ``rstd`` [T] is kept for the backward.  ``h`` may be ``residual`` and ``y`` may be ``x``."""
+    shape = residual.shape
+    if len(shape) != 2:
+        raise ValueError(f"residual must be [T, d], got {tuple(shape)}")
+    T, d = shape
+    bf, f32, u8 = torch.bfloat16, torch.float32, torch.uint8
+    rt = _stream_type(residual, "residual")
+    (px, lx), (pr, lr) = _rows(ctx, x, shape, bf, "x"), _rows(ctx, residual, shape, residual.dtype, "residual")
+    (ph, lh), (py, ly) = _rows(ctx, h, shape, residual.dtype, "h"), _rows(ctx, y, shape, bf, "y")
+    wt = _stream_type(weight, "weight")
+    form, ps = 0, None
+    if q is not None or scales is not None:
+        if q is None or scales is None:
+            raise ValueError("q and scales go together")
+        form = 1 if scales.dtype == f32 else 2
+        ps = _flat(ctx, scales, (T,), f32, "scales") if form == 1 else _flat(ctx, scales, (T, 4 * -(-d // 128)), u8, "scales")
+    _check("moe_add_rmsnorm", lib().moe_add_rmsnorm(
+        ctx.handle, px, lx, pr, lr, rt, _flat(ctx, weight, (d,), weight.dtype, "weight"), wt, T, d, eps, ph, lh, py, ly,
+        _flat(ctx, rstd, (T,), f32, "rstd"), form, _flat(ctx, q, shape, u8, "q"), ps, _stream(stream)))
+
+
+def moe_add_rmsnorm_workspace_bytes(T: int, d: int) -> int:
+    """Bytes of the norm backward's workspace."""
+    b = int(lib().moe_add_rmsnorm_workspace_bytes(T, d))
+    if b <= 0:
+        raise ValueError(f"moe_add_rmsnorm_workspace_bytes: invalid arguments T={T} d={d}")
+    return b
+
+
+def moe_add_rmsnorm_backward(ctx, dy, h, weight, rstd, dh, dx, dresidual, dweight, ws, stream=None):
+    """Gradients of moe_add_rmsnorm for ``dy`` (of y) and ``dh`` (of h along the residual stream, or None): the input's,
+    as ``dx`` (bf16) and / or ``dresidual`` (the stream's type), and ``dweight`` [d] fp32.  ``ws``: uint8 of
+    moe_add_rmsnorm_workspace_bytes(T, d)."""
+    shape = h.shape
+    if len(shape) != 2:
+        raise ValueError(f"h must be [T, d], got {tuple(shape)}")
+    T, d = shape
+    bf, f32 = torch.bfloat16, torch.float32
+    rt = _stream_type(h, "h")
+    (pdy, ldy), (ph, lh) = _rows(ctx, dy, shape, bf, "dy"), _rows(ctx, h, shape, h.dtype, "h")
+    (pdh, ldh), (pdx, ldx) = _rows(ctx, dh, shape, h.dtype, "dh"), _rows(ctx, dx, shape, bf, "dx")
+    pdr, ldr = _rows(ctx, dresidual, shape, h.dtype, "dresidual")
+    wt = _stream_type(weight, "weight")
+    wp, wb = _scratch(ctx, ws)
+    _check("moe_add_rmsnorm_backward", lib().moe_add_rmsnorm_backward(
+        ctx.handle, pdy, ldy, ph, lh, rt, _flat(ctx, weight, (d,), weight.dtype, "weight"), wt,
+        _flat(ctx, rstd, (T,), f32, "rstd"), pdh, ldh, T, d, pdx, ldx, pdr, ldr, _flat(ctx, dweight, (d,), f32, "dweight"), wp, wb,
+        _stream(stream)))
+
+
+def moe_balance_loss_workspace_bytes(T: int, E: int, B: int = 1) -> int:
+    """Bytes of moe_balance_loss's workspace for B sequences."""
+    b = int(lib().moe_balance_loss_workspace_bytes(T, E, B))
+    if b <= 0:
+        raise ValueError(f"moe_balance_loss_workspace_bytes: invalid arguments T={T} E={E} B={B}")
+    return b
+
+
+def moe_balance_loss(ctx, logits, topk_ids, balance_coef, z_coef, loss, counts, probs, dlogits, ws, mask=None,
+                     seq_offsets=None, dloss=None, stream=None):
+    """Balance loss and z loss of the router over the sequences of a packed batch: ``loss`` [3] = (balance_coef *
+    balance + z_coef * z, balance, z), per sequence and expert the ``counts`` [B, E] int32 of the choices and the mean
+    probabilities ``probs`` [B, E], and with ``dlogits`` [T, E] the gradient of loss[0] times ``dloss`` (a device
+    scalar, None for 1).  ``mask`` [T] bool or uint8: tokens that count; ``seq_offsets`` [B + 1] int32.  ``ws``: uint8
+    of moe_balance_loss_workspace_bytes(T, E, B)."""
+    if logits.dim() != 2 or topk_ids.dim() != 2 or counts.dim() != 2:
+        raise ValueError("logits, topk_ids and counts must be [T, E], [T, K] and [B, E]")
+    T, E = logits.shape
+    K, B = topk_ids.shape[1], counts.shape[0]
+    f32, i32 = torch.float32, torch.int32
+    if mask is not None and mask.dtype not in (torch.bool, torch.uint8):
+        raise ValueError(f"mask must be bool or uint8, got {mask.dtype}")
+    if seq_offsets is None and B != 1:
+        raise ValueError(f"{B} sequences need seq_offsets")
+    wp, wb = _scratch(ctx, ws)
+    _check("moe_balance_loss", lib().moe_balance_loss(
+        ctx.handle, _flat(ctx, logits, (T, E), f32, "logits"), _flat(ctx, topk_ids, (T, K), i32, "topk_ids"),
+        _flat(ctx, mask, (T,), None if mask is None else mask.dtype, "mask"),
+        _flat(ctx, seq_offsets, (B + 1,), i32, "seq_offsets"), T, E, K, B, balance_coef, z_coef,
+        None if dloss is None else _flat(ctx, dloss.reshape(-1), (1,), f32, "dloss"), _flat(ctx, loss, (3,), f32, "loss"),
+        _flat(ctx, counts, (B, E), i32, "counts"), _flat(ctx, probs, (B, E), f32, "probs"),
+        _flat(ctx, dlogits, (T, E), f32, "dlogits"), wp, wb, _stream(stream)))
+
+
+def moe_router_backward_workspace_bytes(T: int, d: int, E: int) -> int:
+    """Bytes of moe_router_backward's workspace."""
+    b = int(lib().moe_router_backward_workspace_bytes(T, d, E))
+    if b <= 0:
+        raise ValueError(f"moe_router_backward_workspace_bytes: invalid arguments T={T} d={d} E={E}")
+    return b
+
+
+def moe_router_backward(ctx, dlogits, X, W_r, dX_in, dW_r_in, dX, dW_r, ws, stream=None):
+    """dX = dX_in + dlogits W_r^T (bf16) and dW_r = dW_r_in + X^T dlogits (fp32): what an additional loss on the router
+    logits adds to the gradients that the layer's backward left.  ``dX_in`` / ``dW_r_in`` None: zero; an output may be
+    its own input, and None skips its product.  ``ws``: uint8 of moe_router_backward_workspace_bytes(T, d, E)."""
+    if dlogits.dim() != 2 or X.dim() != 2:
+        raise ValueError("dlogits and X must be [T, E] and [T, d]")
+    T, E = dlogits.shape
+    d = X.shape[1]
+    bf, f32 = torch.bfloat16, torch.float32
+    wp, wb = _scratch(ctx, ws)
+    _check("moe_router_backward", lib().moe_router_backward(
+        ctx.handle, _flat(ctx, dlogits, (T, E), f32, "dlogits"), _flat(ctx, X, (T, d), bf, "X"), _flat(ctx, W_r, (d, E), bf, "W_r"), T, d,
+        E, _flat(ctx, dX_in, (T, d), bf, "dX_in"), _flat(ctx, dW_r_in, (d, E), f32, "dW_r_in"), _flat(ctx, dX, (T, d), bf, "dX"),
+        _flat(ctx, dW_r, (d, E), f32, "dW_r"), wp, wb, _stream(stream)))
 
 
 def moe_test_gemm_varlen_m(ctx, A, idx, B, b_kmajor, offsets, D, stream=None):

@@ -1512,6 +1512,236 @@ int moe_quantize_dx_weights_e4m3(moe_ctx* ctx, const void* W_gate, const void* W
   return MOE_OK;
 }
 
+// ---- around the layer: residual addition with RMS norm, the balance loss, the router's extra gradient ----------
+
+static bool rows_ok(const void* p, long long ld, int d, int elem, bool need) {
+  return p ? (ld >= d && reinterpret_cast<uintptr_t>(p) % elem == 0) : !need;
+}
+static bool rows_vec(const void* p, long long ld) { return !p || (aligned16(p) && ld % 8 == 0); }
+
+int moe_add_rmsnorm(moe_ctx* ctx, const void* x, long long ld_x, const void* residual, long long ld_residual,
+                    int residual_fp32, const void* weight, int weight_fp32, long long T, int d, float eps, void* h,
+                    long long ld_h, void* y, long long ld_y, float* rstd, int q_form, void* q, void* scales,
+                    moe_stream_t stream) {
+  VGG_REQUIRE(ctx && T >= 0 && T < INT_MAX && d >= 1 && d <= kMaxNormCols && eps >= 0.0f && q_form >= 0 && q_form <= 2);
+  VGG_REQUIRE(!q_form || d % 64 == 0);
+  if (T == 0) return MOE_OK;
+  const int es = residual_fp32 ? 4 : 2;
+  VGG_REQUIRE(weight && (h || !x) && (y || q_form) && (!q_form || (q && scales)));
+  VGG_REQUIRE(rows_ok(x, ld_x, d, 2, false) && rows_ok(residual, ld_residual, d, es, true) &&
+              rows_ok(h, ld_h, d, es, false) && rows_ok(y, ld_y, d, 2, false));
+  VGG_REQUIRE(reinterpret_cast<uintptr_t>(weight) % (weight_fp32 ? 4 : 2) == 0);
+  const bool vec = d % 8 == 0 && rows_vec(x, ld_x) && rows_vec(residual, ld_residual) && rows_vec(h, ld_h) &&
+                   rows_vec(y, ld_y) && aligned16(weight);
+  VGG_REQUIRE(!q_form || (vec && aligned16(q) && (q_form == 2 || reinterpret_cast<uintptr_t>(scales) % 4 == 0)));
+  DeviceGuard g(ctx->device);
+  VGG_REQUIRE(g.ok);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  NormFwd a{};
+  a.x = x;
+  a.res = residual;
+  a.weight = weight;
+  a.h = h;
+  a.y = y;
+  a.ld_x = ld_x;
+  a.ld_res = ld_residual;
+  a.ld_h = ld_h;
+  a.ld_y = ld_y;
+  a.T = T;
+  a.d = d;
+  a.res_f32 = residual_fp32 != 0;
+  a.weight_f32 = weight_fp32 != 0;
+  a.form = q_form;
+  a.eps = eps;
+  a.rstd = rstd;
+  a.q = static_cast<uint8_t*>(q);
+  a.scales = static_cast<float*>(scales);
+  a.sf = static_cast<uint8_t*>(scales);
+  a.sf_ld = static_cast<int>(moe_mx_sf_cols(d));
+  VGG_LAUNCH("add_rmsnorm", launch_add_rmsnorm(a, vec, s));
+  return MOE_OK;
+}
+
+size_t moe_add_rmsnorm_workspace_bytes(long long T, int d) {
+  if (T < 0 || T >= INT_MAX || d < 1 || d > kMaxNormCols) return 0;
+  return al(sizeof(float) * static_cast<size_t>(std::max<long long>(1, std::min<long long>(T, kMaxNormParts))) * d);
+}
+
+int moe_add_rmsnorm_backward(moe_ctx* ctx, const void* dy, long long ld_dy, const void* h, long long ld_h,
+                             int residual_fp32, const void* weight, int weight_fp32, const float* rstd, const void* dh,
+                             long long ld_dh, long long T, int d, void* dx, long long ld_dx, void* dresidual,
+                             long long ld_dresidual, float* dweight, void* ws, size_t ws_bytes, moe_stream_t stream) {
+  VGG_REQUIRE(ctx && T >= 0 && T < INT_MAX && d >= 1 && d <= kMaxNormCols && dweight &&
+              reinterpret_cast<uintptr_t>(dweight) % 4 == 0);
+  const int es = residual_fp32 ? 4 : 2;
+  if (T > 0) {
+    VGG_REQUIRE(weight && rstd && (dx || dresidual));
+    VGG_REQUIRE(rows_ok(dy, ld_dy, d, 2, true) && rows_ok(h, ld_h, d, es, true) && rows_ok(dh, ld_dh, d, es, false) &&
+                rows_ok(dx, ld_dx, d, 2, false) && rows_ok(dresidual, ld_dresidual, d, es, false));
+    VGG_REQUIRE(reinterpret_cast<uintptr_t>(weight) % (weight_fp32 ? 4 : 2) == 0 &&
+                reinterpret_cast<uintptr_t>(rstd) % 4 == 0);
+    VGG_REQUIRE(ws && (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1)) == 0 &&
+                ws_bytes >= moe_add_rmsnorm_workspace_bytes(T, d));
+  }
+  const bool vec = d % 8 == 0 && rows_vec(dy, ld_dy) && rows_vec(h, ld_h) && rows_vec(dh, ld_dh) && rows_vec(dx, ld_dx) &&
+                   rows_vec(dresidual, ld_dresidual) && aligned16(weight);
+  DeviceGuard g(ctx->device);
+  VGG_REQUIRE(g.ok);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  NormBwd a{};
+  a.dy = dy;
+  a.h = h;
+  a.weight = weight;
+  a.dh = dh;
+  a.rstd = rstd;
+  a.dx = dx;
+  a.dres = dresidual;
+  a.dweight = dweight;
+  a.part = static_cast<float*>(ws);
+  a.ld_dy = ld_dy;
+  a.ld_h = ld_h;
+  a.ld_dh = ld_dh;
+  a.ld_dx = ld_dx;
+  a.ld_dres = ld_dresidual;
+  a.T = T;
+  a.d = d;
+  a.res_f32 = residual_fp32 != 0;
+  a.weight_f32 = weight_fp32 != 0;
+  const int parts = static_cast<int>(std::min<long long>({T, kMaxNormParts, 2ll * ctx->num_sms}));
+  VGG_LAUNCH("add_rmsnorm_bwd", launch_add_rmsnorm_bwd(a, vec, parts, s));
+  return MOE_OK;
+}
+
+static bool balance_sizes_ok(long long T, int E, int B) {
+  return T >= 0 && T <= (1 << 30) && E >= 1 && E <= kMaxGroups && B >= 1 && B <= (1 << 24) &&
+         static_cast<long long>(B) * E < INT_MAX;
+}
+
+size_t moe_balance_loss_workspace_bytes(long long T, int E, int B) {
+  return balance_sizes_ok(T, E, B) ? balance_ws_bytes(T, E, B) : 0;
+}
+
+int moe_balance_loss(moe_ctx* ctx, const float* logits, const int32_t* topk_ids, const uint8_t* mask,
+                     const int32_t* seq_offsets, long long T, int E, int K, int B, float balance_coef, float z_coef,
+                     const float* dloss, float* loss, int32_t* counts, float* probs, float* dlogits, void* ws,
+                     size_t ws_bytes, moe_stream_t stream) {
+  VGG_REQUIRE(ctx && balance_sizes_ok(T, E, B) && K >= 1 && K <= E && T * K < INT_MAX && (seq_offsets || B == 1));
+  VGG_REQUIRE(loss && counts && probs && (T == 0 || (logits && topk_ids)));
+  VGG_REQUIRE(std::isfinite(balance_coef) && std::isfinite(z_coef));
+  for (const void* p : {static_cast<const void*>(logits), static_cast<const void*>(topk_ids), static_cast<const void*>(seq_offsets),
+                        static_cast<const void*>(dloss), static_cast<const void*>(loss), static_cast<const void*>(counts),
+                        static_cast<const void*>(probs), static_cast<const void*>(dlogits)})
+    VGG_REQUIRE(reinterpret_cast<uintptr_t>(p) % 4 == 0);
+  VGG_REQUIRE(ws && (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1)) == 0 && ws_bytes >= balance_ws_bytes(T, E, B));
+  DeviceGuard g(ctx->device);
+  VGG_REQUIRE(g.ok);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  BalanceArgs a{};
+  a.logits = logits;
+  a.topk_ids = topk_ids;
+  a.mask = mask;
+  a.seq_off = seq_offsets;
+  a.dloss = dloss;
+  a.T = T;
+  a.E = E;
+  a.K = K;
+  a.B = B;
+  a.balance_coef = balance_coef;
+  a.z_coef = z_coef;
+  a.loss = loss;
+  a.counts = counts;
+  a.probs = probs;
+  a.dlogits = dlogits;
+  a.err = ctx->d_err;
+  a.timeout_ns = ctx->timeout_ns;
+  VGG_LAUNCH("balance_loss", launch_balance_loss(a, ws, ctx->num_sms, s));
+  return MOE_OK;
+}
+
+// Splits of the reduction over tokens in dW_r = X^T dlogits: enough for every SM.
+static int router_bwd_split(int Tp, int d, int E, int num_sms) {
+  const int tiles = ceil_div(d, BM) * ceil_div(E, gemm_bn(E));
+  const int split = std::max(1, std::min(num_sms / std::max(tiles, 1), kMaxSplitK));
+  return std::max(1, std::min(split, ceil_div(2 * Tp, 8 * BK)));
+}
+
+static bool router_bwd_sizes_ok(int T, int d, int E) {
+  return T >= 0 && T <= 65536 && d >= 64 && d % 64 == 0 && E >= 8 && E % 8 == 0 && E <= kMaxGroups;
+}
+
+size_t moe_router_backward_workspace_bytes(int T, int d, int E) {
+  if (!router_bwd_sizes_ok(T, d, E)) return 0;
+  const size_t Tp = static_cast<size_t>(ceil_div(T, 64)) * 64;
+  return al(sizeof(__nv_bfloat16) * 2 * Tp * E) + al(sizeof(float) * static_cast<size_t>(kMaxSplitK) * d * E);
+}
+
+int moe_router_backward(moe_ctx* ctx, const float* dlogits, const void* X, const void* W_r, int T, int d, int E,
+                        const void* dX_in, const float* dW_r_in, void* dX, float* dW_r, void* ws, size_t ws_bytes,
+                        moe_stream_t stream) {
+  VGG_REQUIRE(ctx && router_bwd_sizes_ok(T, d, E) && (dX || dW_r));
+  VGG_REQUIRE(T == 0 || (dlogits && (!dX || W_r) && (!dW_r || X)));
+  VGG_REQUIRE(aligned16(dlogits) && aligned16(X) && aligned16(W_r) && aligned16(dX_in) && aligned16(dW_r_in) &&
+              aligned16(dX) && aligned16(dW_r));
+  VGG_REQUIRE(ws && (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1)) == 0 &&
+              ws_bytes >= moe_router_backward_workspace_bytes(T, d, E));
+  DeviceGuard g(ctx->device);
+  VGG_REQUIRE(g.ok);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int Tp = ceil_div(T, 64) * 64;
+  __nv_bfloat16* hi = static_cast<__nv_bfloat16*>(ws);
+  __nv_bfloat16* lo = hi + static_cast<size_t>(Tp) * E;
+  float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + al(sizeof(__nv_bfloat16) * 2 * static_cast<size_t>(Tp) * E));
+  if (T > 0) VGG_LAUNCH("split_dlogits", launch_split_dlogits(dlogits, T, Tp, E, hi, lo, s));
+  if (T > 0 && dX) {
+    // dX = dX_in + hi W_r^T: one bf16 rounding of dlogits (relative 2^-9 of each term) under a bf16 result
+    GemmParams p = base_params(ctx);
+    p.M = T;
+    p.N = d;
+    p.K = E;
+    p.groups = 1;
+    p.out0 = dX;
+    p.ld_out = d;
+    p.add = static_cast<const __nv_bfloat16*>(dX_in);
+    const int BN = gemm_bn(d);
+    Maps m = zero_maps();
+    if (!make_map_2d(&m.a0, hi, E, T, E, BM) || !make_map_3d(&m.b0, W_r, E, d, 1, BN) ||
+        !make_store_map_3d(&m.o0, dX, false, d, T, 1, 64))
+      return MOE_ERR_CUDA;
+    m.a1 = m.a0;
+    m.b1 = m.b0;
+    const int tiles = ceil_div(T, BM) * ceil_div(d, BN);
+    VGG_LAUNCH("router_dx", run_dense_add(BN, p, m, std::min(tiles, ctx->num_sms), s));
+  }
+  if (dW_r) {
+    // dW_r = dW_r_in + X^T (hi + lo), split over tokens; one reduction over 2 Tp rows, X read twice (rows past
+    // T of X are the map's zero fill, of hi and lo zero)
+    int split = 0;
+    if (T > 0) {
+      split = router_bwd_split(Tp, d, E, ctx->num_sms);
+      GemmParams p = base_params(ctx);
+      p.M = d;
+      p.N = E;
+      p.K = 2 * Tp;
+      p.groups = 1;
+      p.a_kwrap = Tp;
+      p.split_k = split;
+      p.ld_out = E;
+      p.out0 = part;
+      const int BN = gemm_bn(E);
+      Maps m = zero_maps();
+      if (!make_map_2d(&m.a0, X, d, T, d, 64) || !make_map_2d(&m.b0, hi, E, 2 * static_cast<uint64_t>(Tp), E, 64) ||
+          !make_store_map_3d(&m.o0, part, true, E, d, split, 32))
+        return MOE_ERR_CUDA;
+      m.a1 = m.a0;
+      m.b1 = m.b0;
+      const int tiles = ceil_div(d, BM) * ceil_div(E, BN);
+      VGG_LAUNCH("router_dw", run_dense_mn_store(BN, p, m, std::min(tiles * split, ctx->num_sms), s));
+    }
+    VGG_LAUNCH("router_dw_reduce", launch_splitk_reduce_add(part, split, static_cast<long long>(d) * E, dW_r_in, dW_r, s));
+  }
+  return MOE_OK;
+}
+
 int moe_test_gemm_varlen_m(moe_ctx* ctx, const void* A, const int32_t* idx, const void* B, int B_kmajor, int G,
                            int rows_a, int K, int N, long long cap, const int32_t* offsets, float* D,
                            moe_stream_t stream) {

@@ -57,6 +57,8 @@ enum VarMode { VAR_M = 0, VAR_K = 1, VAR_NONE = 2 };
 // epilogues of the e4m3 form (operands are e4m3 codes of per-row-scaled rows; the accumulator is
 // multiplied by the A row's scale and the output channel's scale first).
 // EPI_DSWIGLU_Q: the dSwiGLU epilogue of the e4m3 form (the accumulator times q_row[row] q_col[column]).
+// EPI_ADD: the plain bf16 epilogue of a dense product with a bf16 matrix (add, or none) added to it in fp32; N a
+// multiple of 64.
 // Extra forms (bit flags):
 //   X_DUAL_A  the A operand arrives as a bf16 high part (maps a0/a1) and the bf16 rounding of the rest
 //             (maps a2/a3, the same coordinates); every K step issues two UMMAs into one accumulator, so
@@ -88,7 +90,7 @@ enum VarMode { VAR_M = 0, VAR_K = 1, VAR_NONE = 2 };
 enum XFlags { X_DUAL_A = 1, X_TRANS = 2, X_PAIR = 4, X_MX = 8 };
 enum EpiKind {
   EPI_STORE = 0, EPI_SWIGLU = 1, EPI_SCALE = 2, EPI_DSWIGLU = 3, EPI_SWIGLU_Q = 4, EPI_SCALE_Q = 5, EPI_STORE_Q = 6,
-  EPI_DSWIGLU_Q = 7
+  EPI_DSWIGLU_Q = 7, EPI_ADD = 8
 };
 
 struct GemmParams {
@@ -132,6 +134,7 @@ struct GemmParams {
   float* part;  // dSwiGLU epilogue: per-row partial dot products [rows][part_ld]
   int part_ld;
   const float* col_bias;
+  const __nv_bfloat16* add;  // EPI_ADD: [M][ld_out], may be the output itself (a thread reads what it will store)
   const float* q_row;  // e4m3 dSwiGLU: A row scales [rows], B row scales [groups][q_ld]
   const float* q_col;
   int q_ld;
@@ -464,6 +467,7 @@ __global__ void __launch_bounds__(WarpPlan<STAGES, EW, AMODE, BMODE, CN, XF>::kT
                 "block-scaled form: BN = 128 or 192, K-major operands, varlen-M plain epilogue kinds or a varlen-K store");
   static_assert(!kMx || 2 * BN + STAGES * (4 + 4 * mx_b_blocks(BN)) <= 512, "block-scaled form: TMEM columns");
   static_assert(EPI != EPI_STORE_Q || !OUTF32, "the e4m3 plain epilogue stores bf16");
+  static_assert(EPI != EPI_ADD || (!OUTF32 && VAR == VAR_NONE && XF == 0), "the adding epilogue: dense, bf16 out");
   static_assert(!kF8 || ((AMODE == A_GATHER_K || AMODE == A_TMA_K) && (BMODE == B_TMA_K3 || BMODE == B_TMA_K3_GU) &&
                          (VAR == VAR_M || kMx)),
                 "e4m3 form: K-major operands, varlen-M (the block-scaled form also varlen-K)");
@@ -1444,6 +1448,13 @@ __global__ void __launch_bounds__(WarpPlan<STAGES, EW, AMODE, BMODE, CN, XF>::kT
           if (EPI == EPI_STORE_Q && VAR == VAR_M && row_ok) sr = __ldg(p.row_scale + s_off[tl.g] + m);
 #pragma unroll 1
           for (int c = c_lo; c < c_lo + kCols; c += 64) {
+            uint4 ad[EPI == EPI_ADD ? 8 : 1];
+            if constexpr (EPI == EPI_ADD) {  // in flight while the accumulator is read
+              const uint4* src = reinterpret_cast<const uint4*>(p.add + static_cast<long long>(m) * p.ld_out + tl.n0 + c);
+              const bool on = p.add && row_ok && tl.n0 + c < p.N;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) ad[i] = on ? src[i] : make_uint4(0, 0, 0, 0);
+            }
             uint32_t r0[32], r1[32];
             tmem_ld32(tbase + c, r0);
             tmem_ld32(tbase + c + 32, r1);
@@ -1457,6 +1468,18 @@ __global__ void __launch_bounds__(WarpPlan<STAGES, EW, AMODE, BMODE, CN, XF>::kT
               if (p.col_bias) {
                 if (col + i < p.N) v[i] += __ldg(p.col_bias + col + i);
                 if (col + 32 + i < p.N) v[32 + i] += __ldg(p.col_bias + col + 32 + i);
+              }
+            }
+            if constexpr (EPI == EPI_ADD) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const uint32_t w[4] = {ad[i].x, ad[i].y, ad[i].z, ad[i].w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const float2 f = unpack_bf16x2(w[k]);
+                  v[8 * i + 2 * k] += f.x;
+                  v[8 * i + 2 * k + 1] += f.y;
+                }
               }
             }
             if (EPI == EPI_STORE_Q) {

@@ -68,6 +68,12 @@ cudaError_t run_dw_down(int BN, bool f32, const GemmParams& p, const Maps& m, in
              : launch_grouped_gemm<128, 6, 4, 1, A_GATHER_MN, B_TMA_MN2, VAR_K, EPI_STORE, false>(p, m, grid, s);
 }
 
+// Dense A B^T with both operands K-major, plus a bf16 matrix in the epilogue (dX + dlogits W_r^T).
+cudaError_t run_dense_add(int BN, const GemmParams& p, const Maps& m, int grid, cudaStream_t s) {
+  if (BN == 256) return launch_grouped_gemm<256, 4, 4, 1, A_TMA_K, B_TMA_K3, VAR_NONE, EPI_ADD, false>(p, m, grid, s);
+  return launch_grouped_gemm<128, 6, 4, 1, A_TMA_K, B_TMA_K3, VAR_NONE, EPI_ADD, false>(p, m, grid, s);
+}
+
 // Dense A^T B with both operands MN-major (router weight gradient X^T dlogits), split K, fp32 out.
 cudaError_t run_dense_mn_store(int BN, const GemmParams& p, const Maps& m, int grid, cudaStream_t s) {
   if (BN == 256) return launch_grouped_gemm<256, 4, 4, 1, A_TMA_MN, B_TMA_MN2, VAR_NONE, EPI_STORE, true>(p, m, grid, s);

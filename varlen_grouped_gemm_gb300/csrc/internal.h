@@ -95,6 +95,7 @@ cudaError_t run_dw_tiled(int BN, bool f32, const GemmParams& p, const Maps& m, i
 cudaError_t run_dw_tiled_trans(int BN, bool f32, const GemmParams& p, const Maps& m, int grid, cudaStream_t s);
 cudaError_t run_dw_dual(int BN, bool f32, bool trans, bool pair, const GemmParams& p, const Maps& m, int grid,
                         cudaStream_t s);
+cudaError_t run_dense_add(int BN, const GemmParams& p, const Maps& m, int grid, cudaStream_t s);
 cudaError_t run_dense_mn_store(int BN, const GemmParams& p, const Maps& m, int grid, cudaStream_t s);
 // test exports
 cudaError_t run_test_m(int gathered, int b_kmajor, bool pair, const GemmParams& p, const Maps& m, int grid,
@@ -176,6 +177,67 @@ cudaError_t launch_token_backward(const float* part, int part_ld, const int32_t*
                                   __nv_bfloat16* dL_lo, __nv_bfloat16* dX, int* err, cudaStream_t s);
 
 cudaError_t launch_splitk_reduce(const float* part, int splits, long long n, float* out, cudaStream_t s);
+
+// ---- residual addition and RMS norm ----------------------------------------------------------
+// Row strides in elements.  Null: x (nothing is added), h, y, rstd (not written).
+struct NormFwd {
+  const void *x, *res, *weight;
+  void *h, *y;
+  long long ld_x, ld_res, ld_h, ld_y;
+  long long T;
+  int d, res_f32, weight_f32, form;  // form: 0 bf16 alone, 1 per-row e4m3 (q, scales), 2 block-scaled (q, sf)
+  float eps;
+  float* rstd;
+  uint8_t* q;
+  float* scales;
+  uint8_t* sf;
+  int sf_ld;
+};
+constexpr int kMaxNormCols = 16384;  // a row's values stay in the registers of one block
+// vec: d a multiple of 8 and every row 16-byte aligned (required by forms 1 and 2)
+cudaError_t launch_add_rmsnorm(const NormFwd& a, bool vec, cudaStream_t s);
+
+// dh, h, dres have the residual stream's type; null: dh (zero), dx, dres (not written).  part: [parts][d], parts
+// blocks each taking every parts-th row.
+struct NormBwd {
+  const void *dy, *h, *weight, *dh;
+  const float* rstd;
+  void *dx, *dres;
+  float *dweight, *part;
+  long long ld_dy, ld_h, ld_dh, ld_dx, ld_dres;
+  long long T;
+  int d, res_f32, weight_f32;
+};
+constexpr int kMaxNormParts = 1024;
+cudaError_t launch_add_rmsnorm_bwd(const NormBwd& a, bool vec, int parts, cudaStream_t s);
+
+// ---- balance loss ----------------------------------------------------------------------------
+struct BalanceArgs {
+  const float* logits;
+  const int32_t* topk_ids;
+  const uint8_t* mask;     // [T], null: every token counts
+  const int32_t* seq_off;  // [B + 1], null: one sequence
+  const float* dloss;      // null: 1
+  long long T;
+  int E, K, B;
+  float balance_coef, z_coef;
+  float* loss;
+  int32_t* counts;
+  float* probs;
+  float* dlogits;  // null: no gradient
+  int* err;
+  unsigned long long timeout_ns;
+};
+size_t balance_ws_bytes(long long T, int E, int B);
+cudaError_t launch_balance_loss(const BalanceArgs& a, void* ws, int num_sms, cudaStream_t s);
+
+// ---- router products -------------------------------------------------------------------------
+// dlogits [T][E] fp32 to bf16 high parts hi [Tp][E] and the bf16 rounding of the rest lo [Tp][E], rows past T zero.
+cudaError_t launch_split_dlogits(const float* dlogits, long long T, long long Tp, int E, __nv_bfloat16* hi,
+                                 __nv_bfloat16* lo, cudaStream_t s);
+// out[i] = in[i] (or 0) + sum_s part[s][i], s ascending.
+cudaError_t launch_splitk_reduce_add(const float* part, int splits, long long n, const float* in, float* out,
+                                     cudaStream_t s);
 
 cudaError_t launch_wait_timeout_probe(int* err, unsigned long long timeout_ns, cudaStream_t s);
 

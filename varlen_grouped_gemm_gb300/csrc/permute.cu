@@ -353,34 +353,6 @@ __global__ void __launch_bounds__(TB) perm_scatter_kernel(
   }
 }
 
-// Grid-wide barrier of a cooperative launch (every block resident): thread 0 of each block arrives on
-// `counter` (zeroed before the launch) and waits, bounded by timeout_ns, until `target` arrivals.  The
-// block's writes before the barrier are visible to every block after it.  Returns false, with
-// MOE_DEV_TIMEOUT recorded, when the wait gave up.
-__device__ bool grid_barrier(int* counter, int target, unsigned long long timeout_ns, int* err, int* s_ok) {
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    int ok = 1;
-    __threadfence();
-    atomicAdd(counter, 1);
-    const uint64_t t0 = globaltimer_ns();
-    for (uint32_t i = 0;; ++i) {
-      int v;
-      asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(counter) : "memory");
-      if (v >= target) break;
-      if ((i & 15u) == 15u && globaltimer_ns() - t0 > timeout_ns) {
-        set_error(err, DERR_TIMEOUT);
-        ok = 0;
-        break;
-      }
-    }
-    __threadfence();
-    *s_ok = ok;
-  }
-  __syncthreads();
-  return *s_ok != 0;
-}
-
 // The whole grouping in one cooperative launch (one block per TB tokens, all resident), with the results of
 // perm_hist + perm_escan + perm_scan + perm_scatter: (1) a block's membership bits per expert, its per-expert
 // counts hist[e][b] and its pair count; grid barrier; (2) one warp per expert turns hist[e][*] into in-expert

@@ -36,6 +36,34 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
   return t;
 }
 
+// Grid-wide barrier of a cooperative launch (every block resident): thread 0 of each block arrives on
+// `counter` (zeroed before the launch) and waits, bounded by timeout_ns, until `target` arrivals.  The
+// block's writes before the barrier are visible to every block after it.  Returns false, with
+// MOE_DEV_TIMEOUT recorded, when the wait gave up.
+__device__ __forceinline__ bool grid_barrier(int* counter, int target, unsigned long long timeout_ns, int* err, int* s_ok) {
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    int ok = 1;
+    __threadfence();
+    atomicAdd(counter, 1);
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t i = 0;; ++i) {
+      int v;
+      asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(counter) : "memory");
+      if (v >= target) break;
+      if ((i & 15u) == 15u && globaltimer_ns() - t0 > timeout_ns) {
+        set_error(err, DERR_TIMEOUT);
+        ok = 0;
+        break;
+      }
+    }
+    __threadfence();
+    *s_ok = ok;
+  }
+  __syncthreads();
+  return *s_ok != 0;
+}
+
 // ------------------------------------------------------------------ mbarrier
 
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
