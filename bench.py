@@ -127,6 +127,15 @@ def kernel_work(wl, P, dW_bytes=2):
         "dw_gate_up": (4 * P * d * n, 2 * T * d + 4 * P * n + 2 * dWb * E * n * d,
                        2 * P * d + 8 * P * n + 2 * dWb * E * n * d),
         "dw_down": (2 * P * d * n, 2 * T * d + 2 * P * n + dWb * E * d * n, 2 * P * d + 4 * P * n + dWb * E * d * n),
+        # around the layer (outside the step): the norm with per-row codes and its backward on a bf16 stream, the
+        # balance loss with its gradient, the router's products for it (dlogits as bf16 parts)
+        "add_rmsnorm": same(6 * T * d, 9 * T * d + 8 * T + 2 * d),
+        "add_rmsnorm_bwd": same(12 * T * d, 8 * T * d + 4 * T + 6 * d),
+        "balance_loss": same(12 * T * E, 8 * T * E + 4 * T * K + 8 * E),
+        "split_dlogits": same(0, 8 * T * E),
+        "router_dx": same(2 * T * d * E, 2 * T * E + 2 * d * E + 4 * T * d),
+        "router_dw": same(4 * T * d * E, 2 * T * d + 4 * T * E + 4 * d * E),
+        "router_dw_reduce": same(0, 12 * d * E),
     }
 
 
@@ -243,7 +252,7 @@ _GEMM_LABELS = {
     (0, 2, 0, 3): "dact_dswiglu", (0, 2, 0, 0): "dx_gemm", (2, 3, 1, 0): "dw_tiled (gate/up, down)",
     (2, 3, 2, 0): "dwr_gemm", (2, 4, 1, 0): "dw_gather_b", (3, 3, 1, 0): "dw_gather_a",
     (1, 1, 0, 4): "gate_up_swiglu_e4m3", (0, 0, 0, 5): "down_scale_e4m3", (0, 0, 0, 6): "dx_gemm_e4m3",
-    (0, 0, 0, 7): "dact_dswiglu_e4m3",
+    (0, 0, 0, 7): "dact_dswiglu_e4m3", (0, 0, 2, 8): "router_dx",
 }
 # the block-scaled form (template flag X_MX = 8)
 _MX_GEMM_LABELS = {(1, 1, 0, 1): "gate_up_swiglu_mx", (0, 0, 0, 2): "down_scale_mx", (0, 0, 0, 3): "dact_dswiglu_mx",

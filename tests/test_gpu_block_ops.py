@@ -131,6 +131,30 @@ def test_norm_codes(vgg, ctx, T, d, pad, res_t, form):
     assert torch.equal(q2, q) and torch.equal(sc2, sc) and torch.equal(res, h)
 
 
+@pytest.mark.parametrize("form", ["bf16", "e4m3", "mx"])
+@pytest.mark.parametrize("res_t", [BF, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("T,d,pad", [(607, 4160, 0), (608, 4160, 8), (1300, 7168, 0), (2111, 8192, 0)])
+def test_norm_many_wide_rows(vgg, ctx, T, d, pad, res_t, form):
+    """From four wide rows an SM on, the rows go through shared memory (608 on 152 SMs); odd numbers leave
+    the last groups without a row."""
+    g = gen_of(T + d)
+    x, res = rows(T, d, BF, g, pad), rows(T, d, res_t, g, pad, scale=2.0)
+    res[:, 5] *= 20
+    w = (1 + 0.1 * torch.randn(d, device="cuda", generator=g)).to(res_t)
+    h, y, rstd = rows(T, d, res_t, None, pad), rows(T, d, BF, None, pad), torch.empty(T, device="cuda")
+    q = sc = None
+    if form != "bf16":
+        q = torch.empty((T, d), dtype=U8, device="cuda")
+        sc = torch.empty(T, device="cuda") if form == "e4m3" else torch.empty((T, vgg.mx_sf_cols(d)), dtype=U8, device="cuda")
+    vgg.moe_add_rmsnorm(ctx, x, res, w, 1e-5, h, y, rstd, q, sc)
+    check_norm(x, res, w, 1e-5, h, y, rstd, q, sc)
+    y2 = rows(T, d, BF, None)
+    vgg.moe_add_rmsnorm(ctx, None, h, w, 1e-5, None, y2)  # nothing added
+    assert torch.equal(y2, y)
+    vgg.moe_add_rmsnorm(ctx, x, res, w, 1e-5, res, x)  # in place
+    assert torch.equal(res, h) and torch.equal(x, y)
+
+
 def test_norm_in_place(vgg, ctx):
     g = gen_of(5)
     x, res, w = rows(9, 1024, BF, g), rows(9, 1024, BF, g), torch.ones(1024, device="cuda")

@@ -150,8 +150,8 @@ def _ptr(t: torch.Tensor | None, dtype=None, name="tensor"):
 
 
 def _stream(stream) -> int | None:
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:  # the raw handle of the current stream: building a Stream object takes longer than a launch
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -454,16 +454,22 @@ def moe_backward_e4m3(ctx, dO, X, W_r, W_gate, W_up, W_down, Wgu_q, wgu_scale, W
 # ------------------------------------------------------------------ around the layer
 
 
+def _refuse(t, shape, dtype, name, ctx, what=""):
+    raise ValueError(f"{name} must be a {what}{tuple(shape)} {dtype} tensor on CUDA device {ctx.device}, got "
+                     f"{tuple(t.shape)} {t.dtype} with strides {t.stride()} on {t.device}")
+
+
 def _rows(ctx, t: torch.Tensor | None, shape, dtype, name):
     """(pointer, row stride) of a [T, d] tensor whose columns are contiguous; (None, 0) for None."""
     if t is None:
         return None, 0
-    if t.dtype != dtype or t.get_device() != ctx.device or t.shape != shape:
-        raise ValueError(f"{name} must be a {tuple(shape)} {dtype} tensor on CUDA device {ctx.device}, got "
-                         f"{tuple(t.shape)} {t.dtype} on {t.device}")
+    if t.dtype is not dtype or t.get_device() != ctx.device or t.shape != shape:
+        _refuse(t, shape, dtype, name, ctx)
+    if t.is_contiguous():
+        return t.data_ptr(), shape[1]
     ld, one = t.stride()
     if (one != 1 and shape[1] > 1) or (ld < shape[1] and shape[0] > 1):
-        raise ValueError(f"{name} must have contiguous columns and rows that do not overlap, got strides {t.stride()}")
+        _refuse(t, shape, dtype, name, ctx, "row-strided ")
     return t.data_ptr(), max(ld, shape[1])
 
 
@@ -471,9 +477,8 @@ def _flat(ctx, t: torch.Tensor | None, shape, dtype, name):
     """Pointer of a contiguous tensor of the given shape; None for None."""
     if t is None:
         return None
-    if t.dtype != dtype or t.get_device() != ctx.device or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {tuple(shape)} {dtype} tensor on CUDA device {ctx.device}, got "
-                         f"{tuple(t.shape)} {t.dtype} on {t.device}")
+    if t.dtype is not dtype or t.get_device() != ctx.device or t.shape != shape or not t.is_contiguous():
+        _refuse(t, shape, dtype, name, ctx, "contiguous ")
     return t.data_ptr()
 
 
@@ -481,7 +486,7 @@ def _scratch(ctx, ws: torch.Tensor):
     """(pointer, bytes) of a workspace."""
     if ws.get_device() != ctx.device or not ws.is_contiguous():
         raise ValueError(f"ws must be a contiguous tensor on CUDA device {ctx.device}")
-    return ws.data_ptr(), ws.numel() * ws.element_size()
+    return ws.data_ptr(), ws.nbytes
 
 
 def _stream_type(t: torch.Tensor, name):

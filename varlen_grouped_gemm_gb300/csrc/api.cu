@@ -1558,7 +1558,9 @@ int moe_add_rmsnorm(moe_ctx* ctx, const void* x, long long ld_x, const void* res
   a.scales = static_cast<float*>(scales);
   a.sf = static_cast<uint8_t*>(scales);
   a.sf_ld = static_cast<int>(moe_mx_sf_cols(d));
-  VGG_LAUNCH("add_rmsnorm", launch_add_rmsnorm(a, vec, s));
+  a.err = ctx->d_err;
+  a.timeout_ns = ctx->timeout_ns;
+  VGG_LAUNCH("add_rmsnorm", launch_add_rmsnorm(a, vec, ctx->num_sms, s));
   return MOE_OK;
 }
 
@@ -1607,8 +1609,9 @@ int moe_add_rmsnorm_backward(moe_ctx* ctx, const void* dy, long long ld_dy, cons
   a.d = d;
   a.res_f32 = residual_fp32 != 0;
   a.weight_f32 = weight_fp32 != 0;
-  const int parts = static_cast<int>(std::min<long long>({T, kMaxNormParts, 2ll * ctx->num_sms}));
-  VGG_LAUNCH("add_rmsnorm_bwd", launch_add_rmsnorm_bwd(a, vec, parts, s));
+  a.err = ctx->d_err;
+  a.timeout_ns = ctx->timeout_ns;
+  VGG_LAUNCH("add_rmsnorm_bwd", launch_add_rmsnorm_bwd(a, vec, ctx->num_sms, s));
   return MOE_OK;
 }
 

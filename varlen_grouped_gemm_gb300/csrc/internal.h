@@ -192,13 +192,15 @@ struct NormFwd {
   float* scales;
   uint8_t* sf;
   int sf_ld;
+  int* err;
+  unsigned long long timeout_ns;
 };
 constexpr int kMaxNormCols = 16384;  // a row's values stay in the registers of one block
 // vec: d a multiple of 8 and every row 16-byte aligned (required by forms 1 and 2)
-cudaError_t launch_add_rmsnorm(const NormFwd& a, bool vec, cudaStream_t s);
+cudaError_t launch_add_rmsnorm(const NormFwd& a, bool vec, int num_sms, cudaStream_t s);
 
-// dh, h, dres have the residual stream's type; null: dh (zero), dx, dres (not written).  part: [parts][d], parts
-// blocks each taking every parts-th row.
+// dh, h, dres have the residual stream's type; null: dh (zero), dx, dres (not written).  part: [min(T,
+// kMaxNormParts)][d].
 struct NormBwd {
   const void *dy, *h, *weight, *dh;
   const float* rstd;
@@ -207,9 +209,11 @@ struct NormBwd {
   long long ld_dy, ld_h, ld_dh, ld_dx, ld_dres;
   long long T;
   int d, res_f32, weight_f32;
+  int* err;
+  unsigned long long timeout_ns;
 };
 constexpr int kMaxNormParts = 1024;
-cudaError_t launch_add_rmsnorm_bwd(const NormBwd& a, bool vec, int parts, cudaStream_t s);
+cudaError_t launch_add_rmsnorm_bwd(const NormBwd& a, bool vec, int num_sms, cudaStream_t s);
 
 // ---- balance loss ----------------------------------------------------------------------------
 struct BalanceArgs {
