@@ -1,20 +1,21 @@
 // The router's balance and z losses with their gradient, and the per-expert counts.
 //
-// For the valid tokens of every sequence b (n_b of them; n in all, B' sequences with any), p_t = softmax(l_t):
+// For the counted tokens of every sequence b (n_b of them; n in all, B' sequences with any), p_t = softmax(l_t):
 //   f_be = E / (K n_b) #{(t, k): id_tk = e},   P_be = 1 / n_b sum_t p_te
 //   loss = alpha / B' sum_b sum_e f_be P_be  +  beta / n sum_t lse_t^2
 //   dl_te = p_te (c_be - sum_j p_tj c_bj) + 2 beta / n lse_t p_te,   c_be = alpha f_be / (B' n_b)
 //
-// f depends on the choices alone, so once the counts are known one pass over the logits gives P, the z loss and
-// the gradient: 8 bytes an element, bound by HBM for long batches and by the grid barriers for short ones.
-// A shift of c_b by a constant leaves dl unchanged (p sums to one): with c' = alpha E / (B' n_b) (counts_be / (K n_b) -
-// 1 / E), whose numerator counts_be E - K n_b is a whole number, a nearly even load loses nothing to cancellation.
+// f depends on the choices alone, so once the counts are known one pass over the logits gives P, both losses and the
+// gradient: 8 bytes an element, bound by HBM for long batches and by the barriers between the phases for short ones.
+// A shift of c_b by a constant leaves dl unchanged (p sums to one), so the kernel works with u_be = f_be - 1 =
+// (counts_be E - K n_b) / (K n_b): its numerator is a whole number, and a nearly even load loses nothing to
+// cancellation.  A token's share of the balance loss is 1 + <p_t, u_b>, which the gradient needs anyway.
 //
-// One cooperative launch: (1) counts by shared-memory histograms, added with integer atomics (any order, one
-// result); (2) the pass over the logits; (3) the probabilities' sums and the loss.  Block c takes the tokens of
-// chunk c; where a chunk crosses into another sequence it closes a piece.  The piece of (chunk c, sequence b) has
-// the index c + b, unique because every next piece moves on by a chunk, a sequence or both.  Sums over tokens run
-// in a fixed order, so equal calls give equal bits.
+// One launch: (1) counts by shared-memory histograms, added with integer atomics (any order, one result); (2) the
+// pass over the logits; (3) the probabilities' sums and the loss.  Block c takes the tokens of chunk c; where a
+// chunk crosses into another sequence it closes a piece.  The piece of (chunk c, sequence b) has the index c + b,
+// unique because every next piece moves on by a chunk, a sequence or both.  Sums over tokens run in a fixed order,
+// so equal calls give equal bits.
 #include "internal.h"
 
 namespace vgg {
@@ -24,16 +25,18 @@ namespace {
 constexpr int kBalThreads = 512;
 constexpr int kBalWarps = kBalThreads / 32;
 constexpr int kBalMaxBlocks = 1024;  // bounds the number of pieces, and with it the workspace
+constexpr int kBalCluster = 16;      // up to so many blocks wait for one another as a cluster, more as a whole grid
+constexpr long long kBalOneCluster = 1 << 18;  // most logits that one cluster takes
 
 inline size_t al256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 struct BalWs {
-  int* ctrl;      // [0] grid barrier, [1] blocks that have finished phase 3
+  int* ctrl;      // [0] grid barrier
   int* nvalid;    // [B]
-  float* zpart;   // [pieces]
+  float* zpart;   // [pieces] sums of lse^2
+  float* bpart;   // [pieces] sums of the balance loss's shares, over n_b
   int* cnt;       // [B][E]
   float* ppart;   // [pieces][E]
-  float* lpart;   // [B][ceil(E / 32)]
   size_t zeroed;  // bytes from ctrl up to ppart
   size_t bytes;
 };
@@ -48,13 +51,13 @@ BalWs carve_balance(void* ws, long long T, int E, int B) {
     return r;
   };
   BalWs w{};
-  w.ctrl = reinterpret_cast<int*>(take(2 * sizeof(int)));
+  w.ctrl = reinterpret_cast<int*>(take(sizeof(int)));
   w.nvalid = reinterpret_cast<int*>(take(sizeof(int) * B));
   w.zpart = reinterpret_cast<float*>(take(sizeof(float) * pieces));
+  w.bpart = reinterpret_cast<float*>(take(sizeof(float) * pieces));
   w.cnt = reinterpret_cast<int*>(take(sizeof(int) * static_cast<size_t>(B) * E));
   w.zeroed = at;
   w.ppart = reinterpret_cast<float*>(take(sizeof(float) * pieces * E));
-  w.lpart = reinterpret_cast<float*>(take(sizeof(float) * static_cast<size_t>(B) * ((E + 31) / 32)));
   w.bytes = at;
   return w;
 }
@@ -87,67 +90,169 @@ struct Piece {
   }
 };
 
-__device__ __forceinline__ float block_sum(float v, float* red) {
+// A warp's tiles of up to kTile tokens in order: of every piece, each kBalWarps-th from the warp's own.
+template <int kTile>
+struct Tiles {
+  Piece pc;
+  int tb;
+  bool ok;
+  __device__ void skip(const BalanceArgs& a, int c1, int warp) {
+    while (ok && tb >= pc.t1) {
+      ok = pc.next(a, c1);
+      tb = pc.t0 + warp * kTile;
+    }
+  }
+  __device__ void first(const BalanceArgs& a, int c0, int c1, int warp) {
+    pc.first(a, c0);
+    ok = true;
+    tb = pc.t1;
+    skip(a, c1, warp);
+  }
+  __device__ void next(const BalanceArgs& a, int c1, int warp) {
+    tb += kBalWarps * kTile;
+    skip(a, c1, warp);
+  }
+};
+
+// Sums of two values over the block, the same in every thread.
+__device__ __forceinline__ float2 block_sum2(float x, float y, float2* red) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  for (int o = 16; o > 0; o >>= 1) {
+    x += __shfl_xor_sync(0xffffffffu, x, o);
+    y += __shfl_xor_sync(0xffffffffu, y, o);
+  }
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(x, y);
   __syncthreads();
-  float s = 0.0f;
+  float2 s = make_float2(0.0f, 0.0f);
 #pragma unroll
-  for (int i = 0; i < kBalWarps; ++i) s += red[i];
+  for (int i = 0; i < kBalWarps; ++i) {
+    s.x += red[i].x;
+    s.y += red[i].y;
+  }
   __syncthreads();
   return s;
 }
 
-// VEC: a token's row by 16-byte loads, LPT lanes a token (32 / LPT tokens in a warp), NV vectors a lane; else one
-// value a load, a warp a token, NV values a lane.  UN tokens a lane group are in flight at once.
-template <bool VEC, int LPT, int NV, int UN>
+// 2^x, at most 2 steps off; results below 2^-126 are 0.
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Two fp32 values side by side: the packed instructions take both in one issue slot, and the pass over the logits is
+// bound by issue slots as much as by HBM.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pack2(float a, float b) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(f32x2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// Largest of v over LPT neighbouring lanes.
+template <int LPT>
+__device__ __forceinline__ float lanes_max(float v) {
+  if constexpr (LPT == 32) {
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(v) : "f"(v));
+    return v;
+  }
+#pragma unroll
+  for (int o = LPT / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+// VEC: LPT lanes a token (32 / LPT tokens in a warp), NV vectors of four logits a lane; a warp's tiles of kTile tokens come
+// through a ring of ST stages of its own, one bulk copy a tile (the tokens' rows are contiguous), so the bytes in
+// flight do not depend on registers, and the ring runs on from one piece into the next.  Else one value a load, a warp
+// a token, NV values a lane.
+template <bool VEC, int LPT, int NV, int UN, int ST>
 __global__ void __launch_bounds__(kBalThreads) balance_kernel(const BalanceArgs a, const BalWs w, int chunk) {
-  constexpr int W = VEC ? 4 : 1;
-  constexpr int kTok = 32 / LPT;
-  extern __shared__ float bal_smem[];  // [kBalWarps][E] partial sums; phase 1: the histogram
-  __shared__ float s_red[kBalWarps];
+  constexpr int kPairs = VEC ? 2 * NV : NV / 2;
+  constexpr int kTok = 32 / LPT, kTile = kTok * UN;
+  extern __shared__ __align__(128) uint8_t bal_smem[];
+  __shared__ float2 s_red[kBalWarps];
   __shared__ float s_tile[kBalWarps][33];
-  __shared__ int s_n, s_ok;
+  __shared__ __align__(8) uint64_t full[kBalWarps][ST];
+  __shared__ int s_n, s_ok, s_abort;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int G = gridDim.x, E = a.E, K = a.K, T = static_cast<int>(a.T);
   const int c0 = min(T, static_cast<int>(blockIdx.x) * chunk), c1 = min(T, c0 + chunk);
+  float* sums = reinterpret_cast<float*>(bal_smem);                // [kBalWarps][E] partial sums (phase 1: the histogram)
+  float* su = sums + kBalWarps * E;                                // [E] u of the current sequence
+  float* ring = su + (E + 3) / 4 * 4 + static_cast<size_t>(warp) * ST * kTile * E;
   auto barrier = [&](int nth) -> bool {
     if (G == 1) {
       __syncthreads();
       return true;
     }
+    if (G <= kBalCluster) {
+      cluster_sync();
+      return true;
+    }
     return grid_barrier(w.ctrl, nth * G, a.timeout_ns, a.err, &s_ok);
   };
-  if (G == 1) {  // nothing was cleared for a single block
+  if (tid == 0) s_abort = s_n = 0;
+  if (VEC && lane < ST) mbar_init(&full[warp][lane], 1);
+  fence_mbar_init();
+  int* hist = reinterpret_cast<int*>(sums);
+  for (int e = tid; e < E; e += kBalThreads) hist[e] = 0;
+  if (G <= kBalCluster) {  // a small grid clears its own workspace
     int* z = w.ctrl;
-    for (size_t i = tid; i < w.zeroed / sizeof(int); i += kBalThreads) z[i] = 0;
+    for (size_t i = blockIdx.x * kBalThreads + tid; i < w.zeroed / sizeof(int); i += static_cast<size_t>(G) * kBalThreads)
+      z[i] = 0;
+    barrier(0);
+  } else {
     __syncthreads();
   }
-  if (a.seq_off) {  // offsets: from 0 to T, never falling
-    for (int b = blockIdx.x * kBalThreads + tid; b <= a.B; b += G * kBalThreads) {
-      const int o = a.seq_off[b];
-      if ((b == 0 && o != 0) || (b == a.B && o != T) || (b > 0 && a.seq_off[b - 1] > o)) set_error(a.err, DERR_BAD_OFFSETS);
-    }
-  }
-  Piece pc;
   // (1) counts
-  int* hist = reinterpret_cast<int*>(bal_smem);
-  for (int e = tid; e < E; e += kBalThreads) hist[e] = 0;
-  if (tid == 0) s_n = 0;
-  __syncthreads();
+  Piece pc;
   pc.first(a, c0);
   while (pc.next(a, c1)) {
     const int pairs = (pc.t1 - pc.t0) * K;
     const int32_t* ids = a.topk_ids + static_cast<long long>(pc.t0) * K;
     int n = 0;
-    for (int i = tid; i < pairs; i += kBalThreads) {
-      const int t = i / K;
-      if (a.mask && !a.mask[pc.t0 + t]) continue;
-      if (i - t * K == 0) ++n;
-      const int id = __ldg(ids + i);
-      if (id < 0 || id >= E) set_error(a.err, DERR_BAD_EXPERT);
-      else atomicAdd(&hist[id], 1);
+    for (int i0 = tid; i0 < pairs; i0 += 4 * kBalThreads) {
+      int id[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {  // four loads in flight
+        const int i = i0 + k * kBalThreads;
+        id[k] = -1;
+        if (i >= pairs) continue;
+        const int t = static_cast<int>(static_cast<unsigned>(i) / static_cast<unsigned>(K));
+        id[k] = __ldg(ids + i);
+        if (a.mask && !a.mask[pc.t0 + t]) {
+          id[k] = -1;
+          continue;
+        }
+        if (i - t * K == 0) ++n;
+        if (id[k] < 0 || id[k] >= E) {
+          set_error(a.err, DERR_BAD_EXPERT);
+          id[k] = -1;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (id[k] >= 0) atomicAdd(&hist[id[k]], 1);
     }
     n = __reduce_add_sync(0xffffffffu, n);
     if (lane == 0 && n) atomicAdd(&s_n, n);
@@ -165,213 +270,301 @@ __global__ void __launch_bounds__(kBalThreads) balance_kernel(const BalanceArgs 
     }
     __syncthreads();
   }
-  if (!barrier(1)) return;
-  // (2) the pass over the logits
-  float nf = 0.0f, used = 0.0f;  // valid tokens, sequences with any
-  for (int b = tid; b < a.B; b += kBalThreads) {
-    const int n = __ldcg(w.nvalid + b);
-    nf += static_cast<float>(n);
-    used += n > 0 ? 1.0f : 0.0f;
+  // the first tiles of logits come while the blocks wait for one another
+  Tiles<kTile> in;  // lane 0's next tile to ask for
+  int st_in = 0;
+  auto issue = [&]() {
+    const uint32_t bytes = static_cast<uint32_t>(min(kTile, in.pc.t1 - in.tb)) * E * 4;
+    mbar_arrive_expect_tx(&full[warp][st_in], bytes);
+    bulk_load(ring + static_cast<size_t>(st_in) * kTile * E, a.logits + static_cast<long long>(in.tb) * E, bytes,
+              &full[warp][st_in]);
+    if (++st_in == ST) st_in = 0;
+    in.next(a, c1, warp);
+  };
+  if (VEC && lane == 0) {
+    in.first(a, c0, c1, warp);
+    for (int k = 0; k < ST && in.ok; ++k) issue();
   }
-  nf = block_sum(nf, s_red);
-  used = block_sum(used, s_red);
+  const bool counted = barrier(1);  // where it gave up: run on, so that every copy is waited for
+  // (2) the pass over the logits
+  float2 nu = make_float2(0.0f, 0.0f);  // counted tokens, sequences with any
+  if (a.B == 1) {
+    nu.x = static_cast<float>(__ldcg(w.nvalid));
+    nu.y = nu.x > 0.0f ? 1.0f : 0.0f;
+  } else {
+    for (int b = tid; b < a.B; b += kBalThreads) {
+      const int n = __ldcg(w.nvalid + b);
+      nu.x += static_cast<float>(n);
+      nu.y += n > 0 ? 1.0f : 0.0f;
+    }
+    nu = block_sum2(nu.x, nu.y, s_red);
+  }
   const float scale = a.dloss ? __ldg(a.dloss) : 1.0f;
-  const float zc = nf > 0.0f ? 2.0f * a.z_coef * scale / nf : 0.0f;
+  const float zc = nu.x > 0.0f ? 2.0f * a.z_coef * scale / nu.x : 0.0f;
+  constexpr float kLog2e = 1.4426950408889634f;
   const int sl = lane & (LPT - 1), sub = lane / LPT;
+  auto expert = [&](int i) { return VEC ? 4 * (sl + LPT * (i / 4)) + i % 4 : sl + LPT * i; };  // of a lane's i-th logit
+  int st = 0, ph = 0;
+  // the counts of a piece's sequence are fetched while the piece before it is worked on (experts tid and tid + 512)
+  Piece pn;
+  int nb_next = 0, cnt_next[2] = {0, 0};
+  auto fetch = [&]() {
+    if (!pn.next(a, c1)) return;
+    nb_next = __ldcg(w.nvalid + pn.b);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int e = tid + k * kBalThreads;
+      if (e < E) cnt_next[k] = __ldcg(w.cnt + static_cast<long long>(pn.b) * E + e);
+    }
+  };
+  pn.first(a, c0);
+  fetch();
   pc.first(a, c0);
   while (pc.next(a, c1)) {
-    const int nb = __ldcg(w.nvalid + pc.b);
-    float acc[NV * W], cf[NV * W];
-    float zs = 0.0f;
+    const int nb = nb_next;
+    const float inv_kn = nb > 0 ? 1.0f / (static_cast<float>(K) * static_cast<float>(nb)) : 0.0f;
 #pragma unroll
-    for (int i = 0; i < NV * W; ++i) acc[i] = cf[i] = 0.0f;
-    if (a.dlogits && nb > 0) {
-      // alpha E / (B' n_b) (counts / (K n_b) - 1 / E), from the whole number counts E - K n_b
-      const float kn = static_cast<float>(K) * static_cast<float>(nb);
-      const float s0 = a.balance_coef * scale / (used * static_cast<float>(nb) * kn);
-#pragma unroll
-      for (int i = 0; i < NV * W; ++i) {
-        const int e = VEC ? 4 * (sl + LPT * (i / W)) + i % W : sl + LPT * i;
-        if (e < E) {
-          const long long c = __ldcg(w.cnt + static_cast<long long>(pc.b) * E + e);
-          cf[i] = s0 * static_cast<float>(c * E - static_cast<long long>(K) * nb);
-        }
-      }
+    for (int k = 0; k < 2; ++k) {
+      const int e = tid + k * kBalThreads;
+      if (e < E)
+        su[e] = static_cast<float>(static_cast<long long>(cnt_next[k]) * E - static_cast<long long>(K) * nb) * inv_kn;
     }
-    for (int tb = pc.t0 + (warp * kTok + sub); tb - sub < pc.t1; tb += kBalWarps * kTok * UN) {
-      float v[UN][NV * W];
-      bool ok[UN];
+    __syncthreads();
+    fetch();
+    f32x2 acc[kPairs], u[kPairs];  // a lane's logits in pairs
+    float zs = 0.0f, bs = 0.0f;
 #pragma unroll
-      for (int u = 0; u < UN; ++u) {
-        const int t = tb + u * kBalWarps * kTok;
-        ok[u] = t < pc.t1;
-        const bool on = ok[u] && (!a.mask || a.mask[t]);
-        const float* row = a.logits + static_cast<long long>(t) * E;
+    for (int i = 0; i < kPairs; ++i) {
+      const int e0 = expert(2 * i), e1 = expert(2 * i + 1);
+      acc[i] = pack2(0.0f, 0.0f);
+      u[i] = pack2(e0 < E ? su[e0] : 0.0f, e1 < E ? su[e1] : 0.0f);
+    }
+    const float cb = nb > 0 ? a.balance_coef * scale / (nu.y * static_cast<float>(nb)) : 0.0f;
+    for (int tb = pc.t0 + warp * kTile; tb < pc.t1; tb += kBalWarps * kTile) {
+      const float* src = ring + static_cast<size_t>(st) * kTile * E;
+      const unsigned here = __ballot_sync(0xffffffffu, lane < kTile && tb + lane < pc.t1 && (!a.mask || a.mask[tb + lane]));
+      if (VEC) mbar_wait(&full[warp][st], ph, &s_abort, a.timeout_ns, a.err);
+      // the UN tokens of a lane go through every step together, which hides the latency of the lane sums
+      f32x2 v[UN][kPairs];
+      float m[UN], z[UN], dot[UN];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          const int e = VEC ? 4 * (sl + LPT * i) : sl + LPT * i;
-          if (on && e < E) {
-            if constexpr (VEC) {
-              const float4 q = __ldcs(reinterpret_cast<const float4*>(row + e));
-              v[u][4 * i] = q.x; v[u][4 * i + 1] = q.y; v[u][4 * i + 2] = q.z; v[u][4 * i + 3] = q.w;
-            } else {
-              v[u][i] = __ldcs(row + e);
-            }
+      for (int g = 0; g < UN; ++g) {
+        const int r = g * kTok + sub;
+        const bool on = (here >> r) & 1;
+        m[g] = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < kPairs; i += 2) {
+          float4 q = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+          if constexpr (VEC) {
+            if (on && expert(2 * i) < E) q = *reinterpret_cast<const float4*>(src + r * E + expert(2 * i));
           } else {
-#pragma unroll
-            for (int k = 0; k < W; ++k) v[u][W * i + k] = -INFINITY;
+            const float* row = a.logits + static_cast<long long>(tb + r) * E;
+            if (on && expert(2 * i) < E) q.x = __ldcs(row + expert(2 * i));
+            if (on && expert(2 * i + 1) < E) q.y = __ldcs(row + expert(2 * i + 1));
+            if (on && expert(2 * i + 2) < E) q.z = __ldcs(row + expert(2 * i + 2));
+            if (on && expert(2 * i + 3) < E) q.w = __ldcs(row + expert(2 * i + 3));
           }
+          m[g] = fmaxf(m[g], fmaxf(fmaxf(q.x, q.y), fmaxf(q.z, q.w)));
+          v[g][i] = pack2(q.x, q.y);
+          v[g][i + 1] = pack2(q.z, q.w);
         }
       }
 #pragma unroll
-      for (int u = 0; u < UN; ++u) {
-        const int t = tb + u * kBalWarps * kTok;
-        float m = -INFINITY;
+      for (int g = 0; g < UN; ++g) {
+        m[g] = lanes_max<LPT>(m[g]);
+        if (m[g] == -INFINITY) m[g] = 0.0f;  // a token that does not count, or without a finite logit: all terms are zero
+        const f32x2 nm = pack2(-m[g], -m[g]), l2e = pack2(kLog2e, kLog2e);
+        f32x2 zz = pack2(0.0f, 0.0f), dd = zz;
 #pragma unroll
-        for (int i = 0; i < NV * W; ++i) m = fmaxf(m, v[u][i]);
-#pragma unroll
-        for (int o = LPT / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if (m == -INFINITY) m = 0.0f;  // a masked token, or one without a finite logit: all terms are zero
-        float z = 0.0f, dot = 0.0f;
-#pragma unroll
-        for (int i = 0; i < NV * W; ++i) {
-          v[u][i] = expf(v[u][i] - m);
-          z += v[u][i];
-          dot += v[u][i] * cf[i];
+        for (int i = 0; i < kPairs; ++i) {
+          const float2 x = unpack2(mul2(add2(v[g][i], nm), l2e));  // the difference first: m may be the type's lowest value
+          v[g][i] = pack2(exp2_approx(x.x), exp2_approx(x.y));
+          zz = add2(zz, v[g][i]);
+          dd = fma2(v[g][i], u[i], dd);
         }
+        const float2 zf = unpack2(zz), df = unpack2(dd);
+        z[g] = zf.x + zf.y;
+        dot[g] = df.x + df.y;
+      }
 #pragma unroll
-        for (int o = LPT / 2; o > 0; o >>= 1) {
-          z += __shfl_xor_sync(0xffffffffu, z, o);
-          dot += __shfl_xor_sync(0xffffffffu, dot, o);
-        }
-        const float inv = z == 0.0f ? 0.0f : 1.0f / z;
-        const float lse = z == 0.0f ? 0.0f : m + logf(z);
-        if (sl == 0) zs += lse * lse;
-        const float g0 = zc * lse - dot * inv;
+      for (int o = LPT / 2; o > 0; o >>= 1) {
 #pragma unroll
-        for (int i = 0; i < NV * W; ++i) {
-          v[u][i] *= inv;
-          acc[i] += v[u][i];
+        for (int g = 0; g < UN; ++g) {
+          z[g] += __shfl_xor_sync(0xffffffffu, z[g], o);
+          dot[g] += __shfl_xor_sync(0xffffffffu, dot[g], o);
         }
-        if (a.dlogits && ok[u]) {
+      }
+#pragma unroll
+      for (int g = 0; g < UN; ++g) {
+        const int t = tb + g * kTok + sub;
+        const float inv = z[g] == 0.0f ? 0.0f : __fdividef(1.0f, z[g]);  // z is between 1 and E
+        const float lse = z[g] == 0.0f ? 0.0f : m[g] + __logf(z[g]);
+        dot[g] *= inv;
+        if (sl == 0) {
+          zs += lse * lse;
+          bs += z[g] == 0.0f ? 0.0f : 1.0f + dot[g];
+        }
+        // dl = p (cb (u - dot) + zc lse) with p = v / z
+        const float g0 = inv * (zc * lse - cb * dot[g]), c1 = inv * cb;
+        const f32x2 inv2 = pack2(inv, inv), g2 = pack2(g0, g0), c2 = pack2(c1, c1);
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) {
+          acc[i] = fma2(v[g][i], inv2, acc[i]);
+          v[g][i] = mul2(v[g][i], fma2(c2, u[i], g2));
+        }
+        if (a.dlogits && t < pc.t1) {
           float* out = a.dlogits + static_cast<long long>(t) * E;
 #pragma unroll
-          for (int i = 0; i < NV; ++i) {
-            const int e = VEC ? 4 * (sl + LPT * i) : sl + LPT * i;
-            if (e < E) {
-              if constexpr (VEC)
-                *reinterpret_cast<float4*>(out + e) =
-                    make_float4(v[u][4 * i] * (cf[4 * i] + g0), v[u][4 * i + 1] * (cf[4 * i + 1] + g0),
-                                v[u][4 * i + 2] * (cf[4 * i + 2] + g0), v[u][4 * i + 3] * (cf[4 * i + 3] + g0));
-              else
-                out[e] = v[u][i] * (cf[i] + g0);
+          for (int i = 0; i < kPairs; i += 2) {
+            const float2 lo = unpack2(v[g][i]), hi = unpack2(v[g][i + 1]);
+            if constexpr (VEC) {
+              if (expert(2 * i) < E)
+                *reinterpret_cast<float4*>(out + expert(2 * i)) = make_float4(lo.x, lo.y, hi.x, hi.y);
+            } else {
+              if (expert(2 * i) < E) out[expert(2 * i)] = lo.x;
+              if (expert(2 * i + 1) < E) out[expert(2 * i + 1)] = lo.y;
+              if (expert(2 * i + 2) < E) out[expert(2 * i + 2)] = hi.x;
+              if (expert(2 * i + 3) < E) out[expert(2 * i + 3)] = hi.y;
             }
           }
+        }
+      }
+      if (VEC) {
+        __syncwarp();  // the stage has been read
+        if (lane == 0 && in.ok) issue();
+        if (++st == ST) {
+          st = 0;
+          ph ^= 1;
         }
       }
     }
     // close the piece: lane groups, then warps in order
 #pragma unroll
-    for (int o = LPT; o < 32; o <<= 1) {
-      zs += __shfl_xor_sync(0xffffffffu, zs, o);
+    for (int i = 0; i < kPairs; ++i) {
+      float2 x = unpack2(acc[i]);
 #pragma unroll
-      for (int i = 0; i < NV * W; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
-    }
-    if (sub == 0) {
-#pragma unroll
-      for (int i = 0; i < NV * W; ++i) {
-        const int e = VEC ? 4 * (sl + LPT * (i / W)) + i % W : sl + LPT * i;
-        if (e < E) bal_smem[warp * E + e] = acc[i];
+      for (int o = LPT; o < 32; o <<= 1) {
+        x.x += __shfl_xor_sync(0xffffffffu, x.x, o);
+        x.y += __shfl_xor_sync(0xffffffffu, x.y, o);
       }
+      if (sub == 0 && expert(2 * i) < E) sums[warp * E + expert(2 * i)] = x.x;
+      if (sub == 0 && expert(2 * i + 1) < E) sums[warp * E + expert(2 * i + 1)] = x.y;
     }
-    const float zsum = block_sum(lane == 0 ? zs : 0.0f, s_red);
+    const float2 part = block_sum2(zs, bs, s_red);
     const long long piece = static_cast<long long>(blockIdx.x) + pc.b;
     for (int e = tid; e < E; e += kBalThreads) {
       float s = 0.0f;
 #pragma unroll
-      for (int i = 0; i < kBalWarps; ++i) s += bal_smem[i * E + e];
+      for (int i = 0; i < kBalWarps; ++i) s += sums[i * E + e];
       w.ppart[piece * E + e] = s;
     }
-    if (tid == 0) w.zpart[piece] = zsum;
-    __syncthreads();
+    if (tid == 0) {
+      w.zpart[piece] = part.x;
+      w.bpart[piece] = nb > 0 ? part.y / static_cast<float>(nb) : 0.0f;
+    }
   }
-  if (!barrier(2)) return;
-  // (3) mean probabilities, counts, the loss: 32 experts of one sequence at a time, a warp for every 16th piece
+  if (a.seq_off) {  // offsets: from 0 to T, never falling
+    for (int b = blockIdx.x * kBalThreads + tid; b <= a.B; b += G * kBalThreads) {
+      const int o = a.seq_off[b];
+      if ((b == 0 && o != 0) || (b == a.B && o != T) || (b > 0 && a.seq_off[b - 1] > o)) set_error(a.err, DERR_BAD_OFFSETS);
+    }
+  }
+  if (VEC && s_abort) {  // a wait gave up: let this warp's copies in flight land
+    volatile int never = 0;
+    if (lane == 0)
+      for (int k = 0; k < ST; ++k) mbar_wait(&full[warp][k], k < st ? ph : ph ^ 1, &never, 20000000ull, nullptr);
+    __syncwarp();
+  }
+  if (!barrier(2) || !counted || s_abort) return;
+  // (3) mean probabilities and counts, 32 experts of one sequence at a time: a block for such a unit, its warps sharing
+  // the pieces, while there are no more units than blocks, else a warp
   const int et = (E + 31) / 32;
   const long long units = static_cast<long long>(a.B) * et;
-  for (long long un = blockIdx.x; un < units; un += G) {
+  const bool shared = units <= G;
+  const long long u0 = shared ? blockIdx.x : static_cast<long long>(blockIdx.x) * kBalWarps + warp;
+  for (long long un = u0; un < units; un += shared ? G : static_cast<long long>(G) * kBalWarps) {
     const int b = static_cast<int>(un / et), e = static_cast<int>(un % et) * 32 + lane;
     const int o0 = seq_begin(a, b), o1 = seq_begin(a, b + 1);
     float s = 0.0f;
-    if (o1 > o0 && e < E)
-      for (int c = o0 / chunk + warp; c <= (o1 - 1) / chunk; c += kBalWarps)
-        s += __ldcg(w.ppart + (static_cast<long long>(c) + b) * E + e);
-    s_tile[warp][lane] = s;
-    __syncthreads();
-    if (warp == 0) {
+    if (o1 > o0 && e < E) {
+      const float* src = w.ppart + static_cast<long long>(b) * E + e;
+      const int last = (o1 - 1) / chunk, by = shared ? kBalWarps : 1;
+      int c = o0 / chunk + (shared ? warp : 0);
+      for (; c + 3 * by <= last; c += 4 * by) {
+        float x[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[k] = __ldcg(src + static_cast<long long>(c + k * by) * E);
+        s += (x[0] + x[1]) + (x[2] + x[3]);
+      }
+      for (; c <= last; c += by) s += __ldcg(src + static_cast<long long>(c) * E);
+    }
+    if (shared) {
+      s_tile[warp][lane] = s;
+      __syncthreads();
       s = 0.0f;
 #pragma unroll
       for (int i = 0; i < kBalWarps; ++i) s += s_tile[i][lane];
-      const int n = __ldcg(w.nvalid + b);
-      float term = 0.0f;
-      if (e < E) {
-        const int cnt = __ldcg(w.cnt + static_cast<long long>(b) * E + e);
-        const float p = n > 0 ? s / static_cast<float>(n) : 0.0f;
-        a.probs[static_cast<long long>(b) * E + e] = p;
-        a.counts[static_cast<long long>(b) * E + e] = cnt;
-        if (n > 0) term = static_cast<float>(cnt) * p * (static_cast<float>(E) / (static_cast<float>(K) * static_cast<float>(n)));
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) term += __shfl_xor_sync(0xffffffffu, term, o);
-      if (lane == 0) w.lpart[un] = term;
     }
-    __syncthreads();
+    if ((!shared || warp == 0) && e < E) {
+      const int n = __ldcg(w.nvalid + b);
+      a.probs[static_cast<long long>(b) * E + e] = n > 0 ? s / static_cast<float>(n) : 0.0f;
+      a.counts[static_cast<long long>(b) * E + e] = __ldcg(w.cnt + static_cast<long long>(b) * E + e);
+    }
+    if (shared) __syncthreads();
   }
-  if (tid == 0) {
-    __threadfence();
-    s_n = atomicAdd(w.ctrl + 1, 1);
-    __threadfence();
+  if (blockIdx.x != G - 1) return;
+  float2 l = make_float2(0.0f, 0.0f);
+  for (int i = tid; i < G + a.B; i += kBalThreads) {
+    l.x += __ldcg(w.zpart + i);
+    l.y += __ldcg(w.bpart + i);
   }
-  __syncthreads();
-  if (s_n != G - 1) return;
-  float bl = 0.0f, zl = 0.0f;
-  for (long long i = tid; i < units; i += kBalThreads) bl += __ldcg(w.lpart + i);
-  for (int i = tid; i < G + a.B; i += kBalThreads) zl += __ldcg(w.zpart + i);
-  bl = block_sum(bl, s_red);
-  zl = block_sum(zl, s_red);
+  l = block_sum2(l.x, l.y, s_red);
   if (tid == 0) {
-    bl = used > 0.0f ? bl / used : 0.0f;
-    zl = nf > 0.0f ? zl / nf : 0.0f;
-    a.loss[0] = a.balance_coef * bl + a.z_coef * zl;
+    const float bl = nu.y > 0.0f ? l.y / nu.y : 0.0f, zl = nu.x > 0.0f ? l.x / nu.x : 0.0f;
+    // a loss that is switched off adds nothing, whatever its value
+    a.loss[0] = (a.balance_coef != 0.0f ? a.balance_coef * bl : 0.0f) + (a.z_coef != 0.0f ? a.z_coef * zl : 0.0f);
     a.loss[1] = bl;
     a.loss[2] = zl;
   }
 }
 
-template <bool VEC, int LPT, int NV, int UN>
+template <bool VEC, int LPT, int NV, int UN, int ST>
 cudaError_t run_balance(const BalanceArgs& a, void* ws, int num_sms, cudaStream_t s) {
-  auto kern = balance_kernel<VEC, LPT, NV, UN>;
-  const size_t smem = sizeof(float) * kBalWarps * a.E;
+  auto kern = balance_kernel<VEC, LPT, NV, UN, ST>;
+  constexpr int kTile = 32 / LPT * UN;
+  const size_t smem = sizeof(float) * (kBalWarps * static_cast<size_t>(a.E) * (1 + (VEC ? ST * kTile : 0)) + (a.E + 3) / 4 * 4);
   cudaError_t st = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (st != cudaSuccess) return st;
+  if ((st = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess) return st;
   const BalWs w = carve_balance(ws, a.T, a.E, a.B);
-  const long long per = static_cast<long long>(kBalWarps) * (32 / LPT);  // tokens a block takes at once
-  long long G = (a.T + per - 1) / per;
-  if (G > num_sms) G = num_sms;  // one block an SM: all of them resident
-  if (G > kBalMaxBlocks) G = kBalMaxBlocks;
-  if (G < 1) G = 1;
+  const long long want = (a.T + kBalWarps * kTile - 1) / (kBalWarps * kTile);  // blocks that give every warp a tile
+  long long G;
+  if (a.T * a.E <= kBalOneCluster) {
+    for (G = 1; G < kBalCluster && G < want; G *= 2) {
+    }
+  } else {
+    G = want < num_sms ? want : num_sms;  // one block an SM: all of them resident
+    if (G > kBalMaxBlocks) G = kBalMaxBlocks;
+    if (G <= kBalCluster) G = kBalCluster;
+  }
   const int chunk = a.T > 0 ? static_cast<int>((a.T + G - 1) / G) : 1;
-  if (G > 1 && (st = cudaMemsetAsync(w.ctrl, 0, w.zeroed, s)) != cudaSuccess) return st;
+  if (G > kBalCluster && (st = cudaMemsetAsync(w.ctrl, 0, w.zeroed, s)) != cudaSuccess) return st;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeCooperative;
-  attr[0].val.cooperative = 1;
+  if (G > kBalCluster) {
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+  } else {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(G);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  }
   cfg.gridDim = dim3(static_cast<unsigned>(G), 1, 1);
   cfg.blockDim = dim3(kBalThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = G > 1 ? 1 : 0;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, a, w, chunk);
 }
 
@@ -382,12 +575,14 @@ size_t balance_ws_bytes(long long T, int E, int B) { return carve_balance(nullpt
 cudaError_t launch_balance_loss(const BalanceArgs& a, void* ws, int num_sms, cudaStream_t s) {
   const bool vec = a.E % 4 == 0 && (reinterpret_cast<uintptr_t>(a.logits) & 15) == 0 &&
                    (reinterpret_cast<uintptr_t>(a.dlogits) & 15) == 0;
-  if (!vec) return a.E <= 128 ? run_balance<false, 32, 4, 2>(a, ws, num_sms, s) : run_balance<false, 32, 32, 1>(a, ws, num_sms, s);
-  if (a.E <= 32) return run_balance<true, 8, 1, 2>(a, ws, num_sms, s);
-  if (a.E <= 128) return run_balance<true, 32, 1, 2>(a, ws, num_sms, s);
-  if (a.E <= 256) return run_balance<true, 32, 2, 2>(a, ws, num_sms, s);
-  if (a.E <= 512) return run_balance<true, 32, 4, 2>(a, ws, num_sms, s);
-  return run_balance<true, 32, 8, 1>(a, ws, num_sms, s);
+  if (!vec)
+    return a.E <= 128 ? run_balance<false, 32, 4, 1, 1>(a, ws, num_sms, s) : run_balance<false, 32, 32, 1, 1>(a, ws, num_sms, s);
+  if (a.E <= 32) return run_balance<true, 8, 1, 4, 4>(a, ws, num_sms, s);
+  if (a.E <= 64) return run_balance<true, 16, 1, 4, 4>(a, ws, num_sms, s);
+  if (a.E <= 128) return run_balance<true, 32, 1, 4, 4>(a, ws, num_sms, s);
+  if (a.E <= 256) return run_balance<true, 32, 2, 2, 4>(a, ws, num_sms, s);
+  if (a.E <= 512) return run_balance<true, 32, 4, 2, 2>(a, ws, num_sms, s);
+  return run_balance<true, 32, 8, 1, 2>(a, ws, num_sms, s);
 }
 
 }  // namespace vgg
