@@ -102,7 +102,7 @@ def test_router_backward_refusals(L, fake, bad):
 
 def test_router_workspace(L):
     f = L.moe_router_backward_workspace_bytes
-    assert f(100, 64, 8) == 128 * 8 * 2 * 2 + 16 * 64 * 8 * 4 and f(0, 64, 8) == 16 * 64 * 8 * 4
+    assert f(100, 64, 8) == 128 * 8 * 2 * 3 + 16 * 64 * 8 * 4 and f(0, 64, 8) == 16 * 64 * 8 * 4
     assert f(-1, 64, 8) == f(16, 60, 8) == f(16, 64, 9) == 0
 
 

@@ -1661,13 +1661,6 @@ int moe_balance_loss(moe_ctx* ctx, const float* logits, const int32_t* topk_ids,
   return MOE_OK;
 }
 
-// Splits of the reduction over tokens in dW_r = X^T dlogits: enough for every SM.
-static int router_bwd_split(int Tp, int d, int E, int num_sms) {
-  const int tiles = ceil_div(d, BM) * ceil_div(E, gemm_bn(E));
-  const int split = std::max(1, std::min(num_sms / std::max(tiles, 1), kMaxSplitK));
-  return std::max(1, std::min(split, ceil_div(2 * Tp, 8 * BK)));
-}
-
 static bool router_bwd_sizes_ok(int T, int d, int E) {
   return T >= 0 && T <= 65536 && d >= 64 && d % 64 == 0 && E >= 8 && E % 8 == 0 && E <= kMaxGroups;
 }
@@ -1675,7 +1668,7 @@ static bool router_bwd_sizes_ok(int T, int d, int E) {
 size_t moe_router_backward_workspace_bytes(int T, int d, int E) {
   if (!router_bwd_sizes_ok(T, d, E)) return 0;
   const size_t Tp = static_cast<size_t>(ceil_div(T, 64)) * 64;
-  return al(sizeof(__nv_bfloat16) * 2 * Tp * E) + al(sizeof(float) * static_cast<size_t>(kMaxSplitK) * d * E);
+  return al(sizeof(__nv_bfloat16) * 3 * Tp * E) + al(sizeof(float) * static_cast<size_t>(kMaxRouterSplit) * d * E);
 }
 
 int moe_router_backward(moe_ctx* ctx, const float* dlogits, const void* X, const void* W_r, int T, int d, int E,
@@ -1691,12 +1684,11 @@ int moe_router_backward(moe_ctx* ctx, const float* dlogits, const void* X, const
   VGG_REQUIRE(g.ok);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int Tp = ceil_div(T, 64) * 64;
-  __nv_bfloat16* hi = static_cast<__nv_bfloat16*>(ws);
-  __nv_bfloat16* lo = hi + static_cast<size_t>(Tp) * E;
-  float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + al(sizeof(__nv_bfloat16) * 2 * static_cast<size_t>(Tp) * E));
-  if (T > 0) VGG_LAUNCH("split_dlogits", launch_split_dlogits(dlogits, T, Tp, E, hi, lo, s));
+  __nv_bfloat16* parts = static_cast<__nv_bfloat16*>(ws);
+  float* sums = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + al(sizeof(__nv_bfloat16) * 3 * static_cast<size_t>(Tp) * E));
+  if (T > 0) VGG_LAUNCH("split_dlogits", launch_split_dlogits(dlogits, T, Tp, E, parts, s));
   if (T > 0 && dX) {
-    // dX = dX_in + hi W_r^T: one bf16 rounding of dlogits (relative 2^-9 of each term) under a bf16 result
+    // dX = dX_in + hi W_r^T: one bf16 rounding of dlogits (2^-8 of a term at most) under a bf16 result
     GemmParams p = base_params(ctx);
     p.M = T;
     p.N = d;
@@ -1704,11 +1696,12 @@ int moe_router_backward(moe_ctx* ctx, const float* dlogits, const void* X, const
     p.groups = 1;
     p.out0 = dX;
     p.ld_out = d;
-    p.add = static_cast<const __nv_bfloat16*>(dX_in);
+    p.add = dX_in != nullptr;
     const int BN = gemm_bn(d);
     Maps m = zero_maps();
-    if (!make_map_2d(&m.a0, hi, E, T, E, BM) || !make_map_3d(&m.b0, W_r, E, d, 1, BN) ||
-        !make_store_map_3d(&m.o0, dX, false, d, T, 1, 64))
+    if (!make_map_2d(&m.a0, parts, E, T, E, BM) || !make_map_3d(&m.b0, W_r, E, d, 1, BN) ||
+        !make_store_map_3d(&m.o0, dX, false, d, T, 1, 64) ||
+        (dX_in && !make_store_map_3d(&m.o1, const_cast<void*>(dX_in), false, d, T, 1, 64)))
       return MOE_ERR_CUDA;
     m.a1 = m.a0;
     m.b1 = m.b0;
@@ -1716,31 +1709,12 @@ int moe_router_backward(moe_ctx* ctx, const float* dlogits, const void* X, const
     VGG_LAUNCH("router_dx", run_dense_add(BN, p, m, std::min(tiles, ctx->num_sms), s));
   }
   if (dW_r) {
-    // dW_r = dW_r_in + X^T (hi + lo), split over tokens; one reduction over 2 Tp rows, X read twice (rows past
-    // T of X are the map's zero fill, of hi and lo zero)
-    int split = 0;
-    if (T > 0) {
-      split = router_bwd_split(Tp, d, E, ctx->num_sms);
-      GemmParams p = base_params(ctx);
-      p.M = d;
-      p.N = E;
-      p.K = 2 * Tp;
-      p.groups = 1;
-      p.a_kwrap = Tp;
-      p.split_k = split;
-      p.ld_out = E;
-      p.out0 = part;
-      const int BN = gemm_bn(E);
-      Maps m = zero_maps();
-      if (!make_map_2d(&m.a0, X, d, T, d, 64) || !make_map_2d(&m.b0, hi, E, 2 * static_cast<uint64_t>(Tp), E, 64) ||
-          !make_store_map_3d(&m.o0, part, true, E, d, split, 32))
-        return MOE_ERR_CUDA;
-      m.a1 = m.a0;
-      m.b1 = m.b0;
-      const int tiles = ceil_div(d, BM) * ceil_div(E, BN);
-      VGG_LAUNCH("router_dw", run_dense_mn_store(BN, p, m, std::min(tiles * split, ctx->num_sms), s));
-    }
-    VGG_LAUNCH("router_dw_reduce", launch_splitk_reduce_add(part, split, static_cast<long long>(d) * E, dW_r_in, dW_r, s));
+    // dW_r = dW_r_in + X^T dlogits, split over tokens (rows past T of X are the map's zero fill, of the parts zero)
+    int splits = 0;
+    if (T > 0)
+      VGG_LAUNCH("router_dw", launch_router_dw(static_cast<const __nv_bfloat16*>(X), parts, T, Tp, d, E, dX == nullptr,
+                                               ctx->num_sms, sums, &splits, ctx->d_err, ctx->timeout_ns, s));
+    VGG_LAUNCH("router_dw_reduce", launch_router_dw_reduce(sums, splits, d, E, dW_r_in, dW_r, s));
   }
   return MOE_OK;
 }

@@ -57,8 +57,8 @@ enum VarMode { VAR_M = 0, VAR_K = 1, VAR_NONE = 2 };
 // epilogues of the e4m3 form (operands are e4m3 codes of per-row-scaled rows; the accumulator is
 // multiplied by the A row's scale and the output channel's scale first).
 // EPI_DSWIGLU_Q: the dSwiGLU epilogue of the e4m3 form (the accumulator times q_row[row] q_col[column]).
-// EPI_ADD: the plain bf16 epilogue of a dense product with a bf16 matrix (add, or none) added to it in fp32; N a
-// multiple of 64.
+// EPI_ADD: the plain bf16 epilogue of a dense product with a bf16 matrix (map o1, boxes as the store's) added to it in
+// fp32; N a multiple of 64.
 // Extra forms (bit flags):
 //   X_DUAL_A  the A operand arrives as a bf16 high part (maps a0/a1) and the bf16 rounding of the rest
 //             (maps a2/a3, the same coordinates); every K step issues two UMMAs into one accumulator, so
@@ -134,7 +134,7 @@ struct GemmParams {
   float* part;  // dSwiGLU epilogue: per-row partial dot products [rows][part_ld]
   int part_ld;
   const float* col_bias;
-  const __nv_bfloat16* add;  // EPI_ADD: [M][ld_out], may be the output itself (a thread reads what it will store)
+  int add;  // EPI_ADD: add the matrix of map o1 (it may be the output itself: a warp reads what it will store)
   const float* q_row;  // e4m3 dSwiGLU: A row scales [rows], B row scales [groups][q_ld]
   const float* q_col;
   int q_ld;
@@ -530,6 +530,10 @@ __global__ void __launch_bounds__(WarpPlan<STAGES, EW, AMODE, BMODE, CN, XF>::kT
   const int* s_off = (VAR == VAR_NONE) ? s_off_sm : p.offsets;
   int* s_tile = s_off_sm;  // varlen-M: first tile of every group, [groups + 1]
 
+  constexpr int kAddBufs = EPI == EPI_ADD ? BN / (EW == 8 ? 128 : 64) : 1;  // a warp's column blocks of a tile
+  static_assert(EPI != EPI_ADD || DEPTH == kAddBufs, "the adding epilogue: a staging buffer for every 64 columns");
+  __shared__ uint64_t add_bar[EPI == EPI_ADD ? EW * kAddBufs : 1];
+
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
   const int lane = tid & 31;
@@ -542,6 +546,8 @@ __global__ void __launch_bounds__(WarpPlan<STAGES, EW, AMODE, BMODE, CN, XF>::kT
       mbar_init(&empty_bar[s], kPair ? 1 : CN);  // every CTA of the cluster releases the stage (a pair: one UMMA commit)
       if (kRelay) mbar_init(&gath_bar[s], kGW * 32);
     }
+    if constexpr (EPI == EPI_ADD)
+      for (int b = 0; b < EW * kAddBufs; ++b) mbar_init(&add_bar[b], 1);
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull_bar[b], 1);
       mbar_init(&tempty_bar[b], (kPair ? 2 : 1) * EW * 32);  // a pair: both CTAs' epilogues drain the tile
@@ -608,6 +614,10 @@ __global__ void __launch_bounds__(WarpPlan<STAGES, EW, AMODE, BMODE, CN, XF>::kT
     __syncthreads();
     tc_fence_after();
     cluster_sync();
+  }
+  if constexpr (EPI == EPI_ADD) {  // a dependent launch: the kernel ahead writes A; the one behind may count on its end
+    griddep_wait();
+    griddep_launch();
   }
   const uint32_t tmem_base = *s_tmem;
   const uint32_t cta_rank = kPair ? cluster_ctarank() : 0;
@@ -1151,6 +1161,30 @@ __global__ void __launch_bounds__(WarpPlan<STAGES, EW, AMODE, BMODE, CN, XF>::kT
         bulk_commit();
       }
     };
+    // EPI_ADD: this warp's boxes of the added matrix for a tile, each once the store out of its buffer has been read
+    uint32_t add_phase = 0, add_asked = 0;  // (asked: in lane 0)
+    auto load_add = [&](const Tile& x) {
+      if constexpr (EPI == EPI_ADD) {
+        if (lane == 0) {
+          bulk_wait_read<0>();
+          const int c0 = x.n0 + half * 64 * kAddBufs;
+          for (int q = 0; q < kAddBufs && c0 + 64 * q < p.N; ++q) {
+            uint64_t* bar = &add_bar[warp * kAddBufs + q];
+            mbar_arrive_expect_tx(bar, kStgBuf);
+            add_asked |= 1u << q;
+            tma_load_3d(stg_base + q * kStgBuf, &mp.o1, bar, c0 + 64 * q, x.m0 + quarter * 32, 0);
+          }
+        }
+      }
+    };
+    if constexpr (EPI == EPI_ADD) {
+      if (p.add && sch.first < sch.total) {
+        Tile x;
+        int gn = 0;
+        sch.decode(p, sch.first, gn, x);
+        load_add(x);
+      }
+    }
     // 32 columns (fp32, or bf16 through a 64-byte-swizzled box)
     auto emit32 = [&](const OutRef& o, const float (&v)[32], int col, int ncols, bool full, bool row_ok, bool fp32) {
       if (ncols <= 0) return;
@@ -1399,7 +1433,49 @@ __global__ void __launch_bounds__(WarpPlan<STAGES, EW, AMODE, BMODE, CN, XF>::kT
           o.c_z = tl.split;
           o.c_row = mw;
         }
-        if (VAR == VAR_K && mw >= p.M) {
+        if constexpr (EPI == EPI_ADD) {
+          // 64 columns at a time: the added matrix's box lies in the staging buffer of that column block (asked for
+          // when the buffer came free, a tile ahead); the sum replaces it there and leaves by a TMA store
+#pragma unroll 1
+          for (int q = 0; q < kAddBufs; ++q) {
+            const int col = tl.n0 + c_lo + 64 * q;
+            if (col >= p.N) break;
+            uint8_t* stg = stg_base + q * kStgBuf;
+            uint32_t r0[32], r1[32];
+            tmem_ld32(tbase + c_lo + 64 * q, r0);
+            tmem_ld32(tbase + c_lo + 64 * q + 32, r1);
+            if (p.add) {
+              mbar_wait(&add_bar[warp * kAddBufs + q], (add_phase >> q) & 1, s_abort, p.timeout_ns, p.err);
+              add_phase ^= 1u << q;
+              if (!*s_abort) add_asked &= ~(1u << q);
+            } else if (q == 0) {
+              if (lane == 0) bulk_wait_read<0>();  // the last tile's stores have been read out of the buffers
+              __syncwarp();
+            }
+            tmem_ld_wait();
+            uint8_t* row = stg + lane * 128;
+#pragma unroll
+            for (int c16 = 0; c16 < 8; ++c16) {
+              uint4* piece = reinterpret_cast<uint4*>(row + ((c16 ^ (lane & 7)) << 4));
+              const uint32_t* r = c16 < 4 ? r0 + 8 * c16 : r1 + 8 * (c16 - 4);
+              uint4 x = p.add ? *piece : make_uint4(0, 0, 0, 0);
+              uint32_t* xw = reinterpret_cast<uint32_t*>(&x);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float2 f = unpack_bf16x2(xw[k]);
+                xw[k] = pack_bf16x2(f.x + __uint_as_float(r[2 * k]), f.y + __uint_as_float(r[2 * k + 1]));
+              }
+              *piece = x;
+            }
+            issue_store(o, stg, col);
+          }
+          if (p.add && t + sch.stride < sch.total) {
+            Tile nx;
+            int gn = gcur;
+            sch.decode(p, t + sch.stride, gn, nx);
+            load_add(nx);
+          }
+        } else if (VAR == VAR_K && mw >= p.M) {
           // rows past the output (the odd CTA of a pair on the last row tile): nothing to store
         } else if (kTrans) {
           // Each 32 x 32 block leaves transposed: block row i = accumulator column col + i (an output
@@ -1448,13 +1524,6 @@ __global__ void __launch_bounds__(WarpPlan<STAGES, EW, AMODE, BMODE, CN, XF>::kT
           if (EPI == EPI_STORE_Q && VAR == VAR_M && row_ok) sr = __ldg(p.row_scale + s_off[tl.g] + m);
 #pragma unroll 1
           for (int c = c_lo; c < c_lo + kCols; c += 64) {
-            uint4 ad[EPI == EPI_ADD ? 8 : 1];
-            if constexpr (EPI == EPI_ADD) {  // in flight while the accumulator is read
-              const uint4* src = reinterpret_cast<const uint4*>(p.add + static_cast<long long>(m) * p.ld_out + tl.n0 + c);
-              const bool on = p.add && row_ok && tl.n0 + c < p.N;
-#pragma unroll
-              for (int i = 0; i < 8; ++i) ad[i] = on ? src[i] : make_uint4(0, 0, 0, 0);
-            }
             uint32_t r0[32], r1[32];
             tmem_ld32(tbase + c, r0);
             tmem_ld32(tbase + c + 32, r1);
@@ -1468,18 +1537,6 @@ __global__ void __launch_bounds__(WarpPlan<STAGES, EW, AMODE, BMODE, CN, XF>::kT
               if (p.col_bias) {
                 if (col + i < p.N) v[i] += __ldg(p.col_bias + col + i);
                 if (col + 32 + i < p.N) v[32 + i] += __ldg(p.col_bias + col + 32 + i);
-              }
-            }
-            if constexpr (EPI == EPI_ADD) {
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const uint32_t w[4] = {ad[i].x, ad[i].y, ad[i].z, ad[i].w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const float2 f = unpack_bf16x2(w[k]);
-                  v[8 * i + 2 * k] += f.x;
-                  v[8 * i + 2 * k + 1] += f.y;
-                }
               }
             }
             if (EPI == EPI_STORE_Q) {
@@ -1500,6 +1557,13 @@ __global__ void __launch_bounds__(WarpPlan<STAGES, EW, AMODE, BMODE, CN, XF>::kT
       tc_fence_before();
       if (kPair && cta_rank != 0) mbar_arrive_remote(mapa_shared(smem_u32(&tempty_bar[buf]), 0));
       else mbar_arrive(&tempty_bar[buf]);
+    }
+    if constexpr (EPI == EPI_ADD) {
+      if (lane == 0 && *s_abort) {  // let the boxes still asked for land before the CTA goes away
+        volatile int never = 0;
+        for (int q = 0; q < kAddBufs; ++q)
+          if ((add_asked >> q) & 1) mbar_wait(&add_bar[warp * kAddBufs + q], (add_phase >> q) & 1, &never, 20000000ull, nullptr);
+      }
     }
     if (lane == 0) bulk_wait0();
     __syncwarp();
@@ -1527,12 +1591,23 @@ cudaError_t launch_grouped_gemm(const GemmParams& p, const Maps& maps, int grid,
   if (e != cudaSuccess) return e;
   if (grid <= 0) return cudaSuccess;
   const int threads = WarpPlan<STAGES, EW, AMODE, BMODE, CN, XF>::kThreads;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  if constexpr (EPI == EPI_ADD) {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, p, maps);
+  }
   if (CN == 1) {
     kern<<<grid, threads, smem, stream>>>(p, maps);
     return cudaGetLastError();
   }
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = CN;
   attr[0].val.clusterDim.y = 1;

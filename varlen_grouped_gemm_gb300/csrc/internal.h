@@ -22,8 +22,10 @@ bool make_map_3d(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t rows,
 bool make_chunked_map_2d(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t rows, uint32_t box_chunks);
 bool make_chunked_map_3d(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t rows, uint64_t groups,
                          uint32_t box_chunks);
-bool make_store_map_2d(CUtensorMap* m, void* ptr, bool fp32, uint64_t cols, uint64_t rows, uint64_t row_stride_elems);
-bool make_store_map_3d(CUtensorMap* m, void* ptr, bool fp32, uint64_t cols, uint64_t rows, uint64_t depth);
+bool make_store_map_2d(CUtensorMap* m, void* ptr, bool fp32, uint64_t cols, uint64_t rows, uint64_t row_stride_elems,
+                       uint32_t box_cols);
+bool make_store_map_3d(CUtensorMap* m, void* ptr, bool fp32, uint64_t cols, uint64_t rows, uint64_t depth,
+                       uint32_t box_cols);
 
 // ---- grouped GEMM instantiations (BN chosen at run time: 128 or 256) -------------------------
 // forward
@@ -236,12 +238,16 @@ size_t balance_ws_bytes(long long T, int E, int B);
 cudaError_t launch_balance_loss(const BalanceArgs& a, void* ws, int num_sms, cudaStream_t s);
 
 // ---- router products -------------------------------------------------------------------------
-// dlogits [T][E] fp32 to bf16 high parts hi [Tp][E] and the bf16 rounding of the rest lo [Tp][E], rows past T zero.
-cudaError_t launch_split_dlogits(const float* dlogits, long long T, long long Tp, int E, __nv_bfloat16* hi,
-                                 __nv_bfloat16* lo, cudaStream_t s);
-// out[i] = in[i] (or 0) + sum_s part[s][i], s ascending.
-cudaError_t launch_splitk_reduce_add(const float* part, int splits, long long n, const float* in, float* out,
-                                     cudaStream_t s);
+// dlogits [T][E] fp32 to three bf16 parts [3][Tp][E] (high part, then the bf16 roundings of what is left), rows past T
+// zero.
+cudaError_t launch_split_dlogits(const float* dlogits, long long T, long long Tp, int E, __nv_bfloat16* parts, cudaStream_t s);
+// sums[s][e][i] = sum over the split's tokens of dlogits (from its parts) times X; *splits (at most kMaxRouterSplit).
+// Follows launch_split_dlogits (after_split) or run_dense_add after it on the stream.
+constexpr int kMaxRouterSplit = 16;
+cudaError_t launch_router_dw(const __nv_bfloat16* X, const __nv_bfloat16* parts, int T, int Tp, int d, int E, bool after_split,
+                             int num_sms, float* sums, int* splits, int* err, unsigned long long timeout_ns, cudaStream_t s);
+// out[i][e] = in[i][e] (or 0) + sum_s sums[s][e][i], s ascending.
+cudaError_t launch_router_dw_reduce(const float* sums, int splits, int d, int E, const float* in, float* out, cudaStream_t s);
 
 cudaError_t launch_wait_timeout_probe(int* err, unsigned long long timeout_ns, cudaStream_t s);
 

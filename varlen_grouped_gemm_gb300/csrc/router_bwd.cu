@@ -1,51 +1,310 @@
-// The elementwise steps of the router's gradient products: dlogits into two bf16 parts, and the split-K sums.
+// The router's products for an additional logit gradient: dlogits into three bf16 parts, dW_r = X^T dlogits from them
+// (dX = dlogits W_r^T runs on the shared GEMM template).  The launches of one call follow one another as dependent
+// launches: each sets itself up while the one ahead of it drains.
 #include "internal.h"
 
 namespace vgg {
 
-// Four values a thread (E is a multiple of 8).
+namespace {
+
+// x = hi + mid + lo with hi = bf16(x), mid = bf16(x - hi), lo = bf16(x - hi - mid): three times 8 bits hold an fp32
+// significand, so a product with a bf16 matrix in three bf16 multiplications has fp32 operands' precision (two parts
+// leave 2^-17 of a value, 2.4e-6 normwise, ten times the error of an fp32 product's sums).  parts: [3][np].
 __global__ void __launch_bounds__(256) split_dlogits_kernel(const float* __restrict__ dl, long long n, long long np,
-                                                            __nv_bfloat16* __restrict__ hi,
-                                                            __nv_bfloat16* __restrict__ lo) {
+                                                            __nv_bfloat16* __restrict__ parts) {
+  griddep_launch();
   const long long step = 4ll * gridDim.x * blockDim.x;
   for (long long i = 4ll * (blockIdx.x * static_cast<long long>(blockDim.x) + threadIdx.x); i < np; i += step) {
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (i < n) v = __ldcs(reinterpret_cast<const float4*>(dl + i));
-    const uint2 h = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-    const float2 a = unpack_bf16x2(h.x), b = unpack_bf16x2(h.y);
-    *reinterpret_cast<uint2*>(hi + i) = h;
-    *reinterpret_cast<uint2*>(lo + i) = make_uint2(pack_bf16x2(v.x - a.x, v.y - a.y), pack_bf16x2(v.z - b.x, v.w - b.y));
+#pragma unroll
+    for (int p = 0; p < 3; ++p) {
+      const uint2 h = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+      *reinterpret_cast<uint2*>(parts + p * np + i) = h;
+      const float2 a = unpack_bf16x2(h.x), b = unpack_bf16x2(h.y);
+      v = make_float4(v.x - a.x, v.y - a.y, v.z - b.x, v.w - b.y);
+    }
   }
 }
 
-cudaError_t launch_split_dlogits(const float* dlogits, long long T, long long Tp, int E, __nv_bfloat16* hi,
-                                 __nv_bfloat16* lo, cudaStream_t s) {
+// D[e, i] = sum_t dlogits[t, e] X[t, i] over a split's tokens: tiles of 128 experts x 256 columns, both operands read with
+// the tokens outermost.  A step of 64 tokens takes the X tile once (32 KB) and multiplies it with the three parts' tiles
+// (16 KB each) into one accumulator: 80 KB of shared memory filled for 1536 cycles of tensor work, where a reduction
+// over three times the tokens (every part with its own copy of X) fills 144 KB and was bound by that (32768 x 1536 x 512:
+// 102 us).  X and the parts have rings of their own, each slot free again as soon as its last product has run.
+constexpr int kDwX = 3, kDwP = 7;             // slots of the rings
+constexpr int kDwXBytes = 32768, kDwPBytes = 16384, kDwBox = 64 * 128;
+constexpr size_t kDwSmem = 1024 + kDwX * kDwXBytes + kDwP * kDwPBytes + 4 * kStgBuf;
+constexpr int kDwThreads = 224;  // 4 epilogue warps, X's and the parts' producers, the issuer
+
+struct DwArgs {
+  int E, d, Tp, chunk;  // chunk: tokens of a split, a multiple of 64
+  int etiles, tiles, items;
+  int wait_first;
+  int* err;
+  unsigned long long timeout_ns;
+};
+
+// Maps: X, the parts, the sums [splits][E][d].
+__global__ void __launch_bounds__(kDwThreads, 1) router_dw_kernel(const DwArgs a, const __grid_constant__ CUtensorMap mx,
+                                                                  const __grid_constant__ CUtensorMap mp,
+                                                                  const __grid_constant__ CUtensorMap mo) {
+  extern __shared__ uint8_t dw_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dw_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* xs = smem;
+  uint8_t* ps = smem + kDwX * kDwXBytes;
+  __shared__ uint64_t full_x[kDwX], empty_x[kDwX], full_p[kDwP], empty_p[kDwP], tfull[2], tempty[2], drain;
+  __shared__ uint32_t s_tmem;
+  __shared__ volatile int s_abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < kDwX; ++i) {
+      mbar_init(&full_x[i], 1);
+      mbar_init(&empty_x[i], 1);
+    }
+    for (int i = 0; i < kDwP; ++i) {
+      mbar_init(&full_p[i], 1);
+      mbar_init(&empty_p[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&tfull[i], 1);
+      mbar_init(&tempty[i], 128);
+    }
+    mbar_init(&drain, 1);
+    s_abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 4) {
+    tmem_alloc(&s_tmem, 512);
+    if (lane == 0) {
+      tma_prefetch_desc(&mx);
+      tma_prefetch_desc(&mp);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  // The kernel ahead is the split, or router_dx, which lets this one start only when the split has ended.  Only in the
+  // first case is there something to wait for before the loads; the wait at the end keeps the launches' order.
+  griddep_launch();
+  if (a.wait_first) griddep_wait();
+  // an item: a split (its tokens k0..) of a tile (its experts e0.., its columns i0..)
+  struct Item {
+    int sp, e0, i0, k0, steps;
+  };
+  auto item = [&](int n) {
+    Item it;
+    it.sp = n / a.tiles;
+    const int tile = n % a.tiles;
+    it.e0 = tile % a.etiles * 128;
+    it.i0 = tile / a.etiles * 256;
+    it.k0 = it.sp * a.chunk;
+    it.steps = (min(a.Tp, it.k0 + a.chunk) - it.k0) / 64;
+    return it;
+  };
+  if (warp == 4 && lane == 0) {  // X
+    int n = 0;
+    bool ok = true;
+    for (int id = blockIdx.x; id < a.items && ok; id += gridDim.x) {
+      const Item it = item(id);
+      for (int k = 0; k < it.steps; ++k, ++n) {
+        const int s = n % kDwX;
+        ok = mbar_wait(&empty_x[s], (n / kDwX & 1) ^ 1, &s_abort, a.timeout_ns, a.err);
+        if (!ok) break;
+        mbar_arrive_expect_tx(&full_x[s], kDwXBytes);
+        tma_load_3d(xs + s * kDwXBytes, &mx, &full_x[s], 0, it.k0 + 64 * k, it.i0 / 64);
+      }
+    }
+    if (!ok) {  // let the copies in flight land before the block goes away
+      volatile int never = 0;
+      for (int j = n > kDwX ? n - kDwX : 0; j < n; ++j) mbar_wait(&full_x[j % kDwX], j / kDwX & 1, &never, 20000000ull, nullptr);
+    }
+  } else if (warp == 5 && lane == 0) {  // the parts
+    int n = 0;
+    bool ok = true;
+    for (int id = blockIdx.x; id < a.items && ok; id += gridDim.x) {
+      const Item it = item(id);
+      for (int k = 0; k < it.steps && ok; ++k) {
+        for (int p = 0; p < 3; ++p, ++n) {
+          const int s = n % kDwP;
+          ok = mbar_wait(&empty_p[s], (n / kDwP & 1) ^ 1, &s_abort, a.timeout_ns, a.err);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&full_p[s], kDwPBytes);
+          const int row = p * a.Tp + it.k0 + 64 * k;
+          tma_load_2d(ps + s * kDwPBytes, &mp, &full_p[s], it.e0, row);
+          tma_load_2d(ps + s * kDwPBytes + kDwBox, &mp, &full_p[s], it.e0 + 64, row);
+        }
+      }
+    }
+    if (!ok) {
+      volatile int never = 0;
+      for (int j = n > kDwP ? n - kDwP : 0; j < n; ++j) mbar_wait(&full_p[j % kDwP], j / kDwP & 1, &never, 20000000ull, nullptr);
+    }
+  } else if (warp == 6 && lane == 0) {  // the products
+    constexpr uint32_t kIdesc = idesc_bf16(128, 256, 1, 1);
+    int nx = 0, np = 0, acc = 0;
+    bool ok = true;
+    for (int id = blockIdx.x; id < a.items && ok; id += gridDim.x, ++acc) {
+      const Item it = item(id);
+      const int buf = acc & 1;
+      ok = mbar_wait(&tempty[buf], (acc >> 1 & 1) ^ 1, &s_abort, a.timeout_ns, a.err);
+      if (!ok) break;
+      const uint32_t dt = tmem + buf * 256;
+      for (int k = 0; k < it.steps && ok; ++k, ++nx) {
+        const int sx = nx % kDwX;
+        ok = mbar_wait(&full_x[sx], nx / kDwX & 1, &s_abort, a.timeout_ns, a.err);
+        const uint32_t xb = smem_u32(xs + sx * kDwXBytes);
+        for (int p = 0; p < 3 && ok; ++p, ++np) {
+          const int sp = np % kDwP;
+          ok = mbar_wait(&full_p[sp], np / kDwP & 1, &s_abort, a.timeout_ns, a.err);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t pb = smem_u32(ps + sp * kDwPBytes);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_bf16(dt, sdesc_sw128(pb + kk * 2048, kDwBox, 1024), sdesc_sw128(xb + kk * 2048, kDwBox, 1024), kIdesc,
+                      (k | p | kk) != 0 ? 1u : 0u);
+          umma_commit(&empty_p[sp]);
+        }
+        if (ok) umma_commit(&empty_x[sx]);
+      }
+      if (ok) umma_commit(&tfull[buf]);
+    }
+    if (!ok) {  // the products in flight read shared memory and write TMEM
+      umma_commit(&drain);
+      volatile int never = 0;
+      mbar_wait(&drain, 0, &never, 20000000ull, nullptr);
+    }
+  } else if (warp < 4) {  // the sums: a thread holds an expert, 32 columns at a time leave through shared memory
+    uint8_t* stg = ps + kDwP * kDwPBytes + warp * kStgBuf;
+    int acc = 0;
+    for (int id = blockIdx.x; id < a.items; id += gridDim.x, ++acc) {
+      const Item it = item(id);
+      const int buf = acc & 1;
+      if (!mbar_wait(&tfull[buf], acc >> 1 & 1, &s_abort, a.timeout_ns, a.err)) break;
+      tc_fence_after();
+      const uint32_t t0 = tmem + (static_cast<uint32_t>(warp * 32) << 16) + buf * 256;
+      if (it.e0 + warp * 32 < a.E) {
+#pragma unroll 1
+        for (int c = 0; c < 256 && it.i0 + c < a.d; c += 32) {
+          uint32_t r[32];
+          tmem_ld32(t0 + c, r);
+          tmem_ld_wait();
+          float v[32];
+#pragma unroll
+          for (int q = 0; q < 32; ++q) v[q] = __uint_as_float(r[q]);
+          if (lane == 0) bulk_wait_read<0>();
+          __syncwarp();
+          stage_row32(stg, lane, v, true);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_3d(&mo, stg, it.i0 + c, it.e0 + warp * 32, it.sp);
+            bulk_commit();
+          }
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(&tempty[buf]);
+    }
+    if (lane == 0) bulk_wait0();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 4) tmem_dealloc(tmem, 512);
+  griddep_wait();
+}
+
+// out[i][e] = in[i][e] (or 0) + sum_s part[s][e][i], s ascending: tiles of 128 columns x 8 experts (whole 32-byte
+// sectors on both sides), turned in shared memory; four splits of a thread's four columns are in flight.
+__global__ void __launch_bounds__(256) router_dw_reduce_kernel(const float* __restrict__ part, int splits, int E, int d,
+                                                               const float* in, float* out) {
+  __shared__ __align__(16) float tile[8][132];
+  griddep_wait();
+  const int i0 = blockIdx.x * 128, e0 = blockIdx.y * 8, tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+  const long long plane = static_cast<long long>(E) * d;
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (i0 + 4 * tx < d) {
+    const float* src = part + static_cast<long long>(e0 + ty) * d + i0 + 4 * tx;
+    for (int s0 = 0; s0 < splits; s0 += 4) {
+      float4 x[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        x[k] = s0 + k < splits ? __ldcs(reinterpret_cast<const float4*>(src + (s0 + k) * plane)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        v.x += x[k].x; v.y += x[k].y; v.z += x[k].z; v.w += x[k].w;
+      }
+    }
+  }
+  *reinterpret_cast<float4*>(&tile[ty][4 * tx]) = v;
+  __syncthreads();
+  const int te = threadIdx.x & 7;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int ti = (threadIdx.x >> 3) + 32 * r;
+    if (i0 + ti >= d) break;
+    const long long at = static_cast<long long>(i0 + ti) * E + e0 + te;
+    out[at] = (in ? in[at] : 0.0f) + tile[te][ti];
+  }
+}
+
+template <class... P, class... A>
+cudaError_t launch_dependent(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+}  // namespace
+
+cudaError_t launch_split_dlogits(const float* dlogits, long long T, long long Tp, int E, __nv_bfloat16* parts, cudaStream_t s) {
   const long long np = Tp * E, want = (np / 4 + 255) / 256;
-  if (np > 0) split_dlogits_kernel<<<static_cast<unsigned>(want < 8192 ? want : 8192), 256, 0, s>>>(dlogits, T * E, np, hi, lo);
+  if (np > 0) split_dlogits_kernel<<<static_cast<unsigned>(want < 8192 ? want : 8192), 256, 0, s>>>(dlogits, T * E, np, parts);
   return cudaGetLastError();
 }
 
-__global__ void __launch_bounds__(256) splitk_reduce_add_kernel(const float* __restrict__ part, int splits, long long n,
-                                                                const float* in, float* out) {
-  const long long i = 4ll * (blockIdx.x * static_cast<long long>(blockDim.x) + threadIdx.x);
-  if (i >= n) return;
-  float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  for (int s = 0; s < splits; ++s) {
-    const float4 b = __ldcs(reinterpret_cast<const float4*>(part + s * n + i));
-    a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
-  }
-  if (in) {
-    const float4 b = *reinterpret_cast<const float4*>(in + i);
-    a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
-  }
-  *reinterpret_cast<float4*>(out + i) = a;
+cudaError_t launch_router_dw(const __nv_bfloat16* X, const __nv_bfloat16* parts, int T, int Tp, int d, int E, bool after_split,
+                             int num_sms, float* sums, int* splits, int* err, unsigned long long timeout_ns, cudaStream_t s) {
+  CUtensorMap mx, mp, mo;
+  if (!make_chunked_map_2d(&mx, X, d, T, 4) || !make_map_2d(&mp, parts, E, 3 * static_cast<uint64_t>(Tp), E, 64))
+    return cudaErrorInvalidValue;
+  DwArgs a{};
+  a.E = E;
+  a.d = d;
+  a.Tp = Tp;
+  a.etiles = (E + 127) / 128;
+  a.tiles = a.etiles * ((d + 255) / 256);
+  const int steps = Tp / 64;
+  int split = num_sms / a.tiles;  // about a tile for every SM, two steps of tokens each at least
+  if (split > kMaxRouterSplit) split = kMaxRouterSplit;
+  if (split > steps / 2) split = steps / 2;
+  if (split < 1) split = 1;
+  a.chunk = (steps + split - 1) / split * 64;
+  split = (Tp + a.chunk - 1) / a.chunk;
+  a.items = a.tiles * split;
+  a.wait_first = after_split;
+  a.err = err;
+  a.timeout_ns = timeout_ns;
+  *splits = split;
+  if (!make_store_map_3d(&mo, sums, true, d, E, split, 32)) return cudaErrorInvalidValue;
+  const cudaError_t e = cudaFuncSetAttribute(router_dw_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kDwSmem));
+  if (e != cudaSuccess) return e;
+  return launch_dependent(router_dw_kernel, dim3(a.items < num_sms ? a.items : num_sms), dim3(kDwThreads), kDwSmem, s, a, mx, mp, mo);
 }
 
-cudaError_t launch_splitk_reduce_add(const float* part, int splits, long long n, const float* in, float* out,
-                                     cudaStream_t s) {
-  if (n > 0)
-    splitk_reduce_add_kernel<<<static_cast<unsigned>((n / 4 + 255) / 256), 256, 0, s>>>(part, splits, n, in, out);
-  return cudaGetLastError();
+cudaError_t launch_router_dw_reduce(const float* sums, int splits, int d, int E, const float* in, float* out, cudaStream_t s) {
+  return launch_dependent(router_dw_reduce_kernel, dim3((d + 127) / 128, E / 8), dim3(256), 0, s, sums, splits, E, d, in, out);
 }
 
 }  // namespace vgg
