@@ -246,7 +246,7 @@ cudaError_t launch_split_dlogits(const float* dlogits, long long T, long long Tp
 constexpr int kMaxRouterSplit = 16;
 cudaError_t launch_router_dw(const __nv_bfloat16* X, const __nv_bfloat16* parts, int T, int Tp, int d, int E, bool after_split,
                              int num_sms, float* sums, int* splits, int* err, unsigned long long timeout_ns, cudaStream_t s);
-// out[i][e] = in[i][e] (or 0) + sum_s sums[s][e][i], s ascending.
+// out[i][e] = in[i][e] (or 0) + sum_s sums[s][e][i], in a fixed order.
 cudaError_t launch_router_dw_reduce(const float* sums, int splits, int d, int E, const float* in, float* out, cudaStream_t s);
 
 cudaError_t launch_wait_timeout_probe(int* err, unsigned long long timeout_ns, cudaStream_t s);

@@ -32,10 +32,15 @@ __global__ void __launch_bounds__(256) split_dlogits_kernel(const float* __restr
 // (16 KB each) into one accumulator: 80 KB of shared memory filled for 1536 cycles of tensor work, where a reduction
 // over three times the tokens (every part with its own copy of X) fills 144 KB and was bound by that (32768 x 1536 x 512:
 // 102 us).  X and the parts have rings of their own, each slot free again as soon as its last product has run.
-constexpr int kDwX = 3, kDwP = 7;             // slots of the rings
+//
+// The tensor cores' fp32 accumulator drops the bits that an addition shifts out, always towards zero: sums over 5461
+// tokens in one accumulator came out 1.6e-5 too small.  So an accumulator takes two steps only (24 additions); the
+// epilogue warps add it, rounded to nearest, to sums in registers while the next two run into the other one.
+constexpr int kDwChunk = 2;                   // steps an accumulator takes
+constexpr int kDwX = 3, kDwP = 6;             // slots of the rings
 constexpr int kDwXBytes = 32768, kDwPBytes = 16384, kDwBox = 64 * 128;
-constexpr size_t kDwSmem = 1024 + kDwX * kDwXBytes + kDwP * kDwPBytes + 4 * kStgBuf;
-constexpr int kDwThreads = 224;  // 4 epilogue warps, X's and the parts' producers, the issuer
+constexpr size_t kDwSmem = 1024 + kDwX * kDwXBytes + kDwP * kDwPBytes + 8 * kStgBuf;
+constexpr int kDwThreads = 352;  // 8 epilogue warps, X's and the parts' producers, the issuer
 
 struct DwArgs {
   int E, d, Tp, chunk;  // chunk: tokens of a split, a multiple of 64
@@ -68,13 +73,13 @@ __global__ void __launch_bounds__(kDwThreads, 1) router_dw_kernel(const DwArgs a
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tfull[i], 1);
-      mbar_init(&tempty[i], 128);
+      mbar_init(&tempty[i], 256);
     }
     mbar_init(&drain, 1);
     s_abort = 0;
     fence_mbar_init();
   }
-  if (warp == 4) {
+  if (warp == 8) {
     tmem_alloc(&s_tmem, 512);
     if (lane == 0) {
       tma_prefetch_desc(&mx);
@@ -103,7 +108,7 @@ __global__ void __launch_bounds__(kDwThreads, 1) router_dw_kernel(const DwArgs a
     it.steps = (min(a.Tp, it.k0 + a.chunk) - it.k0) / 64;
     return it;
   };
-  if (warp == 4 && lane == 0) {  // X
+  if (warp == 8 && lane == 0) {  // X
     int n = 0;
     bool ok = true;
     for (int id = blockIdx.x; id < a.items && ok; id += gridDim.x) {
@@ -120,7 +125,7 @@ __global__ void __launch_bounds__(kDwThreads, 1) router_dw_kernel(const DwArgs a
       volatile int never = 0;
       for (int j = n > kDwX ? n - kDwX : 0; j < n; ++j) mbar_wait(&full_x[j % kDwX], j / kDwX & 1, &never, 20000000ull, nullptr);
     }
-  } else if (warp == 5 && lane == 0) {  // the parts
+  } else if (warp == 9 && lane == 0) {  // the parts
     int n = 0;
     bool ok = true;
     for (int id = blockIdx.x; id < a.items && ok; id += gridDim.x) {
@@ -141,113 +146,125 @@ __global__ void __launch_bounds__(kDwThreads, 1) router_dw_kernel(const DwArgs a
       volatile int never = 0;
       for (int j = n > kDwP ? n - kDwP : 0; j < n; ++j) mbar_wait(&full_p[j % kDwP], j / kDwP & 1, &never, 20000000ull, nullptr);
     }
-  } else if (warp == 6 && lane == 0) {  // the products
+  } else if (warp == 10 && lane == 0) {  // the products
     constexpr uint32_t kIdesc = idesc_bf16(128, 256, 1, 1);
     int nx = 0, np = 0, acc = 0;
     bool ok = true;
-    for (int id = blockIdx.x; id < a.items && ok; id += gridDim.x, ++acc) {
+    for (int id = blockIdx.x; id < a.items && ok; id += gridDim.x) {
       const Item it = item(id);
-      const int buf = acc & 1;
-      ok = mbar_wait(&tempty[buf], (acc >> 1 & 1) ^ 1, &s_abort, a.timeout_ns, a.err);
-      if (!ok) break;
-      const uint32_t dt = tmem + buf * 256;
-      for (int k = 0; k < it.steps && ok; ++k, ++nx) {
-        const int sx = nx % kDwX;
-        ok = mbar_wait(&full_x[sx], nx / kDwX & 1, &s_abort, a.timeout_ns, a.err);
-        const uint32_t xb = smem_u32(xs + sx * kDwXBytes);
-        for (int p = 0; p < 3 && ok; ++p, ++np) {
-          const int sp = np % kDwP;
-          ok = mbar_wait(&full_p[sp], np / kDwP & 1, &s_abort, a.timeout_ns, a.err);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t pb = smem_u32(ps + sp * kDwPBytes);
+      for (int k0 = 0; k0 < it.steps && ok; k0 += kDwChunk, ++acc) {
+        const int buf = acc & 1;
+        ok = mbar_wait(&tempty[buf], (acc >> 1 & 1) ^ 1, &s_abort, a.timeout_ns, a.err);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t dt = tmem + buf * 256;
+        for (int k = k0; k < min(k0 + kDwChunk, it.steps) && ok; ++k, ++nx) {
+          const int sx = nx % kDwX;
+          ok = mbar_wait(&full_x[sx], nx / kDwX & 1, &s_abort, a.timeout_ns, a.err);
+          const uint32_t xb = smem_u32(xs + sx * kDwXBytes);
+          for (int p = 0; p < 3 && ok; ++p, ++np) {
+            const int sp = np % kDwP;
+            ok = mbar_wait(&full_p[sp], np / kDwP & 1, &s_abort, a.timeout_ns, a.err);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t pb = smem_u32(ps + sp * kDwPBytes);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            umma_bf16(dt, sdesc_sw128(pb + kk * 2048, kDwBox, 1024), sdesc_sw128(xb + kk * 2048, kDwBox, 1024), kIdesc,
-                      (k | p | kk) != 0 ? 1u : 0u);
-          umma_commit(&empty_p[sp]);
+            for (int kk = 0; kk < 4; ++kk)
+              umma_bf16(dt, sdesc_sw128(pb + kk * 2048, kDwBox, 1024), sdesc_sw128(xb + kk * 2048, kDwBox, 1024), kIdesc,
+                        ((k - k0) | p | kk) != 0 ? 1u : 0u);
+            umma_commit(&empty_p[sp]);
+          }
+          if (ok) umma_commit(&empty_x[sx]);
         }
-        if (ok) umma_commit(&empty_x[sx]);
+        if (ok) umma_commit(&tfull[buf]);
       }
-      if (ok) umma_commit(&tfull[buf]);
     }
     if (!ok) {  // the products in flight read shared memory and write TMEM
       umma_commit(&drain);
       volatile int never = 0;
       mbar_wait(&drain, 0, &never, 20000000ull, nullptr);
     }
-  } else if (warp < 4) {  // the sums: a thread holds an expert, 32 columns at a time leave through shared memory
+  } else if (warp < 8) {  // the sums: a thread holds 128 columns of an expert, which leave through shared memory
+    const int quarter = warp & 3, c0 = (warp >> 2) * 128;
     uint8_t* stg = ps + kDwP * kDwPBytes + warp * kStgBuf;
     int acc = 0;
-    for (int id = blockIdx.x; id < a.items; id += gridDim.x, ++acc) {
+    bool ok = true;
+    for (int id = blockIdx.x; id < a.items && ok; id += gridDim.x) {
       const Item it = item(id);
-      const int buf = acc & 1;
-      if (!mbar_wait(&tfull[buf], acc >> 1 & 1, &s_abort, a.timeout_ns, a.err)) break;
-      tc_fence_after();
-      const uint32_t t0 = tmem + (static_cast<uint32_t>(warp * 32) << 16) + buf * 256;
-      if (it.e0 + warp * 32 < a.E) {
-#pragma unroll 1
-        for (int c = 0; c < 256 && it.i0 + c < a.d; c += 32) {
-          uint32_t r[32];
-          tmem_ld32(t0 + c, r);
-          tmem_ld_wait();
-          float v[32];
+      float v[4][32];
 #pragma unroll
-          for (int q = 0; q < 32; ++q) v[q] = __uint_as_float(r[q]);
-          if (lane == 0) bulk_wait_read<0>();
-          __syncwarp();
-          stage_row32(stg, lane, v, true);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            tma_store_3d(&mo, stg, it.i0 + c, it.e0 + warp * 32, it.sp);
-            bulk_commit();
-          }
+      for (int b = 0; b < 4; ++b)
+#pragma unroll
+        for (int q = 0; q < 32; ++q) v[b][q] = 0.0f;
+      for (int k0 = 0; k0 < it.steps; k0 += kDwChunk, ++acc) {
+        const int buf = acc & 1;
+        ok = mbar_wait(&tfull[buf], acc >> 1 & 1, &s_abort, a.timeout_ns, a.err);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t t0 = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * 256 + c0;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          uint32_t r[32];
+          tmem_ld32(t0 + 32 * b, r);
+          tmem_ld_wait();
+#pragma unroll
+          for (int q = 0; q < 32; ++q) v[b][q] += __uint_as_float(r[q]);
+        }
+        tc_fence_before();
+        mbar_arrive(&tempty[buf]);
+      }
+      if (!ok) break;
+      if (it.e0 + quarter * 32 >= a.E) continue;
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        if (it.i0 + c0 + 32 * b >= a.d) break;
+        if (lane == 0) bulk_wait_read<0>();
+        __syncwarp();
+        stage_row32(stg, lane, v[b], true);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_3d(&mo, stg, it.i0 + c0 + 32 * b, it.e0 + quarter * 32, it.sp);
+          bulk_commit();
         }
       }
-      tc_fence_before();
-      mbar_arrive(&tempty[buf]);
     }
     if (lane == 0) bulk_wait0();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 4) tmem_dealloc(tmem, 512);
+  if (warp == 8) tmem_dealloc(tmem, 512);
   griddep_wait();
 }
 
-// out[i][e] = in[i][e] (or 0) + sum_s part[s][e][i], s ascending: tiles of 128 columns x 8 experts (whole 32-byte
-// sectors on both sides), turned in shared memory; four splits of a thread's four columns are in flight.
+// out[i][e] = in[i][e] (or 0) + sum_s part[s][e][i]: tiles of 64 columns x 8 experts (whole 32-byte sectors on both
+// sides), turned in shared memory.  Two threads share a place's splits and have theirs in flight at once: with one
+// thread and four at a time 16 splits of 2048 x 128 took 5 us more.
 __global__ void __launch_bounds__(256) router_dw_reduce_kernel(const float* __restrict__ part, int splits, int E, int d,
                                                                const float* in, float* out) {
-  __shared__ __align__(16) float tile[8][132];
+  constexpr int kHalf = kMaxRouterSplit / 2;
+  __shared__ __align__(16) float tile[2][8][68];
   griddep_wait();
-  const int i0 = blockIdx.x * 128, e0 = blockIdx.y * 8, tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+  const int i0 = blockIdx.x * 64, e0 = blockIdx.y * 8, tx = threadIdx.x & 15, ty = threadIdx.x >> 4 & 7, tz = threadIdx.x >> 7;
   const long long plane = static_cast<long long>(E) * d;
-  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  if (i0 + 4 * tx < d) {
-    const float* src = part + static_cast<long long>(e0 + ty) * d + i0 + 4 * tx;
-    for (int s0 = 0; s0 < splits; s0 += 4) {
-      float4 x[4];
+  const float* src = part + tz * kHalf * plane + static_cast<long long>(e0 + ty) * d + i0 + 4 * tx;
+  float4 x[kHalf], v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        x[k] = s0 + k < splits ? __ldcs(reinterpret_cast<const float4*>(src + (s0 + k) * plane)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int s = 0; s < kHalf; ++s)
+    x[s] = tz * kHalf + s < splits ? __ldcs(reinterpret_cast<const float4*>(src + s * plane)) : v;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        v.x += x[k].x; v.y += x[k].y; v.z += x[k].z; v.w += x[k].w;
-      }
-    }
+  for (int s = 0; s < kHalf; ++s) {
+    v.x += x[s].x; v.y += x[s].y; v.z += x[s].z; v.w += x[s].w;
   }
-  *reinterpret_cast<float4*>(&tile[ty][4 * tx]) = v;
+  *reinterpret_cast<float4*>(&tile[tz][ty][4 * tx]) = v;
   __syncthreads();
   const int te = threadIdx.x & 7;
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
+  for (int r = 0; r < 2; ++r) {
     const int ti = (threadIdx.x >> 3) + 32 * r;
-    if (i0 + ti >= d) break;
     const long long at = static_cast<long long>(i0 + ti) * E + e0 + te;
-    out[at] = (in ? in[at] : 0.0f) + tile[te][ti];
+    out[at] = (in ? in[at] : 0.0f) + (tile[0][te][ti] + tile[1][te][ti]);
   }
 }
 
@@ -304,7 +321,7 @@ cudaError_t launch_router_dw(const __nv_bfloat16* X, const __nv_bfloat16* parts,
 }
 
 cudaError_t launch_router_dw_reduce(const float* sums, int splits, int d, int E, const float* in, float* out, cudaStream_t s) {
-  return launch_dependent(router_dw_reduce_kernel, dim3((d + 127) / 128, E / 8), dim3(256), 0, s, sums, splits, E, d, in, out);
+  return launch_dependent(router_dw_reduce_kernel, dim3(d / 64, E / 8), dim3(256), 0, s, sums, splits, E, d, in, out);
 }
 
 }  // namespace vgg
