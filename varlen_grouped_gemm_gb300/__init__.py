@@ -864,11 +864,12 @@ class E4m3Weights:
         return w
 
 
-def forward_e4m3(ctx, X, W_r, bias, w8: E4m3Weights, W_down, buf: Buffers, stream=None, cache=True):
+def forward_e4m3(ctx, X, W_r, bias, w8: E4m3Weights, W_down, buf: Buffers, stream=None, cache=True, quantized=False):
     """The forward with the gate/up GEMM on e4m3 operands (``buf`` allocated with ``e4m3=True``): routing and
     grouping as ``forward``, X quantized per token, then the e4m3 grouped GEMMs and the combine.  When ``w8``
     holds W_down's codes the down projection runs on e4m3 operands too (``W_down`` may then be None).
-    ``cache=False``: forward only (H, U not written)."""
+    ``cache=False``: forward only (H, U not written).  ``quantized=True``: ``buf.xq`` and ``buf.xs`` already hold X's
+    codes and scales (as moe_add_rmsnorm writes them); X itself serves the routing."""
     if buf.xq is None:
         raise ValueError("buffers were allocated without e4m3=True")
     moe_route(ctx, X, W_r, bias, buf.K, buf.logits, buf.scores, buf.topk_ids, buf.topk_w, buf.ws, stream)
@@ -879,7 +880,8 @@ def forward_e4m3(ctx, X, W_r, bias, w8: E4m3Weights, W_down, buf: Buffers, strea
     else:
         moe_permute(ctx, buf.topk_ids, buf.topk_w, buf.logits, buf.scores, buf.E, buf.m_tile, buf.counts,
                     buf.offsets, buf.sorted_tok, buf.sorted_w, buf.tok_ptr, buf.tok_pairs, buf.P, buf.ws, stream)
-    moe_quantize_rows_e4m3(ctx, X, buf.xq, buf.xs, stream)
+    if not quantized:
+        moe_quantize_rows_e4m3(ctx, X, buf.xq, buf.xs, stream)
     moe_grouped_gemm_fwd_e4m3(ctx, buf.xq, buf.xs, w8.Wg_q, w8.wg_scale, w8.Wu_q, w8.wu_scale,
                               None if w8.Wd_q is not None else W_down, buf.offsets, buf.sorted_tok, buf.sorted_w,
                               buf.H if cache else None, buf.U if cache else None, buf.A, buf.Yw, Wd_q=w8.Wd_q,
@@ -889,10 +891,11 @@ def forward_e4m3(ctx, X, W_r, bias, w8: E4m3Weights, W_down, buf: Buffers, strea
     moe_combine(ctx, buf.Yw, buf.tok_ptr, buf.tok_pairs, buf.O, stream)
 
 
-def forward_mx(ctx, X, W_r, bias, wmx: MxWeights, buf: Buffers, stream=None, cache=True):
+def forward_mx(ctx, X, W_r, bias, wmx: MxWeights, buf: Buffers, stream=None, cache=True, quantized=False):
     """The forward on block-scaled e4m3 operands (``buf`` allocated with ``mx=True``): routing and grouping as
     ``forward``, X quantized in 1 x 32 blocks, the gate/up GEMM (whose epilogue quantizes A), the down
-    projection and the combine.  ``cache=False``: forward only (H, U not written)."""
+    projection and the combine.  ``cache=False``: forward only (H, U not written).  ``quantized=True``: ``buf.mxq`` and
+    ``buf.mxsf`` already hold X's codes and scales (as moe_add_rmsnorm writes them)."""
     if buf.mxq is None:
         raise ValueError("buffers were allocated without mx=True")
     moe_route(ctx, X, W_r, bias, buf.K, buf.logits, buf.scores, buf.topk_ids, buf.topk_w, buf.ws, stream)
@@ -903,7 +906,8 @@ def forward_mx(ctx, X, W_r, bias, wmx: MxWeights, buf: Buffers, stream=None, cac
     else:
         moe_permute(ctx, buf.topk_ids, buf.topk_w, buf.logits, buf.scores, buf.E, buf.m_tile, buf.counts,
                     buf.offsets, buf.sorted_tok, buf.sorted_w, buf.tok_ptr, buf.tok_pairs, buf.P, buf.ws, stream)
-    moe_quantize_rows_mx(ctx, X, buf.mxq, buf.mxsf, stream)
+    if not quantized:
+        moe_quantize_rows_mx(ctx, X, buf.mxq, buf.mxsf, stream)
     moe_grouped_gemm_fwd_mx(ctx, buf.mxq, buf.mxsf, wmx, buf.offsets, buf.sorted_tok, buf.sorted_w,
                             buf.H if cache else None, buf.U if cache else None, buf.mxsft, buf.maq, buf.masf, buf.Yw,
                             stream)
