@@ -183,6 +183,24 @@ def test_norm_rows_without_values(vgg, ctx, form):
     assert y[4].isnan().all() and y[5, 9].isnan() and not y[5, :9].any()
 
 
+@pytest.mark.parametrize("form", ["e4m3", "mx"])
+def test_norm_of_tiny_weights(vgg, ctx, form):
+    """Normed rows around 1e-33 and, in part, below fp32's smallest normal number: the scales follow them down."""
+    g = gen_of(17)
+    res = rows(5, 128, F32, g)
+    for scale in (1e-33, 2.0 ** -128):
+        w = scale * (1 + torch.rand(128, device="cuda", generator=g))
+        q = torch.empty((5, 128), dtype=U8, device="cuda")
+        sc = torch.empty(5, device="cuda") if form == "e4m3" else torch.empty((5, 4), dtype=U8, device="cuda")
+        vgg.moe_add_rmsnorm(ctx, None, res, w, 1e-6, None, None, None, q, sc)
+        y, _ = bo.rmsnorm(f64(res), f64(w), 1e-6)
+        codes = f64(q.view(torch.float8_e4m3fn))
+        s = f64(sc)[:, None] if form == "e4m3" else np.repeat(2.0 ** (sc.cpu().numpy().astype(np.float64) - 127), 32, axis=1)
+        # e4m3's rounding, a step of fp32's smallest number (2^-149) in y and in the scale (up to 448 of them a code)
+        tol = (2.0 ** -4 + 1e-5) * np.abs(y) + 2.0 ** -10 * s + 450 * 2.0 ** -149
+        assert np.all(np.abs(codes * s - y) <= tol), scale
+
+
 def test_norm_of_no_rows(vgg, ctx):
     e = torch.empty((0, 64), dtype=BF, device="cuda")
     dw = torch.full((64,), 7.0, device="cuda")

@@ -180,6 +180,22 @@ cudaError_t launch_token_backward(const float* part, int part_ld, const int32_t*
 
 cudaError_t launch_splitk_reduce(const float* part, int splits, long long n, float* out, cudaStream_t s);
 
+// Launches kern so that it may start before the kernel ahead of it on the stream has ended; kern waits with griddep_wait.
+template <class... P, class... A>
+cudaError_t launch_dependent(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // ---- residual addition and RMS norm ----------------------------------------------------------
 // Row strides in elements.  Null: x (nothing is added), h, y, rstd (not written).
 struct NormFwd {

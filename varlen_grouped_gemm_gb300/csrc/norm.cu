@@ -6,114 +6,113 @@
 //
 // The codes come from the fp32 y, not from its bf16 rounding: one rounding instead of two.
 //
-// Both directions move every element once and are bound by HBM.  A row's values stay in registers between the
-// reduction and the output: thread i of the row's TPR threads holds the 16-byte vectors i, i + TPR, ... (NV of
-// them).
+// Both directions move every element once and are bound by HBM and, with rows of 2 bytes an element, nearly as much by
+// issue slots (hence the packed arithmetic).  A row's values stay in registers between the reduction and the
+// output: thread i of a row's tpr threads holds the vectors of eight values i, i + tpr, ... (NV of them).
+#include <type_traits>
+
 #include "internal.h"
 
 namespace vgg {
 
 namespace {
 
-// Eight consecutive values of a bf16 or fp32 row (16-byte aligned), as fp32.
+struct Vec8 {
+  f32x2 p[4];
+};
+
+__device__ __forceinline__ Vec8 zero8() {
+  Vec8 v;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v.p[k] = pack2(0.0f, 0.0f);
+  return v;
+}
+
+__device__ __forceinline__ Vec8 from_bf16(const uint4 q) {
+  Vec8 v;
+  v.p[0] = bf16x2_to_f32x2(q.x);
+  v.p[1] = bf16x2_to_f32x2(q.y);
+  v.p[2] = bf16x2_to_f32x2(q.z);
+  v.p[3] = bf16x2_to_f32x2(q.w);
+  return v;
+}
+
+__device__ __forceinline__ Vec8 from_f32(const float4 a, const float4 b) {
+  Vec8 v;
+  v.p[0] = pack2(a.x, a.y);
+  v.p[1] = pack2(a.z, a.w);
+  v.p[2] = pack2(b.x, b.y);
+  v.p[3] = pack2(b.z, b.w);
+  return v;
+}
+
+__device__ __forceinline__ uint4 to_bf16(const Vec8& v) {
+  return make_uint4(f32x2_to_bf16x2(v.p[0]), f32x2_to_bf16x2(v.p[1]), f32x2_to_bf16x2(v.p[2]), f32x2_to_bf16x2(v.p[3]));
+}
+
+// Eight values of a bf16 or fp32 row from element off (16-byte aligned), in global memory (read once) or shared memory.
 template <bool F32>
-__device__ __forceinline__ void load8(const void* base, long long off, float (&v)[8]) {
-  if (F32) {
+__device__ __forceinline__ Vec8 load8(const void* base, long long off) {
+  if constexpr (F32) {
     const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + off);
-    const float4 a = __ldcs(p), b = __ldcs(p + 1);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    return from_f32(__ldcs(p), __ldcs(p + 1));
   } else {
-    const uint4 q = __ldcs(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + off));
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = unpack_bf16x2(w[i]);
-      v[2 * i] = f.x;
-      v[2 * i + 1] = f.y;
-    }
+    return from_bf16(__ldcs(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + off)));
   }
 }
 
 template <bool F32>
-__device__ __forceinline__ void store8(void* base, long long off, const float (&v)[8]) {
-  if (F32) {
+__device__ __forceinline__ Vec8 load_smem8(const uint8_t* row, int j) {
+  if constexpr (F32)
+    return from_f32(*reinterpret_cast<const float4*>(row + 32 * j), *reinterpret_cast<const float4*>(row + 32 * j + 16));
+  else return from_bf16(*reinterpret_cast<const uint4*>(row + 16 * j));
+}
+
+template <bool F32>
+__device__ __forceinline__ void store8(void* base, long long off, const Vec8& v) {
+  if constexpr (F32) {
     float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + off);
-    p[0] = make_float4(v[0], v[1], v[2], v[3]);
-    p[1] = make_float4(v[4], v[5], v[6], v[7]);
+    const float2 a = unpack2(v.p[0]), b = unpack2(v.p[1]), c = unpack2(v.p[2]), d = unpack2(v.p[3]);
+    p[0] = make_float4(a.x, a.y, b.x, b.y);
+    p[1] = make_float4(c.x, c.y, d.x, d.y);
   } else {
-    uint4 q;
-    q.x = pack_bf16x2(v[0], v[1]);
-    q.y = pack_bf16x2(v[2], v[3]);
-    q.z = pack_bf16x2(v[4], v[5]);
-    q.w = pack_bf16x2(v[6], v[7]);
-    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(base) + off) = q;
+    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(base) + off) = to_bf16(v);
   }
 }
 
-// Vector j of a row in shared memory.
-template <bool F32>
-__device__ __forceinline__ void load_smem8(const uint8_t* row, int j, float (&v)[8]) {
-  if (F32) {
-    const float4 a = *reinterpret_cast<const float4*>(row + 32 * j), b = *reinterpret_cast<const float4*>(row + 32 * j + 16);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  } else {
-    const uint4 q = *reinterpret_cast<const uint4*>(row + 16 * j);
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = unpack_bf16x2(w[i]);
-      v[2 * i] = f.x;
-      v[2 * i + 1] = f.y;
-    }
-  }
-}
-
-// V = 8 consecutive values by vector accesses, or V = 1 value (rows of any width and alignment).
-template <int V, bool F32>
-__device__ __forceinline__ void load_v(const void* base, long long off, float (&v)[V]) {
-  if constexpr (V == 8) load8<F32>(base, off, v);
-  else v[0] = F32 ? static_cast<const float*>(base)[off] : __bfloat162float(static_cast<const __nv_bfloat16*>(base)[off]);
-}
-
-template <int V, bool F32>
-__device__ __forceinline__ void store_v(void* base, long long off, const float (&v)[V]) {
-  if constexpr (V == 8) store8<F32>(base, off, v);
-  else if (F32) static_cast<float*>(base)[off] = v[0];
-  else static_cast<__nv_bfloat16*>(base)[off] = __float2bfloat16_rn(v[0]);
-}
-
-template <int V>
-__device__ __forceinline__ void load_weight(const void* w, bool f32, int j, float (&v)[V]) {
+__device__ __forceinline__ Vec8 load_weight8(const void* w, int f32, int j) {
   if (f32) {
-    if constexpr (V == 8) {
-      const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(w) + j);
-      const float4 a = __ldg(p), b = __ldg(p + 1);
-      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    } else {
-      v[0] = __ldg(static_cast<const float*>(w) + j);
-    }
-  } else {
-    if constexpr (V == 8) {
-      const uint4 q = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(w) + j));
-      const uint32_t u[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 f = unpack_bf16x2(u[i]);
-        v[2 * i] = f.x;
-        v[2 * i + 1] = f.y;
-      }
-    } else {
-      v[0] = __bfloat162float(static_cast<const __nv_bfloat16*>(w)[j]);
-    }
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(w) + 8 * j);
+    return from_f32(__ldg(p), __ldg(p + 1));
   }
+  return from_bf16(__ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(w) + 8 * j)));
 }
 
-// Sum (or maximum) of v over the blockDim.x threads of a row, the same value in every one of them.  `red` holds a
-// float for each warp of the block; one __syncthreads when a row has more than one warp, so the next use of
-// the same `red` needs another barrier in between.
+// One value of a row of any alignment.
+template <bool F32>
+__device__ __forceinline__ float load1(const void* base, long long off) {
+  return F32 ? static_cast<const float*>(base)[off] : __bfloat162float(static_cast<const __nv_bfloat16*>(base)[off]);
+}
+
+template <bool F32>
+__device__ __forceinline__ void store1(void* base, long long off, float v) {
+  if (F32) static_cast<float*>(base)[off] = v;
+  else static_cast<__nv_bfloat16*>(base)[off] = __float2bfloat16_rn(v);
+}
+
+__device__ __forceinline__ float load_weight1(const void* w, int f32, int j) {
+  return f32 ? __ldg(static_cast<const float*>(w) + j) : __bfloat162float(static_cast<const __nv_bfloat16*>(w)[j]);
+}
+
+// The stream's next value from its packed parts: the sum of two bf16 values rounded once.
+__device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 s = __hadd2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&s);
+}
+
+// Sum (or maximum of values that are not negative) of v over the blockDim.x threads of a row, the same in every one of
+// them.  `red`: a float for each warp of the block; one __syncthreads when a row has more than one warp, so the next
+// use of the same `red` needs another barrier in between.
 template <bool MAX>
 __device__ __forceinline__ float row_reduce(float v, float* red) {
 #pragma unroll
@@ -137,40 +136,132 @@ __device__ __forceinline__ float row_reduce(float v, float* red) {
 
 enum NormForm { NORM_BF16 = 0, NORM_E4M3 = 1, NORM_MX = 2 };
 
-// What follows a row's rstd: h (with HOUT, else it has been stored), y and the codes.  h holds the row's stream and is
-// used up; row_max gives the maximum over the row's threads (all of them call it).
-template <int V, int NV, bool RES32, int FORM, bool HOUT, class RowMax>
-__device__ __forceinline__ void norm_row_out(const NormFwd& a, long long t, int tx, int tpr, int nvec, bool row_ok, float rstd,
-                                             float (&h)[NV][V], const float (&g)[NV][V], RowMax row_max) {
+// The stream's vector as it is stored: four packed bf16 pairs, or eight fp32 values.
+template <bool F32>
+using Raw8 = std::conditional_t<F32, Vec8, uint4>;
+
+__device__ __forceinline__ Vec8 values(const Vec8& r) { return r; }
+__device__ __forceinline__ Vec8 values(const uint4& r) { return from_bf16(r); }
+
+__device__ __forceinline__ Vec8 add_x(const Vec8& r, const uint4& x) {
+  const Vec8 xv = from_bf16(x);
+  Vec8 h;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) h.p[k] = add2(r.p[k], xv.p[k]);
+  return h;
+}
+__device__ __forceinline__ uint4 add_x(const uint4& r, const uint4& x) {
+  return make_uint4(add_bf16x2(r.x, x.x), add_bf16x2(r.y, x.y), add_bf16x2(r.z, x.z), add_bf16x2(r.w, x.w));
+}
+
+__device__ __forceinline__ void store_raw(void* base, long long off, const Vec8& r) { store8<true>(base, off, r); }
+__device__ __forceinline__ void store_raw(void* base, long long off, const uint4& r) {
+  *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(base) + off) = r;
+}
+
+__device__ __forceinline__ uint4 ldcs4(const void* base, long long off) {
+  return __ldcs(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + off));
+}
+
+// 1 / sqrt(x): the approximation (2 steps) and one Newton step.  Every thread of a row computes it, so a correctly rounded
+// root and two quotients cost a thread as many issue slots as its values do.
+__device__ __forceinline__ float inv_root(float x) {
+  const float r = rsqrtf(x);
+  const float e = fmaf(-x * r, r, 1.0f);
+  return x < 1e30f && x > 1e-30f ? fmaf(0.5f * r, e, r) : r;  // (out there the step's products would leave the range)
+}
+
+__device__ __forceinline__ f32x2 squares(const Vec8& h, f32x2 ss) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) ss = fma2(h.p[k], h.p[k], ss);
+  return ss;
+}
+
+__device__ __forceinline__ float amax8(const Vec8& v, float m) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 f = unpack2(v.p[k]);
+    m = fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));
+  }
+  return m;
+}
+
+__device__ __forceinline__ void store_codes8(uint8_t* q, const Vec8& v, float scale) {
+  const f32x2 s = pack2(scale, scale);
+  const float2 a = unpack2(mul2(v.p[0], s)), b = unpack2(mul2(v.p[1], s)), c = unpack2(mul2(v.p[2], s)),
+               d = unpack2(mul2(v.p[3], s));
+  *reinterpret_cast<uint2*>(q) = make_uint2(e4m3x4(a.x, a.y, b.x, b.y), e4m3x4(c.x, c.y, d.x, d.y));
+}
+
+// Where a thread's first vector of a row goes in h, y and q (null: nowhere), and the row's other outputs.
+struct RowOut {
+  uint8_t *h, *y, *q, *sf;
+  float *rstd, *scale;
+};
+template <bool RES32>
+__device__ __forceinline__ RowOut row_out(const NormFwd& a, long long t, int tx) {
+  RowOut o;
+  o.h = a.h ? static_cast<uint8_t*>(a.h) + (t * a.ld_h + 8ll * tx) * (RES32 ? 4 : 2) : nullptr;
+  o.y = a.y ? static_cast<uint8_t*>(a.y) + (t * a.ld_y + 8ll * tx) * 2 : nullptr;
+  o.q = a.q + t * a.d + 8ll * tx;
+  o.sf = a.sf + t * a.sf_ld;
+  o.rstd = a.rstd ? a.rstd + t : nullptr;
+  o.scale = a.scales + t;
+  return o;
+}
+// The same `rows` rows further on.
+template <bool RES32>
+__device__ __forceinline__ void advance(const NormFwd& a, RowOut& o, long long rows) {
+  if (o.h) o.h += rows * a.ld_h * (RES32 ? 4 : 2);
+  if (o.y) o.y += rows * a.ld_y * 2;
+  o.q += rows * a.d;
+  o.sf += rows * a.sf_ld;
+  if (o.rstd) o.rstd += rows;
+  o.scale += rows;
+}
+
+// What follows a row's rstd, first half: h and y leave, h becomes y in fp32; the largest |y| of the thread's columns.
+// raw holds the row's stream, weight(i, j) gives the weight's vector j.
+template <int NV, bool RES32, int FORM, class Weight>
+__device__ __forceinline__ float norm_row_y(const RowOut& o, int tx, int tpr, int nvec, bool row_ok, float rstd,
+                                            const Raw8<RES32> (&raw)[NV], Vec8 (&h)[NV], Weight weight) {
   float amax = 0.0f;
+  const f32x2 r2 = pack2(rstd, rstd);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int j = tx + tpr * i;
+    h[i] = zero8();
     if (row_ok && j < nvec) {
-      if (HOUT && a.h) store_v<V, RES32>(a.h, t * a.ld_h + static_cast<long long>(j) * V, h[i]);
+      if (o.h) store_raw(o.h, 8 * tpr * i, raw[i]);
+      const Vec8 g = weight(i, j), v = values(raw[i]);
 #pragma unroll
-      for (int k = 0; k < V; ++k) {
-        h[i][k] = h[i][k] * rstd * g[i][k];
-        amax = fmaxf(amax, fabsf(h[i][k]));
-      }
-      if (a.y) store_v<V, false>(a.y, t * a.ld_y + static_cast<long long>(j) * V, h[i]);
+      for (int k = 0; k < 4; ++k) h[i].p[k] = mul2(mul2(v.p[k], r2), g.p[k]);
+      if (FORM == NORM_E4M3) amax = amax8(h[i], amax);
+      if (o.y) store8<false>(o.y, 8 * tpr * i, h[i]);
     }
   }
+  return amax;
+}
+
+// Second half: the codes, from the fp32 y and, with one scale a row, the row's largest |y|.
+template <int NV, int FORM>
+__device__ __forceinline__ void norm_row_codes(const NormFwd& a, const RowOut& o, int tx, int tpr, int nvec, bool row_ok,
+                                               float amax, Vec8 (&h)[NV]) {
   if constexpr (FORM == NORM_E4M3) {
-    amax = row_max(amax);
-    const float s = amax > 0.0f ? __fdiv_rn(amax, 448.0f) : 1.0f;
-    if (row_ok && tx == 0) a.scales[t] = s;
-    // one reciprocal a row; where it would overflow, a quotient for every value
+    if (row_ok && tx == 0) *o.scale = amax > 0.0f ? __fdiv_rn(amax, 448.0f) : 1.0f;
+    // one reciprocal a row; values so small that it would overflow are brought up first
     const bool tiny = amax < 1e-30f;
-    const float inv = tiny ? 1.0f : __fdiv_rn(448.0f, amax);
+    const float up = tiny ? 0x1p100f : 1.0f;
+    const float inv = amax > 0.0f ? 448.0f * __frcp_rn(amax * up) : 1.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int j = tx + tpr * i;
       if (row_ok && j < nvec) {
+        if (tiny) {
 #pragma unroll
-        for (int k = 0; k < V; ++k) h[i][k] = tiny ? __fdiv_rn(h[i][k], s) : h[i][k] * inv;
-        *reinterpret_cast<uint2*>(a.q + t * a.d + 8ll * j) =
-            make_uint2(e4m3x4(h[i][0], h[i][1], h[i][2], h[i][3]), e4m3x4(h[i][4], h[i][5], h[i][6], h[i][7]));
+          for (int k = 0; k < 4; ++k) h[i].p[k] = mul2(h[i].p[k], pack2(up, up));
+        }
+        store_codes8(o.q + 8 * tpr * i, h[i], inv);
       }
     }
   }
@@ -179,80 +270,98 @@ __device__ __forceinline__ void norm_row_out(const NormFwd& a, long long t, int 
     for (int i = 0; i < NV; ++i) {
       const int j = tx + tpr * i;
       // four neighbouring lanes hold a block of 32 columns
-      float m = 0.0f;
-#pragma unroll
-      for (int k = 0; k < V; ++k) m = fmaxf(m, fabsf(h[i][k]));
+      float m = amax8(h[i], 0.0f);
       m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
       m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
       const int e = mx_exponent(m);
-      const float inv = mx_inv_scale(e);
       if (row_ok && j < nvec) {
-#pragma unroll
-        for (int k = 0; k < V; ++k) h[i][k] *= inv;
-        *reinterpret_cast<uint2*>(a.q + t * a.d + 8ll * j) =
-            make_uint2(e4m3x4(h[i][0], h[i][1], h[i][2], h[i][3]), e4m3x4(h[i][4], h[i][5], h[i][6], h[i][7]));
-        if ((j & 3) == 0) a.sf[t * a.sf_ld + (j >> 2)] = static_cast<uint8_t>(e + 127);
+        store_codes8(o.q + 8 * tpr * i, h[i], mx_inv_scale(e));
+        if ((j & 3) == 0) o.sf[j >> 2] = static_cast<uint8_t>(e + 127);
       }
     }
     // bytes past the last block of the row hold scale 1
-    for (int b = (a.d >> 5) + tx; row_ok && b < a.sf_ld; b += tpr) a.sf[t * a.sf_ld + b] = 127;
+    const int b = (a.d >> 5) + tx;
+    if (row_ok && b < a.sf_ld) o.sf[b] = 127;
   }
 }
 
-template <int V, int NV, bool RES32, int FORM>
-__global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const NormFwd a) {
+// blockDim.y rows a block.
+template <int NV, bool RES32, int FORM>
+__global__ void __launch_bounds__(1024, NV == 1 ? 2 : 1) add_rmsnorm_kernel(const NormFwd a) {
   __shared__ float red_sum[32], red_max[32];
   const long long t = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
   const bool row_ok = t < a.T;
-  const int nvec = a.d / V;
-  float h[NV][V];
-  float ss = 0.0f;
+  const int nvec = a.d / 8;
+  const float inv_d = 1.0f / static_cast<float>(a.d);
+  Raw8<RES32> raw[NV];
+  f32x2 s2 = pack2(0.0f, 0.0f);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int j = threadIdx.x + blockDim.x * i;
     if (row_ok && j < nvec) {
-      load_v<V, RES32>(a.res, t * a.ld_res + static_cast<long long>(j) * V, h[i]);
-      if (a.x) {
-        float x[V];
-        load_v<V, false>(a.x, t * a.ld_x + static_cast<long long>(j) * V, x);
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-          h[i][k] += x[k];
-          if (!RES32) h[i][k] = bf16_round(h[i][k]);  // the norm's input is the stream as it is stored
-        }
-      }
-      if (a.h) store_v<V, RES32>(a.h, t * a.ld_h + static_cast<long long>(j) * V, h[i]);
-#pragma unroll
-      for (int k = 0; k < V; ++k) ss += h[i][k] * h[i][k];
-    } else {
-#pragma unroll
-      for (int k = 0; k < V; ++k) h[i][k] = 0.0f;
+      if constexpr (RES32) raw[i] = load8<true>(a.res, t * a.ld_res + 8ll * j);
+      else raw[i] = ldcs4(a.res, t * a.ld_res + 8ll * j);
+      if (a.x) raw[i] = add_x(raw[i], ldcs4(a.x, t * a.ld_x + 8ll * j));
+      if (a.h) store_raw(a.h, t * a.ld_h + 8ll * j, raw[i]);
+      s2 = squares(values(raw[i]), s2);
     }
   }
-  ss = row_reduce<false>(ss, red_sum);
-  const float rstd = 1.0f / sqrtf(ss / static_cast<float>(a.d) + a.eps);
+  const float2 sf = unpack2(s2);
+  const float ss = row_reduce<false>(sf.x + sf.y, red_sum);
+  const float rstd = inv_root(fmaf(ss, inv_d, a.eps));
   if (a.rstd && row_ok && threadIdx.x == 0) a.rstd[t] = rstd;
-  float g[NV][V];
+  RowOut o = row_out<RES32>(a, t, threadIdx.x);
+  o.h = nullptr;  // stored above
+  Vec8 h[NV];
+  float amax = norm_row_y<NV, RES32, FORM>(o, threadIdx.x, blockDim.x, nvec, row_ok, rstd, raw, h,
+                                           [&](int, int j) { return load_weight8(a.weight, a.weight_f32, j); });
+  if (FORM == NORM_E4M3) amax = row_reduce<true>(amax, red_max);
+  norm_row_codes<NV, FORM>(a, o, threadIdx.x, blockDim.x, nvec, row_ok, amax, h);
+}
+
+// Rows of any width and alignment, bf16 out: a block a row, 16 values a thread.
+template <bool RES32>
+__global__ void __launch_bounds__(1024) add_rmsnorm_any_kernel(const NormFwd a) {
+  constexpr int N = 16;
+  __shared__ float red[32];
+  const long long t = blockIdx.x;
+  const float inv_d = 1.0f / static_cast<float>(a.d);
+  float h[N], ss = 0.0f;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
+  for (int i = 0; i < N; ++i) {
     const int j = threadIdx.x + blockDim.x * i;
-    if (row_ok && j < nvec) load_weight<V>(a.weight, a.weight_f32 != 0, j * V, g[i]);
+    h[i] = 0.0f;
+    if (j < a.d) {
+      h[i] = load1<RES32>(a.res, t * a.ld_res + j);
+      if (a.x) {
+        h[i] += load1<false>(a.x, t * a.ld_x + j);
+        if (!RES32) h[i] = bf16_round(h[i]);  // the norm's input is the stream as it is stored
+      }
+      if (a.h) store1<RES32>(a.h, t * a.ld_h + j, h[i]);
+      ss += h[i] * h[i];
+    }
   }
-  norm_row_out<V, NV, RES32, FORM, false>(a, t, threadIdx.x, blockDim.x, nvec, row_ok, rstd, h, g,
-                                          [&](float m) { return row_reduce<true>(m, red_max); });
+  ss = row_reduce<false>(ss, red);
+  const float rstd = inv_root(fmaf(ss, inv_d, a.eps));
+  if (a.rstd && threadIdx.x == 0) a.rstd[t] = rstd;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int j = threadIdx.x + blockDim.x * i;
+    if (j < a.d) store1<false>(a.y, t * a.ld_y + j, h[i] * rstd * load_weight1(a.weight, a.weight_f32, j));
+  }
 }
 
 // ---- rows through a ring of bulk copies
 //
 // Each of the RG = blockDim.y row groups of a persistent block has a ring of `stages` rows in shared memory, filled ahead
 // by the group's first thread, so the bytes in flight do not depend on registers or on how many warps are waiting.
-// A stage is free again at the group's first barrier of a row (by then its values are in registers).  Every wait is
+// A stage is free again at the group's one barrier a row (by then its values are in registers).  Every wait is
 // bounded; a group that gave up runs on with what it has, so that its barriers stay matched, and leaves once its
 // copies have landed.
 constexpr int kRingGroups = 8, kRingStages = 4;
 
 struct RingShared {
-  float red[2][kRingGroups][16];  // 16-byte aligned: read as float4
+  float red[2][kRingGroups][16];
   float red2[2][kRingGroups][16];
   uint64_t full[kRingGroups][kRingStages];
   int abort;
@@ -278,28 +387,33 @@ __device__ __forceinline__ void ring_drain(RingShared& sh, int stages, int rows_
   __syncthreads();
 }
 
-// Sum (or maximum of values that are not negative) over the blockDim.x threads of a row group; `red` is the group's 16
-// floats for this parity of rows (those past its warps stay 0), so that one barrier a row is enough.
+// The sum of v and, with MAX, the maximum of m (not negative) over the threads of a row group, which has a barrier of
+// its own; red and redm are the group's 16 floats for this parity of rows (those past its warps stay 0), so that one
+// barrier a row is enough.
 template <bool MAX>
-__device__ __forceinline__ float group_reduce(float v, float* red) {
+__device__ __forceinline__ void group_reduce(float& v, float& m, float* red, float* redm) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    const float u = __shfl_xor_sync(0xffffffffu, v, o);
-    v = MAX ? fmaxf(v, u) : v + u;
+    v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (MAX) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   }
   const int nw = blockDim.x >> 5;
   if (nw == 1) {
     __syncwarp();
-    return v;
+    return;
   }
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  if ((threadIdx.x & 31) == 0) {
+    red[threadIdx.x >> 5] = v;
+    if (MAX) redm[threadIdx.x >> 5] = m;
+  }
   asm volatile("bar.sync %0, %1;" ::"r"(static_cast<int>(threadIdx.y) + 1), "r"(static_cast<int>(blockDim.x)) : "memory");
-  v = 0.0f;
-  for (int w = 0; w < nw; w += 4) {
-    const float4 r = *reinterpret_cast<const float4*>(red + w);
-    v = MAX ? fmaxf(fmaxf(v, fmaxf(r.x, r.y)), fmaxf(r.z, r.w)) : v + ((r.x + r.y) + (r.z + r.w));
+  v = red[threadIdx.x & 15];
+  if (MAX) m = redm[threadIdx.x & 15];
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) {
+    v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (MAX) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   }
-  return v;
 }
 
 // Launch shape of a ring kernel for rows of d columns and `row` bytes a stage: NV vectors a thread, up to 512 threads as
@@ -325,12 +439,12 @@ inline RingShape ring_shape(long long T, int d, int NV, size_t row, size_t bytes
 }
 
 template <int NV, bool RES32, int FORM>
-__global__ void __launch_bounds__(512) add_rmsnorm_ring_kernel(const NormFwd a, int stages) {
-  constexpr int V = 8, ES = RES32 ? 4 : 2;
+__global__ void __launch_bounds__(512, 1) add_rmsnorm_ring_kernel(const NormFwd a, int stages) {
+  constexpr int ES = RES32 ? 4 : 2;
   extern __shared__ __align__(128) uint8_t nf_ring[];
   __shared__ __align__(16) RingShared sh;
   const int rg = threadIdx.y, tx = threadIdx.x, tpr = blockDim.x;
-  const int nvec = a.d / V;
+  const int nvec = a.d / 8;
   const uint32_t xb = a.x ? 2u * a.d : 0u, rb = static_cast<uint32_t>(ES) * a.d, sb = xb + rb;
   uint8_t* ring = nf_ring + static_cast<size_t>(rg) * stages * sb;
   const long long step = static_cast<long long>(gridDim.x) * blockDim.y;
@@ -346,80 +460,87 @@ __global__ void __launch_bounds__(512) add_rmsnorm_ring_kernel(const NormFwd a, 
   if (tx == 0)
     for (int k = 0; k < stages; ++k)
       if (t0 + k * step < a.T) issue(t0 + k * step, k);
-  float g[NV][V];
+  Vec8 g[NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int j = tx + tpr * i;
-    if (j < nvec) load_weight<V>(a.weight, a.weight_f32 != 0, j * V, g[i]);
-  }
-  int it = 0, st = 0, ph = 0;
-  for (long long t = t0; t < a.T; t += step, ++it) {
+  for (int i = 0; i < NV; ++i)
+    if (tx + tpr * i < nvec) g[i] = load_weight8(a.weight, a.weight_f32, tx + tpr * i);
+  const float inv_d = 1.0f / static_cast<float>(a.d);
+  // The group's next row into registers, and this thread's share of its sum of squares.
+  int st = 0, ph = 0;
+  auto fetch = [&](Raw8<RES32> (&raw)[NV]) {
     mbar_wait(&sh.full[rg][st], ph, &sh.abort, a.timeout_ns, a.err);
-    const uint8_t* src = ring + static_cast<size_t>(st) * sb;
-    float h[NV][V];
-    float ss = 0.0f;
+    const uint8_t* src = ring + static_cast<uint32_t>(st) * sb;
+    f32x2 s2 = pack2(0.0f, 0.0f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int j = tx + tpr * i;
       if (j < nvec) {
-        load_smem8<RES32>(src, j, h[i]);
-        if (a.x) {
-          float x[V];
-          load_smem8<false>(src + rb, j, x);
-#pragma unroll
-          for (int k = 0; k < V; ++k) {
-            h[i][k] += x[k];
-            if (!RES32) h[i][k] = bf16_round(h[i][k]);
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < V; ++k) ss += h[i][k] * h[i][k];
-      } else {
-#pragma unroll
-        for (int k = 0; k < V; ++k) h[i][k] = 0.0f;
+        if constexpr (RES32) raw[i] = load_smem8<true>(src, j);
+        else raw[i] = *reinterpret_cast<const uint4*>(src + 16 * j);
+        if (a.x) raw[i] = add_x(raw[i], *reinterpret_cast<const uint4*>(src + rb + 16 * j));
+        s2 = squares(values(raw[i]), s2);
       }
     }
-    ss = group_reduce<false>(ss, sh.red[it & 1][rg]);
-    if (tx == 0 && t + stages * step < a.T) issue(t + stages * step, st);
+    const float2 f = unpack2(s2);
+    return f.x + f.y;
+  };
+  long long t_in = t0 + stages * step;  // the next row to ask for
+  auto refill = [&]() {  // the stage that the last fetch has emptied
+    if (tx == 0 && t_in < a.T) issue(t_in, st);
+    t_in += step;
     if (++st == stages) {
       st = 0;
       ph ^= 1;
     }
-    const float rstd = 1.0f / sqrtf(ss / static_cast<float>(a.d) + a.eps);
-    if (a.rstd && tx == 0) a.rstd[t] = rstd;
-    norm_row_out<V, NV, RES32, FORM, true>(a, t, tx, tpr, nvec, true, rstd, h, g, [&](float m) {
-      return group_reduce<true>(m, sh.red2[it & 1][rg]);
-    });
+  };
+  // The next row's sum of squares and this row's largest value go through one barrier, and this row's arithmetic fills
+  // the time that the reduction takes.
+  int it = 0;
+  if (t0 < a.T) {
+    Raw8<RES32> raw[NV];
+    float ss = fetch(raw), none = 0.0f;
+    group_reduce<false>(ss, none, sh.red[0][rg], sh.red2[0][rg]);
+    refill();
+    RowOut o = row_out<RES32>(a, t0, tx);
+    for (long long t = t0;; t += step) {
+      const float rstd = inv_root(fmaf(ss, inv_d, a.eps));
+      if (o.rstd && tx == 0) *o.rstd = rstd;
+      const bool more = t + step < a.T;
+      Raw8<RES32> next[NV];
+      Vec8 h[NV];
+      if (more) ss = fetch(next);
+      float amax = norm_row_y<NV, RES32, FORM>(o, tx, tpr, nvec, true, rstd, raw, h, [&](int i, int) { return g[i]; });
+      ++it;
+      if (FORM == NORM_E4M3 || more) group_reduce<FORM == NORM_E4M3>(ss, amax, sh.red[it & 1][rg], sh.red2[it & 1][rg]);
+      if (more) refill();
+      norm_row_codes<NV, FORM>(a, o, tx, tpr, nvec, true, amax, h);
+      if (!more) break;
+      advance<RES32>(a, o, step);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) raw[i] = next[i];
+    }
   }
   ring_drain(sh, stages, it);
 }
 
-template <int V, int NV, bool RES32>
+template <int NV, bool RES32>
 cudaError_t run_norm_form(const NormFwd& a, int tpr, int rows, cudaStream_t s) {
   const dim3 block(tpr, rows);
   const unsigned grid = static_cast<unsigned>((a.T + rows - 1) / rows);
-  if constexpr (V == 8) {
-    if (a.form == NORM_E4M3) {
-      add_rmsnorm_kernel<V, NV, RES32, NORM_E4M3><<<grid, block, 0, s>>>(a);
-      return cudaGetLastError();
-    }
-    if (a.form == NORM_MX) {
-      add_rmsnorm_kernel<V, NV, RES32, NORM_MX><<<grid, block, 0, s>>>(a);
-      return cudaGetLastError();
-    }
-  }
-  add_rmsnorm_kernel<V, NV, RES32, NORM_BF16><<<grid, block, 0, s>>>(a);
+  if (a.form == NORM_E4M3) add_rmsnorm_kernel<NV, RES32, NORM_E4M3><<<grid, block, 0, s>>>(a);
+  else if (a.form == NORM_MX) add_rmsnorm_kernel<NV, RES32, NORM_MX><<<grid, block, 0, s>>>(a);
+  else add_rmsnorm_kernel<NV, RES32, NORM_BF16><<<grid, block, 0, s>>>(a);
   return cudaGetLastError();
 }
 
-template <int V, int NV>
+template <int NV>
 cudaError_t run_norm(const NormFwd& a, int tpr, int rows, cudaStream_t s) {
-  return a.res_f32 ? run_norm_form<V, NV, true>(a, tpr, rows, s) : run_norm_form<V, NV, false>(a, tpr, rows, s);
+  return a.res_f32 ? run_norm_form<NV, true>(a, tpr, rows, s) : run_norm_form<NV, false>(a, tpr, rows, s);
 }
 
 template <bool RES32, int FORM>
 cudaError_t run_norm_ring(const NormFwd& a, const RingShape& r, cudaStream_t s) {
-  auto kern = add_rmsnorm_ring_kernel<2, RES32, FORM>;
+  auto kern = add_rmsnorm_ring_kernel<3, RES32, FORM>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(r.smem));
   if (e != cudaSuccess) return e;
   kern<<<r.grid, dim3(r.tpr, r.rgs), r.smem, s>>>(a, r.stages);
@@ -437,20 +558,25 @@ cudaError_t run_norm_ring_form(const NormFwd& a, const RingShape& r, cudaStream_
 
 cudaError_t launch_add_rmsnorm(const NormFwd& a, bool vec, int num_sms, cudaStream_t s) {
   if (a.T <= 0) return cudaSuccess;
-  // Rows of more than 4096 columns, four for every SM: two ring blocks an SM.  At 8192 x 7168 with per-row codes 87.6 us
-  // against 116 us for a block a row (few such wide blocks fit an SM, and all of one waits at each of its barriers);
-  // at 500 rows 9.2 against 9.8 us.  Narrower rows are as fast or faster with a block a row (4096 x 2048: 14.3 against
-  // 14.5 us, 32768 x 1536 fp32: 96 against 100 us), single rows need fewer threads' work each.
+  // Rows of more than 4096 columns, four for every SM: through the ring, one row in work and 90 KB of them in flight on
+  // an SM.  At 8192 x 7168 with per-row codes 83 us against 105 us for a block a row (few such wide blocks fit an SM, and
+  // all of one waits at each of its barriers); two rows in work 95 us, two vectors a thread instead of three 95 us.
+  // Narrower rows are as fast or faster with a block a row (32768 x 1536 fp32: 96 against 104 us).
   if (vec && a.d > 4096 && a.d <= 8192 && a.T >= 4ll * num_sms) {
     const size_t row = static_cast<size_t>(a.d) * ((a.x ? 2 : 0) + (a.res_f32 ? 4 : 2));
-    const RingShape r = ring_shape(a.T, a.d, 2, row, 106 * 1024, 2 * num_sms);
+    const RingShape r = ring_shape(a.T, a.d, 3, row, 90 * 1024, num_sms);
     return a.res_f32 ? run_norm_ring_form<true>(a, r, s) : run_norm_ring_form<false>(a, r, s);
   }
-  if (!vec) return run_norm<1, 16>(a, round32((a.d + 15) / 16), 1, s);
+  if (!vec) {
+    const int tpr = round32((a.d + 15) / 16);
+    if (a.res_f32) add_rmsnorm_any_kernel<true><<<static_cast<unsigned>(a.T), tpr, 0, s>>>(a);
+    else add_rmsnorm_any_kernel<false><<<static_cast<unsigned>(a.T), tpr, 0, s>>>(a);
+    return cudaGetLastError();
+  }
   const int nvec = a.d / 8;
   // Narrow rows share a block of 128 threads.
-  if (nvec <= 1024) return run_norm<8, 1>(a, round32(nvec), nvec <= 32 ? 4 : nvec <= 64 ? 2 : 1, s);
-  return run_norm<8, 2>(a, round32((nvec + 1) / 2), 1, s);
+  if (nvec <= 1024) return run_norm<1>(a, round32(nvec), nvec <= 32 ? 4 : nvec <= 64 ? 2 : 1, s);
+  return run_norm<2>(a, round32((nvec + 1) / 2), 1, s);
 }
 
 // ------------------------------------------------------------------------------------------- backward
@@ -464,52 +590,64 @@ cudaError_t launch_add_rmsnorm(const NormFwd& a, bool vec, int num_sms, cudaStre
 
 namespace {
 
-// Rows of any width and alignment, straight from global memory; the weight and dh are read where they are needed.
-template <int V, int NV, bool RES32>
-__global__ void __launch_bounds__(512) add_rmsnorm_bwd_kernel(const NormBwd a) {
+// A vector of xhat, of dy g and of the row's sum for c; dg's share grows.
+__device__ __forceinline__ void bwd8(Vec8& dy, Vec8& h, const Vec8& g, Vec8& dg, f32x2 rstd2, f32x2& c) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    h.p[k] = mul2(h.p[k], rstd2);
+    dg.p[k] = fma2(dy.p[k], h.p[k], dg.p[k]);
+    dy.p[k] = mul2(dy.p[k], g.p[k]);
+    c = fma2(dy.p[k], h.p[k], c);
+  }
+}
+
+// o += rstd (dy g) - rstd c xhat, stored in both forms asked for (dx, dres: the vector's places, null: nowhere).
+template <bool RES32>
+__device__ __forceinline__ void bwd_out8(void* dx, void* dres, Vec8& o, const Vec8& dy, const Vec8& h, f32x2 rstd2, f32x2 nc2) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) o.p[k] = fma2(nc2, h.p[k], fma2(rstd2, dy.p[k], o.p[k]));
+  if (dx) store8<false>(dx, 0, o);
+  if (dres) store8<RES32>(dres, 0, o);
+}
+
+template <int ES>
+__device__ __forceinline__ uint8_t* place(void* base, long long t, long long ld, int j) {
+  return base ? static_cast<uint8_t*>(base) + (t * ld + 8ll * j) * ES : nullptr;
+}
+
+// Rows wider than the ring takes, straight from global memory; the weight and dh are read where they are needed.
+template <int NV, bool RES32>
+__global__ void __launch_bounds__(512) add_rmsnorm_bwd_wide_kernel(const NormBwd a) {
   __shared__ float red[2][32];
-  const int nvec = a.d / V;
-  const float inv_d = 1.0f / static_cast<float>(a.d);
-  float dg[NV][V];
+  const int nvec = a.d / 8;
+  Vec8 dg[NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int k = 0; k < V; ++k) dg[i][k] = 0.0f;
+  for (int i = 0; i < NV; ++i) dg[i] = zero8();
+  griddep_launch();
   int it = 0;
   for (long long t = blockIdx.x; t < a.T; t += gridDim.x, ++it) {
     const float rstd = __ldg(a.rstd + t);
-    float dy[NV][V], h[NV][V];
-    float c = 0.0f;
+    const f32x2 rstd2 = pack2(rstd, rstd);
+    Vec8 dy[NV], h[NV];
+    f32x2 c2 = pack2(0.0f, 0.0f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int j = threadIdx.x + blockDim.x * i;
       if (j < nvec) {
-        float g[V];
-        load_v<V, false>(a.dy, t * a.ld_dy + static_cast<long long>(j) * V, dy[i]);
-        load_v<V, RES32>(a.h, t * a.ld_h + static_cast<long long>(j) * V, h[i]);
-        load_weight<V>(a.weight, a.weight_f32 != 0, j * V, g);
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-          h[i][k] *= rstd;
-          dg[i][k] += dy[i][k] * h[i][k];
-          dy[i][k] *= g[k];
-          c += dy[i][k] * h[i][k];
-        }
+        dy[i] = load8<false>(a.dy, t * a.ld_dy + 8ll * j);
+        h[i] = load8<RES32>(a.h, t * a.ld_h + 8ll * j);
+        bwd8(dy[i], h[i], load_weight8(a.weight, a.weight_f32, j), dg[i], rstd2, c2);
       }
     }
-    c = row_reduce<false>(c, red[it & 1]) * inv_d;
+    const float2 cf = unpack2(c2);
+    const float c = row_reduce<false>(cf.x + cf.y, red[it & 1]) / static_cast<float>(a.d);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int j = threadIdx.x + blockDim.x * i;
       if (j < nvec) {
-        float o[V];
-#pragma unroll
-        for (int k = 0; k < V; ++k) o[k] = 0.0f;
-        if (a.dh) load_v<V, RES32>(a.dh, t * a.ld_dh + static_cast<long long>(j) * V, o);
-#pragma unroll
-        for (int k = 0; k < V; ++k) o[k] += rstd * (dy[i][k] - c * h[i][k]);
-        if (a.dx) store_v<V, false>(a.dx, t * a.ld_dx + static_cast<long long>(j) * V, o);
-        if (a.dres) store_v<V, RES32>(a.dres, t * a.ld_dres + static_cast<long long>(j) * V, o);
+        Vec8 o = a.dh ? load8<RES32>(a.dh, t * a.ld_dh + 8ll * j) : zero8();
+        bwd_out8<RES32>(place<2>(a.dx, t, a.ld_dx, j), place<RES32 ? 4 : 2>(a.dres, t, a.ld_dres, j), o, dy[i], h[i], rstd2,
+                        pack2(-rstd * c, -rstd * c));
       }
     }
   }
@@ -517,21 +655,61 @@ __global__ void __launch_bounds__(512) add_rmsnorm_bwd_kernel(const NormBwd a) {
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int j = threadIdx.x + blockDim.x * i;
-    if (j < nvec) {
-#pragma unroll
-      for (int k = 0; k < V; ++k) out[static_cast<long long>(j) * V + k] = dg[i][k];
-    }
+    if (j < nvec) store8<true>(out, 8ll * j, dg[i]);
   }
 }
 
-// The same with the rows (dy, h and dh side by side) through the ring.
+// Rows of any width and alignment, 32 values a thread.
+template <bool RES32>
+__global__ void __launch_bounds__(512) add_rmsnorm_bwd_any_kernel(const NormBwd a) {
+  constexpr int N = 32;
+  __shared__ float red[2][32];
+  float dg[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) dg[i] = 0.0f;
+  griddep_launch();
+  int it = 0;
+  for (long long t = blockIdx.x; t < a.T; t += gridDim.x, ++it) {
+    const float rstd = __ldg(a.rstd + t);
+    float dy[N], h[N], c = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int j = threadIdx.x + blockDim.x * i;
+      if (j < a.d) {
+        dy[i] = load1<false>(a.dy, t * a.ld_dy + j);
+        h[i] = load1<RES32>(a.h, t * a.ld_h + j) * rstd;
+        dg[i] += dy[i] * h[i];
+        dy[i] *= load_weight1(a.weight, a.weight_f32, j);
+        c += dy[i] * h[i];
+      }
+    }
+    c = row_reduce<false>(c, red[it & 1]) / static_cast<float>(a.d);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int j = threadIdx.x + blockDim.x * i;
+      if (j < a.d) {
+        const float o = (a.dh ? load1<RES32>(a.dh, t * a.ld_dh + j) : 0.0f) + rstd * (dy[i] - c * h[i]);
+        if (a.dx) store1<false>(a.dx, t * a.ld_dx + j, o);
+        if (a.dres) store1<RES32>(a.dres, t * a.ld_dres + j, o);
+      }
+    }
+  }
+  float* out = gridDim.x == 1 ? a.dweight : a.part + static_cast<long long>(blockIdx.x) * a.d;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int j = threadIdx.x + blockDim.x * i;
+    if (j < a.d) out[j] = dg[i];
+  }
+}
+
+// Rows (dy, h and dh side by side) through the ring.
 template <int NV, bool RES32>
-__global__ void __launch_bounds__(512) add_rmsnorm_bwd_ring_kernel(const NormBwd a, int stages) {
-  constexpr int V = 8, ES = RES32 ? 4 : 2;
+__global__ void __launch_bounds__(512, 1) add_rmsnorm_bwd_ring_kernel(const NormBwd a, int stages) {
+  constexpr int ES = RES32 ? 4 : 2;
   extern __shared__ __align__(128) uint8_t nb_ring[];
   __shared__ __align__(16) RingShared sh;
   const int rg = threadIdx.y, RG = blockDim.y, tx = threadIdx.x, tpr = blockDim.x;
-  const int nvec = a.d / V;
+  const int nvec = a.d / 8;
   const uint32_t dyb = 2u * a.d, hb = static_cast<uint32_t>(ES) * a.d, sb = dyb + hb + (a.dh ? hb : 0u);
   uint8_t* ring = nb_ring + static_cast<size_t>(rg) * stages * sb;
   const long long step = static_cast<long long>(gridDim.x) * RG, t0 = static_cast<long long>(blockIdx.x) * RG + rg;
@@ -547,60 +725,54 @@ __global__ void __launch_bounds__(512) add_rmsnorm_bwd_ring_kernel(const NormBwd
   if (tx == 0)
     for (int k = 0; k < stages; ++k)
       if (t0 + k * step < a.T) issue(t0 + k * step, k);
-  float g[NV][V], dg[NV][V];
+  griddep_launch();  // the launch that adds the blocks' shares waits for this one's end
+  Vec8 g[NV], dg[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int j = tx + tpr * i;
-#pragma unroll
-    for (int k = 0; k < V; ++k) g[i][k] = dg[i][k] = 0.0f;
-    if (j < nvec) load_weight<V>(a.weight, a.weight_f32 != 0, j * V, g[i]);
+    g[i] = dg[i] = zero8();
+    if (j < nvec) g[i] = load_weight8(a.weight, a.weight_f32, j);
   }
   const float inv_d = 1.0f / static_cast<float>(a.d);
   float rstd_next = t0 < a.T ? __ldg(a.rstd + t0) : 0.0f;
+  uint8_t *dx = place<2>(a.dx, t0, a.ld_dx, tx), *dres = place<ES>(a.dres, t0, a.ld_dres, tx);
   int it = 0, st = 0, ph = 0;
   for (long long t = t0; t < a.T; t += step, ++it) {
     const float rstd = rstd_next;
+    const f32x2 rstd2 = pack2(rstd, rstd);
     if (t + step < a.T) rstd_next = __ldg(a.rstd + t + step);
     mbar_wait(&sh.full[rg][st], ph, &sh.abort, a.timeout_ns, a.err);
     const uint8_t* src = ring + static_cast<size_t>(st) * sb;
-    float dy[NV][V], h[NV][V], o[NV][V];
-    float c = 0.0f;
+    Vec8 dy[NV], h[NV], o[NV];
+    f32x2 c2 = pack2(0.0f, 0.0f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int j = tx + tpr * i;
       if (j < nvec) {
-        load_smem8<false>(src, j, dy[i]);
-        load_smem8<RES32>(src + dyb, j, h[i]);
-        if (a.dh) load_smem8<RES32>(src + dyb + hb, j, o[i]);
-        else {
-#pragma unroll
-          for (int k = 0; k < V; ++k) o[i][k] = 0.0f;
-        }
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-          h[i][k] *= rstd;
-          dg[i][k] += dy[i][k] * h[i][k];
-          dy[i][k] *= g[i][k];
-          c += dy[i][k] * h[i][k];
-        }
+        dy[i] = load_smem8<false>(src, j);
+        h[i] = load_smem8<RES32>(src + dyb, j);
+        o[i] = a.dh ? load_smem8<RES32>(src + dyb + hb, j) : zero8();
+        bwd8(dy[i], h[i], g[i], dg[i], rstd2, c2);
       }
     }
-    c = group_reduce<false>(c, sh.red[it & 1][rg]) * inv_d;
+    const float2 cf = unpack2(c2);
+    float c = cf.x + cf.y, none = 0.0f;
+    group_reduce<false>(c, none, sh.red[it & 1][rg], sh.red2[it & 1][rg]);
+    c *= inv_d;
     if (tx == 0 && t + stages * step < a.T) issue(t + stages * step, st);
     if (++st == stages) {
       st = 0;
       ph ^= 1;
     }
+    const f32x2 nc2 = pack2(-rstd * c, -rstd * c);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int j = tx + tpr * i;
-      if (j < nvec) {
-#pragma unroll
-        for (int k = 0; k < V; ++k) o[i][k] += rstd * (dy[i][k] - c * h[i][k]);
-        if (a.dx) store8<false>(a.dx, t * a.ld_dx + static_cast<long long>(j) * V, o[i]);
-        if (a.dres) store8<RES32>(a.dres, t * a.ld_dres + static_cast<long long>(j) * V, o[i]);
-      }
+      if (j < nvec)
+        bwd_out8<RES32>(dx ? dx + 16 * tpr * i : nullptr, dres ? dres + 8 * ES * tpr * i : nullptr, o[i], dy[i], h[i], rstd2, nc2);
     }
+    if (dx) dx += step * a.ld_dx * 2;
+    if (dres) dres += step * a.ld_dres * ES;
   }
   ring_drain(sh, stages, it);
   // the groups' shares, added in group order
@@ -609,7 +781,7 @@ __global__ void __launch_bounds__(512) add_rmsnorm_bwd_ring_kernel(const NormBwd
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int j = tx + tpr * i;
-    if (j < nvec) store8<true>(RG > 1 ? share + static_cast<size_t>(rg) * a.d : out, static_cast<long long>(j) * V, dg[i]);
+    if (j < nvec) store8<true>(RG > 1 ? share + static_cast<size_t>(rg) * a.d : out, 8ll * j, dg[i]);
   }
   if (RG == 1) return;
   __syncthreads();
@@ -620,14 +792,21 @@ __global__ void __launch_bounds__(512) add_rmsnorm_bwd_ring_kernel(const NormBwd
   }
 }
 
-// out[j] = sum_b part[b][j]: 32 columns a block, 32 threads of partial sums each, added in a fixed order.
+// out[j] = sum_b part[b][j]: 32 columns a block, 32 threads of partial sums each, four loads in flight, added in a fixed
+// order.  A dependent launch: it is set up while the rows are still worked on.
 __global__ void __launch_bounds__(1024) reduce_rows_kernel(const float* __restrict__ part, int parts, int d,
                                                            float* __restrict__ out) {
   __shared__ float sm[32][33];
+  griddep_wait();
   const int j = blockIdx.x * 32 + threadIdx.x;
   float v = 0.0f;
-  if (j < d)
-    for (int b = threadIdx.y; b < parts; b += 32) v += part[static_cast<long long>(b) * d + j];
+  for (int b0 = threadIdx.y; b0 < parts; b0 += 128) {
+    float x[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[k] = j < d && b0 + 32 * k < parts ? part[static_cast<long long>(b0 + 32 * k) * d + j] : 0.0f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v += x[k];
+  }
   sm[threadIdx.y][threadIdx.x] = v;
   __syncthreads();
   v = sm[threadIdx.x][threadIdx.y];
@@ -635,13 +814,6 @@ __global__ void __launch_bounds__(1024) reduce_rows_kernel(const float* __restri
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   const int jo = blockIdx.x * 32 + threadIdx.y;
   if (threadIdx.x == 0 && jo < d) out[jo] = v;
-}
-
-template <int V, int NV>
-cudaError_t run_norm_bwd(const NormBwd& a, int tpr, int grid, cudaStream_t s) {
-  if (a.res_f32) add_rmsnorm_bwd_kernel<V, NV, true><<<grid, tpr, 0, s>>>(a);
-  else add_rmsnorm_bwd_kernel<V, NV, false><<<grid, tpr, 0, s>>>(a);
-  return cudaGetLastError();
 }
 
 template <int NV, bool RES32>
@@ -661,22 +833,28 @@ cudaError_t launch_add_rmsnorm_bwd(const NormBwd& a, bool vec, int num_sms, cuda
   cudaError_t e;
   int parts;
   if (vec && a.d <= 8192) {
-    // 150 KB of rows in flight on an SM: with the whole shared memory 8192 x 7168 fp32 took 164 us against 155 and
-    // 8192 x 5120 fp32 116 against 103, with two stages 8192 x 7168 bf16 81 against 74.
-    const bool narrow = a.d <= 1024;
-    const RingShape r = ring_shape(a.T, a.d, narrow ? 1 : 2, row, 150 * 1024, num_sms);
+    // 144 KB of rows in flight on an SM: 8192 x 5120 fp32 (51 KB a row) takes 105 us with two rows and 116 with three,
+    // 8192 x 7168 bf16 (43 KB) 74 us with three and 80 with two.  One vector a thread for narrow rows and for fp32
+    // streams, which bring twice the work a vector (32768 x 1536 fp32: 119 us against 140 with two), else two (8192 x
+    // 1024 bf16: 17.9 against 19.5).
+    const bool one = a.d <= (a.res_f32 ? 4096 : 256);
+    const RingShape r = ring_shape(a.T, a.d, one ? 1 : 2, row, 144 * 1024, num_sms);
     parts = r.grid;
-    if (narrow) e = a.res_f32 ? run_norm_bwd_ring<1, true>(a, r, s) : run_norm_bwd_ring<1, false>(a, r, s);
+    if (one) e = a.res_f32 ? run_norm_bwd_ring<1, true>(a, r, s) : run_norm_bwd_ring<1, false>(a, r, s);
     else e = a.res_f32 ? run_norm_bwd_ring<2, true>(a, r, s) : run_norm_bwd_ring<2, false>(a, r, s);
   } else {
     const long long most = 4ll * num_sms < kMaxNormParts ? 4ll * num_sms : kMaxNormParts;
     parts = static_cast<int>(a.T < most ? a.T : most);
-    if (!vec) e = run_norm_bwd<1, 32>(a, round32((a.d + 31) / 32), parts, s);
-    else e = run_norm_bwd<8, 4>(a, round32((a.d / 8 + 3) / 4), parts, s);
+    const int tpr = vec ? round32((a.d / 8 + 3) / 4) : round32((a.d + 31) / 32);
+    if (vec && a.res_f32) add_rmsnorm_bwd_wide_kernel<4, true><<<parts, tpr, 0, s>>>(a);
+    else if (vec) add_rmsnorm_bwd_wide_kernel<4, false><<<parts, tpr, 0, s>>>(a);
+    else if (a.res_f32) add_rmsnorm_bwd_any_kernel<true><<<parts, tpr, 0, s>>>(a);
+    else add_rmsnorm_bwd_any_kernel<false><<<parts, tpr, 0, s>>>(a);
+    e = cudaGetLastError();
   }
   if (e != cudaSuccess || parts == 1) return e;
-  reduce_rows_kernel<<<(a.d + 31) / 32, dim3(32, 32), 0, s>>>(a.part, parts, a.d, a.dweight);
-  return cudaGetLastError();
+  return launch_dependent(reduce_rows_kernel, dim3((a.d + 31) / 32), dim3(32, 32), 0, s, static_cast<const float*>(a.part), parts,
+                          a.d, a.dweight);
 }
 
 }  // namespace vgg

@@ -268,21 +268,6 @@ __global__ void __launch_bounds__(256) router_dw_reduce_kernel(const float* __re
   }
 }
 
-template <class... P, class... A>
-cudaError_t launch_dependent(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, args...);
-}
-
 }  // namespace
 
 cudaError_t launch_split_dlogits(const float* dlogits, long long T, long long Tp, int E, __nv_bfloat16* parts, cudaStream_t s) {
