@@ -71,15 +71,10 @@ __device__ __forceinline__ int seq_begin(const BalanceArgs& a, int b) {
 // within the chunk, whatever the offsets hold (the last sequence reaches to T).
 struct Piece {
   int b, t0, t1;
-  __device__ void first(const BalanceArgs& a, int c0) {
-    int lo = 0, hi = a.B;  // the last b with seq_begin(b) <= c0
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (seq_begin(a, mid) <= c0) lo = mid;
-      else hi = mid;
-    }
-    b = lo;
-    t1 = c0;
+  // b0: the last sequence that begins at c0 or before
+  __device__ void first(int b0, int c0) {
+    b = b0;
+    t0 = t1 = c0;
   }
   __device__ bool next(const BalanceArgs& a, int c1) {
     if (t1 >= c1) return false;
@@ -102,8 +97,8 @@ struct Tiles {
       tb = pc.t0 + warp * kTile;
     }
   }
-  __device__ void first(const BalanceArgs& a, int c0, int c1, int warp) {
-    pc.first(a, c0);
+  __device__ void first(const BalanceArgs& a, int b0, int c0, int c1, int warp) {
+    pc.first(b0, c0);
     ok = true;
     tb = pc.t1;
     skip(a, c1, warp);
@@ -195,10 +190,34 @@ __global__ void __launch_bounds__(kBalThreads) balance_kernel(const BalanceArgs 
   } else {
     __syncthreads();
   }
+  // the chunk's first sequence: every thread looks at some of them (a search would take a memory latency a step)
+  int b0 = 0;
+  for (int k = 0; k < a.B; k += kBalThreads) {
+    const int begun = __syncthreads_count(k + tid < a.B && seq_begin(a, k + tid) <= c0);
+    b0 += begun;
+    if (begun < kBalThreads) break;
+  }
+  b0 = max(b0 - 1, 0);
   // (1) counts
   Piece pc;
-  pc.first(a, c0);
-  while (pc.next(a, c1)) {
+  pc.first(b0, c0);
+  if (pc.next(a, c1) && pc.t1 < c1) {
+    // a chunk of several sequences: straight to the sums, without a pass and two barriers for every piece
+    const int32_t* ids = a.topk_ids + static_cast<long long>(c0) * K;
+    int b = pc.b;
+    for (int i = tid; i < (c1 - c0) * K; i += kBalThreads) {
+      const int t = c0 + static_cast<int>(static_cast<unsigned>(i) / static_cast<unsigned>(K));
+      const int id = __ldg(ids + i);
+      while (b + 1 < a.B && seq_begin(a, b + 1) <= t) ++b;
+      if (a.mask && !a.mask[t]) continue;
+      if (i - (t - c0) * K == 0) {  // one addition for a warp's tokens of a sequence
+        const unsigned same = __match_any_sync(__activemask(), b);
+        if (lane == __ffs(same) - 1) atomicAdd(w.nvalid + b, __popc(same));
+      }
+      if (id < 0 || id >= E) set_error(a.err, DERR_BAD_EXPERT);
+      else atomicAdd(w.cnt + static_cast<long long>(b) * E + id, 1);
+    }
+  } else if (pc.t1 > pc.t0) {
     const int pairs = (pc.t1 - pc.t0) * K;
     const int32_t* ids = a.topk_ids + static_cast<long long>(pc.t0) * K;
     int n = 0;
@@ -228,18 +247,9 @@ __global__ void __launch_bounds__(kBalThreads) balance_kernel(const BalanceArgs 
     n = __reduce_add_sync(0xffffffffu, n);
     if (lane == 0 && n) atomicAdd(&s_n, n);
     __syncthreads();
-    for (int e = tid; e < E; e += kBalThreads) {
-      const int v = hist[e];
-      if (v) {
-        atomicAdd(w.cnt + static_cast<long long>(pc.b) * E + e, v);
-        hist[e] = 0;
-      }
-    }
-    if (tid == 0) {
-      if (s_n) atomicAdd(w.nvalid + pc.b, s_n);
-      s_n = 0;
-    }
-    __syncthreads();
+    for (int e = tid; e < E; e += kBalThreads)
+      if (hist[e]) atomicAdd(w.cnt + static_cast<long long>(pc.b) * E + e, hist[e]);
+    if (tid == 0 && s_n) atomicAdd(w.nvalid + pc.b, s_n);
   }
   // the first tiles of logits come while the blocks wait for one another
   Tiles<kTile> in;  // lane 0's next tile to ask for
@@ -253,7 +263,7 @@ __global__ void __launch_bounds__(kBalThreads) balance_kernel(const BalanceArgs 
     in.next(a, c1, warp);
   };
   if (VEC && lane == 0) {
-    in.first(a, c0, c1, warp);
+    in.first(a, b0, c0, c1, warp);
     for (int k = 0; k < ST && in.ok; ++k) issue();
   }
   const bool counted = barrier(1);  // where it gave up: run on, so that every copy is waited for
@@ -288,9 +298,9 @@ __global__ void __launch_bounds__(kBalThreads) balance_kernel(const BalanceArgs 
       if (e < E) cnt_next[k] = __ldcg(w.cnt + static_cast<long long>(pn.b) * E + e);
     }
   };
-  pn.first(a, c0);
+  pn.first(b0, c0);
   fetch();
-  pc.first(a, c0);
+  pc.first(b0, c0);
   while (pc.next(a, c1)) {
     const int nb = nb_next;
     const float inv_kn = nb > 0 ? 1.0f / (static_cast<float>(K) * static_cast<float>(nb)) : 0.0f;
@@ -311,9 +321,13 @@ __global__ void __launch_bounds__(kBalThreads) balance_kernel(const BalanceArgs 
       u[i] = pack2(e0 < E ? su[e0] : 0.0f, e1 < E ? su[e1] : 0.0f);
     }
     const float cb = nb > 0 ? a.balance_coef * scale / (nu.y * static_cast<float>(nb)) : 0.0f;
+    // which of a tile's tokens count, looked up a tile ahead
+    auto counts_here = [&](int t) { return lane < kTile && t + lane < pc.t1 && (!a.mask || a.mask[t + lane]); };
+    bool mine = counts_here(pc.t0 + warp * kTile);
     for (int tb = pc.t0 + warp * kTile; tb < pc.t1; tb += kBalWarps * kTile) {
       const float* src = ring + static_cast<size_t>(st) * kTile * E;
-      const unsigned here = __ballot_sync(0xffffffffu, lane < kTile && tb + lane < pc.t1 && (!a.mask || a.mask[tb + lane]));
+      const unsigned here = __ballot_sync(0xffffffffu, mine);
+      mine = counts_here(tb + kBalWarps * kTile);
       if (VEC) mbar_wait(&full[warp][st], ph, &s_abort, a.timeout_ns, a.err);
       // the UN tokens of a lane go through every step together, which hides the latency of the lane sums
       f32x2 v[UN][kPairs];
