@@ -1177,12 +1177,26 @@ __global__ void __launch_bounds__(WarpPlan<STAGES, EW, AMODE, BMODE, CN, XF>::kT
         }
       }
     };
+    // and those of a tile further ahead into L2: the loads a tile ahead then wait for L2, not for HBM
+    auto prefetch_add = [&](int t2) {
+      if constexpr (EPI == EPI_ADD) {
+        if (lane == 0 && t2 < sch.total) {
+          Tile x;
+          int gn = 0;
+          sch.decode(p, t2, gn, x);
+          const int c0 = x.n0 + half * 64 * kAddBufs;
+          for (int q = 0; q < kAddBufs && c0 + 64 * q < p.N; ++q)
+            tma_prefetch_l2_3d(&mp.o1, c0 + 64 * q, x.m0 + quarter * 32, 0);
+        }
+      }
+    };
     if constexpr (EPI == EPI_ADD) {
       if (p.add && sch.first < sch.total) {
         Tile x;
         int gn = 0;
         sch.decode(p, sch.first, gn, x);
         load_add(x);
+        prefetch_add(sch.first + sch.stride);
       }
     }
     // 32 columns (fp32, or bf16 through a 64-byte-swizzled box)
@@ -1474,6 +1488,7 @@ __global__ void __launch_bounds__(WarpPlan<STAGES, EW, AMODE, BMODE, CN, XF>::kT
             int gn = gcur;
             sch.decode(p, t + sch.stride, gn, nx);
             load_add(nx);
+            prefetch_add(t + 2 * sch.stride);
           }
         } else if (VAR == VAR_K && mw >= p.M) {
           // rows past the output (the odd CTA of a pair on the last row tile): nothing to store
