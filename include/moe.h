@@ -518,9 +518,10 @@ int moe_backward_e4m3(moe_ctx* ctx, const void* dO, const void* X, const void* W
  *   rstd[t] = 1 / sqrt(mean_j h[t,j]^2 + eps)
  *   y[t,j]  = h[t,j] * rstd[t] * weight[j]   in fp32, stored as bf16
  *
- * q_form 0: no codes.  1: scales [T] fp32 = max_j |y[t,j]| / 448 (1 for a zero row), q [T,d] = e4m3(y / scale).
- * 2: scales [T][moe_mx_sf_cols(d)] bytes and q as moe_quantize_rows_mx.  Both quantize the fp32 y (not its bf16
- * rounding) by the rules of moe_quantize_rows_e4m3 / moe_quantize_rows_mx.
+ * q_form 0: no codes.  1: scales [T] fp32 = max_j |y[t,j]| / 448 (1 for a zero row), q [T,d] = e4m3(y * (448 / max))
+ * with the factor rounded to fp32 once a row (moe_quantize_rows_e4m3 divides every value by the scale: the quotients
+ * differ in their last bit at most).  2: scales [T][moe_mx_sf_cols(d)] bytes and q by the rule of
+ * moe_quantize_rows_mx.  Both quantize the fp32 y, not its bf16 rounding.
  *
  * x [T,d] bf16; weight [d] bf16, or fp32 with weight_fp32 != 0; h has the stream's type, y is bf16.  Row strides
  * (ld_*, in elements, >= d) are free; columns are contiguous.  h may be the residual itself and y may be x (every
@@ -572,8 +573,10 @@ int moe_add_rmsnorm_backward(moe_ctx* ctx, const void* dy, long long ld_dy, cons
  * counted); mask [T] bytes; seq_offsets [B+1] int32 (not from 0 to T without falling: MOE_DEV_BAD_OFFSETS, the
  * results are then undefined); counts [B,E] int32, probs [B,E] fp32, loss [3] fp32.  1 <= E <= 1024, 1 <= K <= E,
  * T * K and B * E below 2^31, T = 0 allowed.  ws: caller-owned, 256-byte aligned, at least
- * moe_balance_loss_workspace_bytes(T, E, B) bytes (0 on bad sizes).  One cooperative launch (grid barriers bounded by
- * moe_set_wait_timeout; one that gives up records MOE_DEV_TIMEOUT).  Sums run in a fixed order.
+ * moe_balance_loss_workspace_bytes(T, E, B) bytes (0 on bad sizes).  A small batch is one launch (a block or a
+ * cluster), a larger one the clearing of ws and a cooperative launch (grid barriers bounded by moe_set_wait_timeout; one
+ * that gives up records MOE_DEV_TIMEOUT).  A loss whose coefficient is 0 adds nothing to loss[0], whatever its value.
+ * Sums run in a fixed order.
  */
 size_t moe_balance_loss_workspace_bytes(long long T, int E, int B);
 int moe_balance_loss(moe_ctx* ctx, const float* logits, const int32_t* topk_ids, const uint8_t* mask,
@@ -590,9 +593,9 @@ int moe_balance_loss(moe_ctx* ctx, const float* logits, const int32_t* topk_ids,
  *
  * dlogits [T,E] fp32 enters the first product rounded to bf16 and the second as three bf16 parts, which together
  * hold its 24 significant bits; fp32 accumulation.  X, dX_in, dX [T,d], W_r [d,E] bf16; dW_r_in, dW_r
- * [d,E] fp32; an output may be its own input.  dX or dW_r may be NULL (that product is skipped).  T <= 65536 (0
- * allowed), d a multiple of 64, E a multiple of 8 up to 1024, 16-byte aligned.  ws: caller-owned, 256-byte aligned,
- * at least moe_router_backward_workspace_bytes(T, d, E) bytes (0 on bad sizes).
+ * [d,E] fp32; dX may be dX_in and dW_r may be dW_r_in, no other input.  dX or dW_r may be NULL (that product is
+ * skipped).  T <= 65536 (0 allowed), d a multiple of 64, E a multiple of 8 up to 1024, 16-byte aligned.  ws:
+ * caller-owned, 256-byte aligned, at least moe_router_backward_workspace_bytes(T, d, E) bytes (0 on bad sizes).
  */
 size_t moe_router_backward_workspace_bytes(int T, int d, int E);
 int moe_router_backward(moe_ctx* ctx, const float* dlogits, const void* X, const void* W_r, int T, int d, int E,

@@ -100,6 +100,11 @@ def test_router_backward_refusals(L, fake, bad):
     assert _call(L, fake, "moe_router_backward", ROUTER, **bad) == 1
 
 
+def test_router_backward_of_no_tokens(L, fake):
+    """dX has no elements, so no address; with dW_r left out as well nothing is asked for, and nothing is done."""
+    assert _call(L, fake, "moe_router_backward", ROUTER, T=0, dlogits=None, X=None, dX=None, dW_r=None) == 0
+
+
 def test_router_workspace(L):
     f = L.moe_router_backward_workspace_bytes
     assert f(100, 64, 8) == 128 * 8 * 2 * 3 + 16 * 64 * 8 * 4 and f(0, 64, 8) == 16 * 64 * 8 * 4

@@ -1674,12 +1674,13 @@ size_t moe_router_backward_workspace_bytes(int T, int d, int E) {
 int moe_router_backward(moe_ctx* ctx, const float* dlogits, const void* X, const void* W_r, int T, int d, int E,
                         const void* dX_in, const float* dW_r_in, void* dX, float* dW_r, void* ws, size_t ws_bytes,
                         moe_stream_t stream) {
-  VGG_REQUIRE(ctx && router_bwd_sizes_ok(T, d, E) && (dX || dW_r));
+  VGG_REQUIRE(ctx && router_bwd_sizes_ok(T, d, E) && (dX || dW_r || T == 0));
   VGG_REQUIRE(T == 0 || (dlogits && (!dX || W_r) && (!dW_r || X)));
   VGG_REQUIRE(aligned16(dlogits) && aligned16(X) && aligned16(W_r) && aligned16(dX_in) && aligned16(dW_r_in) &&
               aligned16(dX) && aligned16(dW_r));
   VGG_REQUIRE(ws && (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1)) == 0 &&
               ws_bytes >= moe_router_backward_workspace_bytes(T, d, E));
+  if (T == 0 && !dW_r) return MOE_OK;
   DeviceGuard g(ctx->device);
   VGG_REQUIRE(g.ok);
   cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -16,6 +16,8 @@
 // chunk crosses into another sequence it closes a piece.  The piece of (chunk c, sequence b) has the index c + b,
 // unique because every next piece moves on by a chunk, a sequence or both.  Sums over tokens run in a fixed order,
 // so equal calls give equal bits.
+// 64 x 8 7.8 us and 4096 x 128 12.0 us (the phases' latency and the barriers between them); 32768 x 512 in 37
+// sequences 42.6 us (135 MB; the pass itself 17 us, counting with its barrier 10, uneven blocks 6, the last phase 3).
 #include "internal.h"
 
 namespace vgg {

@@ -9,6 +9,9 @@
 // Both directions move every element once and are bound by HBM and, with rows of 2 bytes an element, nearly as much by
 // issue slots (hence the packed arithmetic).  A row's values stay in registers between the reduction and the
 // output: thread i of a row's tpr threads holds the vectors of eight values i, i + tpr, ... (NV of them).
+// Forward: 8192 x 7168 with per-row codes 83 us (529 MB, 6.4 TB/s), 32768 x 1536 fp32 with block-scaled codes 98 us
+// (656 MB, 6.7 TB/s), a copy running at 6.7; 61 rows of 2048 2.2 us, one row of 7168 3.0 us (a launch and a row's latency).
+// Backward: 8192 x 7168 fp32 155 us (940 MB, 6.0 TB/s), 4096 x 2048 18.4 us with its second launch (67 MB).
 #include <type_traits>
 
 #include "internal.h"
