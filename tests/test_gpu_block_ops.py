@@ -330,6 +330,15 @@ def test_balance_packed(vgg, ctx, T, E, K, B):
     check_balance(run_balance(vgg, ctx, logits, ids, 0.3, 0.0, None, off), logits, ids, 0.3, 0.0, None, off)
 
 
+@pytest.mark.parametrize("T,E,K,B", [(9000, 96, 2, 4000), (5000, 128, 8, 60), (700, 512, 1, 700)])
+def test_balance_many_sequences_in_a_block(vgg, ctx, T, E, K, B):
+    """More sequences in a block's share of the tokens than it has histograms for, and two or three."""
+    logits, ids, g = router_inputs(T, E, K, T + E + B)
+    off = [0] + sorted(np.random.default_rng(B).integers(0, T + 1, B - 1).tolist()) + [T]
+    mask = torch.rand(T, device="cuda", generator=g) < 0.7
+    check_balance(run_balance(vgg, ctx, logits, ids, 0.3, 0.02, mask, off), logits, ids, 0.3, 0.02, mask, off)
+
+
 def test_balance_masked_logits(vgg, ctx):
     """Experts closed to a token (-inf), large logits of both signs, a token with no open expert, and values that
     are not finite in a row that does not count."""

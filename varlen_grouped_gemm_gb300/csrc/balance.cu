@@ -16,8 +16,9 @@
 // chunk crosses into another sequence it closes a piece.  The piece of (chunk c, sequence b) has the index c + b,
 // unique because every next piece moves on by a chunk, a sequence or both.  Sums over tokens run in a fixed order,
 // so equal calls give equal bits.
-// 64 x 8 7.8 us and 4096 x 128 12.0 us (the phases' latency and the barriers between them); 32768 x 512 in 37
-// sequences 42.6 us (135 MB; the pass itself 17 us, counting with its barrier 10, uneven blocks 6, the last phase 3).
+// 64 x 8 7.5 us and 4096 x 128 11.1 us (the phases' latency and the barriers between them); 32768 x 512 in 37
+// sequences 39.8 us (135 MB, 20 us of them): launch and clearing 3, counting under the first loads 6, barriers 3, blocks
+// that memory serves unevenly 5, the last phase 3.
 #include "internal.h"
 
 namespace vgg {
@@ -28,7 +29,9 @@ constexpr int kBalThreads = 512;
 constexpr int kBalWarps = kBalThreads / 32;
 constexpr int kBalMaxBlocks = 1024;  // bounds the number of pieces, and with it the workspace
 constexpr int kBalCluster = 16;      // up to so many blocks wait for one another as a cluster, more as a whole grid
-constexpr long long kBalOneCluster = 1 << 18;  // most logits that one cluster takes
+// Most logits that one cluster takes.  Eager calls of 2048 x 128: 12.3 us in a cluster, 15.4 as a cooperative grid with the
+// clearing ahead of it; 4096 x 128: 16.4 and 15.4 (in a graph 13.8 and 11.3).
+constexpr long long kBalOneCluster = 1 << 18;
 
 inline size_t al256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
@@ -87,20 +90,28 @@ struct Piece {
   }
 };
 
-// A warp's tiles of up to kTile tokens in order: of every piece, each kBalWarps-th from the warp's own.
+// A warp's tiles of up to kTile tokens in order: each kBalWarps-th of the chunk's, whose count runs on from one piece into
+// the next, so that the warps' shares differ by one tile at most however many pieces there are.
 template <int kTile>
 struct Tiles {
   Piece pc;
   int tb;
+  int nth;  // the chunk's tiles before this piece
   bool ok;
+  static __device__ int first_of(const Piece& p, int nth, int warp) {  // the warp's first tile of a piece begins here
+    return p.t0 + ((warp - nth) & (kBalWarps - 1)) * kTile;
+  }
+  static __device__ int count(const Piece& p) { return (p.t1 - p.t0 + kTile - 1) / kTile; }
   __device__ void skip(const BalanceArgs& a, int c1, int warp) {
     while (ok && tb >= pc.t1) {
+      nth += count(pc);
       ok = pc.next(a, c1);
-      tb = pc.t0 + warp * kTile;
+      tb = first_of(pc, nth, warp);
     }
   }
   __device__ void first(const BalanceArgs& a, int b0, int c0, int c1, int warp) {
     pc.first(b0, c0);
+    nth = 0;
     ok = true;
     tb = pc.t1;
     skip(a, c1, warp);
@@ -161,7 +172,7 @@ __global__ void __launch_bounds__(kBalThreads) balance_kernel(const BalanceArgs 
   __shared__ float2 s_red[kBalWarps];
   __shared__ float s_tile[kBalWarps][33];
   __shared__ __align__(8) uint64_t full[kBalWarps][ST];
-  __shared__ int s_n, s_ok, s_abort;
+  __shared__ int s_n[kBalWarps], s_ok, s_abort;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int G = gridDim.x, E = a.E, K = a.K, T = static_cast<int>(a.T);
   const int c0 = min(T, static_cast<int>(blockIdx.x) * chunk), c1 = min(T, c0 + chunk);
@@ -179,11 +190,12 @@ __global__ void __launch_bounds__(kBalThreads) balance_kernel(const BalanceArgs 
     }
     return grid_barrier(w.ctrl, nth * G, a.timeout_ns, a.err, &s_ok);
   };
-  if (tid == 0) s_abort = s_n = 0;
+  if (tid == 0) s_abort = 0;
+  if (tid < kBalWarps) s_n[tid] = 0;
   if (VEC && lane < ST) mbar_init(&full[warp][lane], 1);
   fence_mbar_init();
   int* hist = reinterpret_cast<int*>(sums);
-  for (int e = tid; e < E; e += kBalThreads) hist[e] = 0;
+  for (int i = tid; i < (a.B > 1 ? kBalWarps : 1) * E; i += kBalThreads) hist[i] = 0;
   if (G <= kBalCluster) {  // a small grid clears its own workspace
     int* z = w.ctrl;
     for (size_t i = blockIdx.x * kBalThreads + tid; i < w.zeroed / sizeof(int); i += static_cast<size_t>(G) * kBalThreads)
@@ -200,60 +212,7 @@ __global__ void __launch_bounds__(kBalThreads) balance_kernel(const BalanceArgs 
     if (begun < kBalThreads) break;
   }
   b0 = max(b0 - 1, 0);
-  // (1) counts
-  Piece pc;
-  pc.first(b0, c0);
-  if (pc.next(a, c1) && pc.t1 < c1) {
-    // a chunk of several sequences: straight to the sums, without a pass and two barriers for every piece
-    const int32_t* ids = a.topk_ids + static_cast<long long>(c0) * K;
-    int b = pc.b;
-    for (int i = tid; i < (c1 - c0) * K; i += kBalThreads) {
-      const int t = c0 + static_cast<int>(static_cast<unsigned>(i) / static_cast<unsigned>(K));
-      const int id = __ldg(ids + i);
-      while (b + 1 < a.B && seq_begin(a, b + 1) <= t) ++b;
-      if (a.mask && !a.mask[t]) continue;
-      if (i - (t - c0) * K == 0) {  // one addition for a warp's tokens of a sequence
-        const unsigned same = __match_any_sync(__activemask(), b);
-        if (lane == __ffs(same) - 1) atomicAdd(w.nvalid + b, __popc(same));
-      }
-      if (id < 0 || id >= E) set_error(a.err, DERR_BAD_EXPERT);
-      else atomicAdd(w.cnt + static_cast<long long>(b) * E + id, 1);
-    }
-  } else if (pc.t1 > pc.t0) {
-    const int pairs = (pc.t1 - pc.t0) * K;
-    const int32_t* ids = a.topk_ids + static_cast<long long>(pc.t0) * K;
-    int n = 0;
-    for (int i0 = tid; i0 < pairs; i0 += 4 * kBalThreads) {
-      int id[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {  // four loads in flight
-        const int i = i0 + k * kBalThreads;
-        id[k] = -1;
-        if (i >= pairs) continue;
-        const int t = static_cast<int>(static_cast<unsigned>(i) / static_cast<unsigned>(K));
-        id[k] = __ldg(ids + i);
-        if (a.mask && !a.mask[pc.t0 + t]) {
-          id[k] = -1;
-          continue;
-        }
-        if (i - t * K == 0) ++n;
-        if (id[k] < 0 || id[k] >= E) {
-          set_error(a.err, DERR_BAD_EXPERT);
-          id[k] = -1;
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (id[k] >= 0) atomicAdd(&hist[id[k]], 1);
-    }
-    n = __reduce_add_sync(0xffffffffu, n);
-    if (lane == 0 && n) atomicAdd(&s_n, n);
-    __syncthreads();
-    for (int e = tid; e < E; e += kBalThreads)
-      if (hist[e]) atomicAdd(w.cnt + static_cast<long long>(pc.b) * E + e, hist[e]);
-    if (tid == 0 && s_n) atomicAdd(w.nvalid + pc.b, s_n);
-  }
-  // the first tiles of logits come while the blocks wait for one another
+  // the first tiles of logits come while the choices are counted and the blocks wait for one another
   Tiles<kTile> in;  // lane 0's next tile to ask for
   int st_in = 0;
   auto issue = [&]() {
@@ -268,8 +227,62 @@ __global__ void __launch_bounds__(kBalThreads) balance_kernel(const BalanceArgs 
     in.first(a, b0, c0, c1, warp);
     for (int k = 0; k < ST && in.ok; ++k) issue();
   }
+  // (1) counts: choices and mask bytes four ahead, all loads of a round before its first addition (an error's record
+  // would hold the loads behind it back).  The chunk's first kBalWarps sequences have a histogram each in shared memory,
+  // their rows as in cnt; those of further ones go straight there.
+  Piece pc;
+  pc.first(b0, c0);
+  if (pc.next(a, c1)) {
+    int last = pc.b;  // the last sequence that begins in the chunk, or the last with a histogram
+    while (last + 1 < a.B && last - pc.b < kBalWarps && seq_begin(a, last + 1) < c1) ++last;
+    const int pairs = (c1 - c0) * K;
+    const int32_t* ids = a.topk_ids + static_cast<long long>(c0) * K;
+    int* cnt = w.cnt + static_cast<long long>(pc.b) * E;
+    int b = pc.b;
+    for (int i0 = tid; i0 < pairs; i0 += 4 * kBalThreads) {
+      int id[4], tok[4];
+      bool on[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int i = i0 + k * kBalThreads;
+        tok[k] = static_cast<int>(static_cast<unsigned>(i) / static_cast<unsigned>(K));
+        on[k] = i < pairs && (!a.mask || __ldg(a.mask + c0 + tok[k]));
+        id[k] = i < pairs ? __ldg(ids + i) : 0;
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (!on[k]) continue;
+        if (last > pc.b)
+          while (b + 1 < a.B && seq_begin(a, b + 1) <= c0 + tok[k]) ++b;
+        const int r = b - pc.b;
+        const bool token = i0 + k * kBalThreads == tok[k] * K;  // a token is counted at its first choice
+        if (id[k] < 0 || id[k] >= E) set_error(a.err, DERR_BAD_EXPERT);
+        else atomicAdd((r < kBalWarps ? hist : cnt) + r * E + id[k], 1);
+        if (token) atomicAdd(r < kBalWarps ? s_n + r : w.nvalid + b, 1);
+      }
+    }
+    __syncthreads();
+    const int rows = min(last - pc.b + 1, kBalWarps);
+    for (int i = tid; i < rows * E; i += kBalThreads)
+      if (hist[i]) atomicAdd(cnt + i, hist[i]);
+    if (tid < rows && s_n[tid]) atomicAdd(w.nvalid + pc.b + tid, s_n[tid]);
+  }
   const bool counted = barrier(1);  // where it gave up: run on, so that every copy is waited for
   // (2) the pass over the logits
+  // the counts of a piece's sequence are fetched while the piece before it is worked on (experts tid and tid + 512)
+  Piece pn;
+  int nb_next = 0, cnt_next[2] = {0, 0};
+  auto fetch = [&]() {
+    if (!pn.next(a, c1)) return;
+    nb_next = __ldcg(w.nvalid + pn.b);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int e = tid + k * kBalThreads;
+      if (e < E) cnt_next[k] = __ldcg(w.cnt + static_cast<long long>(pn.b) * E + e);
+    }
+  };
+  pn.first(b0, c0);
+  fetch();
   float2 nu = make_float2(0.0f, 0.0f);  // counted tokens, sequences with any
   if (a.B == 1) {
     nu.x = static_cast<float>(__ldcg(w.nvalid));
@@ -288,22 +301,8 @@ __global__ void __launch_bounds__(kBalThreads) balance_kernel(const BalanceArgs 
   const int sl = lane & (LPT - 1), sub = lane / LPT;
   auto expert = [&](int i) { return VEC ? 4 * (sl + LPT * (i / 4)) + i % 4 : sl + LPT * i; };  // of a lane's i-th logit
   int st = 0, ph = 0;
-  // the counts of a piece's sequence are fetched while the piece before it is worked on (experts tid and tid + 512)
-  Piece pn;
-  int nb_next = 0, cnt_next[2] = {0, 0};
-  auto fetch = [&]() {
-    if (!pn.next(a, c1)) return;
-    nb_next = __ldcg(w.nvalid + pn.b);
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int e = tid + k * kBalThreads;
-      if (e < E) cnt_next[k] = __ldcg(w.cnt + static_cast<long long>(pn.b) * E + e);
-    }
-  };
-  pn.first(b0, c0);
-  fetch();
   pc.first(b0, c0);
-  while (pc.next(a, c1)) {
+  for (int nth = 0; pc.next(a, c1); nth += Tiles<kTile>::count(pc)) {
     const int nb = nb_next;
     const float inv_kn = nb > 0 ? 1.0f / (static_cast<float>(K) * static_cast<float>(nb)) : 0.0f;
 #pragma unroll
@@ -325,8 +324,9 @@ __global__ void __launch_bounds__(kBalThreads) balance_kernel(const BalanceArgs 
     const float cb = nb > 0 ? a.balance_coef * scale / (nu.y * static_cast<float>(nb)) : 0.0f;
     // which of a tile's tokens count, looked up a tile ahead
     auto counts_here = [&](int t) { return lane < kTile && t + lane < pc.t1 && (!a.mask || a.mask[t + lane]); };
-    bool mine = counts_here(pc.t0 + warp * kTile);
-    for (int tb = pc.t0 + warp * kTile; tb < pc.t1; tb += kBalWarps * kTile) {
+    const int tb0 = Tiles<kTile>::first_of(pc, nth, warp);
+    bool mine = counts_here(tb0);
+    for (int tb = tb0; tb < pc.t1; tb += kBalWarps * kTile) {
       const float* src = ring + static_cast<size_t>(st) * kTile * E;
       const unsigned here = __ballot_sync(0xffffffffu, mine);
       mine = counts_here(tb + kBalWarps * kTile);
@@ -465,13 +465,21 @@ __global__ void __launch_bounds__(kBalThreads) balance_kernel(const BalanceArgs 
   if (!barrier(2) || !counted || s_abort) return;
   // (3) mean probabilities and counts, 32 experts of one sequence at a time: a block for such a unit, its warps sharing
   // the pieces, while there are no more units than blocks, else a warp
+  float2 l = make_float2(0.0f, 0.0f);
+  if (blockIdx.x == G - 1) {  // the last block also adds the losses' shares
+    for (int i = tid; i < G + a.B; i += kBalThreads) {
+      l.x += __ldcg(w.zpart + i);
+      l.y += __ldcg(w.bpart + i);
+    }
+  }
   const int et = (E + 31) / 32;
   const long long units = static_cast<long long>(a.B) * et;
   const bool shared = units <= G;
-  const long long u0 = shared ? blockIdx.x : static_cast<long long>(blockIdx.x) * kBalWarps + warp;
+  const long long u0 = shared ? blockIdx.x : blockIdx.x + static_cast<long long>(warp) * G;
   for (long long un = u0; un < units; un += shared ? G : static_cast<long long>(G) * kBalWarps) {
     const int b = static_cast<int>(un / et), e = static_cast<int>(un % et) * 32 + lane;
     const int o0 = seq_begin(a, b), o1 = seq_begin(a, b + 1);
+    const int n = __ldcg(w.nvalid + b), count = e < E ? __ldcg(w.cnt + static_cast<long long>(b) * E + e) : 0;
     float s = 0.0f;
     if (o1 > o0 && e < E) {
       const float* src = w.ppart + static_cast<long long>(b) * E + e;
@@ -493,18 +501,12 @@ __global__ void __launch_bounds__(kBalThreads) balance_kernel(const BalanceArgs 
       for (int i = 0; i < kBalWarps; ++i) s += s_tile[i][lane];
     }
     if ((!shared || warp == 0) && e < E) {
-      const int n = __ldcg(w.nvalid + b);
       a.probs[static_cast<long long>(b) * E + e] = n > 0 ? s / static_cast<float>(n) : 0.0f;
-      a.counts[static_cast<long long>(b) * E + e] = __ldcg(w.cnt + static_cast<long long>(b) * E + e);
+      a.counts[static_cast<long long>(b) * E + e] = count;
     }
     if (shared) __syncthreads();
   }
   if (blockIdx.x != G - 1) return;
-  float2 l = make_float2(0.0f, 0.0f);
-  for (int i = tid; i < G + a.B; i += kBalThreads) {
-    l.x += __ldcg(w.zpart + i);
-    l.y += __ldcg(w.bpart + i);
-  }
   l = block_sum2(l.x, l.y, s_red);
   if (tid == 0) {
     const float bl = nu.y > 0.0f ? l.y / nu.y : 0.0f, zl = nu.x > 0.0f ? l.x / nu.x : 0.0f;

@@ -44,20 +44,22 @@ __device__ __forceinline__ bool grid_barrier(int* counter, int target, unsigned 
   __syncthreads();
   if (threadIdx.x == 0) {
     int ok = 1;
-    __threadfence();
-    atomicAdd(counter, 1);
-    const uint64_t t0 = globaltimer_ns();
+    // release and acquire reach what the block's other threads wrote and will read through the block's barriers
+    asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(counter) : "memory");
+    uint64_t t0 = 0;
     for (uint32_t i = 0;; ++i) {
       int v;
       asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(counter) : "memory");
       if (v >= target) break;
-      if ((i & 15u) == 15u && globaltimer_ns() - t0 > timeout_ns) {
+      if ((i & 15u) != 15u) continue;
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > timeout_ns) {
         set_error(err, DERR_TIMEOUT);
         ok = 0;
         break;
       }
     }
-    __threadfence();
     *s_ok = ok;
   }
   __syncthreads();
