@@ -239,6 +239,35 @@ def test_norm_backward(vgg, ctx, T, d, pad, shift, res_t, up):
     assert torch.equal(dy, dx) and torch.equal(dw2, dw)
 
 
+def far_rows(T, d, ld, dtype, gen):
+    """[T, d] with a row stride of ld elements, the last rows past 2^31 elements from the first."""
+    flat = torch.empty(((T - 1) * ld + d,), dtype=dtype, device="cuda")
+    assert (T - 1) * ld >= 1 << 31
+    t = flat.as_strided((T, d), (ld, 1))
+    if gen is not None:
+        t.copy_(torch.randn((T, d), device="cuda", generator=gen))
+    return t
+
+
+@pytest.mark.parametrize("T,d,ld", [(3, 64, 1 << 30), (5, 33, (1 << 29) + 1), (608, 4160, (1 << 22) - 8), (2, 8200, 1 << 31)])
+def test_norm_offsets_past_32_bits(vgg, ctx, T, d, ld):
+    """Each of the forward's and the backward's kernels; outputs are written with the same strides."""
+    g = gen_of(T + d)
+    w = 1 + 0.1 * torch.randn(d, device="cuda", generator=g)
+    x, r = far_rows(T, d, ld, BF, g), far_rows(T, d, ld, BF, g)
+    y, rstd = far_rows(T, d, ld, BF, None), torch.empty(T, device="cuda")
+    r0 = r.contiguous()
+    vgg.moe_add_rmsnorm(ctx, x, r, w, 1e-6, r, y, rstd)
+    check_norm(x, r0, w, 1e-6, r, y, rstd)
+    # the same rows side by side run on the same kernel and give the same bits
+    dx, dw = far_rows(T, d, ld, BF, None), torch.empty(d, device="cuda")
+    ws = torch.empty(vgg.moe_add_rmsnorm_workspace_bytes(T, d), dtype=U8, device="cuda")
+    vgg.moe_add_rmsnorm_backward(ctx, y, r, w, rstd, x, dx, None, dw, ws)
+    dx2, dw2 = torch.empty((T, d), dtype=BF, device="cuda"), torch.empty(d, device="cuda")
+    vgg.moe_add_rmsnorm_backward(ctx, y.contiguous(), r.contiguous(), w, rstd, x.contiguous(), dx2, None, dw2, ws)
+    assert torch.equal(dx, dx2) and torch.equal(dw, dw2)
+
+
 # ------------------------------------------------------------------------------------------------ balance loss
 
 
@@ -337,6 +366,35 @@ def test_balance_many_sequences_in_a_block(vgg, ctx, T, E, K, B):
     off = [0] + sorted(np.random.default_rng(B).integers(0, T + 1, B - 1).tolist()) + [T]
     mask = torch.rand(T, device="cuda", generator=g) < 0.7
     check_balance(run_balance(vgg, ctx, logits, ids, 0.3, 0.02, mask, off), logits, ids, 0.3, 0.02, mask, off)
+
+
+def test_balance_offsets_past_32_bits(vgg, ctx):
+    """More than 2^31 logits: counts, mean probabilities and the gradient at both ends and around 2^31."""
+    T, E = (1 << 21) + 77, 1024
+    logits = torch.empty((T, E), device="cuda")
+    step = 1 << 16
+    for t in range(0, T, step):
+        logits[t:t + step] = torch.randn((min(step, T - t), E), device="cuda", generator=gen_of(t))
+    ids = torch.randint(0, E, (T, 1), device="cuda", generator=gen_of(1)).to(I32)
+    loss, counts, probs, dl = run_balance(vgg, ctx, logits, ids, 1.0, 0.0)
+    want = torch.bincount(ids.view(-1), minlength=E)
+    assert torch.equal(counts.view(-1).long(), want)
+    total = torch.zeros(E, dtype=torch.float64, device="cuda")
+    for t in range(0, T, step):
+        total += torch.softmax(logits[t:t + step].double(), dim=1).sum(0)
+    p = total / T
+    # a probability's own error (see check_balance, spans below 14), then a warp's chain of T / (152 * 16) tokens at
+    # least a lane, 16 warps and 152 blocks
+    rel = (14 + 4 + 37 + 2 + 863 + 16 + 152 + 8) * U
+    assert bool(((probs.view(-1).double() - p).abs() <= rel * p).all())
+    f = want.double() * E / T
+    assert abs(float(loss[1]) - float((f * p).sum())) <= 2 * rel * float((f * p).sum())
+    u = f - 1.0
+    for t in (0, (1 << 21) - 40, T - 80):
+        q = torch.softmax(logits[t:t + 80].double(), dim=1)
+        ref = q * (u - (q * u).sum(1, keepdim=True)) / T
+        terms = q * (u.abs() + (q * u.abs()).sum(1, keepdim=True)) / T
+        assert bool(((dl[t:t + 80].double() - ref).abs() <= (2 * 57 + 45) * U * terms).all())
 
 
 def test_balance_masked_logits(vgg, ctx):
@@ -479,6 +537,35 @@ def test_router_backward(vgg, ctx, T, d, E, add):
         assert torch.equal(a, dX) and torch.equal(b, dW)
     assert torch.equal(run_router(vgg, ctx, dl, X, W, dX_in, dW_in, (True, False))[0], dX)
     assert torch.equal(run_router(vgg, ctx, dl, X, W, dX_in, dW_in, (False, True))[1], dW)
+
+
+@pytest.mark.parametrize("T,d,E", [(500, 64, 8), (4096, 256, 128), (20000, 128, 264)])
+def test_router_weight_gradient_has_fp32_precision(vgg, ctx, T, d, E):
+    """An element: three bf16 parts leave 2^-24 of a value, an accumulator's 24 additions a step (2^-23) each, the sums
+    over T / 128 accumulators and up to 16 splits half a step each.  In the norm an fp32 product is off by about 2^-21
+    and two parts by 2^-18.7: 2^-20 lies between."""
+    g = gen_of(T)
+    dl = torch.randn((T, E), device="cuda", generator=g)
+    X = torch.randn((T, d), device="cuda", generator=g).to(BF)
+    dW = run_router(vgg, ctx, dl, X, torch.zeros((d, E), dtype=BF, device="cuda"), None, None, (False, True))[1]
+    ref, mag = X.double().T @ dl.double(), X.double().abs().T @ dl.double().abs()
+    err = (dW.double() - ref).abs()
+    assert bool((err <= (1 + 48 + T / 128 + 16 + 2) * U * mag).all())
+    assert float(torch.linalg.norm(err)) <= 2.0 ** -20 * float(torch.linalg.norm(ref))
+
+
+def test_router_backward_offsets_past_32_bits(vgg, ctx):
+    """More than 2^31 elements of X and dX; whole numbers, so both products are exact."""
+    T, d, E = 65536, 32832, 8
+    g = gen_of(5)
+    X = torch.randint(-1, 2, (T, d), device="cuda", generator=g, dtype=torch.int8).to(BF)
+    dl = torch.randint(-1, 2, (T, E), device="cuda", generator=g).float()
+    W = torch.randint(-1, 2, (d, E), device="cuda", generator=g).to(BF)
+    dX, dW = run_router(vgg, ctx, dl, X, W, None, None)
+    for t in (0, 32768, T - 64):
+        assert torch.equal(dX[t:t + 64].double(), dl[t:t + 64].double() @ W.double().T)
+    for i in (0, 16384, d - 64):
+        assert torch.equal(dW[i:i + 64].double(), X[:, i:i + 64].double().T @ dl.double())
 
 
 def test_router_backward_of_no_tokens(vgg, ctx):
