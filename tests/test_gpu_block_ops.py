@@ -239,6 +239,48 @@ def test_norm_backward(vgg, ctx, T, d, pad, shift, res_t, up):
     assert torch.equal(dy, dx) and torch.equal(dw2, dw)
 
 
+@pytest.mark.parametrize("res_t", [BF, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("T,d,pad", [(1, 1, 0), (9, 33, 0), (40, 250, 3), (3000, 57, 0), (5000, 130, 3), (700, 515, 0),
+                                     (1300, 1001, 3), (2500, 4091, 0), (333, 8178, 1), (20, 8179, 0)])
+@pytest.mark.parametrize("apart", [0, 1], ids=["in_phase", "out_of_phase"])
+def test_norm_rows_that_start_anywhere(vgg, ctx, T, d, pad, res_t, apart):
+    """Rows of odd widths and strides, all tensors starting a row at the same place in 16 bytes, or one of them not;
+    what lies between and around the rows stays as it was."""
+    g = gen_of(T + d + pad)
+    x, r = rows(T, d, BF, g, pad, 3), rows(T, d, res_t, g, pad, 3 + apart, 2.0)
+    w = (1 + 0.1 * torch.randn(d, device="cuda", generator=g)).to(BF if pad else F32)
+
+    def out(dtype, shift=3):
+        flat = torch.full((T * (d + pad) + 16,), 777.0, dtype=dtype, device="cuda")
+        return flat, flat[shift:shift + T * (d + pad)].view(T, d + pad)[:, :d]
+
+    def untouched(flat, shift=3):
+        keep = flat.clone()
+        keep[shift:shift + T * (d + pad)].view(T, d + pad)[:, :d] = 777.0
+        return bool((keep == 777.0).all())
+
+    (fh, h), (fy, y), rstd = out(res_t), out(BF), torch.empty(T, device="cuda")
+    vgg.moe_add_rmsnorm(ctx, x, r, w, 1e-6, h, y, rstd)
+    check_norm(x, r, w, 1e-6, h, y, rstd)
+    assert untouched(fh) and untouched(fy)
+    dy, dh = rows(T, d, BF, g, pad, 3), rows(T, d, res_t, g, pad, 3 + apart)
+    (fx, dx), (fr, dr), dw = out(BF), out(res_t), torch.empty(d, device="cuda")
+    ws = torch.empty(vgg.moe_add_rmsnorm_workspace_bytes(T, d), dtype=U8, device="cuda")
+    vgg.moe_add_rmsnorm_backward(ctx, dy, h, w, rstd, dh, dx, dr, dw, ws)
+    gh, gw = bo.rmsnorm_backward(f64(dy), f64(h), f64(w), f64(rstd), f64(dh))
+    xh, gd = f64(h) * f64(rstd)[:, None], f64(dy) * f64(w)
+    # as in test_norm_backward; dweight: at most 33 rows a group, 8 groups, then 1024 / 32 blocks a thread and a tree of 5
+    terms = np.abs(gd) + np.abs(xh) * np.mean(np.abs(gd * xh), axis=1, keepdims=True)
+    err = 52 * U * f64(rstd)[:, None] * terms + 2 * U * np.abs(gh)
+    assert np.all(np.abs(f64(dx) - gh) <= err + 2.0 ** -8 * (np.abs(gh) + err))
+    assert np.all(np.abs(f64(dr) - gh) <= err + (2.0 ** -8 * (np.abs(gh) + err) if res_t == BF else 0))
+    assert np.all(np.abs(f64(dw) - gw) <= (33 + 8 + 32 + 5 + 3) * U * np.sum(np.abs(f64(dy) * xh), axis=0))
+    assert untouched(fx) and untouched(fr)
+    again = torch.empty_like(dw)
+    vgg.moe_add_rmsnorm_backward(ctx, dy, h, w, rstd, dh, dy, None, again, ws)
+    assert torch.equal(dy, dx) and torch.equal(again, dw)
+
+
 def far_rows(T, d, ld, dtype, gen):
     """[T, d] with a row stride of ld elements, the last rows past 2^31 elements from the first."""
     flat = torch.empty(((T - 1) * ld + d,), dtype=dtype, device="cuda")

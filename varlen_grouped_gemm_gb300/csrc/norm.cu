@@ -354,6 +354,115 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_any_kernel(const NormFwd a) 
   }
 }
 
+// ---- rows that start anywhere
+//
+// Where the tensors of a call begin every row at the same element mod 8 (its phase: addresses and strides alike), the
+// row's vectors begin at columns 8 j - phase and are aligned in all of them; a part of a vector is left at either end.
+// A row group takes rows whose numbers differ by multiples of eight, so that its phase, and with it every thread's
+// columns, stay the same: the weight's vector is read once, and the backward's share of dg stays in registers.
+struct Phase {
+  int first, step;  // of row 0, and from one row to the next
+  __device__ int of(long long t) const { return (first + static_cast<int>(t & 7) * step) & 7; }
+};
+inline Phase phase_of(const void* p, long long ld) {  // of a bf16 tensor
+  return {static_cast<int>(reinterpret_cast<uintptr_t>(p) / 2 & 7), static_cast<int>(ld & 7)};
+}
+// Whether a tensor (null: none) has that phase; four fp32 values fill 16 bytes.
+inline bool in_phase(const Phase& f, const void* p, long long ld, bool f32) {
+  const long long m = f32 ? 3 : 7, at = static_cast<long long>(reinterpret_cast<uintptr_t>(p) / (f32 ? 4 : 2));
+  return !p || (((at - f.first) & m) == 0 && ((ld - f.step) & m) == 0);
+}
+constexpr int kPhaseCols = 8178;  // a vector a thread, 1024 of them with the parts at both ends
+
+// The vector at columns c .. c + 7 of the row that begins at element off; columns outside [0, d) are 0, or not stored.
+template <bool F32>
+__device__ __forceinline__ Vec8 load_cols(const void* base, long long off, int c, int d) {
+  if (c >= 0 && c + 8 <= d) return load8<F32>(base, off + c);
+  float f[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) f[k] = c + k >= 0 && c + k < d ? load1<F32>(base, off + c + k) : 0.0f;
+  return from_f32(make_float4(f[0], f[1], f[2], f[3]), make_float4(f[4], f[5], f[6], f[7]));
+}
+template <bool F32>
+__device__ __forceinline__ void store_cols(void* base, long long off, int c, int d, const Vec8& v) {
+  if (c >= 0 && c + 8 <= d) return store8<F32>(base, off + c, v);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const float2 p = unpack2(v.p[k / 2]);
+    if (c + k >= 0 && c + k < d) store1<F32>(base, off + c + k, k % 2 ? p.y : p.x);
+  }
+}
+__device__ __forceinline__ Vec8 weight_cols(const void* w, int f32, int c, int d) {
+  float f[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) f[k] = c + k >= 0 && c + k < d ? load_weight1(w, f32, c + k) : 0.0f;
+  return from_f32(make_float4(f[0], f[1], f[2], f[3]), make_float4(f[4], f[5], f[6], f[7]));
+}
+
+// Sum over the blockDim.x threads of a row group, which has a barrier of its own; red: 32 floats a group, another set
+// for every other row.
+__device__ __forceinline__ float group_sum(float v, float* red) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  const int nw = blockDim.x >> 5, lane = threadIdx.x & 31;
+  if (nw == 1) return v;
+  if (lane == 0) red[threadIdx.x >> 5] = v;
+  asm volatile("bar.sync %0, %1;" ::"r"(static_cast<int>(threadIdx.y) + 1), "r"(static_cast<int>(blockDim.x)) : "memory");
+  v = lane < nw ? red[lane] : 0.0f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Launch shape: row groups of tpr threads, up to 512 threads a block, `threads` on an SM.
+struct PhaseShape {
+  int tpr, rows, grid;
+};
+inline PhaseShape phase_shape(long long T, int d, int threads, int num_sms) {
+  PhaseShape r;
+  r.tpr = ((d + 14) / 8 + 31) & ~31;
+  r.rows = r.tpr >= 512 ? 1 : 512 / r.tpr < 8 ? 512 / r.tpr : 8;
+  const long long want = (T + r.rows - 1) / r.rows;
+  const int most = (num_sms * (threads / (r.tpr * r.rows)) + 7) & ~7;  // a multiple of eight rows from one to the next
+  r.grid = static_cast<int>(want < most ? want : most);
+  return r;
+}
+
+template <bool RES32>
+__global__ void __launch_bounds__(1024) add_rmsnorm_phase_kernel(const NormFwd a, Phase f) {
+  __shared__ float red[2][8][32];
+  const long long t0 = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
+  const long long step = static_cast<long long>(gridDim.x) * blockDim.y;
+  if (t0 >= a.T) return;
+  const int c = 8 * static_cast<int>(threadIdx.x) - f.of(t0), d = a.d;
+  const bool on = c < d;
+  const Vec8 g = weight_cols(a.weight, a.weight_f32, c, d);
+  const float inv_d = 1.0f / static_cast<float>(d);
+  int it = 0;
+  for (long long t = t0; t < a.T; t += step, ++it) {
+    Vec8 h = zero8();
+    if (on) {
+      h = load_cols<RES32>(a.res, t * a.ld_res, c, d);
+      if (a.x) {
+        const Vec8 x = load_cols<false>(a.x, t * a.ld_x, c, d);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) h.p[k] = add2(h.p[k], x.p[k]);
+        if (!RES32) h = from_bf16(to_bf16(h));  // the norm's input is the stream as it is stored
+      }
+      if (a.h) store_cols<RES32>(a.h, t * a.ld_h, c, d, h);
+    }
+    const float2 sq = unpack2(squares(h, pack2(0.0f, 0.0f)));
+    const float rstd = inv_root(fmaf(group_sum(sq.x + sq.y, red[it & 1][threadIdx.y]), inv_d, a.eps));
+    if (a.rstd && threadIdx.x == 0) a.rstd[t] = rstd;
+    if (on) {
+      const f32x2 r2 = pack2(rstd, rstd);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) h.p[k] = mul2(mul2(h.p[k], r2), g.p[k]);
+      store_cols<false>(a.y, t * a.ld_y, c, d, h);
+    }
+  }
+}
+
 // ---- rows through a ring of bulk copies
 //
 // Each of the RG = blockDim.y row groups of a persistent block has a ring of `stages` rows in shared memory, filled ahead
@@ -571,6 +680,14 @@ cudaError_t launch_add_rmsnorm(const NormFwd& a, bool vec, int num_sms, cudaStre
     return a.res_f32 ? run_norm_ring_form<true>(a, r, s) : run_norm_ring_form<false>(a, r, s);
   }
   if (!vec) {
+    const Phase f = phase_of(a.y, a.ld_y);
+    if (a.d <= kPhaseCols && in_phase(f, a.res, a.ld_res, a.res_f32) && in_phase(f, a.x, a.ld_x, false) &&
+        in_phase(f, a.h, a.ld_h, a.res_f32)) {
+      const PhaseShape p = phase_shape(a.T, a.d, 2048, num_sms);
+      if (a.res_f32) add_rmsnorm_phase_kernel<true><<<p.grid, dim3(p.tpr, p.rows), 0, s>>>(a, f);
+      else add_rmsnorm_phase_kernel<false><<<p.grid, dim3(p.tpr, p.rows), 0, s>>>(a, f);
+      return cudaGetLastError();
+    }
     const int tpr = round32((a.d + 15) / 16);
     if (a.res_f32) add_rmsnorm_any_kernel<true><<<static_cast<unsigned>(a.T), tpr, 0, s>>>(a);
     else add_rmsnorm_any_kernel<false><<<static_cast<unsigned>(a.T), tpr, 0, s>>>(a);
@@ -702,6 +819,57 @@ __global__ void __launch_bounds__(512) add_rmsnorm_bwd_any_kernel(const NormBwd 
   for (int i = 0; i < N; ++i) {
     const int j = threadIdx.x + blockDim.x * i;
     if (j < a.d) out[j] = dg[i];
+  }
+}
+
+// Rows that start anywhere, the tensors in phase (see the forward).
+template <bool RES32>
+__global__ void __launch_bounds__(1024) add_rmsnorm_bwd_phase_kernel(const NormBwd a, Phase f) {
+  extern __shared__ __align__(16) float shares[];
+  __shared__ float red[2][8][32];
+  griddep_launch();
+  const long long t0 = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
+  const long long step = static_cast<long long>(gridDim.x) * blockDim.y;
+  const int c = 8 * static_cast<int>(threadIdx.x) - f.of(t0), d = a.d;
+  const bool on = c < d;
+  const Vec8 g = weight_cols(a.weight, a.weight_f32, c, d);
+  const float inv_d = 1.0f / static_cast<float>(d);
+  Vec8 dg = zero8();
+  int it = 0;
+  for (long long t = t0; t < a.T; t += step, ++it) {
+    const float rstd = __ldg(a.rstd + t);
+    const f32x2 rstd2 = pack2(rstd, rstd);
+    Vec8 dy = zero8(), h = zero8(), o = zero8();
+    if (on) {
+      dy = load_cols<false>(a.dy, t * a.ld_dy, c, d);
+      h = load_cols<RES32>(a.h, t * a.ld_h, c, d);
+      if (a.dh) o = load_cols<RES32>(a.dh, t * a.ld_dh, c, d);
+    }
+    f32x2 c2 = pack2(0.0f, 0.0f);
+    bwd8(dy, h, g, dg, rstd2, c2);
+    const float2 cf = unpack2(c2);
+    const float m = group_sum(cf.x + cf.y, red[it & 1][threadIdx.y]) * inv_d;
+    if (!on) continue;
+    const f32x2 nc2 = pack2(-rstd * m, -rstd * m);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o.p[k] = fma2(nc2, h.p[k], fma2(rstd2, dy.p[k], o.p[k]));
+    if (a.dx) store_cols<false>(a.dx, t * a.ld_dx, c, d, o);
+    if (a.dres) store_cols<RES32>(a.dres, t * a.ld_dres, c, d, o);
+  }
+  // the groups' shares, each in its own phase, added in group order
+  float* out = gridDim.x == 1 ? a.dweight : a.part + static_cast<long long>(blockIdx.x) * d;
+  float* mine = blockDim.y > 1 ? shares + threadIdx.y * d : out;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const float2 p = unpack2(dg.p[k / 2]);
+    if (c + k >= 0 && c + k < d) mine[c + k] = k % 2 ? p.y : p.x;
+  }
+  if (blockDim.y == 1) return;
+  __syncthreads();
+  for (int j = threadIdx.y * blockDim.x + threadIdx.x; j < d; j += blockDim.x * blockDim.y) {
+    float v = 0.0f;
+    for (int r = 0; r < static_cast<int>(blockDim.y); ++r) v += shares[r * d + j];
+    out[j] = v;
   }
 }
 
@@ -845,6 +1013,15 @@ cudaError_t launch_add_rmsnorm_bwd(const NormBwd& a, bool vec, int num_sms, cuda
     parts = r.grid;
     if (one) e = a.res_f32 ? run_norm_bwd_ring<1, true>(a, r, s) : run_norm_bwd_ring<1, false>(a, r, s);
     else e = a.res_f32 ? run_norm_bwd_ring<2, true>(a, r, s) : run_norm_bwd_ring<2, false>(a, r, s);
+  } else if (const Phase f = phase_of(a.dy, a.ld_dy);
+             !vec && a.d <= kPhaseCols && in_phase(f, a.h, a.ld_h, a.res_f32) && in_phase(f, a.dh, a.ld_dh, a.res_f32) &&
+             in_phase(f, a.dx, a.ld_dx, false) && in_phase(f, a.dres, a.ld_dres, a.res_f32)) {
+    const PhaseShape p = phase_shape(a.T, a.d, 1024, num_sms < 256 ? num_sms : 256);
+    parts = p.grid;
+    const size_t smem = p.rows > 1 ? sizeof(float) * p.rows * a.d : 0;
+    if (a.res_f32) add_rmsnorm_bwd_phase_kernel<true><<<p.grid, dim3(p.tpr, p.rows), smem, s>>>(a, f);
+    else add_rmsnorm_bwd_phase_kernel<false><<<p.grid, dim3(p.tpr, p.rows), smem, s>>>(a, f);
+    e = cudaGetLastError();
   } else {
     const long long most = 4ll * num_sms < kMaxNormParts ? 4ll * num_sms : kMaxNormParts;
     parts = static_cast<int>(a.T < most ? a.T : most);
