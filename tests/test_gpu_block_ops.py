@@ -241,7 +241,8 @@ def test_norm_backward(vgg, ctx, T, d, pad, shift, res_t, up):
 
 @pytest.mark.parametrize("res_t", [BF, F32], ids=["bf16", "fp32"])
 @pytest.mark.parametrize("T,d,pad", [(1, 1, 0), (9, 33, 0), (40, 250, 3), (3000, 57, 0), (5000, 130, 3), (700, 515, 0),
-                                     (1300, 1001, 3), (2500, 4091, 0), (333, 8178, 1), (20, 8179, 0)])
+                                     (1300, 1001, 3), (2500, 4091, 0), (333, 8178, 1), (20, 8179, 0),
+                                     (170, 8094, 3), (200, 8143, 1), (160, 8102, 0), (2000, 7, 0), (1700, 8, 1)])
 @pytest.mark.parametrize("apart", [0, 1], ids=["in_phase", "out_of_phase"])
 def test_norm_rows_that_start_anywhere(vgg, ctx, T, d, pad, res_t, apart):
     """Rows of odd widths and strides, all tensors starting a row at the same place in 16 bytes, or one of them not;

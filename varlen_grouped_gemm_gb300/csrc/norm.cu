@@ -359,7 +359,10 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_any_kernel(const NormFwd a) 
 // Where the tensors of a call begin every row at the same element mod 8 (its phase: addresses and strides alike), the
 // row's vectors begin at columns 8 j - phase and are aligned in all of them; a part of a vector is left at either end.
 // A row group takes rows whose numbers differ by multiples of eight, so that its phase, and with it every thread's
-// columns, stay the same: the weight's vector is read once, and the backward's share of dg stays in registers.
+// columns, stay the same: the weight's vector is read once, and the backward's share of dg stays in registers.  The next
+// row's loads are on their way while a row is reduced.
+// Against the kernels for any alignment, a value a load: 8192 x 4001 bf16 forward 47 us and 161 (196 MB, 39 us of them),
+// backward 69 and 495; 16384 x 999 24 and 72, 41 and 740; 300 x 1501 3.0 and 8.2, 7.2 and 17.6.
 struct Phase {
   int first, step;  // of row 0, and from one row to the next
   __device__ int of(long long t) const { return (first + static_cast<int>(t & 7) * step) & 7; }
@@ -372,30 +375,53 @@ inline bool in_phase(const Phase& f, const void* p, long long ld, bool f32) {
   const long long m = f32 ? 3 : 7, at = static_cast<long long>(reinterpret_cast<uintptr_t>(p) / (f32 ? 4 : 2));
   return !p || (((at - f.first) & m) == 0 && ((ld - f.step) & m) == 0);
 }
-constexpr int kPhaseCols = 8178;  // a vector a thread, 1024 of them with the parts at both ends
+// Threads of a row: the fewest vectors that a phase leaves, and a thread for every column outside them.
+inline int phase_threads(int d) { return d < 8 ? d : d - 7 * ((d - 7) / 8); }
 
-// The vector at columns c .. c + 7 of the row that begins at element off; columns outside [0, d) are 0, or not stored.
-template <bool F32>
-__device__ __forceinline__ Vec8 load_cols(const void* base, long long off, int c, int d) {
-  if (c >= 0 && c + 8 <= d) return load8<F32>(base, off + c);
-  float f[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) f[k] = c + k >= 0 && c + k < d ? load1<F32>(base, off + c + k) : 0.0f;
-  return from_f32(make_float4(f[0], f[1], f[2], f[3]), make_float4(f[4], f[5], f[6], f[7]));
-}
-template <bool F32>
-__device__ __forceinline__ void store_cols(void* base, long long off, int c, int d, const Vec8& v) {
-  if (c >= 0 && c + 8 <= d) return store8<F32>(base, off + c, v);
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const float2 p = unpack2(v.p[k / 2]);
-    if (c + k >= 0 && c + k < d) store1<F32>(base, off + c + k, k % 2 ? p.y : p.x);
+// What a thread has of such a row: columns c .. c + n - 1, a vector (n = 8) or one of the up to 14 columns at the ends
+// (n = 1; as the first value of a vector of zeros), or nothing.  A thread with a part of a vector instead takes eight
+// turns at loading and storing, and the row waits for it (8192 x 2049 bf16: forward 53 us against 34).
+struct Cols {
+  int c, n;
+  __device__ Cols(int phase, int d, int i) {
+    const int head = min(d, (8 - phase) & 7), full = (d - head) / 8, tail = d - head - 8 * full, e = i - full;
+    n = e < 0 ? 8 : e < head + tail ? 1 : 0;
+    c = e < 0 ? head + 8 * i : e < head ? e : 8 * full + e;
   }
+};
+struct Pair4 {
+  float4 a, b;
+};
+// As loaded, so that nothing waits for the load before the values are used.
+template <bool F32>
+using Cols8 = std::conditional_t<F32, Pair4, uint4>;
+template <bool F32>
+__device__ __forceinline__ Cols8<F32> load_cols(const void* base, long long off, const Cols& w) {
+  Cols8<F32> v{};
+  if constexpr (F32) {
+    const float* p = static_cast<const float*>(base) + off + w.c;
+    if (w.n == 8) {
+      v.a = __ldcs(reinterpret_cast<const float4*>(p));
+      v.b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+    } else if (w.n) {
+      v.a.x = *p;
+    }
+  } else {
+    if (w.n == 8) v = ldcs4(base, off + w.c);
+    else if (w.n) v.x = static_cast<const uint16_t*>(base)[off + w.c];
+  }
+  return v;
 }
-__device__ __forceinline__ Vec8 weight_cols(const void* w, int f32, int c, int d) {
+__device__ __forceinline__ Vec8 values(const Pair4& r) { return from_f32(r.a, r.b); }
+template <bool F32>
+__device__ __forceinline__ void store_cols(void* base, long long off, const Cols& w, const Vec8& v) {
+  if (w.n == 8) store8<F32>(base, off + w.c, v);
+  else if (w.n) store1<F32>(base, off + w.c, unpack2(v.p[0]).x);
+}
+__device__ __forceinline__ Vec8 weight_cols(const void* w, int f32, const Cols& l) {
   float f[8];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) f[k] = c + k >= 0 && c + k < d ? load_weight1(w, f32, c + k) : 0.0f;
+  for (int k = 0; k < 8; ++k) f[k] = k < l.n ? load_weight1(w, f32, l.c + k) : 0.0f;
   return from_f32(make_float4(f[0], f[1], f[2], f[3]), make_float4(f[4], f[5], f[6], f[7]));
 }
 
@@ -420,7 +446,7 @@ struct PhaseShape {
 };
 inline PhaseShape phase_shape(long long T, int d, int threads, int num_sms) {
   PhaseShape r;
-  r.tpr = ((d + 14) / 8 + 31) & ~31;
+  r.tpr = (phase_threads(d) + 31) & ~31;
   r.rows = r.tpr >= 512 ? 1 : 512 / r.tpr < 8 ? 512 / r.tpr : 8;
   const long long want = (T + r.rows - 1) / r.rows;
   const int most = (num_sms * (threads / (r.tpr * r.rows)) + 7) & ~7;  // a multiple of eight rows from one to the next
@@ -434,32 +460,32 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_phase_kernel(const NormFwd a
   const long long t0 = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
   const long long step = static_cast<long long>(gridDim.x) * blockDim.y;
   if (t0 >= a.T) return;
-  const int c = 8 * static_cast<int>(threadIdx.x) - f.of(t0), d = a.d;
-  const bool on = c < d;
-  const Vec8 g = weight_cols(a.weight, a.weight_f32, c, d);
+  const int d = a.d;
+  const Cols w(f.of(t0), d, threadIdx.x);
+  const Vec8 g = weight_cols(a.weight, a.weight_f32, w);
   const float inv_d = 1.0f / static_cast<float>(d);
+  Cols8<RES32> res{};
+  uint4 x{};
+  auto fetch = [&](long long t) {  // a row ahead
+    if (t >= a.T) return;
+    res = load_cols<RES32>(a.res, t * a.ld_res, w);
+    if (a.x) x = load_cols<false>(a.x, t * a.ld_x, w);
+  };
+  fetch(t0);
   int it = 0;
   for (long long t = t0; t < a.T; t += step, ++it) {
-    Vec8 h = zero8();
-    if (on) {
-      h = load_cols<RES32>(a.res, t * a.ld_res, c, d);
-      if (a.x) {
-        const Vec8 x = load_cols<false>(a.x, t * a.ld_x, c, d);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) h.p[k] = add2(h.p[k], x.p[k]);
-        if (!RES32) h = from_bf16(to_bf16(h));  // the norm's input is the stream as it is stored
-      }
-      if (a.h) store_cols<RES32>(a.h, t * a.ld_h, c, d, h);
-    }
+    Vec8 h;
+    if constexpr (RES32) h = a.x ? add_x(values(res), x) : values(res);
+    else h = values(a.x ? add_x(res, x) : res);
+    if (a.h) store_cols<RES32>(a.h, t * a.ld_h, w, h);
+    fetch(t + step);
     const float2 sq = unpack2(squares(h, pack2(0.0f, 0.0f)));
     const float rstd = inv_root(fmaf(group_sum(sq.x + sq.y, red[it & 1][threadIdx.y]), inv_d, a.eps));
     if (a.rstd && threadIdx.x == 0) a.rstd[t] = rstd;
-    if (on) {
-      const f32x2 r2 = pack2(rstd, rstd);
+    const f32x2 r2 = pack2(rstd, rstd);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) h.p[k] = mul2(mul2(h.p[k], r2), g.p[k]);
-      store_cols<false>(a.y, t * a.ld_y, c, d, h);
-    }
+    for (int k = 0; k < 4; ++k) h.p[k] = mul2(mul2(h.p[k], r2), g.p[k]);
+    store_cols<false>(a.y, t * a.ld_y, w, h);
   }
 }
 
@@ -681,7 +707,7 @@ cudaError_t launch_add_rmsnorm(const NormFwd& a, bool vec, int num_sms, cudaStre
   }
   if (!vec) {
     const Phase f = phase_of(a.y, a.ld_y);
-    if (a.d <= kPhaseCols && in_phase(f, a.res, a.ld_res, a.res_f32) && in_phase(f, a.x, a.ld_x, false) &&
+    if (phase_threads(a.d) <= 1024 && in_phase(f, a.res, a.ld_res, a.res_f32) && in_phase(f, a.x, a.ld_x, false) &&
         in_phase(f, a.h, a.ld_h, a.res_f32)) {
       const PhaseShape p = phase_shape(a.T, a.d, 2048, num_sms);
       if (a.res_f32) add_rmsnorm_phase_kernel<true><<<p.grid, dim3(p.tpr, p.rows), 0, s>>>(a, f);
@@ -825,48 +851,63 @@ __global__ void __launch_bounds__(512) add_rmsnorm_bwd_any_kernel(const NormBwd 
 // Rows that start anywhere, the tensors in phase (see the forward).
 template <bool RES32>
 __global__ void __launch_bounds__(1024) add_rmsnorm_bwd_phase_kernel(const NormBwd a, Phase f) {
-  extern __shared__ __align__(16) float shares[];
+  extern __shared__ __align__(16) float4 weights[];  // every thread's, which registers have no room for; then the shares
   __shared__ float red[2][8][32];
   griddep_launch();
   const long long t0 = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
   const long long step = static_cast<long long>(gridDim.x) * blockDim.y;
-  const int c = 8 * static_cast<int>(threadIdx.x) - f.of(t0), d = a.d;
-  const bool on = c < d;
-  const Vec8 g = weight_cols(a.weight, a.weight_f32, c, d);
+  const int d = a.d;
+  const Cols w(f.of(t0), d, threadIdx.x);
+  const int threads = blockDim.x * blockDim.y, me = threadIdx.y * blockDim.x + threadIdx.x;
+  {
+    const Vec8 g = weight_cols(a.weight, a.weight_f32, w);
+    const float2 p0 = unpack2(g.p[0]), p1 = unpack2(g.p[1]), p2 = unpack2(g.p[2]), p3 = unpack2(g.p[3]);
+    weights[me] = make_float4(p0.x, p0.y, p1.x, p1.y);
+    weights[threads + me] = make_float4(p2.x, p2.y, p3.x, p3.y);
+  }
   const float inv_d = 1.0f / static_cast<float>(d);
   Vec8 dg = zero8();
+  uint4 dy_in{};
+  Cols8<RES32> h_in{}, dh_in{};
+  float rstd_in = 0.0f;
+  constexpr bool kAhead = !RES32;
+  auto fetch = [&](long long t) {  // a row ahead where the registers suffice (1024 threads of 64)
+    if (t >= a.T) return;
+    rstd_in = __ldg(a.rstd + t);
+    dy_in = load_cols<false>(a.dy, t * a.ld_dy, w);
+    h_in = load_cols<RES32>(a.h, t * a.ld_h, w);
+    if (a.dh) dh_in = load_cols<RES32>(a.dh, t * a.ld_dh, w);
+  };
+  if (kAhead) fetch(t0);
   int it = 0;
   for (long long t = t0; t < a.T; t += step, ++it) {
-    const float rstd = __ldg(a.rstd + t);
+    if (!kAhead) fetch(t);
+    const float rstd = rstd_in;
     const f32x2 rstd2 = pack2(rstd, rstd);
-    Vec8 dy = zero8(), h = zero8(), o = zero8();
-    if (on) {
-      dy = load_cols<false>(a.dy, t * a.ld_dy, c, d);
-      h = load_cols<RES32>(a.h, t * a.ld_h, c, d);
-      if (a.dh) o = load_cols<RES32>(a.dh, t * a.ld_dh, c, d);
-    }
+    Vec8 dy = values(dy_in), h = values(h_in), o = values(dh_in);
+    if (kAhead) fetch(t + step);
     f32x2 c2 = pack2(0.0f, 0.0f);
-    bwd8(dy, h, g, dg, rstd2, c2);
+    bwd8(dy, h, from_f32(weights[me], weights[threads + me]), dg, rstd2, c2);
     const float2 cf = unpack2(c2);
     const float m = group_sum(cf.x + cf.y, red[it & 1][threadIdx.y]) * inv_d;
-    if (!on) continue;
     const f32x2 nc2 = pack2(-rstd * m, -rstd * m);
 #pragma unroll
     for (int k = 0; k < 4; ++k) o.p[k] = fma2(nc2, h.p[k], fma2(rstd2, dy.p[k], o.p[k]));
-    if (a.dx) store_cols<false>(a.dx, t * a.ld_dx, c, d, o);
-    if (a.dres) store_cols<RES32>(a.dres, t * a.ld_dres, c, d, o);
+    if (a.dx) store_cols<false>(a.dx, t * a.ld_dx, w, o);
+    if (a.dres) store_cols<RES32>(a.dres, t * a.ld_dres, w, o);
   }
   // the groups' shares, each in its own phase, added in group order
   float* out = gridDim.x == 1 ? a.dweight : a.part + static_cast<long long>(blockIdx.x) * d;
+  float* shares = reinterpret_cast<float*>(weights + 2 * threads);
   float* mine = blockDim.y > 1 ? shares + threadIdx.y * d : out;
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     const float2 p = unpack2(dg.p[k / 2]);
-    if (c + k >= 0 && c + k < d) mine[c + k] = k % 2 ? p.y : p.x;
+    if (k < w.n) mine[w.c + k] = k % 2 ? p.y : p.x;
   }
   if (blockDim.y == 1) return;
   __syncthreads();
-  for (int j = threadIdx.y * blockDim.x + threadIdx.x; j < d; j += blockDim.x * blockDim.y) {
+  for (int j = me; j < d; j += threads) {
     float v = 0.0f;
     for (int r = 0; r < static_cast<int>(blockDim.y); ++r) v += shares[r * d + j];
     out[j] = v;
@@ -1014,11 +1055,11 @@ cudaError_t launch_add_rmsnorm_bwd(const NormBwd& a, bool vec, int num_sms, cuda
     if (one) e = a.res_f32 ? run_norm_bwd_ring<1, true>(a, r, s) : run_norm_bwd_ring<1, false>(a, r, s);
     else e = a.res_f32 ? run_norm_bwd_ring<2, true>(a, r, s) : run_norm_bwd_ring<2, false>(a, r, s);
   } else if (const Phase f = phase_of(a.dy, a.ld_dy);
-             !vec && a.d <= kPhaseCols && in_phase(f, a.h, a.ld_h, a.res_f32) && in_phase(f, a.dh, a.ld_dh, a.res_f32) &&
+             !vec && phase_threads(a.d) <= 1024 && in_phase(f, a.h, a.ld_h, a.res_f32) && in_phase(f, a.dh, a.ld_dh, a.res_f32) &&
              in_phase(f, a.dx, a.ld_dx, false) && in_phase(f, a.dres, a.ld_dres, a.res_f32)) {
     const PhaseShape p = phase_shape(a.T, a.d, 1024, num_sms < 256 ? num_sms : 256);
     parts = p.grid;
-    const size_t smem = p.rows > 1 ? sizeof(float) * p.rows * a.d : 0;
+    const size_t smem = 32 * static_cast<size_t>(p.tpr) * p.rows + (p.rows > 1 ? sizeof(float) * p.rows * a.d : 0);  // up to 32 KB
     if (a.res_f32) add_rmsnorm_bwd_phase_kernel<true><<<p.grid, dim3(p.tpr, p.rows), smem, s>>>(a, f);
     else add_rmsnorm_bwd_phase_kernel<false><<<p.grid, dim3(p.tpr, p.rows), smem, s>>>(a, f);
     e = cudaGetLastError();
