@@ -402,9 +402,11 @@ def test_balance_packed(vgg, ctx, T, E, K, B):
     check_balance(run_balance(vgg, ctx, logits, ids, 0.3, 0.0, None, off), logits, ids, 0.3, 0.0, None, off)
 
 
-@pytest.mark.parametrize("T,E,K,B", [(9000, 96, 2, 4000), (5000, 128, 8, 60), (700, 512, 1, 700)])
+@pytest.mark.parametrize("T,E,K,B", [(9000, 96, 2, 4000), (5000, 128, 8, 60), (700, 512, 1, 700), (15, 8, 2, 49), (9, 24, 1, 55),
+                                     (3, 8, 2, 5), (42, 24, 8, 34), (41, 16, 2, 41), (200, 24, 2, 2000), (19685, 8, 8, 7)])
 def test_balance_many_sequences_in_a_block(vgg, ctx, T, E, K, B):
-    """More sequences in a block's share of the tokens than it has histograms for, and two or three."""
+    """More sequences in a block's share of the tokens than it has histograms for, and two or three; about as many
+    blocks as tokens."""
     logits, ids, g = router_inputs(T, E, K, T + E + B)
     off = [0] + sorted(np.random.default_rng(B).integers(0, T + 1, B - 1).tolist()) + [T]
     mask = torch.rand(T, device="cuda", generator=g) < 0.7

@@ -29,9 +29,12 @@ constexpr int kBalThreads = 512;
 constexpr int kBalWarps = kBalThreads / 32;
 constexpr int kBalMaxBlocks = 1024;  // bounds the number of pieces, and with it the workspace
 constexpr int kBalCluster = 16;      // up to so many blocks wait for one another as a cluster, more as a whole grid
-// Most logits that one cluster takes.  Eager calls of 2048 x 128: 12.3 us in a cluster, 15.4 as a cooperative grid with the
-// clearing ahead of it; 4096 x 128: 16.4 and 15.4 (in a graph 13.8 and 11.3).
-constexpr long long kBalOneCluster = 1 << 18;
+// What one cluster takes: T (E + 16), the 16 standing for a token's choices and reductions, below kBalOneCluster, and at
+// most kBalClusterSeqs sequences, each of which a block closes with two barriers.  Eager calls in a cluster and as a
+// cooperative grid with the clearing ahead of it: 2048 x 128 12.3 and 15.4 us, 4096 x 128 16.4 and 15.4, 8192 x 16 14.4 and
+// 15.4, 16384 x 16 16.4 and 15.4; 1500 x 64 in 32 sequences 24.2 and 25.6, in 48 27.3 and 26.5.
+constexpr long long kBalOneCluster = 3 << 17;
+constexpr int kBalClusterSeqs = 40;
 
 inline size_t al256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
@@ -47,7 +50,8 @@ struct BalWs {
 };
 
 BalWs carve_balance(void* ws, long long T, int E, int B) {
-  const size_t pieces = static_cast<size_t>(T < kBalMaxBlocks ? (T > 0 ? T : 1) : kBalMaxBlocks) + B;
+  // a launch has at most max(T, kBalCluster) blocks
+  const size_t pieces = static_cast<size_t>(T < kBalCluster ? kBalCluster : T < kBalMaxBlocks ? T : kBalMaxBlocks) + B;
   uint8_t* p = static_cast<uint8_t*>(ws);
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -526,9 +530,12 @@ cudaError_t run_balance(const BalanceArgs& a, void* ws, int num_sms, cudaStream_
   if (st != cudaSuccess) return st;
   if ((st = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess) return st;
   const BalWs w = carve_balance(ws, a.T, a.E, a.B);
-  const long long want = (a.T + kBalWarps * kTile - 1) / (kBalWarps * kTile);  // blocks that give every warp a tile
+  // blocks that give every warp a tile, or every sequence a block where that is more (a block works on one sequence after
+  // the other: 42 tokens in 34 sequences took 93 us in one block, 15 us in sixteen)
+  const long long seqs = a.T < a.B ? a.T : a.B, tiles = (a.T + kBalWarps * kTile - 1) / (kBalWarps * kTile);
+  const long long want = tiles > seqs ? tiles : seqs;
   long long G;
-  if (a.T * a.E <= kBalOneCluster) {
+  if (a.T * (a.E + 16) < kBalOneCluster && seqs <= kBalClusterSeqs) {
     for (G = 1; G < kBalCluster && G < want; G *= 2) {
     }
   } else {
