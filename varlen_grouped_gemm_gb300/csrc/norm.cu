@@ -322,7 +322,8 @@ __global__ void __launch_bounds__(1024, NV == 1 ? 2 : 1) add_rmsnorm_kernel(cons
   norm_row_codes<NV, FORM>(a, o, threadIdx.x, blockDim.x, nvec, row_ok, amax, h);
 }
 
-// Rows of any width and alignment, bf16 out: a block a row, 16 values a thread.
+// Rows that are not aligned and too wide for a vector a thread (more than about 8100 columns): a block a row, 16 values a
+// thread, each a load of its own.
 template <bool RES32>
 __global__ void __launch_bounds__(1024) add_rmsnorm_any_kernel(const NormFwd a) {
   constexpr int N = 16;
@@ -356,24 +357,34 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_any_kernel(const NormFwd a) 
 
 // ---- rows that start anywhere
 //
-// Where the tensors of a call begin every row at the same element mod 8 (its phase: addresses and strides alike), the
-// row's vectors begin at columns 8 j - phase and are aligned in all of them; a part of a vector is left at either end.
+// A row's phase is the element mod 8 at which it begins; tensors of a call mostly have it in common (addresses and strides
+// alike).  In its phase a row's vectors begin at its first aligned column and are aligned in all of those tensors;
+// the others are read and written a value at a time.
 // A row group takes rows whose numbers differ by multiples of eight, so that its phase, and with it every thread's
 // columns, stay the same: the weight's vector is read once, and the backward's share of dg stays in registers.  The next
 // row's loads are on their way while a row is reduced.
-// Against the kernels for any alignment, a value a load: 8192 x 4001 bf16 forward 47 us and 161 (196 MB, 39 us of them),
-// backward 69 and 495; 16384 x 999 24 and 72, 41 and 740; 300 x 1501 3.0 and 8.2, 7.2 and 17.6.
+// Against the kernels that load a value at a time: 8192 x 4001 bf16 forward 48 us and 161 (196 MB, 39 us of them), backward
+// 70 and 495; 16384 x 999 26 and 72, 42 and 740; 300 x 1501 3.1 and 8.2, 7.0 and 17.6.  One tensor out of phase: 61 and 95
+// us at 8192 x 4001.
 struct Phase {
   int first, step;  // of row 0, and from one row to the next
+  unsigned in;      // bit i: the call's tensor i has this phase
   __device__ int of(long long t) const { return (first + static_cast<int>(t & 7) * step) & 7; }
+  __device__ bool has(int i) const { return in >> i & 1; }
 };
-inline Phase phase_of(const void* p, long long ld) {  // of a bf16 tensor
-  return {static_cast<int>(reinterpret_cast<uintptr_t>(p) / 2 & 7), static_cast<int>(ld & 7)};
-}
-// Whether a tensor (null: none) has that phase; four fp32 values fill 16 bytes.
-inline bool in_phase(const Phase& f, const void* p, long long ld, bool f32) {
-  const long long m = f32 ? 3 : 7, at = static_cast<long long>(reinterpret_cast<uintptr_t>(p) / (f32 ? 4 : 2));
-  return !p || (((at - f.first) & m) == 0 && ((ld - f.step) & m) == 0);
+struct PhaseOf {
+  const void* p;
+  long long ld;
+  bool f32;
+};
+// The phase of a bf16 tensor, and which of n tensors have it (a missing one does; four fp32 values fill 16 bytes).
+inline Phase phase_of(const void* p, long long ld, const PhaseOf* t, int n) {
+  Phase f{static_cast<int>(reinterpret_cast<uintptr_t>(p) / 2 & 7), static_cast<int>(ld & 7), 0};
+  for (int i = 0; i < n; ++i) {
+    const long long m = t[i].f32 ? 3 : 7, at = static_cast<long long>(reinterpret_cast<uintptr_t>(t[i].p) / (t[i].f32 ? 4 : 2));
+    if (!t[i].p || (((at - f.first) & m) == 0 && ((t[i].ld - f.step) & m) == 0)) f.in |= 1u << i;
+  }
+  return f;
 }
 // Threads of a row: the fewest vectors that a phase leaves, and a thread for every column outside them.
 inline int phase_threads(int d) { return d < 8 ? d : d - 7 * ((d - 7) / 8); }
@@ -396,27 +407,41 @@ struct Pair4 {
 template <bool F32>
 using Cols8 = std::conditional_t<F32, Pair4, uint4>;
 template <bool F32>
-__device__ __forceinline__ Cols8<F32> load_cols(const void* base, long long off, const Cols& w) {
+__device__ __forceinline__ Cols8<F32> load_cols(const void* base, long long off, const Cols& w, bool in_phase) {
   Cols8<F32> v{};
   if constexpr (F32) {
     const float* p = static_cast<const float*>(base) + off + w.c;
-    if (w.n == 8) {
+    if (w.n == 8 && in_phase) {
       v.a = __ldcs(reinterpret_cast<const float4*>(p));
       v.b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+    } else if (w.n == 8) {
+      v.a = make_float4(p[0], p[1], p[2], p[3]);
+      v.b = make_float4(p[4], p[5], p[6], p[7]);
     } else if (w.n) {
       v.a.x = *p;
     }
   } else {
-    if (w.n == 8) v = ldcs4(base, off + w.c);
-    else if (w.n) v.x = static_cast<const uint16_t*>(base)[off + w.c];
+    const uint16_t* p = static_cast<const uint16_t*>(base) + off + w.c;
+    if (w.n == 8 && in_phase) {
+      v = ldcs4(base, off + w.c);
+    } else if (w.n == 8) {
+      v = make_uint4(p[0] | static_cast<uint32_t>(p[1]) << 16, p[2] | static_cast<uint32_t>(p[3]) << 16,
+                     p[4] | static_cast<uint32_t>(p[5]) << 16, p[6] | static_cast<uint32_t>(p[7]) << 16);
+    } else if (w.n) {
+      v.x = *p;
+    }
   }
   return v;
 }
 __device__ __forceinline__ Vec8 values(const Pair4& r) { return from_f32(r.a, r.b); }
 template <bool F32>
-__device__ __forceinline__ void store_cols(void* base, long long off, const Cols& w, const Vec8& v) {
-  if (w.n == 8) store8<F32>(base, off + w.c, v);
-  else if (w.n) store1<F32>(base, off + w.c, unpack2(v.p[0]).x);
+__device__ __forceinline__ void store_cols(void* base, long long off, const Cols& w, bool in_phase, const Vec8& v) {
+  if (w.n == 8 && in_phase) return store8<F32>(base, off + w.c, v);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const float2 p = unpack2(v.p[k / 2]);
+    if (k < w.n) store1<F32>(base, off + w.c + k, k % 2 ? p.y : p.x);
+  }
 }
 __device__ __forceinline__ Vec8 weight_cols(const void* w, int f32, const Cols& l) {
   float f[8];
@@ -468,8 +493,8 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_phase_kernel(const NormFwd a
   uint4 x{};
   auto fetch = [&](long long t) {  // a row ahead
     if (t >= a.T) return;
-    res = load_cols<RES32>(a.res, t * a.ld_res, w);
-    if (a.x) x = load_cols<false>(a.x, t * a.ld_x, w);
+    res = load_cols<RES32>(a.res, t * a.ld_res, w, f.has(0));
+    if (a.x) x = load_cols<false>(a.x, t * a.ld_x, w, f.has(1));
   };
   fetch(t0);
   int it = 0;
@@ -477,7 +502,7 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_phase_kernel(const NormFwd a
     Vec8 h;
     if constexpr (RES32) h = a.x ? add_x(values(res), x) : values(res);
     else h = values(a.x ? add_x(res, x) : res);
-    if (a.h) store_cols<RES32>(a.h, t * a.ld_h, w, h);
+    if (a.h) store_cols<RES32>(a.h, t * a.ld_h, w, f.has(2), h);
     fetch(t + step);
     const float2 sq = unpack2(squares(h, pack2(0.0f, 0.0f)));
     const float rstd = inv_root(fmaf(group_sum(sq.x + sq.y, red[it & 1][threadIdx.y]), inv_d, a.eps));
@@ -485,7 +510,7 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_phase_kernel(const NormFwd a
     const f32x2 r2 = pack2(rstd, rstd);
 #pragma unroll
     for (int k = 0; k < 4; ++k) h.p[k] = mul2(mul2(h.p[k], r2), g.p[k]);
-    store_cols<false>(a.y, t * a.ld_y, w, h);
+    store_cols<false>(a.y, t * a.ld_y, w, f.has(3), h);
   }
 }
 
@@ -706,9 +731,10 @@ cudaError_t launch_add_rmsnorm(const NormFwd& a, bool vec, int num_sms, cudaStre
     return a.res_f32 ? run_norm_ring_form<true>(a, r, s) : run_norm_ring_form<false>(a, r, s);
   }
   if (!vec) {
-    const Phase f = phase_of(a.y, a.ld_y);
-    if (phase_threads(a.d) <= 1024 && in_phase(f, a.res, a.ld_res, a.res_f32) && in_phase(f, a.x, a.ld_x, false) &&
-        in_phase(f, a.h, a.ld_h, a.res_f32)) {
+    if (phase_threads(a.d) <= 1024) {
+      const PhaseOf t[] = {{a.res, a.ld_res, a.res_f32 != 0}, {a.x, a.ld_x, false}, {a.h, a.ld_h, a.res_f32 != 0}, {a.y, a.ld_y, false}};
+      const PhaseOf& lead = a.x ? t[1] : a.res_f32 ? t[3] : t[0];  // what is read, if it is bf16
+      const Phase f = phase_of(lead.p, lead.ld, t, 4);
       const PhaseShape p = phase_shape(a.T, a.d, 2048, num_sms);
       if (a.res_f32) add_rmsnorm_phase_kernel<true><<<p.grid, dim3(p.tpr, p.rows), 0, s>>>(a, f);
       else add_rmsnorm_phase_kernel<false><<<p.grid, dim3(p.tpr, p.rows), 0, s>>>(a, f);
@@ -805,7 +831,7 @@ __global__ void __launch_bounds__(512) add_rmsnorm_bwd_wide_kernel(const NormBwd
   }
 }
 
-// Rows of any width and alignment, 32 values a thread.
+// Rows that are not aligned and too wide for a vector a thread, 32 values a thread.
 template <bool RES32>
 __global__ void __launch_bounds__(512) add_rmsnorm_bwd_any_kernel(const NormBwd a) {
   constexpr int N = 32;
@@ -848,7 +874,7 @@ __global__ void __launch_bounds__(512) add_rmsnorm_bwd_any_kernel(const NormBwd 
   }
 }
 
-// Rows that start anywhere, the tensors in phase (see the forward).
+// Rows that start anywhere (see the forward).
 template <bool RES32>
 __global__ void __launch_bounds__(1024) add_rmsnorm_bwd_phase_kernel(const NormBwd a, Phase f) {
   extern __shared__ __align__(16) float4 weights[];  // every thread's, which registers have no room for; then the shares
@@ -874,9 +900,9 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_bwd_phase_kernel(const NormB
   auto fetch = [&](long long t) {  // a row ahead where the registers suffice (1024 threads of 64)
     if (t >= a.T) return;
     rstd_in = __ldg(a.rstd + t);
-    dy_in = load_cols<false>(a.dy, t * a.ld_dy, w);
-    h_in = load_cols<RES32>(a.h, t * a.ld_h, w);
-    if (a.dh) dh_in = load_cols<RES32>(a.dh, t * a.ld_dh, w);
+    dy_in = load_cols<false>(a.dy, t * a.ld_dy, w, true);
+    h_in = load_cols<RES32>(a.h, t * a.ld_h, w, f.has(0));
+    if (a.dh) dh_in = load_cols<RES32>(a.dh, t * a.ld_dh, w, f.has(1));
   };
   if (kAhead) fetch(t0);
   int it = 0;
@@ -893,8 +919,8 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_bwd_phase_kernel(const NormB
     const f32x2 nc2 = pack2(-rstd * m, -rstd * m);
 #pragma unroll
     for (int k = 0; k < 4; ++k) o.p[k] = fma2(nc2, h.p[k], fma2(rstd2, dy.p[k], o.p[k]));
-    if (a.dx) store_cols<false>(a.dx, t * a.ld_dx, w, o);
-    if (a.dres) store_cols<RES32>(a.dres, t * a.ld_dres, w, o);
+    if (a.dx) store_cols<false>(a.dx, t * a.ld_dx, w, f.has(2), o);
+    if (a.dres) store_cols<RES32>(a.dres, t * a.ld_dres, w, f.has(3), o);
   }
   // the groups' shares, each in its own phase, added in group order
   float* out = gridDim.x == 1 ? a.dweight : a.part + static_cast<long long>(blockIdx.x) * d;
@@ -1054,9 +1080,10 @@ cudaError_t launch_add_rmsnorm_bwd(const NormBwd& a, bool vec, int num_sms, cuda
     parts = r.grid;
     if (one) e = a.res_f32 ? run_norm_bwd_ring<1, true>(a, r, s) : run_norm_bwd_ring<1, false>(a, r, s);
     else e = a.res_f32 ? run_norm_bwd_ring<2, true>(a, r, s) : run_norm_bwd_ring<2, false>(a, r, s);
-  } else if (const Phase f = phase_of(a.dy, a.ld_dy);
-             !vec && phase_threads(a.d) <= 1024 && in_phase(f, a.h, a.ld_h, a.res_f32) && in_phase(f, a.dh, a.ld_dh, a.res_f32) &&
-             in_phase(f, a.dx, a.ld_dx, false) && in_phase(f, a.dres, a.ld_dres, a.res_f32)) {
+  } else if (!vec && phase_threads(a.d) <= 1024) {
+    const bool f32 = a.res_f32 != 0;
+    const PhaseOf t[] = {{a.h, a.ld_h, f32}, {a.dh, a.ld_dh, f32}, {a.dx, a.ld_dx, false}, {a.dres, a.ld_dres, f32}};
+    const Phase f = phase_of(a.dy, a.ld_dy, t, 4);
     const PhaseShape p = phase_shape(a.T, a.d, 1024, num_sms < 256 ? num_sms : 256);
     parts = p.grid;
     const size_t smem = 32 * static_cast<size_t>(p.tpr) * p.rows + (p.rows > 1 ? sizeof(float) * p.rows * a.d : 0);  // up to 32 KB
