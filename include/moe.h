@@ -527,7 +527,7 @@ int moe_backward_e4m3(moe_ctx* ctx, const void* dO, const void* X, const void* W
  * (ld_*, in elements, >= d) are free; columns are contiguous.  h may be the residual itself and y may be x (every
  * element is read before it is written).  NULL allowed: x, h (when x is NULL), rstd, and y (when codes are asked
  * for).  1 <= d <= 16384 and any T >= 0 (T = 0 does nothing); d a multiple of 64 and rows 16-byte aligned with codes,
- * else any alignment of the type (vector accesses need d % 8 == 0 and 16-byte aligned rows).  eps >= 0.
+ * else any alignment of the type (d % 8 == 0 with 16-byte aligned rows is fastest).  eps >= 0.
  * Squares are summed in fp32: |h| up to about 1e18.  MOE_ERR_INVALID_ARG on a violated rule.
  */
 int moe_add_rmsnorm(moe_ctx* ctx, const void* x, long long ld_x, const void* residual, long long ld_residual,
