@@ -823,11 +823,20 @@ __global__ void __launch_bounds__(512) add_rmsnorm_bwd_wide_kernel(const NormBwd
       }
     }
   }
-  float* out = gridDim.x == 1 ? a.dweight : a.part + static_cast<long long>(blockIdx.x) * a.d;
+  // dweight may begin at any float, the shares' rows are aligned
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int j = threadIdx.x + blockDim.x * i;
-    if (j < nvec) store8<true>(out, 8ll * j, dg[i]);
+    if (j >= nvec) continue;
+    if (gridDim.x > 1) {
+      store8<true>(a.part + static_cast<long long>(blockIdx.x) * a.d, 8ll * j, dg[i]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float2 p = unpack2(dg[i].p[k / 2]);
+        a.dweight[8 * j + k] = k % 2 ? p.y : p.x;
+      }
+    }
   }
 }
 
@@ -1013,15 +1022,17 @@ __global__ void __launch_bounds__(512, 1) add_rmsnorm_bwd_ring_kernel(const Norm
     if (dres) dres += step * a.ld_dres * ES;
   }
   ring_drain(sh, stages, it);
-  // the groups' shares, added in group order
+  // the groups' shares, added in group order; a block of one group stores its vectors itself, but not to dweight, which
+  // may begin at any float
   float* share = reinterpret_cast<float*>(nb_ring);
   float* out = gridDim.x == 1 ? a.dweight : a.part + static_cast<long long>(blockIdx.x) * a.d;
+  const bool direct = RG == 1 && gridDim.x > 1;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int j = tx + tpr * i;
-    if (j < nvec) store8<true>(RG > 1 ? share + static_cast<size_t>(rg) * a.d : out, 8ll * j, dg[i]);
+    if (j < nvec) store8<true>(direct ? out : share + static_cast<size_t>(rg) * a.d, 8ll * j, dg[i]);
   }
-  if (RG == 1) return;
+  if (direct) return;
   __syncthreads();
   for (int j = rg * tpr + tx; j < a.d; j += RG * tpr) {
     float v = 0.0f;
