@@ -59,3 +59,72 @@ def test_norm_backward_weight_gradient_begins_at_any_float(vgg, ctx, T, d, res_t
     _, gw = bo.rmsnorm_backward(f64(dy), f64(h), f64(w), f64(rstd), None)
     assert np.all(np.abs(f64(dw) - gw) <= (T + 3) * U * np.sum(np.abs(f64(dy) * xh), axis=0))
     assert bool((flat[:shift] == 777.0).all()) and bool((flat[shift + d:] == 777.0).all())
+
+
+# ------------------------------------------------------------------------------------------------ host threads
+
+
+def threaded_call(vgg, c, st, kind, size, g):
+    """(outputs, the call) with every pointer looked up once, so that calls of two threads overlap."""
+    L, s = vgg.lib(), st.cuda_stream
+    keep = []
+
+    def p(t):
+        keep.append(t)
+        return t.data_ptr()
+
+    if kind == "balance":
+        T, E = 300, size
+        logits = torch.randn((T, E), device="cuda", generator=g)
+        ids = torch.topk(logits, 1, dim=1).indices.to(I32)
+        out = [torch.empty(3, device="cuda"), torch.empty((1, E), dtype=I32, device="cuda"),
+               torch.empty((1, E), device="cuda"), torch.empty((T, E), device="cuda")]
+        n = vgg.moe_balance_loss_workspace_bytes(T, E, 1)
+        args = (p(logits), p(ids), None, None, T, E, 1, 1, 1.0, 1.0, None, *map(p, out),
+                p(torch.empty(n, dtype=U8, device="cuda")), n, s)
+        f = L.moe_balance_loss
+    elif kind == "norm":
+        T, d = 640, size
+        x, r, w = (torch.randn((n, d), device="cuda", generator=g).to(BF) for n in (T, T, 1))
+        out = [torch.empty_like(x), torch.empty_like(x)]
+        args = (p(x), d, p(r), d, 0, p(w), 0, T, d, 1e-6, p(out[0]), d, p(out[1]), d, None, 0, None, None, s)
+        f = L.moe_add_rmsnorm
+    elif kind == "norm_backward":
+        T, d = 40, size
+        dy, h, w = (torch.randn((n, d), device="cuda", generator=g).to(BF) for n in (T, T, 1))
+        out = [torch.empty_like(dy), torch.empty(d, device="cuda")]
+        n = vgg.moe_add_rmsnorm_workspace_bytes(T, d)
+        args = (p(dy), d, p(h), d, 0, p(w), 0, p(torch.ones(T, device="cuda")), None, 0, T, d, p(out[0]), d, None, 0,
+                p(out[1]), p(torch.empty(n, dtype=U8, device="cuda")), n, s)
+        f = L.moe_add_rmsnorm_backward
+    else:
+        E = size
+        off = torch.arange(E + 1, dtype=I32, device="cuda") * 2
+        A = torch.randn((2 * E, 64), device="cuda", generator=g).to(BF)
+        B = torch.randn((E, 64, 64), device="cuda", generator=g).to(BF)
+        out = [torch.empty((2 * E, 64), device="cuda")]
+        args = (p(A), None, p(B), 1, E, 2 * E, 64, 64, 2 * E, p(off), p(out[0]), s)
+        f = L.moe_test_gemm_varlen_m
+    keep.append(out)
+    return out, lambda keep=keep: f(c.handle, *args)
+
+
+@pytest.mark.parametrize("kind", ["balance", "norm", "norm_backward", "product"])
+def test_first_call_of_a_thread(vgg, kind):
+    """A thread that has made no CUDA call yet has no current context: the call brings it about."""
+    import threading
+
+    c, st = vgg.Context(0), torch.cuda.Stream()
+    out, call = threaded_call(vgg, c, st, kind, 64, gen_of(3))
+    torch.cuda.synchronize()
+    status = []
+    t = threading.Thread(target=lambda: status.append(call()))
+    t.start()
+    t.join()
+    torch.cuda.synchronize()
+    assert status == [0]
+    there = [t.clone() for t in out]
+    assert call() == 0
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(out, there))
+    assert vgg.moe_get_error(c) == (vgg.MOE_OK, 0)

@@ -132,16 +132,18 @@ inline size_t al(size_t x) { return (x + kAlign - 1) & ~(kAlign - 1); }
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline int ceil_div(long long a, long long b) { return static_cast<int>((a + b - 1) / b); }
 
-// Restores the caller's current device on scope exit.
+// Restores the caller's current device on scope exit.  The device is set even where it is the current one already: only
+// that makes its context the thread's, without which a thread's first call could not encode a tensor map.
 struct DeviceGuard {
+  const int dev;
   int prev = -1;
   bool ok = false;
-  explicit DeviceGuard(int dev) {
+  explicit DeviceGuard(int d) : dev(d) {
     if (cudaGetDevice(&prev) != cudaSuccess) prev = -1;
-    ok = (prev == dev) || cudaSetDevice(dev) == cudaSuccess;
+    ok = cudaSetDevice(dev) == cudaSuccess;
   }
   ~DeviceGuard() {
-    if (prev >= 0) cudaSetDevice(prev);
+    if (prev >= 0 && prev != dev) cudaSetDevice(prev);
   }
 };
 
