@@ -128,3 +128,39 @@ def test_first_call_of_a_thread(vgg, kind):
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(out, there))
     assert vgg.moe_get_error(c) == (vgg.MOE_OK, 0)
+
+
+@pytest.mark.parametrize("kind,small,large", [("balance", 4, 32), ("balance", 516, 1024), ("norm", 4160, 8192),
+                                              ("norm_backward", 512, 8192), ("product", 4, 600)])
+def test_calls_from_two_threads(vgg, kind, small, large):
+    """Contexts, streams and sizes of their own, but one kernel whose shared memory depends on the size: every call is
+    launched, and the results are those of a call alone."""
+    import threading
+
+    work = []
+    for i, size in enumerate((small, large)):
+        c, st = vgg.Context(0), torch.cuda.Stream()
+        out, call = threaded_call(vgg, c, st, kind, size, gen_of(100 + i))
+        torch.cuda.synchronize()
+        assert call() == 0
+        torch.cuda.synchronize()
+        work.append((c, st, out, [t.clone() for t in out], call))
+    status = [0, 0]
+
+    def loop(i):
+        st, call = work[i][1], work[i][4]
+        for k in range(6000):
+            status[i] = status[i] or call()
+            if k % 100 == 99:
+                st.synchronize()
+
+    threads = [threading.Thread(target=loop, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert status == [0, 0]
+    for c, _, out, alone, _ in work:
+        assert all(torch.equal(a, b) for a, b in zip(out, alone))
+        assert vgg.moe_get_error(c) == (vgg.MOE_OK, 0)

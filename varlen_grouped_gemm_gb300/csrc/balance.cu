@@ -525,8 +525,13 @@ template <bool VEC, int LPT, int NV, int UN, int ST>
 cudaError_t run_balance(const BalanceArgs& a, void* ws, int num_sms, cudaStream_t s) {
   auto kern = balance_kernel<VEC, LPT, NV, UN, ST>;
   constexpr int kTile = 32 / LPT * UN;
-  const size_t smem = sizeof(float) * (kBalWarps * static_cast<size_t>(a.E) * (1 + (VEC ? ST * kTile : 0)) + (a.E + 3) / 4 * 4);
-  cudaError_t st = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  auto bytes = [](int E) {
+    return sizeof(float) * (kBalWarps * static_cast<size_t>(E) * (1 + (VEC ? ST * kTile : 0)) + (E + 3) / 4 * 4);
+  };
+  const size_t smem = bytes(a.E);
+  // the attribute is the kernel's, whichever thread launches it with however many experts: always the same value
+  cudaError_t st = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        static_cast<int>(bytes(VEC ? 4 * LPT * NV : LPT * NV)));
   if (st != cudaSuccess) return st;
   if ((st = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess) return st;
   const BalWs w = carve_balance(ws, a.T, a.E, a.B);

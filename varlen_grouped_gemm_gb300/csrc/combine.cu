@@ -267,7 +267,7 @@ cudaError_t launch_token_backward(const float* part, int part_ld, const int32_t*
   if (T <= 0) return cudaSuccess;
   const size_t smem = token_backward_smem(E);
   cudaError_t e = cudaFuncSetAttribute(token_backward_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+                                       static_cast<int>(token_backward_smem(kMaxGroups)));  // one value for all threads
   if (e != cudaSuccess) return e;
   token_backward_kernel<<<(T + kTbWarps - 1) / kTbWarps, 32 * kTbWarps, smem, s>>>(
       part, part_ld, tok_ptr, tok_pairs, offsets, E, sorted_w, topk_ids, topk_w, K, dXp, WrT, T, d, cap, dS, dlogits,

@@ -1603,9 +1603,11 @@ template <int BN, int STAGES, int EW, int DEPTH, int AMODE, int BMODE, int VAR, 
           int XF = 0>
 cudaError_t launch_grouped_gemm(const GemmParams& p, const Maps& maps, int grid, cudaStream_t stream) {
   auto kern = grouped_gemm_kernel<BN, STAGES, EW, DEPTH, AMODE, BMODE, VAR, EPI, OUTF32, CN, XF>;
-  const size_t smem = SmemLayout<BN, STAGES, EW, DEPTH, (XF & X_DUAL_A) ? 2 : 1, (XF & X_PAIR) ? BN / 2 : BN,
-                                 mx_stage_bytes(BN, XF)>::bytes(p.groups, VAR);
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  using L = SmemLayout<BN, STAGES, EW, DEPTH, (XF & X_DUAL_A) ? 2 : 1, (XF & X_PAIR) ? BN / 2 : BN, mx_stage_bytes(BN, XF)>;
+  const size_t smem = L::bytes(p.groups, VAR);
+  // the attribute is the kernel's, whichever thread launches it with however many groups: always the same value
+  constexpr size_t most = L::bytes(kMaxGroups, VAR) < kMaxSmem ? L::bytes(kMaxGroups, VAR) : kMaxSmem;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most));
   if (e != cudaSuccess) return e;
   if (grid <= 0) return cudaSuccess;
   const int threads = WarpPlan<STAGES, EW, AMODE, BMODE, CN, XF>::kThreads;

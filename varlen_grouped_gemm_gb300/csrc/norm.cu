@@ -585,6 +585,9 @@ struct RingShape {
   int tpr, rgs, stages, grid;
   size_t smem;
 };
+// The most that a shape takes: two of the backward's widest rows (8192 columns in bf16 and twice in fp32).  The kernels'
+// attribute is always set to it: with a call's own size one thread could lower it between another's setting and launch.
+constexpr int kRingMost = 2 * 8192 * (2 + 4 + 4);
 inline int round32(int x) { return (x + 31) & ~31; }
 inline RingShape ring_shape(long long T, int d, int NV, size_t row, size_t bytes, int blocks) {
   RingShape r;
@@ -704,7 +707,7 @@ cudaError_t run_norm(const NormFwd& a, int tpr, int rows, cudaStream_t s) {
 template <bool RES32, int FORM>
 cudaError_t run_norm_ring(const NormFwd& a, const RingShape& r, cudaStream_t s) {
   auto kern = add_rmsnorm_ring_kernel<3, RES32, FORM>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(r.smem));
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingMost);
   if (e != cudaSuccess) return e;
   kern<<<r.grid, dim3(r.tpr, r.rgs), r.smem, s>>>(a, r.stages);
   return cudaGetLastError();
@@ -1068,7 +1071,7 @@ __global__ void __launch_bounds__(1024) reduce_rows_kernel(const float* __restri
 template <int NV, bool RES32>
 cudaError_t run_norm_bwd_ring(const NormBwd& a, const RingShape& r, cudaStream_t s) {
   auto kern = add_rmsnorm_bwd_ring_kernel<NV, RES32>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(r.smem));
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingMost);
   if (e != cudaSuccess) return e;
   kern<<<r.grid, dim3(r.tpr, r.rgs), r.smem, s>>>(a, r.stages);
   return cudaGetLastError();
