@@ -591,8 +591,8 @@ int moe_balance_loss(moe_ctx* ctx, const float* logits, const int32_t* topk_ids,
  *   dX[t,i]   = dX_in[t,i] + sum_e dlogits[t,e] W_r[i,e]        (bf16; dX_in NULL: 0)
  *   dW_r[i,e] = dW_r_in[i,e] + sum_t X[t,i] dlogits[t,e]        (fp32; dW_r_in NULL: 0)
  *
- * dlogits [T,E] fp32 enters the first product rounded to bf16 and the second as three bf16 parts, which together
- * hold its 24 significant bits; fp32 accumulation.  X, dX_in, dX [T,d], W_r [d,E] bf16; dW_r_in, dW_r
+ * dlogits [T,E] fp32 enters the first product as two bf16 parts (what they leave is 2^-16 of a value) and the second
+ * as three, which together hold its 24 significant bits; fp32 accumulation.  X, dX_in, dX [T,d], W_r [d,E] bf16; dW_r_in, dW_r
  * [d,E] fp32; dX may be dX_in and dW_r may be dW_r_in, no other input.  dX or dW_r may be NULL (that product is
  * skipped).  T <= 65536 (0 allowed), d a multiple of 64, E a multiple of 8 up to 1024, 16-byte aligned.  ws:
  * caller-owned, 256-byte aligned, at least moe_router_backward_workspace_bytes(T, d, E) bytes (0 on bad sizes).

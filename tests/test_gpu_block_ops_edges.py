@@ -61,6 +61,66 @@ def test_norm_backward_weight_gradient_begins_at_any_float(vgg, ctx, T, d, res_t
     assert bool((flat[:shift] == 777.0).all()) and bool((flat[shift + d:] == 777.0).all())
 
 
+# ------------------------------------------------------------------------------------------------ router products
+
+
+def run_router(vgg, ctx, dl, X, W, dX_in=None, dW_in=None, want=(True, True)):
+    (T, E), d = dl.shape, X.shape[1]
+    dX = torch.full((T, d), 9.0, dtype=BF, device="cuda") if want[0] else None
+    dW = torch.full((d, E), 9.0, device="cuda") if want[1] else None
+    ws = torch.randint(0, 256, (vgg.moe_router_backward_workspace_bytes(T, d, E),), dtype=U8, device="cuda")
+    vgg.moe_router_backward(ctx, dl, X, W, dX_in, dW_in, dX, dW, ws)
+    return dX, dW
+
+
+@pytest.mark.parametrize("shared", [1.0, 10.0, 100.0])
+@pytest.mark.parametrize("T,d,E", [(3, 128, 16), (512, 512, 128), (300, 192, 1024), (129, 2880, 136), (2561, 2112, 264),
+                                   (3000, 2048, 1024)])
+def test_router_input_gradient_where_the_sum_cancels(vgg, ctx, T, d, E, shared):
+    """Rows of a gradient behind a softmax sum to zero, so what W_r's columns have in common cancels in the result, and
+    only there: a rounding of dlogits to 8 bits would stand out.  Two bf16 parts leave 2^-16 of a value."""
+    g = gen_of(T + d + E)
+    p = torch.softmax(2 * torch.randn((T, E), device="cuda", generator=g).double(), 1)
+    u = torch.randn(E, device="cuda", generator=g).double()
+    dl = (1e-2 * p * (u - p @ u[:, None])).float()
+    W = ((torch.randn((d, E), device="cuda", generator=g) + shared * torch.randn((d, 1), device="cuda", generator=g)) /
+         d ** 0.5).to(BF)
+    X = torch.zeros((T, d), dtype=BF, device="cuda")
+    ref = dl.double() @ W.double().T
+    err = (2.0 ** -16 + 2 * (E + 2) * U) * (dl.double().abs() @ W.double().abs().T)  # and a step for every addition
+    both, _ = run_router(vgg, ctx, dl, X, W)
+    assert bool(((both.double() - ref).abs() <= err + 2.0 ** -8 * (ref.abs() + err)).all())
+    alone, _ = run_router(vgg, ctx, dl, X, W, want=(True, False))
+    assert torch.equal(alone, both)
+
+
+ROUTER_SIZES = [(1, 64, 8), (3, 128, 16), (64, 192, 64), (65, 256, 128), (127, 320, 136), (300, 64, 1024), (700, 512, 264),
+                (2000, 1536, 96), (129, 2880, 128), (2561, 2112, 264)]
+
+
+@pytest.mark.parametrize("T,d,E", ROUTER_SIZES)
+def test_router_weight_gradient_to_the_last_bit_of_dlogits(vgg, ctx, T, d, E):
+    """dlogits of 17 to 24 significant bits, each element of the product a single one of them: three bf16 parts leave
+    2^-24, their additions a step (2^-23) each, the sums of accumulators and splits and the added matrix half a step."""
+    g = gen_of(T * d + E)
+    n = torch.randint(1 << 16, 1 << 24, (T, E), device="cuda", generator=g)
+    dl = torch.where(torch.rand((T, E), device="cuda", generator=g) < 0.5, -n, n).float()
+    at = torch.randint(0, T, (d,), device="cuda", generator=g)
+    X = torch.zeros((T, d), dtype=BF, device="cuda")
+    X[at, torch.arange(d, device="cuda")] = 1.0
+    W = torch.zeros((d, E), dtype=BF, device="cuda")
+    pick = torch.randint(0, E, (d,), device="cuda", generator=g)
+    W[torch.arange(d, device="cuda"), pick] = 1.0
+    dX_in = torch.randint(-8, 9, (T, d), device="cuda", generator=g).to(BF)
+    dW_in = torch.randint(-8, 9, (d, E), device="cuda", generator=g).float()
+    dX, dW = run_router(vgg, ctx, dl, X, W, dX_in, dW_in)
+    value = dl[at].double()
+    assert bool(((dW.double() - value - dW_in.double()).abs() <= (1 + 6 + 2) * U * (value.abs() + 8)).all())
+    ref = dl[:, pick].double() + dX_in.double()
+    err = (2.0 ** -16 + 4 * U) * (ref.abs() + 8)
+    assert bool(((dX.double() - ref).abs() <= err + 2.0 ** -8 * (ref.abs() + err)).all())
+
+
 # ------------------------------------------------------------------------------------------------ host threads
 
 

@@ -1691,7 +1691,8 @@ int moe_router_backward(moe_ctx* ctx, const float* dlogits, const void* X, const
   float* sums = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + al(sizeof(__nv_bfloat16) * 3 * static_cast<size_t>(Tp) * E));
   if (T > 0) VGG_LAUNCH("split_dlogits", launch_split_dlogits(dlogits, T, Tp, E, parts, s));
   if (T > 0 && dX) {
-    // dX = dX_in + hi W_r^T: one bf16 rounding of dlogits (2^-8 of a term at most) under a bf16 result
+    // dX = dX_in + (hi + mid) W_r^T: rows of a gradient behind a softmax sum to zero, so what W_r's columns share cancels
+    // in the sum but not in the rounding of its terms; two parts leave 2^-16 of a term under a bf16 result
     GemmParams p = base_params(ctx);
     p.M = T;
     p.N = d;
@@ -1701,15 +1702,20 @@ int moe_router_backward(moe_ctx* ctx, const float* dlogits, const void* X, const
     p.ld_out = d;
     p.add = dX_in != nullptr;
     const int BN = gemm_bn(d);
+    // CTA pairs on 256 x 256 tiles where the reduction is long and every pair has a tile: see run_dense_add
+    const int pair_tiles = ceil_div(T, 2 * BM) * ceil_div(d, BN);
+    const bool pair = BN == 256 && E > 256 && pair_tiles > ctx->num_sms / 2;
     Maps m = zero_maps();
-    if (!make_map_2d(&m.a0, parts, E, T, E, BM) || !make_map_3d(&m.b0, W_r, E, d, 1, BN) ||
+    if (!make_map_2d(&m.a0, parts, E, T, E, BM) || !make_map_2d(&m.a2, parts + static_cast<size_t>(Tp) * E, E, T, E, BM) ||
+        !make_map_3d(&m.b0, W_r, E, d, 1, pair ? BN / 2 : BN) ||
         !make_store_map_3d(&m.o0, dX, false, d, T, 1, 64) ||
         (dX_in && !make_store_map_3d(&m.o1, const_cast<void*>(dX_in), false, d, T, 1, 64)))
       return MOE_ERR_CUDA;
     m.a1 = m.a0;
+    m.a3 = m.a2;
     m.b1 = m.b0;
-    const int tiles = ceil_div(T, BM) * ceil_div(d, BN);
-    VGG_LAUNCH("router_dx", run_dense_add(BN, p, m, std::min(tiles, ctx->num_sms), s));
+    const int grid = pair ? ctx->num_sms / 2 * 2 : std::min(ceil_div(T, BM) * ceil_div(d, BN), ctx->num_sms);
+    VGG_LAUNCH("router_dx", run_dense_add(BN, pair, p, m, grid, s));
   }
   if (dW_r) {
     // dW_r = dW_r_in + X^T dlogits, split over tokens (rows past T of X are the map's zero fill, of the parts zero)

@@ -57,20 +57,21 @@ enum VarMode { VAR_M = 0, VAR_K = 1, VAR_NONE = 2 };
 // epilogues of the e4m3 form (operands are e4m3 codes of per-row-scaled rows; the accumulator is
 // multiplied by the A row's scale and the output channel's scale first).
 // EPI_DSWIGLU_Q: the dSwiGLU epilogue of the e4m3 form (the accumulator times q_row[row] q_col[column]).
-// EPI_ADD: the plain bf16 epilogue of a dense product with a bf16 matrix (map o1, boxes as the store's) added to it in
-// fp32; N a multiple of 64.
+// EPI_ADD: the plain bf16 epilogue of a dense product (A in two parts) with a bf16 matrix (map o1, boxes as the store's)
+// added to it in fp32; N a multiple of 64.
 // Extra forms (bit flags):
 //   X_DUAL_A  the A operand arrives as a bf16 high part (maps a0/a1) and the bf16 rounding of the rest
 //             (maps a2/a3, the same coordinates); every K step issues two UMMAs into one accumulator, so
 //             the product carries about 16 significant bits of A.  The weight-gradient GEMMs take the
 //             per-pair gradients (fp32 in the dSwiGLU epilogue) this way, the down projection the
-//             activations A (fp32 in the SwiGLU epilogue).
+//             activations A (fp32 in the SwiGLU epilogue), the adding product the logits' gradient.
 //   X_TRANS   varlen-K plain store of the transposed tile: the tile's rows (TMEM lanes) are output
 //             columns, its accumulator columns output rows; each 32 x 32 block is transposed while it is
 //             staged for the TMA store.
 //   X_PAIR    a CTA pair (cluster of 2, cta_group::2) computes a 256-row tile: each CTA loads its 128 rows of A
 //             and half of B's columns, both CTAs' TMA loads complete on the even CTA's barriers, the even CTA
-//             issues the M = 256 UMMAs, and each CTA drains its own 128 TMEM rows (varlen-K with padded B).
+//             issues the M = 256 UMMAs, and each CTA drains its own 128 TMEM rows (varlen-K with padded B, varlen-M and the
+//             adding product with a tiled K-major A).
 //   X_MX      block-scaled e4m3 operands (kind::mxf8f6f4): every 32 codes of an operand row along K carry
 //             one power-of-two scale (UE8M0 byte).  A stage holds, after its A and B tiles, the 4 scale
 //             bytes of each of A's 128 rows and of B's rows (one 512-byte block per 128 rows, the last one
@@ -211,7 +212,7 @@ struct Tile {
 // consecutive column tiles: a work unit is (group, row tile, group of CN column tiles) and the CTA
 // of cluster rank r computes column tile CN * unit_col + r (past the last one it computes nothing
 // that is stored, but still takes part in loading the shared operand).
-// With PAIR (varlen-K) the two CTAs of a cluster take the same tile of 256 rows, rank r rows 128 r ..
+// With PAIR the two CTAs of a cluster take the same tile of 256 rows, rank r rows 128 r ..
 template <int BN, int BMODE, int VAR, int CN = 1, bool PAIR = false>
 struct Sched {
   static constexpr int kColsPerTile = (BMODE == B_TMA_K3_GU) ? BN / 2 : BN;
@@ -274,11 +275,11 @@ struct Sched {
       const int sp = t / per_group;
       const int l = t - sp * per_group;
       // The adding product is bound by what it reads and stores, and whole rows in work at a time serve memory better
-      // than columns of 256 (with the split of dlogits: 32768 x 1536 x 512 88 -> 83 us, 8192 x 7168 x 256 51 -> 49).
+      // than columns of 256 (one part of dlogits, with the split: 32768 x 1536 x 512 88 -> 83 us, 8192 x 7168 x 256 51 -> 49).
       constexpr bool kRows = BMODE == B_TMA_K3;
       const int mt = kRows ? l / ntiles : l % mtiles, nt = kRows ? l % ntiles : l / mtiles;
       tl.g = 0;
-      tl.m0 = mt * BM;
+      tl.m0 = PAIR ? mt * 2 * BM + BM * rank : mt * BM;
       tl.nt = nt;
       tl.n0 = nt * kColsPerTile;
       tl.rows = min(BM, p.M - tl.m0);
@@ -470,7 +471,7 @@ __global__ void __launch_bounds__(WarpPlan<STAGES, EW, AMODE, BMODE, CN, XF>::kT
                 "block-scaled form: BN = 128 or 192, K-major operands, varlen-M plain epilogue kinds or a varlen-K store");
   static_assert(!kMx || 2 * BN + STAGES * (4 + 4 * mx_b_blocks(BN)) <= 512, "block-scaled form: TMEM columns");
   static_assert(EPI != EPI_STORE_Q || !OUTF32, "the e4m3 plain epilogue stores bf16");
-  static_assert(EPI != EPI_ADD || (!OUTF32 && VAR == VAR_NONE && XF == 0), "the adding epilogue: dense, bf16 out");
+  static_assert(EPI != EPI_ADD || (!OUTF32 && VAR == VAR_NONE && (XF & ~X_PAIR) == X_DUAL_A), "the adding epilogue: dense, two-part A, bf16 out");
   static_assert(!kF8 || ((AMODE == A_GATHER_K || AMODE == A_TMA_K) && (BMODE == B_TMA_K3 || BMODE == B_TMA_K3_GU) &&
                          (VAR == VAR_M || kMx)),
                 "e4m3 form: K-major operands, varlen-M (the block-scaled form also varlen-K)");
@@ -492,8 +493,9 @@ __global__ void __launch_bounds__(WarpPlan<STAGES, EW, AMODE, BMODE, CN, XF>::kT
   static_assert(CN == 1 || kPair || (AMODE == A_GATHER_K && VAR == VAR_M && !kBGather), "clusters share a gathered A");
   static_assert(!kPair || (CN == 2 && !kF8 && BN == 256 &&
                             ((VAR == VAR_K && AMODE == A_TMA_MN && BMODE == B_TMA_MN2) ||
-                             (VAR == VAR_M && AMODE == A_TMA_K && (BMODE == B_TMA_K3 || BMODE == B_TMA_MN3)))),
-                "CTA pair: BN = 256, tiled bf16 operands (varlen-K: MN-major A, chunked B; varlen-M: K-major A)");
+                             (VAR == VAR_M && AMODE == A_TMA_K && (BMODE == B_TMA_K3 || BMODE == B_TMA_MN3)) ||
+                             (EPI == EPI_ADD && AMODE == A_TMA_K && BMODE == B_TMA_K3))),
+                "CTA pair: BN = 256, tiled bf16 operands (varlen-K: MN-major A, chunked B; varlen-M: K-major A; the adding product)");
   constexpr bool kRelay = (CN > 1) && !kPair;
   constexpr int kSlice = BM / CN;               // A rows gathered by each CTA of a cluster
   constexpr uint32_t kSliceBytes = kSlice * 128;
@@ -1612,31 +1614,27 @@ cudaError_t launch_grouped_gemm(const GemmParams& p, const Maps& maps, int grid,
   if (grid <= 0) return cudaSuccess;
   const int threads = WarpPlan<STAGES, EW, AMODE, BMODE, CN, XF>::kThreads;
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  if constexpr (EPI == EPI_ADD) {
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(grid, 1, 1);
-    cfg.blockDim = dim3(threads, 1, 1);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, p, maps);
-  }
-  if (CN == 1) {
+  cudaLaunchAttribute attr[2];
+  if (CN == 1 && EPI != EPI_ADD) {
     kern<<<grid, threads, smem, stream>>>(p, maps);
     return cudaGetLastError();
   }
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = CN;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
   cfg.blockDim = dim3(threads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  if (EPI == EPI_ADD) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (CN == 1) {
+    cfg.gridDim = dim3(grid, 1, 1);
+    return cudaLaunchKernelEx(&cfg, kern, p, maps);
+  }
+  attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+  attr[cfg.numAttrs].val.clusterDim.x = CN;
+  attr[cfg.numAttrs].val.clusterDim.y = 1;
+  attr[cfg.numAttrs++].val.clusterDim.z = 1;
   cfg.gridDim = dim3(CN, 1, 1);
   int max_clusters = 0;
   e = cudaOccupancyMaxActiveClusters(&max_clusters, kern, &cfg);

@@ -68,16 +68,18 @@ cudaError_t run_dw_down(int BN, bool f32, const GemmParams& p, const Maps& m, in
              : launch_grouped_gemm<128, 6, 4, 1, A_GATHER_MN, B_TMA_MN2, VAR_K, EPI_STORE, false>(p, m, grid, s);
 }
 
-// Dense A B^T with both operands K-major, plus a bf16 matrix in the epilogue (dX + dlogits W_r^T), as a dependent launch.
-// The reduction over the experts is short, so the product is bound by the passes over [T, d]: a stage of the ring is
-// given up for staging buffers that hold the added matrix's boxes a tile ahead.  With the split of dlogits: eight epilogue
-// warps against four 13.5 against 15.6 us at 4096 x 2048 x 128 and 55 against 67 at 8192 x 7168 x 256; the boxes of two
-// tiles ahead asked into L2 12.7 and 51 (49 with a row's tiles side by side).  CTA pairs (256-row tiles) 14.7 and 64, and 85
-// against 88 at 32768 x 1536 x 512.  A stage of 64 columns takes 96 bytes a cycle out of shared memory and as much
-// into it, and the staged tiles 1 us of that path: the product alone runs at 1.3 PFLOP/s.
-cudaError_t run_dense_add(int BN, const GemmParams& p, const Maps& m, int grid, cudaStream_t s) {
-  if (BN == 256) return launch_grouped_gemm<256, 3, 8, 2, A_TMA_K, B_TMA_K3, VAR_NONE, EPI_ADD, false>(p, m, grid, s);
-  return launch_grouped_gemm<128, 5, 8, 1, A_TMA_K, B_TMA_K3, VAR_NONE, EPI_ADD, false>(p, m, grid, s);
+// Dense A B^T with both operands K-major and A in two bf16 parts, plus a bf16 matrix in the epilogue (dX + dlogits W_r^T), as
+// a dependent launch.  A short reduction leaves the product bound by the passes over [T, d]: shared memory for a stage of
+// the ring is given up for staging buffers that hold the added matrix's boxes a tile ahead (the boxes of two tiles ahead are
+// asked into L2).  A long one is bound by L2: 64 KB for 64 columns of the reduction at 32768 x 1536 x 512 are 9 TB/s, and a
+// CTA pair, which reads W_r's tile once for 256 rows, takes 96 KB for twice the tile.  With the split of dlogits, single and
+// paired: 32768 x 1536 x 512 111 and 97.5 us, 8192 x 2048 x 512 37.2 and 34.2, 4096 x 7168 x 1024 88.8 and 78.4; 8192 x 7168 x
+// 256 59 and 63.5, 8192 x 2048 x 128 18.0 and 21.4; with fewer tiles than pairs (2048 x 2048 x 512) 12.9 and 13.6.
+// One part of dlogits alone takes 82 us at the first size, 10.0 instead of 10.8 at 4096 x 2048 x 128.
+cudaError_t run_dense_add(int BN, bool pair, const GemmParams& p, const Maps& m, int grid, cudaStream_t s) {
+  if (pair) return launch_grouped_gemm<256, 3, 8, 2, A_TMA_K, B_TMA_K3, VAR_NONE, EPI_ADD, false, 2, X_DUAL_A | X_PAIR>(p, m, grid, s);
+  if (BN == 256) return launch_grouped_gemm<256, 2, 8, 2, A_TMA_K, B_TMA_K3, VAR_NONE, EPI_ADD, false, 1, X_DUAL_A>(p, m, grid, s);
+  return launch_grouped_gemm<128, 4, 8, 1, A_TMA_K, B_TMA_K3, VAR_NONE, EPI_ADD, false, 1, X_DUAL_A>(p, m, grid, s);
 }
 
 // Dense A^T B with both operands MN-major (router weight gradient X^T dlogits), split K, fp32 out.

@@ -97,7 +97,7 @@ cudaError_t run_dw_tiled(int BN, bool f32, const GemmParams& p, const Maps& m, i
 cudaError_t run_dw_tiled_trans(int BN, bool f32, const GemmParams& p, const Maps& m, int grid, cudaStream_t s);
 cudaError_t run_dw_dual(int BN, bool f32, bool trans, bool pair, const GemmParams& p, const Maps& m, int grid,
                         cudaStream_t s);
-cudaError_t run_dense_add(int BN, const GemmParams& p, const Maps& m, int grid, cudaStream_t s);
+cudaError_t run_dense_add(int BN, bool pair, const GemmParams& p, const Maps& m, int grid, cudaStream_t s);
 cudaError_t run_dense_mn_store(int BN, const GemmParams& p, const Maps& m, int grid, cudaStream_t s);
 // test exports
 cudaError_t run_test_m(int gathered, int b_kmajor, bool pair, const GemmParams& p, const Maps& m, int grid,
