@@ -121,6 +121,32 @@ def test_router_weight_gradient_to_the_last_bit_of_dlogits(vgg, ctx, T, d, E):
     assert bool(((dX.double() - ref).abs() <= err + 2.0 ** -8 * (ref.abs() + err)).all())
 
 
+def test_router_backward_of_values_at_the_end_of_the_range(vgg, ctx):
+    """An infinite dlogit gives infinities of the products' signs, one above bf16's largest number a finite product."""
+    T, d, E = 70, 192, 64
+    g = gen_of(9)
+
+    def away_from_zero(rows, cols):
+        s = torch.where(torch.rand((rows, cols), device="cuda", generator=g) < 0.5, -1.0, 1.0)
+        return (2.0 ** -10 * s * (1 + torch.rand((rows, cols), device="cuda", generator=g))).to(BF)
+
+    X, W = away_from_zero(T, d), away_from_zero(d, E)
+    dl = torch.zeros((T, E), device="cuda")
+    dl[3, 5], dl[7, 9], dl[11, 2], dl[13, 40] = float("inf"), -float("inf"), 3.4e38, -3.4e38
+    dX, dW = run_router(vgg, ctx, dl, X, W)
+    wx, ww = torch.zeros((T, d), device="cuda", dtype=torch.float64), torch.zeros((d, E), device="cuda", dtype=torch.float64)
+    for t, e in ((3, 5), (7, 9), (11, 2), (13, 40)):
+        wx[t] = dl[t, e].double() * W[:, e].double()
+        ww[:, e] = dl[t, e].double() * X[t].double()
+    for got, want, rel in ((dX, wx, 2.0 ** -8 + 2.0 ** -15), (dW, ww, 8 * U)):
+        fin = want.isfinite()
+        assert torch.equal(got.double()[~fin], want[~fin])
+        assert bool(((got.double() - want).abs()[fin] <= rel * want.abs()[fin]).all())
+    dl[20, 1] = float("nan")
+    dX, dW = run_router(vgg, ctx, dl, X, W)
+    assert dX[20].isnan().all() and dW[:, 1].isnan().all() and not dX[21].isnan().any()
+
+
 # ------------------------------------------------------------------------------------------------ host threads
 
 

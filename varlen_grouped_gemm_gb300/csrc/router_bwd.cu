@@ -10,6 +10,10 @@ namespace {
 // x = hi + mid + lo with hi = bf16(x), mid = bf16(x - hi), lo = bf16(x - hi - mid): three times 8 bits hold an fp32
 // significand, so a product with a bf16 matrix in three bf16 multiplications has fp32 operands' precision (two parts
 // leave 2^-17 of a value, 2.4e-6 normwise, ten times the error of an fp32 product's sums).  parts: [3][np].
+// A value that rounds to infinity has bf16's largest number as its high part, an infinite one no other parts (infinity
+// less itself would make NaN of every product).
+__device__ __forceinline__ float far_high(float x) { return isinf(x) ? x : copysignf(0x1.fep127f, x); }
+__device__ __forceinline__ bool is_far(float x) { return fabsf(x) >= 0x1.ffp127f; }
 __global__ void __launch_bounds__(256) split_dlogits_kernel(const float* __restrict__ dl, long long n, long long np,
                                                             __nv_bfloat16* __restrict__ parts) {
   griddep_launch();
@@ -17,12 +21,20 @@ __global__ void __launch_bounds__(256) split_dlogits_kernel(const float* __restr
   for (long long i = 4ll * (blockIdx.x * static_cast<long long>(blockDim.x) + threadIdx.x); i < np; i += step) {
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (i < n) v = __ldcs(reinterpret_cast<const float4*>(dl + i));
+    const bool far = is_far(v.x) || is_far(v.y) || is_far(v.z) || is_far(v.w);
 #pragma unroll
     for (int p = 0; p < 3; ++p) {
-      const uint2 h = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+      uint2 h = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+      if (p == 0 && far) {
+        const float4 f = make_float4(is_far(v.x) ? far_high(v.x) : v.x, is_far(v.y) ? far_high(v.y) : v.y,
+                                     is_far(v.z) ? far_high(v.z) : v.z, is_far(v.w) ? far_high(v.w) : v.w);
+        h = make_uint2(pack_bf16x2(f.x, f.y), pack_bf16x2(f.z, f.w));
+      }
       *reinterpret_cast<uint2*>(parts + p * np + i) = h;
       const float2 a = unpack_bf16x2(h.x), b = unpack_bf16x2(h.y);
       v = make_float4(v.x - a.x, v.y - a.y, v.z - b.x, v.w - b.y);
+      if (p == 0 && far)
+        v = make_float4(isinf(a.x) ? 0.0f : v.x, isinf(a.y) ? 0.0f : v.y, isinf(b.x) ? 0.0f : v.z, isinf(b.y) ? 0.0f : v.w);
     }
   }
 }
