@@ -1689,7 +1689,8 @@ int moe_router_backward(moe_ctx* ctx, const float* dlogits, const void* X, const
   const int Tp = ceil_div(T, 64) * 64;
   __nv_bfloat16* parts = static_cast<__nv_bfloat16*>(ws);
   float* sums = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + al(sizeof(__nv_bfloat16) * 3 * static_cast<size_t>(Tp) * E));
-  if (T > 0) VGG_LAUNCH("split_dlogits", launch_split_dlogits(dlogits, T, Tp, E, parts, s));
+  // dX reads two parts, dW_r three
+  if (T > 0) VGG_LAUNCH("split_dlogits", launch_split_dlogits(dlogits, T, Tp, E, dW_r ? 3 : 2, parts, s));
   if (T > 0 && dX) {
     // dX = dX_in + (hi + mid) W_r^T: rows of a gradient behind a softmax sum to zero, so what W_r's columns share cancels
     // in the sum but not in the rounding of its terms; two parts leave 2^-16 of a term under a bf16 result

@@ -72,10 +72,11 @@ cudaError_t run_dw_down(int BN, bool f32, const GemmParams& p, const Maps& m, in
 // a dependent launch.  A short reduction leaves the product bound by the passes over [T, d]: shared memory for a stage of
 // the ring is given up for staging buffers that hold the added matrix's boxes a tile ahead (the boxes of two tiles ahead are
 // asked into L2).  A long one is bound by L2: 64 KB for 64 columns of the reduction at 32768 x 1536 x 512 are 9 TB/s, and a
-// CTA pair, which reads W_r's tile once for 256 rows, takes 96 KB for twice the tile.  With the split of dlogits, single and
-// paired: 32768 x 1536 x 512 111 and 97.5 us, 8192 x 2048 x 512 37.2 and 34.2, 4096 x 7168 x 1024 88.8 and 78.4; 8192 x 7168 x
-// 256 59 and 63.5, 8192 x 2048 x 128 18.0 and 21.4; with fewer tiles than pairs (2048 x 2048 x 512) 12.9 and 13.6.
-// One part of dlogits alone takes 82 us at the first size, 10.0 instead of 10.8 at 4096 x 2048 x 128.
+// CTA pair, which reads W_r's tile once for 256 rows, takes 96 KB for twice the tile.  With a split of dlogits into three
+// parts, single and paired: 32768 x 1536 x 512 111 and 97.5 us (91.5 with the two parts that it reads), 8192 x 2048 x 512 37.2
+// and 34.2, 4096 x 7168 x 1024 88.8 and 78.4; 8192 x 7168 x 256 59 and 63.5, 8192 x 2048 x 128 18.0 and 21.4; with fewer tiles
+// than pairs (2048 x 2048 x 512) 12.9 and 13.6.  One part of dlogits alone: 82 us at the first size, 10.0 instead of 10.5 at
+// 4096 x 2048 x 128.
 cudaError_t run_dense_add(int BN, bool pair, const GemmParams& p, const Maps& m, int grid, cudaStream_t s) {
   if (pair) return launch_grouped_gemm<256, 3, 8, 2, A_TMA_K, B_TMA_K3, VAR_NONE, EPI_ADD, false, 2, X_DUAL_A | X_PAIR>(p, m, grid, s);
   if (BN == 256) return launch_grouped_gemm<256, 2, 8, 2, A_TMA_K, B_TMA_K3, VAR_NONE, EPI_ADD, false, 1, X_DUAL_A>(p, m, grid, s);

@@ -254,9 +254,10 @@ size_t balance_ws_bytes(long long T, int E, int B);
 cudaError_t launch_balance_loss(const BalanceArgs& a, void* ws, int num_sms, cudaStream_t s);
 
 // ---- router products -------------------------------------------------------------------------
-// dlogits [T][E] fp32 to three bf16 parts [3][Tp][E] (high part, then the bf16 roundings of what is left), rows past T
-// zero.
-cudaError_t launch_split_dlogits(const float* dlogits, long long T, long long Tp, int E, __nv_bfloat16* parts, cudaStream_t s);
+// dlogits [T][E] fp32 to two or three bf16 parts [nparts][Tp][E] (high part, then the bf16 roundings of what is left), rows
+// past T zero.
+cudaError_t launch_split_dlogits(const float* dlogits, long long T, long long Tp, int E, int nparts, __nv_bfloat16* parts,
+                                 cudaStream_t s);
 // sums[s][e][i] = sum over the split's tokens of dlogits (from its parts) times X; *splits (at most kMaxRouterSplit).
 // Follows launch_split_dlogits (after_split) or run_dense_add after it on the stream.
 constexpr int kMaxRouterSplit = 16;

@@ -9,11 +9,12 @@ namespace {
 
 // x = hi + mid + lo with hi = bf16(x), mid = bf16(x - hi), lo = bf16(x - hi - mid): three times 8 bits hold an fp32
 // significand, so a product with a bf16 matrix in three bf16 multiplications has fp32 operands' precision (two parts
-// leave 2^-17 of a value, 2.4e-6 normwise, ten times the error of an fp32 product's sums).  parts: [3][np].
+// leave 2^-17 of a value, 2.4e-6 normwise, ten times the error of an fp32 product's sums).  parts: [PARTS][np].
 // A value that rounds to infinity has bf16's largest number as its high part, an infinite one no other parts (infinity
 // less itself would make NaN of every product).
 __device__ __forceinline__ float far_high(float x) { return isinf(x) ? x : copysignf(0x1.fep127f, x); }
 __device__ __forceinline__ bool is_far(float x) { return fabsf(x) >= 0x1.ffp127f; }
+template <int PARTS>
 __global__ void __launch_bounds__(256) split_dlogits_kernel(const float* __restrict__ dl, long long n, long long np,
                                                             __nv_bfloat16* __restrict__ parts) {
   griddep_launch();
@@ -23,7 +24,7 @@ __global__ void __launch_bounds__(256) split_dlogits_kernel(const float* __restr
     if (i < n) v = __ldcs(reinterpret_cast<const float4*>(dl + i));
     const bool far = is_far(v.x) || is_far(v.y) || is_far(v.z) || is_far(v.w);
 #pragma unroll
-    for (int p = 0; p < 3; ++p) {
+    for (int p = 0; p < PARTS; ++p) {
       uint2 h = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
       if (p == 0 && far) {
         const float4 f = make_float4(is_far(v.x) ? far_high(v.x) : v.x, is_far(v.y) ? far_high(v.y) : v.y,
@@ -287,9 +288,13 @@ __global__ void __launch_bounds__(256) router_dw_reduce_kernel(const float* __re
 
 }  // namespace
 
-cudaError_t launch_split_dlogits(const float* dlogits, long long T, long long Tp, int E, __nv_bfloat16* parts, cudaStream_t s) {
+cudaError_t launch_split_dlogits(const float* dlogits, long long T, long long Tp, int E, int nparts, __nv_bfloat16* parts,
+                                 cudaStream_t s) {
   const long long np = Tp * E, want = (np / 4 + 255) / 256;
-  if (np > 0) split_dlogits_kernel<<<static_cast<unsigned>(want < 8192 ? want : 8192), 256, 0, s>>>(dlogits, T * E, np, parts);
+  const unsigned grid = static_cast<unsigned>(want < 8192 ? want : 8192);
+  if (np <= 0) return cudaSuccess;
+  if (nparts == 2) split_dlogits_kernel<2><<<grid, 256, 0, s>>>(dlogits, T * E, np, parts);
+  else split_dlogits_kernel<3><<<grid, 256, 0, s>>>(dlogits, T * E, np, parts);
   return cudaGetLastError();
 }
 
