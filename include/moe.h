@@ -520,7 +520,7 @@ int moe_backward_e4m3(moe_ctx* ctx, const void* dO, const void* X, const void* W
  *
  * q_form 0: no codes.  1: scales [T] fp32 = max_j |y[t,j]| / 448 (1 for a zero row), q [T,d] = e4m3(y * (448 / max))
  * with the factor rounded to fp32 once a row (moe_quantize_rows_e4m3 divides every value by the scale: the quotients
- * differ in their last bit at most).  2: scales [T][moe_mx_sf_cols(d)] bytes and q by the rule of
+ * differ by up to 2^-22 of their value).  2: scales [T][moe_mx_sf_cols(d)] bytes and q by the rule of
  * moe_quantize_rows_mx.  Both quantize the fp32 y, not its bf16 rounding.
  *
  * x [T,d] bf16; weight [d] bf16, or fp32 with weight_fp32 != 0; h has the stream's type, y is bf16.  Row strides

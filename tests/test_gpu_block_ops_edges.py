@@ -61,6 +61,32 @@ def test_norm_backward_weight_gradient_begins_at_any_float(vgg, ctx, T, d, res_t
     assert bool((flat[:shift] == 777.0).all()) and bool((flat[shift + d:] == 777.0).all())
 
 
+def e4m3_borders():
+    """Values half way between neighbouring codes of normal size."""
+    return np.array([(2 * m + 1) * 2.0 ** (e - 4) for e in range(-6, 8) for m in range(8, 16) if (2 * m + 1) * 2.0 ** (e - 4) < 440])
+
+
+def test_norm_codes_take_a_factor_that_is_rounded_once(vgg, ctx):
+    """q = e4m3(y f) with f = 448 / max|y| rounded to fp32: values that f brings next to a border between two codes."""
+    d = 512
+    gen = np.random.default_rng(3)
+    res = torch.ones((2, d), device="cuda")
+    res[1, 1::2] = -1.0  # mean square 1, rstd 1: y is the weight itself, up to its sign
+    q, sc = torch.empty((2, d), dtype=U8, device="cuda"), torch.empty(2, device="cuda")
+    sign = f64(res).astype(np.float32)
+    borders = e4m3_borders()
+    for k in range(150):
+        amax = np.float32(gen.uniform(1, 2) * 2.0 ** gen.integers(-20, 20))
+        f = np.float32(448) / amax
+        near = (gen.choice(borders, d) / np.float64(f)).astype(np.float32)
+        w = (near.view(np.int32) + gen.integers(-2, 3, d).astype(np.int32)).view(np.float32)
+        w[0] = amax
+        vgg.moe_add_rmsnorm(ctx, None, res, torch.from_numpy(w).cuda(), 0.0, None, None, None, q, sc)
+        want = torch.from_numpy(sign * w * f).to(torch.float8_e4m3fn).view(U8)
+        assert torch.equal(q.cpu(), want), k
+        assert bool((sc.cpu() == torch.from_numpy(np.array([amax]) / np.float32(448))).all())
+
+
 # ------------------------------------------------------------------------------------------------ router products
 
 

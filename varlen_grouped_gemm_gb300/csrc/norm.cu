@@ -252,10 +252,10 @@ __device__ __forceinline__ void norm_row_codes(const NormFwd& a, const RowOut& o
                                                float amax, Vec8 (&h)[NV]) {
   if constexpr (FORM == NORM_E4M3) {
     if (row_ok && tx == 0) *o.scale = amax > 0.0f ? __fdiv_rn(amax, 448.0f) : 1.0f;
-    // one reciprocal a row; values so small that it would overflow are brought up first
+    // one factor a row; values so small that it would overflow are brought up first
     const bool tiny = amax < 1e-30f;
     const float up = tiny ? 0x1p100f : 1.0f;
-    const float inv = amax > 0.0f ? 448.0f * __frcp_rn(amax * up) : 1.0f;
+    const float inv = amax > 0.0f ? __fdiv_rn(448.0f, amax * up) : 1.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int j = tx + tpr * i;
