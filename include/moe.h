@@ -568,7 +568,8 @@ int moe_add_rmsnorm_backward(moe_ctx* ctx, const void* dy, long long ld_dy, cons
  *
  * (the counts are constants of the gradient).  dloss: a device scalar, NULL for 1.  A balanced load has
  * loss[1] = 1.  A logit may be -infinity (its probability is 0); a token with none above that adds to the counts
- * alone.  No counted token: losses, probabilities and gradients are 0.
+ * alone.  No counted token: losses, probabilities and gradients are 0.  All in fp32: e^(l - max) is off by 3 (max - l)
+ * 2^-24 of its value (its argument's roundings) and two steps, and 0 below 2^-126; the logarithm by one step.
  * logits, dlogits [T,E] fp32; topk_ids [T,K] int32 (an id outside [0, E) records MOE_DEV_BAD_EXPERT and is not
  * counted); mask [T] bytes; seq_offsets [B+1] int32 (not from 0 to T without falling: MOE_DEV_BAD_OFFSETS, the
  * results are then undefined); counts [B,E] int32, probs [B,E] fp32, loss [3] fp32.  1 <= E <= 1024, 1 <= K <= E,

@@ -87,6 +87,31 @@ def test_norm_codes_take_a_factor_that_is_rounded_once(vgg, ctx):
         assert bool((sc.cpu() == torch.from_numpy(np.array([amax]) / np.float32(448))).all())
 
 
+# ------------------------------------------------------------------------------------------------ balance loss
+
+
+@pytest.mark.parametrize("E", [2, 4])
+def test_z_loss_gradient_near_a_log_sum_of_zero(vgg, ctx, E):
+    """Two logits 0 and x < 0: lse = log(1 + e^x).  The sum's rounding is half a step of [1, 2), e^x is off by the
+    argument's roundings (3 |x| u) and two steps, the logarithm by one step of its value."""
+    T = 2000
+    x = -torch.linspace(0.3, 14.0, T, device="cuda")
+    logits = torch.full((T, E), float("-inf"), device="cuda")
+    logits[:, 0], logits[:, 1] = 0.0, x
+    ids = torch.zeros((T, 1), dtype=I32, device="cuda")
+    loss, counts = torch.empty(3, device="cuda"), torch.empty((1, E), dtype=I32, device="cuda")
+    probs, dl = torch.empty((1, E), device="cuda"), torch.empty((T, E), device="cuda")
+    ws = torch.empty(vgg.moe_balance_loss_workspace_bytes(T, E, 1), dtype=U8, device="cuda")
+    vgg.moe_balance_loss(ctx, logits, ids, 0.0, 1.0, loss, counts, probs, dl, ws)
+    x64 = f64(x)
+    small = np.exp(x64)
+    lse, p = np.log1p(small), 1 / (1 + small)
+    lse_abs = (1 + small * (3 * np.abs(x64) + 4) + 2 * lse) * U
+    # p: the sum's error, the quotient (2 steps); the products and the factor 2 / n, half a step each
+    tol = 2 / T * p * (lse_abs + 14 * U * lse)
+    assert np.all(np.abs(f64(dl)[:, 0] - 2 / T * lse * p) <= tol)
+
+
 # ------------------------------------------------------------------------------------------------ router products
 
 

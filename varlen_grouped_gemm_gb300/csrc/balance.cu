@@ -145,7 +145,8 @@ __device__ __forceinline__ float2 block_sum2(float x, float y, float2* red) {
   return s;
 }
 
-// 2^x, at most 2 steps off; results below 2^-126 are 0.
+// 2^x, at most 2 steps off; results below 2^-126 are 0.  As e^(l - m) from x = (l - m) log2 e the three roundings of x come
+// first, 3 (m - l) 2^-24 of the value: an exact exponential of the rounded l - m would keep one of them.
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -385,11 +386,19 @@ __global__ void __launch_bounds__(kBalThreads) balance_kernel(const BalanceArgs 
           dot[g] += __shfl_xor_sync(0xffffffffu, dot[g], o);
         }
       }
+      // The fast logarithm is off by 2^-21.4 near 1, too much for a log-sum that the z loss drives towards 0.  The exact one
+      // is taken once for the UN tokens, each in lanes of its own.
+      float logz = z[0];
+#pragma unroll
+      for (int g = 1; g < UN; ++g)
+        if ((sl & (UN - 1)) == g) logz = z[g];
+      logz = logf(logz);
 #pragma unroll
       for (int g = 0; g < UN; ++g) {
         const int t = tb + g * kTok + sub;
         const float inv = z[g] == 0.0f ? 0.0f : __fdividef(1.0f, z[g]);  // z is between 1 and E
-        const float lse = z[g] == 0.0f ? 0.0f : m[g] + __logf(z[g]);
+        const float lz = __shfl_sync(0xffffffffu, logz, (lane & ~(LPT - 1)) + g);  // (by every lane)
+        const float lse = z[g] == 0.0f ? 0.0f : m[g] + lz;
         dot[g] *= inv;
         if (sl == 0) {
           zs += lse * lse;
