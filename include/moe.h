@@ -528,7 +528,7 @@ int moe_backward_e4m3(moe_ctx* ctx, const void* dO, const void* X, const void* W
  * element is read before it is written).  NULL allowed: x, h (when x is NULL), rstd, and y (when codes are asked
  * for).  1 <= d <= 16384 and any T >= 0 (T = 0 does nothing); d a multiple of 64 and rows 16-byte aligned with codes,
  * else any alignment of the type (d % 8 == 0 with 16-byte aligned rows is fastest).  eps >= 0.
- * Squares are summed in fp32: |h| up to about 1e18.  MOE_ERR_INVALID_ARG on a violated rule.
+ * Squares are summed in fp32: |h| up to 2^63.5 / sqrt(d), 1e17 at d = 16384 (further out rstd and y are 0).  MOE_ERR_INVALID_ARG on a violated rule.
  */
 int moe_add_rmsnorm(moe_ctx* ctx, const void* x, long long ld_x, const void* residual, long long ld_residual,
                     int residual_fp32, const void* weight, int weight_fp32, long long T, int d, float eps, void* h,

@@ -61,6 +61,22 @@ def test_norm_backward_weight_gradient_begins_at_any_float(vgg, ctx, T, d, res_t
     assert bool((flat[:shift] == 777.0).all()) and bool((flat[shift + d:] == 777.0).all())
 
 
+@pytest.mark.parametrize("T,d", [(1, 64), (3, 7168), (2, 16384), (608, 8192), (5, 999), (2, 9001)])
+def test_norm_up_to_the_stated_range(vgg, ctx, T, d):
+    """Squares are summed in fp32: values up to sqrt(2^127 / d)."""
+    g = gen_of(T + d)
+    top = float(np.sqrt(2.0 ** 127 / d))
+    res = torch.where(torch.rand((T, d), device="cuda", generator=g) < 0.5, -top, top) * (1 - 2.0 ** -20)
+    w = torch.ones(d, device="cuda")
+    y, rstd = torch.empty((T, d), dtype=BF, device="cuda"), torch.empty(T, device="cuda")
+    vgg.moe_add_rmsnorm(ctx, None, res, w, 0.0, None, y, rstd)
+    y64, r64 = bo.rmsnorm(f64(res), f64(w), 0.0)
+    # as in test_norm_bf16, and two steps of the root's approximation, which are not refined out there
+    rel = ((16 + 10 + 1 + 2) / 2 + 2 + 4) * U
+    assert np.all(np.abs(f64(rstd) - r64) <= rel * r64)
+    assert np.all(np.abs(f64(y) - y64) <= (2.0 ** -8 + 2 * (rel + 2 * U)) * np.abs(y64))
+
+
 def e4m3_borders():
     """Values half way between neighbouring codes of normal size."""
     return np.array([(2 * m + 1) * 2.0 ** (e - 4) for e in range(-6, 8) for m in range(8, 16) if (2 * m + 1) * 2.0 ** (e - 4) < 440])
