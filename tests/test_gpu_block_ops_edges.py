@@ -188,6 +188,23 @@ def test_router_weight_gradient_to_the_last_bit_of_dlogits(vgg, ctx, T, d, E):
     assert bool(((dX.double() - ref).abs() <= err + 2.0 ** -8 * (ref.abs() + err)).all())
 
 
+@pytest.mark.parametrize("T,d,E", ROUTER_SIZES)
+def test_router_weight_gradient_has_fp32_precision_beside_the_other_product(vgg, ctx, T, d, E):
+    """As test_router_weight_gradient_has_fp32_precision, with both products and both added matrices."""
+    g = gen_of(T + d + 2 * E)
+    dl = torch.randn((T, E), device="cuda", generator=g)
+    X = torch.randn((T, d), device="cuda", generator=g).to(BF)
+    W = (torch.randn((d, E), device="cuda", generator=g) / d ** 0.5).to(BF)
+    dX_in = torch.randn((T, d), device="cuda", generator=g).to(BF)
+    dW_in = torch.randn((d, E), device="cuda", generator=g)
+    _, dW = run_router(vgg, ctx, dl, X, W, dX_in, dW_in)
+    prod, mag = X.double().T @ dl.double(), X.double().abs().T @ dl.double().abs()
+    err = (dW.double() - dW_in.double() - prod).abs()
+    assert bool((err <= (1 + 48 + T / 128 + 16 + 2) * U * mag + 2 * U * dW_in.double().abs()).all())
+    assert float(torch.linalg.norm(err)) <= 2.0 ** -20 * float(torch.linalg.norm(prod)) + \
+        U * float(torch.linalg.norm(dW_in))
+
+
 def test_router_backward_of_values_at_the_end_of_the_range(vgg, ctx):
     """An infinite dlogit gives infinities of the products' signs, one above bf16's largest number a finite product."""
     T, d, E = 70, 192, 64
