@@ -128,13 +128,13 @@ def kernel_work(wl, P, dW_bytes=2):
                        2 * P * d + 8 * P * n + 2 * dWb * E * n * d),
         "dw_down": (2 * P * d * n, 2 * T * d + 2 * P * n + dWb * E * d * n, 2 * P * d + 4 * P * n + dWb * E * d * n),
         # around the layer (outside the step): the norm with per-row codes and its backward on a bf16 stream, the
-        # balance loss with its gradient, the router's products for it (dlogits as bf16 parts)
+        # balance loss with its gradient, the router's products for it (dlogits as three bf16 parts, dX takes two)
         "add_rmsnorm": same(6 * T * d, 9 * T * d + 8 * T + 2 * d),
         "add_rmsnorm_bwd": same(12 * T * d, 8 * T * d + 4 * T + 6 * d),
         "balance_loss": same(12 * T * E, 8 * T * E + 4 * T * K + 8 * E),
-        "split_dlogits": same(0, 8 * T * E),
-        "router_dx": same(2 * T * d * E, 2 * T * E + 2 * d * E + 4 * T * d),
-        "router_dw": same(4 * T * d * E, 2 * T * d + 4 * T * E + 4 * d * E),
+        "split_dlogits": same(0, 10 * T * E),
+        "router_dx": same(4 * T * d * E, 4 * T * E + 2 * d * E + 4 * T * d),
+        "router_dw": same(6 * T * d * E, 2 * T * d + 6 * T * E + 4 * d * E),
         "router_dw_reduce": same(0, 12 * d * E),
     }
 
