@@ -1532,7 +1532,7 @@ int moe_add_rmsnorm(moe_ctx* ctx, const void* x, long long ld_x, const void* res
   VGG_REQUIRE(weight && (h || !x) && (y || q_form) && (!q_form || (q && scales)));
   VGG_REQUIRE(rows_ok(x, ld_x, d, 2, false) && rows_ok(residual, ld_residual, d, es, true) &&
               rows_ok(h, ld_h, d, es, false) && rows_ok(y, ld_y, d, 2, false));
-  VGG_REQUIRE(reinterpret_cast<uintptr_t>(weight) % (weight_fp32 ? 4 : 2) == 0);
+  VGG_REQUIRE(reinterpret_cast<uintptr_t>(weight) % (weight_fp32 ? 4 : 2) == 0 && reinterpret_cast<uintptr_t>(rstd) % 4 == 0);
   const bool vec = d % 8 == 0 && rows_vec(x, ld_x) && rows_vec(residual, ld_residual) && rows_vec(h, ld_h) &&
                    rows_vec(y, ld_y) && aligned16(weight);
   VGG_REQUIRE(!q_form || (vec && aligned16(q) && (q_form == 2 || reinterpret_cast<uintptr_t>(scales) % 4 == 0)));
