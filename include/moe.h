@@ -27,7 +27,8 @@
  *   default stream) and returns a host-side status.  Argument errors
  *   (NULL pointers, sizes out of range, d or n not multiples of 64,
  *   misaligned pointers) return MOE_ERR_INVALID_ARG before anything is
- *   launched; a failed launch returns MOE_ERR_CUDA.
+ *   launched; a failed launch, or a device that cannot be made current,
+ *   returns MOE_ERR_CUDA.
  * - Errors found on the device (an expert id out of range, corrupt offsets,
  *   a pair count beyond capacity, a bounded wait that timed out) never trap:
  *   the kernel records a code in the context's error word and returns early.

@@ -385,7 +385,7 @@ int vgg::permute_plain_with_scratch(moe_ctx* ctx, const int32_t* topk_ids, const
   const int nb = (T + tb - 1) / tb;
   if (static_cast<long long>(E + 1) * nb + 2 > scratch_ints) return MOE_ERR_UNSUPPORTED;
   DeviceGuard g(ctx->device);
-  VGG_REQUIRE(g.ok);
+  if (!g.ok) return MOE_ERR_CUDA;
   PermuteWs w{};
   w.hist = scratch;
   w.tokblk = scratch + static_cast<long long>(E) * nb;
@@ -521,7 +521,7 @@ int moe_route(moe_ctx* ctx, const void* X, const void* W_r, const float* bias, i
   VGG_REQUIRE(shapes_ok(T, d, E, 64, K));
   VGG_REQUIRE(aligned16(X) && aligned16(W_r) && aligned16(logits));
   DeviceGuard g(ctx->device);
-  VGG_REQUIRE(g.ok);
+  if (!g.ok) return MOE_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   int split = route_split(T, d, E, ctx->num_sms);
   // without room in the caller's workspace the GEMM writes the logits (plus bias) itself
@@ -567,7 +567,7 @@ int moe_permute(moe_ctx* ctx, const int32_t* topk_ids, const float* topk_w, cons
     if (T > 32768) return MOE_ERR_UNSUPPORTED;
   }
   DeviceGuard g(ctx->device);
-  VGG_REQUIRE(g.ok);
+  if (!g.ok) return MOE_ERR_CUDA;
   PermuteWs w = carve_permute_ws(ws, T, E, K, m_tile);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   VGG_LAUNCH("permute", launch_permute(topk_ids, topk_w, logits, scores, T, E, K, m_tile, cap, counts, offsets,
@@ -589,7 +589,7 @@ int moe_permute_capacity(moe_ctx* ctx, const int32_t* topk_ids, const float* top
   VGG_REQUIRE((reinterpret_cast<uintptr_t>(ws) & (kAlign - 1)) == 0);
   if (T > 32768) return MOE_ERR_UNSUPPORTED;
   DeviceGuard g(ctx->device);
-  VGG_REQUIRE(g.ok);
+  if (!g.ok) return MOE_ERR_CUDA;
   PermuteWs w = carve_permute_ws(ws, T, E, K, 1);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   VGG_LAUNCH("permute", launch_permute_capacity(topk_ids, topk_w, T, E, K, C, policy, cap, counts, offsets,
@@ -618,7 +618,7 @@ int moe_grouped_gemm_fwd(moe_ctx* ctx, const void* X, const void* W_gate, const 
   VGG_REQUIRE(aligned16(X) && aligned16(W_gate) && aligned16(W_up) && aligned16(W_down) && aligned16(H) &&
               aligned16(U) && aligned16(A) && aligned16(Yw));
   DeviceGuard g(ctx->device);
-  VGG_REQUIRE(g.ok);
+  if (!g.ok) return MOE_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   void* A_lo = ws;
   // gate/up + SwiGLU: A = X rows gathered by sorted_tok, B = the W_gate / W_up pair
@@ -658,7 +658,7 @@ int moe_quantize_rows_e4m3(moe_ctx* ctx, const void* M, long long rows, int cols
   VGG_REQUIRE(rows >= 0 && rows <= (1ll << 31) && cols >= 16 && cols % 16 == 0);
   VGG_REQUIRE(aligned16(M) && aligned16(q));
   DeviceGuard g(ctx->device);
-  VGG_REQUIRE(g.ok);
+  if (!g.ok) return MOE_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   VGG_LAUNCH("quantize_e4m3", launch_quantize_rows_e4m3(static_cast<const __nv_bfloat16*>(M), rows, nullptr, cols,
                                                         static_cast<uint8_t*>(q), scales, s));
@@ -681,7 +681,7 @@ int moe_grouped_gemm_fwd_e4m3(moe_ctx* ctx, const void* Xq, const float* x_scale
   VGG_REQUIRE(aligned16(Xq) && aligned16(Wg_q) && aligned16(Wu_q) && aligned16(W_down) && aligned16(H) &&
               aligned16(U) && aligned16(A) && aligned16(Yw));
   DeviceGuard g(ctx->device);
-  VGG_REQUIRE(g.ok);
+  if (!g.ok) return MOE_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   {
     // e4m3 rows are handed to TMA and to the gather as rows of d / 2 16-bit units (code pairs): the
@@ -817,7 +817,7 @@ int moe_quantize_rows_mx(moe_ctx* ctx, const void* M, long long rows, int cols, 
   VGG_REQUIRE(rows >= 0 && rows <= (1ll << 31) && cols >= 64 && cols % 64 == 0);
   VGG_REQUIRE(aligned16(M) && aligned16(q) && (reinterpret_cast<uintptr_t>(sf) & 3u) == 0);
   DeviceGuard g(ctx->device);
-  VGG_REQUIRE(g.ok);
+  if (!g.ok) return MOE_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   VGG_LAUNCH("quantize_mx", launch_quantize_rows_mx(static_cast<const __nv_bfloat16*>(M), rows, nullptr, cols,
                                                     static_cast<uint8_t*>(q), static_cast<uint8_t*>(sf),
@@ -833,7 +833,7 @@ int moe_quantize_weights_mx(moe_ctx* ctx, const void* W_gate, const void* W_up, 
   VGG_REQUIRE(aligned16(W_gate) && aligned16(W_up) && aligned16(W_down) && aligned16(Wg_q) && aligned16(Wu_q) &&
               aligned16(gu_sf) && aligned16(Wd_q) && aligned16(dn_sf));
   DeviceGuard g(ctx->device);
-  VGG_REQUIRE(g.ok);
+  if (!g.ok) return MOE_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   // every entry of the blocks that no operand row or column fills holds scale 1
   VGG_CUDA(cudaMemsetAsync(gu_sf, 127, static_cast<size_t>(moe_mx_weight_sf_bytes(E, d, n, 0)), s));
@@ -865,7 +865,7 @@ int moe_grouped_gemm_fwd_mx(moe_ctx* ctx, const void* Xq, const void* x_sf, cons
               aligned16(Wu_q) && aligned16(gu_sf) && aligned16(Wd_q) && aligned16(dn_sf) && aligned16(H) &&
               aligned16(U) && aligned16(x_sf_tiles) && aligned16(Aq) && aligned16(a_sf) && aligned16(Yw));
   DeviceGuard g(ctx->device);
-  VGG_REQUIRE(g.ok);
+  if (!g.ok) return MOE_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int dk = d / 2, nk = n / 2;  // e4m3 rows as 16-bit units (code pairs) for TMA and the gather
   // the gathered X rows' scales, laid out per sorted row tile and stage of K as the GEMM's producer loads them
@@ -934,7 +934,7 @@ int moe_combine(moe_ctx* ctx, const void* Yw, const int32_t* tok_ptr, const int3
   VGG_REQUIRE(T >= 1 && T <= 65536 && d >= 8 && d % 8 == 0 && cap >= 1);
   VGG_REQUIRE(aligned16(Yw) && aligned16(O));
   DeviceGuard g(ctx->device);
-  VGG_REQUIRE(g.ok);
+  if (!g.ok) return MOE_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   VGG_LAUNCH("combine", launch_combine(static_cast<const __nv_bfloat16*>(Yw), tok_ptr, tok_pairs, T, d, cap,
                                        static_cast<__nv_bfloat16*>(O), ctx->d_err, s));
@@ -979,7 +979,7 @@ static int backward_impl(moe_ctx* ctx, const void* dO, const void* X, const void
               aligned16(W_down) && aligned16(H) && aligned16(U) && aligned16(dX) && aligned16(dW_gate) &&
               aligned16(dW_up) && aligned16(dW_down) && aligned16(dW_r));
   DeviceGuard g(ctx->device);
-  VGG_REQUIRE(g.ok);
+  if (!g.ok) return MOE_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   BwdWs w = carve_bwd(ws, T, d, E, n, cap);
   const bool f32 = dW_fp32 != 0;
@@ -1457,7 +1457,7 @@ int moe_quantize_bwd_weights_mx(moe_ctx* ctx, const void* W_gate, const void* W_
   VGG_REQUIRE(aligned16(W_gate) && aligned16(W_up) && aligned16(W_down) && aligned16(tmp) && aligned16(Wdt_q) &&
               aligned16(wdt_sf) && aligned16(Wgu_q) && aligned16(wgu_sf));
   DeviceGuard g(ctx->device);
-  VGG_REQUIRE(g.ok);
+  if (!g.ok) return MOE_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   __nv_bfloat16* t = static_cast<__nv_bfloat16*>(tmp);
   const int bn = mx_tile_cols(n), bd = mx_tile_cols(d);
@@ -1486,7 +1486,7 @@ int moe_quantize_dact_weights_e4m3(moe_ctx* ctx, const void* W_down, int E, int 
   VGG_REQUIRE(shapes_ok(1, d, E, n, 1));
   VGG_REQUIRE(aligned16(W_down) && aligned16(tmp) && aligned16(Wdt_q));
   DeviceGuard g(ctx->device);
-  VGG_REQUIRE(g.ok);
+  if (!g.ok) return MOE_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   __nv_bfloat16* t = static_cast<__nv_bfloat16*>(tmp);
   VGG_LAUNCH("quantize_e4m3", launch_transpose_into_bf16(static_cast<const __nv_bfloat16*>(W_down), E, d, n, t, d, 0,
@@ -1502,7 +1502,7 @@ int moe_quantize_dx_weights_e4m3(moe_ctx* ctx, const void* W_gate, const void* W
   VGG_REQUIRE(shapes_ok(1, d, E, n, 1));
   VGG_REQUIRE(aligned16(W_gate) && aligned16(W_up) && aligned16(tmp) && aligned16(Wgu_q));
   DeviceGuard g(ctx->device);
-  VGG_REQUIRE(g.ok);
+  if (!g.ok) return MOE_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   __nv_bfloat16* t = static_cast<__nv_bfloat16*>(tmp);
   VGG_LAUNCH("quantize_e4m3", launch_transpose_into_bf16(static_cast<const __nv_bfloat16*>(W_gate), E, n, d, t, 2 * n,
@@ -1537,7 +1537,7 @@ int moe_add_rmsnorm(moe_ctx* ctx, const void* x, long long ld_x, const void* res
                    rows_vec(y, ld_y) && aligned16(weight);
   VGG_REQUIRE(!q_form || (vec && aligned16(q) && (q_form == 2 || reinterpret_cast<uintptr_t>(scales) % 4 == 0)));
   DeviceGuard g(ctx->device);
-  VGG_REQUIRE(g.ok);
+  if (!g.ok) return MOE_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   NormFwd a{};
   a.x = x;
@@ -1590,7 +1590,7 @@ int moe_add_rmsnorm_backward(moe_ctx* ctx, const void* dy, long long ld_dy, cons
   const bool vec = d % 8 == 0 && rows_vec(dy, ld_dy) && rows_vec(h, ld_h) && rows_vec(dh, ld_dh) && rows_vec(dx, ld_dx) &&
                    rows_vec(dresidual, ld_dresidual) && aligned16(weight);
   DeviceGuard g(ctx->device);
-  VGG_REQUIRE(g.ok);
+  if (!g.ok) return MOE_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   NormBwd a{};
   a.dy = dy;
@@ -1639,7 +1639,7 @@ int moe_balance_loss(moe_ctx* ctx, const float* logits, const int32_t* topk_ids,
     VGG_REQUIRE(reinterpret_cast<uintptr_t>(p) % 4 == 0);
   VGG_REQUIRE(ws && (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1)) == 0 && ws_bytes >= balance_ws_bytes(T, E, B));
   DeviceGuard g(ctx->device);
-  VGG_REQUIRE(g.ok);
+  if (!g.ok) return MOE_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   BalanceArgs a{};
   a.logits = logits;
@@ -1684,7 +1684,7 @@ int moe_router_backward(moe_ctx* ctx, const float* dlogits, const void* X, const
               ws_bytes >= moe_router_backward_workspace_bytes(T, d, E));
   if (T == 0 && !dW_r) return MOE_OK;
   DeviceGuard g(ctx->device);
-  VGG_REQUIRE(g.ok);
+  if (!g.ok) return MOE_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int Tp = ceil_div(T, 64) * 64;
   __nv_bfloat16* parts = static_cast<__nv_bfloat16*>(ws);
@@ -1736,7 +1736,7 @@ int moe_test_gemm_varlen_m(moe_ctx* ctx, const void* A, const int32_t* idx, cons
   VGG_REQUIRE(G >= 1 && G <= kMaxGroups && rows_a >= 1 && K >= 64 && K % 64 == 0 && N >= 8 && N % 8 == 0);
   VGG_REQUIRE(cap >= 1 && cap < INT_MAX && aligned16(A) && aligned16(B) && aligned16(D));
   DeviceGuard g(ctx->device);
-  VGG_REQUIRE(g.ok);
+  if (!g.ok) return MOE_ERR_CUDA;
   GemmParams p = base_params(ctx);
   p.N = N;
   p.K = K;
@@ -1773,7 +1773,7 @@ int moe_test_gemm_varlen_m_dual(moe_ctx* ctx, const void* A_hi, const void* A_lo
   VGG_REQUIRE(cap >= 1 && cap < INT_MAX && rows_a >= cap && aligned16(A_hi) && aligned16(A_lo) && aligned16(B) &&
               aligned16(D));
   DeviceGuard g(ctx->device);
-  VGG_REQUIRE(g.ok);
+  if (!g.ok) return MOE_ERR_CUDA;
   GemmParams p = base_params(ctx);
   p.N = N;
   p.K = K;
@@ -1802,7 +1802,7 @@ int moe_test_gemm_varlen_k(moe_ctx* ctx, const void* A, const int32_t* idx_a, in
               rows_b >= 1);
   VGG_REQUIRE(cap >= 1 && cap < INT_MAX && aligned16(A) && aligned16(B) && aligned16(D));
   DeviceGuard g(ctx->device);
-  VGG_REQUIRE(g.ok);
+  if (!g.ok) return MOE_ERR_CUDA;
   GemmParams p = base_params(ctx);
   p.M = M;
   p.N = N;
@@ -1843,7 +1843,7 @@ int moe_test_gemm_varlen_k_dual(moe_ctx* ctx, const void* A_hi, const void* A_lo
               rows_b >= 1);
   VGG_REQUIRE(cap >= 1 && cap < INT_MAX && aligned16(A_hi) && aligned16(A_lo) && aligned16(B) && aligned16(D));
   DeviceGuard g(ctx->device);
-  VGG_REQUIRE(g.ok);
+  if (!g.ok) return MOE_ERR_CUDA;
   GemmParams p = base_params(ctx);
   p.M = M;
   p.N = N;
@@ -1903,7 +1903,7 @@ int moe_profile_read(moe_ctx* ctx, int max_kernels, char* names, double* total_m
 int moe_test_wait_timeout(moe_ctx* ctx, unsigned long long timeout_ns, moe_stream_t stream) {
   VGG_REQUIRE(ctx && timeout_ns > 0 && timeout_ns <= 10000000000ull);
   DeviceGuard g(ctx->device);
-  VGG_REQUIRE(g.ok);
+  if (!g.ok) return MOE_ERR_CUDA;
   return cuda_status(launch_wait_timeout_probe(ctx->d_err, timeout_ns, static_cast<cudaStream_t>(stream)));
 }
 
