@@ -16,9 +16,11 @@
 // chunk crosses into another sequence it closes a piece.  The piece of (chunk c, sequence b) has the index c + b,
 // unique because every next piece moves on by a chunk, a sequence or both.  Sums over tokens run in a fixed order,
 // so equal calls give equal bits.
-// 64 x 8 7.5 us and 4096 x 128 11.1 us (the phases' latency and the barriers between them); 32768 x 512 in 37
-// sequences 39.8 us (135 MB, 20 us of them): launch and clearing 3, counting under the first loads 6, barriers 3, blocks
-// that memory serves unevenly 5, the last phase 3.
+// 64 x 8 7.8 us and 4096 x 128 11.5 us (the phases' latency and the barriers between them); 32768 x 512 in 37
+// sequences 40.3 us (135 MB, 20 us of them): launch and clearing 3, counting under the first loads 6, barriers 3, blocks
+// that memory serves unevenly 5, the last phase 3.  Without the gradient 26 us there (35 with it for sequences of one length
+// and no mask), 10.9 us at 4096 x 128.  The widest form (513 to 1024 experts) spills 104 bytes at the 128 registers that 512
+// threads leave it: 16384 x 1024 35.9 us.
 #include "internal.h"
 
 namespace vgg {

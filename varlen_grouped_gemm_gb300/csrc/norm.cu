@@ -288,7 +288,8 @@ __device__ __forceinline__ void norm_row_codes(const NormFwd& a, const RowOut& o
   }
 }
 
-// blockDim.y rows a block.
+// blockDim.y rows a block.  32 registers keep 2048 threads on an SM; the fp32 stream with per-row codes spills 20 bytes
+// for that (32768 x 1536 107.0 us, with 40 registers and none 108.1; 8192 x 4096 77.1 and 80.2).
 template <int NV, bool RES32, int FORM>
 __global__ void __launch_bounds__(1024, NV == 1 ? 2 : 1) add_rmsnorm_kernel(const NormFwd a) {
   __shared__ float red_sum[32], red_max[32];
@@ -363,7 +364,7 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_any_kernel(const NormFwd a) 
 // A row group takes rows whose numbers differ by multiples of eight, so that its phase, and with it every thread's
 // columns, stay the same: the weight's vector is read once, and the backward's share of dg stays in registers.  The next
 // row's loads are on their way while a row is reduced.
-// Against the kernels that load a value at a time: 8192 x 4001 bf16 forward 48 us and 161 (196 MB, 39 us of them), backward
+// Against the kernels that load a value at a time: 8192 x 4001 bf16 forward 48 us and 161 (262 MB, 39 us of them), backward
 // 70 and 495; 16384 x 999 26 and 72, 42 and 740; 300 x 1501 3.1 and 8.2, 7.0 and 17.6.  One tensor out of phase: 61 and 95
 // us at 8192 x 4001.
 struct Phase {
@@ -886,7 +887,8 @@ __global__ void __launch_bounds__(512) add_rmsnorm_bwd_any_kernel(const NormBwd 
   }
 }
 
-// Rows that start anywhere (see the forward).
+// Rows that start anywhere (see the forward).  1024 threads of 64 registers an SM: the bf16 form spills 36 bytes and takes
+// 72 us at 8192 x 4001, without spills in 80 registers, and fewer rows in work, 89.
 template <bool RES32>
 __global__ void __launch_bounds__(1024) add_rmsnorm_bwd_phase_kernel(const NormBwd a, Phase f) {
   extern __shared__ __align__(16) float4 weights[];  // every thread's, which registers have no room for; then the shares

@@ -1,5 +1,5 @@
 // The router's products for an additional logit gradient: dlogits into three bf16 parts, dW_r = X^T dlogits from them
-// (dX = dlogits W_r^T runs on the shared GEMM template).  The launches of one call follow one another as dependent
+// (dX = dlogits W_r^T runs on the shared GEMM template, on two of them).  The launches of one call follow one another as dependent
 // launches: each sets itself up while the one ahead of it drains.
 #include "internal.h"
 
