@@ -97,6 +97,11 @@ def _normal(gen, *shape, std=1.0):
     return out
 
 
+def _ratio(v, c):
+    """v / c as one fp32 division: of a number torch multiplies by the reciprocal, and bf16 quotients meet ties."""
+    return torch.div(v, torch.full_like(v, c))
+
+
 def _row_codes(W):
     """e4m3 codes and the scale of each row, as the framework's per-row form has them; by slices of the first axis."""
     q = torch.empty(W.shape, dtype=torch.uint8, device=W.device)
@@ -104,7 +109,7 @@ def _row_codes(W):
     for i in range(0, W.shape[0], 16):
         w = W[i:i + 16].float()
         top = w.abs().amax(-1)
-        s[i:i + 16] = torch.where(top > 0, top / 448.0, torch.ones_like(top))
+        s[i:i + 16] = torch.where(top > 0, _ratio(top, 448.0), torch.ones_like(top))
         q[i:i + 16] = (w / s[i:i + 16, ..., None]).to(E4M3).view(torch.uint8)
     return q, s
 
@@ -112,7 +117,7 @@ def _row_codes(W):
 def _kept(v):
     """8-bit codes and bf16 scales of 32 columns each: scale = max|v| / 127 rounded up to bf16 (at least 2^-126)."""
     b = v.unflatten(-1, (-1, 32))
-    bits = (b.abs().amax(-1) / 127.0).clamp(min=2.0 ** -126).view(I32)
+    bits = _ratio(b.abs().amax(-1), 127.0).clamp(min=2.0 ** -126).view(I32)
     scale = ((bits + 0xFFFF) & ~0xFFFF).view(F32)
     q = torch.round(b * (1.0 / scale)[..., None]).to(torch.int8).flatten(-2)
     return q, scale.to(BF)
@@ -192,7 +197,7 @@ def prepare(case, seed):
 def _plain_codes(v):
     """Per-row e4m3 values of fp32 rows, and their scales."""
     top = v.abs().amax(-1, keepdim=True)
-    scale = torch.where(top > 0, top / 448.0, torch.ones_like(top))
+    scale = torch.where(top > 0, _ratio(top, 448.0), torch.ones_like(top))
     return (v / scale).to(E4M3).float(), scale
 
 
@@ -381,10 +386,10 @@ def _exact_logits(s):
 
 
 def _exact_quantize(v):
-    """The values of v's per-row codes: v holds bf16 values, and the rule divides in fp32 (bf16 quotients meet ties)."""
+    """The values of v's per-row codes: v holds bf16 values, and the rule divides in fp32."""
     v = v.float()
     top = torch.linalg.vector_norm(v, ord=float("inf"), dim=-1, keepdim=True)
-    scale = torch.where(top > 0, top / 448.0, torch.ones_like(top))
+    scale = torch.where(top > 0, _ratio(top, 448.0), torch.ones_like(top))
     return torch.div(v, scale).to(E4M3).double() * scale.double()
 
 
