@@ -605,6 +605,41 @@ int moe_router_backward(moe_ctx* ctx, const float* dlogits, const void* X, const
                         moe_stream_t stream);
 
 /*
+ * moe_forward_few — the whole layer for the few tokens of a decoding step (1 to 64), in two launches: router product;
+ * choice, the chosen experts' three products and the weighted sums.  The pages describe no such call (their inference
+ * path is out of the benchmark's scope); it is an addition of this library.  It computes what moe_route, moe_permute,
+ * moe_grouped_gemm_fwd and moe_combine compute, with fewer roundings (the experts' weighted outputs are added in fp32 and
+ * rounded once):
+ *
+ *   logits = X W_r + bias;  topk_ids[t,:], topk_w[t,:] by the rule of moe_route
+ *   O[t] = sum_k topk_w[t,k] (silu(X[t] W_gate[e]^T) * (X[t] W_up[e]^T)) W_down[e]^T,  e = topk_ids[t,k]
+ *
+ * Each chosen expert's weights are read once, an expert that no token chose not at all.
+ *
+ * X [T,d] bf16 with row stride ld_x >= d (a multiple of 8), O [T,d] bf16 with row stride ld_o >= d (a multiple of 4);
+ * weights, bias (or NULL) and shape rules as moe_route and moe_grouped_gemm_fwd; topk_ids [T,K] int32, topk_w [T,K] fp32.
+ * 0 <= T <= 64 (T = 0 does nothing).  X, W_r and the weights 16-byte aligned, O 8-byte.  ws: caller-owned, 256-byte
+ * aligned, at least moe_few_workspace_bytes(T, d, E, n, K) bytes (0 on bad sizes); calls that may overlap need one each.
+ * The second launch is cooperative (all of its blocks resident at once; their waits for one another are bounded by
+ * moe_set_wait_timeout, one that gives up records MOE_DEV_TIMEOUT and leaves O undefined).  Sums run in a fixed order:
+ * the same call gives the same bits on the same GPU.
+ */
+size_t moe_few_workspace_bytes(int T, int d, int E, int n, int K);
+int moe_forward_few(moe_ctx* ctx, const void* X, long long ld_x, const void* W_r, const float* bias, const void* W_gate,
+                    const void* W_up, const void* W_down, int T, int d, int E, int n, int K, int32_t* topk_ids,
+                    float* topk_w, void* O, long long ld_o, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * moe_forward_few_e4m3 — the same on e4m3 weights: Wg_q, Wu_q [E,n,d], Wd_q [E,d,n] with wg_scale, wu_scale [E,n], wd_scale
+ * [E,d] as moe_grouped_gemm_fwd_e4m3 takes them (moe_quantize_rows_e4m3).  The call quantizes X per token and A, rounded to
+ * bf16, per pair by the rule of moe_quantize_rows_e4m3; the router takes X and W_r in bf16.
+ */
+int moe_forward_few_e4m3(moe_ctx* ctx, const void* X, long long ld_x, const void* W_r, const float* bias, const void* Wg_q,
+                         const float* wg_scale, const void* Wu_q, const float* wu_scale, const void* Wd_q,
+                         const float* wd_scale, int T, int d, int E, int n, int K, int32_t* topk_ids, float* topk_w, void* O,
+                         long long ld_o, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/*
  * Per-kernel timing (tracing).  With profiling enabled, every kernel the
  * library launches is bracketed by a CUDA event pair on its stream (events
  * come from a pool created by the first moe_profile_enable).  moe_profile_read

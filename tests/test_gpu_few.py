@@ -1,0 +1,167 @@
+"""The layer for a few tokens against a plain implementation in 64 bits.
+
+What a result may be off, from the formats alone.  The choice and its weights are compared on logits that lie further
+apart than fp32 tells apart.  A sum of k products in fp32 is off by at most k 2^-23 of the sum of their magnitudes (half a
+step a rounding, twice that where the tensor core truncates); the sigmoid by 2^-20 of its value.  bf16: A's two parts leave
+2^-16 of a value.  e4m3: A's codes are those of some A within its bound, so the bound of the sum holds the spread of
+the codes (the rule is monotone in A; where the row's largest value itself may round either way, a whole step, 2^-3 of
+each).  O adds half a bf16 step, 2^-8."""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+BF, F32, F64, I32 = torch.bfloat16, torch.float32, torch.float64, torch.int32
+E4M3 = torch.float8_e4m3fn
+
+
+@pytest.fixture(scope="module")
+def vgg():
+    import varlen_grouped_gemm_gb300 as m
+    return m
+
+
+@pytest.fixture(scope="module")
+def ctx(vgg):
+    return vgg.Context(0)
+
+
+def make(T, d, E, n, K, seed=0, bias=None):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+
+    def normal(*shape, std):
+        return (torch.randn(shape, device="cuda", generator=g) * std).to(BF)
+
+    s = dict(X=normal(T, d, std=1.0), W_r=normal(d, E, std=d ** -0.5), W_gate=normal(E, n, d, std=d ** -0.5),
+             W_up=normal(E, n, d, std=d ** -0.5), W_down=normal(E, d, n, std=n ** -0.5), bias=None, K=K)
+    if bias == "normal":
+        s["bias"] = 0.5 * torch.randn(E, device="cuda", generator=g)
+    elif bias == "few":  # every token prefers the same K experts
+        s["bias"] = torch.zeros(E, device="cuda")
+        s["bias"][E // 2:E // 2 + K] = 40.0
+    separate(s)
+    return s
+
+
+def logits64(s):
+    v = s["X"].double() @ s["W_r"].double()
+    return v if s["bias"] is None else v + s["bias"].double()
+
+
+def separate(s):
+    """Tokens whose choice fp32 could not decide take the clearest token's X."""
+    E, K = s["W_r"].shape[1], s["K"]
+    if E == 1 or s["X"].shape[0] == 0:
+        return
+    top = torch.topk(logits64(s), min(K + 1, E), dim=1).values
+    gap = (top[:, :-1] - top[:, 1:]).amin(1)
+    s["X"] = torch.where((gap > 1e-4)[:, None], s["X"], s["X"][gap.argmax()]).contiguous()
+
+
+def row_scale(top):
+    """max / 448 as one division (of a number torch multiplies by the reciprocal), 1 for a zero row."""
+    return torch.where(top > 0, torch.div(top, torch.full_like(top, 448.0)), torch.ones_like(top))
+
+
+def codes(w):
+    scale = row_scale(w.float().abs().amax(-1))
+    return (w.float() / scale[..., None]).to(E4M3).view(torch.uint8), scale
+
+
+def rule(a):
+    """Values of the per-row codes of bf16 rows, by the stated rule."""
+    q, scale = codes(a)
+    return q.view(E4M3).double() * scale.double()[:, None]
+
+
+def reference(s, form, w8=None):
+    """(O, bound, ids, w) in 64 bits."""
+    K = s["K"]
+    top = torch.sort(logits64(s), dim=1, descending=True)
+    ids, w = top.indices[:, :K], torch.softmax(top.values[:, :K], 1)
+    T, d = s["X"].shape
+    n = s["W_gate"].shape[1]
+    O, bound = torch.zeros((T, d), dtype=F64, device="cuda"), torch.zeros((T, d), dtype=F64, device="cuda")
+    for e in ids.unique().tolist():
+        t, k = torch.nonzero(ids == e, as_tuple=True)
+        x = s["X"][t]
+        if form == "e4m3":
+            x = rule(x)
+            wg, wu, wd = (q[e].view(E4M3).double() * c[e].double()[:, None]
+                          for q, c in ((w8.Wg_q, w8.wg_scale), (w8.Wu_q, w8.wu_scale), (w8.Wd_q, w8.wd_scale)))
+        else:
+            x, wg, wu, wd = x.double(), s["W_gate"][e].double(), s["W_up"][e].double(), s["W_down"][e].double()
+        h, u = x @ wg.T, x @ wu.T
+        dh, du = (d + 4) * 2.0 ** -23 * (x.abs() @ wg.abs().T), (d + 4) * 2.0 ** -23 * (x.abs() @ wu.abs().T)
+        sg = 1 / (1 + torch.exp(-h))
+        a = h * sg * u
+        # |d silu / dh| <= 1.1
+        da = 1.1 * dh * (u.abs() + du) + (h * sg).abs() * du + 2.0 ** -20 * a.abs() + 1e-38
+        if form == "e4m3":
+            mid, lo, hi = rule(a.to(BF)), rule_of(a - da, a), rule_of(a + da, a)
+            slack = torch.maximum((hi - mid).abs(), (mid - lo).abs())
+            most = (a.abs() + da).amax(1)
+            unsure = most.to(BF) != (a.abs() - da).amax(1).to(BF)
+            slack = torch.where(unsure[:, None], slack + 2.0 ** -3 * a.abs(), slack)
+            a = mid
+        else:
+            slack = da + 2.0 ** -16 * a.abs()
+        y = a @ wd.T
+        dy = slack @ wd.abs().T + (n + 4) * 2.0 ** -23 * (a.abs() @ wd.abs().T)
+        O[t] += w[t, k, None] * y
+        bound[t] += w[t, k, None] * (dy + 2.0 ** -18 * y.abs())
+    return O, bound * (1 + 2.0 ** -8) + 2.0 ** -8 * O.abs(), ids.to(I32), w
+
+
+def rule_of(v, a):
+    """v's codes with the scale of a's rows."""
+    scale = row_scale(a.to(BF).float().abs().amax(1, keepdim=True))
+    return (v.to(BF).float() / scale).clamp(-448, 448).to(E4M3).double() * scale.double()
+
+
+def call(vgg, ctx, s, form="bf16", w8=None, X=None, O=None, ws=None, stream=None):
+    T, d = s["X"].shape
+    E, n = s["W_gate"].shape[:2]
+    K = s["K"]
+    O = torch.full((T, d), float("nan"), dtype=BF, device="cuda") if O is None else O
+    ids, w = torch.full((T, K), -1, dtype=I32, device="cuda"), torch.zeros((T, K), device="cuda")
+    if ws is None:
+        ws = torch.full((vgg.moe_few_workspace_bytes(T, d, E, n, K),), 0xFF, dtype=torch.uint8, device="cuda")
+    X = s["X"] if X is None else X
+    if form == "e4m3":
+        vgg.moe_forward_few_e4m3(ctx, X, s["W_r"], s["bias"], w8, K, O, ids, w, ws, stream=stream)
+    else:
+        vgg.moe_forward_few(ctx, X, s["W_r"], s["bias"], s["W_gate"], s["W_up"], s["W_down"], K, O, ids, w, ws, stream=stream)
+    return O, ids, w
+
+
+def weights8(vgg, ctx, s):
+    return vgg.E4m3Weights.quantize(ctx, s["W_gate"], s["W_up"], s["W_down"])
+
+
+def check(got, want):
+    (O, ids, w), (ref, bound, rids, rw) = got, want
+    assert torch.equal(ids, rids)
+    np.testing.assert_allclose(w.cpu().numpy(), rw.cpu().numpy(), rtol=1e-4, atol=1e-7)  # logits' error times 1
+    over = ((O.double() - ref).abs() - bound).amax().item()
+    assert over <= 0, over
+
+
+CASES = [
+    (1, 128, 8, 64, 2, None), (1, 2048, 128, 512, 8, None), (2, 64, 8, 64, 1, None), (3, 192, 8, 64, 2, "normal"),
+    (1, 64, 8, 64, 8, None), (7, 320, 24, 448, 3, None), (8, 256, 16, 128, 4, "few"), (9, 256, 16, 128, 4, "few"),
+    (16, 1536, 512, 256, 8, None), (17, 192, 1024, 192, 8, None), (24, 512, 8, 320, 8, "normal"), (33, 448, 40, 64, 5, None),
+    (61, 256, 32, 128, 2, "normal"), (64, 2048, 128, 512, 8, None), (64, 128, 8, 64, 8, "few"), (64, 704, 16, 192, 1, "few"),
+]
+
+
+@pytest.mark.parametrize("form", ["bf16", "e4m3"])
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(map(str, c)))
+def test_matches_64_bits(vgg, ctx, case, form):
+    T, d, E, n, K, bias = case
+    s = make(T, d, E, n, K, seed=T + d, bias=bias)
+    w8 = weights8(vgg, ctx, s) if form == "e4m3" else None
+    got = call(vgg, ctx, s, form, w8)
+    assert vgg.moe_get_error(ctx) == (vgg.MOE_OK, 0)
+    check(got, reference(s, form, w8))

@@ -34,7 +34,7 @@ EXPORTS = (
     "moe_quantize_weights_mx", "moe_grouped_gemm_fwd_mx", "moe_quantize_bwd_weights_mx", "moe_backward_mx",
     "moe_mx_dw_ws_bytes", "moe_add_rmsnorm", "moe_add_rmsnorm_workspace_bytes", "moe_add_rmsnorm_backward",
     "moe_balance_loss", "moe_balance_loss_workspace_bytes", "moe_router_backward",
-    "moe_router_backward_workspace_bytes",
+    "moe_router_backward_workspace_bytes", "moe_few_workspace_bytes", "moe_forward_few", "moe_forward_few_e4m3",
 )
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA, MOE_ERR_DEVICE, MOE_ERR_DEVICE_TIMEOUT = range(6)
@@ -121,6 +121,11 @@ def lib() -> ctypes.CDLL:
         L.moe_router_backward_workspace_bytes.argtypes = [_I, _I, _I]
         L.moe_router_backward_workspace_bytes.restype = _SZ
         L.moe_router_backward.argtypes = [_P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P, _P, _SZ, _P]
+        L.moe_few_workspace_bytes.argtypes = [_I, _I, _I, _I, _I]
+        L.moe_few_workspace_bytes.restype = _SZ
+        L.moe_forward_few.argtypes = [_P, _P, _LL, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _LL, _P, _SZ, _P]
+        L.moe_forward_few_e4m3.argtypes = [_P, _P, _LL, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P,
+                                           _LL, _P, _SZ, _P]
         L.moe_profile_enable.argtypes = [_P, _I]
         L.moe_profile_read.argtypes = [_P, _I, ctypes.c_char_p, ctypes.POINTER(ctypes.c_double),
                                        ctypes.POINTER(_LL), ctypes.POINTER(_I)]
@@ -609,6 +614,55 @@ def moe_router_backward(ctx, dlogits, X, W_r, dX_in, dW_r_in, dX, dW_r, ws, stre
         ctx.handle, _flat(ctx, dlogits, (T, E), f32, "dlogits"), _flat(ctx, X, (T, d), bf, "X"), _flat(ctx, W_r, (d, E), bf, "W_r"), T, d,
         E, _flat(ctx, dX_in, (T, d), bf, "dX_in"), _flat(ctx, dW_r_in, (d, E), f32, "dW_r_in"), _flat(ctx, dX, (T, d), bf, "dX"),
         _flat(ctx, dW_r, (d, E), f32, "dW_r"), wp, wb, _stream(stream)))
+
+
+# ------------------------------------------------------------------ a few tokens
+
+
+def moe_few_workspace_bytes(T: int, d: int, E: int, n: int, K: int) -> int:
+    """Bytes of the workspace of moe_forward_few and moe_forward_few_e4m3."""
+    b = int(lib().moe_few_workspace_bytes(T, d, E, n, K))
+    if b <= 0:
+        raise ValueError(f"moe_few_workspace_bytes: invalid arguments T={T} d={d} E={E} n={n} K={K}")
+    return b
+
+
+def _few(ctx, X, W_r, bias, W_gate, W_up, W_down, dtype, K, O, topk_ids, topk_w, ws):
+    """Sizes and checked pointers common to both forms of the layer for a few tokens."""
+    if X.dim() != 2 or W_gate.dim() != 3:
+        raise ValueError(f"X must be [T, d] and W_gate [E, n, d], got {tuple(X.shape)} and {tuple(W_gate.shape)}")
+    T, d = X.shape
+    E, n = W_gate.shape[:2]
+    bf, f32 = torch.bfloat16, torch.float32
+    px, lx = _rows(ctx, X, (T, d), bf, "X")
+    po, lo = _rows(ctx, O, (T, d), bf, "O")
+    head = (ctx.handle, px, lx, _flat(ctx, W_r, (d, E), bf, "W_r"), _flat(ctx, bias, (E,), f32, "bias"))
+    weights = (_flat(ctx, W_gate, (E, n, d), dtype, "W_gate"), _flat(ctx, W_up, (E, n, d), dtype, "W_up"),
+               _flat(ctx, W_down, (E, d, n), dtype, "W_down"))
+    wp, wb = _scratch(ctx, ws)
+    tail = (T, d, E, n, K, _flat(ctx, topk_ids, (T, K), torch.int32, "topk_ids"), _flat(ctx, topk_w, (T, K), f32, "topk_w"),
+            po, lo, wp, wb)
+    return head, weights, tail
+
+
+def moe_forward_few(ctx, X, W_r, bias, W_gate, W_up, W_down, K, O, topk_ids, topk_w, ws, stream=None):
+    """The whole layer for up to 64 tokens: ``topk_ids`` and ``topk_w`` [T, K] as moe_route gives them, ``O`` [T, d] bf16.
+    ``X`` and ``O`` may have any row stride (a multiple of 8 and 4 elements).  ``ws``: uint8 of
+    moe_few_workspace_bytes(T, d, E, n, K), one for each call that may overlap another."""
+    head, w, tail = _few(ctx, X, W_r, bias, W_gate, W_up, W_down, torch.bfloat16, K, O, topk_ids, topk_w, ws)
+    _check("moe_forward_few", lib().moe_forward_few(*head, *w, *tail, _stream(stream)))
+
+
+def moe_forward_few_e4m3(ctx, X, W_r, bias, w8, K, O, topk_ids, topk_w, ws, stream=None):
+    """moe_forward_few on e4m3 weights (``w8``: E4m3Weights with W_down's codes); the call quantizes X and the activations."""
+    if w8.Wd_q is None:
+        raise ValueError("moe_forward_few_e4m3 needs W_down's codes (E4m3Weights.quantize with W_down)")
+    head, (g, u, dn), tail = _few(ctx, X, W_r, bias, w8.Wg_q, w8.Wu_q, w8.Wd_q, torch.uint8, K, O, topk_ids, topk_w, ws)
+    E, n, d = w8.Wg_q.shape
+    f32 = torch.float32
+    _check("moe_forward_few_e4m3", lib().moe_forward_few_e4m3(
+        *head, g, _flat(ctx, w8.wg_scale, (E, n), f32, "wg_scale"), u, _flat(ctx, w8.wu_scale, (E, n), f32, "wu_scale"),
+        dn, _flat(ctx, w8.wd_scale, (E, d), f32, "wd_scale"), *tail, _stream(stream)))
 
 
 def moe_test_gemm_varlen_m(ctx, A, idx, B, b_kmajor, offsets, D, stream=None):

@@ -1729,6 +1729,93 @@ int moe_router_backward(moe_ctx* ctx, const float* dlogits, const void* X, const
   return MOE_OK;
 }
 
+static bool few_sizes_ok(int T, int d, int E, int n, int K) {
+  return T >= 0 && T <= kFewMaxTokens && shapes_ok(1, d, E, n, K);
+}
+
+size_t moe_few_workspace_bytes(int T, int d, int E, int n, int K) {
+  if (!few_sizes_ok(T, d, E, n, K)) return 0;
+  return std::max<size_t>(few_layout(T, d, E, n, K).bytes, kAlign);
+}
+
+// Both forms of the layer for a few tokens: bf16 weights, or e4m3 codes with their scales (wg_scale != NULL).
+static int forward_few(moe_ctx* ctx, const void* X, long long ld_x, const void* W_r, const float* bias, const void* Wg,
+                       const float* wg_scale, const void* Wu, const float* wu_scale, const void* Wd, const float* wd_scale,
+                       int T, int d, int E, int n, int K, int32_t* topk_ids, float* topk_w, void* O, long long ld_o, void* ws,
+                       size_t ws_bytes, moe_stream_t stream) {
+  VGG_REQUIRE(ctx && few_sizes_ok(T, d, E, n, K));
+  VGG_REQUIRE(ws && (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1)) == 0 &&
+              ws_bytes >= moe_few_workspace_bytes(T, d, E, n, K));
+  if (T == 0) return MOE_OK;
+  VGG_REQUIRE(X && W_r && Wg && Wu && Wd && topk_ids && topk_w && O);
+  VGG_REQUIRE(ld_x >= d && ld_x % 8 == 0 && ld_o >= d && ld_o % 4 == 0);
+  VGG_REQUIRE(aligned16(X) && aligned16(W_r) && aligned16(Wg) && aligned16(Wu) && aligned16(Wd) && aligned16(wd_scale) &&
+              (reinterpret_cast<uintptr_t>(O) & 7u) == 0);
+  DeviceGuard g(ctx->device);
+  if (!g.ok) return MOE_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const FewLayout l = few_layout(T, d, E, n, K);
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  const bool f8 = wg_scale != nullptr;
+  FewArgs a{};
+  a.X = static_cast<const __nv_bfloat16*>(X);
+  a.ld_x = ld_x;
+  a.W_r = static_cast<const __nv_bfloat16*>(W_r);
+  a.bias = bias;
+  a.T = T;
+  a.d = d;
+  a.E = E;
+  a.n = n;
+  a.K = K;
+  a.wg_scale = wg_scale;
+  a.wu_scale = wu_scale;
+  a.wd_scale = wd_scale;
+  a.ids = topk_ids;
+  a.w = topk_w;
+  a.O = static_cast<__nv_bfloat16*>(O);
+  a.ld_o = ld_o;
+  a.ctr = reinterpret_cast<int*>(base + l.ctr);
+  a.nctr = l.nctr;
+  a.amax = reinterpret_cast<uint32_t*>(base + l.amax);
+  a.part = reinterpret_cast<float*>(base + l.part);
+  a.splits = few_splits(d, E, ctx->num_sms);
+  if (f8) {
+    a.xq = base + l.xq;
+    a.xs = reinterpret_cast<float*>(base + l.xs);
+  }
+  a.hu = reinterpret_cast<float*>(base + l.hu);
+  a.A = reinterpret_cast<__nv_bfloat16*>(base + l.A);
+  a.A_lo = reinterpret_cast<__nv_bfloat16*>(base + l.A_lo);
+  a.y = reinterpret_cast<float*>(base + l.y);
+  a.ov1 = reinterpret_cast<float*>(base + l.ov1);
+  a.ov2 = reinterpret_cast<float*>(base + l.ov2);
+  a.err = ctx->d_err;
+  a.timeout_ns = ctx->timeout_ns;
+  const int du = f8 ? d / 2 : d, nu = f8 ? n / 2 : n;  // the reduction in 16-bit units
+  CUtensorMap mg, mu, md;
+  if (!make_map_3d(&mg, Wg, du, n, E, 64) || !make_map_3d(&mu, Wu, du, n, E, 64) || !make_map_3d(&md, Wd, nu, d, E, 128))
+    return MOE_ERR_CUDA;
+  VGG_LAUNCH("few_router", launch_few_router(a, ctx->num_sms, s));
+  VGG_LAUNCH("few_layer", launch_few_layer(a, f8, mg, mu, md, ctx->num_sms, s));
+  return MOE_OK;
+}
+
+int moe_forward_few(moe_ctx* ctx, const void* X, long long ld_x, const void* W_r, const float* bias, const void* W_gate,
+                    const void* W_up, const void* W_down, int T, int d, int E, int n, int K, int32_t* topk_ids,
+                    float* topk_w, void* O, long long ld_o, void* ws, size_t ws_bytes, moe_stream_t stream) {
+  return forward_few(ctx, X, ld_x, W_r, bias, W_gate, nullptr, W_up, nullptr, W_down, nullptr, T, d, E, n, K, topk_ids,
+                     topk_w, O, ld_o, ws, ws_bytes, stream);
+}
+
+int moe_forward_few_e4m3(moe_ctx* ctx, const void* X, long long ld_x, const void* W_r, const float* bias, const void* Wg_q,
+                         const float* wg_scale, const void* Wu_q, const float* wu_scale, const void* Wd_q,
+                         const float* wd_scale, int T, int d, int E, int n, int K, int32_t* topk_ids, float* topk_w, void* O,
+                         long long ld_o, void* ws, size_t ws_bytes, moe_stream_t stream) {
+  VGG_REQUIRE(wg_scale && wu_scale && wd_scale);
+  return forward_few(ctx, X, ld_x, W_r, bias, Wg_q, wg_scale, Wu_q, wu_scale, Wd_q, wd_scale, T, d, E, n, K, topk_ids,
+                     topk_w, O, ld_o, ws, ws_bytes, stream);
+}
+
 int moe_test_gemm_varlen_m(moe_ctx* ctx, const void* A, const int32_t* idx, const void* B, int B_kmajor, int G,
                            int rows_a, int K, int N, long long cap, const int32_t* offsets, float* D,
                            moe_stream_t stream) {

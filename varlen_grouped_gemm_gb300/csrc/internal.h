@@ -266,6 +266,46 @@ cudaError_t launch_router_dw(const __nv_bfloat16* X, const __nv_bfloat16* parts,
 // out[i][e] = in[i][e] (or 0) + sum_s sums[s][e][i], in a fixed order.
 cudaError_t launch_router_dw_reduce(const float* sums, int splits, int d, int E, const float* in, float* out, cudaStream_t s);
 
+// ---- the layer for a few tokens ---------------------------------------------------------------
+constexpr int kFewMaxTokens = 64;
+constexpr int kFewMaxBlocks = 256;  // persistent blocks (bounds the workspace's overflow rows)
+constexpr int kFewMaxSplits = 32;   // shares of d in the router's product
+// Pointers into the caller's arrays and the workspace.  xq, xs, wg_scale, wu_scale, wd_scale: the e4m3 form alone.
+struct FewArgs {
+  const __nv_bfloat16* X;
+  long long ld_x;
+  const __nv_bfloat16* W_r;
+  const float* bias;
+  int T, d, E, n, K;
+  const float *wg_scale, *wu_scale, *wd_scale;
+  int32_t* ids;  // [T][K]
+  float* w;      // [T][K]
+  __nv_bfloat16* O;
+  long long ld_o;
+  int* ctr;         // [nctr] counters: choices, items with activations, blocks done, then one for each shared item
+  uint32_t* amax;   // [P] largest |A| of a pair (e4m3)
+  float* part;      // [splits][T][E] parts of the logits
+  uint8_t* xq;      // [T][d]
+  float* xs;        // [T]
+  float* hu;        // [P][n / 64][64 of H, 64 of U]: an item's first part
+  __nv_bfloat16 *A, *A_lo;  // [P][n]
+  float* y;         // [P][d rounded up to 128]
+  float *ov1, *ov2; // [blocks][T][128]: parts of items that began in another block
+  int nctr, splits, stages, nrows;
+  int* err;
+  unsigned long long timeout_ns;
+};
+struct FewLayout {
+  size_t ctr, amax, part, xq, xs, hu, A, A_lo, y, ov1, ov2, bytes;
+  int nctr;
+};
+FewLayout few_layout(int T, int d, int E, int n, int K);
+int few_splits(int d, int E, int num_sms);
+cudaError_t launch_few_router(const FewArgs& args, int num_sms, cudaStream_t s);
+// Maps over 16-bit units: gate and up with boxes of 64 rows, down of 128.
+cudaError_t launch_few_layer(const FewArgs& args, bool f8, const CUtensorMap& mg, const CUtensorMap& mu,
+                             const CUtensorMap& md, int num_sms, cudaStream_t s);
+
 cudaError_t launch_wait_timeout_probe(int* err, unsigned long long timeout_ns, cudaStream_t s);
 
 }  // namespace vgg
