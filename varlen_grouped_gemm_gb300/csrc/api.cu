@@ -1754,6 +1754,9 @@ static int forward_few(moe_ctx* ctx, const void* X, long long ld_x, const void* 
   DeviceGuard g(ctx->device);
   if (!g.ok) return MOE_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  // the kernel counts a list's stages times its blocks in 32 bits
+  const long long tiles = static_cast<long long>(std::min(E, T * K)) * std::max(n / 64 * ceil_div(d, 64), ceil_div(d, 128) * (n / 64));
+  if (tiles * few_blocks(ctx->num_sms) >= (1ll << 32)) return MOE_ERR_UNSUPPORTED;
   const FewLayout l = few_layout(T, d, E, n, K);
   uint8_t* base = static_cast<uint8_t*>(ws);
   const bool f8 = wg_scale != nullptr;
@@ -1778,7 +1781,7 @@ static int forward_few(moe_ctx* ctx, const void* X, long long ld_x, const void* 
   a.nctr = l.nctr;
   a.amax = reinterpret_cast<uint32_t*>(base + l.amax);
   a.part = reinterpret_cast<float*>(base + l.part);
-  a.splits = few_splits(d, E, ctx->num_sms);
+  a.splits = few_splits(T, d, E, ctx->num_sms);
   if (f8) {
     a.xq = base + l.xq;
     a.xs = reinterpret_cast<float*>(base + l.xs);
@@ -1795,7 +1798,7 @@ static int forward_few(moe_ctx* ctx, const void* X, long long ld_x, const void* 
   CUtensorMap mg, mu, md;
   if (!make_map_3d(&mg, Wg, du, n, E, 64) || !make_map_3d(&mu, Wu, du, n, E, 64) || !make_map_3d(&md, Wd, nu, d, E, 128))
     return MOE_ERR_CUDA;
-  VGG_LAUNCH("few_router", launch_few_router(a, ctx->num_sms, s));
+  VGG_LAUNCH("few_router", launch_few_router(a, s));
   VGG_LAUNCH("few_layer", launch_few_layer(a, f8, mg, mu, md, ctx->num_sms, s));
   return MOE_OK;
 }

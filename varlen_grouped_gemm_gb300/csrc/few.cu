@@ -34,16 +34,20 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kRows = 128;             // weight rows of a tile
 constexpr int kWBytes = kRows * 128;   // weight bytes of a stage
 constexpr int kMaxPairs = kFewMaxTokens * 8;
-constexpr int kMaxStages = 12;
+constexpr int kMaxStages = 12, kMinStages = kProd;  // (the producers take stages in turn, too)
 // Every block finds the choice of so few tokens itself; of more, each is found by one block behind a barrier (a block
 // reads splits x T x E partial logits otherwise).
 constexpr int kOwnChoice = 8;
+constexpr int kRound = 16;   // tokens whose logits a block holds at a time
+// counters: choices made, items with activations of each half, blocks done, then one for each shared item
+constexpr int kCtrChoice = 0, kCtrItems = 1, kCtrDone = 3, kCtrShared = 4;
 
 struct Lists {
   uint64_t full[kMaxStages], empty[kMaxStages], tfull[2], tempty[2], drain;
   uint32_t tmem;
   volatile int abort;
   int active, last, ok;
+  uint32_t chunk[32];          // pairs and experts (<< 16) of 32 experts each
   float pw[kMaxPairs];         // [token][rank]: combine weight, experts of a token ascending
   uint16_t act_e[kMaxPairs];   // expert of each chosen expert's index, ascending
   uint16_t act_off[kMaxPairs + 1];  // its first pair
@@ -57,7 +61,14 @@ __device__ __forceinline__ uint32_t order_key(float x) {
 }
 __device__ __forceinline__ float key_value(uint32_t k) { return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k); }
 
-__device__ __forceinline__ void red_release(int* p) { asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(p) : "memory"); }
+__device__ __forceinline__ void red_release(int* p, int v) {
+  asm volatile("red.release.gpu.global.add.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+__device__ __forceinline__ int atom_acq_rel(int* p) {
+  int v;
+  asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
 
 // Waits (bounded) until *p >= target, acquiring what the arrivals released.
 __device__ __forceinline__ bool wait_count(const int* p, int target, volatile int* abort_flag, unsigned long long timeout_ns,
@@ -79,12 +90,61 @@ __device__ __forceinline__ bool wait_count(const int* p, int target, volatile in
   }
 }
 
-// The blocks' shares of a list of S stages: block b has [b S / G, (b + 1) S / G).
-struct Share {
-  long long S;
-  int G;
-  __device__ __forceinline__ long long begin(int b) const { return b >= G ? S : b * S / G; }
-  __device__ __forceinline__ int owner(long long s) const { return static_cast<int>(((s + 1) * G - 1) / S); }
+// The work as lists of stages: the first product of the first half of the chosen experts, of the second half, then the second
+// product of either.  A list's items (an expert's 128-row tiles) are c stages each; block b of its G takes the stages
+// [b S / G, (b + 1) S / G).  With halves the activations that a block waits for at the second product's start have been
+// complete for half a product's time.
+struct List {
+  int ph, half, a0, tiles, c, S, G;
+  __device__ __forceinline__ int begin(int b) const {
+    return b >= G ? S : static_cast<int>(static_cast<long long>(b) * S / G);
+  }
+  // the block that has stage s (the host refuses sizes where S G would pass 32 bits)
+  __device__ __forceinline__ int owner(int s) const {
+    return static_cast<int>((static_cast<uint32_t>(s + 1) * static_cast<uint32_t>(G) - 1u) / static_cast<uint32_t>(S));
+  }
+};
+constexpr int kLists = 4;
+
+struct Plan {
+  int A, G, t1, c1, t2, c2;
+  __device__ __forceinline__ List list(int l) const {
+    List x;
+    x.ph = l >> 1;
+    x.half = l & 1;
+    x.a0 = x.half ? A / 2 : 0;
+    x.tiles = x.ph ? t2 : t1;
+    x.c = x.ph ? c2 : c1;
+    x.S = ((x.half ? A : A / 2) - x.a0) * x.tiles * x.c;
+    x.G = min(x.S, G);
+    return x;
+  }
+};
+
+// A block's way through a list: stage q is reduction step k of tile `tile` of the chosen expert ai.
+struct Walk {
+  int q, end, k, tile, ai;
+  __device__ __forceinline__ void start(const List& x, int b) {
+    q = x.begin(b);
+    end = x.begin(b + 1);
+    const int item = q / x.c;
+    k = q - item * x.c;
+    const int i = item / x.tiles;
+    ai = x.a0 + i;
+    tile = item - i * x.tiles;
+  }
+  __device__ __forceinline__ void next_item(const List& x) {
+    k = 0;
+    if (++tile == x.tiles) {
+      tile = 0;
+      ++ai;
+    }
+  }
+  __device__ __forceinline__ void next(const List& x) {
+    ++q;
+    if (++k == x.c) next_item(x);
+  }
+  __device__ __forceinline__ int item(const List& x) const { return (ai - x.a0) * x.tiles + tile; }
 };
 
 __device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpi) : "memory"); }
@@ -128,17 +188,21 @@ __device__ __forceinline__ uint4 codes16(const uint4 x, const uint4 y, float s) 
 }  // namespace
 
 // ---- first launch: parts of the logits, X's codes, cleared counters -------------------------------------------------
-// Blocks [0, strips * splits): 16 experts (32 bytes of every row of W_r, a memory sector) times a share of d: part[split][t][e].
-// Thread: two experts (tid & 7) and every 32nd row of the share; NT tokens at a time.  The blocks behind clear the counters
-// and, for the e4m3 form, quantize a token each.
+// Block (x, y), x < strips * splits: 16 experts (32 bytes of every row of W_r, a memory sector) times a share of d, for the
+// tokens NT y .. : part[split][t][e].  Thread: two experts (tid & 7) and four rows of every 128.  The blocks behind (y = 0)
+// clear the counters and, for the e4m3 form, quantize a token each.
+constexpr int kRtRows = 128;
 template <int NT>
 __global__ void __launch_bounds__(256) few_router_kernel(const __grid_constant__ FewArgs a) {
   __shared__ float red[8][NT][16];
+  __shared__ __align__(16) float s_x[NT][kRtRows];
   __shared__ float s_top[8];
+  griddep_launch();  // the second launch's start may overlap; it waits for this one's end
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int strips = (a.E + 15) / 16;
   const int b = blockIdx.x;
   if (b >= strips * a.splits) {
+    if (blockIdx.y > 0) return;
     const int q = b - strips * a.splits;
     if (q == 0) {
       for (int i = tid; i < a.nctr; i += 256) a.ctr[i] = 0;
@@ -172,92 +236,121 @@ __global__ void __launch_bounds__(256) few_router_kernel(const __grid_constant__
     }
     return;
   }
-  const int strip = b % strips, split = b / strips;
-  const int r0 = static_cast<int>(static_cast<long long>(a.d) * split / a.splits);
-  const int r1 = static_cast<int>(static_cast<long long>(a.d) * (split + 1) / a.splits);
+  const int strip = b % strips, split = b / strips, t0 = blockIdx.y * NT;
+  const int d8 = a.d / 8;
+  const int r0 = d8 * split / a.splits * 8, r1 = d8 * (split + 1) / a.splits * 8;
   const int e0 = strip * 16 + 2 * (tid & 7);
   const bool in = e0 < a.E;  // E is a multiple of 8: a pair is in or out
-  const int rg = tid >> 3;
-  for (int t0 = 0; t0 < a.T; t0 += NT) {
-    float acc[NT][2];
+  const int rg = 4 * (tid >> 3);
+  float acc[NT][2];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = 0.0f;
-    if (in) {
-#pragma unroll 4
-      for (int r = r0 + rg; r < r1; r += 32) {
-        const float2 w = unpack_bf16x2(__ldg(reinterpret_cast<const uint32_t*>(a.W_r + static_cast<long long>(r) * a.E + e0)));
+  for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = 0.0f;
+  for (int c = r0; c < r1; c += kRtRows) {
+    uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          const float x = t0 + i < a.T ? __bfloat162float(__ldg(a.X + (t0 + i) * a.ld_x + r)) : 0.0f;
-          acc[i][0] = fmaf(x, w.x, acc[i][0]);
-          acc[i][1] = fmaf(x, w.y, acc[i][1]);
+    for (int j = 0; j < 4; ++j)
+      w[j] = (in && c + rg + j < r1)
+                 ? __ldg(reinterpret_cast<const uint32_t*>(a.W_r + static_cast<long long>(c + rg + j) * a.E + e0))
+                 : 0u;
+    __syncthreads();
+    for (int i = tid; i < NT * (kRtRows / 8); i += 256) {
+      const int t = i / (kRtRows / 8), v = i % (kRtRows / 8) * 8;
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (t0 + t < a.T && c + v < r1) x = __ldg(reinterpret_cast<const uint4*>(a.X + (t0 + t) * a.ld_x + c + v));
+      const float2 f0 = unpack_bf16x2(x.x), f1 = unpack_bf16x2(x.y), f2 = unpack_bf16x2(x.z), f3 = unpack_bf16x2(x.w);
+      *reinterpret_cast<float4*>(&s_x[t][v]) = make_float4(f0.x, f0.y, f1.x, f1.y);
+      *reinterpret_cast<float4*>(&s_x[t][v + 4]) = make_float4(f2.x, f2.y, f3.x, f3.y);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const float4 x = *reinterpret_cast<const float4*>(&s_x[i][rg]);
+      const float xv[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = unpack_bf16x2(w[j]);
+        if (c + rg + j < r1) {  // (an infinite X beside a row that is not there)
+          acc[i][0] = fmaf(xv[j], f.x, acc[i][0]);
+          acc[i][1] = fmaf(xv[j], f.y, acc[i][1]);
         }
       }
     }
+  }
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
+  for (int i = 0; i < NT; ++i) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        acc[i][j] += __shfl_xor_sync(0xffffffffu, acc[i][j], 8);
-        acc[i][j] += __shfl_xor_sync(0xffffffffu, acc[i][j], 16);
-      }
-      if (lane < 8) {
-        red[warp][i][2 * lane] = acc[i][0];
-        red[warp][i][2 * lane + 1] = acc[i][1];
-      }
+    for (int j = 0; j < 2; ++j) {
+      acc[i][j] += __shfl_xor_sync(0xffffffffu, acc[i][j], 8);
+      acc[i][j] += __shfl_xor_sync(0xffffffffu, acc[i][j], 16);
     }
-    __syncthreads();
-    for (int i = tid; i < NT * 16; i += 256) {
-      const int t = t0 + i / 16, e = strip * 16 + i % 16;
-      if (t < a.T && e < a.E) {
-        float s = 0.0f;
-#pragma unroll
-        for (int w = 0; w < 8; ++w) s += red[w][i / 16][i % 16];
-        a.part[(static_cast<long long>(split) * a.T + t) * a.E + e] = s;
-      }
+    if (lane < 8) {
+      red[warp][i][2 * lane] = acc[i][0];
+      red[warp][i][2 * lane + 1] = acc[i][1];
     }
-    __syncthreads();
+  }
+  __syncthreads();
+  for (int i = tid; i < NT * 16; i += 256) {
+    const int t = t0 + i / 16, e = strip * 16 + i % 16;
+    if (t < a.T && e < a.E) {
+      float s = 0.0f;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) s += red[w][i / 16][i % 16];
+      a.part[(static_cast<long long>(split) * a.T + t) * a.E + e] = s;
+    }
   }
 }
 
-// One warp finds token t's choice: its logits as order keys in keys[E] (shared memory), then K rounds of the largest key, the
-// lower expert among equal ones (the rule of moe_route).  Lane k < K returns the k-th choice and its weight.
-__device__ __forceinline__ void choose(const FewArgs& a, int t, uint32_t* keys, int& id, float& w) {
-  const int lane = threadIdx.x & 31;
+// The choice of up to kRound tokens first, first + step, ...: the block adds up their logits as order keys in keys [.][E]
+// (shared memory), then one warp a token takes K times the largest key, the lower expert among equal ones (the rule of
+// moe_route).  put(t, k, id, w) receives each.
+template <class Put>
+__device__ __forceinline__ void choose(const FewArgs& a, int first, int step, int count, uint32_t* keys, const Put& put) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long plane = static_cast<long long>(a.T) * a.E;
-  const float* row = a.part + static_cast<long long>(t) * a.E;
-  for (int e = lane; e < a.E; e += 32) {
-    float v = __ldcg(row + e);
-#pragma unroll 8
-    for (int sp = 1; sp < a.splits; ++sp) v += __ldcg(row + sp * plane + e);
-    if (a.bias) v += __ldg(a.bias + e);
-    keys[e] = max(order_key(v), 1u);
+  for (int x = threadIdx.x; x < count * a.E; x += kThreads) {
+    const int i = x / a.E, e = x - i * a.E;
+    const float* p = a.part + static_cast<long long>(first + i * step) * a.E + e;
+    float v = a.bias ? __ldg(a.bias + e) : 0.0f;
+    for (int s0 = 0; s0 < a.splits; s0 += 16) {  // sixteen loads in flight
+      float y[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) y[j] = s0 + j < a.splits ? __ldcg(p + (s0 + j) * plane) : 0.0f;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v += y[j];
+    }
+    keys[x] = max(order_key(v), 1u);
   }
-  float vmax = 0.0f, sum = 0.0f, ex_k = 0.0f;
-  id = 0;
-  for (int k = 0; k < a.K; ++k) {
-    uint32_t bk = 0;
-    int be = 0x7fffffff;
-    for (int e = lane; e < a.E; e += 32) {
-      const uint32_t q = keys[e];
-      if (q > bk) {
-        bk = q;
-        be = e;
+  __syncthreads();
+  if (warp < count) {
+    uint32_t* key = keys + warp * a.E;
+    float vmax = 0.0f, sum = 0.0f, ex_k = 0.0f;
+    int id = 0;
+    for (int k = 0; k < a.K; ++k) {
+      uint32_t bk = 0;
+      int be = 0x7fffffff;
+#pragma unroll 4
+      for (int e = lane; e < a.E; e += 32) {
+        const uint32_t q = key[e];
+        if (q > bk) {
+          bk = q;
+          be = e;
+        }
+      }
+      const uint32_t top = __reduce_max_sync(0xffffffffu, bk);
+      const int e = __reduce_min_sync(0xffffffffu, bk == top ? be : 0x7fffffff);
+      if ((e & 31) == lane) key[e] = 0;
+      const float v = key_value(top);
+      if (k == 0) vmax = v;
+      const float ex = expf(v - vmax);
+      sum += ex;
+      if (lane == k) {
+        id = e;
+        ex_k = ex;
       }
     }
-    const uint32_t top = __reduce_max_sync(0xffffffffu, bk);
-    const int e = __reduce_min_sync(0xffffffffu, bk == top ? be : 0x7fffffff);
-    if ((e & 31) == lane) keys[e] = 0;
-    const float v = key_value(top);
-    if (k == 0) vmax = v;
-    const float ex = expf(v - vmax);
-    sum += ex;
-    if (lane == k) {
-      id = e;
-      ex_k = ex;
-    }
+    if (lane < a.K) put(first + warp * step, lane, id, ex_k / sum);
   }
-  w = ex_k / sum;
+  __syncthreads();
 }
 
 template <bool F8>
@@ -277,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
 
   if (tid == 0) {
     for (int s = 0; s < a.stages; ++s) {
-      mbar_init(&L.full[s], 1 + 32 * kGath);
+      mbar_init(&L.full[s], 1 + 32);
       mbar_init(&L.empty[s], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -295,41 +388,33 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
   if (warp == kMma) tmem_alloc(&L.tmem, tmem_cols);
 
   // ---- the choice, and the pairs grouped by expert (the ring's memory is scratch until the first load) ----
-  uint32_t* keys = reinterpret_cast<uint32_t*>(ring) + warp * a.E;
-  int* s_ids = reinterpret_cast<int*>(ring) + kWarps * a.E;  // [P]
+  uint32_t* keys = reinterpret_cast<uint32_t*>(ring);              // [kRound][E]
+  uint64_t* s_mask = reinterpret_cast<uint64_t*>(keys + kRound * a.E);  // [E] tokens of each expert
+  int* s_ids = reinterpret_cast<int*>(s_mask + a.E);                // [P]
   float* s_w = reinterpret_cast<float*>(s_ids + kMaxPairs);
-  uint64_t* s_mask = reinterpret_cast<uint64_t*>(s_w + kMaxPairs);  // [E] tokens of each expert
-  uint16_t* s_eoff = reinterpret_cast<uint16_t*>(s_mask + a.E);      // [E] first pair, index
+  uint16_t* s_eoff = reinterpret_cast<uint16_t*>(s_w + kMaxPairs);  // [E] first pair, index
   uint16_t* s_ea = s_eoff + a.E;
   for (int e = tid; e < a.E; e += kThreads) s_mask[e] = 0;
+  griddep_wait();  // the first launch's parts and cleared counters
   if (a.T <= kOwnChoice) {
-    if (warp < a.T) {
-      int id;
-      float w;
-      choose(a, warp, keys, id, w);
-      if (lane < a.K) {
-        s_ids[warp * a.K + lane] = id;
-        s_w[warp * a.K + lane] = w;
-        if (b == 0) {
-          a.ids[warp * a.K + lane] = id;
-          a.w[warp * a.K + lane] = w;
-        }
+    choose(a, 0, 1, a.T, keys, [&](int t, int k, int id, float w) {
+      s_ids[t * a.K + k] = id;
+      s_w[t * a.K + k] = w;
+      if (b == 0) {
+        a.ids[t * a.K + k] = id;
+        a.w[t * a.K + k] = w;
       }
-    }
-    __syncthreads();
+    });
   } else {
-    for (int t = b + warp * G; t < a.T; t += kWarps * G) {
-      int id;
-      float w;
-      choose(a, t, keys, id, w);
-      if (lane < a.K) {
-        a.ids[t * a.K + lane] = id;
-        a.w[t * a.K + lane] = w;
-      }
-      __syncwarp();
-      if (lane == 0) red_release(&a.ctr[0]);
+    for (int t = b; t < a.T; t += kRound * G) {
+      const int count = min(kRound, (a.T - t + G - 1) / G);
+      choose(a, t, G, count, keys, [&](int t2, int k, int id, float w) {
+        a.ids[t2 * a.K + k] = id;
+        a.w[t2 * a.K + k] = w;
+      });
+      if (tid == 0) red_release(&a.ctr[kCtrChoice], count);
     }
-    if (tid == 0) L.ok = wait_count(&a.ctr[0], a.T, &L.abort, a.timeout_ns, a.err) ? 1 : 0;
+    if (tid == 0) L.ok = wait_count(&a.ctr[kCtrChoice], a.T, &L.abort, a.timeout_ns, a.err) ? 1 : 0;
     __syncthreads();
     if (L.ok)
       for (int i = tid; i < P; i += kThreads) {
@@ -343,32 +428,36 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
     for (int i = tid; i < P; i += kThreads)
       atomicOr(reinterpret_cast<unsigned long long*>(&s_mask[s_ids[i]]), 1ull << (i / a.K));
   __syncthreads();
-  if (warp == 0) {
-    int run = 0, act = 0;
-    for (int e0 = 0; e0 < a.E; e0 += 32) {
-      const int e = e0 + lane;
-      const int cnt = (ok && e < a.E) ? __popcll(s_mask[e]) : 0;
-      int v = cnt | (cnt ? 1 << 16 : 0), incl = v;
+  const int chunks = (a.E + 31) / 32;
+  for (int c = warp; c < chunks; c += kWarps) {
+    const int e = 32 * c + lane;
+    const int cnt = (ok && e < a.E) ? __popcll(s_mask[e]) : 0;
+    const uint32_t tot = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(cnt | (cnt ? 1 << 16 : 0)));
+    if (lane == 0) L.chunk[c] = tot;
+  }
+  __syncthreads();
+  for (int c = warp; c < chunks; c += kWarps) {
+    const int e = 32 * c + lane;
+    const uint64_t mask = (ok && e < a.E) ? s_mask[e] : 0;
+    const int cnt = __popcll(mask);
+    const uint32_t before = __reduce_add_sync(0xffffffffu, lane < c ? L.chunk[lane] : 0u);
+    const uint32_t v = cnt | (cnt ? 1u << 16 : 0u);
+    uint32_t incl = v;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-      }
-      const int excl = incl - v;
-      if (cnt) {
-        const int ai = act + (excl >> 16);
-        s_eoff[e] = static_cast<uint16_t>(run + (excl & 0xffff));
-        s_ea[e] = static_cast<uint16_t>(ai);
-        L.act_e[ai] = static_cast<uint16_t>(e);
-        L.act_off[ai] = static_cast<uint16_t>(run + (excl & 0xffff));
-      }
-      const int tot = __shfl_sync(0xffffffffu, incl, 31);
-      run += tot & 0xffff;
-      act += tot >> 16;
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
     }
-    if (lane == 0) {
-      L.active = act;
-      L.act_off[act] = static_cast<uint16_t>(run);
+    const uint32_t at = before + incl - v;
+    if (cnt) {
+      s_eoff[e] = static_cast<uint16_t>(at);
+      s_ea[e] = static_cast<uint16_t>(at >> 16);
+      L.act_e[at >> 16] = static_cast<uint16_t>(e);
+      L.act_off[at >> 16] = static_cast<uint16_t>(at);
+    }
+    if (c == chunks - 1 && lane == 31) {
+      L.active = static_cast<int>((before + incl) >> 16);
+      L.act_off[(before + incl) >> 16] = static_cast<uint16_t>(before + incl);
     }
   }
   __syncthreads();
@@ -388,18 +477,16 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = L.tmem;
-  const int A = L.active;
 
-  // ---- the two lists of stages ----
   const int es = F8 ? 1 : 2;
-  const int t1 = a.n / 64, c1 = (a.d * es + 127) / 128;           // tiles of an expert, stages of a tile
-  const int t2 = (a.d + kRows - 1) / kRows, c2 = (a.n * es + 127) / 128;
-  Share sh[2];
-  sh[0].S = static_cast<long long>(A) * t1 * c1;
-  sh[1].S = static_cast<long long>(A) * t2 * c2;
-  sh[0].G = static_cast<int>(sh[0].S < G ? sh[0].S : G);
-  sh[1].G = static_cast<int>(sh[1].S < G ? sh[1].S : G);
-  auto columns = [&](int ph, int m) { return (!F8 && ph == 1) ? 2 * ((m + 7) & ~7) : (m + 15) & ~15; };
+  Plan plan;
+  plan.A = L.active;
+  plan.G = G;
+  plan.t1 = a.n / 64;  // 64 rows of W_gate and 64 of W_up a tile
+  plan.c1 = (a.d * es + 127) / 128;
+  plan.t2 = (a.d + kRows - 1) / kRows;
+  plan.c2 = (a.n * es + 127) / 128;
+  const int ld_hu = plan.t1 * kRows, ld_y = plan.t2 * kRows;
 
   if (warp >= kProd0) {
     // ---------------------------------------------------------------- weights (lane 0 of each producer warp)
@@ -408,27 +495,24 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
       int it = 0, s = 0;
       uint32_t par = 1;  // parity of the empty barrier's wait
       bool stop = false;
-      for (int ph = 0; ph < 2 && !stop; ++ph) {
-        const int c = ph ? c2 : c1;
-        const long long end = sh[ph].begin(b + 1);
-        for (long long q = sh[ph].begin(b); q < end && !stop; ++q, ++it) {
+      for (int l = 0; l < kLists && !stop; ++l) {
+        const List x = plan.list(l);
+        if (b >= x.G) continue;
+        Walk w;
+        for (w.start(x, b); w.q < w.end; w.next(x), ++it) {
           if ((it & (kProd - 1)) == pj) {
-            const long long item = q / c;
-            const int k = static_cast<int>(q - item * c) * 64;
             if (!mbar_wait(&L.empty[s], par, &L.abort, a.timeout_ns, a.err)) {
               stop = true;
               break;
             }
             uint8_t* dst = ring + s * stage_bytes;
+            const int e = L.act_e[w.ai];
             mbar_arrive_expect_tx(&L.full[s], kWBytes);
-            if (ph == 0) {
-              const int ai = static_cast<int>(item / t1), tile = static_cast<int>(item - static_cast<long long>(ai) * t1);
-              const int e = L.act_e[ai];
-              tma_load_3d(dst, &mg, &L.full[s], k, tile * 64, e);
-              tma_load_3d(dst + kWBytes / 2, &mu, &L.full[s], k, tile * 64, e);
+            if (x.ph == 0) {
+              tma_load_3d(dst, &mg, &L.full[s], w.k * 64, w.tile * 64, e);
+              tma_load_3d(dst + kWBytes / 2, &mu, &L.full[s], w.k * 64, w.tile * 64, e);
             } else {
-              const int tile = static_cast<int>(item / A), ai = static_cast<int>(item - static_cast<long long>(tile) * A);
-              tma_load_3d(dst, &md, &L.full[s], k, tile * kRows, L.act_e[ai]);
+              tma_load_3d(dst, &md, &L.full[s], w.k * 64, w.tile * kRows, e);
             }
           }
           if (++s == a.stages) {
@@ -445,85 +529,85 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
     }
   } else if (warp >= kGath0 && warp < kGath0 + kGath) {
     // ---------------------------------------------------------------- the tokens' rows
-    // Thread: the 16-byte piece c16 of rows rsub and rsub + 32 of every stage.  Rows past the expert's tokens hold
-    // whatever was there: they are columns of their own in the product.
-    const int ptid = tid - 32 * kGath0, c16 = ptid & 7, rsub = ptid >> 3;
-    int s = 0;
+    // The warps take stages in turn, so that several stages' loads are in flight whatever each waits for.  No more warps
+    // than the ring has stages: a warp's next stage must not lie more than one turn of the ring ahead of its last, or the
+    // parity that it waits for could be that of two turns before.  Lane: the 16-byte piece c16 of every fourth row.  Rows past
+    // the expert's tokens hold whatever was there: they are columns of their own in the product.
+    const int gj = warp - kGath0, c16 = lane & 7, rsub = lane >> 3;
+    const int turns = a.stages < kGath ? a.stages : kGath;
+    int turn = 0, s = 0;
     uint32_t par = 1;
     bool stop = false;
-    for (int ph = 0; ph < 2 && !stop; ++ph) {
-      const int c = ph ? c2 : c1;
-      const long long end = sh[ph].begin(b + 1);
-      long long q = sh[ph].begin(b);
-      if (ph == 1 && q < end) {
-        // every pair's activations are there
+    for (int l = 0; l < kLists && !stop; ++l) {
+      const List x = plan.list(l);
+      if (b >= x.G) continue;
+      if (x.ph == 1) {
+        // every pair's activations of this half are there
+        const List first = plan.list(x.half);
         int go = 0;
-        if (lane == 0) go = wait_count(&a.ctr[1], A * t1, &L.abort, a.timeout_ns, a.err) ? 1 : 0;
+        if (lane == 0)
+          go = wait_count(&a.ctr[kCtrItems + x.half], first.S / first.c, &L.abort, a.timeout_ns, a.err) ? 1 : 0;
         __syncwarp();
-        stop = !__shfl_sync(0xffffffffu, go, 0);
-      }
-      while (q < end && !stop) {
-        const long long item = q / c;
-        int k = static_cast<int>(q - item * c);
-        const int k1 = static_cast<int>(min(static_cast<long long>(c), k + (end - q)));
-        const int ai = ph == 0 ? static_cast<int>(item / t1) : static_cast<int>(item % A);
-        const int p0 = L.act_off[ai], m = L.act_off[ai + 1] - p0;
-        const int mh = (m + 7) & ~7;
-        // this thread's rows of the tile: source row and, of the second product's e4m3 form, its scale
-        const uint8_t* src[4];
-        float sc[4] = {1.0f, 1.0f, 1.0f, 1.0f};
-        const int rows = (!F8 && ph == 1) ? mh + m : m;
-        const int kbytes = ph == 0 ? a.d * es : a.n * (F8 ? 1 : 2);  // bytes of an operand row
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          int r = rsub + 32 * i;
-          src[i] = nullptr;
-          if (r >= rows) continue;
-          if (ph == 0) {
-            const long long t = L.ptok[p0 + r];
-            src[i] = F8 ? a.xq + t * a.d : reinterpret_cast<const uint8_t*>(a.X + t * a.ld_x);
-          } else if (F8) {
-            src[i] = reinterpret_cast<const uint8_t*>(a.A + static_cast<long long>(p0 + r) * a.n);
-            sc[i] = row_scale(__ldcg(a.amax + p0 + r));
-          } else if (r < m) {
-            src[i] = reinterpret_cast<const uint8_t*>(a.A + static_cast<long long>(p0 + r) * a.n);
-          } else if (r >= mh) {
-            src[i] = reinterpret_cast<const uint8_t*>(a.A_lo + static_cast<long long>(p0 + r - mh) * a.n);
-          }
+        if (!__shfl_sync(0xffffffffu, go, 0)) {
+          stop = true;
+          break;
         }
-        for (; k < k1; ++k, ++q) {
-          if (!mbar_wait(&L.empty[s], par, &L.abort, a.timeout_ns, a.err)) {
-            stop = true;
-            break;
-          }
+      }
+      Walk w;
+      for (w.start(x, b); w.q < w.end; w.next(x)) {
+        if (turn == gj) {
+          const int p0 = L.act_off[w.ai], m = L.act_off[w.ai + 1] - p0;
+          if (!mbar_wait(&L.empty[s], par, &L.abort, a.timeout_ns, a.err)) stop = true;
+          stop = __any_sync(0xffffffffu, stop);
+          if (stop) break;
           uint8_t* tok = ring + s * stage_bytes + kWBytes;
-          const int off = k * 128 + c16 * 16;
-          const bool in = off < kbytes;  // a last stage half past the reduction reads zeros (the weights do, too)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (!src[i]) continue;
-            const uint32_t o = sw128_offset(rsub + 32 * i, c16);
-            if (F8 && ph == 1) {
-              uint4 v = make_uint4(0, 0, 0, 0);
-              if (in) {
-                const uint4* x = reinterpret_cast<const uint4*>(src[i] + 2 * off);
-                v = codes16(__ldcg(x), __ldcg(x + 1), sc[i]);
-              }
-              *reinterpret_cast<uint4*>(tok + o) = v;
-            } else {
-              cp_async_16(smem_u32(tok) + o, in ? src[i] + off : src[i], in ? 16u : 0u);
+          const int off = w.k * 128 + c16 * 16;  // bytes of the operand's row; half a last stage may be past its end: zeros
+          if (x.ph == 0) {
+            const bool in = off < a.d * es;
+            const uint8_t* src = (F8 ? a.xq : reinterpret_cast<const uint8_t*>(a.X)) + (in ? off : 0);
+            const long long ld = F8 ? a.d : a.ld_x * 2;
+            for (int r = rsub; r < m; r += 4)
+              cp_async_16(smem_u32(tok) + sw128_offset(r, c16), src + L.ptok[p0 + r] * ld, in ? 16u : 0u);
+            cp_async_mbar_arrive_noinc(&L.full[s]);
+          } else if (!F8) {
+            const int mh = (m + 7) & ~7;
+            const uint8_t* hi = reinterpret_cast<const uint8_t*>(a.A + static_cast<long long>(p0) * a.n) + off;
+            const uint8_t* lo = reinterpret_cast<const uint8_t*>(a.A_lo + static_cast<long long>(p0) * a.n) + off;
+            for (int r = rsub; r < m; r += 4) {
+              const long long o = static_cast<long long>(r) * a.n * 2;
+              cp_async_16(smem_u32(tok) + sw128_offset(r, c16), hi + o, 16u);
+              cp_async_16(smem_u32(tok) + sw128_offset(mh + r, c16), lo + o, 16u);
             }
-          }
-          if (F8 && ph == 1) {
+            cp_async_mbar_arrive_noinc(&L.full[s]);
+          } else {
+            const bool in = off < a.n;
+            const uint4* src = reinterpret_cast<const uint4*>(a.A + static_cast<long long>(p0) * a.n + (in ? off : 0));
+            const int ld = a.n / 8;
+            for (int r0 = rsub; r0 < m; r0 += 16) {  // four rows' loads in flight
+              uint4 v[4][2];
+              float sc[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (r0 + 4 * i < m) {
+                  const uint4* row = src + static_cast<long long>(r0 + 4 * i) * ld;
+                  v[i][0] = __ldcg(row);
+                  v[i][1] = __ldcg(row + 1);
+                  sc[i] = row_scale(__ldcg(a.amax + p0 + r0 + 4 * i));
+                }
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (r0 + 4 * i < m)
+                  *reinterpret_cast<uint4*>(tok + sw128_offset(r0 + 4 * i, c16)) =
+                      in ? codes16(v[i][0], v[i][1], sc[i]) : make_uint4(0, 0, 0, 0);
+            }
             fence_proxy_async_smem();
             mbar_arrive(&L.full[s]);
-          } else {
-            cp_async_mbar_arrive_noinc(&L.full[s]);
           }
-          if (++s == a.stages) {
-            s = 0;
-            par ^= 1;
-          }
+        }
+        if (++turn == turns) turn = 0;
+        if (++s == a.stages) {
+          s = 0;
+          par ^= 1;
         }
       }
     }
@@ -534,15 +618,14 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
       int s = 0, acc = 0;
       uint32_t par = 0;
       bool stop = false;
-      for (int ph = 0; ph < 2 && !stop; ++ph) {
-        const int c = ph ? c2 : c1;
-        const long long end = sh[ph].begin(b + 1);
-        for (long long q = sh[ph].begin(b); q < end && !stop; ++acc) {
-          const long long item = q / c;
-          const int k0 = static_cast<int>(q - item * c);
-          const int k1 = static_cast<int>(min(static_cast<long long>(c), k0 + (end - q)));
-          const int ai = ph == 0 ? static_cast<int>(item / t1) : static_cast<int>(item % A);
-          const int N = columns(ph, L.act_off[ai + 1] - L.act_off[ai]);
+      for (int l = 0; l < kLists && !stop; ++l) {
+        const List x = plan.list(l);
+        if (b >= x.G) continue;
+        Walk w;
+        for (w.start(x, b); w.q < w.end && !stop; ++acc) {
+          const int k1 = min(x.c, w.k + (w.end - w.q));
+          const int m = L.act_off[w.ai + 1] - L.act_off[w.ai];
+          const int N = (!F8 && x.ph == 1) ? 2 * ((m + 7) & ~7) : (m + 15) & ~15;
           const uint32_t idesc = F8 ? idesc_e4m3(kRows, N, 0, 0) : idesc_bf16(kRows, N, 0, 0);
           if (!mbar_wait(&L.tempty[acc & 1], ((acc >> 1) & 1) ^ 1, &L.abort, a.timeout_ns, a.err)) {
             stop = true;
@@ -550,7 +633,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
           }
           tc_fence_after();
           const uint32_t d_tmem = tmem + (acc & 1) * acc_cols;
-          for (int k = k0; k < k1; ++k, ++q) {
+          uint32_t more = 0;
+          for (; w.k < k1; ++w.k, ++w.q) {
             if (!mbar_wait(&L.full[s], par, &L.abort, a.timeout_ns, a.err)) {
               stop = true;
               break;
@@ -559,9 +643,10 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
             tc_fence_after();
             const uint32_t sa = smem_u32(ring + s * stage_bytes), sb = sa + kWBytes;
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              umma_step<F8>(d_tmem, sdesc_sw128(sa + kk * 32, 16, 1024), sdesc_sw128(sb + kk * 32, 16, 1024), idesc,
-                            (k != k0 || kk) ? 1u : 0u);
+            for (int kk = 0; kk < 4; ++kk) {
+              umma_step<F8>(d_tmem, sdesc_sw128(sa + kk * 32, 16, 1024), sdesc_sw128(sb + kk * 32, 16, 1024), idesc, more);
+              more = 1;
+            }
             umma_commit(&L.empty[s]);
             if (++s == a.stages) {
               s = 0;
@@ -569,6 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
             }
           }
           if (!stop) umma_commit(&L.tfull[acc & 1]);
+          if (w.k == x.c) w.next_item(x);
         }
       }
       if (L.abort) {
@@ -580,24 +666,23 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
   } else {
     // ---------------------------------------------------------------- accumulators out (warps 0..3)
     // Warp w's lanes hold rows 32 w .. of the tile, a column per token.  The part of the block that has an item's first
-    // stage goes to the item's place, another block's to that block's own overflow rows (a block goes on with at most one
-    // item that began elsewhere).
+    // stage goes to the item's place, another block's to that block's own overflow rows (in a list a block goes on with at
+    // most one item that began elsewhere).
     const int row = tid;
     int acc = 0;
     bool stop = false;
-    for (int ph = 0; ph < 2 && !stop; ++ph) {
-      const int c = ph ? c2 : c1;
-      const long long end = sh[ph].begin(b + 1);
-      long long q = sh[ph].begin(b);
-      const bool any = q < end;
-      const long long ld = ph ? static_cast<long long>(t2) * kRows : static_cast<long long>(t1) * kRows;
-      for (; q < end; ++acc) {
-        const long long item = q / c;
-        const int k0 = static_cast<int>(q - item * c);
-        const int k1 = static_cast<int>(min(static_cast<long long>(c), k0 + (end - q)));
-        q += k1 - k0;
-        const int ai = ph == 0 ? static_cast<int>(item / t1) : static_cast<int>(item % A);
-        const int tile = ph == 0 ? static_cast<int>(item % t1) : static_cast<int>(item / A);
+    for (int l = 0; l < kLists && !stop; ++l) {
+      const List x = plan.list(l);
+      if (b >= x.G) continue;
+      const int ld = x.ph ? ld_y : ld_hu;
+      float* const first = x.ph ? a.y : a.hu;
+      float* const over = (x.ph ? a.ov2 : a.ov1) + static_cast<long long>(x.half) * kFewMaxBlocks * a.T * kRows;
+      Walk w;
+      for (w.start(x, b); w.q < w.end; ++acc) {
+        const int k0 = w.k, k1 = min(x.c, k0 + (w.end - w.q));
+        const int ai = w.ai, tile = w.tile, item = w.item(x);
+        w.q += k1 - k0;
+        if (k1 == x.c) w.next_item(x);
         const int p0 = L.act_off[ai], m = L.act_off[ai + 1] - p0, mh = (m + 7) & ~7;
         // one verdict for all: a thread alone at the barriers below would wait for ever
         if (!epi_all(mbar_wait(&L.tfull[acc & 1], (acc >> 1) & 1, &L.abort, a.timeout_ns, a.err))) {
@@ -607,18 +692,18 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
         tc_fence_after();
         const uint32_t tb = tmem + (static_cast<uint32_t>(warp * 32) << 16) + (acc & 1) * acc_cols;
         float* dst;
-        long long step;
+        int step;
         if (k0 == 0) {
-          dst = (ph ? a.y : a.hu) + p0 * ld + tile * kRows + row;
+          dst = first + static_cast<long long>(p0) * ld + tile * kRows + row;
           step = ld;
         } else {
-          dst = (ph ? a.ov2 : a.ov1) + static_cast<long long>(b) * a.T * kRows + row;
+          dst = over + static_cast<long long>(b) * a.T * kRows + row;
           step = kRows;
         }
         for (int j0 = 0; j0 < m; j0 += 8) {
           float v[8];
           tmem_ld8(tb + j0, v);
-          if (!F8 && ph == 1) {
+          if (!F8 && x.ph == 1) {
             float lo[8];
             tmem_ld8(tb + mh + j0, lo);
             tmem_ld_wait();
@@ -629,59 +714,72 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
           }
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            if (j0 + i < m) __stcg(dst + (j0 + i) * step, v[i]);
+            if (j0 + i < m) __stcg(dst + static_cast<long long>(j0 + i) * step, v[i]);
         }
         tc_fence_before();
         mbar_arrive(&L.tempty[acc & 1]);
-        if (ph == 1) continue;
+        if (x.ph == 1) continue;
         // first product: who completes the item makes its activations
         int b0 = b, b1 = b;
         epi_sync();
-        if (k1 - k0 < c) {
-          b0 = sh[0].owner(item * c);
-          b1 = sh[0].owner(item * c + c - 1);
-          if (tid == 0) {
-            __threadfence();
-            L.last = atomicAdd(&a.ctr[4 + b0], 1) == b1 - b0;
-            __threadfence();
-          }
+        if (k1 - k0 < x.c) {
+          b0 = x.owner(item * x.c);
+          b1 = x.owner(item * x.c + x.c - 1);
+          if (tid == 0) L.last = atom_acq_rel(&a.ctr[kCtrShared + x.half * kFewMaxBlocks + b0]) == b1 - b0;
           epi_sync();
           if (!L.last) continue;
         }
         const int e = L.act_e[ai];
-        for (int i = tid; i < m * 64; i += 32 * kEpi) {
-          const int j = i >> 6, r = i & 63;
-          const float* hu = a.hu + (p0 + j) * ld + tile * kRows + r;
-          float h = __ldcg(hu), u = __ldcg(hu + 64);
+        constexpr int U = 4;  // values of a thread at a time: their loads in flight together
+        for (int i0 = tid; i0 < m * 64; i0 += U * 32 * kEpi) {
+          float h[U], u[U];
+#pragma unroll
+          for (int q = 0; q < U; ++q) {
+            const int i = i0 + q * 32 * kEpi, j = i >> 6, r = i & 63;
+            const float* hu = a.hu + static_cast<long long>(p0 + j) * ld + tile * kRows + r;
+            h[q] = i < m * 64 ? __ldcg(hu) : 0.0f;
+            u[q] = i < m * 64 ? __ldcg(hu + 64) : 0.0f;
+          }
           for (int o = b0 + 1; o <= b1; ++o) {
-            const float* ov = a.ov1 + (static_cast<long long>(o) * a.T + j) * kRows + r;
-            h += __ldcg(ov);
-            u += __ldcg(ov + 64);
+#pragma unroll
+            for (int q = 0; q < U; ++q) {
+              const int i = i0 + q * 32 * kEpi, j = i >> 6, r = i & 63;
+              if (i < m * 64) {
+                const float* ov = over + (static_cast<long long>(o) * a.T + j) * kRows + r;
+                h[q] += __ldcg(ov);
+                u[q] += __ldcg(ov + 64);
+              }
+            }
           }
-          if (F8) {
-            const float sx = __ldcg(a.xs + L.ptok[p0 + j]);
-            const long long col = static_cast<long long>(e) * a.n + tile * 64 + r;
-            h *= sx * __ldg(a.wg_scale + col);
-            u *= sx * __ldg(a.wu_scale + col);
-          }
-          const float act = h * sigmoidf_(h) * u;
-          const __nv_bfloat16 hi = __float2bfloat16_rn(act);
-          const long long at = static_cast<long long>(p0 + j) * a.n + tile * 64 + r;
-          a.A[at] = hi;
-          if (F8) {
-            const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(__bfloat162float(hi))));
-            if (lane == 0) atomicMax(a.amax + p0 + j, top);
-          } else {
-            a.A_lo[at] = __float2bfloat16_rn(act - __bfloat162float(hi));
+#pragma unroll
+          for (int q = 0; q < U; ++q) {
+            const int i = i0 + q * 32 * kEpi, j = i >> 6, r = i & 63;
+            if (i >= m * 64) break;  // (the same for a whole warp)
+            if (F8) {
+              const float sx = __ldcg(a.xs + L.ptok[p0 + j]);
+              const long long col = static_cast<long long>(e) * a.n + tile * 64 + r;
+              h[q] *= sx * __ldg(a.wg_scale + col);
+              u[q] *= sx * __ldg(a.wu_scale + col);
+            }
+            const float act = h[q] * sigmoidf_(h[q]) * u[q];
+            const __nv_bfloat16 hi = __float2bfloat16_rn(act);
+            const long long at = static_cast<long long>(p0 + j) * a.n + tile * 64 + r;
+            a.A[at] = hi;
+            if (F8) {
+              const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(__bfloat162float(hi))));
+              if (lane == 0) atomicMax(a.amax + p0 + j, top);
+            } else {
+              a.A_lo[at] = __float2bfloat16_rn(act - __bfloat162float(hi));
+            }
           }
         }
         epi_sync();
-        if (tid == 0) red_release(&a.ctr[1]);
+        if (tid == 0) red_release(&a.ctr[kCtrItems + x.half], 1);
       }
-      if (ph == 1 && any && !stop) {
-        epi_sync();
-        if (tid == 0) red_release(&a.ctr[2]);
-      }
+    }
+    if (!stop) {
+      epi_sync();
+      if (tid == 0) red_release(&a.ctr[kCtrDone], 1);
     }
   }
 
@@ -690,27 +788,28 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
   tc_fence_after();
   if (warp == kMma) tmem_dealloc(tmem, tmem_cols);
   // ---- the weighted sums, once every block's parts are there: eight lanes a token and four columns, one a choice ----
-  if (tid == 0) L.ok = ok && !L.abort && wait_count(&a.ctr[2], sh[1].G, &L.abort, a.timeout_ns, a.err) ? 1 : 0;
+  if (tid == 0) L.ok = ok && !L.abort && wait_count(&a.ctr[kCtrDone], G, &L.abort, a.timeout_ns, a.err) ? 1 : 0;
   __syncthreads();
   if (!L.ok) return;
-  const int quads = a.d / 4;
-  const long long units = static_cast<long long>(a.T) * quads;
-  const long long u1 = units * (b + 1) / G;
-  for (long long u0 = units * b / G + 4 * warp; u0 < u1; u0 += 4 * kWarps) {
-    const long long u = u0 + (lane >> 3);
-    const int k = lane & 7;
+  const int quads = a.d / 4, units = a.T * quads;
+  const List y0 = plan.list(2), y1 = plan.list(3);
+  const int u1 = static_cast<int>(static_cast<long long>(units) * (b + 1) / G);
+  for (int u0 = static_cast<int>(static_cast<long long>(units) * b / G) + 4 * warp; u0 < u1; u0 += 4 * kWarps) {
+    const int u = u0 + (lane >> 3), k = lane & 7;
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    const int t = static_cast<int>(u < u1 ? u / quads : 0), col = static_cast<int>(u < u1 ? u - static_cast<long long>(t) * quads : 0) * 4;
+    const int t = u < u1 ? u / quads : 0, col = u < u1 ? (u - t * quads) * 4 : 0;
     if (u < u1 && k < a.K) {
       const int p = L.tok_pair[t * a.K + k], ai = L.tok_a[t * a.K + k];
-      const int tile = col / kRows, r = col % kRows;
-      v = __ldcg(reinterpret_cast<const float4*>(a.y + static_cast<long long>(p) * t2 * kRows + col));
-      const long long item = static_cast<long long>(tile) * A + ai;
-      const int b0 = sh[1].owner(item * c2), b1 = sh[1].owner(item * c2 + c2 - 1);
+      v = __ldcg(reinterpret_cast<const float4*>(a.y + static_cast<long long>(p) * ld_y + col));
+      const bool h = ai >= y1.a0;
+      const List& x = h ? y1 : y0;
+      const int s0 = ((ai - x.a0) * x.tiles + col / kRows) * x.c;
+      const int b0 = x.owner(s0), b1 = x.owner(s0 + x.c - 1);
+      const float* over = a.ov2 + static_cast<long long>(h) * kFewMaxBlocks * a.T * kRows;
       for (int o = b0 + 1; o <= b1; ++o) {
-        const float4 x = __ldcg(reinterpret_cast<const float4*>(
-            a.ov2 + (static_cast<long long>(o) * a.T + (p - L.act_off[ai])) * kRows + r));
-        v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+        const float4 z = __ldcg(reinterpret_cast<const float4*>(
+            over + (static_cast<long long>(o) * a.T + (p - L.act_off[ai])) * kRows + col % kRows));
+        v.x += z.x; v.y += z.y; v.z += z.z; v.w += z.w;
       }
       float w = L.pw[t * a.K + k];
       if (F8) {
@@ -744,7 +843,7 @@ FewLayout few_layout(int T, int d, int E, int n, int K) {
     return r;
   };
   const size_t P = static_cast<size_t>(T) * K;
-  l.nctr = 4 + kFewMaxBlocks;
+  l.nctr = kCtrShared + 2 * kFewMaxBlocks;
   l.ctr = take(sizeof(int) * l.nctr);
   l.amax = take(sizeof(uint32_t) * P);
   l.part = take(sizeof(float) * static_cast<size_t>(kFewMaxSplits) * T * E);
@@ -754,25 +853,26 @@ FewLayout few_layout(int T, int d, int E, int n, int K) {
   l.A = take(sizeof(__nv_bfloat16) * P * n);
   l.A_lo = take(sizeof(__nv_bfloat16) * P * n);
   l.y = take(sizeof(float) * P * ((d + kRows - 1) / kRows) * kRows);
-  l.ov1 = take(sizeof(float) * static_cast<size_t>(kFewMaxBlocks) * T * kRows);
-  l.ov2 = take(sizeof(float) * static_cast<size_t>(kFewMaxBlocks) * T * kRows);
+  l.ov1 = take(sizeof(float) * 2 * static_cast<size_t>(kFewMaxBlocks) * T * kRows);
+  l.ov2 = take(sizeof(float) * 2 * static_cast<size_t>(kFewMaxBlocks) * T * kRows);
   l.bytes = p;
   return l;
 }
 
-cudaError_t launch_few_router(const FewArgs& args, int num_sms, cudaStream_t s) {
+// Shares of d in the router's product: about four blocks an SM over all tokens, 64 rows a share at least.
+int few_splits(int T, int d, int E, int num_sms) {
+  const int blocks = (E + 15) / 16 * ((T + 7) / 8);
+  int sp = 4 * num_sms / blocks;
+  sp = sp < 1 ? 1 : sp > kFewMaxSplits ? kFewMaxSplits : sp;
+  return sp > d / 64 ? d / 64 : sp;
+}
+
+cudaError_t launch_few_router(const FewArgs& args, cudaStream_t s) {
   const int strips = (args.E + 15) / 16;
-  const int grid = strips * args.splits + (args.xq ? args.T : 1);
+  const dim3 grid(strips * args.splits + (args.xq ? args.T : 1), (args.T + 7) / 8);
   if (args.T == 1) few_router_kernel<1><<<grid, 256, 0, s>>>(args);
   else few_router_kernel<8><<<grid, 256, 0, s>>>(args);
   return cudaGetLastError();
-}
-
-int few_splits(int d, int E, int num_sms) {
-  const int strips = (E + 15) / 16;
-  int sp = num_sms / strips;
-  sp = sp < 1 ? 1 : sp > kFewMaxSplits ? kFewMaxSplits : sp;
-  return sp > d / 64 ? d / 64 : sp;
 }
 
 template <bool F8>
@@ -784,19 +884,22 @@ static cudaError_t launch(FewArgs args, const CUtensorMap& mg, const CUtensorMap
   const int stage_bytes = kWBytes + args.nrows * 128;
   const int room = static_cast<int>(kMaxSmem) - 1024 - static_cast<int>(sizeof(Lists));
   args.stages = room / stage_bytes < kMaxStages ? room / stage_bytes : kMaxStages;
+  if (args.stages < kMinStages) return cudaErrorInvalidConfiguration;
   const size_t smem = 1024 + static_cast<size_t>(args.stages) * stage_bytes + sizeof(Lists);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMaxSmem));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeCooperative;  // blocks wait for one another's parts: all of them resident at once
   attr[0].val.cooperative = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // its start overlaps the first launch's end
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3(few_blocks(num_sms), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kern, args, mg, mu, md);
 }
 

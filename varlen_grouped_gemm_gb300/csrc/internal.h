@@ -282,7 +282,7 @@ struct FewArgs {
   float* w;      // [T][K]
   __nv_bfloat16* O;
   long long ld_o;
-  int* ctr;         // [nctr] counters: choices, items with activations, blocks done, then one for each shared item
+  int* ctr;         // [nctr] counters
   uint32_t* amax;   // [P] largest |A| of a pair (e4m3)
   float* part;      // [splits][T][E] parts of the logits
   uint8_t* xq;      // [T][d]
@@ -290,7 +290,7 @@ struct FewArgs {
   float* hu;        // [P][n / 64][64 of H, 64 of U]: an item's first part
   __nv_bfloat16 *A, *A_lo;  // [P][n]
   float* y;         // [P][d rounded up to 128]
-  float *ov1, *ov2; // [blocks][T][128]: parts of items that began in another block
+  float *ov1, *ov2; // [2][blocks][T][128]: parts of items that began in another block
   int nctr, splits, stages, nrows;
   int* err;
   unsigned long long timeout_ns;
@@ -300,8 +300,9 @@ struct FewLayout {
   int nctr;
 };
 FewLayout few_layout(int T, int d, int E, int n, int K);
-int few_splits(int d, int E, int num_sms);
-cudaError_t launch_few_router(const FewArgs& args, int num_sms, cudaStream_t s);
+int few_blocks(int num_sms);
+int few_splits(int T, int d, int E, int num_sms);
+cudaError_t launch_few_router(const FewArgs& args, cudaStream_t s);
 // Maps over 16-bit units: gate and up with boxes of 64 rows, down of 128.
 cudaError_t launch_few_layer(const FewArgs& args, bool f8, const CUtensorMap& mg, const CUtensorMap& mu,
                              const CUtensorMap& md, int num_sms, cudaStream_t s);
