@@ -19,6 +19,8 @@
 // and A (rounded to bf16) per pair, as moe_quantize_rows_e4m3 does.  Sums are fp32; O is rounded once.
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
 #include "internal.h"
 
 namespace vgg {
@@ -93,7 +95,8 @@ __device__ __forceinline__ bool wait_count(const int* p, int target, volatile in
 // The work as lists of stages: the first product of the first half of the chosen experts, of the second half, then the second
 // product of either.  A list's items (an expert's 128-row tiles) are c stages each; block b of its G takes the stages
 // [b S / G, (b + 1) S / G).  With halves the activations that a block waits for at the second product's start have been
-// complete for half a product's time.
+// complete for half a product's time; a short list is one, since a further list is a further chain of steps (a block's
+// stages of the first product times 0.38 us against about 10 us: 1 x 2048 x 128 x 512, 13 stages, 41.5 us in halves).
 struct List {
   int ph, half, a0, tiles, c, S, G;
   __device__ __forceinline__ int begin(int b) const {
@@ -105,17 +108,18 @@ struct List {
   }
 };
 constexpr int kLists = 4;
+constexpr int kHalves = 32;  // stages of a block in the first product from which there are halves
 
 struct Plan {
-  int A, G, t1, c1, t2, c2;
+  int A, cut, G, t1, c1, t2, c2;  // cut: the second half's first expert
   __device__ __forceinline__ List list(int l) const {
     List x;
     x.ph = l >> 1;
     x.half = l & 1;
-    x.a0 = x.half ? A / 2 : 0;
+    x.a0 = x.half ? cut : 0;
     x.tiles = x.ph ? t2 : t1;
     x.c = x.ph ? c2 : c1;
-    x.S = ((x.half ? A : A / 2) - x.a0) * x.tiles * x.c;
+    x.S = ((x.half ? A : cut) - x.a0) * x.tiles * x.c;
     x.G = min(x.S, G);
     return x;
   }
@@ -189,12 +193,12 @@ __device__ __forceinline__ uint4 codes16(const uint4 x, const uint4 y, float s) 
 
 // ---- first launch: parts of the logits, X's codes, cleared counters -------------------------------------------------
 // Block (x, y), x < strips * splits: 16 experts (32 bytes of every row of W_r, a memory sector) times a share of d, for the
-// tokens NT y .. : part[split][t][e].  Thread: two experts (tid & 7) and four rows of every 128.  The blocks behind (y = 0)
+// tokens NT y .. : part[split][t][e].  Thread: two experts (tid & 7) and four rows of every 128, R times 128 rows at a time.  The blocks behind (y = 0)
 // clear the counters and, for the e4m3 form, quantize a token each.
-constexpr int kRtRows = 128;
-template <int NT>
+template <int NT, int R>
 __global__ void __launch_bounds__(256) few_router_kernel(const __grid_constant__ FewArgs a) {
   __shared__ float red[8][NT][16];
+  constexpr int kRtRows = 128 * R;
   __shared__ __align__(16) float s_x[NT][kRtRows];
   __shared__ float s_top[8];
   griddep_launch();  // the second launch's start may overlap; it waits for this one's end
@@ -246,12 +250,14 @@ __global__ void __launch_bounds__(256) few_router_kernel(const __grid_constant__
 #pragma unroll
   for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = 0.0f;
   for (int c = r0; c < r1; c += kRtRows) {
-    uint32_t w[4];
+    uint32_t w[R][4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      w[j] = (in && c + rg + j < r1)
-                 ? __ldg(reinterpret_cast<const uint32_t*>(a.W_r + static_cast<long long>(c + rg + j) * a.E + e0))
-                 : 0u;
+    for (int q = 0; q < R; ++q)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int r = c + 128 * q + rg + j;
+        w[q][j] = (in && r < r1) ? __ldg(reinterpret_cast<const uint32_t*>(a.W_r + static_cast<long long>(r) * a.E + e0)) : 0u;
+      }
     __syncthreads();
     for (int i = tid; i < NT * (kRtRows / 8); i += 256) {
       const int t = i / (kRtRows / 8), v = i % (kRtRows / 8) * 8;
@@ -263,18 +269,18 @@ __global__ void __launch_bounds__(256) few_router_kernel(const __grid_constant__
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      const float4 x = *reinterpret_cast<const float4*>(&s_x[i][rg]);
-      const float xv[4] = {x.x, x.y, x.z, x.w};
+    for (int q = 0; q < R; ++q)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 f = unpack_bf16x2(w[j]);
-        if (c + rg + j < r1) {  // (an infinite X beside a row that is not there)
+      for (int i = 0; i < NT; ++i) {
+        const float4 x = *reinterpret_cast<const float4*>(&s_x[i][128 * q + rg]);
+        const float xv[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 f = unpack_bf16x2(w[q][j]);  // zero past the share, as X's values there
           acc[i][0] = fmaf(xv[j], f.x, acc[i][0]);
           acc[i][1] = fmaf(xv[j], f.y, acc[i][1]);
         }
       }
-    }
   }
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
@@ -394,7 +400,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
   float* s_w = reinterpret_cast<float*>(s_ids + kMaxPairs);
   uint16_t* s_eoff = reinterpret_cast<uint16_t*>(s_w + kMaxPairs);  // [E] first pair, index
   uint16_t* s_ea = s_eoff + a.E;
-  for (int e = tid; e < a.E; e += kThreads) s_mask[e] = 0;
+  if (P > 32)
+    for (int e = tid; e < a.E; e += kThreads) s_mask[e] = 0;
   griddep_wait();  // the first launch's parts and cleared counters
   if (a.T <= kOwnChoice) {
     choose(a, 0, 1, a.T, keys, [&](int t, int k, int id, float w) {
@@ -424,6 +431,39 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
     __syncthreads();
   }
   const bool ok = L.ok != 0;  // the wait gave up: nothing below runs
+  if (P <= 32) {
+    // one warp, a lane a pair: its place is the number of pairs before it by (expert, token)
+    if (warp == 0) {
+      const int t = lane / a.K, e = lane < P ? s_ids[lane] : 0x7fff;
+      int p = 0, ai = 0, rank = 0;
+      bool head = true;
+      for (int j = 0; j < P; ++j) {
+        const int ej = __shfl_sync(0xffffffffu, e, j), tj = j / a.K;
+        p += ej < e || (ej == e && tj < t);
+        rank += tj == t && ej < e;
+        head = head && !(ej == e && tj < t);
+      }
+      for (int j = 0; j < P; ++j) {
+        const int ej = __shfl_sync(0xffffffffu, e, j), hj = __shfl_sync(0xffffffffu, static_cast<int>(head), j);
+        ai += hj && ej < e;
+      }
+      if (lane < P) {
+        if (head) {
+          L.act_e[ai] = static_cast<uint16_t>(e);
+          L.act_off[ai] = static_cast<uint16_t>(p);
+        }
+        L.ptok[p] = static_cast<uint8_t>(t);
+        L.tok_pair[t * a.K + rank] = static_cast<uint16_t>(p);
+        L.tok_a[t * a.K + rank] = static_cast<uint16_t>(ai);
+        L.pw[t * a.K + rank] = s_w[lane];
+      }
+      const int act = __popc(__ballot_sync(0xffffffffu, lane < P && head));
+      if (lane == 0) {
+        L.active = ok ? act : 0;
+        L.act_off[act] = static_cast<uint16_t>(P);
+      }
+    }
+  } else {
   if (ok)
     for (int i = tid; i < P; i += kThreads)
       atomicOr(reinterpret_cast<unsigned long long*>(&s_mask[s_ids[i]]), 1ull << (i / a.K));
@@ -472,6 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
       L.tok_a[t * a.K + rank] = s_ea[e];
       L.pw[t * a.K + rank] = s_w[i];
     }
+  }
   fence_proxy_async_smem();  // the scratch's uses come before the copies that overwrite it
   tc_fence_before();
   __syncthreads();
@@ -486,6 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
   plan.c1 = (a.d * es + 127) / 128;
   plan.t2 = (a.d + kRows - 1) / kRows;
   plan.c2 = (a.n * es + 127) / 128;
+  plan.cut = plan.A * plan.t1 * plan.c1 >= kHalves * G ? plan.A / 2 : 0;
   const int ld_hu = plan.t1 * kRows, ld_y = plan.t2 * kRows;
 
   if (warp >= kProd0) {
@@ -730,49 +772,64 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
           if (!L.last) continue;
         }
         const int e = L.act_e[ai];
-        constexpr int U = 4;  // values of a thread at a time: their loads in flight together
-        for (int i0 = tid; i0 < m * 64; i0 += U * 32 * kEpi) {
-          float h[U], u[U];
+        // U values of a thread and O parts of each at a time, their loads in flight together: an item cut into many parts is one
+        // of a short list, with few values
+        auto finish = [&](auto u_, auto o_) {
+          constexpr int U = decltype(u_)::value, O = decltype(o_)::value;
+          for (int i0 = tid; i0 < m * 64; i0 += U * 32 * kEpi) {
+            float h[U], u[U];
 #pragma unroll
-          for (int q = 0; q < U; ++q) {
-            const int i = i0 + q * 32 * kEpi, j = i >> 6, r = i & 63;
-            const float* hu = a.hu + static_cast<long long>(p0 + j) * ld + tile * kRows + r;
-            h[q] = i < m * 64 ? __ldcg(hu) : 0.0f;
-            u[q] = i < m * 64 ? __ldcg(hu + 64) : 0.0f;
-          }
-          for (int o = b0 + 1; o <= b1; ++o) {
+            for (int q = 0; q < U; ++q) {
+              const int i = i0 + q * 32 * kEpi;
+              const float* hu = a.hu + static_cast<long long>(p0 + (i >> 6)) * ld + tile * kRows + (i & 63);
+              h[q] = i < m * 64 ? __ldcg(hu) : 0.0f;
+              u[q] = i < m * 64 ? __ldcg(hu + 64) : 0.0f;
+            }
+            for (int o = b0 + 1; o <= b1; o += O) {
+              float y[U][O][2];
+#pragma unroll
+              for (int q = 0; q < U; ++q)
+#pragma unroll
+                for (int r = 0; r < O; ++r) {
+                  const int i = i0 + q * 32 * kEpi;
+                  const bool in = i < m * 64 && o + r <= b1;
+                  const float* ov = over + (static_cast<long long>(o + r) * a.T + (i >> 6)) * kRows + (i & 63);
+                  y[q][r][0] = in ? __ldcg(ov) : 0.0f;
+                  y[q][r][1] = in ? __ldcg(ov + 64) : 0.0f;
+                }
+#pragma unroll
+              for (int q = 0; q < U; ++q)
+#pragma unroll
+                for (int r = 0; r < O; ++r) {
+                  h[q] += y[q][r][0];
+                  u[q] += y[q][r][1];
+                }
+            }
 #pragma unroll
             for (int q = 0; q < U; ++q) {
               const int i = i0 + q * 32 * kEpi, j = i >> 6, r = i & 63;
-              if (i < m * 64) {
-                const float* ov = over + (static_cast<long long>(o) * a.T + j) * kRows + r;
-                h[q] += __ldcg(ov);
-                u[q] += __ldcg(ov + 64);
+              if (i >= m * 64) break;  // (the same for a whole warp)
+              if (F8) {
+                const float sx = __ldcg(a.xs + L.ptok[p0 + j]);
+                const long long col = static_cast<long long>(e) * a.n + tile * 64 + r;
+                h[q] *= sx * __ldg(a.wg_scale + col);
+                u[q] *= sx * __ldg(a.wu_scale + col);
+              }
+              const float act = h[q] * sigmoidf_(h[q]) * u[q];
+              const __nv_bfloat16 hi = __float2bfloat16_rn(act);
+              const long long at = static_cast<long long>(p0 + j) * a.n + tile * 64 + r;
+              a.A[at] = hi;
+              if (F8) {
+                const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(__bfloat162float(hi))));
+                if (lane == 0) atomicMax(a.amax + p0 + j, top);
+              } else {
+                a.A_lo[at] = __float2bfloat16_rn(act - __bfloat162float(hi));
               }
             }
           }
-#pragma unroll
-          for (int q = 0; q < U; ++q) {
-            const int i = i0 + q * 32 * kEpi, j = i >> 6, r = i & 63;
-            if (i >= m * 64) break;  // (the same for a whole warp)
-            if (F8) {
-              const float sx = __ldcg(a.xs + L.ptok[p0 + j]);
-              const long long col = static_cast<long long>(e) * a.n + tile * 64 + r;
-              h[q] *= sx * __ldg(a.wg_scale + col);
-              u[q] *= sx * __ldg(a.wu_scale + col);
-            }
-            const float act = h[q] * sigmoidf_(h[q]) * u[q];
-            const __nv_bfloat16 hi = __float2bfloat16_rn(act);
-            const long long at = static_cast<long long>(p0 + j) * a.n + tile * 64 + r;
-            a.A[at] = hi;
-            if (F8) {
-              const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(__bfloat162float(hi))));
-              if (lane == 0) atomicMax(a.amax + p0 + j, top);
-            } else {
-              a.A_lo[at] = __float2bfloat16_rn(act - __bfloat162float(hi));
-            }
-          }
-        }
+        };
+        if (b1 - b0 > 1) finish(std::integral_constant<int, 2>{}, std::integral_constant<int, 8>{});
+        else finish(std::integral_constant<int, 8>{}, std::integral_constant<int, 1>{});
         epi_sync();
         if (tid == 0) red_release(&a.ctr[kCtrItems + x.half], 1);
       }
@@ -806,10 +863,17 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
       const int s0 = ((ai - x.a0) * x.tiles + col / kRows) * x.c;
       const int b0 = x.owner(s0), b1 = x.owner(s0 + x.c - 1);
       const float* over = a.ov2 + static_cast<long long>(h) * kFewMaxBlocks * a.T * kRows;
-      for (int o = b0 + 1; o <= b1; ++o) {
-        const float4 z = __ldcg(reinterpret_cast<const float4*>(
-            over + (static_cast<long long>(o) * a.T + (p - L.act_off[ai])) * kRows + col % kRows));
-        v.x += z.x; v.y += z.y; v.z += z.z; v.w += z.w;
+      for (int o = b0 + 1; o <= b1; o += 4) {
+        float4 z[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          z[r] = o + r <= b1 ? __ldcg(reinterpret_cast<const float4*>(
+                                   over + (static_cast<long long>(o + r) * a.T + (p - L.act_off[ai])) * kRows + col % kRows))
+                             : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          v.x += z[r].x; v.y += z[r].y; v.z += z[r].z; v.w += z[r].w;
+        }
       }
       float w = L.pw[t * a.K + k];
       if (F8) {
@@ -870,8 +934,8 @@ int few_splits(int T, int d, int E, int num_sms) {
 cudaError_t launch_few_router(const FewArgs& args, cudaStream_t s) {
   const int strips = (args.E + 15) / 16;
   const dim3 grid(strips * args.splits + (args.xq ? args.T : 1), (args.T + 7) / 8);
-  if (args.T == 1) few_router_kernel<1><<<grid, 256, 0, s>>>(args);
-  else few_router_kernel<8><<<grid, 256, 0, s>>>(args);
+  if (args.T == 1) few_router_kernel<1, 4><<<grid, 256, 0, s>>>(args);
+  else few_router_kernel<8, 1><<<grid, 256, 0, s>>>(args);
   return cudaGetLastError();
 }
 

@@ -269,7 +269,7 @@ cudaError_t launch_router_dw_reduce(const float* sums, int splits, int d, int E,
 // ---- the layer for a few tokens ---------------------------------------------------------------
 constexpr int kFewMaxTokens = 64;
 constexpr int kFewMaxBlocks = 256;  // persistent blocks (bounds the workspace's overflow rows)
-constexpr int kFewMaxSplits = 32;   // shares of d in the router's product
+constexpr int kFewMaxSplits = 16;   // shares of d in the router's product
 // Pointers into the caller's arrays and the workspace.  xq, xs, wg_scale, wu_scale, wd_scale: the e4m3 form alone.
 struct FewArgs {
   const __nv_bfloat16* X;
