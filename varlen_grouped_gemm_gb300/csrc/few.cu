@@ -151,6 +151,13 @@ struct Walk {
   __device__ __forceinline__ int item(const List& x) const { return (ai - x.a0) * x.tiles + tile; }
 };
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
 __device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpi) : "memory"); }
 
 // The same barrier; true when every epilogue thread says so.
@@ -655,55 +662,53 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
     }
     cp_async_wait_all();
   } else if (warp == kMma) {
-    // ---------------------------------------------------------------- the products (lane 0)
-    if (lane == 0) {
-      int s = 0, acc = 0;
-      uint32_t par = 0;
-      bool stop = false;
-      for (int l = 0; l < kLists && !stop; ++l) {
-        const List x = plan.list(l);
-        if (b >= x.G) continue;
-        Walk w;
-        for (w.start(x, b); w.q < w.end && !stop; ++acc) {
-          const int k1 = min(x.c, w.k + (w.end - w.q));
-          const int m = L.act_off[w.ai + 1] - L.act_off[w.ai];
-          const int N = (!F8 && x.ph == 1) ? 2 * ((m + 7) & ~7) : (m + 15) & ~15;
-          const uint32_t idesc = F8 ? idesc_e4m3(kRows, N, 0, 0) : idesc_bf16(kRows, N, 0, 0);
-          if (!mbar_wait(&L.tempty[acc & 1], ((acc >> 1) & 1) ^ 1, &L.abort, a.timeout_ns, a.err)) {
-            stop = true;
-            break;
-          }
+    // ---------------------------------------------------------------- the products
+    // The whole warp goes through the stages, one lane issues: operands that all lanes agree on stay in uniform registers
+    // (issued out of a branch of lane 0's, a stage's four products took 300 cycles).
+    const bool one = elect_one();
+    int s = 0, acc = 0;
+    uint32_t par = 0;
+    bool stop = false;
+    for (int l = 0; l < kLists && !stop; ++l) {
+      const List x = plan.list(l);
+      if (b >= x.G) continue;
+      Walk w;
+      for (w.start(x, b); w.q < w.end && !stop; ++acc) {
+        const int k1 = min(x.c, w.k + (w.end - w.q));
+        const int m = L.act_off[w.ai + 1] - L.act_off[w.ai];
+        const int N = (!F8 && x.ph == 1) ? 2 * ((m + 7) & ~7) : (m + 15) & ~15;
+        const uint32_t idesc = F8 ? idesc_e4m3(kRows, N, 0, 0) : idesc_bf16(kRows, N, 0, 0);
+        stop = __any_sync(0xffffffffu, !mbar_wait(&L.tempty[acc & 1], ((acc >> 1) & 1) ^ 1, &L.abort, a.timeout_ns, a.err));
+        if (stop) break;
+        tc_fence_after();
+        const uint32_t d_tmem = tmem + (acc & 1) * acc_cols;
+        uint32_t more = 0;
+        for (; w.k < k1; ++w.k, ++w.q) {
+          stop = __any_sync(0xffffffffu, !mbar_wait(&L.full[s], par, &L.abort, a.timeout_ns, a.err));
+          if (stop) break;
+          fence_proxy_async_smem();  // cp.async writes -> operand reads
           tc_fence_after();
-          const uint32_t d_tmem = tmem + (acc & 1) * acc_cols;
-          uint32_t more = 0;
-          for (; w.k < k1; ++w.k, ++w.q) {
-            if (!mbar_wait(&L.full[s], par, &L.abort, a.timeout_ns, a.err)) {
-              stop = true;
-              break;
-            }
-            fence_proxy_async_smem();  // cp.async writes -> operand reads
-            tc_fence_after();
-            const uint32_t sa = smem_u32(ring + s * stage_bytes), sb = sa + kWBytes;
+          const uint32_t sa = smem_u32(ring + s * stage_bytes);
+          const uint64_t ad = sdesc_sw128(sa, 16, 1024), bd = sdesc_sw128(sa + kWBytes, 16, 1024);
+          if (one) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              umma_step<F8>(d_tmem, sdesc_sw128(sa + kk * 32, 16, 1024), sdesc_sw128(sb + kk * 32, 16, 1024), idesc, more);
-              more = 1;
-            }
+            for (int kk = 0; kk < 4; ++kk) umma_step<F8>(d_tmem, ad + 2 * kk, bd + 2 * kk, idesc, kk ? 1u : more);
             umma_commit(&L.empty[s]);
-            if (++s == a.stages) {
-              s = 0;
-              par ^= 1;
-            }
           }
-          if (!stop) umma_commit(&L.tfull[acc & 1]);
-          if (w.k == x.c) w.next_item(x);
+          more = 1;
+          if (++s == a.stages) {
+            s = 0;
+            par ^= 1;
+          }
         }
+        if (!stop && one) umma_commit(&L.tfull[acc & 1]);
+        if (w.k == x.c) w.next_item(x);
       }
-      if (L.abort) {
-        umma_commit(&L.drain);
-        volatile int never = 0;
-        mbar_wait(&L.drain, 0, &never, 20000000ull, nullptr);
-      }
+    }
+    if (L.abort && one) {
+      umma_commit(&L.drain);
+      volatile int never = 0;
+      mbar_wait(&L.drain, 0, &never, 20000000ull, nullptr);
     }
   } else {
     // ---------------------------------------------------------------- accumulators out (warps 0..3)
