@@ -605,6 +605,80 @@ int moe_router_backward(moe_ctx* ctx, const float* dlogits, const void* X, const
                         moe_stream_t stream);
 
 /*
+ * Activations kept in 8 bits.  Between its forward and its backward a training step keeps X, H and U of every layer (8
+ * bytes a pair and column of H and U in fp32, 2 a value of X).  The calls below keep them as whole numbers of 8 bits with a
+ * scale for every 32 columns of a row, 1.0625 bytes a value; the pages describe none of them ([SM] "3 기여 ①" keeps H for
+ * the backward), they are additions of this library.  For a block of 32 columns with values v:
+ *
+ *   scale = max|v| / 127 (fp32 division), rounded up to bf16, at least 2^-126; NaN for a block with an infinity or a NaN
+ *   code  = v * (1 / scale) rounded to the nearest whole number (ties to even), the reciprocal and the product in fp32
+ *   value = code * scale, rounded to bf16: what the backward takes the kept number for
+ *
+ * A value is off by at most scale / 2 and the rounding to bf16 (2^-8 of it).  Codes are int8 [rows, cols], scales bf16
+ * [rows, cols / 32]; both 16-byte aligned.
+ *
+ * moe_keep_rows8 / moe_read_rows8 — a bf16 matrix M [rows, cols] to codes and scales, and codes and scales to their values.
+ * cols a multiple of 32; rows = 0 does nothing.
+ */
+int moe_keep_rows8(moe_ctx* ctx, const void* M, long long rows, int cols, void* q, void* scales, moe_stream_t stream);
+int moe_read_rows8(moe_ctx* ctx, const void* q, const void* scales, long long rows, int cols, void* M, moe_stream_t stream);
+
+/*
+ * moe_grouped_gemm_fwd_kept8, _e4m3_kept8, _mx_kept8 — the forwards of those names with H and U kept in 8 bits: codes Hq, Uq
+ * [cap,n] and scales h_scale, u_scale [cap,n/32] in place of the fp32 H and U, written by the gate/up epilogue from its fp32
+ * values.  Rows at or past offsets[E] are not written.  Everything else, A and Yw among it, as without.
+ */
+int moe_grouped_gemm_fwd_kept8(moe_ctx* ctx, const void* X, const void* W_gate, const void* W_up, const void* W_down, int T,
+                               int d, int E, int n, long long cap, const int32_t* offsets, const int32_t* sorted_tok,
+                               const float* sorted_w, void* Hq, void* h_scale, void* Uq, void* u_scale, void* A, void* Yw,
+                               void* ws, size_t ws_bytes, moe_stream_t stream);
+int moe_grouped_gemm_fwd_e4m3_kept8(moe_ctx* ctx, const void* Xq, const float* x_scale, const void* Wg_q,
+                                    const float* wg_scale, const void* Wu_q, const float* wu_scale, const void* W_down,
+                                    const void* Wd_q, const float* wd_scale, int T, int d, int E, int n, long long cap,
+                                    const int32_t* offsets, const int32_t* sorted_tok, const float* sorted_w, void* Hq,
+                                    void* h_scale, void* Uq, void* u_scale, void* A, void* Aq, float* a_scale, void* Yw,
+                                    moe_stream_t stream);
+int moe_grouped_gemm_fwd_mx_kept8(moe_ctx* ctx, const void* Xq, const void* x_sf, const void* Wg_q, const void* Wu_q,
+                                  const void* gu_sf, const void* Wd_q, const void* dn_sf, int T, int d, int E, int n,
+                                  long long cap, const int32_t* offsets, const int32_t* sorted_tok, const float* sorted_w,
+                                  void* Hq, void* h_scale, void* Uq, void* u_scale, void* x_sf_tiles, void* Aq, void* a_sf,
+                                  void* Yw, moe_stream_t stream);
+
+/*
+ * moe_backward_kept8, _e4m3_kept8, _mx_kept8 — the backwards of those names from H and U kept in 8 bits, read in the dSwiGLU
+ * epilogue, and from X in bf16 or, with X == NULL, as codes Xq [T,d] and scales x_scale [T,d/32] (moe_keep_rows8).  The
+ * gradients are those of the layer at the kept values.  ws: at least moe_kept8_workspace_bytes(T, d, E, n, cap) bytes (0 on
+ * bad sizes; cap: the pair arrays' length).  Everything else as without; CTA pairs (moe_set_cta_pairs) do not apply to the
+ * dSwiGLU product here.
+ */
+size_t moe_kept8_workspace_bytes(int T, int d, int E, int n, long long cap);
+int moe_backward_kept8(moe_ctx* ctx, const void* dO, const void* X, const void* Xq, const void* x_scale, const void* W_r,
+                       const void* W_gate, const void* W_up, const void* W_down, int T, int d, int E, int n, int K, int m_tile,
+                       long long cap, const int32_t* topk_ids, const float* topk_w, const int32_t* offsets,
+                       const int32_t* sorted_tok, const float* sorted_w, const int32_t* tok_ptr, const int32_t* tok_pairs,
+                       const void* Hq, const void* h_scale, const void* Uq, const void* u_scale, void* dX, void* dW_gate,
+                       void* dW_up, void* dW_down, int dW_fp32, float* dS, float* dlogits, float* dW_r, void* ws,
+                       size_t ws_bytes, moe_stream_t stream);
+int moe_backward_e4m3_kept8(moe_ctx* ctx, const void* dO, const void* X, const void* Xq, const void* x_scale, const void* W_r,
+                            const void* W_gate, const void* W_up, const void* W_down, const void* Wgu_q,
+                            const float* wgu_scale, const void* Wdt_q, const float* wdt_scale, int T, int d, int E, int n,
+                            int K, int m_tile, long long cap, const int32_t* topk_ids, const float* topk_w,
+                            const int32_t* offsets, const int32_t* sorted_tok, const float* sorted_w, const int32_t* tok_ptr,
+                            const int32_t* tok_pairs, const void* Hq, const void* h_scale, const void* Uq,
+                            const void* u_scale, void* HUq, float* hu_scale, void* dOq, float* do_scale, void* dX,
+                            void* dW_gate, void* dW_up, void* dW_down, int dW_fp32, float* dS, float* dlogits, float* dW_r,
+                            void* ws, size_t ws_bytes, moe_stream_t stream);
+int moe_backward_mx_kept8(moe_ctx* ctx, const void* dO, const void* X, const void* Xq, const void* x_scale, const void* W_r,
+                          const void* W_gate, const void* W_up, const void* W_down, const void* Wdt_q, const void* wdt_sf,
+                          const void* Wgu_q, const void* wgu_sf, int T, int d, int E, int n, int K, int m_tile, long long cap,
+                          const int32_t* topk_ids, const float* topk_w, const int32_t* offsets, const int32_t* sorted_tok,
+                          const float* sorted_w, const int32_t* tok_ptr, const int32_t* tok_pairs, const void* Hq,
+                          const void* h_scale, const void* Uq, const void* u_scale, void* dOq, void* do_sf_tiles, void* HUq,
+                          void* hu_sf, void* dX, void* dW_gate, void* dW_up, void* dW_down, int dW_fp32, float* dS,
+                          float* dlogits, float* dW_r, void* ws, size_t ws_bytes, void* dw_ws, size_t dw_ws_bytes,
+                          moe_stream_t stream);
+
+/*
  * moe_forward_few — the whole layer for the few tokens of a decoding step (1 to 64), in two launches: router product;
  * choice, the chosen experts' three products and the weighted sums.  The pages describe no such call (their inference
  * path is out of the benchmark's scope); it is an addition of this library.  It computes what moe_route, moe_permute,

@@ -35,6 +35,9 @@ EXPORTS = (
     "moe_mx_dw_ws_bytes", "moe_add_rmsnorm", "moe_add_rmsnorm_workspace_bytes", "moe_add_rmsnorm_backward",
     "moe_balance_loss", "moe_balance_loss_workspace_bytes", "moe_router_backward",
     "moe_router_backward_workspace_bytes", "moe_few_workspace_bytes", "moe_forward_few", "moe_forward_few_e4m3",
+    "moe_keep_rows8", "moe_read_rows8", "moe_grouped_gemm_fwd_kept8", "moe_grouped_gemm_fwd_e4m3_kept8",
+    "moe_grouped_gemm_fwd_mx_kept8", "moe_kept8_workspace_bytes", "moe_backward_kept8", "moe_backward_e4m3_kept8",
+    "moe_backward_mx_kept8",
 )
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA, MOE_ERR_DEVICE, MOE_ERR_DEVICE_TIMEOUT = range(6)
@@ -121,6 +124,22 @@ def lib() -> ctypes.CDLL:
         L.moe_router_backward_workspace_bytes.argtypes = [_I, _I, _I]
         L.moe_router_backward_workspace_bytes.restype = _SZ
         L.moe_router_backward.argtypes = [_P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P, _P, _SZ, _P]
+        L.moe_keep_rows8.argtypes = [_P, _P, _LL, _I, _P, _P, _P]
+        L.moe_read_rows8.argtypes = [_P, _P, _P, _LL, _I, _P, _P]
+        L.moe_grouped_gemm_fwd_kept8.argtypes = [_P, _P, _P, _P, _P, _I, _I, _I, _I, _LL, _P, _P, _P, _P, _P, _P, _P, _P, _P,
+                                                 _P, _SZ, _P]
+        L.moe_grouped_gemm_fwd_e4m3_kept8.argtypes = [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _LL, _P, _P, _P,
+                                                      _P, _P, _P, _P, _P, _P, _P, _P, _P]
+        L.moe_grouped_gemm_fwd_mx_kept8.argtypes = [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _LL, _P, _P, _P, _P, _P,
+                                                    _P, _P, _P, _P, _P, _P, _P]
+        L.moe_kept8_workspace_bytes.argtypes = [_I, _I, _I, _I, _LL]
+        L.moe_kept8_workspace_bytes.restype = _SZ
+        L.moe_backward_kept8.argtypes = [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _LL] + [_P] * 7 + \
+            [_P] * 8 + [_I, _P, _P, _P, _P, _SZ, _P]
+        L.moe_backward_e4m3_kept8.argtypes = [_P] * 13 + [_I, _I, _I, _I, _I, _I, _LL] + [_P] * 7 + [_P] * 12 + \
+            [_I, _P, _P, _P, _P, _SZ, _P]
+        L.moe_backward_mx_kept8.argtypes = [_P] * 13 + [_I, _I, _I, _I, _I, _I, _LL] + [_P] * 7 + [_P] * 12 + \
+            [_I, _P, _P, _P, _P, _SZ, _P, _SZ, _P]
         L.moe_few_workspace_bytes.argtypes = [_I, _I, _I, _I, _I]
         L.moe_few_workspace_bytes.restype = _SZ
         L.moe_forward_few.argtypes = [_P, _P, _LL, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _LL, _P, _SZ, _P]
@@ -186,6 +205,49 @@ class Context:
     def set_cta_pairs(self, varlen_m: bool, varlen_k: bool):
         """CTA pairs (two CTAs per 256-row tile) for the tiled varlen-M and the weight-gradient GEMMs."""
         _check("moe_set_cta_pairs", lib().moe_set_cta_pairs(self.handle, int(varlen_m), int(varlen_k)))
+
+
+@dataclass
+class Kept8:
+    """Rows kept in 8 bits for the backward: codes ``q`` int8 [rows, cols] and bf16 scales ``scale`` [rows, cols / 32]."""
+
+    q: torch.Tensor
+    scale: torch.Tensor
+
+    @staticmethod
+    def empty(rows: int, cols: int, device="cuda") -> "Kept8":
+        if cols % 32:
+            raise ValueError(f"kept rows are whole blocks of 32 columns, got {cols}")
+        return Kept8(torch.zeros((rows, cols), dtype=torch.int8, device=device),
+                     torch.zeros((rows, cols // 32), dtype=torch.bfloat16, device=device))
+
+    @property
+    def shape(self):
+        return self.q.shape
+
+    def pointers(self, ctx: "Context", shape, name: str):
+        """(codes, scales) of rows of the given shape on the context's device."""
+        rows, cols = shape
+        if cols % 32:
+            raise ValueError(f"{name}: kept rows are whole blocks of 32 columns, got {cols}")
+        return (_flat(ctx, self.q, (rows, cols), torch.int8, f"{name}.q"),
+                _flat(ctx, self.scale, (rows, cols // 32), torch.bfloat16, f"{name}.scale"))
+
+
+def _kept_pair(ctx, H, U, shape):
+    """Pointers of H and U where they are kept in 8 bits, None where they are fp32 tensors (or absent)."""
+    if not isinstance(H, Kept8) and not isinstance(U, Kept8):
+        return None
+    if not (isinstance(H, Kept8) and isinstance(U, Kept8)):
+        raise ValueError("H and U are kept in the same way: both fp32 or both Kept8")
+    return (*H.pointers(ctx, shape, "H"), *U.pointers(ctx, shape, "U"))
+
+
+def _kept_x(ctx, X, T, d):
+    """(X, its codes, their scales) for a backward from kept activations: X a bf16 tensor or Kept8."""
+    if isinstance(X, Kept8):
+        return (None, *X.pointers(ctx, (T, d), "X"))
+    return (_ptr(X, torch.bfloat16, "X"), None, None)
 
 
 def moe_profile_enable(ctx: Context, enable: bool = True):
@@ -291,15 +353,37 @@ def moe_capacity_workspace_bytes(T: int, d: int, E: int, n: int, K: int, C: int)
 
 def moe_grouped_gemm_fwd(ctx, X, W_gate, W_up, W_down, offsets, sorted_tok, sorted_w, H, U, A, Yw, ws=None,
                          stream=None):
+    """The experts' products of every pair; H and U fp32 [cap, n], Kept8 (8 bits), or None (forward only)."""
     T, d = X.shape
     E, n, _ = W_gate.shape
     cap = sorted_tok.numel()
     wp, wb = _ws(ws)
     bf = torch.bfloat16
-    _check("moe_grouped_gemm_fwd", lib().moe_grouped_gemm_fwd(
-        ctx.handle, _ptr(X, bf), _ptr(W_gate, bf), _ptr(W_up, bf), _ptr(W_down, bf), T, d, E, n, cap,
-        _ptr(offsets, torch.int32), _ptr(sorted_tok, torch.int32), _ptr(sorted_w, torch.float32),
-        _ptr(H, torch.float32), _ptr(U, torch.float32), _ptr(A, bf), _ptr(Yw, bf), wp, wb, _stream(stream)))
+    head = (ctx.handle, _ptr(X, bf), _ptr(W_gate, bf), _ptr(W_up, bf), _ptr(W_down, bf), T, d, E, n, cap,
+            _ptr(offsets, torch.int32), _ptr(sorted_tok, torch.int32), _ptr(sorted_w, torch.float32))
+    tail = (_ptr(A, bf), _ptr(Yw, bf), wp, wb, _stream(stream))
+    kept = _kept_pair(ctx, H, U, (cap, n))
+    if kept:
+        _check("moe_grouped_gemm_fwd_kept8", lib().moe_grouped_gemm_fwd_kept8(*head, *kept, *tail))
+    else:
+        _check("moe_grouped_gemm_fwd", lib().moe_grouped_gemm_fwd(
+            *head, _ptr(H, torch.float32), _ptr(U, torch.float32), *tail))
+
+
+def moe_keep_rows8(ctx, M, kept: Kept8, stream=None):
+    """M [rows, cols] bf16 as codes and scales (one for 32 columns) into ``kept``."""
+    rows, cols = M.shape
+    q, scale = kept.pointers(ctx, (rows, cols), "kept")
+    _check("moe_keep_rows8", lib().moe_keep_rows8(
+        ctx.handle, _flat(ctx, M, (rows, cols), torch.bfloat16, "M"), rows, cols, q, scale, _stream(stream)))
+
+
+def moe_read_rows8(ctx, kept: Kept8, M, stream=None):
+    """The values that ``kept`` stands for into M [rows, cols] bf16."""
+    rows, cols = M.shape
+    q, scale = kept.pointers(ctx, (rows, cols), "kept")
+    _check("moe_read_rows8", lib().moe_read_rows8(
+        ctx.handle, q, scale, rows, cols, _flat(ctx, M, (rows, cols), torch.bfloat16, "M"), _stream(stream)))
 
 
 def moe_quantize_rows_e4m3(ctx, M, q, scales, stream=None):
@@ -321,11 +405,15 @@ def moe_grouped_gemm_fwd_e4m3(ctx, Xq, x_scale, Wg_q, wg_scale, Wu_q, wu_scale, 
     E, n, _ = Wg_q.shape
     cap = sorted_tok.numel()
     u8, f32 = torch.uint8, torch.float32
-    _check("moe_grouped_gemm_fwd_e4m3", lib().moe_grouped_gemm_fwd_e4m3(
-        ctx.handle, _ptr(Xq, u8), _ptr(x_scale, f32), _ptr(Wg_q, u8), _ptr(wg_scale, f32), _ptr(Wu_q, u8),
-        _ptr(wu_scale, f32), _ptr(W_down, torch.bfloat16), _ptr(Wd_q, u8), _ptr(wd_scale, f32), T, d, E, n, cap,
-        _ptr(offsets, torch.int32), _ptr(sorted_tok, torch.int32), _ptr(sorted_w, f32), _ptr(H, f32), _ptr(U, f32),
-        _ptr(A, torch.bfloat16), _ptr(Aq, u8), _ptr(a_scale, f32), _ptr(Yw, torch.bfloat16), _stream(stream)))
+    head = (ctx.handle, _ptr(Xq, u8), _ptr(x_scale, f32), _ptr(Wg_q, u8), _ptr(wg_scale, f32), _ptr(Wu_q, u8),
+            _ptr(wu_scale, f32), _ptr(W_down, torch.bfloat16), _ptr(Wd_q, u8), _ptr(wd_scale, f32), T, d, E, n, cap,
+            _ptr(offsets, torch.int32), _ptr(sorted_tok, torch.int32), _ptr(sorted_w, f32))
+    tail = (_ptr(A, torch.bfloat16), _ptr(Aq, u8), _ptr(a_scale, f32), _ptr(Yw, torch.bfloat16), _stream(stream))
+    kept = _kept_pair(ctx, H, U, (cap, n))
+    if kept:
+        _check("moe_grouped_gemm_fwd_e4m3_kept8", lib().moe_grouped_gemm_fwd_e4m3_kept8(*head, *kept, *tail))
+    else:
+        _check("moe_grouped_gemm_fwd_e4m3", lib().moe_grouped_gemm_fwd_e4m3(*head, _ptr(H, f32), _ptr(U, f32), *tail))
 
 
 def mx_sf_cols(cols: int) -> int:
@@ -384,11 +472,15 @@ def moe_grouped_gemm_fwd_mx(ctx, Xq, x_sf, w, offsets, sorted_tok, sorted_w, H, 
     E, n, _ = w.Wg_q.shape
     cap = sorted_tok.numel()
     u8, f32 = torch.uint8, torch.float32
-    _check("moe_grouped_gemm_fwd_mx", lib().moe_grouped_gemm_fwd_mx(
-        ctx.handle, _ptr(Xq, u8), _ptr(x_sf, u8), _ptr(w.Wg_q, u8), _ptr(w.Wu_q, u8), _ptr(w.gu_sf, u8),
-        _ptr(w.Wd_q, u8), _ptr(w.dn_sf, u8), T, d, E, n, cap, _ptr(offsets, torch.int32),
-        _ptr(sorted_tok, torch.int32), _ptr(sorted_w, f32), _ptr(H, f32), _ptr(U, f32), _ptr(x_sf_tiles, u8),
-        _ptr(Aq, u8), _ptr(a_sf, u8), _ptr(Yw, torch.bfloat16), _stream(stream)))
+    head = (ctx.handle, _ptr(Xq, u8), _ptr(x_sf, u8), _ptr(w.Wg_q, u8), _ptr(w.Wu_q, u8), _ptr(w.gu_sf, u8),
+            _ptr(w.Wd_q, u8), _ptr(w.dn_sf, u8), T, d, E, n, cap, _ptr(offsets, torch.int32),
+            _ptr(sorted_tok, torch.int32), _ptr(sorted_w, f32))
+    tail = (_ptr(x_sf_tiles, u8), _ptr(Aq, u8), _ptr(a_sf, u8), _ptr(Yw, torch.bfloat16), _stream(stream))
+    kept = _kept_pair(ctx, H, U, (cap, n))
+    if kept:
+        _check("moe_grouped_gemm_fwd_mx_kept8", lib().moe_grouped_gemm_fwd_mx_kept8(*head, *kept, *tail))
+    else:
+        _check("moe_grouped_gemm_fwd_mx", lib().moe_grouped_gemm_fwd_mx(*head, _ptr(H, f32), _ptr(U, f32), *tail))
 
 
 def moe_combine(ctx, Yw, tok_ptr, tok_pairs, O, stream=None):
@@ -401,20 +493,40 @@ def moe_combine(ctx, Yw, tok_ptr, tok_pairs, O, stream=None):
 def moe_backward(ctx, dO, X, W_r, W_gate, W_up, W_down, K, m_tile, topk_ids, topk_w, offsets, sorted_tok,
                  sorted_w, tok_ptr, tok_pairs, H, U, dX, dW_gate, dW_up, dW_down, dS, dlogits, dW_r, ws,
                  stream=None):
+    """Gradients of the layer.  With H and U as Kept8 (``ws`` of moe_kept8_workspace_bytes) X may be Kept8, too."""
     T, d = X.shape
     E, n, _ = W_gate.shape
     cap = sorted_tok.numel()
     wp, wb = _ws(ws)
-    bf = torch.bfloat16
-    dw_fp32 = 1 if dW_gate.dtype == torch.float32 else 0
-    _check("moe_backward", lib().moe_backward(
-        ctx.handle, _ptr(dO, bf), _ptr(X, bf), _ptr(W_r, bf), _ptr(W_gate, bf), _ptr(W_up, bf), _ptr(W_down, bf),
-        T, d, E, n, K, m_tile, cap, _ptr(topk_ids, torch.int32), _ptr(topk_w, torch.float32),
-        _ptr(offsets, torch.int32), _ptr(sorted_tok, torch.int32), _ptr(sorted_w, torch.float32),
-        _ptr(tok_ptr, torch.int32), _ptr(tok_pairs, torch.int32), _ptr(H, torch.float32), _ptr(U, torch.float32),
-        _ptr(dX, bf),
-        _ptr(dW_gate), _ptr(dW_up), _ptr(dW_down), dw_fp32, _ptr(dS, torch.float32),
-        _ptr(dlogits, torch.float32), _ptr(dW_r, torch.float32), wp, wb, _stream(stream)))
+    bf, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    dw_fp32 = 1 if dW_gate.dtype == f32 else 0
+    mid = (_ptr(W_r, bf), _ptr(W_gate, bf), _ptr(W_up, bf), _ptr(W_down, bf), T, d, E, n, K, m_tile, cap, _ptr(topk_ids, i32),
+           _ptr(topk_w, f32), _ptr(offsets, i32), _ptr(sorted_tok, i32), _ptr(sorted_w, f32), _ptr(tok_ptr, i32),
+           _ptr(tok_pairs, i32))
+    tail = (_ptr(dX, bf), _ptr(dW_gate), _ptr(dW_up), _ptr(dW_down), dw_fp32, _ptr(dS, f32), _ptr(dlogits, f32),
+            _ptr(dW_r, f32), wp, wb, _stream(stream))
+    kept = _kept_pair(ctx, H, U, (cap, n))
+    if kept:
+        _check("moe_backward_kept8", lib().moe_backward_kept8(
+            ctx.handle, _ptr(dO, bf), *_kept_x(ctx, X, T, d), *mid, *kept, *tail))
+    else:
+        _check("moe_backward", lib().moe_backward(
+            ctx.handle, _ptr(dO, bf), _ptr(_plain_x(X), bf), *mid, _ptr(H, f32), _ptr(U, f32), *tail))
+
+
+def _plain_x(X):
+    if isinstance(X, Kept8):
+        raise ValueError("X kept in 8 bits goes with H and U kept in 8 bits")
+    return X
+
+
+def moe_kept8_workspace_bytes(T: int, d: int, E: int, n: int, K: int, m_tile: int = 0, cap: int | None = None) -> int:
+    """Bytes of the workspace of a backward from activations kept in 8 bits (``cap``: the pair arrays' length where it is
+    not moe_pair_capacity(T, E, K, m_tile))."""
+    b = int(lib().moe_kept8_workspace_bytes(T, d, E, n, moe_pair_capacity(T, E, K, m_tile) if cap is None else cap))
+    if b <= 0:
+        raise ValueError(f"moe_kept8_workspace_bytes: invalid arguments T={T} d={d} E={E} n={n} K={K} m_tile={m_tile} cap={cap}")
+    return b
 
 
 def moe_quantize_dx_weights_e4m3(ctx, W_gate, W_up, Wgu_q, wgu_scale, stream=None):
@@ -446,14 +558,19 @@ def moe_backward_e4m3(ctx, dO, X, W_r, W_gate, W_up, W_down, Wgu_q, wgu_scale, W
     wp, wb = _ws(ws)
     bf, f32, i32 = torch.bfloat16, torch.float32, torch.int32
     dw_fp32 = 1 if dW_gate.dtype == torch.float32 else 0
-    _check("moe_backward_e4m3", lib().moe_backward_e4m3(
-        ctx.handle, _ptr(dO, bf), _ptr(X, bf), _ptr(W_r, bf), _ptr(W_gate, bf), _ptr(W_up, bf), _ptr(W_down, bf),
-        _ptr(Wgu_q, torch.uint8), _ptr(wgu_scale, f32), _ptr(Wdt_q, torch.uint8), _ptr(wdt_scale, f32), T, d, E, n,
-        K, m_tile, cap, _ptr(topk_ids, i32), _ptr(topk_w, f32), _ptr(offsets, i32), _ptr(sorted_tok, i32),
-        _ptr(sorted_w, f32), _ptr(tok_ptr, i32), _ptr(tok_pairs, i32), _ptr(H, f32), _ptr(U, f32),
-        _ptr(HUq, torch.uint8), _ptr(hu_scale, f32), _ptr(dOq, torch.uint8), _ptr(do_scale, f32), _ptr(dX, bf),
-        _ptr(dW_gate), _ptr(dW_up), _ptr(dW_down), dw_fp32, _ptr(dS, f32), _ptr(dlogits, f32), _ptr(dW_r, f32), wp,
-        wb, _stream(stream)))
+    mid = (_ptr(W_r, bf), _ptr(W_gate, bf), _ptr(W_up, bf), _ptr(W_down, bf), _ptr(Wgu_q, torch.uint8), _ptr(wgu_scale, f32),
+           _ptr(Wdt_q, torch.uint8), _ptr(wdt_scale, f32), T, d, E, n, K, m_tile, cap, _ptr(topk_ids, i32), _ptr(topk_w, f32),
+           _ptr(offsets, i32), _ptr(sorted_tok, i32), _ptr(sorted_w, f32), _ptr(tok_ptr, i32), _ptr(tok_pairs, i32))
+    tail = (_ptr(HUq, torch.uint8), _ptr(hu_scale, f32), _ptr(dOq, torch.uint8), _ptr(do_scale, f32), _ptr(dX, bf),
+            _ptr(dW_gate), _ptr(dW_up), _ptr(dW_down), dw_fp32, _ptr(dS, f32), _ptr(dlogits, f32), _ptr(dW_r, f32), wp, wb,
+            _stream(stream))
+    kept = _kept_pair(ctx, H, U, (cap, n))
+    if kept:
+        _check("moe_backward_e4m3_kept8", lib().moe_backward_e4m3_kept8(
+            ctx.handle, _ptr(dO, bf), *_kept_x(ctx, X, T, d), *mid, *kept, *tail))
+    else:
+        _check("moe_backward_e4m3", lib().moe_backward_e4m3(
+            ctx.handle, _ptr(dO, bf), _ptr(_plain_x(X), bf), *mid, _ptr(H, f32), _ptr(U, f32), *tail))
 
 
 # ------------------------------------------------------------------ around the layer
@@ -731,8 +848,8 @@ class Buffers:
     tok_ptr: torch.Tensor
     tok_pairs: torch.Tensor
     P: torch.Tensor
-    H: torch.Tensor
-    U: torch.Tensor
+    H: torch.Tensor | Kept8
+    U: torch.Tensor | Kept8
     A: torch.Tensor
     Yw: torch.Tensor
     O: torch.Tensor
@@ -764,13 +881,15 @@ class Buffers:
     mhuq: torch.Tensor | None = None
     mhusf: torch.Tensor | None = None
     mdw: torch.Tensor | None = None  # block-scaled weight gradients' workspace (moe_mx_dw_ws_bytes), on first use
+    xk: Kept8 | None = None  # activations kept in 8 bits: X (H and U are Kept8, too)
 
     @staticmethod
     def allocate(T, d, E, n, K, m_tile=0, backward=True, dW_dtype=torch.bfloat16, device="cuda", capacity=0,
-                 drop_policy="position", capacity_factor=0.0, e4m3=False, mx=False):
+                 drop_policy="position", capacity_factor=0.0, e4m3=False, mx=False, kept8=False):
         """Buffers for one configuration; capacity > 0 (or capacity_factor > 0, giving
         ceil(capacity_factor * T * K / E)) selects the capacity (drop/pad) dispatch with that many slots per
-        expert (pair-indexed arrays sized E * capacity)."""
+        expert (pair-indexed arrays sized E * capacity).  ``kept8``: the forwards keep X, H and U in 8 bits (Kept8) for the
+        backward, which then takes None for X."""
         if capacity_factor and not capacity:
             capacity = expert_capacity(T, E, K, capacity_factor)
         if capacity and m_tile:
@@ -785,13 +904,16 @@ class Buffers:
             moe_workspace_bytes(T, d, E, n, K, m_tile)
         if ws_bytes == 0:
             raise ValueError(f"unsupported sizes T={T} d={d} E={E} n={n} K={K}")
+        if kept8:
+            ws_bytes = max(ws_bytes, moe_kept8_workspace_bytes(T, d, E, n, K, cap=cap))
         return Buffers(
             T, d, E, n, K, m_tile, cap,
             logits=z((T, E), f32), scores=z((T, E), f32) if m_tile else None,
             topk_ids=z((T, K), i32), topk_w=z((T, K), f32), counts=z((E,), i32), offsets=z((E + 1,), i32),
             sorted_tok=z((cap,), i32), sorted_w=z((cap,), f32), tok_ptr=z((T + 1,), i32),
             tok_pairs=z((cap,), i32), P=z((1,), i32),
-            H=z((cap, n), f32), U=z((cap, n), f32), A=z((cap, n), bf), Yw=z((cap, d), bf), O=z((T, d), bf),
+            H=Kept8.empty(cap, n, device) if kept8 else z((cap, n), f32),
+            U=Kept8.empty(cap, n, device) if kept8 else z((cap, n), f32), xk=Kept8.empty(T, d, device) if kept8 else None, A=z((cap, n), bf), Yw=z((cap, d), bf), O=z((T, d), bf),
             dX=z((T, d), bf) if backward else None,
             dW_gate=z((E, n, d), dW_dtype) if backward else None,
             dW_up=z((E, n, d), dW_dtype) if backward else None,
@@ -815,9 +937,21 @@ class Buffers:
             mhusf=z((mx_act_sf_bytes(cap, E, 2 * n),), torch.uint8) if (mx and backward) else None)
 
 
+def _keep_x(ctx, X, buf: Buffers, cache, stream):
+    if cache and buf.xk is not None:
+        moe_keep_rows8(ctx, X, buf.xk, stream)
+
+
+def _kept_input(X, buf: Buffers):
+    """The backward's X: the caller's, or the one kept in 8 bits."""
+    if X is None and buf.xk is None:
+        raise ValueError("the backward needs X (buffers allocated with kept8=True keep it)")
+    return buf.xk if X is None else X
+
+
 def forward(ctx, X, W_r, bias, W_gate, W_up, W_down, buf: Buffers, stream=None, cache=True):
     """Routing, grouping, grouped GEMMs and combine; the output is ``buf.O``.  ``cache=False``: forward only,
-    the pre-activations H, U the backward needs are not written."""
+    the activations that the backward needs (H and U; with ``kept8`` buffers X, too) are not written."""
     moe_route(ctx, X, W_r, bias, buf.K, buf.logits, buf.scores, buf.topk_ids, buf.topk_w, buf.ws, stream)
     if buf.capacity:
         moe_permute_capacity(ctx, buf.topk_ids, buf.topk_w, buf.E, buf.capacity, buf.drop_policy, buf.counts,
@@ -826,6 +960,7 @@ def forward(ctx, X, W_r, bias, W_gate, W_up, W_down, buf: Buffers, stream=None, 
     else:
         moe_permute(ctx, buf.topk_ids, buf.topk_w, buf.logits, buf.scores, buf.E, buf.m_tile, buf.counts,
                     buf.offsets, buf.sorted_tok, buf.sorted_w, buf.tok_ptr, buf.tok_pairs, buf.P, buf.ws, stream)
+    _keep_x(ctx, X, buf, cache, stream)
     moe_grouped_gemm_fwd(ctx, X, W_gate, W_up, W_down, buf.offsets, buf.sorted_tok, buf.sorted_w,
                          buf.H if cache else None, buf.U if cache else None, buf.A, buf.Yw, buf.ws, stream)
     moe_combine(ctx, buf.Yw, buf.tok_ptr, buf.tok_pairs, buf.O, stream)
@@ -936,6 +1071,7 @@ def forward_e4m3(ctx, X, W_r, bias, w8: E4m3Weights, W_down, buf: Buffers, strea
                     buf.offsets, buf.sorted_tok, buf.sorted_w, buf.tok_ptr, buf.tok_pairs, buf.P, buf.ws, stream)
     if not quantized:
         moe_quantize_rows_e4m3(ctx, X, buf.xq, buf.xs, stream)
+    _keep_x(ctx, X, buf, cache, stream)
     moe_grouped_gemm_fwd_e4m3(ctx, buf.xq, buf.xs, w8.Wg_q, w8.wg_scale, w8.Wu_q, w8.wu_scale,
                               None if w8.Wd_q is not None else W_down, buf.offsets, buf.sorted_tok, buf.sorted_w,
                               buf.H if cache else None, buf.U if cache else None, buf.A, buf.Yw, Wd_q=w8.Wd_q,
@@ -962,6 +1098,7 @@ def forward_mx(ctx, X, W_r, bias, wmx: MxWeights, buf: Buffers, stream=None, cac
                     buf.offsets, buf.sorted_tok, buf.sorted_w, buf.tok_ptr, buf.tok_pairs, buf.P, buf.ws, stream)
     if not quantized:
         moe_quantize_rows_mx(ctx, X, buf.mxq, buf.mxsf, stream)
+    _keep_x(ctx, X, buf, cache, stream)
     moe_grouped_gemm_fwd_mx(ctx, buf.mxq, buf.mxsf, wmx, buf.offsets, buf.sorted_tok, buf.sorted_w,
                             buf.H if cache else None, buf.U if cache else None, buf.mxsft, buf.maq, buf.masf, buf.Yw,
                             stream)
@@ -977,6 +1114,7 @@ def backward_mx(ctx, dO, X, W_r, W_gate, W_up, W_down, wmx: MxWeights, buf: Buff
     quantization pass."""
     if wmx.Wdt_q is None or buf.mhuq is None:
         raise ValueError("block-scaled backward needs MxWeights.quantize(..., backward=True) and Buffers(mx=True)")
+    X = _kept_input(X, buf)
     T, d = X.shape
     E, n, _ = W_gate.shape
     cap = buf.sorted_tok.numel()
@@ -985,15 +1123,20 @@ def backward_mx(ctx, dO, X, W_r, W_gate, W_up, W_down, wmx: MxWeights, buf: Buff
     dw_fp32 = 1 if buf.dW_gate.dtype == f32 else 0
     if dw and buf.mdw is None:
         buf.mdw = torch.empty(mx_dw_ws_bytes(d, E, n, cap), dtype=u8, device=dO.device)
-    _check("moe_backward_mx", lib().moe_backward_mx(
-        ctx.handle, _ptr(dO, bf), _ptr(X, bf), _ptr(W_r, bf), _ptr(W_gate, bf), _ptr(W_up, bf), _ptr(W_down, bf),
-        _ptr(wmx.Wdt_q, u8), _ptr(wmx.wdt_sf, u8), _ptr(wmx.Wgu_q, u8), _ptr(wmx.wgu_sf, u8), T, d, E, n, buf.K,
-        buf.m_tile, cap, _ptr(buf.topk_ids, i32), _ptr(buf.topk_w, f32), _ptr(buf.offsets, i32),
-        _ptr(buf.sorted_tok, i32), _ptr(buf.sorted_w, f32), _ptr(buf.tok_ptr, i32), _ptr(buf.tok_pairs, i32),
-        _ptr(buf.H, f32), _ptr(buf.U, f32), _ptr(buf.mdoq, u8), _ptr(buf.mdosft, u8), _ptr(buf.mhuq, u8),
-        _ptr(buf.mhusf, u8), _ptr(buf.dX, bf), _ptr(buf.dW_gate), _ptr(buf.dW_up), _ptr(buf.dW_down), dw_fp32,
-        _ptr(buf.dS, f32), _ptr(buf.dlogits, f32), _ptr(buf.dW_r, f32), wp, wb,
-        _ptr(buf.mdw, u8) if dw else None, buf.mdw.numel() if dw else 0, _stream(stream)))
+    mid = (_ptr(W_r, bf), _ptr(W_gate, bf), _ptr(W_up, bf), _ptr(W_down, bf), _ptr(wmx.Wdt_q, u8), _ptr(wmx.wdt_sf, u8),
+           _ptr(wmx.Wgu_q, u8), _ptr(wmx.wgu_sf, u8), T, d, E, n, buf.K, buf.m_tile, cap, _ptr(buf.topk_ids, i32),
+           _ptr(buf.topk_w, f32), _ptr(buf.offsets, i32), _ptr(buf.sorted_tok, i32), _ptr(buf.sorted_w, f32),
+           _ptr(buf.tok_ptr, i32), _ptr(buf.tok_pairs, i32))
+    tail = (_ptr(buf.mdoq, u8), _ptr(buf.mdosft, u8), _ptr(buf.mhuq, u8), _ptr(buf.mhusf, u8), _ptr(buf.dX, bf),
+            _ptr(buf.dW_gate), _ptr(buf.dW_up), _ptr(buf.dW_down), dw_fp32, _ptr(buf.dS, f32), _ptr(buf.dlogits, f32),
+            _ptr(buf.dW_r, f32), wp, wb, _ptr(buf.mdw, u8) if dw else None, buf.mdw.numel() if dw else 0, _stream(stream))
+    kept = _kept_pair(ctx, buf.H, buf.U, (cap, n))
+    if kept:
+        _check("moe_backward_mx_kept8", lib().moe_backward_mx_kept8(
+            ctx.handle, _ptr(dO, bf), *_kept_x(ctx, X, T, d), *mid, *kept, *tail))
+    else:
+        _check("moe_backward_mx", lib().moe_backward_mx(
+            ctx.handle, _ptr(dO, bf), _ptr(_plain_x(X), bf), *mid, _ptr(buf.H, f32), _ptr(buf.U, f32), *tail))
 
 
 def backward_e4m3(ctx, dO, X, W_r, W_gate, W_up, W_down, w8: E4m3Weights, buf: Buffers, stream=None, dx=True,
@@ -1005,6 +1148,7 @@ def backward_e4m3(ctx, dO, X, W_r, W_gate, W_up, W_down, w8: E4m3Weights, buf: B
     quantization passes take most of what the shorter GEMMs save)."""
     if w8.Wgu_q is None or buf.huq is None:
         raise ValueError("e4m3 backward needs E4m3Weights.quantize(..., backward=True) and Buffers(e4m3=True)")
+    X = _kept_input(X, buf)
     moe_backward_e4m3(ctx, dO, X, W_r, W_gate, W_up, W_down, w8.Wgu_q if dx else None, w8.wgu_scale if dx else None,
                       w8.Wdt_q if dact else None, w8.wdt_scale if dact else None, buf.K, buf.m_tile, buf.topk_ids,
                       buf.topk_w, buf.offsets, buf.sorted_tok, buf.sorted_w, buf.tok_ptr, buf.tok_pairs, buf.H, buf.U,
@@ -1014,7 +1158,8 @@ def backward_e4m3(ctx, dO, X, W_r, W_gate, W_up, W_down, w8: E4m3Weights, buf: B
 
 
 def backward(ctx, dO, X, W_r, W_gate, W_up, W_down, buf: Buffers, stream=None):
-    moe_backward(ctx, dO, X, W_r, W_gate, W_up, W_down, buf.K, buf.m_tile, buf.topk_ids, buf.topk_w, buf.offsets,
+    """Gradients into ``buf``; X None: the X that a forward on ``kept8`` buffers kept."""
+    moe_backward(ctx, dO, _kept_input(X, buf), W_r, W_gate, W_up, W_down, buf.K, buf.m_tile, buf.topk_ids, buf.topk_w, buf.offsets,
                  buf.sorted_tok, buf.sorted_w, buf.tok_ptr, buf.tok_pairs, buf.H, buf.U, buf.dX, buf.dW_gate,
                  buf.dW_up, buf.dW_down, buf.dS, buf.dlogits, buf.dW_r, buf.ws, stream)
 

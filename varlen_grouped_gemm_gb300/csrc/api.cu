@@ -344,6 +344,37 @@ using namespace vgg;
     if (e_ != cudaSuccess) return MOE_ERR_CUDA;   \
   } while (0)
 
+// X, H and U kept in 8 bits: codes and scales (a call's outputs or inputs).
+struct Kept8 {
+  void *hq, *hs, *uq, *us;
+  const void *xq, *xs;  // the backward's X; null: X is given in bf16
+};
+static bool kept8_ok(const Kept8* k) {
+  return !k || (k->hq && k->hs && k->uq && k->us && aligned16(k->hq) && aligned16(k->uq) && aligned16(k->hs) && aligned16(k->us));
+}
+
+// Where a gate/up product leaves H and U: fp32 (their store maps too), or kept in 8 bits.
+static bool set_hu_outputs(GemmParams& p, Maps& m, void* H, void* U, const Kept8* k, int n, long long cap) {
+  p.out0 = k ? k->hq : H;
+  p.out1 = k ? k->uq : U;
+  if (k) {
+    p.k_h = static_cast<__nv_bfloat16*>(k->hs);
+    p.k_u = static_cast<__nv_bfloat16*>(k->us);
+    return true;
+  }
+  return !H || (make_store_map_2d(&m.o0, H, true, n, cap, n, 32) && make_store_map_2d(&m.o1, U, true, n, cap, n, 32));
+}
+// Where a dSwiGLU product finds them.
+static void set_hu_inputs(GemmParams& p, const void* H, const void* U, const Kept8* k, int n) {
+  p.in0 = static_cast<const float*>(k ? k->hq : H);
+  p.in1 = static_cast<const float*>(k ? k->uq : U);
+  p.ld_in = n;
+  if (k) {
+    p.k_h = static_cast<__nv_bfloat16*>(k->hs);
+    p.k_u = static_cast<__nv_bfloat16*>(k->us);
+  }
+}
+
 // Down projection of the sorted activation rows A, each row scaled by its combine weight (Yw).  With A_lo
 // (the bf16 rounding of what A's bf16 value leaves of the fp32 activation) the GEMM takes A as two parts.
 static int down_projection(moe_ctx* ctx, const void* A, const void* A_lo, const void* W_down, int d, int E, int n,
@@ -604,10 +635,9 @@ size_t moe_capacity_workspace_bytes(int T, int d, int E, int n, int K, int C) {
   return std::max({permute_ws_bytes(T, E, K, 1), bwd_ws_bytes(T, d, E, n, cap), route_ws_bytes(T, E)}) + kAlign;
 }
 
-int moe_grouped_gemm_fwd(moe_ctx* ctx, const void* X, const void* W_gate, const void* W_up, const void* W_down,
-                         int T, int d, int E, int n, long long cap, const int32_t* offsets,
-                         const int32_t* sorted_tok, const float* sorted_w, void* H, void* U, void* A, void* Yw,
-                         void* ws, size_t ws_bytes, moe_stream_t stream) {
+static int fwd_bf16(moe_ctx* ctx, const void* X, const void* W_gate, const void* W_up, const void* W_down, int T, int d,
+                    int E, int n, long long cap, const int32_t* offsets, const int32_t* sorted_tok, const float* sorted_w,
+                    void* H, void* U, const Kept8* kept, void* A, void* Yw, void* ws, size_t ws_bytes, moe_stream_t stream) {
   VGG_REQUIRE(ctx && X && W_gate && W_up && W_down && offsets && sorted_tok && sorted_w && A && Yw && ws);
   VGG_REQUIRE((H == nullptr) == (U == nullptr));  // both NULL: forward only, no backward cache
   VGG_REQUIRE(shapes_ok(T, d, E, n, 1));
@@ -633,23 +663,64 @@ int moe_grouped_gemm_fwd(moe_ctx* ctx, const void* X, const void* W_gate, const 
     p.a_rows = T;
     p.a_src = static_cast<const __nv_bfloat16*>(X);
     p.a_ld = d;
-    p.out0 = H;
-    p.out1 = U;
     p.out2 = A;
     p.out3 = A_lo;
     p.ld_out = n;
     const int BN = n > 64 ? 256 : 128;
     Maps m = zero_maps();
     if (!make_map_3d(&m.b0, W_gate, d, n, E, BN / 2) || !make_map_3d(&m.b1, W_up, d, n, E, BN / 2) ||
-        (H && (!make_store_map_2d(&m.o0, H, true, n, cap, n, 32) || !make_store_map_2d(&m.o1, U, true, n, cap, n, 32))) ||
-        !make_store_map_2d(&m.o2, A, false, n, cap, n, 32) || !make_store_map_2d(&m.o3, A_lo, false, n, cap, n, 32))
+        !set_hu_outputs(p, m, H, U, kept, n, cap) || !make_store_map_2d(&m.o2, A, false, n, cap, n, 32) || !make_store_map_2d(&m.o3, A_lo, false, n, cap, n, 32))
       return MOE_ERR_CUDA;
     const int tiles = (ceil_div(cap, BM) + E) * ceil_div(n, BN / 2);
     // pairs of CTAs on neighbouring column tiles share the gathered X rows (each gathers half)
     const int cn = ceil_div(n, BN / 2) >= 2 ? 2 : 1;
-    VGG_LAUNCH("gate_up_swiglu", run_gate_up_swiglu(BN, cn, p, m, std::min(tiles, ctx->num_sms), s));
+    const int grid = std::min(tiles, ctx->num_sms);
+    if (kept) VGG_LAUNCH("gate_up_swiglu_kept8", run_gate_up_swiglu_kept8(BN, cn, p, m, grid, s));
+    else VGG_LAUNCH("gate_up_swiglu", run_gate_up_swiglu(BN, cn, p, m, grid, s));
   }
   return down_projection(ctx, A, A_lo, W_down, d, E, n, cap, offsets, sorted_w, Yw, s);
+}
+
+int moe_grouped_gemm_fwd(moe_ctx* ctx, const void* X, const void* W_gate, const void* W_up, const void* W_down,
+                         int T, int d, int E, int n, long long cap, const int32_t* offsets,
+                         const int32_t* sorted_tok, const float* sorted_w, void* H, void* U, void* A, void* Yw,
+                         void* ws, size_t ws_bytes, moe_stream_t stream) {
+  return fwd_bf16(ctx, X, W_gate, W_up, W_down, T, d, E, n, cap, offsets, sorted_tok, sorted_w, H, U, nullptr, A, Yw, ws,
+                  ws_bytes, stream);
+}
+
+int moe_grouped_gemm_fwd_kept8(moe_ctx* ctx, const void* X, const void* W_gate, const void* W_up, const void* W_down, int T,
+                               int d, int E, int n, long long cap, const int32_t* offsets, const int32_t* sorted_tok,
+                               const float* sorted_w, void* Hq, void* h_scale, void* Uq, void* u_scale, void* A, void* Yw,
+                               void* ws, size_t ws_bytes, moe_stream_t stream) {
+  const Kept8 k{Hq, h_scale, Uq, u_scale, nullptr, nullptr};
+  VGG_REQUIRE(kept8_ok(&k));
+  return fwd_bf16(ctx, X, W_gate, W_up, W_down, T, d, E, n, cap, offsets, sorted_tok, sorted_w, nullptr, nullptr, &k, A, Yw,
+                  ws, ws_bytes, stream);
+}
+
+int moe_keep_rows8(moe_ctx* ctx, const void* M, long long rows, int cols, void* q, void* scales, moe_stream_t stream) {
+  VGG_REQUIRE(ctx && rows >= 0 && rows <= (1ll << 31) && cols >= 32 && cols % 32 == 0);
+  VGG_REQUIRE(rows == 0 || (M && q && scales));
+  VGG_REQUIRE(aligned16(M) && aligned16(q) && aligned16(scales));
+  DeviceGuard g(ctx->device);
+  if (!g.ok) return MOE_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  VGG_LAUNCH("keep_rows8", launch_keep_rows8(static_cast<const __nv_bfloat16*>(M), rows * cols, static_cast<uint8_t*>(q),
+                                             static_cast<__nv_bfloat16*>(scales), s));
+  return MOE_OK;
+}
+
+int moe_read_rows8(moe_ctx* ctx, const void* q, const void* scales, long long rows, int cols, void* M, moe_stream_t stream) {
+  VGG_REQUIRE(ctx && rows >= 0 && rows <= (1ll << 31) && cols >= 32 && cols % 32 == 0);
+  VGG_REQUIRE(rows == 0 || (M && q && scales));
+  VGG_REQUIRE(aligned16(M) && aligned16(q) && aligned16(scales));
+  DeviceGuard g(ctx->device);
+  if (!g.ok) return MOE_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  VGG_LAUNCH("read_rows8", launch_read_rows8(static_cast<const uint8_t*>(q), static_cast<const __nv_bfloat16*>(scales),
+                                             rows * cols, static_cast<__nv_bfloat16*>(M), s));
+  return MOE_OK;
 }
 
 int moe_quantize_rows_e4m3(moe_ctx* ctx, const void* M, long long rows, int cols, void* q, float* scales,
@@ -665,11 +736,11 @@ int moe_quantize_rows_e4m3(moe_ctx* ctx, const void* M, long long rows, int cols
   return MOE_OK;
 }
 
-int moe_grouped_gemm_fwd_e4m3(moe_ctx* ctx, const void* Xq, const float* x_scale, const void* Wg_q,
-                              const float* wg_scale, const void* Wu_q, const float* wu_scale, const void* W_down,
-                              const void* Wd_q, const float* wd_scale, int T, int d, int E, int n, long long cap,
-                              const int32_t* offsets, const int32_t* sorted_tok, const float* sorted_w, void* H,
-                              void* U, void* A, void* Aq, float* a_scale, void* Yw, moe_stream_t stream) {
+static int fwd_e4m3(moe_ctx* ctx, const void* Xq, const float* x_scale, const void* Wg_q, const float* wg_scale,
+                    const void* Wu_q, const float* wu_scale, const void* W_down, const void* Wd_q, const float* wd_scale,
+                    int T, int d, int E, int n, long long cap, const int32_t* offsets, const int32_t* sorted_tok,
+                    const float* sorted_w, void* H, void* U, const Kept8* kept, void* A, void* Aq, float* a_scale, void* Yw,
+                    moe_stream_t stream) {
   VGG_REQUIRE(ctx && Xq && x_scale && Wg_q && wg_scale && Wu_q && wu_scale && offsets && sorted_tok && sorted_w &&
               A && Yw);
   VGG_REQUIRE((H == nullptr) == (U == nullptr));  // both NULL: forward only, no backward cache
@@ -697,8 +768,6 @@ int moe_grouped_gemm_fwd_e4m3(moe_ctx* ctx, const void* Xq, const float* x_scale
     p.a_rows = T;
     p.a_src = static_cast<const __nv_bfloat16*>(Xq);
     p.a_ld = dk;
-    p.out0 = H;
-    p.out1 = U;
     p.out2 = A;
     p.ld_out = n;
     p.row_scale = x_scale;
@@ -708,12 +777,13 @@ int moe_grouped_gemm_fwd_e4m3(moe_ctx* ctx, const void* Xq, const float* x_scale
     const int BN = n > 64 ? 256 : 128;
     Maps m = zero_maps();
     if (!make_map_3d(&m.b0, Wg_q, dk, n, E, BN / 2) || !make_map_3d(&m.b1, Wu_q, dk, n, E, BN / 2) ||
-        (H && (!make_store_map_2d(&m.o0, H, true, n, cap, n, 32) || !make_store_map_2d(&m.o1, U, true, n, cap, n, 32))) ||
-        !make_store_map_2d(&m.o2, A, false, n, cap, n, 32))
+        !set_hu_outputs(p, m, H, U, kept, n, cap) || !make_store_map_2d(&m.o2, A, false, n, cap, n, 32))
       return MOE_ERR_CUDA;
     const int tiles = (ceil_div(cap, BM) + E) * ceil_div(n, BN / 2);
     const int cn = ceil_div(n, BN / 2) >= 2 ? 2 : 1;
-    VGG_LAUNCH("gate_up_swiglu_e4m3", run_gate_up_swiglu_e4m3(BN, cn, p, m, std::min(tiles, ctx->num_sms), s));
+    const int grid = std::min(tiles, ctx->num_sms);
+    if (kept) VGG_LAUNCH("gate_up_swiglu_e4m3_kept8", run_gate_up_swiglu_e4m3_kept8(BN, cn, p, m, grid, s));
+    else VGG_LAUNCH("gate_up_swiglu_e4m3", run_gate_up_swiglu_e4m3(BN, cn, p, m, grid, s));
   }
   if (!down8) return down_projection(ctx, A, nullptr, W_down, d, E, n, cap, offsets, sorted_w, Yw, s);
   // A's rows (those below offsets[E]) to e4m3, then the e4m3 down projection
@@ -744,6 +814,27 @@ int moe_grouped_gemm_fwd_e4m3(moe_ctx* ctx, const void* Xq, const float* x_scale
     VGG_LAUNCH("down_scale_e4m3", run_down_scale_e4m3(BN, p, m, std::min(tiles, ctx->num_sms), s));
   }
   return MOE_OK;
+}
+
+int moe_grouped_gemm_fwd_e4m3(moe_ctx* ctx, const void* Xq, const float* x_scale, const void* Wg_q,
+                              const float* wg_scale, const void* Wu_q, const float* wu_scale, const void* W_down,
+                              const void* Wd_q, const float* wd_scale, int T, int d, int E, int n, long long cap,
+                              const int32_t* offsets, const int32_t* sorted_tok, const float* sorted_w, void* H,
+                              void* U, void* A, void* Aq, float* a_scale, void* Yw, moe_stream_t stream) {
+  return fwd_e4m3(ctx, Xq, x_scale, Wg_q, wg_scale, Wu_q, wu_scale, W_down, Wd_q, wd_scale, T, d, E, n, cap, offsets,
+                  sorted_tok, sorted_w, H, U, nullptr, A, Aq, a_scale, Yw, stream);
+}
+
+int moe_grouped_gemm_fwd_e4m3_kept8(moe_ctx* ctx, const void* Xq, const float* x_scale, const void* Wg_q,
+                                    const float* wg_scale, const void* Wu_q, const float* wu_scale, const void* W_down,
+                                    const void* Wd_q, const float* wd_scale, int T, int d, int E, int n, long long cap,
+                                    const int32_t* offsets, const int32_t* sorted_tok, const float* sorted_w, void* Hq,
+                                    void* h_scale, void* Uq, void* u_scale, void* A, void* Aq, float* a_scale, void* Yw,
+                                    moe_stream_t stream) {
+  const Kept8 k{Hq, h_scale, Uq, u_scale, nullptr, nullptr};
+  VGG_REQUIRE(kept8_ok(&k));
+  return fwd_e4m3(ctx, Xq, x_scale, Wg_q, wg_scale, Wu_q, wu_scale, W_down, Wd_q, wd_scale, T, d, E, n, cap, offsets,
+                  sorted_tok, sorted_w, nullptr, nullptr, &k, A, Aq, a_scale, Yw, stream);
 }
 
 long long moe_mx_sf_cols(int cols) { return cols > 0 ? 4ll * ceil_div(cols, 128) : 0; }
@@ -852,10 +943,10 @@ int moe_quantize_weights_mx(moe_ctx* ctx, const void* W_gate, const void* W_up, 
   return MOE_OK;
 }
 
-int moe_grouped_gemm_fwd_mx(moe_ctx* ctx, const void* Xq, const void* x_sf, const void* Wg_q, const void* Wu_q,
-                            const void* gu_sf, const void* Wd_q, const void* dn_sf, int T, int d, int E, int n,
-                            long long cap, const int32_t* offsets, const int32_t* sorted_tok, const float* sorted_w,
-                            void* H, void* U, void* x_sf_tiles, void* Aq, void* a_sf, void* Yw, moe_stream_t stream) {
+static int fwd_mx(moe_ctx* ctx, const void* Xq, const void* x_sf, const void* Wg_q, const void* Wu_q, const void* gu_sf,
+                  const void* Wd_q, const void* dn_sf, int T, int d, int E, int n, long long cap, const int32_t* offsets,
+                  const int32_t* sorted_tok, const float* sorted_w, void* H, void* U, const Kept8* kept, void* x_sf_tiles,
+                  void* Aq, void* a_sf, void* Yw, moe_stream_t stream) {
   VGG_REQUIRE(ctx && Xq && x_sf && Wg_q && Wu_q && gu_sf && Wd_q && dn_sf && offsets && sorted_tok && sorted_w &&
               x_sf_tiles && Aq && a_sf && Yw);
   VGG_REQUIRE((H == nullptr) == (U == nullptr));  // both NULL: forward only, no backward cache
@@ -884,8 +975,6 @@ int moe_grouped_gemm_fwd_mx(moe_ctx* ctx, const void* Xq, const void* x_sf, cons
     p.a_rows = T;
     p.a_src = static_cast<const __nv_bfloat16*>(Xq);
     p.a_ld = dk;
-    p.out0 = H;
-    p.out1 = U;
     p.out2 = Aq;
     p.ld_out = n;
     p.a_sf = static_cast<const uint8_t*>(x_sf_tiles);
@@ -895,12 +984,14 @@ int moe_grouped_gemm_fwd_mx(moe_ctx* ctx, const void* Xq, const void* x_sf, cons
     p.o_sf_kst = ceil_div(n, 128);
     Maps m = zero_maps();
     if (!make_map_3d(&m.b0, Wg_q, dk, n, E, kMxBN / 2) || !make_map_3d(&m.b1, Wu_q, dk, n, E, kMxBN / 2) ||
-        (H && (!make_store_map_2d(&m.o0, H, true, n, cap, n, 32) || !make_store_map_2d(&m.o1, U, true, n, cap, n, 32))))
+        !set_hu_outputs(p, m, H, U, kept, n, cap))
       return MOE_ERR_CUDA;
     const int tiles = (ceil_div(cap, BM) + E) * ceil_div(n, kMxBN / 2);
     // pairs of CTAs on neighbouring column tiles share the gathered X rows (each gathers half the codes)
     const int cn = ceil_div(n, kMxBN / 2) >= 2 ? 2 : 1;
-    VGG_LAUNCH("gate_up_swiglu_mx", run_gate_up_swiglu_mx(cn, p, m, std::min(tiles, ctx->num_sms), s));
+    const int grid = std::min(tiles, ctx->num_sms);
+    if (kept) VGG_LAUNCH("gate_up_swiglu_mx_kept8", run_gate_up_swiglu_mx_kept8(cn, p, m, grid, s));
+    else VGG_LAUNCH("gate_up_swiglu_mx", run_gate_up_swiglu_mx(cn, p, m, grid, s));
   }
   {
     GemmParams p = base_params(ctx);
@@ -926,6 +1017,25 @@ int moe_grouped_gemm_fwd_mx(moe_ctx* ctx, const void* Xq, const void* x_sf, cons
     VGG_LAUNCH("down_scale_mx", run_down_scale_mx(BN, p, m, std::min(tiles, ctx->num_sms), s));
   }
   return MOE_OK;
+}
+
+int moe_grouped_gemm_fwd_mx(moe_ctx* ctx, const void* Xq, const void* x_sf, const void* Wg_q, const void* Wu_q,
+                            const void* gu_sf, const void* Wd_q, const void* dn_sf, int T, int d, int E, int n,
+                            long long cap, const int32_t* offsets, const int32_t* sorted_tok, const float* sorted_w,
+                            void* H, void* U, void* x_sf_tiles, void* Aq, void* a_sf, void* Yw, moe_stream_t stream) {
+  return fwd_mx(ctx, Xq, x_sf, Wg_q, Wu_q, gu_sf, Wd_q, dn_sf, T, d, E, n, cap, offsets, sorted_tok, sorted_w, H, U, nullptr,
+                x_sf_tiles, Aq, a_sf, Yw, stream);
+}
+
+int moe_grouped_gemm_fwd_mx_kept8(moe_ctx* ctx, const void* Xq, const void* x_sf, const void* Wg_q, const void* Wu_q,
+                                  const void* gu_sf, const void* Wd_q, const void* dn_sf, int T, int d, int E, int n,
+                                  long long cap, const int32_t* offsets, const int32_t* sorted_tok, const float* sorted_w,
+                                  void* Hq, void* h_scale, void* Uq, void* u_scale, void* x_sf_tiles, void* Aq, void* a_sf,
+                                  void* Yw, moe_stream_t stream) {
+  const Kept8 k{Hq, h_scale, Uq, u_scale, nullptr, nullptr};
+  VGG_REQUIRE(kept8_ok(&k));
+  return fwd_mx(ctx, Xq, x_sf, Wg_q, Wu_q, gu_sf, Wd_q, dn_sf, T, d, E, n, cap, offsets, sorted_tok, sorted_w, nullptr,
+                nullptr, &k, x_sf_tiles, Aq, a_sf, Yw, stream);
 }
 
 int moe_combine(moe_ctx* ctx, const void* Yw, const int32_t* tok_ptr, const int32_t* tok_pairs, int T, int d,
@@ -965,15 +1075,17 @@ static int backward_impl(moe_ctx* ctx, const void* dO, const void* X, const void
                          void* dW_up, void* dW_down, int dW_fp32, float* dS, float* dlogits, float* dW_r, void* ws,
                          size_t ws_bytes, moe_stream_t stream, const void* Wgu_q, const float* wgu_scale, void* HUq,
                          float* hu_scale, const void* Wdt_q, const float* wdt_scale, void* dOq, float* do_scale,
-                         const MxBwd* mx = nullptr) {
-  VGG_REQUIRE(ctx && dO && X && W_r && W_gate && W_up && W_down && topk_ids && topk_w && offsets && sorted_tok &&
-              sorted_w && tok_ptr && tok_pairs && H && U && dX && dW_gate && dW_up && dW_down && dS && dlogits &&
+                         const MxBwd* mx = nullptr, const Kept8* kept = nullptr) {
+  VGG_REQUIRE(kept8_ok(kept));
+  VGG_REQUIRE(X || (kept && kept->xq && kept->xs && aligned16(kept->xq) && aligned16(kept->xs)));
+  VGG_REQUIRE(ctx && dO && W_r && W_gate && W_up && W_down && topk_ids && topk_w && offsets && sorted_tok &&
+              sorted_w && tok_ptr && tok_pairs && (kept || (H && U)) && dX && dW_gate && dW_up && dW_down && dS && dlogits &&
               dW_r && ws);
   VGG_REQUIRE(shapes_ok(T, d, E, n, K));
   // cap: the pair arrays' length (moe_pair_capacity, or E*C for the capacity dispatch); the device checks
   // offsets[E] <= cap
   VGG_REQUIRE(m_tile >= 0 && cap >= 1 && cap < INT_MAX);
-  VGG_REQUIRE(ws_bytes >= bwd_ws_bytes(T, d, E, n, cap));
+  VGG_REQUIRE(ws_bytes >= (kept ? moe_kept8_workspace_bytes(T, d, E, n, cap) : bwd_ws_bytes(T, d, E, n, cap)));
   VGG_REQUIRE((reinterpret_cast<uintptr_t>(ws) & (kAlign - 1)) == 0);
   VGG_REQUIRE(aligned16(dO) && aligned16(X) && aligned16(W_r) && aligned16(W_gate) && aligned16(W_up) &&
               aligned16(W_down) && aligned16(H) && aligned16(U) && aligned16(dX) && aligned16(dW_gate) &&
@@ -982,6 +1094,12 @@ static int backward_impl(moe_ctx* ctx, const void* dO, const void* X, const void
   if (!g.ok) return MOE_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   BwdWs w = carve_bwd(ws, T, d, E, n, cap);
+  if (!X) {  // the values that X's codes stand for, once: the copies by expert and the router's product read them
+    __nv_bfloat16* const xv = reinterpret_cast<__nv_bfloat16*>(static_cast<uint8_t*>(ws) + bwd_ws_bytes(T, d, E, n, cap));
+    VGG_LAUNCH("read_rows8", launch_read_rows8(static_cast<const uint8_t*>(kept->xq),
+                                               static_cast<const __nv_bfloat16*>(kept->xs), static_cast<long long>(T) * d, xv, s));
+    X = xv;
+  }
   const bool f32 = dW_fp32 != 0;
   const int bn6 = dact_bn(n, cap, E, ctx->num_sms);
   // one dS partial per (column tile, epilogue column half); the block-scaled form tiles n by mx_tile_cols(n)
@@ -1048,9 +1166,7 @@ static int backward_impl(moe_ctx* ctx, const void* dO, const void* X, const void
     p.groups = E;
     p.offsets = offsets;
     p.rows_cap = static_cast<int>(cap);
-    p.in0 = static_cast<const float*>(H);
-    p.in1 = static_cast<const float*>(U);
-    p.ld_in = n;
+    set_hu_inputs(p, H, U, kept, n);
     p.out0 = w.dH;
     p.out1 = w.dU;
     p.out2 = w.Ap;
@@ -1077,7 +1193,9 @@ static int backward_impl(moe_ctx* ctx, const void* dO, const void* X, const void
     m.a1 = m.a0;
     m.b1 = m.b0;
     const int tiles = (ceil_div(cap, BM) + E) * ceil_div(n, BN);
-    VGG_LAUNCH("dact_dswiglu_mx", run_dact_dswiglu_mx(BN, p, m, std::min(tiles, ctx->num_sms), s));
+    const int grid = std::min(tiles, ctx->num_sms);
+    if (kept) VGG_LAUNCH("dact_dswiglu_mx_kept8", run_dact_dswiglu_mx_kept8(BN, p, m, grid, s));
+    else VGG_LAUNCH("dact_dswiglu_mx", run_dact_dswiglu_mx(BN, p, m, grid, s));
   } else if (Wdt_q) {
     // e4m3: the sorted dO code rows (gathered above, else the sorted rows below offsets[E] quantized here),
     // B = W_down^T quantized per row by moe_quantize_dact_weights_e4m3; rows handed to TMA as 16-bit units
@@ -1090,9 +1208,7 @@ static int backward_impl(moe_ctx* ctx, const void* dO, const void* X, const void
     p.groups = E;
     p.offsets = offsets;
     p.rows_cap = static_cast<int>(cap);
-    p.in0 = static_cast<const float*>(H);
-    p.in1 = static_cast<const float*>(U);
-    p.ld_in = n;
+    set_hu_inputs(p, H, U, kept, n);
     p.out0 = w.dH;
     p.out1 = w.dU;
     p.out2 = w.Ap;
@@ -1114,7 +1230,9 @@ static int backward_impl(moe_ctx* ctx, const void* dO, const void* X, const void
     m.a1 = m.a0;
     m.b1 = m.b0;
     const int tiles = (ceil_div(cap, BM) + E) * ceil_div(n, bn6);
-    VGG_LAUNCH("dact_dswiglu_e4m3", run_dact_dswiglu_e4m3(bn6, p, m, std::min(tiles, ctx->num_sms), s));
+    const int grid = std::min(tiles, ctx->num_sms);
+    if (kept) VGG_LAUNCH("dact_dswiglu_e4m3_kept8", run_dact_dswiglu_e4m3_kept8(bn6, p, m, grid, s));
+    else VGG_LAUNCH("dact_dswiglu_e4m3", run_dact_dswiglu_e4m3(bn6, p, m, grid, s));
   } else {
     GemmParams p = base_params(ctx);
     p.N = n;
@@ -1122,9 +1240,7 @@ static int backward_impl(moe_ctx* ctx, const void* dO, const void* X, const void
     p.groups = E;
     p.offsets = offsets;
     p.rows_cap = static_cast<int>(cap);
-    p.in0 = static_cast<const float*>(H);
-    p.in1 = static_cast<const float*>(U);
-    p.ld_in = n;
+    set_hu_inputs(p, H, U, kept, n);
     p.out0 = w.dH;
     p.out1 = w.dU;
     p.out2 = w.Ap;
@@ -1136,7 +1252,7 @@ static int backward_impl(moe_ctx* ctx, const void* dO, const void* X, const void
     p.part = w.part;
     p.part_ld = part_ld;
     p.a_offsets = poff;  // dO's sorted copy may be padded per expert
-    const VmShape sh = vm_shape(ctx, bn6, true, cap, E, n);
+    const VmShape sh = vm_shape(ctx, bn6, !kept, cap, E, n);  // (no CTA pairs with activations kept in 8 bits)
     Maps m = zero_maps();
     if (!make_map_2d(&m.a0, w.dOs, d, cap_pad, d, BM) || !make_chunked_map_3d(&m.b0, W_down, n, d, E, sh.b_cols / 64) ||
         !make_store_map_2d(&m.o0, w.dH, false, n, cap, n, 32) || !make_store_map_2d(&m.o1, w.dU, false, n, cap, n, 32) ||
@@ -1144,7 +1260,8 @@ static int backward_impl(moe_ctx* ctx, const void* dO, const void* X, const void
       return MOE_ERR_CUDA;
     m.a1 = m.a0;
     m.b1 = m.b0;
-    VGG_LAUNCH("dact_dswiglu", run_dact_dswiglu(bn6, sh.pair, p, m, sh.grid, s));
+    if (kept) VGG_LAUNCH("dact_dswiglu_kept8", run_dact_dswiglu_kept8(bn6, p, m, sh.grid, s));
+    else VGG_LAUNCH("dact_dswiglu", run_dact_dswiglu(bn6, sh.pair, p, m, sh.grid, s));
   }
   // dXp = [dH | dU] [W_gate[e]; W_up[e]]
   if (mx) {
@@ -1447,6 +1564,65 @@ int moe_backward_mx(moe_ctx* ctx, const void* dO, const void* X, const void* W_r
                        sorted_tok, sorted_w, tok_ptr, tok_pairs, H, U, dX, dW_gate, dW_up, dW_down, dW_fp32, dS,
                        dlogits, dW_r, ws, ws_bytes, stream, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr,
                        nullptr, nullptr, &mx);
+}
+
+size_t moe_kept8_workspace_bytes(int T, int d, int E, int n, long long cap) {
+  if (!shapes_ok(T, d, E, n, 1) || cap < 1 || cap >= INT_MAX) return 0;
+  return bwd_ws_bytes(T, d, E, n, cap) + al(sizeof(__nv_bfloat16) * static_cast<size_t>(T) * d);
+}
+
+int moe_backward_kept8(moe_ctx* ctx, const void* dO, const void* X, const void* Xq, const void* x_scale, const void* W_r,
+                       const void* W_gate, const void* W_up, const void* W_down, int T, int d, int E, int n, int K, int m_tile,
+                       long long cap, const int32_t* topk_ids, const float* topk_w, const int32_t* offsets,
+                       const int32_t* sorted_tok, const float* sorted_w, const int32_t* tok_ptr, const int32_t* tok_pairs,
+                       const void* Hq, const void* h_scale, const void* Uq, const void* u_scale, void* dX, void* dW_gate,
+                       void* dW_up, void* dW_down, int dW_fp32, float* dS, float* dlogits, float* dW_r, void* ws,
+                       size_t ws_bytes, moe_stream_t stream) {
+  const Kept8 k{const_cast<void*>(Hq), const_cast<void*>(h_scale), const_cast<void*>(Uq), const_cast<void*>(u_scale), Xq, x_scale};
+  return backward_impl(ctx, dO, X, W_r, W_gate, W_up, W_down, T, d, E, n, K, m_tile, cap, topk_ids, topk_w, offsets,
+                       sorted_tok, sorted_w, tok_ptr, tok_pairs, nullptr, nullptr, dX, dW_gate, dW_up, dW_down, dW_fp32, dS,
+                       dlogits, dW_r, ws, ws_bytes, stream, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr,
+                       nullptr, nullptr, &k);
+}
+
+int moe_backward_e4m3_kept8(moe_ctx* ctx, const void* dO, const void* X, const void* Xq, const void* x_scale, const void* W_r,
+                            const void* W_gate, const void* W_up, const void* W_down, const void* Wgu_q,
+                            const float* wgu_scale, const void* Wdt_q, const float* wdt_scale, int T, int d, int E, int n,
+                            int K, int m_tile, long long cap, const int32_t* topk_ids, const float* topk_w,
+                            const int32_t* offsets, const int32_t* sorted_tok, const float* sorted_w, const int32_t* tok_ptr,
+                            const int32_t* tok_pairs, const void* Hq, const void* h_scale, const void* Uq,
+                            const void* u_scale, void* HUq, float* hu_scale, void* dOq, float* do_scale, void* dX,
+                            void* dW_gate, void* dW_up, void* dW_down, int dW_fp32, float* dS, float* dlogits, float* dW_r,
+                            void* ws, size_t ws_bytes, moe_stream_t stream) {
+  VGG_REQUIRE(!Wgu_q || (wgu_scale && HUq && hu_scale && aligned16(Wgu_q) && aligned16(HUq)));
+  VGG_REQUIRE(!Wdt_q || (wdt_scale && dOq && do_scale && aligned16(Wdt_q) && aligned16(dOq)));
+  const Kept8 k{const_cast<void*>(Hq), const_cast<void*>(h_scale), const_cast<void*>(Uq), const_cast<void*>(u_scale), Xq, x_scale};
+  return backward_impl(ctx, dO, X, W_r, W_gate, W_up, W_down, T, d, E, n, K, m_tile, cap, topk_ids, topk_w, offsets,
+                       sorted_tok, sorted_w, tok_ptr, tok_pairs, nullptr, nullptr, dX, dW_gate, dW_up, dW_down, dW_fp32, dS,
+                       dlogits, dW_r, ws, ws_bytes, stream, Wgu_q, wgu_scale, HUq, hu_scale, Wdt_q, wdt_scale, dOq, do_scale,
+                       nullptr, &k);
+}
+
+int moe_backward_mx_kept8(moe_ctx* ctx, const void* dO, const void* X, const void* Xq, const void* x_scale, const void* W_r,
+                          const void* W_gate, const void* W_up, const void* W_down, const void* Wdt_q, const void* wdt_sf,
+                          const void* Wgu_q, const void* wgu_sf, int T, int d, int E, int n, int K, int m_tile, long long cap,
+                          const int32_t* topk_ids, const float* topk_w, const int32_t* offsets, const int32_t* sorted_tok,
+                          const float* sorted_w, const int32_t* tok_ptr, const int32_t* tok_pairs, const void* Hq,
+                          const void* h_scale, const void* Uq, const void* u_scale, void* dOq, void* do_sf_tiles, void* HUq,
+                          void* hu_sf, void* dX, void* dW_gate, void* dW_up, void* dW_down, int dW_fp32, float* dS,
+                          float* dlogits, float* dW_r, void* ws, size_t ws_bytes, void* dw_ws, size_t dw_ws_bytes,
+                          moe_stream_t stream) {
+  VGG_REQUIRE(Wdt_q && wdt_sf && Wgu_q && wgu_sf && dOq && do_sf_tiles && HUq && hu_sf);
+  VGG_REQUIRE(aligned16(Wdt_q) && aligned16(wdt_sf) && aligned16(Wgu_q) && aligned16(wgu_sf) && aligned16(dOq) &&
+              aligned16(do_sf_tiles) && aligned16(HUq) && aligned16(hu_sf));
+  VGG_REQUIRE(!dw_ws || ((reinterpret_cast<uintptr_t>(dw_ws) & (kAlign - 1)) == 0 &&
+                         dw_ws_bytes >= moe_mx_dw_ws_bytes(d, E, n, cap) && moe_mx_dw_ws_bytes(d, E, n, cap) > 0));
+  const MxBwd mx{Wdt_q, wdt_sf, Wgu_q, wgu_sf, dOq, do_sf_tiles, HUq, hu_sf, dw_ws};
+  const Kept8 k{const_cast<void*>(Hq), const_cast<void*>(h_scale), const_cast<void*>(Uq), const_cast<void*>(u_scale), Xq, x_scale};
+  return backward_impl(ctx, dO, X, W_r, W_gate, W_up, W_down, T, d, E, n, K, m_tile, cap, topk_ids, topk_w, offsets,
+                       sorted_tok, sorted_w, tok_ptr, tok_pairs, nullptr, nullptr, dX, dW_gate, dW_up, dW_down, dW_fp32, dS,
+                       dlogits, dW_r, ws, ws_bytes, stream, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr,
+                       nullptr, &mx, &k);
 }
 
 int moe_quantize_bwd_weights_mx(moe_ctx* ctx, const void* W_gate, const void* W_up, const void* W_down, int E, int d,

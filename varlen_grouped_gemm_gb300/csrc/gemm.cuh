@@ -88,7 +88,10 @@ enum VarMode { VAR_M = 0, VAR_K = 1, VAR_NONE = 2 };
 //             Varlen-K (the weight gradients): both operands are K-major code matrices [rows][K] whose groups
 //             each start on a whole stage (128 codes; the reduction padded per group with zero codes), one
 //             [N][K] matrix for B, and the scale blocks of both indexed by the stage of the whole reduction.
-enum XFlags { X_DUAL_A = 1, X_TRANS = 2, X_PAIR = 4, X_MX = 8 };
+//   X_KEPT8   H and U are kept in 8 bits (kept8_block32): the SwiGLU epilogues write their codes and scales (out0, out1,
+//             k_h, k_u) in place of fp32, the dSwiGLU epilogues read them (in0, in1).  A thread holds 32 columns of
+//             its row, a block with its scale, so nothing is exchanged.
+enum XFlags { X_DUAL_A = 1, X_TRANS = 2, X_PAIR = 4, X_MX = 8, X_KEPT8 = 16 };
 enum EpiKind {
   EPI_STORE = 0, EPI_SWIGLU = 1, EPI_SCALE = 2, EPI_DSWIGLU = 3, EPI_SWIGLU_Q = 4, EPI_SCALE_Q = 5, EPI_STORE_Q = 6,
   EPI_DSWIGLU_Q = 7, EPI_ADD = 8
@@ -147,6 +150,7 @@ struct GemmParams {
   int sf_kst;
   uint8_t* o_sf;
   int o_sf_kst;
+  __nv_bfloat16 *k_h, *k_u;  // X_KEPT8: scales of H and U, [rows][N / 32]
   uint8_t* o_q;        // the dSwiGLU epilogue's block-scaled [dH | dU] codes [rows][o_q_ld] (o_sf: their blocks)
   long long o_q_ld;
   int* err;
@@ -452,6 +456,9 @@ __global__ void __launch_bounds__(WarpPlan<STAGES, EW, AMODE, BMODE, CN, XF>::kT
   constexpr bool kTrans = (XF & X_TRANS) != 0;
   constexpr bool kPair = (XF & X_PAIR) != 0;
   constexpr bool kMx = (XF & X_MX) != 0;
+  constexpr bool kKept8 = (XF & X_KEPT8) != 0;
+  static_assert(!kKept8 || EPI == EPI_SWIGLU || EPI == EPI_SWIGLU_Q || EPI == EPI_DSWIGLU || EPI == EPI_DSWIGLU_Q,
+                "activations kept in 8 bits: the SwiGLU epilogues and their gradient's");
   constexpr int kSfStage = mx_stage_bytes(BN, XF);
   using L = SmemLayout<BN, STAGES, EW, DEPTH, kDual ? 2 : 1, kPair ? BN / 2 : BN, kSfStage>;
   static_assert(EW == 4 || EW == 8, "4 or 8 epilogue warps");
@@ -1289,7 +1296,13 @@ __global__ void __launch_bounds__(WarpPlan<STAGES, EW, AMODE, BMODE, CN, XF>::kT
                 u[i] *= sx * __shfl_sync(0xffffffffu, ul, i);
               }
             }
-            if (p.out0) {  // H, U stay fp32 for the backward; a forward-only call passes neither
+            if constexpr (kKept8) {
+              if (row_ok && ncols > 0) {  // N is a multiple of 64: a block is there or not
+                const long long at = orow * p.ld_out + col;
+                kept8_block32(h, static_cast<uint8_t*>(p.out0) + at, p.k_h + at / 32);
+                kept8_block32(u, static_cast<uint8_t*>(p.out1) + at, p.k_u + at / 32);
+              }
+            } else if (p.out0) {  // H, U stay fp32 for the backward; a forward-only call passes neither
               emit32(o0, h, col, ncols, full, row_ok, true);
               emit32(o1, u, col, ncols, full, row_ok, true);
             }
@@ -1370,7 +1383,11 @@ __global__ void __launch_bounds__(WarpPlan<STAGES, EW, AMODE, BMODE, CN, XF>::kT
                 r[i] = __float_as_uint(__uint_as_float(r[i]) * sq * __shfl_sync(0xffffffffu, cs, i));
             }
             float h[32], u[32];
-            if (row_ok) {
+            if (kKept8 && row_ok) {
+              const long long at = orow * p.ld_in + col;
+              kept8_load32(reinterpret_cast<const uint8_t*>(p.in0) + at, p.k_h + at / 32, h);
+              kept8_load32(reinterpret_cast<const uint8_t*>(p.in1) + at, p.k_u + at / 32, u);
+            } else if (row_ok) {
               load_f32_row32(p.in0 + orow * p.ld_in + col, h, ncols);
               load_f32_row32(p.in1 + orow * p.ld_in + col, u, ncols);
             } else {

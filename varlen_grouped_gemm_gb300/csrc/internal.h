@@ -266,6 +266,17 @@ cudaError_t launch_router_dw(const __nv_bfloat16* X, const __nv_bfloat16* parts,
 // out[i][e] = in[i][e] (or 0) + sum_s sums[s][e][i], in a fixed order.
 cudaError_t launch_router_dw_reduce(const float* sums, int splits, int d, int E, const float* in, float* out, cudaStream_t s);
 
+// ---- activations kept in 8 bits ----------------------------------------------------------------
+cudaError_t run_gate_up_swiglu_kept8(int BN, int cn, const GemmParams& p, const Maps& m, int grid, cudaStream_t s);
+cudaError_t run_gate_up_swiglu_e4m3_kept8(int BN, int cn, const GemmParams& p, const Maps& m, int grid, cudaStream_t s);
+cudaError_t run_gate_up_swiglu_mx_kept8(int cn, const GemmParams& p, const Maps& m, int grid, cudaStream_t s);
+cudaError_t run_dact_dswiglu_kept8(int BN, const GemmParams& p, const Maps& m, int grid, cudaStream_t s);
+cudaError_t run_dact_dswiglu_e4m3_kept8(int BN, const GemmParams& p, const Maps& m, int grid, cudaStream_t s);
+cudaError_t run_dact_dswiglu_mx_kept8(int BN, const GemmParams& p, const Maps& m, int grid, cudaStream_t s);
+// n values (a multiple of 32) in rows of whole blocks; scale [n / 32]
+cudaError_t launch_keep_rows8(const __nv_bfloat16* M, long long n, uint8_t* q, __nv_bfloat16* scale, cudaStream_t s);
+cudaError_t launch_read_rows8(const uint8_t* q, const __nv_bfloat16* scale, long long n, __nv_bfloat16* M, cudaStream_t s);
+
 // ---- the layer for a few tokens ---------------------------------------------------------------
 constexpr int kFewMaxTokens = 64;
 constexpr int kFewMaxBlocks = 256;  // persistent blocks (bounds the workspace's overflow rows)
