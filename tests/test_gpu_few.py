@@ -165,3 +165,134 @@ def test_matches_64_bits(vgg, ctx, case, form):
     got = call(vgg, ctx, s, form, w8)
     assert vgg.moe_get_error(ctx) == (vgg.MOE_OK, 0)
     check(got, reference(s, form, w8))
+
+
+def test_more_tokens_than_a_round_and_every_width(vgg, ctx):
+    """Every number of tokens once, on sizes that change the ring, the tiles' halves and the lists."""
+    for T in range(1, 65):
+        s = make(T, 64 * (1 + T % 5), 8 * (1 + T % 4), 64 * (1 + T % 3), 1 + T % 8, seed=T)
+        check(call(vgg, ctx, s), reference(s, "bf16"))
+    assert vgg.moe_get_error(ctx) == (vgg.MOE_OK, 0)
+
+
+def test_rows_of_larger_matrices(vgg, ctx):
+    s = make(11, 192, 16, 64, 4, seed=5)
+    X = torch.full((11, 200), float("nan"), dtype=BF, device="cuda")
+    X[:, :192] = s["X"]
+    O = torch.full((11, 196), 7.0, dtype=BF, device="cuda")
+    plain = call(vgg, ctx, s)
+    got = call(vgg, ctx, s, X=X[:, :192], O=O[:, :192])
+    assert torch.equal(O[:, :192], plain[0]) and (O[:, 192:] == 7.0).all()
+    assert torch.equal(got[1], plain[1]) and torch.equal(got[2], plain[2])
+
+
+@pytest.mark.parametrize("form", ["bf16", "e4m3"])
+def test_same_bits_again_and_on_another_stream_and_in_a_graph(vgg, ctx, form):
+    s = make(40, 512, 64, 192, 6, seed=6)
+    w8 = weights8(vgg, ctx, s) if form == "e4m3" else None
+    want = [t.clone() for t in call(vgg, ctx, s, form, w8)]
+    T, d = s["X"].shape
+    E, n = s["W_gate"].shape[:2]
+    buf = vgg.FewBuffers.allocate(T, d, E, n, s["K"])
+    weights = w8 if form == "e4m3" else (s["W_gate"], s["W_up"], s["W_down"])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        vgg.forward_few(ctx, s["X"], s["W_r"], s["bias"], weights, buf)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip((buf.O, buf.topk_ids, buf.topk_w), want))
+    graphs = []
+    for _ in range(2):  # two captured calls share the workspace and run one after the other
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            vgg.forward_few(ctx, s["X"], s["W_r"], s["bias"], weights, buf)
+    other = make(40, 512, 64, 192, 6, seed=7)["X"]
+    kept = s["X"].clone()
+    for X in (kept, other, kept):
+        s["X"].copy_(X)
+        for g in graphs:
+            buf.O.zero_()
+            g.replay()
+        torch.cuda.synchronize()
+        if X is kept:
+            assert torch.equal(buf.O, want[0])
+        else:
+            check((buf.O, buf.topk_ids, buf.topk_w), reference(dict(s, X=other), form, w8))
+    assert vgg.moe_get_error(ctx) == (vgg.MOE_OK, 0)
+
+
+def test_two_calls_at_once(vgg, ctx):
+    """Two streams, each with its workspace."""
+    cases = [make(5, 1024, 32, 256, 4, seed=8), make(64, 512, 64, 128, 8, seed=9)]
+    want = [call(vgg, ctx, s) for s in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    ws = [torch.empty(vgg.moe_few_workspace_bytes(s["X"].shape[0], s["X"].shape[1], *s["W_gate"].shape[:2], s["K"]),
+                      dtype=torch.uint8, device="cuda") for s in cases]
+    out = [[torch.zeros_like(t) for t in w] for w in want]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, st, w, o in zip(cases, streams, ws, out):
+            vgg.moe_forward_few(ctx, s["X"], s["W_r"], s["bias"], s["W_gate"], s["W_up"], s["W_down"], s["K"], *o, w,
+                                stream=st)
+    torch.cuda.synchronize()
+    for o, w in zip(out, want):
+        assert all(torch.equal(a, b) for a, b in zip(o, w))
+    assert vgg.moe_get_error(ctx) == (vgg.MOE_OK, 0)
+
+
+def test_choice_is_that_of_the_router(vgg, ctx):
+    """Ties, masked experts and a token of infinities: the choice and the weights by the rule of moe_route."""
+    T, d, E, n, K = 24, 64, 32, 64, 4
+    s = make(T, d, E, n, K, seed=10)
+    # whole numbers: logits exact whatever the order of the sum; experts in equal pairs
+    s["X"] = s["X"].float().round().to(BF)
+    s["W_r"] = (4 * s["W_r"].float()).round().to(BF)
+    s["W_r"][:, 1::2] = s["W_r"][:, 0::2]
+    s["bias"] = torch.zeros(E, device="cuda")
+    s["bias"][3], s["bias"][8:] = 2.0, float("-inf")  # 8 experts are left
+    s["X"][5] = 0.0
+    logits, scores = torch.empty((T, E), device="cuda"), None
+    ids, w = torch.empty((T, K), dtype=I32, device="cuda"), torch.empty((T, K), device="cuda")
+    vgg.moe_route(ctx, s["X"], s["W_r"], s["bias"], K, logits, scores, ids, w)
+    got = call(vgg, ctx, s)
+    assert torch.equal(got[1], ids)
+    np.testing.assert_allclose(got[2].cpu().numpy(), w.cpu().numpy(), rtol=1e-6)
+    assert got[1][5].tolist() == [3, 0, 1, 2]
+    assert vgg.moe_get_error(ctx) == (vgg.MOE_OK, 0)
+
+
+@pytest.mark.parametrize("form", ["bf16", "e4m3"])
+def test_a_token_that_is_not_finite_stays_alone(vgg, ctx, form):
+    """Tokens share tiles, not columns: a NaN and an infinity leave the others' outputs what they were, within the bound."""
+    s = make(20, 256, 8, 128, 2, seed=11)
+    w8 = weights8(vgg, ctx, s) if form == "e4m3" else None
+    ref = reference(s, form, w8)
+    bad = dict(s, X=s["X"].clone())
+    bad["X"][3, 7], bad["X"][11, 200] = float("nan"), float("inf")
+    O, ids, w = call(vgg, ctx, bad, form, w8)
+    keep = torch.ones(20, dtype=torch.bool, device="cuda")
+    keep[3] = keep[11] = False
+    check((O[keep], ids[keep], w[keep]), tuple(t[keep] for t in ref))
+    assert not torch.isfinite(O[3]).any() and ((ids >= 0) & (ids < 8)).all()
+    assert vgg.moe_get_error(ctx) == (vgg.MOE_OK, 0)
+
+
+def test_no_tokens_and_one_expert_row(vgg, ctx):
+    ws = torch.empty(vgg.moe_few_workspace_bytes(0, 64, 8, 64, 2), dtype=torch.uint8, device="cuda")
+    e = torch.empty((0, 64), dtype=BF, device="cuda")
+    s = make(1, 64, 8, 64, 2)
+    vgg.moe_forward_few(ctx, e, s["W_r"], None, s["W_gate"], s["W_up"], s["W_down"], 2, torch.empty_like(e),
+                        torch.empty((0, 2), dtype=I32, device="cuda"), torch.empty((0, 2), device="cuda"), ws)
+    assert vgg.moe_get_error(ctx) == (vgg.MOE_OK, 0)
+
+
+def test_beside_the_layer_s_own_path(vgg, ctx):
+    """The training path's forward on the same tokens: the same choice, outputs within both paths' roundings."""
+    s = make(48, 512, 32, 256, 4, seed=12)
+    buf = vgg.Buffers.allocate(48, 512, 32, 256, 4, backward=False)
+    vgg.forward(ctx, s["X"], s["W_r"], None, s["W_gate"], s["W_up"], s["W_down"], buf, cache=False)
+    O, ids, w = call(vgg, ctx, s)
+    assert torch.equal(ids, buf.topk_ids)
+    # bf16 roundings: O twice, the pairs' outputs once
+    assert ((O.float() - buf.O.float()).norm() / O.float().norm()).item() <= 1.25 * 3 ** 0.5 * 1.6e-3

@@ -782,6 +782,32 @@ def moe_forward_few_e4m3(ctx, X, W_r, bias, w8, K, O, topk_ids, topk_w, ws, stre
         dn, _flat(ctx, w8.wd_scale, (E, d), f32, "wd_scale"), *tail, _stream(stream)))
 
 
+@dataclass
+class FewBuffers:
+    """Outputs and workspace of the layer for up to 64 tokens (a decoding step of T sequences)."""
+
+    O: torch.Tensor         # [T, d] bf16
+    topk_ids: torch.Tensor  # [T, K] int32
+    topk_w: torch.Tensor    # [T, K] fp32
+    ws: torch.Tensor
+
+    @staticmethod
+    def allocate(T, d, E, n, K, device="cuda") -> "FewBuffers":
+        return FewBuffers(torch.zeros((T, d), dtype=torch.bfloat16, device=device),
+                          torch.zeros((T, K), dtype=torch.int32, device=device), torch.zeros((T, K), device=device),
+                          torch.empty(moe_few_workspace_bytes(T, d, E, n, K), dtype=torch.uint8, device=device))
+
+
+def forward_few(ctx, X, W_r, bias, weights, buf: FewBuffers, stream=None):
+    """The layer for the few tokens of X; the output is ``buf.O``.  ``weights``: (W_gate, W_up, W_down) in bf16, or
+    E4m3Weights."""
+    K = buf.topk_ids.shape[1]
+    if isinstance(weights, E4m3Weights):
+        moe_forward_few_e4m3(ctx, X, W_r, bias, weights, K, buf.O, buf.topk_ids, buf.topk_w, buf.ws, stream)
+    else:
+        moe_forward_few(ctx, X, W_r, bias, *weights, K, buf.O, buf.topk_ids, buf.topk_w, buf.ws, stream)
+
+
 def moe_test_gemm_varlen_m(ctx, A, idx, B, b_kmajor, offsets, D, stream=None):
     G = B.shape[0]
     K = A.shape[1]

@@ -570,11 +570,6 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
           }
         }
       }
-      if (stop) {  // let the copies in flight land before the block goes away
-        const uint64_t t0 = globaltimer_ns();
-        while (globaltimer_ns() - t0 < 20000000ull) {
-        }
-      }
     }
   } else if (warp >= kGath0 && warp < kGath0 + kGath) {
     // ---------------------------------------------------------------- the tokens' rows
@@ -850,7 +845,14 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
   tc_fence_after();
   if (warp == kMma) tmem_dealloc(tmem, tmem_cols);
   // ---- the weighted sums, once every block's parts are there: eight lanes a token and four columns, one a choice ----
-  if (tid == 0) L.ok = ok && !L.abort && wait_count(&a.ctr[kCtrDone], G, &L.abort, a.timeout_ns, a.err) ? 1 : 0;
+  if (L.abort) {  // a wait gave up (every thread sees so): let the copies in flight land before the block goes away
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 20000000ull) {
+    }
+    return;
+  }
+  __syncthreads();  // (the wait below may raise the flag)
+  if (tid == 0) L.ok = ok && wait_count(&a.ctr[kCtrDone], G, &L.abort, a.timeout_ns, a.err) ? 1 : 0;
   __syncthreads();
   if (!L.ok) return;
   const int quads = a.d / 4, units = a.T * quads;
