@@ -36,6 +36,9 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kRows = 128;             // weight rows of a tile
 constexpr int kWBytes = kRows * 128;   // weight bytes of a stage
 constexpr int kMaxPairs = kFewMaxTokens * 8;
+// Accumulators: the second product's items may be as short as a stage or two, and a pair of them left the products waiting for
+// the epilogue's latency (61 x 1536 x 512 x 256 e4m3: 99 us).
+constexpr int kAccs = 4;
 constexpr int kMaxStages = 12, kMinStages = kProd;  // (the producers take stages in turn, too)
 // Every block finds the choice of so few tokens itself; of more, each is found by one block behind a barrier (a block
 // reads splits x T x E partial logits otherwise).
@@ -45,7 +48,7 @@ constexpr int kRound = 16;   // tokens whose logits a block holds at a time
 constexpr int kCtrChoice = 0, kCtrItems = 1, kCtrDone = 3, kCtrShared = 4;
 
 struct Lists {
-  uint64_t full[kMaxStages], empty[kMaxStages], tfull[2], tempty[2], drain;
+  uint64_t full[kMaxStages], empty[kMaxStages], tfull[kAccs], tempty[kAccs], drain;
   uint32_t tmem;
   volatile int abort;
   int active, last, ok;
@@ -256,8 +259,11 @@ __global__ void __launch_bounds__(256) few_router_kernel(const __grid_constant__
   float acc[NT][2];
 #pragma unroll
   for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = 0.0f;
-  for (int c = r0; c < r1; c += kRtRows) {
-    uint32_t w[R][4];
+  // a chunk's rows of W_r and of X in registers while the one before is multiplied
+  constexpr int kXv = NT * (kRtRows / 8), kXn = (kXv + 255) / 256;
+  uint32_t w[R][4];
+  uint4 xr[kXn];
+  auto load = [&](int c) {
 #pragma unroll
     for (int q = 0; q < R; ++q)
 #pragma unroll
@@ -265,16 +271,34 @@ __global__ void __launch_bounds__(256) few_router_kernel(const __grid_constant__
         const int r = c + 128 * q + rg + j;
         w[q][j] = (in && r < r1) ? __ldg(reinterpret_cast<const uint32_t*>(a.W_r + static_cast<long long>(r) * a.E + e0)) : 0u;
       }
-    __syncthreads();
-    for (int i = tid; i < NT * (kRtRows / 8); i += 256) {
-      const int t = i / (kRtRows / 8), v = i % (kRtRows / 8) * 8;
-      uint4 x = make_uint4(0, 0, 0, 0);
-      if (t0 + t < a.T && c + v < r1) x = __ldg(reinterpret_cast<const uint4*>(a.X + (t0 + t) * a.ld_x + c + v));
-      const float2 f0 = unpack_bf16x2(x.x), f1 = unpack_bf16x2(x.y), f2 = unpack_bf16x2(x.z), f3 = unpack_bf16x2(x.w);
-      *reinterpret_cast<float4*>(&s_x[t][v]) = make_float4(f0.x, f0.y, f1.x, f1.y);
-      *reinterpret_cast<float4*>(&s_x[t][v + 4]) = make_float4(f2.x, f2.y, f3.x, f3.y);
+#pragma unroll
+    for (int q = 0; q < kXn; ++q) {
+      const int i = tid + 256 * q, t = i / (kRtRows / 8), v = i % (kRtRows / 8) * 8;
+      xr[q] = make_uint4(0, 0, 0, 0);
+      if (i < kXv && t0 + t < a.T && c + v < r1)
+        xr[q] = __ldg(reinterpret_cast<const uint4*>(a.X + (t0 + t) * a.ld_x + c + v));
     }
+  };
+  load(r0);
+  for (int c = r0; c < r1; c += kRtRows) {
     __syncthreads();
+#pragma unroll
+    for (int q = 0; q < kXn; ++q) {
+      const int i = tid + 256 * q, t = i / (kRtRows / 8), v = i % (kRtRows / 8) * 8;
+      const float2 f0 = unpack_bf16x2(xr[q].x), f1 = unpack_bf16x2(xr[q].y), f2 = unpack_bf16x2(xr[q].z),
+                   f3 = unpack_bf16x2(xr[q].w);
+      if (i < kXv) {
+        *reinterpret_cast<float4*>(&s_x[t][v]) = make_float4(f0.x, f0.y, f1.x, f1.y);
+        *reinterpret_cast<float4*>(&s_x[t][v + 4]) = make_float4(f2.x, f2.y, f3.x, f3.y);
+      }
+    }
+    float2 f[R][4];  // zero past the share, as X's values there
+#pragma unroll
+    for (int q = 0; q < R; ++q)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f[q][j] = unpack_bf16x2(w[q][j]);
+    __syncthreads();
+    if (c + kRtRows < r1) load(c + kRtRows);
 #pragma unroll
     for (int q = 0; q < R; ++q)
 #pragma unroll
@@ -283,9 +307,8 @@ __global__ void __launch_bounds__(256) few_router_kernel(const __grid_constant__
         const float xv[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float2 f = unpack_bf16x2(w[q][j]);  // zero past the share, as X's values there
-          acc[i][0] = fmaf(xv[j], f.x, acc[i][0]);
-          acc[i][1] = fmaf(xv[j], f.y, acc[i][1]);
+          acc[i][0] = fmaf(xv[j], f[q][j].x, acc[i][0]);
+          acc[i][1] = fmaf(xv[j], f[q][j].y, acc[i][1]);
         }
       }
   }
@@ -379,14 +402,14 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
   const int G = gridDim.x, b = blockIdx.x;
   const int P = a.T * a.K;
   const int acc_cols = a.nrows <= 16 ? 16 : a.nrows <= 32 ? 32 : a.nrows <= 64 ? 64 : 128;  // of an accumulator
-  const uint32_t tmem_cols = 2 * acc_cols;  // two of them: a power of two, 32 at least
+  const uint32_t tmem_cols = kAccs * acc_cols;  // a power of two, 64 at least
 
   if (tid == 0) {
     for (int s = 0; s < a.stages; ++s) {
       mbar_init(&L.full[s], 1 + 32);
       mbar_init(&L.empty[s], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kAccs; ++i) {
       mbar_init(&L.tfull[i], 1);
       mbar_init(&L.tempty[i], 32 * kEpi);
     }
@@ -673,10 +696,10 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
         const int m = L.act_off[w.ai + 1] - L.act_off[w.ai];
         const int N = (!F8 && x.ph == 1) ? 2 * ((m + 7) & ~7) : (m + 15) & ~15;
         const uint32_t idesc = F8 ? idesc_e4m3(kRows, N, 0, 0) : idesc_bf16(kRows, N, 0, 0);
-        stop = __any_sync(0xffffffffu, !mbar_wait(&L.tempty[acc & 1], ((acc >> 1) & 1) ^ 1, &L.abort, a.timeout_ns, a.err));
+        stop = __any_sync(0xffffffffu, !mbar_wait(&L.tempty[acc % kAccs], ((acc / kAccs) & 1) ^ 1, &L.abort, a.timeout_ns, a.err));
         if (stop) break;
         tc_fence_after();
-        const uint32_t d_tmem = tmem + (acc & 1) * acc_cols;
+        const uint32_t d_tmem = tmem + (acc % kAccs) * acc_cols;
         uint32_t more = 0;
         for (; w.k < k1; ++w.k, ++w.q) {
           stop = __any_sync(0xffffffffu, !mbar_wait(&L.full[s], par, &L.abort, a.timeout_ns, a.err));
@@ -696,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
             par ^= 1;
           }
         }
-        if (!stop && one) umma_commit(&L.tfull[acc & 1]);
+        if (!stop && one) umma_commit(&L.tfull[acc % kAccs]);
         if (w.k == x.c) w.next_item(x);
       }
     }
@@ -726,13 +749,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
         w.q += k1 - k0;
         if (k1 == x.c) w.next_item(x);
         const int p0 = L.act_off[ai], m = L.act_off[ai + 1] - p0, mh = (m + 7) & ~7;
-        // one verdict for all: a thread alone at the barriers below would wait for ever
-        if (!epi_all(mbar_wait(&L.tfull[acc & 1], (acc >> 1) & 1, &L.abort, a.timeout_ns, a.err))) {
-          stop = true;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t tb = tmem + (static_cast<uint32_t>(warp * 32) << 16) + (acc & 1) * acc_cols;
+        const uint32_t tb = tmem + (static_cast<uint32_t>(warp * 32) << 16) + (acc % kAccs) * acc_cols;
         float* dst;
         int step;
         if (k0 == 0) {
@@ -742,6 +759,12 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
           dst = over + static_cast<long long>(b) * a.T * kRows + row;
           step = kRows;
         }
+        // one verdict for all: a thread alone at the barriers below would wait for ever
+        if (!epi_all(mbar_wait(&L.tfull[acc % kAccs], (acc / kAccs) & 1, &L.abort, a.timeout_ns, a.err))) {
+          stop = true;
+          break;
+        }
+        tc_fence_after();
         for (int j0 = 0; j0 < m; j0 += 8) {
           float v[8];
           tmem_ld8(tb + j0, v);
@@ -759,7 +782,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
             if (j0 + i < m) __stcg(dst + static_cast<long long>(j0 + i) * step, v[i]);
         }
         tc_fence_before();
-        mbar_arrive(&L.tempty[acc & 1]);
+        mbar_arrive(&L.tempty[acc % kAccs]);
         if (x.ph == 1) continue;
         // first product: who completes the item makes its activations
         int b0 = b, b1 = b;
@@ -855,50 +878,70 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
   if (tid == 0) L.ok = ok && wait_count(&a.ctr[kCtrDone], G, &L.abort, a.timeout_ns, a.err) ? 1 : 0;
   __syncthreads();
   if (!L.ok) return;
-  const int quads = a.d / 4, units = a.T * quads;
+  const int quads = a.d / 4, units = a.T * quads, t2 = plan.t2, c2 = plan.c2;
   const List y0 = plan.list(2), y1 = plan.list(3);
   const int u1 = static_cast<int>(static_cast<long long>(units) * (b + 1) / G);
-  for (int u0 = static_cast<int>(static_cast<long long>(units) * b / G) + 4 * warp; u0 < u1; u0 += 4 * kWarps) {
-    const int u = u0 + (lane >> 3), k = lane & 7;
-    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    const int t = u < u1 ? u / quads : 0, col = u < u1 ? (u - t * quads) * 4 : 0;
-    if (u < u1 && k < a.K) {
-      const int p = L.tok_pair[t * a.K + k], ai = L.tok_a[t * a.K + k];
-      v = __ldcg(reinterpret_cast<const float4*>(a.y + static_cast<long long>(p) * ld_y + col));
-      const bool h = ai >= y1.a0;
-      const List& x = h ? y1 : y0;
-      const int s0 = ((ai - x.a0) * x.tiles + col / kRows) * x.c;
-      const int b0 = x.owner(s0), b1 = x.owner(s0 + x.c - 1);
-      const float* over = a.ov2 + static_cast<long long>(h) * kFewMaxBlocks * a.T * kRows;
-      for (int o = b0 + 1; o <= b1; o += 4) {
+  constexpr int kU = 2;  // units of a lane group at a time: their loads in flight together
+  for (int u0 = static_cast<int>(static_cast<long long>(units) * b / G) + 4 * kU * warp; u0 < u1; u0 += 4 * kU * kWarps) {
+    const int k = lane & 7;
+    float4 v[kU];
+    float w[kU];
+    int t[kU], col[kU], over0[kU], over1[kU];
+    const float* over[kU];
+    float4 scale[kU];
+#pragma unroll
+    for (int q = 0; q < kU; ++q) {
+      const int u = u0 + 4 * q + (lane >> 3);
+      const bool in = u < u1 && k < a.K;
+      v[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      scale[q] = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+      over0[q] = over1[q] = 0;
+      over[q] = nullptr;
+      w[q] = 0.0f;
+      t[q] = u / quads;
+      col[q] = (u - t[q] * quads) * 4;
+      if (in) {
+        const int p = L.tok_pair[t[q] * a.K + k], ai = L.tok_a[t[q] * a.K + k];
+        v[q] = __ldcg(reinterpret_cast<const float4*>(a.y + static_cast<long long>(p) * ld_y + col[q]));
+        w[q] = L.pw[t[q] * a.K + k];
+        if (F8) {
+          w[q] *= row_scale(__ldcg(a.amax + p));
+          scale[q] = __ldg(reinterpret_cast<const float4*>(a.wd_scale + static_cast<long long>(L.act_e[ai]) * a.d + col[q]));
+        }
+        const bool h = ai >= y1.a0;
+        const int s0 = ((ai - (h ? y1.a0 : 0)) * t2 + col[q] / kRows) * c2;
+        over0[q] = (h ? y1 : y0).owner(s0) + 1;
+        over1[q] = (h ? y1 : y0).owner(s0 + c2 - 1) + 1;
+        over[q] = a.ov2 + ((static_cast<long long>(h) * kFewMaxBlocks + over0[q]) * a.T + (p - L.act_off[ai])) * kRows + col[q] % kRows;
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < kU; ++q)
+      for (int o = over0[q]; o < over1[q]; o += 4) {
         float4 z[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          z[r] = o + r <= b1 ? __ldcg(reinterpret_cast<const float4*>(
-                                   over + (static_cast<long long>(o + r) * a.T + (p - L.act_off[ai])) * kRows + col % kRows))
-                             : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          z[r] = o + r < over1[q] ? __ldcg(reinterpret_cast<const float4*>(over[q] + static_cast<long long>(o - over0[q] + r) * a.T * kRows))
+                                  : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          v.x += z[r].x; v.y += z[r].y; v.z += z[r].z; v.w += z[r].w;
+          v[q].x += z[r].x; v[q].y += z[r].y; v[q].z += z[r].z; v[q].w += z[r].w;
         }
       }
-      float w = L.pw[t * a.K + k];
-      if (F8) {
-        w *= row_scale(__ldcg(a.amax + p));
-        const float4 c = __ldg(reinterpret_cast<const float4*>(a.wd_scale + static_cast<long long>(L.act_e[ai]) * a.d + col));
-        v.x *= c.x; v.y *= c.y; v.z *= c.z; v.w *= c.w;
-      }
-      v.x *= w; v.y *= w; v.z *= w; v.w *= w;
-    }
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) {
-      v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-      v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
-      v.z += __shfl_xor_sync(0xffffffffu, v.z, o);
-      v.w += __shfl_xor_sync(0xffffffffu, v.w, o);
+    for (int q = 0; q < kU; ++q) {
+      float4 x = v[q];
+      x.x *= w[q] * scale[q].x; x.y *= w[q] * scale[q].y; x.z *= w[q] * scale[q].z; x.w *= w[q] * scale[q].w;
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) {
+        x.x += __shfl_xor_sync(0xffffffffu, x.x, o);
+        x.y += __shfl_xor_sync(0xffffffffu, x.y, o);
+        x.z += __shfl_xor_sync(0xffffffffu, x.z, o);
+        x.w += __shfl_xor_sync(0xffffffffu, x.w, o);
+      }
+      if (k == 0 && u0 + 4 * q + (lane >> 3) < u1)
+        *reinterpret_cast<uint2*>(a.O + t[q] * a.ld_o + col[q]) = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
     }
-    if (k == 0 && u < u1)
-      *reinterpret_cast<uint2*>(a.O + t * a.ld_o + col) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
   }
 }
 
