@@ -1931,7 +1931,7 @@ static int forward_few(moe_ctx* ctx, const void* X, long long ld_x, const void* 
   if (!g.ok) return MOE_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   // the kernel counts a list's stages times its blocks in 32 bits
-  const long long tiles = static_cast<long long>(std::min(E, T * K)) * std::max(n / 64 * ceil_div(d, 64), ceil_div(d, 128) * (n / 64));
+  const long long tiles = static_cast<long long>(std::min(E, T * K)) * std::max(ceil_div(n, 128) * (d / 64), ceil_div(d, 256) * (n / 64));
   if (tiles * few_blocks(ctx->num_sms) >= (1ll << 32)) return MOE_ERR_UNSUPPORTED;
   const FewLayout l = few_layout(T, d, E, n, K);
   uint8_t* base = static_cast<uint8_t*>(ws);
@@ -1972,7 +1972,7 @@ static int forward_few(moe_ctx* ctx, const void* X, long long ld_x, const void* 
   a.timeout_ns = ctx->timeout_ns;
   const int du = f8 ? d / 2 : d, nu = f8 ? n / 2 : n;  // the reduction in 16-bit units
   CUtensorMap mg, mu, md;
-  if (!make_map_3d(&mg, Wg, du, n, E, 64) || !make_map_3d(&mu, Wu, du, n, E, 64) || !make_map_3d(&md, Wd, nu, d, E, 128))
+  if (!make_map_3d(&mg, Wg, du, n, E, 128) || !make_map_3d(&mu, Wu, du, n, E, 128) || !make_map_3d(&md, Wd, nu, d, E, 128))
     return MOE_ERR_CUDA;
   VGG_LAUNCH("few_router", launch_few_router(a, s));
   VGG_LAUNCH("few_layer", launch_few_layer(a, f8, mg, mu, md, ctx->num_sms, s));

@@ -7,7 +7,7 @@
 // that is the chain of dependent steps.  The design follows from both:
 //   * the weights are the 128-row operand of the tensor cores and the tokens the narrow one (N = 16 .. 128 columns), so a
 //     weight tile moves once through shared memory whatever the number of tokens;
-//   * the stages (128 weight rows x 128 bytes of the reduction) of all chosen experts form one list, of which each of the
+//   * the stages (256 weight rows x 128 bytes of the reduction) of all chosen experts form one list, of which each of the
 //     persistent blocks takes an equal, contiguous share: blocks finish together whatever the sizes and the choice.
 //     An output tile that several blocks share is summed from their parts in block order, so results do not depend
 //     on which of them ends last;
@@ -28,18 +28,23 @@ namespace vgg {
 namespace {
 
 constexpr int kEpi = 4;      // epilogue warps 0..3 (TMEM lanes 32 w ..)
-constexpr int kGath = 8;     // gather warps
+constexpr int kGath = 6;     // gather warps: a stage of the ring each
 constexpr int kProd = 4;     // TMA producers: loads issued by one thread complete one after another
 constexpr int kGath0 = kEpi, kMma = kEpi + kGath, kProd0 = kMma + 1;
 constexpr int kWarps = kProd0 + kProd;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kRows = 128;             // weight rows of a tile
-constexpr int kWBytes = kRows * 128;   // weight bytes of a stage
+// A tile is two halves of 128 weight rows: the same rows of W_gate and W_up, so that the thread that holds a row of H holds that
+// of U; or 256 rows of W_down.  The halves share the tokens' operand: its rows are gathered, and every step of the roles
+// made, once for 32 KB of weights (with halves of 64 rows, 16 KB a stage: 61 x 1536 x 512 x 256 e4m3 101 us).
+constexpr int kRows = 128;             // weight rows of a half
+constexpr int kTile = 2 * kRows;
+constexpr int kHBytes = kRows * 128;   // weight bytes of a half's stage
+constexpr int kWBytes = 2 * kHBytes;
 constexpr int kMaxPairs = kFewMaxTokens * 8;
-// Accumulators: the second product's items may be as short as a stage or two, and a pair of them left the products waiting for
-// the epilogue's latency (61 x 1536 x 512 x 256 e4m3: 99 us).
-constexpr int kAccs = 4;
-constexpr int kMaxStages = 12, kMinStages = kProd;  // (the producers take stages in turn, too)
+// Tiles' accumulators, where TMEM has room: the second product's items may be as short as a stage, and a pair of accumulators
+// leaves the products waiting for the epilogue's latency.
+constexpr int kMaxAccs = 4;
+constexpr int kMaxStages = 6, kMinStages = kProd;  // (the producers take stages in turn, too)
 // Every block finds the choice of so few tokens itself; of more, each is found by one block behind a barrier (a block
 // reads splits x T x E partial logits otherwise).
 constexpr int kOwnChoice = 8;
@@ -48,11 +53,12 @@ constexpr int kRound = 16;   // tokens whose logits a block holds at a time
 constexpr int kCtrChoice = 0, kCtrItems = 1, kCtrDone = 3, kCtrShared = 4;
 
 struct Lists {
-  uint64_t full[kMaxStages], empty[kMaxStages], tfull[kAccs], tempty[kAccs], drain;
+  uint64_t full[kMaxStages], empty[kMaxStages], tfull[kMaxAccs], tempty[kMaxAccs], drain;
   uint32_t tmem;
   volatile int abort;
   int active, last, ok;
   uint32_t chunk[32];          // pairs and experts (<< 16) of 32 experts each
+  float xs[kFewMaxTokens];     // scales of X's codes (e4m3)
   float pw[kMaxPairs];         // [token][rank]: combine weight, experts of a token ascending
   uint16_t act_e[kMaxPairs];   // expert of each chosen expert's index, ascending
   uint16_t act_off[kMaxPairs + 1];  // its first pair
@@ -99,7 +105,7 @@ __device__ __forceinline__ bool wait_count(const int* p, int target, volatile in
 // product of either.  A list's items (an expert's 128-row tiles) are c stages each; block b of its G takes the stages
 // [b S / G, (b + 1) S / G).  With halves the activations that a block waits for at the second product's start have been
 // complete for half a product's time; a short list is one, since a further list is a further chain of steps (a block's
-// stages of the first product times 0.38 us against about 10 us: 1 x 2048 x 128 x 512, 13 stages, 41.5 us in halves).
+// stages of the first product times 0.76 us against about 10 us: 1 x 2048 x 128 x 512, 7 stages, 33 us and in halves 41.5).
 struct List {
   int ph, half, a0, tiles, c, S, G;
   __device__ __forceinline__ int begin(int b) const {
@@ -111,7 +117,7 @@ struct List {
   }
 };
 constexpr int kLists = 4;
-constexpr int kHalves = 32;  // stages of a block in the first product from which there are halves
+constexpr int kHalves = 16;  // stages of a block in the first product from which there are halves
 
 struct Plan {
   int A, cut, G, t1, c1, t2, c2;  // cut: the second half's first expert
@@ -187,8 +193,28 @@ __device__ __forceinline__ float row_scale(uint32_t amax_bits) {
   return amax_bits ? __fdiv_rn(__uint_as_float(amax_bits), 448.0f) : 1.0f;
 }
 
+// x / s, correctly rounded, for many x with one s: Markstein's correction of a product with the correctly rounded reciprocal
+// (P. Markstein, IBM J. Res. Dev. 34, 1990).  Scales from 2^-60 to 2^60; a quotient so small that the remainder
+// underflows is far below the smallest code.
+__device__ __forceinline__ float quotient(float x, float s, float inv) {
+  const float q = x * inv;
+  return fmaf(fmaf(-q, s, x), inv, q);
+}
+
 // 16 bf16 values to 16 codes of a row with scale s.
-__device__ __forceinline__ uint4 codes16(const uint4 x, const uint4 y, float s) {
+__device__ __forceinline__ uint4 codes16(const uint4 x, const uint4 y, float s, float inv) {
+  const uint32_t v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 a = unpack_bf16x2(v[2 * i]), b = unpack_bf16x2(v[2 * i + 1]);
+    w[i] = e4m3x4(quotient(a.x, s, inv), quotient(a.y, s, inv), quotient(b.x, s, inv), quotient(b.y, s, inv));
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The same for any scale.
+__device__ __noinline__ uint4 codes16_any(const uint4 x, const uint4 y, float s) {
   const uint32_t v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
   uint32_t w[4];
 #pragma unroll
@@ -197,6 +223,10 @@ __device__ __forceinline__ uint4 codes16(const uint4 x, const uint4 y, float s) 
     w[i] = e4m3x4(__fdiv_rn(a.x, s), __fdiv_rn(a.y, s), __fdiv_rn(b.x, s), __fdiv_rn(b.y, s));
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ uint4 codes16(const uint4 x, const uint4 y, float s) {
+  if (s >= 8.673617379884035e-19f && s <= 1.152921504606847e18f) return codes16(x, y, s, __frcp_rn(s));
+  return codes16_any(x, y, s);
 }
 
 }  // namespace
@@ -401,15 +431,16 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = gridDim.x, b = blockIdx.x;
   const int P = a.T * a.K;
-  const int acc_cols = a.nrows <= 16 ? 16 : a.nrows <= 32 ? 32 : a.nrows <= 64 ? 64 : 128;  // of an accumulator
-  const uint32_t tmem_cols = kAccs * acc_cols;  // a power of two, 64 at least
+  const int half_cols = a.nrows <= 16 ? 16 : a.nrows <= 32 ? 32 : a.nrows <= 64 ? 64 : 128;  // of a half's accumulator
+  const int accs = a.nrows <= 64 ? kMaxAccs : kMaxAccs / 2, acc_bit = a.nrows <= 64 ? 2 : 1;  // 512 columns at most
+  const uint32_t tmem_cols = accs * 2 * half_cols;  // a power of two
 
   if (tid == 0) {
     for (int s = 0; s < a.stages; ++s) {
       mbar_init(&L.full[s], 1 + 32);
       mbar_init(&L.empty[s], 1);
     }
-    for (int i = 0; i < kAccs; ++i) {
+    for (int i = 0; i < accs; ++i) {
       mbar_init(&L.tfull[i], 1);
       mbar_init(&L.tempty[i], 32 * kEpi);
     }
@@ -433,6 +464,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
   if (P > 32)
     for (int e = tid; e < a.E; e += kThreads) s_mask[e] = 0;
   griddep_wait();  // the first launch's parts and cleared counters
+  if (F8)
+    for (int t = tid; t < a.T; t += kThreads) L.xs[t] = __ldcg(a.xs + t);
   if (a.T <= kOwnChoice) {
     choose(a, 0, 1, a.T, keys, [&](int t, int k, int id, float w) {
       s_ids[t * a.K + k] = id;
@@ -553,12 +586,14 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
   Plan plan;
   plan.A = L.active;
   plan.G = G;
-  plan.t1 = a.n / 64;  // 64 rows of W_gate and 64 of W_up a tile
+  plan.t1 = (a.n + kRows - 1) / kRows;
   plan.c1 = (a.d * es + 127) / 128;
-  plan.t2 = (a.d + kRows - 1) / kRows;
+  plan.t2 = (a.d + kTile - 1) / kTile;
   plan.c2 = (a.n * es + 127) / 128;
   plan.cut = plan.A * plan.t1 * plan.c1 >= kHalves * G ? plan.A / 2 : 0;
-  const int ld_hu = plan.t1 * kRows, ld_y = plan.t2 * kRows;
+  const int ld_hu = plan.t1 * kTile, ld_y = plan.t2 * kTile;
+  // a last tile of W_down may have rows in its first half alone
+  auto halves = [&](const List& x, int tile) { return x.ph == 1 && a.d - tile * kTile <= kRows ? 1 : 2; };
 
   if (warp >= kProd0) {
     // ---------------------------------------------------------------- weights (lane 0 of each producer warp)
@@ -579,12 +614,14 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
             }
             uint8_t* dst = ring + s * stage_bytes;
             const int e = L.act_e[w.ai];
-            mbar_arrive_expect_tx(&L.full[s], kWBytes);
+            const int hs = halves(x, w.tile);
+            mbar_arrive_expect_tx(&L.full[s], hs * kHBytes);
             if (x.ph == 0) {
-              tma_load_3d(dst, &mg, &L.full[s], w.k * 64, w.tile * 64, e);
-              tma_load_3d(dst + kWBytes / 2, &mu, &L.full[s], w.k * 64, w.tile * 64, e);
+              tma_load_3d(dst, &mg, &L.full[s], w.k * 64, w.tile * kRows, e);
+              tma_load_3d(dst + kHBytes, &mu, &L.full[s], w.k * 64, w.tile * kRows, e);
             } else {
-              tma_load_3d(dst, &md, &L.full[s], w.k * 64, w.tile * kRows, e);
+              tma_load_3d(dst, &md, &L.full[s], w.k * 64, w.tile * kTile, e);
+              if (hs == 2) tma_load_3d(dst + kHBytes, &md, &L.full[s], w.k * 64, w.tile * kTile + kRows, e);
             }
           }
           if (++s == a.stages) {
@@ -696,10 +733,11 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
         const int m = L.act_off[w.ai + 1] - L.act_off[w.ai];
         const int N = (!F8 && x.ph == 1) ? 2 * ((m + 7) & ~7) : (m + 15) & ~15;
         const uint32_t idesc = F8 ? idesc_e4m3(kRows, N, 0, 0) : idesc_bf16(kRows, N, 0, 0);
-        stop = __any_sync(0xffffffffu, !mbar_wait(&L.tempty[acc % kAccs], ((acc / kAccs) & 1) ^ 1, &L.abort, a.timeout_ns, a.err));
+        stop = __any_sync(0xffffffffu, !mbar_wait(&L.tempty[acc & (accs - 1)], ((acc >> acc_bit) & 1) ^ 1, &L.abort, a.timeout_ns, a.err));
         if (stop) break;
         tc_fence_after();
-        const uint32_t d_tmem = tmem + (acc % kAccs) * acc_cols;
+        const uint32_t d_tmem = tmem + (acc & (accs - 1)) * 2 * half_cols;
+        const bool two = halves(x, w.tile) == 2;
         uint32_t more = 0;
         for (; w.k < k1; ++w.k, ++w.q) {
           stop = __any_sync(0xffffffffu, !mbar_wait(&L.full[s], par, &L.abort, a.timeout_ns, a.err));
@@ -711,6 +749,11 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
           if (one) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) umma_step<F8>(d_tmem, ad + 2 * kk, bd + 2 * kk, idesc, kk ? 1u : more);
+            if (two) {
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                umma_step<F8>(d_tmem + half_cols, ad + (kHBytes >> 4) + 2 * kk, bd + 2 * kk, idesc, kk ? 1u : more);
+            }
             umma_commit(&L.empty[s]);
           }
           more = 1;
@@ -719,7 +762,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
             par ^= 1;
           }
         }
-        if (!stop && one) umma_commit(&L.tfull[acc % kAccs]);
+        if (!stop && one) umma_commit(&L.tfull[acc & (accs - 1)]);
         if (w.k == x.c) w.next_item(x);
       }
     }
@@ -730,7 +773,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
     }
   } else {
     // ---------------------------------------------------------------- accumulators out (warps 0..3)
-    // Warp w's lanes hold rows 32 w .. of the tile, a column per token.  The part of the block that has an item's first
+    // A thread has a row of either half, a column per token.  Of an item that other blocks share, the part with the first
     // stage goes to the item's place, another block's to that block's own overflow rows (in a list a block goes on with at
     // most one item that began elsewhere).
     const int row = tid;
@@ -741,7 +784,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
       if (b >= x.G) continue;
       const int ld = x.ph ? ld_y : ld_hu;
       float* const first = x.ph ? a.y : a.hu;
-      float* const over = (x.ph ? a.ov2 : a.ov1) + static_cast<long long>(x.half) * kFewMaxBlocks * a.T * kRows;
+      float* const over = (x.ph ? a.ov2 : a.ov1) + static_cast<long long>(x.half) * kFewMaxBlocks * a.T * kTile;
+      int items = 0;  // completed here, of the first product
       Walk w;
       for (w.start(x, b); w.q < w.end; ++acc) {
         const int k0 = w.k, k1 = min(x.c, k0 + (w.end - w.q));
@@ -749,64 +793,106 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
         w.q += k1 - k0;
         if (k1 == x.c) w.next_item(x);
         const int p0 = L.act_off[ai], m = L.act_off[ai + 1] - p0, mh = (m + 7) & ~7;
-        const uint32_t tb = tmem + (static_cast<uint32_t>(warp * 32) << 16) + (acc % kAccs) * acc_cols;
+        const bool whole = k1 - k0 == x.c, two = halves(x, tile) == 2;
+        const int slot = acc & (accs - 1);
+        const uint32_t tb = tmem + (static_cast<uint32_t>(warp * 32) << 16) + slot * 2 * half_cols;
+        // the first product's column of this thread
+        const int col = tile * kRows + row;
+        const bool in = col < a.n;
+        float gs = 1.0f, us = 1.0f;
+        if (F8 && x.ph == 0 && in) {
+          const long long at = static_cast<long long>(L.act_e[ai]) * a.n + col;
+          gs = __ldg(a.wg_scale + at);
+          us = __ldg(a.wu_scale + at);
+        }
+        // A = silu(H) U of this thread's column for pair p0 + j
+        auto activate = [&](int j, float h, float u) {
+          if (F8) {
+            const float sx = L.xs[L.ptok[p0 + j]];
+            h *= sx * gs;
+            u *= sx * us;
+          }
+          const float act = h * sigmoidf_(h) * u;
+          const __nv_bfloat16 hi = __float2bfloat16_rn(act);
+          const long long at = static_cast<long long>(p0 + j) * a.n + col;
+          if (in) a.A[at] = hi;
+          if (F8) {
+            const uint32_t top = __reduce_max_sync(0xffffffffu, in ? __float_as_uint(fabsf(__bfloat162float(hi))) : 0u);
+            if (lane == 0) atomicMax(a.amax + p0 + j, top);
+          } else if (in) {
+            a.A_lo[at] = __float2bfloat16_rn(act - __bfloat162float(hi));
+          }
+        };
         float* dst;
         int step;
         if (k0 == 0) {
-          dst = first + static_cast<long long>(p0) * ld + tile * kRows + row;
+          dst = first + static_cast<long long>(p0) * ld + tile * kTile + row;
           step = ld;
         } else {
-          dst = over + static_cast<long long>(b) * a.T * kRows + row;
-          step = kRows;
+          dst = over + static_cast<long long>(b) * a.T * kTile + row;
+          step = kTile;
         }
         // one verdict for all: a thread alone at the barriers below would wait for ever
-        if (!epi_all(mbar_wait(&L.tfull[acc % kAccs], (acc / kAccs) & 1, &L.abort, a.timeout_ns, a.err))) {
+        if (!epi_all(mbar_wait(&L.tfull[slot], (acc >> acc_bit) & 1, &L.abort, a.timeout_ns, a.err))) {
           stop = true;
           break;
         }
         tc_fence_after();
         for (int j0 = 0; j0 < m; j0 += 8) {
-          float v[8];
-          tmem_ld8(tb + j0, v);
+          float v[2][8];
+          tmem_ld8(tb + j0, v[0]);
+          if (two) tmem_ld8(tb + half_cols + j0, v[1]);
           if (!F8 && x.ph == 1) {
-            float lo[8];
-            tmem_ld8(tb + mh + j0, lo);
+            float lo[2][8];
+            tmem_ld8(tb + mh + j0, lo[0]);
+            if (two) tmem_ld8(tb + half_cols + mh + j0, lo[1]);
             tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] += lo[i];
+            for (int i = 0; i < 8; ++i) {
+              v[0][i] += lo[0][i];
+              v[1][i] += lo[1][i];
+            }
           } else {
             tmem_ld_wait();
           }
+          if (x.ph == 0 && whole) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (j0 + i < m) __stcg(dst + static_cast<long long>(j0 + i) * step, v[i]);
+            for (int i = 0; i < 8; ++i)
+              if (j0 + i < m) activate(j0 + i, v[0][i], v[1][i]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (j0 + i < m) {
+                __stcg(dst + static_cast<long long>(j0 + i) * step, v[0][i]);
+                if (two) __stcg(dst + static_cast<long long>(j0 + i) * step + kRows, v[1][i]);
+              }
+          }
         }
         tc_fence_before();
-        mbar_arrive(&L.tempty[acc % kAccs]);
+        mbar_arrive(&L.tempty[slot]);
         if (x.ph == 1) continue;
-        // first product: who completes the item makes its activations
-        int b0 = b, b1 = b;
-        epi_sync();
-        if (k1 - k0 < x.c) {
-          b0 = x.owner(item * x.c);
-          b1 = x.owner(item * x.c + x.c - 1);
-          if (tid == 0) L.last = atom_acq_rel(&a.ctr[kCtrShared + x.half * kFewMaxBlocks + b0]) == b1 - b0;
-          epi_sync();
-          if (!L.last) continue;
+        if (whole) {
+          ++items;
+          continue;
         }
-        const int e = L.act_e[ai];
-        // U values of a thread and O parts of each at a time, their loads in flight together: an item cut into many parts is one
-        // of a short list, with few values
+        // an item in parts: the block that brings the last of them adds them up in block order
+        const int b0 = x.owner(item * x.c), b1 = x.owner(item * x.c + x.c - 1);
+        epi_sync();
+        if (tid == 0) L.last = atom_acq_rel(&a.ctr[kCtrShared + x.half * kFewMaxBlocks + b0]) == b1 - b0;
+        epi_sync();
+        if (!L.last) continue;
+        ++items;
+        // U pairs and O parts of each at a time, their loads in flight together: an item cut into many parts is one of a
+        // short list, with few pairs
         auto finish = [&](auto u_, auto o_) {
           constexpr int U = decltype(u_)::value, O = decltype(o_)::value;
-          for (int i0 = tid; i0 < m * 64; i0 += U * 32 * kEpi) {
+          for (int j0 = 0; j0 < m; j0 += U) {
             float h[U], u[U];
 #pragma unroll
             for (int q = 0; q < U; ++q) {
-              const int i = i0 + q * 32 * kEpi;
-              const float* hu = a.hu + static_cast<long long>(p0 + (i >> 6)) * ld + tile * kRows + (i & 63);
-              h[q] = i < m * 64 ? __ldcg(hu) : 0.0f;
-              u[q] = i < m * 64 ? __ldcg(hu + 64) : 0.0f;
+              const float* hu = a.hu + static_cast<long long>(p0 + j0 + q) * ld + tile * kTile + row;
+              h[q] = j0 + q < m ? __ldcg(hu) : 0.0f;
+              u[q] = j0 + q < m ? __ldcg(hu + kRows) : 0.0f;
             }
             for (int o = b0 + 1; o <= b1; o += O) {
               float y[U][O][2];
@@ -814,11 +900,10 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
               for (int q = 0; q < U; ++q)
 #pragma unroll
                 for (int r = 0; r < O; ++r) {
-                  const int i = i0 + q * 32 * kEpi;
-                  const bool in = i < m * 64 && o + r <= b1;
-                  const float* ov = over + (static_cast<long long>(o + r) * a.T + (i >> 6)) * kRows + (i & 63);
-                  y[q][r][0] = in ? __ldcg(ov) : 0.0f;
-                  y[q][r][1] = in ? __ldcg(ov + 64) : 0.0f;
+                  const bool has = j0 + q < m && o + r <= b1;
+                  const float* ov = over + (static_cast<long long>(o + r) * a.T + j0 + q) * kTile + row;
+                  y[q][r][0] = has ? __ldcg(ov) : 0.0f;
+                  y[q][r][1] = has ? __ldcg(ov + kRows) : 0.0f;
                 }
 #pragma unroll
               for (int q = 0; q < U; ++q)
@@ -829,33 +914,16 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
                 }
             }
 #pragma unroll
-            for (int q = 0; q < U; ++q) {
-              const int i = i0 + q * 32 * kEpi, j = i >> 6, r = i & 63;
-              if (i >= m * 64) break;  // (the same for a whole warp)
-              if (F8) {
-                const float sx = __ldcg(a.xs + L.ptok[p0 + j]);
-                const long long col = static_cast<long long>(e) * a.n + tile * 64 + r;
-                h[q] *= sx * __ldg(a.wg_scale + col);
-                u[q] *= sx * __ldg(a.wu_scale + col);
-              }
-              const float act = h[q] * sigmoidf_(h[q]) * u[q];
-              const __nv_bfloat16 hi = __float2bfloat16_rn(act);
-              const long long at = static_cast<long long>(p0 + j) * a.n + tile * 64 + r;
-              a.A[at] = hi;
-              if (F8) {
-                const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(__bfloat162float(hi))));
-                if (lane == 0) atomicMax(a.amax + p0 + j, top);
-              } else {
-                a.A_lo[at] = __float2bfloat16_rn(act - __bfloat162float(hi));
-              }
-            }
+            for (int q = 0; q < U; ++q)
+              if (j0 + q < m) activate(j0 + q, h[q], u[q]);
           }
         };
-        if (b1 - b0 > 1) finish(std::integral_constant<int, 2>{}, std::integral_constant<int, 8>{});
-        else finish(std::integral_constant<int, 8>{}, std::integral_constant<int, 1>{});
-        epi_sync();
-        if (tid == 0) red_release(&a.ctr[kCtrItems + x.half], 1);
+        if (b1 - b0 > 1) finish(std::integral_constant<int, 1>{}, std::integral_constant<int, 8>{});
+        else finish(std::integral_constant<int, 4>{}, std::integral_constant<int, 1>{});
       }
+      if (stop || x.ph == 1) continue;
+      epi_sync();
+      if (tid == 0 && items > 0) red_release(&a.ctr[kCtrItems + x.half], items);
     }
     if (!stop) {
       epi_sync();
@@ -909,10 +977,10 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
           scale[q] = __ldg(reinterpret_cast<const float4*>(a.wd_scale + static_cast<long long>(L.act_e[ai]) * a.d + col[q]));
         }
         const bool h = ai >= y1.a0;
-        const int s0 = ((ai - (h ? y1.a0 : 0)) * t2 + col[q] / kRows) * c2;
+        const int s0 = ((ai - (h ? y1.a0 : 0)) * t2 + col[q] / kTile) * c2;
         over0[q] = (h ? y1 : y0).owner(s0) + 1;
         over1[q] = (h ? y1 : y0).owner(s0 + c2 - 1) + 1;
-        over[q] = a.ov2 + ((static_cast<long long>(h) * kFewMaxBlocks + over0[q]) * a.T + (p - L.act_off[ai])) * kRows + col[q] % kRows;
+        over[q] = a.ov2 + ((static_cast<long long>(h) * kFewMaxBlocks + over0[q]) * a.T + (p - L.act_off[ai])) * kTile + col[q] % kTile;
       }
     }
 #pragma unroll
@@ -921,7 +989,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
         float4 z[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          z[r] = o + r < over1[q] ? __ldcg(reinterpret_cast<const float4*>(over[q] + static_cast<long long>(o - over0[q] + r) * a.T * kRows))
+          z[r] = o + r < over1[q] ? __ldcg(reinterpret_cast<const float4*>(over[q] + static_cast<long long>(o - over0[q] + r) * a.T * kTile))
                                   : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
@@ -963,12 +1031,12 @@ FewLayout few_layout(int T, int d, int E, int n, int K) {
   l.part = take(sizeof(float) * static_cast<size_t>(kFewMaxSplits) * T * E);
   l.xq = take(static_cast<size_t>(T) * d);
   l.xs = take(sizeof(float) * T);
-  l.hu = take(sizeof(float) * P * 2 * n);
+  l.hu = take(sizeof(float) * P * ((n + kRows - 1) / kRows) * kTile);
   l.A = take(sizeof(__nv_bfloat16) * P * n);
   l.A_lo = take(sizeof(__nv_bfloat16) * P * n);
-  l.y = take(sizeof(float) * P * ((d + kRows - 1) / kRows) * kRows);
-  l.ov1 = take(sizeof(float) * 2 * static_cast<size_t>(kFewMaxBlocks) * T * kRows);
-  l.ov2 = take(sizeof(float) * 2 * static_cast<size_t>(kFewMaxBlocks) * T * kRows);
+  l.y = take(sizeof(float) * P * ((d + kTile - 1) / kTile) * kTile);
+  l.ov1 = take(sizeof(float) * 2 * static_cast<size_t>(kFewMaxBlocks) * T * kTile);
+  l.ov2 = take(sizeof(float) * 2 * static_cast<size_t>(kFewMaxBlocks) * T * kTile);
   l.bytes = p;
   return l;
 }

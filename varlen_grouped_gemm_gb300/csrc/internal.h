@@ -279,7 +279,7 @@ cudaError_t launch_read_rows8(const uint8_t* q, const __nv_bfloat16* scale, long
 
 // ---- the layer for a few tokens ---------------------------------------------------------------
 constexpr int kFewMaxTokens = 64;
-constexpr int kFewMaxBlocks = 256;  // persistent blocks (bounds the workspace's overflow rows)
+constexpr int kFewMaxBlocks = 160;  // persistent blocks (bounds the workspace's overflow rows)
 constexpr int kFewMaxSplits = 16;   // shares of d in the router's product
 // Pointers into the caller's arrays and the workspace.  xq, xs, wg_scale, wu_scale, wd_scale: the e4m3 form alone.
 struct FewArgs {
@@ -298,10 +298,10 @@ struct FewArgs {
   float* part;      // [splits][T][E] parts of the logits
   uint8_t* xq;      // [T][d]
   float* xs;        // [T]
-  float* hu;        // [P][n / 64][64 of H, 64 of U]: an item's first part
+  float* hu;        // [P][n / 128 up][128 of H, 128 of U]: the first part of an item in parts
   __nv_bfloat16 *A, *A_lo;  // [P][n]
-  float* y;         // [P][d rounded up to 128]
-  float *ov1, *ov2; // [2][blocks][T][128]: parts of items that began in another block
+  float* y;         // [P][d rounded up to 256]
+  float *ov1, *ov2; // [2][blocks][T][256]: parts of items that began in another block
   int nctr, splits, stages, nrows;
   int* err;
   unsigned long long timeout_ns;
@@ -314,7 +314,7 @@ FewLayout few_layout(int T, int d, int E, int n, int K);
 int few_blocks(int num_sms);
 int few_splits(int T, int d, int E, int num_sms);
 cudaError_t launch_few_router(const FewArgs& args, cudaStream_t s);
-// Maps over 16-bit units: gate and up with boxes of 64 rows, down of 128.
+// Maps over 16-bit units, boxes of 128 rows.
 cudaError_t launch_few_layer(const FewArgs& args, bool f8, const CUtensorMap& mg, const CUtensorMap& mu,
                              const CUtensorMap& md, int num_sms, cudaStream_t s);
 
