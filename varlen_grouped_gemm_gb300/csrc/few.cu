@@ -14,12 +14,13 @@
 //   * both products run in one launch, and the loads of the second do not wait for the first: the producers go on to
 //     W_down's stages while the activations are still being made, so HBM keeps working through that step.
 //
+// A block runs through most of the code once or a few times, and fetches it from memory as it goes: loops are kept short rather
+// than unrolled.
+//
 // bf16: A = silu(H) U enters the second product as its bf16 value and the bf16 rounding of the rest, as further columns
 // of the same tile (they cost nothing: the products are far below the tensor cores' rate).  e4m3: X quantized per token
 // and A (rounded to bf16) per pair, as moe_quantize_rows_e4m3 does.  Sums are fp32; O is rounded once.
 #include <cuda_fp8.h>
-
-#include <type_traits>
 
 #include "internal.h"
 
@@ -29,7 +30,7 @@ namespace {
 
 constexpr int kEpi = 4;      // epilogue warps 0..3 (TMEM lanes 32 w ..)
 constexpr int kGath = 6;     // gather warps: a stage of the ring each
-constexpr int kProd = 4;     // TMA producers: loads issued by one thread complete one after another
+constexpr int kProd = 2;     // TMA producers (loads issued by one thread complete one after another)
 constexpr int kGath0 = kEpi, kMma = kEpi + kGath, kProd0 = kMma + 1;
 constexpr int kWarps = kProd0 + kProd;
 constexpr int kThreads = 32 * kWarps;
@@ -44,7 +45,8 @@ constexpr int kMaxPairs = kFewMaxTokens * 8;
 // Tiles' accumulators, where TMEM has room: the second product's items may be as short as a stage, and a pair of accumulators
 // leaves the products waiting for the epilogue's latency.
 constexpr int kMaxAccs = 4;
-constexpr int kMaxStages = 6, kMinStages = kProd;  // (the producers take stages in turn, too)
+constexpr int kMaxStages = 6, kMinStages = 4;  // (the producers take stages in turn, too)
+static_assert(kProd <= kMinStages && kMinStages >= 3, "the ring");
 // Every block finds the choice of so few tokens itself; of more, each is found by one block behind a barrier (a block
 // reads splits x T x E partial logits otherwise).
 constexpr int kOwnChoice = 8;
@@ -52,14 +54,16 @@ constexpr int kRound = 16;   // tokens whose logits a block holds at a time
 // counters: choices made, items with activations of each half, blocks done, then one for each shared item
 constexpr int kCtrChoice = 0, kCtrItems = 1, kCtrDone = 3, kCtrShared = 4;
 
+// landed, full, empty: a stage's weights are there, its tokens' rows, its place is free.
 struct Lists {
-  uint64_t full[kMaxStages], empty[kMaxStages], tfull[kMaxAccs], tempty[kMaxAccs], drain;
+  uint64_t landed[kMaxStages], full[kMaxStages], empty[kMaxStages], tfull[kMaxAccs], tempty[kMaxAccs], drain;
   uint32_t tmem;
   volatile int abort;
   int active, last, ok;
   uint32_t chunk[32];          // pairs and experts (<< 16) of 32 experts each
   float xs[kFewMaxTokens];     // scales of X's codes (e4m3)
-  float pw[kMaxPairs];         // [token][rank]: combine weight, experts of a token ascending
+  float pw[kMaxPairs];         // combine weight of a pair
+  float factor[2][kFewMaxTokens];  // of the second product's columns, for two experts in turn
   uint16_t act_e[kMaxPairs];   // expert of each chosen expert's index, ascending
   uint16_t act_off[kMaxPairs + 1];  // its first pair
   uint16_t tok_pair[kMaxPairs], tok_a[kMaxPairs];  // [token][rank]: pair, index of its expert
@@ -187,6 +191,12 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
                : "r"(taddr));
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ void tmem_ld1(uint32_t taddr, float& v) {
+  uint32_t r;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
+  v = __uint_as_float(r);
 }
 
 __device__ __forceinline__ float row_scale(uint32_t amax_bits) {
@@ -419,6 +429,22 @@ __device__ __forceinline__ void choose(const FewArgs& a, int first, int step, in
   __syncthreads();
 }
 
+// A = silu(H) U of one column (a lane's) of pair p: bf16 and the bf16 rounding of the rest, or, for the e4m3 form, bf16 and the
+// pair's largest magnitude.  Lanes past the last column (in false) have none.
+template <bool F8>
+__device__ __forceinline__ void activate(const FewArgs& a, long long p, int col, bool in, float h, float u) {
+  const float act = h * sigmoidf_(h) * u;
+  const __nv_bfloat16 hi = __float2bfloat16_rn(act);
+  const long long at = p * a.n + col;
+  if (in) a.A[at] = hi;
+  if (F8) {
+    const uint32_t top = __reduce_max_sync(0xffffffffu, in ? __float_as_uint(fabsf(__bfloat162float(hi))) : 0u);
+    if ((threadIdx.x & 31) == 0) atomicMax(a.amax + p, top);
+  } else if (in) {
+    a.A_lo[at] = __float2bfloat16_rn(act - __bfloat162float(hi));
+  }
+}
+
 template <bool F8>
 __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_constant__ FewArgs a,
                                                                const __grid_constant__ CUtensorMap mg,
@@ -437,7 +463,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
 
   if (tid == 0) {
     for (int s = 0; s < a.stages; ++s) {
-      mbar_init(&L.full[s], 1 + 32);
+      mbar_init(&L.landed[s], 1);
+      mbar_init(&L.full[s], 32);
       mbar_init(&L.empty[s], 1);
     }
     for (int i = 0; i < accs; ++i) {
@@ -518,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
         L.ptok[p] = static_cast<uint8_t>(t);
         L.tok_pair[t * a.K + rank] = static_cast<uint16_t>(p);
         L.tok_a[t * a.K + rank] = static_cast<uint16_t>(ai);
-        L.pw[t * a.K + rank] = s_w[lane];
+        L.pw[p] = s_w[lane];
       }
       const int act = __popc(__ballot_sync(0xffffffffu, lane < P && head));
       if (lane == 0) {
@@ -573,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
       for (int k = 0; k < a.K; ++k) rank += s_ids[t * a.K + k] < e;
       L.tok_pair[t * a.K + rank] = static_cast<uint16_t>(p);
       L.tok_a[t * a.K + rank] = s_ea[e];
-      L.pw[t * a.K + rank] = s_w[i];
+      L.pw[p] = s_w[i];
     }
   }
   fence_proxy_async_smem();  // the scratch's uses come before the copies that overwrite it
@@ -591,6 +618,13 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
   plan.t2 = (a.d + kTile - 1) / kTile;
   plan.c2 = (a.n * es + 127) / 128;
   plan.cut = plan.A * plan.t1 * plan.c1 >= kHalves * G ? plan.A / 2 : 0;
+  // Stages of weights asked for and not there yet.  HBM needs about 100 KB a block in flight; what is asked for beyond waits in
+  // the memory system, and everything else behind it: the activations' way through L2 takes several times as long.  Long
+  // lists gain by the deeper queue, short ones by the shorter way (two and all six stages: 4 x 2048 x 128 x 512 51.7 and
+  // 59.0 us, 64 tokens e4m3 94 and 99, bf16 152 and 144; 24 x 2880 x 128 x 2880 553 and 518; three: 1 x 7168 x 64 x 2048 e4m3
+  // 74.1 and 77.5).  The ring is as deep all the same: it fills while a block waits for the activations.
+  const int share = plan.A * (plan.t1 * plan.c1 + plan.t2 * plan.c2) / G;
+  const int ahead = share < 100 ? 2 : share < 150 ? 3 : a.stages;
   const int ld_hu = plan.t1 * kTile, ld_y = plan.t2 * kTile;
   // a last tile of W_down may have rows in its first half alone
   auto halves = [&](const List& x, int tile) { return x.ph == 1 && a.d - tile * kTile <= kRows ? 1 : 2; };
@@ -612,16 +646,23 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
               stop = true;
               break;
             }
+            // not more than `ahead` stages on their way: the one that many back has landed
+            const int back = s - ahead;
+            if (it >= ahead && !mbar_wait(&L.landed[back < 0 ? back + a.stages : back], back < 0 ? par : par ^ 1, &L.abort,
+                                           a.timeout_ns, a.err)) {
+              stop = true;
+              break;
+            }
             uint8_t* dst = ring + s * stage_bytes;
             const int e = L.act_e[w.ai];
             const int hs = halves(x, w.tile);
-            mbar_arrive_expect_tx(&L.full[s], hs * kHBytes);
+            mbar_arrive_expect_tx(&L.landed[s], hs * kHBytes);
             if (x.ph == 0) {
-              tma_load_3d(dst, &mg, &L.full[s], w.k * 64, w.tile * kRows, e);
-              tma_load_3d(dst + kHBytes, &mu, &L.full[s], w.k * 64, w.tile * kRows, e);
+              tma_load_3d(dst, &mg, &L.landed[s], w.k * 64, w.tile * kRows, e);
+              tma_load_3d(dst + kHBytes, &mu, &L.landed[s], w.k * 64, w.tile * kRows, e);
             } else {
-              tma_load_3d(dst, &md, &L.full[s], w.k * 64, w.tile * kTile, e);
-              if (hs == 2) tma_load_3d(dst + kHBytes, &md, &L.full[s], w.k * 64, w.tile * kTile + kRows, e);
+              tma_load_3d(dst, &md, &L.landed[s], w.k * 64, w.tile * kTile, e);
+              if (hs == 2) tma_load_3d(dst + kHBytes, &md, &L.landed[s], w.k * 64, w.tile * kTile + kRows, e);
             }
           }
           if (++s == a.stages) {
@@ -687,22 +728,21 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
             const bool in = off < a.n;
             const uint4* src = reinterpret_cast<const uint4*>(a.A + static_cast<long long>(p0) * a.n + (in ? off : 0));
             const int ld = a.n / 8;
-            for (int r0 = rsub; r0 < m; r0 += 16) {  // four rows' loads in flight
-              uint4 v[4][2];
-              float sc[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (r0 + 4 * i < m) {
-                  const uint4* row = src + static_cast<long long>(r0 + 4 * i) * ld;
-                  v[i][0] = __ldcg(row);
-                  v[i][1] = __ldcg(row + 1);
-                  sc[i] = row_scale(__ldcg(a.amax + p0 + r0 + 4 * i));
-                }
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (r0 + 4 * i < m)
-                  *reinterpret_cast<uint4*>(tok + sw128_offset(r0 + 4 * i, c16)) =
-                      in ? codes16(v[i][0], v[i][1], sc[i]) : make_uint4(0, 0, 0, 0);
+            uint4 v0, v1;
+            uint32_t top = 0;
+            auto load = [&](int r) {
+              const uint4* at = src + static_cast<long long>(r) * ld;
+              v0 = __ldcg(at);
+              v1 = __ldcg(at + 1);
+              top = __ldcg(a.amax + p0 + r);
+            };
+            if (rsub < m) load(rsub);
+#pragma unroll 1
+            for (int r = rsub; r < m; r += 4) {
+              const uint4 x0 = v0, x1 = v1;
+              const float sc = row_scale(top);
+              if (r + 4 < m) load(r + 4);
+              *reinterpret_cast<uint4*>(tok + sw128_offset(r, c16)) = in ? codes16(x0, x1, sc) : make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async_smem();
             mbar_arrive(&L.full[s]);
@@ -740,7 +780,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
         const bool two = halves(x, w.tile) == 2;
         uint32_t more = 0;
         for (; w.k < k1; ++w.k, ++w.q) {
-          stop = __any_sync(0xffffffffu, !mbar_wait(&L.full[s], par, &L.abort, a.timeout_ns, a.err));
+          stop = __any_sync(0xffffffffu, !mbar_wait(&L.landed[s], par, &L.abort, a.timeout_ns, a.err) ||
+                                             !mbar_wait(&L.full[s], par, &L.abort, a.timeout_ns, a.err));
           if (stop) break;
           fence_proxy_async_smem();  // cp.async writes -> operand reads
           tc_fence_after();
@@ -777,7 +818,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
     // stage goes to the item's place, another block's to that block's own overflow rows (in a list a block goes on with at
     // most one item that began elsewhere).
     const int row = tid;
-    int acc = 0;
+    int acc = 0, last = -1, turn = 0;
     bool stop = false;
     for (int l = 0; l < kLists && !stop; ++l) {
       const List x = plan.list(l);
@@ -786,6 +827,14 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
       float* const first = x.ph ? a.y : a.hu;
       float* const over = (x.ph ? a.ov2 : a.ov1) + static_cast<long long>(x.half) * kFewMaxBlocks * a.T * kTile;
       int items = 0;  // completed here, of the first product
+      if (F8 && x.ph == 1) {  // the factors below need the pairs' largest magnitudes
+        const List made = plan.list(x.half);
+        const bool go = tid > 0 || wait_count(&a.ctr[kCtrItems + x.half], made.S / made.c, &L.abort, a.timeout_ns, a.err);
+        if (!epi_all(go)) {
+          stop = true;
+          break;
+        }
+      }
       Walk w;
       for (w.start(x, b); w.q < w.end; ++acc) {
         const int k0 = w.k, k1 = min(x.c, k0 + (w.end - w.q));
@@ -796,33 +845,28 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
         const bool whole = k1 - k0 == x.c, two = halves(x, tile) == 2;
         const int slot = acc & (accs - 1);
         const uint32_t tb = tmem + (static_cast<uint32_t>(warp * 32) << 16) + slot * 2 * half_cols;
-        // the first product's column of this thread
-        const int col = tile * kRows + row;
+        const int col = tile * kRows + row;  // the first product's column of this thread
         const bool in = col < a.n;
-        float gs = 1.0f, us = 1.0f;
+        // e4m3: scales of this thread's two rows of weights; H and U take their token's, the second product's columns a factor
+        float s0 = 1.0f, s1 = 1.0f;
         if (F8 && x.ph == 0 && in) {
           const long long at = static_cast<long long>(L.act_e[ai]) * a.n + col;
-          gs = __ldg(a.wg_scale + at);
-          us = __ldg(a.wu_scale + at);
+          s0 = __ldg(a.wg_scale + at);
+          s1 = __ldg(a.wu_scale + at);
         }
-        // A = silu(H) U of this thread's column for pair p0 + j
-        auto activate = [&](int j, float h, float u) {
+        if (x.ph == 1) {
           if (F8) {
-            const float sx = L.xs[L.ptok[p0 + j]];
-            h *= sx * gs;
-            u *= sx * us;
+            const int r = tile * kTile + row;
+            const float* at = a.wd_scale + static_cast<long long>(L.act_e[ai]) * a.d + r;
+            s0 = r < a.d ? __ldg(at) : 0.0f;
+            s1 = r + kRows < a.d ? __ldg(at + kRows) : 0.0f;
           }
-          const float act = h * sigmoidf_(h) * u;
-          const __nv_bfloat16 hi = __float2bfloat16_rn(act);
-          const long long at = static_cast<long long>(p0 + j) * a.n + col;
-          if (in) a.A[at] = hi;
-          if (F8) {
-            const uint32_t top = __reduce_max_sync(0xffffffffu, in ? __float_as_uint(fabsf(__bfloat162float(hi))) : 0u);
-            if (lane == 0) atomicMax(a.amax + p0 + j, top);
-          } else if (in) {
-            a.A_lo[at] = __float2bfloat16_rn(act - __bfloat162float(hi));
+          if (ai != last) {  // the factors are the expert's: one load for all of its tiles
+            last = ai;
+            turn ^= 1;
+            if (row < m) L.factor[turn][row] = L.pw[p0 + row] * (F8 ? row_scale(__ldcg(a.amax + p0 + row)) : 1.0f);
           }
-        };
+        }
         float* dst;
         int step;
         if (k0 == 0) {
@@ -838,33 +882,43 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
           break;
         }
         tc_fence_after();
-        for (int j0 = 0; j0 < m; j0 += 8) {
-          float v[2][8];
-          tmem_ld8(tb + j0, v[0]);
-          if (two) tmem_ld8(tb + half_cols + j0, v[1]);
-          if (!F8 && x.ph == 1) {
-            float lo[2][8];
-            tmem_ld8(tb + mh + j0, lo[0]);
-            if (two) tmem_ld8(tb + half_cols + mh + j0, lo[1]);
+        if (x.ph == 0 && whole) {
+#pragma unroll 1
+          for (int j = 0; j < m; ++j) {
+            float h, u;
+            tmem_ld1(tb + j, h);
+            tmem_ld1(tb + half_cols + j, u);
             tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              v[0][i] += lo[0][i];
-              v[1][i] += lo[1][i];
-            }
-          } else {
-            tmem_ld_wait();
+            const float sx = F8 ? L.xs[L.ptok[p0 + j]] : 1.0f;
+            activate<F8>(a, p0 + j, col, in, h * (sx * s0), u * (sx * s1));
           }
-          if (x.ph == 0 && whole) {
+        } else {
+          const float* factor = L.factor[turn];
+#pragma unroll 1
+          for (int j0 = 0; j0 < m; j0 += 8) {
+            float v[2][8];
+            tmem_ld8(tb + j0, v[0]);
+            if (two) tmem_ld8(tb + half_cols + j0, v[1]);
+            if (!F8 && x.ph == 1) {
+              float lo[2][8];
+              tmem_ld8(tb + mh + j0, lo[0]);
+              if (two) tmem_ld8(tb + half_cols + mh + j0, lo[1]);
+              tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (j0 + i < m) activate(j0 + i, v[0][i], v[1][i]);
-          } else {
+              for (int i = 0; i < 8; ++i) {
+                v[0][i] += lo[0][i];
+                v[1][i] += lo[1][i];
+              }
+            } else {
+              tmem_ld_wait();
+            }
 #pragma unroll
             for (int i = 0; i < 8; ++i)
               if (j0 + i < m) {
-                __stcg(dst + static_cast<long long>(j0 + i) * step, v[0][i]);
-                if (two) __stcg(dst + static_cast<long long>(j0 + i) * step + kRows, v[1][i]);
+                const float f = x.ph ? factor[j0 + i] : 1.0f;
+                float* to = dst + static_cast<long long>(j0 + i) * step;
+                __stcg(to, v[0][i] * (F8 && x.ph ? f * s0 : f));
+                if (two) __stcg(to + kRows, v[1][i] * (F8 && x.ph ? f * s1 : f));
               }
           }
         }
@@ -875,51 +929,45 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
           ++items;
           continue;
         }
-        // an item in parts: the block that brings the last of them adds them up in block order
-        const int b0 = x.owner(item * x.c), b1 = x.owner(item * x.c + x.c - 1);
+        // an item in parts: the block that brings the last of them adds them up in block order, two pairs and four parts at a
+        // time
+        const int b0 = x.owner(item * x.c), parts = x.owner(item * x.c + x.c - 1) - b0 + 1;
         epi_sync();
-        if (tid == 0) L.last = atom_acq_rel(&a.ctr[kCtrShared + x.half * kFewMaxBlocks + b0]) == b1 - b0;
+        if (tid == 0) L.last = atom_acq_rel(&a.ctr[kCtrShared + x.half * kFewMaxBlocks + b0]) == parts - 1;
         epi_sync();
         if (!L.last) continue;
         ++items;
-        // U pairs and O parts of each at a time, their loads in flight together: an item cut into many parts is one of a
-        // short list, with few pairs
-        auto finish = [&](auto u_, auto o_) {
-          constexpr int U = decltype(u_)::value, O = decltype(o_)::value;
-          for (int j0 = 0; j0 < m; j0 += U) {
-            float h[U], u[U];
+#pragma unroll 1
+        for (int j0 = 0; j0 < m; j0 += 2) {
+          float h[2] = {0.0f, 0.0f}, u[2] = {0.0f, 0.0f};
+#pragma unroll 1
+          for (int o0 = 0; o0 < parts; o0 += 4) {
+            float y[2][4][2];
 #pragma unroll
-            for (int q = 0; q < U; ++q) {
-              const float* hu = a.hu + static_cast<long long>(p0 + j0 + q) * ld + tile * kTile + row;
-              h[q] = j0 + q < m ? __ldcg(hu) : 0.0f;
-              u[q] = j0 + q < m ? __ldcg(hu + kRows) : 0.0f;
-            }
-            for (int o = b0 + 1; o <= b1; o += O) {
-              float y[U][O][2];
+            for (int q = 0; q < 2; ++q)
 #pragma unroll
-              for (int q = 0; q < U; ++q)
+              for (int r = 0; r < 4; ++r) {
+                const bool has = j0 + q < m && o0 + r < parts;
+                const float* at = o0 + r == 0 ? a.hu + static_cast<long long>(p0 + j0 + q) * ld + tile * kTile + row
+                                              : over + (static_cast<long long>(b0 + o0 + r) * a.T + j0 + q) * kTile + row;
+                y[q][r][0] = has ? __ldcg(at) : 0.0f;
+                y[q][r][1] = has ? __ldcg(at + kRows) : 0.0f;
+              }
 #pragma unroll
-                for (int r = 0; r < O; ++r) {
-                  const bool has = j0 + q < m && o + r <= b1;
-                  const float* ov = over + (static_cast<long long>(o + r) * a.T + j0 + q) * kTile + row;
-                  y[q][r][0] = has ? __ldcg(ov) : 0.0f;
-                  y[q][r][1] = has ? __ldcg(ov + kRows) : 0.0f;
-                }
+            for (int q = 0; q < 2; ++q)
 #pragma unroll
-              for (int q = 0; q < U; ++q)
-#pragma unroll
-                for (int r = 0; r < O; ++r) {
-                  h[q] += y[q][r][0];
-                  u[q] += y[q][r][1];
-                }
-            }
-#pragma unroll
-            for (int q = 0; q < U; ++q)
-              if (j0 + q < m) activate(j0 + q, h[q], u[q]);
+              for (int r = 0; r < 4; ++r) {
+                h[q] += y[q][r][0];
+                u[q] += y[q][r][1];
+              }
           }
-        };
-        if (b1 - b0 > 1) finish(std::integral_constant<int, 1>{}, std::integral_constant<int, 8>{});
-        else finish(std::integral_constant<int, 4>{}, std::integral_constant<int, 1>{});
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+            if (j0 + q < m) {
+              const float sx = F8 ? L.xs[L.ptok[p0 + j0 + q]] : 1.0f;
+              activate<F8>(a, p0 + j0 + q, col, in, h[q] * (sx * s0), u[q] * (sx * s1));
+            }
+        }
       }
       if (stop || x.ph == 1) continue;
       epi_sync();
@@ -935,7 +983,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
   __syncthreads();
   tc_fence_after();
   if (warp == kMma) tmem_dealloc(tmem, tmem_cols);
-  // ---- the weighted sums, once every block's parts are there: eight lanes a token and four columns, one a choice ----
+  // ---- the sums over a token's choices, once every block's parts are there: eight lanes a token and four columns, one a choice ----
   if (L.abort) {  // a wait gave up (every thread sees so): let the copies in flight land before the block goes away
     const uint64_t t0 = globaltimer_ns();
     while (globaltimer_ns() - t0 < 20000000ull) {
@@ -949,57 +997,52 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
   const int quads = a.d / 4, units = a.T * quads, t2 = plan.t2, c2 = plan.c2;
   const List y0 = plan.list(2), y1 = plan.list(3);
   const int u1 = static_cast<int>(static_cast<long long>(units) * (b + 1) / G);
-  constexpr int kU = 2;  // units of a lane group at a time: their loads in flight together
+  constexpr int kU = 2;  // units of a lane group at a time, and four parts: their loads in flight together
+#pragma unroll 1
   for (int u0 = static_cast<int>(static_cast<long long>(units) * b / G) + 4 * kU * warp; u0 < u1; u0 += 4 * kU * kWarps) {
     const int k = lane & 7;
     float4 v[kU];
-    float w[kU];
-    int t[kU], col[kU], over0[kU], over1[kU];
-    const float* over[kU];
-    float4 scale[kU];
+    const float *main[kU], *over[kU];
+    int t[kU], col[kU], parts[kU];
 #pragma unroll
     for (int q = 0; q < kU; ++q) {
       const int u = u0 + 4 * q + (lane >> 3);
-      const bool in = u < u1 && k < a.K;
       v[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      scale[q] = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
-      over0[q] = over1[q] = 0;
-      over[q] = nullptr;
-      w[q] = 0.0f;
       t[q] = u / quads;
       col[q] = (u - t[q] * quads) * 4;
-      if (in) {
+      parts[q] = 0;
+      main[q] = over[q] = a.y;
+      if (u < u1 && k < a.K) {
         const int p = L.tok_pair[t[q] * a.K + k], ai = L.tok_a[t[q] * a.K + k];
-        v[q] = __ldcg(reinterpret_cast<const float4*>(a.y + static_cast<long long>(p) * ld_y + col[q]));
-        w[q] = L.pw[t[q] * a.K + k];
-        if (F8) {
-          w[q] *= row_scale(__ldcg(a.amax + p));
-          scale[q] = __ldg(reinterpret_cast<const float4*>(a.wd_scale + static_cast<long long>(L.act_e[ai]) * a.d + col[q]));
-        }
         const bool h = ai >= y1.a0;
         const int s0 = ((ai - (h ? y1.a0 : 0)) * t2 + col[q] / kTile) * c2;
-        over0[q] = (h ? y1 : y0).owner(s0) + 1;
-        over1[q] = (h ? y1 : y0).owner(s0 + c2 - 1) + 1;
-        over[q] = a.ov2 + ((static_cast<long long>(h) * kFewMaxBlocks + over0[q]) * a.T + (p - L.act_off[ai])) * kTile + col[q] % kTile;
+        const int b0 = (h ? y1 : y0).owner(s0);
+        parts[q] = (h ? y1 : y0).owner(s0 + c2 - 1) - b0 + 1;
+        main[q] = a.y + static_cast<long long>(p) * ld_y + col[q];
+        over[q] = a.ov2 + ((static_cast<long long>(h) * kFewMaxBlocks + b0) * a.T + (p - L.act_off[ai])) * kTile + col[q] % kTile;
       }
     }
+    const int most = __reduce_max_sync(0xffffffffu, max(parts[0], parts[1]));
+#pragma unroll 1
+    for (int o = 0; o < most; o += 4) {
+      float4 z[kU][4];
 #pragma unroll
-    for (int q = 0; q < kU; ++q)
-      for (int o = over0[q]; o < over1[q]; o += 4) {
-        float4 z[4];
+      for (int q = 0; q < kU; ++q)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          z[r] = o + r < over1[q] ? __ldcg(reinterpret_cast<const float4*>(over[q] + static_cast<long long>(o - over0[q] + r) * a.T * kTile))
-                                  : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          z[q][r] = o + r < parts[q] ? __ldcg(reinterpret_cast<const float4*>(
+                                           o + r == 0 ? main[q] : over[q] + static_cast<long long>(o + r) * a.T * kTile))
+                                     : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int q = 0; q < kU; ++q)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          v[q].x += z[r].x; v[q].y += z[r].y; v[q].z += z[r].z; v[q].w += z[r].w;
+          v[q].x += z[q][r].x; v[q].y += z[q][r].y; v[q].z += z[q][r].z; v[q].w += z[q][r].w;
         }
-      }
+    }
 #pragma unroll
     for (int q = 0; q < kU; ++q) {
       float4 x = v[q];
-      x.x *= w[q] * scale[q].x; x.y *= w[q] * scale[q].y; x.z *= w[q] * scale[q].z; x.w *= w[q] * scale[q].w;
 #pragma unroll
       for (int o = 1; o < 8; o <<= 1) {
         x.x += __shfl_xor_sync(0xffffffffu, x.x, o);
