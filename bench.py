@@ -127,6 +127,27 @@ def kernel_work(wl, P, dW_bytes=2):
         "dw_gate_up": (4 * P * d * n, 2 * T * d + 4 * P * n + 2 * dWb * E * n * d,
                        2 * P * d + 8 * P * n + 2 * dWb * E * n * d),
         "dw_down": (2 * P * d * n, 2 * T * d + 2 * P * n + dWb * E * d * n, 2 * P * d + 4 * P * n + dWb * E * d * n),
+        # activations kept in 8 bits (34 bytes for 32 values): the products that write and read H and U so, in the byte
+        # model's place of their bf16, and the passes over X
+        "gate_up_swiglu_kept8": (4 * P * d * n, 2 * T * d + 4 * E * n * d + 2 * P * n + 2 * P * n * 34 // 32,
+                                 2 * T * d + 4 * E * n * d + 4 * P * n + 2 * P * n * 34 // 32),
+        "gate_up_swiglu_e4m3_kept8": same(4 * P * d * n, T * d + 4 * T + 2 * E * n * d + 8 * E * n + 2 * P * n
+                                          + 2 * P * n * 34 // 32),
+        "gate_up_swiglu_mx_kept8": same(4 * P * d * n, T * d + T * d // 32 + 2 * E * n * d + 2 * E * n * d // 32 + P * n
+                                        + P * n // 32 + 2 * P * n * 34 // 32),
+        "dact_dswiglu_kept8": (2 * P * d * n, 2 * T * d + 2 * E * d * n + 6 * P * n + 2 * P * n * 34 // 32,
+                               2 * P * d + 2 * E * d * n + 12 * P * n + 2 * P * n * 34 // 32),
+        "dact_dswiglu_e4m3_kept8": (2 * P * d * n, T * d + 4 * T + E * d * n + 4 * E * n + 6 * P * n + 2 * P * n * 34 // 32,
+                                    P * d + 4 * P + E * d * n + 4 * E * n + 12 * P * n + 2 * P * n * 34 // 32),
+        "dact_dswiglu_mx_kept8": (2 * P * d * n, T * d + T * d // 32 + E * d * n + E * d * n // 32 + 8 * P * n
+                                  + 2 * P * n // 32 + 2 * P * n * 34 // 32,
+                                  P * d + P * d // 32 + E * d * n + E * d * n // 32 + 14 * P * n + 2 * P * n // 32
+                                  + 2 * P * n * 34 // 32),
+        "keep_rows8": same(0, 2 * T * d + T * d * 34 // 32),
+        "read_rows8": same(0, 2 * T * d + T * d * 34 // 32),
+        # the layer for a few tokens (outside the step), for 64 of the workload's with experts of their own as far as they go
+        "few_router": same(2 * min(T, 64) * d * E, 2 * d * E + 2 * min(T, 64) * d),
+        "few_layer": same(6 * min(T, 64) * K * d * n, 6 * min(E, min(T, 64) * K) * d * n + 4 * min(T, 64) * d),
         # around the layer (outside the step): the norm with per-row codes and its backward on a bf16 stream, the
         # balance loss with its gradient, the router's products for it (dlogits as three bf16 parts, dX takes two)
         "add_rmsnorm": same(6 * T * d, 9 * T * d + 8 * T + 2 * d),
@@ -253,10 +274,14 @@ _GEMM_LABELS = {
     (2, 3, 2, 0): "dwr_gemm", (2, 4, 1, 0): "dw_gather_b", (3, 3, 1, 0): "dw_gather_a",
     (1, 1, 0, 4): "gate_up_swiglu_e4m3", (0, 0, 0, 5): "down_scale_e4m3", (0, 0, 0, 6): "dx_gemm_e4m3",
     (0, 0, 0, 7): "dact_dswiglu_e4m3", (0, 0, 2, 8): "router_dx",
+    # H and U kept in 8 bits (template flag X_KEPT8 = 16)
+    (1, 1, 0, 1, 16): "gate_up_swiglu_kept8", (0, 2, 0, 3, 16): "dact_dswiglu_kept8",
+    (1, 1, 0, 4, 16): "gate_up_swiglu_e4m3_kept8", (0, 0, 0, 7, 16): "dact_dswiglu_e4m3_kept8",
 }
 # the block-scaled form (template flag X_MX = 8)
 _MX_GEMM_LABELS = {(1, 1, 0, 1): "gate_up_swiglu_mx", (0, 0, 0, 2): "down_scale_mx", (0, 0, 0, 3): "dact_dswiglu_mx",
-                   (0, 0, 0, 0): "dx_gemm_mx", (0, 0, 1, 0): "dw_mx (gate/up, down)"}
+                   (0, 0, 0, 0): "dx_gemm_mx", (0, 0, 1, 0): "dw_mx (gate/up, down)",
+                   (1, 1, 0, 1, 16): "gate_up_swiglu_mx_kept8", (0, 0, 0, 3, 16): "dact_dswiglu_mx_kept8"}
 _OTHER_LABELS = {
     "topk_softmax_kernel": "topk_softmax", "perm_hist_kernel": "permute", "perm_scan_kernel": "permute",
     "perm_scatter_kernel": "permute", "tr_select_kernel": "permute", "transpose_f32_kernel": "permute",
@@ -268,6 +293,8 @@ _OTHER_LABELS = {
     "zero_tail_rows_kernel": "zero_tail", "quantize_rows_e4m3_kernel": "quantize_e4m3",
     "pad_offsets_kernel": "pad_offsets", "quantize_rows_mx_kernel": "quantize_mx",
     "quantize_weight_mx_kernel": "quantize_mx_weights", "mx_tile_scales_kernel": "mx_tile_scales",
+    "keep_rows8_kernel": "keep_rows8", "read_rows8_kernel": "read_rows8", "few_router_kernel": "few_router",
+    "few_layer_kernel": "few_layer",
     "quantize_cols_mx_kernel": "quantize_cols_mx", "mx_stage_offsets_kernel": "mx_stage_offsets",
 }
 
@@ -290,7 +317,10 @@ def _label_of(name: str):
     if m:
         a = [x.strip() for x in m.group(1).split(",")]
         key = (int(a[4]), int(a[5]), int(a[6]), int(a[7]))
-        if len(a) > 10 and a[10].isdigit() and int(a[10]) & 8:
+        flags = int(a[10]) if len(a) > 10 and a[10].isdigit() else 0
+        if flags & 16:
+            key += (16,)
+        if flags & 8:
             return _MX_GEMM_LABELS.get(key, "grouped_gemm " + m.group(1))
         return _GEMM_LABELS.get(key, "grouped_gemm " + m.group(1))
     for k, v in _OTHER_LABELS.items():

@@ -1,6 +1,6 @@
 """One training step of a pre-norm block whose feed-forward part is the expert layer, with a router balance loss.
 
-    python examples/prenorm_block.py [--form bf16|e4m3|mx] [--tokens T] [--steps N]
+    python examples/prenorm_block.py [--form bf16|e4m3|mx] [--tokens T] [--steps N] [--kept8] [--decode B]
 
 For a sublayer's output x and the residual stream r (attention and the rest of the model lie outside):
 
@@ -8,7 +8,8 @@ For a sublayer's output x and the residual stream r (attention and the rest of t
     out = h + MoE(y),  loss = mean((out - target)^2) / 2 + balance_coef * balance + z_coef * z
 
 and backwards: the layer, the balance loss's gradient through the router, the norm.  Each weight takes a
-step against its gradient, so the printed loss falls.
+step against its gradient, so the printed loss falls.  With --kept8 the step keeps the layer's activations in 8 bits.
+--decode B then runs the trained block on B tokens at a time, as a decoding step of B sequences does.
 """
 from __future__ import annotations
 
@@ -53,12 +54,13 @@ class Block:
     ws_balance: torch.Tensor
     ws_router: torch.Tensor
     seq_offsets: torch.Tensor | None = None
+    kept8: bool = False     # the layer's activations are kept in 8 bits
     balance_coef: float = 1e-2
     z_coef: float = 1e-3
     eps: float = 1e-6
 
     @staticmethod
-    def make(T, d, E, n, K, form="bf16", seq_offsets=None, seed=0, device="cuda") -> "Block":
+    def make(T, d, E, n, K, form="bf16", seq_offsets=None, seed=0, device="cuda", kept8=False) -> "Block":
         g = torch.Generator(device=device).manual_seed(seed)
 
         def normal(*shape, std):
@@ -72,12 +74,12 @@ class Block:
             vgg.Context(torch.device(device).index or 0), form, torch.ones(d, device=device),
             normal(d, E, std=d ** -0.5), normal(E, n, d, std=d ** -0.5), normal(E, n, d, std=d ** -0.5),
             normal(E, d, n, std=n ** -0.5),
-            vgg.Buffers.allocate(T, d, E, n, K, e4m3=form == "e4m3", mx=form == "mx", device=device),
+            vgg.Buffers.allocate(T, d, E, n, K, e4m3=form == "e4m3", mx=form == "mx", device=device, kept8=kept8),
             empty(T, d), empty(T, d, dtype=BF), empty(T), empty(3), empty(B, E, dtype=torch.int32), empty(B, E),
             empty(T, E), empty(T, d, dtype=BF), empty(T, d), empty(d),
             empty(vgg.moe_add_rmsnorm_workspace_bytes(T, d), dtype=U8),
             empty(vgg.moe_balance_loss_workspace_bytes(T, E, B), dtype=U8),
-            empty(vgg.moe_router_backward_workspace_bytes(T, d, E), dtype=U8), seq_offsets)
+            empty(vgg.moe_router_backward_workspace_bytes(T, d, E), dtype=U8), seq_offsets, kept8)
 
     def forward(self, x, residual):
         """out = h + MoE(rmsnorm(h)), fp32, for x [T, d] bf16 and the stream residual [T, d] fp32."""
@@ -100,15 +102,33 @@ class Block:
         """Gradients for dout [T, d] fp32: dx, dres, dweight here, the layer's (dW_r with the balance loss's) in buf."""
         b, w = self.buf, (self.W_r, self.W_gate, self.W_up, self.W_down)
         dO = dout.to(BF)
+        y = None if self.kept8 else self.y  # kept in 8 bits: the layer's X comes from its codes, y may go after the forward
         if self.form == "e4m3":
-            vgg.backward_e4m3(self.ctx, dO, self.y, *w, self.quantized, b)
+            vgg.backward_e4m3(self.ctx, dO, y, *w, self.quantized, b)
         elif self.form == "mx":
-            vgg.backward_mx(self.ctx, dO, self.y, *w, self.quantized, b)
+            vgg.backward_mx(self.ctx, dO, y, *w, self.quantized, b)
         else:
-            vgg.backward(self.ctx, dO, self.y, *w, b)
+            vgg.backward(self.ctx, dO, y, *w, b)
         vgg.moe_router_backward(self.ctx, self.dlogits, self.y, self.W_r, b.dX, b.dW_r, b.dX, b.dW_r, self.ws_router)
         vgg.moe_add_rmsnorm_backward(self.ctx, b.dX, self.h, self.weight, self.rstd, dout, self.dx, self.dres, self.dweight,
                                      self.ws_norm)
+
+
+    def decoder(self, tokens):
+        """step(x, residual) for up to 64 tokens: the block's output as ``forward`` gives it, without what a backward needs."""
+        E, n, d = self.W_gate.shape
+        few = vgg.FewBuffers.allocate(tokens, d, E, n, self.buf.K, device=self.W_gate.device)
+        h, y = torch.empty((tokens, d), device=self.W_gate.device), torch.empty((tokens, d), dtype=BF, device=self.W_gate.device)
+        weights = (self.W_gate, self.W_up, self.W_down)
+        if self.form == "e4m3":
+            weights = vgg.E4m3Weights.quantize(self.ctx, *weights)
+
+        def step(x, residual):
+            vgg.moe_add_rmsnorm(self.ctx, x, residual, self.weight, self.eps, h, y)
+            vgg.forward_few(self.ctx, y, self.W_r, None, weights, few)
+            return h + few.O
+
+        return step
 
 
 def main():
@@ -117,9 +137,11 @@ def main():
     ap.add_argument("--tokens", type=int, default=4096)
     ap.add_argument("--steps", type=int, default=8)
     ap.add_argument("--lr", type=float, default=0.02)
+    ap.add_argument("--kept8", action="store_true", help="keep the layer's activations in 8 bits between forward and backward")
+    ap.add_argument("--decode", type=int, default=0, metavar="B", help="then decode B tokens at a time (at most 64)")
     a = ap.parse_args()
     T, d, E, n, K = a.tokens, 2048, 128, 512, 8
-    blk = Block.make(T, d, E, n, K, a.form)
+    blk = Block.make(T, d, E, n, K, a.form, kept8=a.kept8)
     g = torch.Generator(device="cuda").manual_seed(1)
     x = torch.randn((T, d), device="cuda", generator=g).to(BF)
     residual = torch.randn((T, d), device="cuda", generator=g)
@@ -138,6 +160,18 @@ def main():
                       (blk.W_up, blk.buf.dW_up), (blk.W_down, blk.buf.dW_down)):
             # a step against the gradient, a share lr of the weight's own size
             w.sub_(a.lr * w.float().norm() / dw.float().norm().clamp(min=1e-30) * dw.float())
+    if a.decode:
+        step = blk.decoder(a.decode)
+        xd, rd = x[:a.decode].contiguous(), residual[:a.decode].contiguous()
+        for _ in range(3):
+            step(xd, rd)
+        beg, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        beg.record()
+        for _ in range(32):
+            rd = step(xd, rd)  # each step's output is the next one's stream
+        end.record()
+        end.synchronize()
+        print(f"decoding {a.decode} tokens: {beg.elapsed_time(end) / 32 * 1e3:.1f} us a step")
     rc, code = vgg.moe_get_error(blk.ctx)
     if rc != vgg.MOE_OK:
         raise RuntimeError(f"device error {code}: {vgg.status_str(rc)}")

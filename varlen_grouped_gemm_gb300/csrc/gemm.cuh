@@ -91,7 +91,7 @@ enum VarMode { VAR_M = 0, VAR_K = 1, VAR_NONE = 2 };
 //   X_KEPT8   H and U are kept in 8 bits (kept8_block32): the SwiGLU epilogues write their codes and scales (out0, out1,
 //             k_h, k_u) in place of fp32, the dSwiGLU epilogues read them (in0, in1).  A thread holds 32 columns of
 //             its row, a block with its scale, so nothing is exchanged.
-enum XFlags { X_DUAL_A = 1, X_TRANS = 2, X_PAIR = 4, X_MX = 8, X_KEPT8 = 16 };
+enum XFlags { X_DUAL_A = 1, X_TRANS = 2, X_PAIR = 4, X_MX = 8, X_KEPT8 = 16, X_MX_KEPT8 = 24 };
 enum EpiKind {
   EPI_STORE = 0, EPI_SWIGLU = 1, EPI_SCALE = 2, EPI_DSWIGLU = 3, EPI_SWIGLU_Q = 4, EPI_SCALE_Q = 5, EPI_STORE_Q = 6,
   EPI_DSWIGLU_Q = 7, EPI_ADD = 8

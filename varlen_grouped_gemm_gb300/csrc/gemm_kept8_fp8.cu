@@ -14,9 +14,9 @@ cudaError_t run_gate_up_swiglu_e4m3_kept8(int BN, int cn, const GemmParams& p, c
 
 cudaError_t run_gate_up_swiglu_mx_kept8(int cn, const GemmParams& p, const Maps& m, int grid, cudaStream_t s) {
   if (cn == 2)
-    return launch_grouped_gemm<kMxBN, 4, 4, 1, A_GATHER_K, B_TMA_K3_GU, VAR_M, EPI_SWIGLU, false, 2, X_MX | X_KEPT8>(p, m, grid,
+    return launch_grouped_gemm<kMxBN, 4, 4, 1, A_GATHER_K, B_TMA_K3_GU, VAR_M, EPI_SWIGLU, false, 2, X_MX_KEPT8>(p, m, grid,
                                                                                                               s);
-  return launch_grouped_gemm<kMxBN, 4, 4, 1, A_GATHER_K, B_TMA_K3_GU, VAR_M, EPI_SWIGLU, false, 1, X_MX | X_KEPT8>(p, m, grid, s);
+  return launch_grouped_gemm<kMxBN, 4, 4, 1, A_GATHER_K, B_TMA_K3_GU, VAR_M, EPI_SWIGLU, false, 1, X_MX_KEPT8>(p, m, grid, s);
 }
 
 cudaError_t run_dact_dswiglu_e4m3_kept8(int BN, const GemmParams& p, const Maps& m, int grid, cudaStream_t s) {
@@ -29,8 +29,8 @@ cudaError_t run_dact_dswiglu_e4m3_kept8(int BN, const GemmParams& p, const Maps&
 
 cudaError_t run_dact_dswiglu_mx_kept8(int BN, const GemmParams& p, const Maps& m, int grid, cudaStream_t s) {
   if (BN == 128)
-    return launch_grouped_gemm<128, 4, 8, 2, A_TMA_K, B_TMA_K3, VAR_M, EPI_DSWIGLU, false, 1, X_MX | X_KEPT8>(p, m, grid, s);
-  return launch_grouped_gemm<kMxBN, 4, 8, 1, A_TMA_K, B_TMA_K3, VAR_M, EPI_DSWIGLU, false, 1, X_MX | X_KEPT8>(p, m, grid, s);
+    return launch_grouped_gemm<128, 4, 8, 2, A_TMA_K, B_TMA_K3, VAR_M, EPI_DSWIGLU, false, 1, X_MX_KEPT8>(p, m, grid, s);
+  return launch_grouped_gemm<kMxBN, 4, 8, 1, A_TMA_K, B_TMA_K3, VAR_M, EPI_DSWIGLU, false, 1, X_MX_KEPT8>(p, m, grid, s);
 }
 
 }  // namespace vgg
