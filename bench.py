@@ -275,6 +275,7 @@ _GEMM_LABELS = {
     (1, 1, 0, 4): "gate_up_swiglu_e4m3", (0, 0, 0, 5): "down_scale_e4m3", (0, 0, 0, 6): "dx_gemm_e4m3",
     (0, 0, 0, 7): "dact_dswiglu_e4m3", (0, 0, 2, 8): "router_dx",
     # H and U kept in 8 bits (template flag X_KEPT8 = 16)
+    (0, 2, 0, 0, 32): "dx_gemm",  # (its rows in scaled fp16: X_F16S = 32)
     (1, 1, 0, 1, 16): "gate_up_swiglu_kept8", (0, 2, 0, 3, 16): "dact_dswiglu_kept8",
     (1, 1, 0, 4, 16): "gate_up_swiglu_e4m3_kept8", (0, 0, 0, 7, 16): "dact_dswiglu_e4m3_kept8",
 }
@@ -318,8 +319,8 @@ def _label_of(name: str):
         a = [x.strip() for x in m.group(1).split(",")]
         key = (int(a[4]), int(a[5]), int(a[6]), int(a[7]))
         flags = int(a[10]) if len(a) > 10 and a[10].isdigit() else 0
-        if flags & 16:
-            key += (16,)
+        if flags & 48:
+            key += (flags & 48,)
         if flags & 8:
             return _MX_GEMM_LABELS.get(key, "grouped_gemm " + m.group(1))
         return _GEMM_LABELS.get(key, "grouped_gemm " + m.group(1))

@@ -220,6 +220,27 @@ size_t bwd_ws_bytes(int T, int d, int E, int n, long long cap) {
          al(sizeof(float) * static_cast<size_t>(kMaxSplitK) * d * E);
 }
 
+// Behind the backward's workspace, from activations kept in 8 bits: X's values, the scales of the pairs' dX rows.
+struct KeptWs {
+  __nv_bfloat16* x;
+  float* dxp_scale;
+  size_t bytes;  // of the whole
+};
+KeptWs kept_ws(void* ws, int T, int d, int E, int n, long long cap) {
+  uint8_t* const base = static_cast<uint8_t*>(ws);
+  size_t p = bwd_ws_bytes(T, d, E, n, cap);
+  auto take = [&](size_t bytes) {
+    uint8_t* r = base + p;
+    p += al(bytes);
+    return r;
+  };
+  KeptWs w{};
+  w.x = reinterpret_cast<__nv_bfloat16*>(take(sizeof(__nv_bfloat16) * static_cast<size_t>(T) * d));
+  w.dxp_scale = reinterpret_cast<float*>(take(sizeof(float) * cap * (d / 64)));
+  w.bytes = p;
+  return w;
+}
+
 // Store maps of the dSwiGLU epilogue's low parts (o3..o5), like those of dH, dU, A'.
 bool make_lo_maps(Maps& m, const BwdWs& w, int n, long long cap) {
   return make_store_map_2d(&m.o3, w.dH_lo, false, n, cap, n, 32) && make_store_map_2d(&m.o4, w.dU_lo, false, n, cap, n, 32) &&
@@ -1095,11 +1116,15 @@ static int backward_impl(moe_ctx* ctx, const void* dO, const void* X, const void
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   BwdWs w = carve_bwd(ws, T, d, E, n, cap);
   if (!X) {  // the values that X's codes stand for, once: the copies by expert and the router's product read them
-    __nv_bfloat16* const xv = reinterpret_cast<__nv_bfloat16*>(static_cast<uint8_t*>(ws) + bwd_ws_bytes(T, d, E, n, cap));
+    __nv_bfloat16* const xv = kept_ws(ws, T, d, E, n, cap).x;
     VGG_LAUNCH("read_rows8", launch_read_rows8(static_cast<const uint8_t*>(kept->xq),
                                                static_cast<const __nv_bfloat16*>(kept->xs), static_cast<long long>(T) * d, xv, s));
     X = xv;
   }
+  // The bf16 form from kept activations holds dX closer: the pairs' dX rows are scaled fp16 (with bf16 rows the roundings of dH
+  // and dU, of the rows and of their sum leave 1.6 times the sum's own, 2.6e-3 normwise; so 1.3 times).
+  const bool fine = kept && !Wgu_q && !Wdt_q && !mx;
+  float* const dxp_scale = fine ? kept_ws(ws, T, d, E, n, cap).dxp_scale : nullptr;
   const bool f32 = dW_fp32 != 0;
   const int bn6 = dact_bn(n, cap, E, ctx->num_sms);
   // one dS partial per (column tile, epilogue column half); the block-scaled form tiles n by mx_tile_cols(n)
@@ -1322,14 +1347,16 @@ static int backward_impl(moe_ctx* ctx, const void* dO, const void* X, const void
     p.b_ksplit = n;
     p.out0 = w.dXp;
     p.ld_out = d;
+    p.o_scale = dxp_scale;
     const int BN = gemm_bn(d);
-    const VmShape sh = vm_shape(ctx, BN, true, cap, E, d);
+    const VmShape sh = vm_shape(ctx, BN, !fine, cap, E, d);
     Maps m = zero_maps();
     if (!make_map_2d(&m.a0, w.dH, n, cap, n, BM) || !make_map_2d(&m.a1, w.dU, n, cap, n, BM) ||
         !make_chunked_map_3d(&m.b0, W_gate, d, n, E, sh.b_cols / 64) ||
         !make_chunked_map_3d(&m.b1, W_up, d, n, E, sh.b_cols / 64) || !make_store_map_2d(&m.o0, w.dXp, false, d, cap, d, 64))
       return MOE_ERR_CUDA;
-    VGG_LAUNCH("dx_gemm", run_dx_store(BN, sh.pair, p, m, sh.grid, s));
+    if (fine) VGG_LAUNCH("dx_gemm", run_dx_store_f16s(BN, p, m, sh.grid, s));
+    else VGG_LAUNCH("dx_gemm", run_dx_store(BN, sh.pair, p, m, sh.grid, s));
   }
   // The per-token chain (wr_transpose, token_backward, dW_r) reads what the GEMMs above wrote and writes only
   // its own outputs and workspace regions, so it runs on the side stream while the weight-gradient GEMMs below
@@ -1355,8 +1382,8 @@ static int backward_impl(moe_ctx* ctx, const void* dO, const void* X, const void
       return MOE_ERR_CUDA;
   }
   VGG_LAUNCH("token_backward", launch_token_backward(w.part, part_ld, tok_ptr, tok_pairs, offsets, E, sorted_w,
-                                                     topk_ids, topk_w, K, w.dXp, w.WrT, T, d, cap, dS, dlogits, w.dL,
-                                                     dL_lo, static_cast<__nv_bfloat16*>(dX), ctx->d_err, s));
+                                                     topk_ids, topk_w, K, w.dXp, dxp_scale, w.WrT, T, d, cap, dS, dlogits,
+                                                     w.dL, dL_lo, static_cast<__nv_bfloat16*>(dX), ctx->d_err, s));
   // dW_r = X^T dlogits, split over tokens.  dlogits enters as X^T hi + X^T lo with hi = bf16(dlogits) and
   // lo = bf16(dlogits - hi), about 16 significant bits: a single bf16 rounding of dlogits costs up to a few
   // percent on the columns of heavily loaded experts, whose gradient sums thousands of tokens' rounding
@@ -1568,7 +1595,7 @@ int moe_backward_mx(moe_ctx* ctx, const void* dO, const void* X, const void* W_r
 
 size_t moe_kept8_workspace_bytes(int T, int d, int E, int n, long long cap) {
   if (!shapes_ok(T, d, E, n, 1) || cap < 1 || cap >= INT_MAX) return 0;
-  return bwd_ws_bytes(T, d, E, n, cap) + al(sizeof(__nv_bfloat16) * static_cast<size_t>(T) * d);
+  return kept_ws(nullptr, T, d, E, n, cap).bytes;
 }
 
 int moe_backward_kept8(moe_ctx* ctx, const void* dO, const void* X, const void* Xq, const void* x_scale, const void* W_r,

@@ -145,12 +145,13 @@ size_t token_backward_smem(int E) {
          kTbWarps * (sizeof(int) * kMaxTokPairs + (sizeof(int) + sizeof(float)) * kTbNz);
 }
 
+template <bool F16S>
 __global__ void __launch_bounds__(256) token_backward_kernel(
     const float* __restrict__ part, int part_ld, const int32_t* __restrict__ tok_ptr,
     const int32_t* __restrict__ tok_pairs, const int32_t* __restrict__ offsets, int E,
     const float* __restrict__ sorted_w, const int32_t* __restrict__ topk_ids, const float* __restrict__ topk_w, int K,
-    const __nv_bfloat16* __restrict__ dXp, const __nv_bfloat16* __restrict__ WrT, int T, int d, long long cap,
-    float* __restrict__ dS, float* __restrict__ dlogits, __nv_bfloat16* __restrict__ dL_bf16,
+    const __nv_bfloat16* __restrict__ dXp, const float* __restrict__ dXp_scale, const __nv_bfloat16* __restrict__ WrT, int T,
+    int d, long long cap, float* __restrict__ dS, float* __restrict__ dlogits, __nv_bfloat16* __restrict__ dL_bf16,
     __nv_bfloat16* __restrict__ dL_lo, __nv_bfloat16* __restrict__ dX, int* err) {
   extern __shared__ __align__(16) uint8_t tb_smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -226,19 +227,36 @@ __global__ void __launch_bounds__(256) token_backward_kernel(
   // of up to eight pairs), added in pair order; then the router part, eight W_r^T rows (L2-resident) per
   // round trip, in nonzero order.
   constexpr int kB = 8;
-  for (int c = lane; c < nv; c += 32) {
+  const int cols = F16S ? (nv + 31) & ~31 : nv;  // the lanes exchange scales: whole warps of columns
+  for (int c = lane; c < cols; c += 32) {
     float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     for (int r0 = 0; r0 < cnt; r0 += kB) {
       uint4 q[kB];
+      float sc = 0.0f;  // lane l: the scale of pair r0 + l / 4 for the columns of lanes 8 (l % 4) ..
+      if (F16S) {
+        const int u = r0 + (lane >> 2), at = (c - lane) / 8 + (lane & 3);
+        if (u < cnt && s_j[u] >= 0 && at < d / 64) sc = __ldg(dXp_scale + static_cast<long long>(s_j[u]) * (d / 64) + at);
+      }
 #pragma unroll
       for (int u = 0; u < kB; ++u) {
         const int j = r0 + u < cnt ? s_j[r0 + u] : -1;
-        q[u] = j >= 0 ? ldg_nc_v4(dXp + static_cast<long long>(j) * d + 8 * c) : make_uint4(0, 0, 0, 0);
+        q[u] = j >= 0 && (!F16S || c < nv) ? ldg_nc_v4(dXp + static_cast<long long>(j) * d + 8 * c) : make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
-      for (int u = 0; u < kB; ++u)
-        if (r0 + u < cnt && s_j[r0 + u] >= 0) add_bf16x8(acc, q[u]);
+      for (int u = 0; u < kB; ++u) {
+        const float f16 = F16S ? __shfl_sync(0xffffffffu, sc, 4 * u + (lane >> 3)) : 0.0f;
+        if (r0 + u < cnt && s_j[r0 + u] >= 0) {
+          if (F16S) {
+            const float2 a = unpack_f16x2(q[u].x), b = unpack_f16x2(q[u].y), e = unpack_f16x2(q[u].z), f = unpack_f16x2(q[u].w);
+            acc[0] += f16 * a.x; acc[1] += f16 * a.y; acc[2] += f16 * b.x; acc[3] += f16 * b.y;
+            acc[4] += f16 * e.x; acc[5] += f16 * e.y; acc[6] += f16 * f.x; acc[7] += f16 * f.y;
+          } else {
+            add_bf16x8(acc, q[u]);
+          }
+        }
+      }
     }
+    if (F16S && c >= nv) break;
     for (int i0 = 0; i0 < nnz; i0 += kB) {
       uint4 q[kB];
 #pragma unroll
@@ -261,17 +279,18 @@ __global__ void __launch_bounds__(256) token_backward_kernel(
 
 cudaError_t launch_token_backward(const float* part, int part_ld, const int32_t* tok_ptr, const int32_t* tok_pairs,
                                   const int32_t* offsets, int E, const float* sorted_w, const int32_t* topk_ids,
-                                  const float* topk_w, int K, const __nv_bfloat16* dXp, const __nv_bfloat16* WrT,
-                                  int T, int d, long long cap, float* dS, float* dlogits, __nv_bfloat16* dL_bf16,
-                                  __nv_bfloat16* dL_lo, __nv_bfloat16* dX, int* err, cudaStream_t s) {
+                                  const float* topk_w, int K, const __nv_bfloat16* dXp, const float* dXp_scale,
+                                  const __nv_bfloat16* WrT, int T, int d, long long cap, float* dS, float* dlogits,
+                                  __nv_bfloat16* dL_bf16, __nv_bfloat16* dL_lo, __nv_bfloat16* dX, int* err, cudaStream_t s) {
   if (T <= 0) return cudaSuccess;
   const size_t smem = token_backward_smem(E);
-  cudaError_t e = cudaFuncSetAttribute(token_backward_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  auto kern = dXp_scale ? token_backward_kernel<true> : token_backward_kernel<false>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(token_backward_smem(kMaxGroups)));  // one value for all threads
   if (e != cudaSuccess) return e;
-  token_backward_kernel<<<(T + kTbWarps - 1) / kTbWarps, 32 * kTbWarps, smem, s>>>(
-      part, part_ld, tok_ptr, tok_pairs, offsets, E, sorted_w, topk_ids, topk_w, K, dXp, WrT, T, d, cap, dS, dlogits,
-      dL_bf16, dL_lo, dX, err);
+  kern<<<(T + kTbWarps - 1) / kTbWarps, 32 * kTbWarps, smem, s>>>(
+      part, part_ld, tok_ptr, tok_pairs, offsets, E, sorted_w, topk_ids, topk_w, K, dXp, dXp_scale, WrT, T, d, cap, dS,
+      dlogits, dL_bf16, dL_lo, dX, err);
   return cudaGetLastError();
 }
 

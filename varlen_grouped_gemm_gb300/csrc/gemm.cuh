@@ -91,7 +91,9 @@ enum VarMode { VAR_M = 0, VAR_K = 1, VAR_NONE = 2 };
 //   X_KEPT8   H and U are kept in 8 bits (kept8_block32): the SwiGLU epilogues write their codes and scales (out0, out1,
 //             k_h, k_u) in place of fp32, the dSwiGLU epilogues read them (in0, in1).  A thread holds 32 columns of
 //             its row, a block with its scale, so nothing is exchanged.
-enum XFlags { X_DUAL_A = 1, X_TRANS = 2, X_PAIR = 4, X_MX = 8, X_KEPT8 = 16, X_MX_KEPT8 = 24 };
+//   X_F16S    the plain epilogue stores fp16 with a power of two for 64 columns of a row (o_scale) in place of bf16: the pairs'
+//             dX rows are added up afterwards, and fp16's three more bits make their rounding a tenth of the sum's.
+enum XFlags { X_DUAL_A = 1, X_TRANS = 2, X_PAIR = 4, X_MX = 8, X_KEPT8 = 16, X_MX_KEPT8 = 24, X_F16S = 32 };
 enum EpiKind {
   EPI_STORE = 0, EPI_SWIGLU = 1, EPI_SCALE = 2, EPI_DSWIGLU = 3, EPI_SWIGLU_Q = 4, EPI_SCALE_Q = 5, EPI_STORE_Q = 6,
   EPI_DSWIGLU_Q = 7, EPI_ADD = 8
@@ -150,6 +152,7 @@ struct GemmParams {
   int sf_kst;
   uint8_t* o_sf;
   int o_sf_kst;
+  float* o_scale;            // X_F16S: [rows][N / 64]
   __nv_bfloat16 *k_h, *k_u;  // X_KEPT8: scales of H and U, [rows][N / 32]
   uint8_t* o_q;        // the dSwiGLU epilogue's block-scaled [dH | dU] codes [rows][o_q_ld] (o_sf: their blocks)
   long long o_q_ld;
@@ -457,6 +460,8 @@ __global__ void __launch_bounds__(WarpPlan<STAGES, EW, AMODE, BMODE, CN, XF>::kT
   constexpr bool kPair = (XF & X_PAIR) != 0;
   constexpr bool kMx = (XF & X_MX) != 0;
   constexpr bool kKept8 = (XF & X_KEPT8) != 0;
+  constexpr bool kF16s = (XF & X_F16S) != 0;
+  static_assert(!kF16s || (EPI == EPI_STORE && VAR == VAR_M && !OUTF32 && XF == X_F16S), "scaled fp16: the plain varlen-M epilogue");
   static_assert(!kKept8 || EPI == EPI_SWIGLU || EPI == EPI_SWIGLU_Q || EPI == EPI_DSWIGLU || EPI == EPI_DSWIGLU_Q,
                 "activations kept in 8 bits: the SwiGLU epilogues and their gradient's");
   constexpr int kSfStage = mx_stage_bytes(BN, XF);
@@ -1240,6 +1245,25 @@ __global__ void __launch_bounds__(WarpPlan<STAGES, EW, AMODE, BMODE, CN, XF>::kT
         if (ncols > 32) store_row32(o.ptr, o.row_off + col + 32, hi, ncols - 32, false);
       }
     };
+    // the same with fp16 values
+    auto emit64_f16 = [&](const OutRef& o, const float (&v)[64], int col, int ncols, bool full, bool row_ok) {
+      if (ncols <= 0) return;  // N is a multiple of 64
+      uint4 w[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        w[q] = make_uint4(pack_f16x2(v[8 * q], v[8 * q + 1]), pack_f16x2(v[8 * q + 2], v[8 * q + 3]),
+                          pack_f16x2(v[8 * q + 4], v[8 * q + 5]), pack_f16x2(v[8 * q + 6], v[8 * q + 7]));
+      if (full) {
+        uint8_t* stg = next_stage_buf();
+#pragma unroll
+        for (int q = 0; q < 8; ++q) *reinterpret_cast<uint4*>(stg + lane * 128 + ((q ^ (lane & 7)) << 4)) = w[q];
+        issue_store(o, stg, col);
+      } else if (row_ok) {
+        uint4* to = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(o.ptr) + o.row_off + col);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) to[q] = w[q];
+      }
+    };
     for (int t = sch.first; t < sch.total; t += sch.stride, ++acc) {
       Tile tl;
       sch.decode(p, t, gcur, tl);
@@ -1587,7 +1611,20 @@ __global__ void __launch_bounds__(WarpPlan<STAGES, EW, AMODE, BMODE, CN, XF>::kT
                 v[32 + i] *= sr * __shfl_sync(0xffffffffu, s1, i);
               }
             }
-            emit64(o, v, col, p.N - col, full, row_ok);
+            if constexpr (kF16s) {
+              // the power of two that takes the largest magnitude to [2^14, 2^15) (infinities and NaN stay what they are)
+              const int be = max(15, static_cast<int>(__float_as_uint(max_abs_nan(v)) >> 23));
+              const float inv = __uint_as_float(static_cast<uint32_t>(268 - be) << 23);
+              if (row_ok && col < p.N)
+                p.o_scale[(s_off[tl.g] + static_cast<long long>(m)) * (p.N / 64) + col / 64] =
+                    __uint_as_float(static_cast<uint32_t>(be - 14) << 23);
+              // staged and stored like bf16: the words are fp16 pairs
+#pragma unroll
+              for (int i = 0; i < 64; ++i) v[i] *= inv;
+              emit64_f16(o, v, col, p.N - col, full, row_ok);
+            } else {
+              emit64(o, v, col, p.N - col, full, row_ok);
+            }
           }
         }
       }

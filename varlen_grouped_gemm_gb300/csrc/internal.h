@@ -171,11 +171,11 @@ cudaError_t launch_transpose_bf16(const __nv_bfloat16* in, int rows, int cols, _
 
 // Per token: dS of its pairs (sum of the per-column-tile partials), the router-logit gradient
 // (fp32, and as bf16 high and low parts dL_bf16[T][E], dL_lo[T][E]), and dX = sum of the pairs' dX
-// rows + dlogits W_r^T.
+// rows + dlogits W_r^T.  With dXp_scale the rows are fp16 times a scale for 64 columns (X_F16S).
 cudaError_t launch_token_backward(const float* part, int part_ld, const int32_t* tok_ptr, const int32_t* tok_pairs,
                                   const int32_t* offsets, int E, const float* sorted_w, const int32_t* topk_ids,
-                                  const float* topk_w, int K, const __nv_bfloat16* dXp, const __nv_bfloat16* WrT,
-                                  int T, int d, long long cap, float* dS, float* dlogits, __nv_bfloat16* dL_bf16,
+                                  const float* topk_w, int K, const __nv_bfloat16* dXp, const float* dXp_scale,
+                                  const __nv_bfloat16* WrT, int T, int d, long long cap, float* dS, float* dlogits, __nv_bfloat16* dL_bf16,
                                   __nv_bfloat16* dL_lo, __nv_bfloat16* dX, int* err, cudaStream_t s);
 
 cudaError_t launch_splitk_reduce(const float* part, int splits, long long n, float* out, cudaStream_t s);
@@ -271,6 +271,7 @@ cudaError_t run_gate_up_swiglu_kept8(int BN, int cn, const GemmParams& p, const 
 cudaError_t run_gate_up_swiglu_e4m3_kept8(int BN, int cn, const GemmParams& p, const Maps& m, int grid, cudaStream_t s);
 cudaError_t run_gate_up_swiglu_mx_kept8(int cn, const GemmParams& p, const Maps& m, int grid, cudaStream_t s);
 cudaError_t run_dact_dswiglu_kept8(int BN, const GemmParams& p, const Maps& m, int grid, cudaStream_t s);
+cudaError_t run_dx_store_f16s(int BN, const GemmParams& p, const Maps& m, int grid, cudaStream_t s);
 cudaError_t run_dact_dswiglu_e4m3_kept8(int BN, const GemmParams& p, const Maps& m, int grid, cudaStream_t s);
 cudaError_t run_dact_dswiglu_mx_kept8(int BN, const GemmParams& p, const Maps& m, int grid, cudaStream_t s);
 // n values (a multiple of 32) in rows of whole blocks; scale [n / 32]

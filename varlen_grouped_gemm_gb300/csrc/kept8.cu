@@ -25,6 +25,12 @@ cudaError_t run_dact_dswiglu_kept8(int BN, const GemmParams& p, const Maps& m, i
   return launch_grouped_gemm<128, 4, 8, 2, A_TMA_K, B_TMA_MN3, VAR_M, EPI_DSWIGLU, false, 1, X_KEPT8>(p, m, grid, s);
 }
 
+// dXp = [dH | dU] [W_gate[e]; W_up[e]] in scaled fp16 for the sum over a token's pairs.
+cudaError_t run_dx_store_f16s(int BN, const GemmParams& p, const Maps& m, int grid, cudaStream_t s) {
+  if (BN == 256) return launch_grouped_gemm<256, 4, 4, 1, A_TMA_K, B_TMA_MN3, VAR_M, EPI_STORE, false, 1, X_F16S>(p, m, grid, s);
+  return launch_grouped_gemm<128, 6, 4, 1, A_TMA_K, B_TMA_MN3, VAR_M, EPI_STORE, false, 1, X_F16S>(p, m, grid, s);
+}
+
 // A matrix of bf16 values to codes and scales.  Four lanes have a block's 32 columns, 8 (16 bytes) each: loads and stores
 // are contiguous over the warp.  Rows are whole blocks, so the matrix is one run of them.
 __global__ void __launch_bounds__(256) keep_rows8_kernel(const __nv_bfloat16* __restrict__ M, long long n8,
@@ -33,15 +39,14 @@ __global__ void __launch_bounds__(256) keep_rows8_kernel(const __nv_bfloat16* __
   for (long long i = blockIdx.x * static_cast<long long>(blockDim.x) + threadIdx.x; i < n8; i += step) {
     const uint4 x = __ldg(reinterpret_cast<const uint4*>(M) + i);
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    float v[8], amax = 0.0f;
+    float v[8];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float2 f = unpack_bf16x2(w[j]);
       v[2 * j] = f.x;
       v[2 * j + 1] = f.y;
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) amax = max_abs_nan(amax, v[j]);
+    float amax = max_abs_nan(v);
     // n8 and the step are multiples of 4: the four lanes of a block are in the loop together
     const unsigned quad = 0xFu << (threadIdx.x & 28);
     amax = max_abs_nan(amax, __shfl_xor_sync(quad, amax, 1));

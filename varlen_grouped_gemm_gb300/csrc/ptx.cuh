@@ -6,6 +6,7 @@
 
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -445,6 +446,16 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+
+__device__ __forceinline__ float2 unpack_f16x2(uint32_t u) {
+  __half2 v = *reinterpret_cast<__half2*>(&u);
+  return __half22float2(v);
+}
+
 __device__ __forceinline__ float2 unpack_bf16x2(uint32_t u) {
   __nv_bfloat162 v = *reinterpret_cast<__nv_bfloat162*>(&u);
   return __bfloat1622float2(v);
@@ -669,6 +680,14 @@ __device__ __forceinline__ float max_abs_nan(float m, float a) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(fabsf(a)));
   return r;
 }
+// The largest magnitude of N values (a NaN if there is one), in four chains: one would wait for itself N times.
+template <int N>
+__device__ __forceinline__ float max_abs_nan(const float (&v)[N]) {
+  float m[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < N; ++i) m[i & 3] = max_abs_nan(m[i & 3], v[i]);
+  return max_abs_nan(max_abs_nan(m[0], m[1]), max_abs_nan(m[2], m[3]));
+}
 // Four codes, little-endian: adding 1.5 * 2^23 leaves the nearest whole number in the low bits.
 __device__ __forceinline__ uint32_t kept8_x4(float a, float b, float c, float d, float inv) {
   constexpr float kM = 12582912.0f;
@@ -678,11 +697,8 @@ __device__ __forceinline__ uint32_t kept8_x4(float a, float b, float c, float d,
 }
 // One block of 32 columns of a row.
 __device__ __forceinline__ void kept8_block32(const float (&v)[32], uint8_t* q, __nv_bfloat16* scale) {
-  float amax = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 32; ++i) amax = max_abs_nan(amax, v[i]);
   float inv;
-  const uint32_t bits = kept8_scale(amax, inv);
+  const uint32_t bits = kept8_scale(max_abs_nan(v), inv);
   *reinterpret_cast<uint16_t*>(scale) = static_cast<uint16_t>(bits);
 #pragma unroll
   for (int j = 0; j < 32; j += 16)
