@@ -929,8 +929,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
           ++items;
           continue;
         }
-        // an item in parts: the block that brings the last of them adds them up in block order, two pairs and four parts at a
-        // time
+        // an item in parts: the block that brings the last of them adds them up in block order, eight loads at a time: four
+        // parts of two pairs, or eight of the only one (short lists are cut into many parts and have few pairs)
         const int b0 = x.owner(item * x.c), parts = x.owner(item * x.c + x.c - 1) - b0 + 1;
         epi_sync();
         if (tid == 0) L.last = atom_acq_rel(&a.ctr[kCtrShared + x.half * kFewMaxBlocks + b0]) == parts - 1;
@@ -940,26 +940,29 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
 #pragma unroll 1
         for (int j0 = 0; j0 < m; j0 += 2) {
           float h[2] = {0.0f, 0.0f}, u[2] = {0.0f, 0.0f};
+          const bool one = m == 1;
 #pragma unroll 1
-          for (int o0 = 0; o0 < parts; o0 += 4) {
-            float y[2][4][2];
+          for (int o0 = 0; o0 < parts; o0 += one ? 8 : 4) {
+            float y[8][2];
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
+            for (int r = 0; r < 8; ++r) {
+              const int j = one ? 0 : j0 + (r >> 2), o = o0 + (one ? r : r & 3);
+              const bool has = j < m && o < parts;
+              const float* at = o == 0 ? a.hu + static_cast<long long>(p0 + j) * ld + tile * kTile + row
+                                       : over + (static_cast<long long>(b0 + o) * a.T + j) * kTile + row;
+              y[r][0] = has ? __ldcg(at) : 0.0f;
+              y[r][1] = has ? __ldcg(at + kRows) : 0.0f;
+            }
 #pragma unroll
-              for (int r = 0; r < 4; ++r) {
-                const bool has = j0 + q < m && o0 + r < parts;
-                const float* at = o0 + r == 0 ? a.hu + static_cast<long long>(p0 + j0 + q) * ld + tile * kTile + row
-                                              : over + (static_cast<long long>(b0 + o0 + r) * a.T + j0 + q) * kTile + row;
-                y[q][r][0] = has ? __ldcg(at) : 0.0f;
-                y[q][r][1] = has ? __ldcg(at + kRows) : 0.0f;
+            for (int r = 0; r < 8; ++r) {
+              if (r < 4 || one) {
+                h[0] += y[r][0];
+                u[0] += y[r][1];
+              } else {
+                h[1] += y[r][0];
+                u[1] += y[r][1];
               }
-#pragma unroll
-            for (int q = 0; q < 2; ++q)
-#pragma unroll
-              for (int r = 0; r < 4; ++r) {
-                h[q] += y[q][r][0];
-                u[q] += y[q][r][1];
-              }
+            }
           }
 #pragma unroll
           for (int q = 0; q < 2; ++q)
