@@ -622,11 +622,16 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
   // the memory system, and everything else behind it: the activations' way through L2 takes several times as long.  Long
   // lists gain by the deeper queue, short ones by the shorter way (two and all six stages: 4 x 2048 x 128 x 512 51.7 and
   // 59.0 us, 64 tokens e4m3 94 and 99, bf16 152 and 144; 24 x 2880 x 128 x 2880 553 and 518; three: 1 x 7168 x 64 x 2048 e4m3
-  // 74.1 and 77.5).  The shortest keep HBM busy for a moment only, the activations' way included: there the queue starts the stream
-  // sooner (layers of a stack, two and three: 1 x 2048 x 128 x 512 25.5 and 24.6 us, 4 x the same 44.9 and 46.2).  The ring is
-  // as deep all the same: it fills while a block waits for the activations.
+  // 74.1 and 77.5).  The shortest of few tokens keep HBM busy for a moment only, their way included: there the queue starts the
+  // stream sooner (layers of a stack, two and four: 1 x 2048 x 128 x 512 25.5 and 24.8 us, 4 x the same 44.9 and 48.0; but 64 x
+  // 2048 x 8 x 512, with many rows to gather, 90 and 102).  The ring is as deep all the same: it fills while a block waits for
+  // the activations.
+  // The number is odd where the ring's is: the stage whose landing a producer waits for is then its own to fill again, and its
+  // barrier cannot go on by a second phase, of the same parity, before the wait has seen the first.
+  static_assert(kProd == 2, "the parity of ahead");
   const int share = plan.A * (plan.t1 * plan.c1 + plan.t2 * plan.c2) / G;
-  const int ahead = share < 20 ? 3 : share < 100 ? 2 : share < 150 ? 3 : a.stages;
+  const int want = share < 20 && a.stages == kMaxStages ? 4 : share < 100 ? 2 : share < 150 ? 3 : a.stages;
+  const int ahead = want + ((a.stages - want) & 1);
   const int ld_hu = plan.t1 * kTile, ld_y = plan.t2 * kTile;
   // a last tile of W_down may have rows in its first half alone
   auto halves = [&](const List& x, int tile) { return x.ph == 1 && a.d - tile * kTile <= kRows ? 1 : 2; };
