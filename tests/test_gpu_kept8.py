@@ -221,6 +221,24 @@ def test_backward_matches_64_bits_at_the_kept_values(vgg, ctx, shape, dw):
     assert not buf.dW_gate[empty].any() and not buf.dW_down[empty].any()
 
 
+@pytest.mark.parametrize("d, n", [(576, 64), (4096, 64), (4096, 192), (4160, 64)])
+def test_logit_gradients_of_long_reductions(vgg, ctx, d, n):
+    """The tensor cores' accumulator drops what an addition shifts out.  One of the sums behind dS takes 32 steps (up to d =
+    4096; 512 of the reduction), so half a unit of 24 bits each, all in one direction, is 32 2^-24 = 1.9e-6; longer reductions
+    have theirs in one accumulator, d / 16 steps.  The parts' sums, the dots and dW_r's product add a few 2^-24."""
+    shape = T, _, E, _, K = 517, d, 8, n, 2
+    s = layer(*shape, seed=3)
+    buf = buffers(vgg, *shape, "bf16", dW_dtype=F32, kept8=True)
+    forward(vgg, ctx, s, "bf16", None, buf)
+    backward(vgg, ctx, s, "bf16", None, buf, None)
+    assert vgg.moe_get_error(ctx) == (vgg.MOE_OK, 0)
+    ref = formula(s, buf, values(buf.xk), values(buf.H), values(buf.U))
+    bound = ((min(d, 512) if d <= 4096 else d) / 16 + 12) * 2.0 ** -24
+    for name in ("dS", "dlogits", "dW_r"):
+        got = buf.dS[:T * K] if name == "dS" else getattr(buf, name)
+        assert rel(got, ref[name]) <= bound, (name, rel(got, ref[name]), bound)
+
+
 @pytest.mark.parametrize("form", ["bf16", "e4m3", "mx"])
 @pytest.mark.parametrize("kw", [dict(), dict(m_tile=64), dict(capacity=40)], ids=["plain", "rounded", "capacity"])
 def test_backward_is_the_fp32_one_at_the_kept_values(vgg, ctx, form, kw):

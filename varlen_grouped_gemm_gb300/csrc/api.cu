@@ -220,10 +220,17 @@ size_t bwd_ws_bytes(int T, int d, int E, int n, long long cap) {
          al(sizeof(float) * static_cast<size_t>(kMaxSplitK) * d * E);
 }
 
-// Behind the backward's workspace, from activations kept in 8 bits: X's values, the scales of the pairs' dX rows.
+size_t router_bwd_ws_bytes(int T, int d, int E) {
+  const size_t Tp = static_cast<size_t>(ceil_div(T, 64)) * 64;
+  return al(sizeof(__nv_bfloat16) * 3 * Tp * E) + al(sizeof(float) * static_cast<size_t>(kMaxRouterSplit) * d * E);
+}
+
+// Behind the backward's workspace, from activations kept in 8 bits: X's values, the scales of the pairs' dX rows, the workspace
+// of dW_r's product.
 struct KeptWs {
   __nv_bfloat16* x;
   float* dxp_scale;
+  void* router;
   size_t bytes;  // of the whole
 };
 KeptWs kept_ws(void* ws, int T, int d, int E, int n, long long cap) {
@@ -237,6 +244,7 @@ KeptWs kept_ws(void* ws, int T, int d, int E, int n, long long cap) {
   KeptWs w{};
   w.x = reinterpret_cast<__nv_bfloat16*>(take(sizeof(__nv_bfloat16) * static_cast<size_t>(T) * d));
   w.dxp_scale = reinterpret_cast<float*>(take(sizeof(float) * cap * (d / 64)));
+  w.router = take(router_bwd_ws_bytes(T, d, E));
   w.bytes = p;
   return w;
 }
@@ -394,6 +402,23 @@ static void set_hu_inputs(GemmParams& p, const void* H, const void* U, const Kep
     p.k_h = static_cast<__nv_bfloat16*>(k->hs);
     p.k_u = static_cast<__nv_bfloat16*>(k->us);
   }
+}
+
+// dW_r = in + X^T dlogits with fp32 operands' precision: dlogits split into three bf16 parts (here, or before: after_split the
+// launch ahead is the split), the product over shares of the tokens, their sum.
+static int router_dw(moe_ctx* ctx, const void* X, const float* dlogits, int T, int d, int E, bool split_first, bool after_split,
+                     const float* in, float* dW_r, void* ws, cudaStream_t s) {
+  const int Tp = ceil_div(T, 64) * 64;
+  __nv_bfloat16* parts = static_cast<__nv_bfloat16*>(ws);
+  float* sums = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + al(sizeof(__nv_bfloat16) * 3 * static_cast<size_t>(Tp) * E));
+  int splits = 0;
+  if (T > 0 && split_first) VGG_LAUNCH("split_dlogits", launch_split_dlogits(dlogits, T, Tp, E, 3, parts, s));
+  // (rows past T of X are the map's zero fill, of the parts zero)
+  if (T > 0)
+    VGG_LAUNCH("router_dw", launch_router_dw(static_cast<const __nv_bfloat16*>(X), parts, T, Tp, d, E, after_split, ctx->num_sms,
+                                             sums, &splits, ctx->d_err, ctx->timeout_ns, s));
+  VGG_LAUNCH("router_dw_reduce", launch_router_dw_reduce(sums, splits, d, E, in, dW_r, s));
+  return MOE_OK;
 }
 
 // Down projection of the sorted activation rows A, each row scaled by its combine weight (Yw).  With A_lo
@@ -1126,7 +1151,10 @@ static int backward_impl(moe_ctx* ctx, const void* dO, const void* X, const void
   const bool fine = kept && !Wgu_q && !Wdt_q && !mx;
   float* const dxp_scale = fine ? kept_ws(ws, T, d, E, n, cap).dxp_scale : nullptr;
   const bool f32 = dW_fp32 != 0;
-  const int bn6 = dact_bn(n, cap, E, ctx->num_sms);
+  // Kept activations: dA' to fp32's precision (tiles of 128 columns, whose epilogue adds up short accumulations) up to d = 4096.
+  // Longer reductions are bound by the tensor cores, which 128 columns keep busy two thirds of the time: 8192 x 7168 x 256 x 2048
+  // 3.01 and 2.14 ms, but 16384 x 2048 x 64 x 1024 0.82 and 0.85, 32768 x 1536 x 512 x 256 0.53 and 0.45.
+  const int bn6 = fine && d <= 4096 ? 128 : dact_bn(n, cap, E, ctx->num_sms);
   // one dS partial per (column tile, epilogue column half); the block-scaled form tiles n by mx_tile_cols(n)
   const int part_ld = (mx ? ceil_div(n, mx_tile_cols(n)) : ceil_div(n, bn6)) * 2;
   if (cap > static_cast<long long>(T) * K) {
@@ -1376,7 +1404,7 @@ static int backward_impl(moe_ctx* ctx, const void* dO, const void* X, const void
   VGG_LAUNCH("wr_transpose", launch_transpose_bf16(static_cast<const __nv_bfloat16*>(W_r), d, E, w.WrT, s));
   const int Tp = ceil_div(T, 64) * 64;
   __nv_bfloat16* dL_lo = w.dL + static_cast<size_t>(Tp) * E;
-  if (Tp > T) {  // zero rows past the last token in both halves
+  if (Tp > T && !fine) {  // zero rows past the last token in both halves
     if (cudaMemsetAsync(w.dL + static_cast<size_t>(T) * E, 0, sizeof(__nv_bfloat16) * (Tp - T) * E, s) != cudaSuccess ||
         cudaMemsetAsync(dL_lo + static_cast<size_t>(T) * E, 0, sizeof(__nv_bfloat16) * (Tp - T) * E, s) != cudaSuccess)
       return MOE_ERR_CUDA;
@@ -1388,7 +1416,11 @@ static int backward_impl(moe_ctx* ctx, const void* dO, const void* X, const void
   // lo = bf16(dlogits - hi), about 16 significant bits: a single bf16 rounding of dlogits costs up to a few
   // percent on the columns of heavily loaded experts, whose gradient sums thousands of tokens' rounding
   // errors.  One launch reduces over 2 Tp rows: [hi; lo] against X read twice (rows k >= Tp wrap to k - Tp).
-  {
+  // From kept activations dW_r has fp32 operands' precision, as its dlogits have.
+  if (fine) {
+    const int rc = router_dw(ctx, X, dlogits, T, d, E, true, true, nullptr, dW_r, kept_ws(ws, T, d, E, n, cap).router, s);
+    if (rc != MOE_OK) return rc;
+  } else {
     GemmParams p = base_params(ctx);
     p.M = d;
     p.N = E;
@@ -1872,8 +1904,7 @@ static bool router_bwd_sizes_ok(int T, int d, int E) {
 
 size_t moe_router_backward_workspace_bytes(int T, int d, int E) {
   if (!router_bwd_sizes_ok(T, d, E)) return 0;
-  const size_t Tp = static_cast<size_t>(ceil_div(T, 64)) * 64;
-  return al(sizeof(__nv_bfloat16) * 3 * Tp * E) + al(sizeof(float) * static_cast<size_t>(kMaxRouterSplit) * d * E);
+  return router_bwd_ws_bytes(T, d, E);
 }
 
 int moe_router_backward(moe_ctx* ctx, const float* dlogits, const void* X, const void* W_r, int T, int d, int E,
@@ -1891,7 +1922,6 @@ int moe_router_backward(moe_ctx* ctx, const float* dlogits, const void* X, const
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int Tp = ceil_div(T, 64) * 64;
   __nv_bfloat16* parts = static_cast<__nv_bfloat16*>(ws);
-  float* sums = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + al(sizeof(__nv_bfloat16) * 3 * static_cast<size_t>(Tp) * E));
   // dX reads two parts, dW_r three
   if (T > 0) VGG_LAUNCH("split_dlogits", launch_split_dlogits(dlogits, T, Tp, E, dW_r ? 3 : 2, parts, s));
   if (T > 0 && dX) {
@@ -1921,14 +1951,7 @@ int moe_router_backward(moe_ctx* ctx, const float* dlogits, const void* X, const
     const int grid = pair ? ctx->num_sms / 2 * 2 : std::min(ceil_div(T, BM) * ceil_div(d, BN), ctx->num_sms);
     VGG_LAUNCH("router_dx", run_dense_add(BN, pair, p, m, grid, s));
   }
-  if (dW_r) {
-    // dW_r = dW_r_in + X^T dlogits, split over tokens (rows past T of X are the map's zero fill, of the parts zero)
-    int splits = 0;
-    if (T > 0)
-      VGG_LAUNCH("router_dw", launch_router_dw(static_cast<const __nv_bfloat16*>(X), parts, T, Tp, d, E, dX == nullptr,
-                                               ctx->num_sms, sums, &splits, ctx->d_err, ctx->timeout_ns, s));
-    VGG_LAUNCH("router_dw_reduce", launch_router_dw_reduce(sums, splits, d, E, dW_r_in, dW_r, s));
-  }
+  if (dW_r) return router_dw(ctx, X, dlogits, T, d, E, false, dX == nullptr, dW_r_in, dW_r, ws, s);
   return MOE_OK;
 }
 

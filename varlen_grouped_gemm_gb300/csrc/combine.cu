@@ -204,8 +204,10 @@ __global__ void __launch_bounds__(256) token_backward_kernel(
     if (e < E) {
       dlogits[rowE + e] = v;
       const __nv_bfloat16 hi = __float2bfloat16_rn(v);
-      dL_bf16[rowE + e] = hi;
-      dL_lo[rowE + e] = __float2bfloat16_rn(v - __bfloat162float(hi));
+      if (!F16S) {  // (scaled rows: dW_r's product takes dlogits itself)
+        dL_bf16[rowE + e] = hi;
+        dL_lo[rowE + e] = __float2bfloat16_rn(v - __bfloat162float(hi));
+      }
     }
     const unsigned m = __ballot_sync(0xffffffffu, v != 0.0f);
     if (v != 0.0f) {

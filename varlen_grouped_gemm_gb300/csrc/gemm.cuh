@@ -461,6 +461,15 @@ __global__ void __launch_bounds__(WarpPlan<STAGES, EW, AMODE, BMODE, CN, XF>::kT
   constexpr bool kMx = (XF & X_MX) != 0;
   constexpr bool kKept8 = (XF & X_KEPT8) != 0;
   constexpr bool kF16s = (XF & X_F16S) != 0;
+  // The tensor cores' accumulator drops the bits that an addition shifts out, always towards zero: with all of d = 2048 in one
+  // accumulator dA', and with it dS, came out 1.8e-6 too small.  From kept activations it takes kChain stages (512 of the
+  // reduction) only; the epilogue adds it, rounded to nearest, to sums in registers while the next ones run (dS 2.1e-6 -> 5.0e-7
+  // normwise, an fp32 product's 4e-7).  Four accumulators let the products run up to a tile ahead of a tile's
+  // epilogue (4096 x 2048 x 128 x 512: 156 us, with two 180; 155 without the sums).  256 columns would need 128
+  // sums a thread.  0: an accumulator takes the whole reduction.
+  constexpr int kChain = kKept8 && EPI == EPI_DSWIGLU && !kMx && BN == 128 ? 8 : 0;
+  constexpr int kAccs = kChain ? 4 : 2, kAccBit = kChain ? 2 : 1;  // accumulators in turn
+  static_assert(!kChain || (EW == 8 && !kPair), "sums of 64 columns a thread");
   static_assert(!kF16s || (EPI == EPI_STORE && VAR == VAR_M && !OUTF32 && XF == X_F16S), "scaled fp16: the plain varlen-M epilogue");
   static_assert(!kKept8 || EPI == EPI_SWIGLU || EPI == EPI_SWIGLU_Q || EPI == EPI_DSWIGLU || EPI == EPI_DSWIGLU_Q,
                 "activations kept in 8 bits: the SwiGLU epilogues and their gradient's");
@@ -526,7 +535,7 @@ __global__ void __launch_bounds__(WarpPlan<STAGES, EW, AMODE, BMODE, CN, XF>::kT
       kPair ? 2 * (L::kABytes + L::kBBytes)
             : (kAGather ? (CN - 1) * kSliceBytes : L::kABytes) + (kBGather ? 0 : L::kBBytes) +
                   (kMx ? 512 * mx_b_blocks(BN) + 512 : 0);
-  constexpr uint32_t kTmemCols = kMx ? 512 : (2 * BN <= 128) ? 128 : (2 * BN <= 256 ? 256 : 512);
+  constexpr uint32_t kTmemCols = kMx ? 512 : (kAccs * BN <= 128) ? 128 : (kAccs * BN <= 256 ? 256 : 512);
   constexpr int kSfCols = 4 + 4 * mx_b_blocks(BN);  // TMEM columns of one stage's scales (A: 4, B: 4 per block)
   constexpr uint32_t kIdesc =
       kF8 ? idesc_e4m3(BM, BN, kAMn ? 1 : 0, kBMn ? 1 : 0) : idesc_bf16(kPair ? 2 * BM : BM, BN, kAMn ? 1 : 0, kBMn ? 1 : 0);
@@ -537,9 +546,10 @@ __global__ void __launch_bounds__(WarpPlan<STAGES, EW, AMODE, BMODE, CN, XF>::kT
   uint64_t* full_bar = bars;
   uint64_t* empty_bar = bars + STAGES;
   uint64_t* tfull_bar = bars + 2 * STAGES;
-  uint64_t* tempty_bar = bars + 2 * STAGES + 2;
-  uint64_t* drain_bar = bars + 2 * STAGES + 4;
-  uint64_t* gath_bar = bars + 2 * STAGES + 5;  // [STAGES] own A slice gathered (relay mode)
+  uint64_t* tempty_bar = bars + 2 * STAGES + kAccs;
+  uint64_t* drain_bar = bars + 2 * STAGES + 2 * kAccs;
+  uint64_t* gath_bar = bars + 2 * STAGES + 2 * kAccs + 1;  // [STAGES] own A slice gathered (relay mode)
+  static_assert(2 * STAGES + 2 * kAccs + 1 + (kRelay ? STAGES : 0) <= L::kNumBars, "barriers");
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + L::kMiscOffset);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + L::kMiscOffset + 4);
   int* s_bad = reinterpret_cast<int*>(smem + L::kMiscOffset + 8);
@@ -565,7 +575,7 @@ __global__ void __launch_bounds__(WarpPlan<STAGES, EW, AMODE, BMODE, CN, XF>::kT
     }
     if constexpr (EPI == EPI_ADD)
       for (int b = 0; b < EW * kAddBufs; ++b) mbar_init(&add_bar[b], 1);
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < kAccs; ++b) {
       mbar_init(&tfull_bar[b], 1);
       mbar_init(&tempty_bar[b], (kPair ? 2 : 1) * EW * 32);  // a pair: both CTAs' epilogues drain the tile
     }
@@ -1000,14 +1010,18 @@ __global__ void __launch_bounds__(WarpPlan<STAGES, EW, AMODE, BMODE, CN, XF>::kT
           Tile tl;
           sch.decode(p, t, gcur, tl);
           const int nk = (tl.k_len + BK - 1) / BK;
-          const int buf = acc & 1;
+          for (int k0 = 0;; k0 += kChain, ++acc) {
+          const int k1 = kChain ? min(nk, k0 + kChain) : nk;
+          const int buf = acc & (kAccs - 1);
           // a pair: the odd CTA's epilogue released the accumulator with cluster-scope arrivals
-          if (!(kPair ? mbar_wait_cluster(&tempty_bar[buf], ((acc >> 1) & 1) ^ 1, s_abort, p.timeout_ns, p.err)
-                      : mbar_wait(&tempty_bar[buf], ((acc >> 1) & 1) ^ 1, s_abort, p.timeout_ns, p.err)))
+          if (!(kPair ? mbar_wait_cluster(&tempty_bar[buf], ((acc >> kAccBit) & 1) ^ 1, s_abort, p.timeout_ns, p.err)
+                      : mbar_wait(&tempty_bar[buf], ((acc >> kAccBit) & 1) ^ 1, s_abort, p.timeout_ns, p.err))) {
+            aborted = true;
             break;
+          }
           tc_fence_after();
           const uint32_t d_tmem = tmem_base + buf * BN;
-          for (int ks = 0; ks < nk; ++ks, ++it) {
+          for (int ks = k0; ks < k1; ++ks, ++it) {
             const int s = it % STAGES;
             const uint32_t ph = (it / STAGES) & 1;
             if (!mbar_wait(&full_bar[s], ph, s_abort, p.timeout_ns, p.err)) {
@@ -1039,12 +1053,12 @@ __global__ void __launch_bounds__(WarpPlan<STAGES, EW, AMODE, BMODE, CN, XF>::kT
               const uint64_t adl = kAMn ? sdesc_sw128(sa + L::kA1Bytes + kk * 2048, BK * 128, 1024)
                                         : sdesc_sw128(sa + L::kA1Bytes + kk * 32, 16, 1024);
               if (kMx) {  // K step kk = 32-code block kk of the stage: byte kk of every scale word
-                umma_mx(d_tmem, ad, bd, idesc_mx(BM, BN, 0, 0, kk, kk), sf_t, sf_t + 4, (ks | kk) != 0 ? 1u : 0u);
+                umma_mx(d_tmem, ad, bd, idesc_mx(BM, BN, 0, 0, kk, kk), sf_t, sf_t + 4, (ks != k0 || kk != 0) ? 1u : 0u);
               } else if (kPair) {  // same offsets in both CTAs: each holds its rows of A and its columns of B
-                umma_bf16_pair(d_tmem, ad, bd, kIdesc, (ks | kk) != 0 ? 1u : 0u);
+                umma_bf16_pair(d_tmem, ad, bd, kIdesc, (ks != k0 || kk != 0) ? 1u : 0u);
                 if (kDual) umma_bf16_pair(d_tmem, adl, bd, kIdesc, 1u);
               } else {
-                umma_step<kF8>(d_tmem, ad, bd, kIdesc, (ks | kk) != 0 ? 1u : 0u);
+                umma_step<kF8>(d_tmem, ad, bd, kIdesc, (ks != k0 || kk != 0) ? 1u : 0u);
                 if (kDual) umma_step<kF8>(d_tmem, adl, bd, kIdesc, 1u);
               }
             }
@@ -1055,6 +1069,9 @@ __global__ void __launch_bounds__(WarpPlan<STAGES, EW, AMODE, BMODE, CN, XF>::kT
           if (aborted) break;
           if (kPair) umma_commit_pair_mc(&tfull_bar[buf], 3);  // both CTAs' halves of the accumulator are ready
           else umma_commit(&tfull_bar[buf]);
+          if (k1 == nk) break;
+          }
+          if (aborted) break;
         }
         if (*s_abort) {
           if (kPair) umma_commit_pair_mc(drain_bar, 1);
@@ -1267,8 +1284,8 @@ __global__ void __launch_bounds__(WarpPlan<STAGES, EW, AMODE, BMODE, CN, XF>::kT
     for (int t = sch.first; t < sch.total; t += sch.stride, ++acc) {
       Tile tl;
       sch.decode(p, t, gcur, tl);
-      const int buf = acc & 1;
-      if (!mbar_wait(&tfull_bar[buf], (acc >> 1) & 1, s_abort, p.timeout_ns, p.err)) break;
+      const int buf = acc & (kAccs - 1);
+      if (!mbar_wait(&tfull_bar[buf], (acc >> kAccBit) & 1, s_abort, p.timeout_ns, p.err)) break;
       tc_fence_after();
       const uint32_t tbase = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + buf * BN;
       const bool row_ok = row_local < tl.rows;
@@ -1391,11 +1408,45 @@ __global__ void __launch_bounds__(WarpPlan<STAGES, EW, AMODE, BMODE, CN, XF>::kT
           const float w = row_ok ? __ldg(p.row_scale + orow) : 0.0f;
           const float sq = (EPI == EPI_DSWIGLU_Q && row_ok) ? __ldg(p.q_row + orow) : 1.0f;  // e4m3: A row scale
           float ds = 0.0f;
+          float sum[kChain ? kCols : 1];
+          if constexpr (kChain > 0) {
+#pragma unroll
+            for (int i = 0; i < kCols; ++i) sum[i] = 0.0f;
+            bool there = true;
+#pragma unroll 1
+            for (int k0 = 0;; k0 += kChain) {
+              const uint32_t tb = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + (acc & (kAccs - 1)) * BN + c_lo;
+#pragma unroll
+              for (int c = 0; c < kCols; c += 32) {
+                uint32_t r[32];
+                tmem_ld32(tb + c, r);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) sum[c + i] += __uint_as_float(r[i]);
+              }
+              tc_fence_before();
+              mbar_arrive(&tempty_bar[acc & (kAccs - 1)]);
+              if (k0 + kChain >= (tl.k_len + BK - 1) / BK) break;
+              ++acc;
+              there = mbar_wait(&tfull_bar[acc & (kAccs - 1)], (acc >> kAccBit) & 1, s_abort, p.timeout_ns, p.err);
+              if (!there) break;
+              tc_fence_after();
+            }
+            if (!there) break;
+          }
 #pragma unroll 1
           for (int c = c_lo; c < c_lo + kCols; c += 32) {
             uint32_t r[32];
-            tmem_ld32(tbase + c, r);
-            tmem_ld_wait();
+            if constexpr (kChain > 0) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                r[i] = __float_as_uint(sum[i]);
+                sum[i] = sum[32 + i];  // (two turns)
+              }
+            } else {
+              tmem_ld32(tbase + c, r);
+              tmem_ld_wait();
+            }
             const int col = tl.n0 + c;
             const int ncols = p.N - col;
             if (ncols <= 0) continue;
@@ -1628,6 +1679,7 @@ __global__ void __launch_bounds__(WarpPlan<STAGES, EW, AMODE, BMODE, CN, XF>::kT
           }
         }
       }
+      if (kChain > 0) continue;  // (released above)
       tc_fence_before();
       if (kPair && cta_rank != 0) mbar_arrive_remote(mapa_shared(smem_u32(&tempty_bar[buf]), 0));
       else mbar_arrive(&tempty_bar[buf]);
