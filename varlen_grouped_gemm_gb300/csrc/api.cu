@@ -404,15 +404,14 @@ static void set_hu_inputs(GemmParams& p, const void* H, const void* U, const Kep
   }
 }
 
-// dW_r = in + X^T dlogits with fp32 operands' precision: dlogits split into three bf16 parts (here, or before: after_split the
-// launch ahead is the split), the product over shares of the tokens, their sum.
-static int router_dw(moe_ctx* ctx, const void* X, const float* dlogits, int T, int d, int E, bool split_first, bool after_split,
-                     const float* in, float* dW_r, void* ws, cudaStream_t s) {
+// dW_r = in + X^T dlogits with fp32 operands' precision, from dlogits' three bf16 parts at ws (after_split: the launch ahead
+// writes them): the product over shares of the tokens, and their sum.
+static int router_dw(moe_ctx* ctx, const void* X, int T, int d, int E, bool after_split, const float* in, float* dW_r, void* ws,
+                     cudaStream_t s) {
   const int Tp = ceil_div(T, 64) * 64;
   __nv_bfloat16* parts = static_cast<__nv_bfloat16*>(ws);
   float* sums = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + al(sizeof(__nv_bfloat16) * 3 * static_cast<size_t>(Tp) * E));
   int splits = 0;
-  if (T > 0 && split_first) VGG_LAUNCH("split_dlogits", launch_split_dlogits(dlogits, T, Tp, E, 3, parts, s));
   // (rows past T of X are the map's zero fill, of the parts zero)
   if (T > 0)
     VGG_LAUNCH("router_dw", launch_router_dw(static_cast<const __nv_bfloat16*>(X), parts, T, Tp, d, E, after_split, ctx->num_sms,
@@ -1403,22 +1402,22 @@ static int backward_impl(moe_ctx* ctx, const void* dO, const void* X, const void
   // per token: dS, router-logit gradient, dX
   VGG_LAUNCH("wr_transpose", launch_transpose_bf16(static_cast<const __nv_bfloat16*>(W_r), d, E, w.WrT, s));
   const int Tp = ceil_div(T, 64) * 64;
-  __nv_bfloat16* dL_lo = w.dL + static_cast<size_t>(Tp) * E;
-  if (Tp > T && !fine) {  // zero rows past the last token in both halves
-    if (cudaMemsetAsync(w.dL + static_cast<size_t>(T) * E, 0, sizeof(__nv_bfloat16) * (Tp - T) * E, s) != cudaSuccess ||
-        cudaMemsetAsync(dL_lo + static_cast<size_t>(T) * E, 0, sizeof(__nv_bfloat16) * (Tp - T) * E, s) != cudaSuccess)
-      return MOE_ERR_CUDA;
-  }
+  // dlogits' parts [2 or 3][Tp][E], with zero rows past the last token
+  const int parts = fine ? 3 : 2;
+  __nv_bfloat16* const dL = fine ? static_cast<__nv_bfloat16*>(kept_ws(ws, T, d, E, n, cap).router) : w.dL;
+  __nv_bfloat16* const dL_lo = dL + static_cast<size_t>(Tp) * E;
+  for (int i = 0; Tp > T && i < parts; ++i)
+    VGG_CUDA(cudaMemsetAsync(dL + (static_cast<size_t>(i) * Tp + T) * E, 0, sizeof(__nv_bfloat16) * (Tp - T) * E, s));
   VGG_LAUNCH("token_backward", launch_token_backward(w.part, part_ld, tok_ptr, tok_pairs, offsets, E, sorted_w,
                                                      topk_ids, topk_w, K, w.dXp, dxp_scale, w.WrT, T, d, cap, dS, dlogits,
-                                                     w.dL, dL_lo, static_cast<__nv_bfloat16*>(dX), ctx->d_err, s));
+                                                     dL, dL_lo, static_cast<__nv_bfloat16*>(dX), ctx->d_err, s));
   // dW_r = X^T dlogits, split over tokens.  dlogits enters as X^T hi + X^T lo with hi = bf16(dlogits) and
   // lo = bf16(dlogits - hi), about 16 significant bits: a single bf16 rounding of dlogits costs up to a few
   // percent on the columns of heavily loaded experts, whose gradient sums thousands of tokens' rounding
   // errors.  One launch reduces over 2 Tp rows: [hi; lo] against X read twice (rows k >= Tp wrap to k - Tp).
   // From kept activations dW_r has fp32 operands' precision, as its dlogits have.
   if (fine) {
-    const int rc = router_dw(ctx, X, dlogits, T, d, E, true, true, nullptr, dW_r, kept_ws(ws, T, d, E, n, cap).router, s);
+    const int rc = router_dw(ctx, X, T, d, E, true, nullptr, dW_r, dL, s);
     if (rc != MOE_OK) return rc;
   } else {
     GemmParams p = base_params(ctx);
@@ -1435,7 +1434,7 @@ static int backward_impl(moe_ctx* ctx, const void* dO, const void* X, const void
     p.ld_out = E;
     p.out0 = w.wr_part;
     Maps m = zero_maps();
-    if (!make_map_2d(&m.a0, X, d, T, d, 64) || !make_map_2d(&m.b0, w.dL, E, 2 * static_cast<uint64_t>(Tp), E, 64) ||
+    if (!make_map_2d(&m.a0, X, d, T, d, 64) || !make_map_2d(&m.b0, dL, E, 2 * static_cast<uint64_t>(Tp), E, 64) ||
         !make_store_map_3d(&m.o0, w.wr_part, true, E, d, split, 32))
       return MOE_ERR_CUDA;
     m.a1 = m.a0;
@@ -1951,7 +1950,7 @@ int moe_router_backward(moe_ctx* ctx, const float* dlogits, const void* X, const
     const int grid = pair ? ctx->num_sms / 2 * 2 : std::min(ceil_div(T, BM) * ceil_div(d, BN), ctx->num_sms);
     VGG_LAUNCH("router_dx", run_dense_add(BN, pair, p, m, grid, s));
   }
-  if (dW_r) return router_dw(ctx, X, dlogits, T, d, E, false, dX == nullptr, dW_r_in, dW_r, ws, s);
+  if (dW_r) return router_dw(ctx, X, T, d, E, dX == nullptr, dW_r_in, dW_r, ws, s);
   return MOE_OK;
 }
 

@@ -203,8 +203,14 @@ __global__ void __launch_bounds__(256) token_backward_kernel(
     const float v = e < E ? s_dl[e] : 0.0f;
     if (e < E) {
       dlogits[rowE + e] = v;
-      const __nv_bfloat16 hi = __float2bfloat16_rn(v);
-      if (!F16S) {  // (scaled rows: dW_r's product takes dlogits itself)
+      if (F16S) {  // three parts, for a dW_r of fp32 operands' precision
+        float part[3];
+        split3(v, part);
+        dL_bf16[rowE + e] = __float2bfloat16_rn(part[0]);
+        dL_lo[rowE + e] = __float2bfloat16_rn(part[1]);
+        dL_lo[(dL_lo - dL_bf16) + rowE + e] = __float2bfloat16_rn(part[2]);
+      } else {
+        const __nv_bfloat16 hi = __float2bfloat16_rn(v);
         dL_bf16[rowE + e] = hi;
         dL_lo[rowE + e] = __float2bfloat16_rn(v - __bfloat162float(hi));
       }

@@ -171,7 +171,8 @@ cudaError_t launch_transpose_bf16(const __nv_bfloat16* in, int rows, int cols, _
 
 // Per token: dS of its pairs (sum of the per-column-tile partials), the router-logit gradient
 // (fp32, and as bf16 high and low parts dL_bf16[T][E], dL_lo[T][E]), and dX = sum of the pairs' dX
-// rows + dlogits W_r^T.  With dXp_scale the rows are fp16 times a scale for 64 columns (X_F16S).
+// rows + dlogits W_r^T.  With dXp_scale the rows are fp16 times a scale for 64 columns (X_F16S), and dlogits comes in three
+// parts, the third as far behind dL_lo as that behind dL_bf16.
 cudaError_t launch_token_backward(const float* part, int part_ld, const int32_t* tok_ptr, const int32_t* tok_pairs,
                                   const int32_t* offsets, int E, const float* sorted_w, const int32_t* topk_ids,
                                   const float* topk_w, int K, const __nv_bfloat16* dXp, const float* dXp_scale,

@@ -735,4 +735,16 @@ __device__ __forceinline__ void kept8_load32(const uint8_t* q, const __nv_bfloat
   }
 }
 
+// The high part of a value that bf16's range does not hold: its largest number; of an infinite one, itself.
+__device__ __forceinline__ float far_high(float x) { return isinf(x) ? x : copysignf(0x1.fep127f, x); }
+__device__ __forceinline__ bool is_far(float x) { return fabsf(x) >= 0x1.ffp127f; }
+
+// x as three bf16 values, highest first (see split_dlogits).
+__device__ __forceinline__ void split3(float x, float (&part)[3]) {
+  part[0] = is_far(x) ? far_high(x) : bf16_round(x);
+  const float r = isinf(part[0]) ? 0.0f : x - part[0];
+  part[1] = bf16_round(r);
+  part[2] = bf16_round(r - part[1]);
+}
+
 }  // namespace vgg

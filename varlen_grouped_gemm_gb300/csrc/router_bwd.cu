@@ -12,8 +12,6 @@ namespace {
 // leave 2^-17 of a value, 2.4e-6 normwise, ten times the error of an fp32 product's sums).  parts: [PARTS][np].
 // A value that rounds to infinity has bf16's largest number as its high part, an infinite one no other parts (infinity
 // less itself would make NaN of every product).
-__device__ __forceinline__ float far_high(float x) { return isinf(x) ? x : copysignf(0x1.fep127f, x); }
-__device__ __forceinline__ bool is_far(float x) { return fabsf(x) >= 0x1.ffp127f; }
 template <int PARTS>
 __global__ void __launch_bounds__(256) split_dlogits_kernel(const float* __restrict__ dl, long long n, long long np,
                                                             __nv_bfloat16* __restrict__ parts) {
