@@ -647,7 +647,9 @@ int moe_grouped_gemm_fwd_mx_kept8(moe_ctx* ctx, const void* Xq, const void* x_sf
 /*
  * moe_backward_kept8, _e4m3_kept8, _mx_kept8 — the backwards of those names from H and U kept in 8 bits, read in the dSwiGLU
  * epilogue, and from X in bf16 or, with X == NULL, as codes Xq [T,d] and scales x_scale [T,d/32] (moe_keep_rows8).  The
- * gradients are those of the layer at the kept values.  ws: at least moe_kept8_workspace_bytes(T, d, E, n, cap) bytes (0 on
+ * gradients are those of the layer at the kept values; in the bf16 form dX's rows of a pair are summed from fp16 values with a
+ * scale for 64 columns, dW_r takes dlogits as three bf16 parts, and dS (with dlogits) up to d = 4096 has sums of 512 terms of the
+ * tensor cores added up in fp32.  ws: at least moe_kept8_workspace_bytes(T, d, E, n, cap) bytes (0 on
  * bad sizes; cap: the pair arrays' length).  Everything else as without; CTA pairs (moe_set_cta_pairs) do not apply to the
  * dSwiGLU product here.
  */
@@ -694,6 +696,7 @@ int moe_backward_mx_kept8(moe_ctx* ctx, const void* dO, const void* X, const voi
  * weights, bias (or NULL) and shape rules as moe_route and moe_grouped_gemm_fwd; topk_ids [T,K] int32, topk_w [T,K] fp32.
  * 0 <= T <= 64 (T = 0 does nothing).  X, W_r and the weights 16-byte aligned, O 8-byte.  ws: caller-owned, 256-byte
  * aligned, at least moe_few_workspace_bytes(T, d, E, n, K) bytes (0 on bad sizes); calls that may overlap need one each.
+ * MOE_ERR_UNSUPPORTED: min(E, T K) n d past about 2 10^11, where the count of the work leaves 32 bits.
  * The second launch is cooperative (all of its blocks resident at once; their waits for one another are bounded by
  * moe_set_wait_timeout, one that gives up records MOE_DEV_TIMEOUT and leaves O undefined).  Sums run in a fixed order:
  * the same call gives the same bits on the same GPU.

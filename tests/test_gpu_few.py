@@ -296,3 +296,24 @@ def test_beside_the_layer_s_own_path(vgg, ctx):
     assert torch.equal(ids, buf.topk_ids)
     # bf16 roundings: O twice, the pairs' outputs once
     assert ((O.float() - buf.O.float()).norm() / O.float().norm()).item() <= 1.25 * 3 ** 0.5 * 1.6e-3
+
+
+@pytest.mark.parametrize("form", ["bf16", "e4m3"])
+def test_buffers_with_room_for_more_tokens(vgg, ctx, form):
+    """One set of buffers for batches of any size up to theirs: the same bits as in buffers of that size, the rows behind as they were."""
+    s = make(21, 256, 16, 128, 3, seed=13)
+    weights = weights8(vgg, ctx, s) if form == "e4m3" else (s["W_gate"], s["W_up"], s["W_down"])
+    buf = vgg.FewBuffers.allocate(40, 256, 16, 128, 3)
+    for T in (21, 1, 9, 0):
+        for t in (buf.O, buf.topk_ids, buf.topk_w):
+            t.fill_(7)
+        buf.ws.fill_(0xFF)
+        one = vgg.FewBuffers.allocate(T, 256, 16, 128, 3)
+        for b in (buf, one):
+            vgg.forward_few(ctx, s["X"][:T], s["W_r"], None, weights, b)
+        for name in ("O", "topk_ids", "topk_w"):
+            t = getattr(buf, name)
+            assert torch.equal(t[:T], getattr(one, name)) and (t[T:] == 7).all(), (T, name)
+    assert vgg.moe_get_error(ctx) == (vgg.MOE_OK, 0)
+    with pytest.raises(ValueError):
+        vgg.forward_few(ctx, torch.zeros((41, 256), dtype=BF, device="cuda"), s["W_r"], None, weights, buf)

@@ -784,7 +784,7 @@ def moe_forward_few_e4m3(ctx, X, W_r, bias, w8, K, O, topk_ids, topk_w, ws, stre
 
 @dataclass
 class FewBuffers:
-    """Outputs and workspace of the layer for up to 64 tokens (a decoding step of T sequences)."""
+    """Outputs and workspace of the layer for up to T tokens (a decoding step of T sequences), T <= 64."""
 
     O: torch.Tensor         # [T, d] bf16
     topk_ids: torch.Tensor  # [T, K] int32
@@ -799,13 +799,14 @@ class FewBuffers:
 
 
 def forward_few(ctx, X, W_r, bias, weights, buf: FewBuffers, stream=None):
-    """The layer for the few tokens of X; the output is ``buf.O``.  ``weights``: (W_gate, W_up, W_down) in bf16, or
-    E4m3Weights."""
-    K = buf.topk_ids.shape[1]
+    """The layer for the few tokens of X [T, d], at most those that ``buf`` has room for; the output is ``buf.O[:T]``.
+    ``weights``: (W_gate, W_up, W_down) in bf16, or E4m3Weights."""
+    T, K = X.shape[0], buf.topk_ids.shape[1]
+    out = K, buf.O[:T], buf.topk_ids[:T], buf.topk_w[:T], buf.ws, stream
     if isinstance(weights, E4m3Weights):
-        moe_forward_few_e4m3(ctx, X, W_r, bias, weights, K, buf.O, buf.topk_ids, buf.topk_w, buf.ws, stream)
+        moe_forward_few_e4m3(ctx, X, W_r, bias, weights, *out)
     else:
-        moe_forward_few(ctx, X, W_r, bias, *weights, K, buf.O, buf.topk_ids, buf.topk_w, buf.ws, stream)
+        moe_forward_few(ctx, X, W_r, bias, *weights, *out)
 
 
 def moe_test_gemm_varlen_m(ctx, A, idx, B, b_kmajor, offsets, D, stream=None):

@@ -17,6 +17,11 @@
 // A block runs through most of the code once or a few times, and fetches it from memory as it goes: loops are kept short rather
 // than unrolled.
 //
+// Measured, a layer of a captured stack whose weights come from HBM (bf16, e4m3; tokens x d x experts x n): 1 x 2048 x 128 x 512
+// 25 and 22 us, a chain of latencies (its 50 MB take 7.6); 4 tokens 45 and 35; 61 x 1536 x 512 x 256 136 us (5.5 TB/s) and 88;
+// 24 x 2880 x 128 x 2880 with 4 choices 505 us (6.7 TB/s, what a copy reaches) and 284.  The layer's own path, 128 rows of
+// tokens a tile in seven launches, takes 127 us for one token and 371 for the 61.
+//
 // bf16: A = silu(H) U enters the second product as its bf16 value and the bf16 rounding of the rest, as further columns
 // of the same tile (they cost nothing: the products are far below the tensor cores' rate).  e4m3: X quantized per token
 // and A (rounded to bf16) per pair, as moe_quantize_rows_e4m3 does.  Sums are fp32; O is rounded once.
@@ -244,7 +249,8 @@ __device__ __forceinline__ uint4 codes16(const uint4 x, const uint4 y, float s) 
 // ---- first launch: parts of the logits, X's codes, cleared counters -------------------------------------------------
 // Block (x, y), x < strips * splits: 16 experts (32 bytes of every row of W_r, a memory sector) times a share of d, for the
 // tokens NT y .. : part[split][t][e].  Thread: two experts (tid & 7) and four rows of every 128, R times 128 rows at a time.  The blocks behind (y = 0)
-// clear the counters and, for the e4m3 form, quantize a token each.
+// clear the counters and, for the e4m3 form, quantize a token each.  The chunk ahead is loaded while one is multiplied: 4.7 us for
+// a token of 2048 x 128, latencies of two chunks and the launch (0.5 MB).
 template <int NT, int R>
 __global__ void __launch_bounds__(256) few_router_kernel(const __grid_constant__ FewArgs a) {
   __shared__ float red[8][NT][16];
