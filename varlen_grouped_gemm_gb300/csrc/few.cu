@@ -257,6 +257,7 @@ __global__ void __launch_bounds__(256) few_router_kernel(const __grid_constant__
   constexpr int kRtRows = 128 * R;
   __shared__ __align__(16) float s_x[NT][kRtRows];
   __shared__ float s_top[8];
+  griddep_wait();    // a dependent launch too: eager calls in a row 24.6 -> 22.6 us (a token of 2048 x 128 x 512)
   griddep_launch();  // the second launch's start may overlap; it waits for this one's end
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int strips = (a.E + 15) / 16;
@@ -1111,9 +1112,8 @@ int few_splits(int T, int d, int E, int num_sms) {
 cudaError_t launch_few_router(const FewArgs& args, cudaStream_t s) {
   const int strips = (args.E + 15) / 16;
   const dim3 grid(strips * args.splits + (args.xq ? args.T : 1), (args.T + 7) / 8);
-  if (args.T == 1) few_router_kernel<1, 4><<<grid, 256, 0, s>>>(args);
-  else few_router_kernel<8, 1><<<grid, 256, 0, s>>>(args);
-  return cudaGetLastError();
+  if (args.T == 1) return launch_dependent(few_router_kernel<1, 4>, grid, dim3(256), 0, s, args);
+  return launch_dependent(few_router_kernel<8, 1>, grid, dim3(256), 0, s, args);
 }
 
 template <bool F8>
