@@ -50,6 +50,12 @@ constexpr int kMaxPairs = kFewMaxTokens * 8;
 // Tiles' accumulators, where TMEM has room: the second product's items may be as short as a stage, and a pair of accumulators
 // leaves the products waiting for the epilogue's latency.
 constexpr int kMaxAccs = 4;
+// In one list (no halves), the bf16 form of up to so many tokens leaves the parts of H and U as they are, and the gather warps of
+// the second product add them up and make the activations as they fill a stage: an atomic and a round trip through L2 fewer in the
+// chain, for a sum that every row tile of W_down repeats (layers of a stack: 1 x 2048 x 128 x 512 24.9 -> 23.5 us,
+// 3 x 192 x 8 x 64 13.6 -> 12.6, 24 x 320 x 24 x 448 25.1 -> 23.3, 32 x 512 x 8 x 256 24.8 -> 24.5; 64 x 512 x 16 x 128 30.8 ->
+// 32.2).  e4m3 cannot: a code needs the largest magnitude of its whole row.
+constexpr int kDirect = 32;
 constexpr int kMaxStages = 6, kMinStages = 4;  // (the producers take stages in turn, too)
 static_assert(kProd <= kMinStages && kMinStages >= 3, "the ring");
 // Every block finds the choice of so few tokens itself; of more, each is found by one block behind a barrier (a block
@@ -640,6 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
   const int want = share < 20 && a.stages == kMaxStages ? 4 : share < 100 ? 2 : share < 150 ? 3 : a.stages;
   const int ahead = want + ((a.stages - want) & 1);
   const int ld_hu = plan.t1 * kTile, ld_y = plan.t2 * kTile;
+  const bool direct = !F8 && plan.cut == 0 && a.T <= kDirect;
   // a last tile of W_down may have rows in its first half alone
   auto halves = [&](const List& x, int tile) { return x.ph == 1 && a.d - tile * kTile <= kRows ? 1 : 2; };
 
@@ -705,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
         const List first = plan.list(x.half);
         int go = 0;
         if (lane == 0)
-          go = wait_count(&a.ctr[kCtrItems + x.half], first.S / first.c, &L.abort, a.timeout_ns, a.err) ? 1 : 0;
+          go = wait_count(&a.ctr[kCtrItems + x.half], direct ? first.G : first.S / first.c, &L.abort, a.timeout_ns, a.err) ? 1 : 0;
         __syncwarp();
         if (!__shfl_sync(0xffffffffu, go, 0)) {
           stop = true;
@@ -728,6 +735,42 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
             for (int r = rsub; r < m; r += 4)
               cp_async_16(smem_u32(tok) + sw128_offset(r, c16), src + L.ptok[p0 + r] * ld, in ? 16u : 0u);
             cp_async_mbar_arrive_noinc(&L.full[s]);
+          } else if (!F8 && direct) {
+            // lane: two of the stage's columns; their parts of H and U lie where the first product's blocks left them
+            const List made = plan.list(x.half);
+            const int mh = (m + 7) & ~7, c0 = w.k * 64 + 2 * lane, tile = c0 / kRows, s0 = ((w.ai - made.a0) * plan.t1 + tile) * plan.c1;
+            const int b0 = made.owner(s0), parts = made.owner(s0 + plan.c1 - 1) - b0 + 1;
+            const float* main = a.hu + static_cast<long long>(p0) * ld_hu + tile * kTile + c0 % kRows;
+            const float* over = a.ov1 + (static_cast<long long>(x.half) * kFewMaxBlocks + b0) * a.T * kTile + c0 % kRows;
+#pragma unroll 1
+            for (int r = 0; r < m; ++r) {
+              float2 h = make_float2(0.0f, 0.0f), u = h;
+#pragma unroll 1
+              for (int o0 = 0; o0 < parts; o0 += 8) {
+                float2 yh[8], yu[8];
+#pragma unroll
+                for (int o = 0; o < 8; ++o) {
+                  const float* at = o0 + o == 0 ? main + static_cast<long long>(r) * ld_hu
+                                                : over + (static_cast<long long>(o0 + o) * a.T + r) * kTile;
+                  const bool has = o0 + o < parts;
+                  yh[o] = has ? __ldcg(reinterpret_cast<const float2*>(at)) : make_float2(0.0f, 0.0f);
+                  yu[o] = has ? __ldcg(reinterpret_cast<const float2*>(at + kRows)) : make_float2(0.0f, 0.0f);
+                }
+#pragma unroll
+                for (int o = 0; o < 8; ++o) {
+                  h.x += yh[o].x; h.y += yh[o].y;
+                  u.x += yu[o].x; u.y += yu[o].y;
+                }
+              }
+              const float ax = h.x * sigmoidf_(h.x) * u.x, ay = h.y * sigmoidf_(h.y) * u.y;
+              const uint32_t hi = pack_bf16x2(ax, ay);
+              const float2 back = unpack_bf16x2(hi);
+              uint8_t* to = tok + 4 * (lane & 3);
+              *reinterpret_cast<uint32_t*>(to + sw128_offset(r, lane >> 2)) = hi;
+              *reinterpret_cast<uint32_t*>(to + sw128_offset(mh + r, lane >> 2)) = pack_bf16x2(ax - back.x, ay - back.y);
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(&L.full[s]);
           } else if (!F8) {
             const int mh = (m + 7) & ~7;
             const uint8_t* hi = reinterpret_cast<const uint8_t*>(a.A + static_cast<long long>(p0) * a.n) + off;
@@ -896,7 +939,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
           break;
         }
         tc_fence_after();
-        if (x.ph == 0 && whole) {
+        if (x.ph == 0 && whole && !direct) {
 #pragma unroll 1
           for (int j = 0; j < m; ++j) {
             float h, u;
@@ -938,7 +981,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
         }
         tc_fence_before();
         mbar_arrive(&L.tempty[slot]);
-        if (x.ph == 1) continue;
+        if (x.ph == 1 || direct) continue;
         if (whole) {
           ++items;
           continue;
@@ -988,7 +1031,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
       }
       if (stop || x.ph == 1) continue;
       epi_sync();
-      if (tid == 0 && items > 0) red_release(&a.ctr[kCtrItems + x.half], items);
+      if (tid == 0 && (direct || items > 0)) red_release(&a.ctr[kCtrItems + x.half], direct ? 1 : items);
     }
     if (!stop) {
       epi_sync();
