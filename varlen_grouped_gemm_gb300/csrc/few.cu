@@ -18,7 +18,7 @@
 // than unrolled.
 //
 // Measured, a layer of a captured stack whose weights come from HBM (bf16, e4m3; tokens x d x experts x n): 1 x 2048 x 128 x 512
-// 25 and 22 us, a chain of latencies (its 50 MB take 7.6); 4 tokens 45 and 35; 61 x 1536 x 512 x 256 136 us (5.5 TB/s) and 88;
+// 23.4 and 22 us, a chain of latencies (its 50 MB take 7.6); 4 tokens 44 and 35; 61 x 1536 x 512 x 256 134 to 136 us (5.5 TB/s) and 88;
 // 24 x 2880 x 128 x 2880 with 4 choices 505 us (6.7 TB/s, what a copy reaches) and 284.  The layer's own path, 128 rows of
 // tokens a tile in seven launches, takes 127 us for one token and 371 for the 61.
 //
@@ -636,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
   // lists gain by the deeper queue, short ones by the shorter way (two and all six stages: 4 x 2048 x 128 x 512 51.7 and
   // 59.0 us, 64 tokens e4m3 94 and 99, bf16 152 and 144; 24 x 2880 x 128 x 2880 553 and 518; three: 1 x 7168 x 64 x 2048 e4m3
   // 74.1 and 77.5).  The shortest of few tokens keep HBM busy for a moment only, their way included: there the queue starts the
-  // stream sooner (layers of a stack, two and four: 1 x 2048 x 128 x 512 25.5 and 24.8 us, 4 x the same 44.9 and 48.0; but 64 x
+  // stream sooner (layers of a stack, two and four: 1 x 2048 x 128 x 512 25.5 and 24.8 us, but 4 x the same 44.9 and 48.0, and 64 x
   // 2048 x 8 x 512, with many rows to gather, 90 and 102).  The ring is as deep all the same: it fills while a block waits for
   // the activations.
   // The number is odd where the ring's is: the stage whose landing a producer waits for is then its own to fill again, and its
