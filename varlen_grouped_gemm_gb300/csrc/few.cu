@@ -50,11 +50,12 @@ constexpr int kMaxPairs = kFewMaxTokens * 8;
 // Tiles' accumulators, where TMEM has room: the second product's items may be as short as a stage, and a pair of accumulators
 // leaves the products waiting for the epilogue's latency.
 constexpr int kMaxAccs = 4;
-// In one list (no halves), the bf16 form of up to so many tokens leaves the parts of H and U as they are, and the gather warps of
-// the second product add them up and make the activations as they fill a stage: an atomic and a round trip through L2 fewer in the
-// chain, for a sum that every row tile of W_down repeats (layers of a stack: 1 x 2048 x 128 x 512 24.9 -> 23.5 us,
-// 3 x 192 x 8 x 64 13.6 -> 12.6, 24 x 320 x 24 x 448 25.1 -> 23.3, 32 x 512 x 8 x 256 24.8 -> 24.5; 64 x 512 x 16 x 128 30.8 ->
-// 32.2).  e4m3 cannot: a code needs the largest magnitude of its whole row.
+// In lists of less than 100 stages a block, the bf16 form of up to so many tokens leaves the parts of H and U as they are, and the
+// gather warps of the second product add them up and make the activations as they fill a stage: an atomic and a round trip through
+// L2 fewer in the chain, for a sum that every row tile of W_down repeats (layers of a stack: 1 x 2048 x 128 x 512 24.9 -> 23.4 us,
+// 4 x the same 44.9 -> 43.2, 3 x 192 x 8 x 64 13.6 -> 12.6, 24 x 320 x 24 x 448 25.1 -> 23.3, 32 x 512 x 8 x 256 24.8 -> 24.5; but 64 x
+// 512 x 16 x 128 30.8 -> 32.2, 32 x 2048 x 128 x 512 123.1 -> 126.1, 8 x 7168 x 64 x 2048 480 -> 485).  e4m3 cannot: a code
+// needs the largest magnitude of its whole row.
 constexpr int kDirect = 32;
 constexpr int kMaxStages = 6, kMinStages = 4;  // (the producers take stages in turn, too)
 static_assert(kProd <= kMinStages && kMinStages >= 3, "the ring");
@@ -646,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
   const int want = share < 20 && a.stages == kMaxStages ? 4 : share < 100 ? 2 : share < 150 ? 3 : a.stages;
   const int ahead = want + ((a.stages - want) & 1);
   const int ld_hu = plan.t1 * kTile, ld_y = plan.t2 * kTile;
-  const bool direct = !F8 && plan.cut == 0 && a.T <= kDirect;
+  const bool direct = !F8 && share < 100 && a.T <= kDirect;
   // a last tile of W_down may have rows in its first half alone
   auto halves = [&](const List& x, int tile) { return x.ph == 1 && a.d - tile * kTile <= kRows ? 1 : 2; };
 
