@@ -1011,65 +1011,65 @@ __global__ void __launch_bounds__(WarpPlan<STAGES, EW, AMODE, BMODE, CN, XF>::kT
           sch.decode(p, t, gcur, tl);
           const int nk = (tl.k_len + BK - 1) / BK;
           for (int k0 = 0;; k0 += kChain, ++acc) {
-          const int k1 = kChain ? min(nk, k0 + kChain) : nk;
-          const int buf = acc & (kAccs - 1);
-          // a pair: the odd CTA's epilogue released the accumulator with cluster-scope arrivals
-          if (!(kPair ? mbar_wait_cluster(&tempty_bar[buf], ((acc >> kAccBit) & 1) ^ 1, s_abort, p.timeout_ns, p.err)
-                      : mbar_wait(&tempty_bar[buf], ((acc >> kAccBit) & 1) ^ 1, s_abort, p.timeout_ns, p.err))) {
-            aborted = true;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t d_tmem = tmem_base + buf * BN;
-          for (int ks = k0; ks < k1; ++ks, ++it) {
-            const int s = it % STAGES;
-            const uint32_t ph = (it / STAGES) & 1;
-            if (!mbar_wait(&full_bar[s], ph, s_abort, p.timeout_ns, p.err)) {
+            const int k1 = kChain ? min(nk, k0 + kChain) : nk;
+            const int buf = acc & (kAccs - 1);
+            // a pair: the odd CTA's epilogue released the accumulator with cluster-scope arrivals
+            if (!(kPair ? mbar_wait_cluster(&tempty_bar[buf], ((acc >> kAccBit) & 1) ^ 1, s_abort, p.timeout_ns, p.err)
+                        : mbar_wait(&tempty_bar[buf], ((acc >> kAccBit) & 1) ^ 1, s_abort, p.timeout_ns, p.err))) {
               aborted = true;
               break;
             }
-            const uint32_t sa = smem_u32(smem + s * L::kStageBytes);
-            const uint32_t sb = sa + L::kABytes;
-            if (kGather) fence_proxy_async_smem();  // cp.async writes -> UMMA operand reads
             tc_fence_after();
-            // block-scaled form: this stage's scale blocks into its own TMEM columns (their previous readers, the
-            // UMMAs of the stage's last use, completed before the stage was refilled); tcgen05.cp and the UMMAs
-            // after it run in issue order
-            const uint32_t sf_t = tmem_base + 2 * BN + s * kSfCols;
-            if (kMx) {
-              const uint32_t sf_s = sb + L::kBBytes;
-              tmem_cp_32x128b_x4(sf_t, sdesc_plain(sf_s, 128, 128));
-#pragma unroll
-              for (int a = 0; a < mx_b_blocks(BN); ++a)
-                tmem_cp_32x128b_x4(sf_t + 4 + 4 * a, sdesc_plain(sf_s + 512 + 512 * a, 128, 128));
-            }
-#pragma unroll
-            for (int kk = 0; kk < BK / 16; ++kk) {
-              const uint64_t ad =
-                  kAMn ? sdesc_sw128(sa + kk * 2048, BK * 128, 1024) : sdesc_sw128(sa + kk * 32, 16, 1024);
-              const uint64_t bd =
-                  kBMn ? sdesc_sw128(sb + kk * 2048, BK * 128, 1024) : sdesc_sw128(sb + kk * 32, 16, 1024);
-              // dual A: the low part of A times the same B, into the same accumulator
-              const uint64_t adl = kAMn ? sdesc_sw128(sa + L::kA1Bytes + kk * 2048, BK * 128, 1024)
-                                        : sdesc_sw128(sa + L::kA1Bytes + kk * 32, 16, 1024);
-              if (kMx) {  // K step kk = 32-code block kk of the stage: byte kk of every scale word
-                umma_mx(d_tmem, ad, bd, idesc_mx(BM, BN, 0, 0, kk, kk), sf_t, sf_t + 4, (ks != k0 || kk != 0) ? 1u : 0u);
-              } else if (kPair) {  // same offsets in both CTAs: each holds its rows of A and its columns of B
-                umma_bf16_pair(d_tmem, ad, bd, kIdesc, (ks != k0 || kk != 0) ? 1u : 0u);
-                if (kDual) umma_bf16_pair(d_tmem, adl, bd, kIdesc, 1u);
-              } else {
-                umma_step<kF8>(d_tmem, ad, bd, kIdesc, (ks != k0 || kk != 0) ? 1u : 0u);
-                if (kDual) umma_step<kF8>(d_tmem, adl, bd, kIdesc, 1u);
+            const uint32_t d_tmem = tmem_base + buf * BN;
+            for (int ks = k0; ks < k1; ++ks, ++it) {
+              const int s = it % STAGES;
+              const uint32_t ph = (it / STAGES) & 1;
+              if (!mbar_wait(&full_bar[s], ph, s_abort, p.timeout_ns, p.err)) {
+                aborted = true;
+                break;
               }
+              const uint32_t sa = smem_u32(smem + s * L::kStageBytes);
+              const uint32_t sb = sa + L::kABytes;
+              if (kGather) fence_proxy_async_smem();  // cp.async writes -> UMMA operand reads
+              tc_fence_after();
+              // block-scaled form: this stage's scale blocks into its own TMEM columns (their previous readers, the
+              // UMMAs of the stage's last use, completed before the stage was refilled); tcgen05.cp and the UMMAs
+              // after it run in issue order
+              const uint32_t sf_t = tmem_base + 2 * BN + s * kSfCols;
+              if (kMx) {
+                const uint32_t sf_s = sb + L::kBBytes;
+                tmem_cp_32x128b_x4(sf_t, sdesc_plain(sf_s, 128, 128));
+#pragma unroll
+                for (int a = 0; a < mx_b_blocks(BN); ++a)
+                  tmem_cp_32x128b_x4(sf_t + 4 + 4 * a, sdesc_plain(sf_s + 512 + 512 * a, 128, 128));
+              }
+#pragma unroll
+              for (int kk = 0; kk < BK / 16; ++kk) {
+                const uint64_t ad =
+                    kAMn ? sdesc_sw128(sa + kk * 2048, BK * 128, 1024) : sdesc_sw128(sa + kk * 32, 16, 1024);
+                const uint64_t bd =
+                    kBMn ? sdesc_sw128(sb + kk * 2048, BK * 128, 1024) : sdesc_sw128(sb + kk * 32, 16, 1024);
+                // dual A: the low part of A times the same B, into the same accumulator
+                const uint64_t adl = kAMn ? sdesc_sw128(sa + L::kA1Bytes + kk * 2048, BK * 128, 1024)
+                                          : sdesc_sw128(sa + L::kA1Bytes + kk * 32, 16, 1024);
+                if (kMx) {  // K step kk = 32-code block kk of the stage: byte kk of every scale word
+                  umma_mx(d_tmem, ad, bd, idesc_mx(BM, BN, 0, 0, kk, kk), sf_t, sf_t + 4, (ks != k0 || kk != 0) ? 1u : 0u);
+                } else if (kPair) {  // same offsets in both CTAs: each holds its rows of A and its columns of B
+                  umma_bf16_pair(d_tmem, ad, bd, kIdesc, (ks != k0 || kk != 0) ? 1u : 0u);
+                  if (kDual) umma_bf16_pair(d_tmem, adl, bd, kIdesc, 1u);
+                } else {
+                  umma_step<kF8>(d_tmem, ad, bd, kIdesc, (ks != k0 || kk != 0) ? 1u : 0u);
+                  if (kDual) umma_step<kF8>(d_tmem, adl, bd, kIdesc, 1u);
+                }
+              }
+              if (kPair) umma_commit_pair_mc(&empty_bar[s], 3);  // both CTAs' stage s is free
+              else if (CN > 1) umma_commit_mc(&empty_bar[s], static_cast<uint16_t>((1u << CN) - 1u));
+              else umma_commit(&empty_bar[s]);
             }
-            if (kPair) umma_commit_pair_mc(&empty_bar[s], 3);  // both CTAs' stage s is free
-            else if (CN > 1) umma_commit_mc(&empty_bar[s], static_cast<uint16_t>((1u << CN) - 1u));
-            else umma_commit(&empty_bar[s]);
-          }
-          if (aborted) break;
-          if (kPair) umma_commit_pair_mc(&tfull_bar[buf], 3);  // both CTAs' halves of the accumulator are ready
-          else umma_commit(&tfull_bar[buf]);
-          if (k1 == nk) break;
+            if (aborted) break;
+            if (kPair) umma_commit_pair_mc(&tfull_bar[buf], 3);  // both CTAs' halves of the accumulator are ready
+            else umma_commit(&tfull_bar[buf]);
+            if (k1 == nk) break;
           }
           if (aborted) break;
         }
@@ -1428,7 +1428,8 @@ __global__ void __launch_bounds__(WarpPlan<STAGES, EW, AMODE, BMODE, CN, XF>::kT
               mbar_arrive(&tempty_bar[acc & (kAccs - 1)]);
               if (k0 + kChain >= (tl.k_len + BK - 1) / BK) break;
               ++acc;
-              there = mbar_wait(&tfull_bar[acc & (kAccs - 1)], (acc >> kAccBit) & 1, s_abort, p.timeout_ns, p.err);
+              // one verdict for the warp: it reads the accumulator together
+              there = __all_sync(0xffffffffu, mbar_wait(&tfull_bar[acc & (kAccs - 1)], (acc >> kAccBit) & 1, s_abort, p.timeout_ns, p.err));
               if (!there) break;
               tc_fence_after();
             }
