@@ -648,10 +648,10 @@ int moe_grouped_gemm_fwd_mx_kept8(moe_ctx* ctx, const void* Xq, const void* x_sf
  * moe_backward_kept8, _e4m3_kept8, _mx_kept8 — the backwards of those names from H and U kept in 8 bits, read in the dSwiGLU
  * epilogue, and from X in bf16 or, with X == NULL, as codes Xq [T,d] and scales x_scale [T,d/32] (moe_keep_rows8).  The
  * gradients are those of the layer at the kept values; in the bf16 form dX's rows of a pair are summed from fp16 values with a
- * scale for 64 columns, dW_r takes dlogits as three bf16 parts, and dS (with dlogits) up to d = 4096 has sums of 512 terms of the
- * tensor cores added up in fp32.  ws: at least moe_kept8_workspace_bytes(T, d, E, n, cap) bytes (0 on
- * bad sizes; cap: the pair arrays' length).  Everything else as without; CTA pairs (moe_set_cta_pairs) do not apply to the
- * dSwiGLU product here.
+ * scale for 64 columns (off by 2^-11 of a value, or 2^-39 of the largest finite one of the 64 where that is more), dW_r takes
+ * dlogits as three bf16 parts, and dS (with dlogits) up to d = 4096 has sums of 512 terms of the tensor cores added up in fp32.
+ * ws: at least moe_kept8_workspace_bytes(T, d, E, n, cap) bytes (0 on bad sizes; cap: the pair arrays' length).  Everything
+ * else as without; CTA pairs (moe_set_cta_pairs) do not apply to the dSwiGLU product here.
  */
 size_t moe_kept8_workspace_bytes(int T, int d, int E, int n, long long cap);
 int moe_backward_kept8(moe_ctx* ctx, const void* dO, const void* X, const void* Xq, const void* x_scale, const void* W_r,

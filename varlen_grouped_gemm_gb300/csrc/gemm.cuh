@@ -1664,8 +1664,9 @@ __global__ void __launch_bounds__(WarpPlan<STAGES, EW, AMODE, BMODE, CN, XF>::kT
               }
             }
             if constexpr (kF16s) {
-              // the power of two that takes the largest magnitude to [2^14, 2^15) (infinities and NaN stay what they are)
-              const int be = max(15, static_cast<int>(__float_as_uint(max_abs_nan(v)) >> 23));
+              // the power of two that takes the largest finite magnitude to [2^14, 2^15): infinities and NaN stay what they
+              // are whatever the factor, and the columns beside them keep their values
+              const int be = max(15, static_cast<int>(__float_as_uint(max_abs_finite(v)) >> 23));
               const float inv = __uint_as_float(static_cast<uint32_t>(268 - be) << 23);
               if (row_ok && col < p.N)
                 p.o_scale[(s_off[tl.g] + static_cast<long long>(m)) * (p.N / 64) + col / 64] =

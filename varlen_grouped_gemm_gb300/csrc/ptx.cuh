@@ -688,6 +688,17 @@ __device__ __forceinline__ float max_abs_nan(const float (&v)[N]) {
   for (int i = 0; i < N; ++i) m[i & 3] = max_abs_nan(m[i & 3], v[i]);
   return max_abs_nan(max_abs_nan(m[0], m[1]), max_abs_nan(m[2], m[3]));
 }
+// The largest magnitude of the finite ones among N values.
+template <int N>
+__device__ __forceinline__ float max_abs_finite(const float (&v)[N]) {
+  constexpr float kMax = 3.4028235e38f;
+  float m = max_abs_nan(v);
+  if (m <= kMax) return m;
+  m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) m = fmaxf(m, fabsf(v[i]) <= kMax ? fabsf(v[i]) : 0.0f);
+  return m;
+}
 // Four codes, little-endian: adding 1.5 * 2^23 leaves the nearest whole number in the low bits.
 __device__ __forceinline__ uint32_t kept8_x4(float a, float b, float c, float d, float inv) {
   constexpr float kM = 12582912.0f;
