@@ -612,7 +612,7 @@ int moe_router_backward(moe_ctx* ctx, const float* dlogits, const void* X, const
  *
  *   scale = max|v| / 127 (fp32 division), rounded up to bf16, at least 2^-126; NaN for a block with an infinity or a NaN
  *   code  = v * (1 / scale) rounded to the nearest whole number (ties to even), the reciprocal and the product in fp32
- *   value = code * scale, rounded to bf16: what the backward takes the kept number for
+ *   value = code * scale, rounded to bf16, at most its largest finite number: what the backward takes the kept number for
  *
  * A value is off by at most scale / 2 and the rounding to bf16 (2^-8 of it).  Codes are int8 [rows, cols], scales bf16
  * [rows, cols / 32]; both 16-byte aligned.

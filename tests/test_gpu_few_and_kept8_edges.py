@@ -3,7 +3,7 @@ test_gpu_few.py, whose references these tests use."""
 import pytest
 import torch
 
-from test_gpu_kept8 import BF, ROUND, backward, buffers, formula, forward, layer, rel
+from test_gpu_kept8 import BF, F32, ROUND, backward, buffers, formula, forward, layer, rel, rule, same
 
 pytestmark = pytest.mark.gpu
 
@@ -47,3 +47,58 @@ def read(vgg, ctx, k):
     out = torch.empty(k.q.shape, dtype=BF, device="cuda")
     vgg.moe_read_rows8(ctx, k, out)
     return out
+
+
+LARGEST = torch.finfo(BF).max
+
+
+def ends(k):
+    """What codes and scales stand for: code * scale, rounded, at most bf16's largest number."""
+    v = (k.q.float().unflatten(-1, (-1, 32)) * k.scale.float()[..., None]).flatten(-2)
+    return v.clamp(-LARGEST, LARGEST).to(BF)
+
+
+def test_finite_values_come_back_finite(vgg, ctx):
+    """The largest numbers, whose code times their scale lies past them: 127 * 2.6792e36 = 3.4026e38."""
+    M = torch.zeros((8, 96), dtype=BF, device="cuda")
+    M[0, 0], M[1, 33], M[2, 95] = LARGEST, -LARGEST, LARGEST
+    M[2, 64:90] = -LARGEST
+    big = torch.tensor([0x7F7F, 0x7F7E, 0x7F7D, 0x7F70, 0x7F00, 0x7E80], dtype=torch.int16, device="cuda").view(BF)
+    for i, v in enumerate(big[1:]):
+        M[3 + i, 32 * (i % 3)] = -v
+    M[3:, 95] = big[torch.arange(5, device="cuda")]
+    k, out = vgg.Kept8.empty(8, 96), torch.empty_like(M)
+    vgg.moe_keep_rows8(ctx, M, k)
+    vgg.moe_read_rows8(ctx, k, out)
+    q, s = rule(M)
+    assert torch.equal(k.q, q) and same(k.scale, s) and same(out, ends(k))
+    assert torch.isfinite(out).all()
+    # half a scale, and the rounding to bf16
+    err = (out.double() - M.double()).abs().unflatten(-1, (-1, 32))
+    assert (err <= 0.5 * (1 + 2.0 ** -20) * s.double()[..., None] + 2.0 ** -8 * M.double().abs().unflatten(-1, (-1, 32))).all()
+    k.scale[4] = float("nan")  # of a block that holds a value that is not finite
+    vgg.moe_read_rows8(ctx, k, out)
+    assert out[4].isnan().all()
+
+
+def test_backward_at_the_largest_kept_value(vgg, ctx):
+    """H at the end of the range (an infinite one would leave 0 * inf in its gradient)."""
+    shape = T, d, E, n, K = 130, 128, 8, 64, 2
+    s = layer(*shape, seed=21)
+    s["dO"] = (s["dO"].float() * 1e-20).to(BF)  # dU = dA' silu(H): finite
+    buf = buffers(vgg, *shape, "bf16", dW_dtype=F32, kept8=True)
+    forward(vgg, ctx, s, "bf16", None, buf)
+    row = torch.zeros((1, 32), dtype=BF, device="cuda")
+    row[0, 0] = LARGEST
+    k = vgg.Kept8.empty(1, 32)
+    vgg.moe_keep_rows8(ctx, row, k)
+    buf.H.q[5, :32], buf.H.scale[5, 0] = k.q[0], k.scale[0, 0]
+    buf.U.q[5] = 0
+    backward(vgg, ctx, s, "bf16", None, buf, None)
+    assert vgg.moe_get_error(ctx) == (vgg.MOE_OK, 0)
+    ref = formula(s, buf, ends(buf.xk), ends(buf.H), ends(buf.U))
+    # dX is that row's single dU times a row of W_up: its rounding is the same in every column, 2^-8 at most
+    assert rel(buf.dX, ref["dX"]) <= 2.0 ** -8 + DX
+    assert rel(buf.dW_up, ref["dW_up"]) <= 2e-5
+    for name in ("dW_gate", "dW_down", "dS", "dlogits"):
+        assert torch.isfinite(getattr(buf, name)).all(), name

@@ -446,6 +446,13 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
+// The same with bf16's largest number in place of what rounds past it, infinities among it; NaN stays NaN.
+__device__ __forceinline__ uint32_t pack_bf16x2_finite(float lo, float hi) {
+  uint32_t v;
+  asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(v) : "f"(hi), "f"(lo));
+  return v;
+}
+
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&v);
@@ -718,7 +725,8 @@ __device__ __forceinline__ void kept8_block32(const float (&v)[32], uint8_t* q, 
                    kept8_x4(v[j + 8], v[j + 9], v[j + 10], v[j + 11], inv),
                    kept8_x4(v[j + 12], v[j + 13], v[j + 14], v[j + 15], inv));
 }
-// The values of four codes: code times scale, rounded to bf16; as two bf16 pairs.  A code c as a byte c + 128 under the
+// The values of four codes: code times scale, rounded to bf16; as two bf16 pairs.  The codes of the largest numbers stand for
+// more than bf16 holds (0x7F7F: 127 times 2.6792e36 is 3.4026e38): its largest number then, which is nearer to what was kept.  A code c as a byte c + 128 under the
 // exponent of 2^23 is 2^23 + 128 + c.
 __device__ __forceinline__ uint2 kept8_values4(uint32_t w, float scale) {
   const uint32_t x = w ^ 0x80808080u;
@@ -729,7 +737,7 @@ __device__ __forceinline__ uint2 kept8_values4(uint32_t w, float scale) {
   f[3] = __uint_as_float(__byte_perm(x, 0x4B000000u, 0x7443));
 #pragma unroll
   for (int i = 0; i < 4; ++i) f[i] = (f[i] - 8388736.0f) * scale;
-  return make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
+  return make_uint2(pack_bf16x2_finite(f[0], f[1]), pack_bf16x2_finite(f[2], f[3]));
 }
 __device__ __forceinline__ void kept8_load32(const uint8_t* q, const __nv_bfloat16* scale, float (&v)[32]) {
   const float s = __bfloat162float(__ldg(scale));
