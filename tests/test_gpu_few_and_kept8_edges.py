@@ -1,8 +1,11 @@
 """Ends of the range of the layer for a few tokens and of the activations kept in 8 bits.  Bounds as in test_gpu_kept8.py and
 test_gpu_few.py, whose references these tests use."""
+import ctypes
+
 import pytest
 import torch
 
+import test_gpu_few as few
 from test_gpu_kept8 import BF, F32, ROUND, backward, buffers, formula, forward, layer, rel, rule, same
 
 pytestmark = pytest.mark.gpu
@@ -102,3 +105,18 @@ def test_backward_at_the_largest_kept_value(vgg, ctx):
     assert rel(buf.dW_up, ref["dW_up"]) <= 2e-5
     for name in ("dW_gate", "dW_down", "dS", "dlogits"):
         assert torch.isfinite(getattr(buf, name)).all(), name
+
+
+@pytest.mark.parametrize("form", ["bf16", "e4m3"])
+@pytest.mark.parametrize("blocks", [1, 3, 4, 7])
+def test_few_tokens_on_few_processors(vgg, blocks, form):
+    """More tokens than blocks: a block finds the choice of several, more of them than it has warps (1 and 3 blocks)."""
+    ctx = vgg.Context(0)
+    sms = ctypes.c_int.from_address(ctx.handle.value + 4)  # a context holds its device and the blocks that run at once
+    assert sms.value == torch.cuda.get_device_properties(0).multi_processor_count
+    sms.value = blocks
+    for T in (9, 16, 47, 64):
+        s = few.make(T, 64 * (1 + T % 3), 16, 64, 1 + T % 4, seed=T)
+        w8 = few.weights8(vgg, ctx, s) if form == "e4m3" else None
+        few.check(few.call(vgg, ctx, s, form, w8), few.reference(s, form, w8))
+    assert vgg.moe_get_error(ctx) == (vgg.MOE_OK, 0)

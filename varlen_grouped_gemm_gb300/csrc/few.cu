@@ -62,7 +62,7 @@ static_assert(kProd <= kMinStages && kMinStages >= 3, "the ring");
 // Every block finds the choice of so few tokens itself; of more, each is found by one block behind a barrier (a block
 // reads splits x T x E partial logits otherwise).
 constexpr int kOwnChoice = 8;
-constexpr int kRound = 16;   // tokens whose logits a block holds at a time
+static_assert(kOwnChoice <= kWarps, "a warp for each token of a choice");
 // counters: choices made, items with activations of each half, blocks done, then one for each shared item
 constexpr int kCtrChoice = 0, kCtrItems = 1, kCtrDone = 3, kCtrShared = 4;
 
@@ -390,16 +390,16 @@ __global__ void __launch_bounds__(256) few_router_kernel(const __grid_constant__
   }
 }
 
-// The choice of up to kRound tokens first, first + step, ...: the block adds up their logits as order keys in keys [.][E]
-// (shared memory), then one warp a token takes K times the largest key, the lower expert among equal ones (the rule of
-// moe_route).  put(t, k, id, w) receives each.
+// The choice of the tokens first .. first + count - 1, kOwnChoice at most: the block adds up their logits as order keys in
+// keys [.][E] (shared memory), then one warp a token takes K times the largest key, the lower expert among equal ones (the rule
+// of moe_route).  put(t, k, id, w) receives each.
 template <class Put>
-__device__ __forceinline__ void choose(const FewArgs& a, int first, int step, int count, uint32_t* keys, const Put& put) {
+__device__ __forceinline__ void choose(const FewArgs& a, int first, int count, uint32_t* keys, const Put& put) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long plane = static_cast<long long>(a.T) * a.E;
   for (int x = threadIdx.x; x < count * a.E; x += kThreads) {
     const int i = x / a.E, e = x - i * a.E;
-    const float* p = a.part + static_cast<long long>(first + i * step) * a.E + e;
+    const float* p = a.part + static_cast<long long>(first + i) * a.E + e;
     float v = a.bias ? __ldg(a.bias + e) : 0.0f;
     for (int s0 = 0; s0 < a.splits; s0 += 16) {  // sixteen loads in flight
       float y[16];
@@ -438,7 +438,7 @@ __device__ __forceinline__ void choose(const FewArgs& a, int first, int step, in
         ex_k = ex;
       }
     }
-    if (lane < a.K) put(first + warp * step, lane, id, ex_k / sum);
+    if (lane < a.K) put(first + warp, lane, id, ex_k / sum);
   }
   __syncthreads();
 }
@@ -496,8 +496,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
   if (warp == kMma) tmem_alloc(&L.tmem, tmem_cols);
 
   // ---- the choice, and the pairs grouped by expert (the ring's memory is scratch until the first load) ----
-  uint32_t* keys = reinterpret_cast<uint32_t*>(ring);              // [kRound][E]
-  uint64_t* s_mask = reinterpret_cast<uint64_t*>(keys + kRound * a.E);  // [E] tokens of each expert
+  uint32_t* keys = reinterpret_cast<uint32_t*>(ring);              // [kOwnChoice][E]
+  uint64_t* s_mask = reinterpret_cast<uint64_t*>(keys + kOwnChoice * a.E);  // [E] tokens of each expert
   int* s_ids = reinterpret_cast<int*>(s_mask + a.E);                // [P]
   float* s_w = reinterpret_cast<float*>(s_ids + kMaxPairs);
   uint16_t* s_eoff = reinterpret_cast<uint16_t*>(s_w + kMaxPairs);  // [E] first pair, index
@@ -508,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
   if (F8)
     for (int t = tid; t < a.T; t += kThreads) L.xs[t] = __ldcg(a.xs + t);
   if (a.T <= kOwnChoice) {
-    choose(a, 0, 1, a.T, keys, [&](int t, int k, int id, float w) {
+    choose(a, 0, a.T, keys, [&](int t, int k, int id, float w) {
       s_ids[t * a.K + k] = id;
       s_w[t * a.K + k] = w;
       if (b == 0) {
@@ -517,13 +517,12 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
       }
     });
   } else {
-    for (int t = b; t < a.T; t += kRound * G) {
-      const int count = min(kRound, (a.T - t + G - 1) / G);
-      choose(a, t, G, count, keys, [&](int t2, int k, int id, float w) {
+    for (int t = b; t < a.T; t += G) {
+      choose(a, t, 1, keys, [&](int t2, int k, int id, float w) {
         a.ids[t2 * a.K + k] = id;
         a.w[t2 * a.K + k] = w;
       });
-      if (tid == 0) red_release(&a.ctr[kCtrChoice], count);
+      if (tid == 0) red_release(&a.ctr[kCtrChoice], 1);
     }
     if (tid == 0) L.ok = wait_count(&a.ctr[kCtrChoice], a.T, &L.abort, a.timeout_ns, a.err) ? 1 : 0;
     __syncthreads();
