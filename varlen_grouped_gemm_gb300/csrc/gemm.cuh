@@ -1285,7 +1285,8 @@ __global__ void __launch_bounds__(WarpPlan<STAGES, EW, AMODE, BMODE, CN, XF>::kT
       Tile tl;
       sch.decode(p, t, gcur, tl);
       const int buf = acc & (kAccs - 1);
-      if (!mbar_wait(&tfull_bar[buf], (acc >> kAccBit) & 1, s_abort, p.timeout_ns, p.err)) break;
+      // one verdict for the warp: what follows are its loads of the accumulator and its exchanges
+      if (!__all_sync(0xffffffffu, mbar_wait(&tfull_bar[buf], (acc >> kAccBit) & 1, s_abort, p.timeout_ns, p.err))) break;
       tc_fence_after();
       const uint32_t tbase = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + buf * BN;
       const bool row_ok = row_local < tl.rows;

@@ -214,7 +214,8 @@ __global__ void __launch_bounds__(kDwThreads, 1) router_dw_kernel(const DwArgs a
         for (int q = 0; q < 32; ++q) v[b][q] = 0.0f;
       for (int k0 = 0; k0 < it.steps; k0 += kDwChunk, ++acc) {
         const int buf = acc & 1;
-        ok = mbar_wait(&tfull[buf], acc >> 1 & 1, &s_abort, a.timeout_ns, a.err);
+        // one verdict for the warp: what follows are its loads of the accumulator
+        ok = __all_sync(0xffffffffu, mbar_wait(&tfull[buf], acc >> 1 & 1, &s_abort, a.timeout_ns, a.err));
         if (!ok) break;
         tc_fence_after();
         const uint32_t t0 = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * 256 + c0;
