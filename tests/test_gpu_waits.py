@@ -4,6 +4,8 @@ that one looks at it."""
 import pytest
 import torch
 
+import test_gpu_few as few
+
 pytestmark = pytest.mark.gpu
 
 SECONDS = 2_000_000_000
@@ -38,3 +40,17 @@ def test_grouped_product(vgg):
     give_up(vgg, ctx, lambda: vgg.moe_test_gemm_varlen_m(ctx, A, None, B, True, offsets, D))
     both = 2.0 * ((K + 20) // 21)  # whole numbers: exact
     assert (D[:1000] == both).all() and (D[1000:] == 2 * both).all()
+
+
+@pytest.mark.parametrize("form", ["bf16", "e4m3"])
+@pytest.mark.parametrize("T", [5, 50])
+def test_few_tokens(vgg, form, T):
+    """Wide experts, whose tiles take a hundred microseconds each, on the same workspace and outputs."""
+    ctx = vgg.Context(0)
+    s = few.make(T, 16384, 16, 2048, 8, seed=30)
+    weights = few.weights8(vgg, ctx, s) if form == "e4m3" else (s["W_gate"], s["W_up"], s["W_down"])
+    buf, fresh = (vgg.FewBuffers.allocate(T, 16384, 16, 2048, 8) for _ in range(2))
+    vgg.forward_few(ctx, s["X"], s["W_r"], None, weights, fresh)
+    give_up(vgg, ctx, lambda: vgg.forward_few(ctx, s["X"], s["W_r"], None, weights, buf))
+    for name in ("O", "topk_ids", "topk_w"):
+        assert torch.equal(getattr(buf, name), getattr(fresh, name)), name

@@ -1042,14 +1042,11 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const __grid_con
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  const bool gave_up = L.abort;  // (every thread sees so)
+  if (gave_up) linger();
   if (warp == kMma) tmem_dealloc(tmem, tmem_cols);
   // ---- the sums over a token's choices, once every block's parts are there: eight lanes a token and four columns, one a choice ----
-  if (L.abort) {  // a wait gave up (every thread sees so): let the copies in flight land before the block goes away
-    const uint64_t t0 = globaltimer_ns();
-    while (globaltimer_ns() - t0 < 20000000ull) {
-    }
-    return;
-  }
+  if (gave_up) return;
   __syncthreads();  // (the wait below may raise the flag)
   if (tid == 0) L.ok = ok && wait_count(&a.ctr[kCtrDone], G, &L.abort, a.timeout_ns, a.err) ? 1 : 0;
   __syncthreads();

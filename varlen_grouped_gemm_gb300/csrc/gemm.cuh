@@ -836,17 +836,7 @@ __global__ void __launch_bounds__(WarpPlan<STAGES, EW, AMODE, BMODE, CN, XF>::kT
         ++it;
         pos_next(sch, p, gcur, q);
       }
-      if (aborted && kPair) {
-        // the copies count on the even CTA's barriers: give those in flight 20 ms to land
-        const uint64_t t0 = globaltimer_ns();
-        while (globaltimer_ns() - t0 < 20000000ull) {
-        }
-      } else if (aborted) {
-        // let this thread's copies already in flight land before the CTA goes away
-        volatile int never = 0;
-        for (int j = (it > STAGES ? it - STAGES : 0); j < it; ++j)
-          if (j % kNP == pj) mbar_wait(&full_bar[j % STAGES], (j / STAGES) & 1, &never, 20000000ull, nullptr);
-      } else if (CN > 1) {
+      if (!aborted && CN > 1) {
         // every CTA's release of this thread's last stages has arrived here, so no peer still
         // targets this CTA's barriers when it leaves
         for (int j = (it > STAGES ? it - STAGES : 0); j < it; ++j)
@@ -1196,7 +1186,7 @@ __global__ void __launch_bounds__(WarpPlan<STAGES, EW, AMODE, BMODE, CN, XF>::kT
       }
     };
     // EPI_ADD: this warp's boxes of the added matrix for a tile, each once the store out of its buffer has been read
-    uint32_t add_phase = 0, add_asked = 0;  // (asked: in lane 0)
+    uint32_t add_phase = 0;
     auto load_add = [&](const Tile& x) {
       if constexpr (EPI == EPI_ADD) {
         if (lane == 0) {
@@ -1205,7 +1195,6 @@ __global__ void __launch_bounds__(WarpPlan<STAGES, EW, AMODE, BMODE, CN, XF>::kT
           for (int q = 0; q < kAddBufs && c0 + 64 * q < p.N; ++q) {
             uint64_t* bar = &add_bar[warp * kAddBufs + q];
             mbar_arrive_expect_tx(bar, kStgBuf);
-            add_asked |= 1u << q;
             tma_load_3d(stg_base + q * kStgBuf, &mp.o1, bar, c0 + 64 * q, x.m0 + quarter * 32, 0);
           }
         }
@@ -1560,7 +1549,6 @@ __global__ void __launch_bounds__(WarpPlan<STAGES, EW, AMODE, BMODE, CN, XF>::kT
             if (p.add) {
               mbar_wait(&add_bar[warp * kAddBufs + q], (add_phase >> q) & 1, s_abort, p.timeout_ns, p.err);
               add_phase ^= 1u << q;
-              if (!*s_abort) add_asked &= ~(1u << q);
             } else if (q == 0) {
               if (lane == 0) bulk_wait_read<0>();  // the last tile's stores have been read out of the buffers
               __syncwarp();
@@ -1687,13 +1675,6 @@ __global__ void __launch_bounds__(WarpPlan<STAGES, EW, AMODE, BMODE, CN, XF>::kT
       if (kPair && cta_rank != 0) mbar_arrive_remote(mapa_shared(smem_u32(&tempty_bar[buf]), 0));
       else mbar_arrive(&tempty_bar[buf]);
     }
-    if constexpr (EPI == EPI_ADD) {
-      if (lane == 0 && *s_abort) {  // let the boxes still asked for land before the CTA goes away
-        volatile int never = 0;
-        for (int q = 0; q < kAddBufs; ++q)
-          if ((add_asked >> q) & 1) mbar_wait(&add_bar[warp * kAddBufs + q], (add_phase >> q) & 1, &never, 20000000ull, nullptr);
-      }
-    }
     if (lane == 0) bulk_wait0();
     __syncwarp();
   }
@@ -1701,6 +1682,7 @@ __global__ void __launch_bounds__(WarpPlan<STAGES, EW, AMODE, BMODE, CN, XF>::kT
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (*s_abort) linger();
   if (CN > 1) cluster_sync();  // peers finished with this CTA's shared memory
   if (warp == kProdWarp) {
     if (kPair) tmem_dealloc_pair(tmem_base, kTmemCols);

@@ -118,6 +118,14 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   }
 }
 
+// A block whose wait gave up goes on to its end 20 ms later, before it gives back its memory: the copies and products that any of
+// its roles has asked for have landed by then (a role may have asked for its last ones and be done).
+__device__ __forceinline__ void linger() {
+  const uint64_t t0 = globaltimer_ns();
+  while (globaltimer_ns() - t0 < 20000000ull) {
+  }
+}
+
 // ------------------------------------------------------------------ dependent launches
 // A kernel launched with programmatic stream serialization may start before the kernel ahead of it has ended:
 // griddep_wait waits for that kernel's end (its writes are then visible), griddep_launch lets the kernel behind start.

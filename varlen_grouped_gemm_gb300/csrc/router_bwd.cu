@@ -137,10 +137,6 @@ __global__ void __launch_bounds__(kDwThreads, 1) router_dw_kernel(const DwArgs a
         tma_load_3d(xs + s * kDwXBytes, &mx, &full_x[s], 0, it.k0 + 64 * k, it.i0 / 64);
       }
     }
-    if (!ok) {  // let the copies in flight land before the block goes away
-      volatile int never = 0;
-      for (int j = n > kDwX ? n - kDwX : 0; j < n; ++j) mbar_wait(&full_x[j % kDwX], j / kDwX & 1, &never, 20000000ull, nullptr);
-    }
   } else if (warp == 9 && lane == 0) {  // the parts
     int n = 0;
     bool ok = true;
@@ -157,10 +153,6 @@ __global__ void __launch_bounds__(kDwThreads, 1) router_dw_kernel(const DwArgs a
           tma_load_2d(ps + s * kDwPBytes + kDwBox, &mp, &full_p[s], it.e0 + 64, row);
         }
       }
-    }
-    if (!ok) {
-      volatile int never = 0;
-      for (int j = n > kDwP ? n - kDwP : 0; j < n; ++j) mbar_wait(&full_p[j % kDwP], j / kDwP & 1, &never, 20000000ull, nullptr);
     }
   } else if (warp == 10 && lane == 0) {  // the products
     constexpr uint32_t kIdesc = idesc_bf16(128, 256, 1, 1);
@@ -251,6 +243,7 @@ __global__ void __launch_bounds__(kDwThreads, 1) router_dw_kernel(const DwArgs a
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (s_abort) linger();
   if (warp == 8) tmem_dealloc(tmem, 512);
   griddep_wait();
 }
