@@ -102,13 +102,15 @@ class Block:
         """Gradients for dout [T, d] fp32: dx, dres, dweight here, the layer's (dW_r with the balance loss's) in buf."""
         b, w = self.buf, (self.W_r, self.W_gate, self.W_up, self.W_down)
         dO = dout.to(BF)
-        y = None if self.kept8 else self.y  # kept in 8 bits: the layer's X comes from its codes, y may go after the forward
+        y = None if self.kept8 else self.y  # kept in 8 bits: the layer's X comes from its codes
         if self.form == "e4m3":
             vgg.backward_e4m3(self.ctx, dO, y, *w, self.quantized, b)
         elif self.form == "mx":
             vgg.backward_mx(self.ctx, dO, y, *w, self.quantized, b)
         else:
             vgg.backward(self.ctx, dO, y, *w, b)
+        if self.kept8:  # y's memory may have served others since the forward (one y for all blocks of a model will do)
+            vgg.moe_read_rows8(self.ctx, b.xk, self.y)
         vgg.moe_router_backward(self.ctx, self.dlogits, self.y, self.W_r, b.dX, b.dW_r, b.dX, b.dW_r, self.ws_router)
         vgg.moe_add_rmsnorm_backward(self.ctx, b.dX, self.h, self.weight, self.rstd, dout, self.dx, self.dres, self.dweight,
                                      self.ws_norm)
