@@ -120,3 +120,75 @@ def test_few_tokens_on_few_processors(vgg, blocks, form):
         w8 = few.weights8(vgg, ctx, s) if form == "e4m3" else None
         few.check(few.call(vgg, ctx, s, form, w8), few.reference(s, form, w8))
     assert vgg.moe_get_error(ctx) == (vgg.MOE_OK, 0)
+
+
+def test_rows_of_more_than_2_31_values(vgg, ctx):
+    rows, cols = (1 << 17) + 3, 1 << 14
+    M = torch.zeros((rows, cols), dtype=BF, device="cuda")
+    tail = torch.randn((5, cols), device="cuda", generator=torch.Generator(device="cuda").manual_seed(22)).to(BF)
+    M[:2], M[-3:] = tail[:2], tail[2:]
+    k, out = vgg.Kept8.empty(rows, cols), torch.full_like(M, 7.0)
+    vgg.moe_keep_rows8(ctx, M, k)
+    vgg.moe_read_rows8(ctx, k, out)
+    q, s = rule(tail)
+    assert torch.equal(torch.cat((k.q[:2], k.q[-3:])), q) and same(torch.cat((k.scale[:2], k.scale[-3:])), s)
+    want = ends(vgg.Kept8(q, s))
+    assert same(out[:2], want[:2]) and same(out[-3:], want[2:]) and not out[2:-3].any()
+
+
+def test_epilogues_past_2_31_values(vgg, ctx):
+    """Pairs times columns past 2^31: the last rows' codes against the rule on the plain forward's own H and U, and their gradients
+    against 64 bits."""
+    shape = T, d, E, n, K = 65536, 64, 8, 4160, 8
+    s = layer(*shape, seed=23)
+    plain, kept = (vgg.Buffers.allocate(*shape, backward=k8, kept8=k8) for k8 in (False, True))
+    assert kept.cap * n > 1 << 31
+    forward(vgg, ctx, s, "bf16", None, plain)
+    forward(vgg, ctx, s, "bf16", None, kept)
+    assert vgg.moe_get_error(ctx) == (vgg.MOE_OK, 0)
+    rows = slice(kept.cap - 300, kept.cap)
+    for full, k in ((plain.H, kept.H), (plain.U, kept.U)):
+        q, scale = rule(full[rows])
+        assert torch.equal(k.q[rows], q) and same(k.scale[rows], scale)
+    del plain
+    backward(vgg, ctx, s, "bf16", None, kept, None)
+    assert vgg.moe_get_error(ctx) == (vgg.MOE_OK, 0)
+    h, u = (ends(vgg.Kept8(k.q[rows], k.scale[rows])).double() for k in (kept.H, kept.U))
+    t = kept.sorted_tok[rows].long()
+    want = ((s["dO"][t].double() @ s["W_down"][E - 1].double()) * (torch.nn.functional.silu(h) * u)).sum(1)
+    assert rel(kept.dS[rows], want) <= 2e-5
+
+
+@pytest.mark.parametrize("exponent", [-80, *range(-62, -52), -30, 0, 30, *range(58, 68), 80])
+def test_codes_of_tokens_at_every_scale(vgg, ctx, exponent):
+    """X's codes by the rule, x / scale in one division, from scales far below 2^-60 to far above 2^60 (between them the kernel divides
+    by way of the reciprocal).  Even rows: a scale m 2^(exponent - 6), m in 1 .. 36, and quotients in the middle of two codes;
+    odd rows: a scale that is rounded itself.
+
+    The layer is made so that O shows the codes: one expert, W_gate's rows all the same, so that H is one number for a token,
+    W_up and W_down the identity.  A is U times one number, rounded to bf16 (2^-8 at most, far less than half the distance of
+    two codes), so A's own codes are X's; O is their multiple, rounded to bf16 again."""
+    T, d, n, E = 64, 64, 64, 8
+    g = torch.Generator().manual_seed(exponent + 100)
+    m = torch.randint(1, 37, (T,), generator=g).double()
+    top = torch.where(torch.arange(T) % 2 == 0, 7 * m, torch.randint(128, 256, (T,), generator=g).double())
+    x = (torch.randn((T, d), generator=g, dtype=torch.float64) * top[:, None] / 3).clamp(-top[:, None], top[:, None])
+    for t in range(0, T, 2):
+        odd = 2 * torch.randint(8, 16, (24,), generator=g).double() + 1  # five bits: in the middle of two four-bit numbers
+        tie = m[t] / 64 * odd * 2.0 ** torch.randint(-6, 4, (24,), generator=g).double()
+        exact = (tie == tie.to(BF).double()) & (tie < top[t])
+        x[t, 1:25] = torch.where(exact, tie * torch.sign(x[t, 1:25]), x[t, 1:25])
+    x[:, 0] = top
+    X = (x * 2.0 ** exponent).to(BF).cuda()
+    one = torch.tensor(1.0).to(few.E4M3).view(torch.uint8).item()
+    identity = (torch.eye(n).repeat(E, 1, 1) * one).to(torch.uint8).cuda()
+    gate = torch.zeros_like(identity)
+    gate[:, :, 0] = one
+    scale = torch.full((E, n), 2.0 ** -exponent, device="cuda")  # H = top, U = x
+    w8 = vgg.E4m3Weights(gate, scale, identity, scale.clone(), identity.clone(), torch.ones((E, d), device="cuda"))
+    s = dict(X=X, W_r=torch.zeros((d, E), dtype=BF, device="cuda"), bias=None, K=1, W_gate=identity)
+    O = few.call(vgg, ctx, s, "e4m3", w8)[0].double()
+    assert vgg.moe_get_error(ctx) == (vgg.MOE_OK, 0)
+    want = few.codes(X)[0].view(few.E4M3).double()
+    assert (want[:, 0] == 448).all()
+    assert torch.equal((O / O[:, :1] * 448).float().to(few.E4M3).double(), want)
