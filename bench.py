@@ -512,6 +512,28 @@ def whole_job_rate(world: int, units_per_rank: float, ms_per_step: float) -> flo
     return world * units_per_rank / (ms_per_step * 1e-3)
 
 
+# What the line says of a further workload.
+_FURTHER = ("workload", "ms_per_step", "tflops", "pct_of_peak_bf16", "tokens_per_s", "steps")
+
+
+def six_digits(x):
+    """x with every float in it to six significant digits."""
+    if isinstance(x, float):
+        return float(f"{x:.6g}")
+    if isinstance(x, dict):
+        return {k: six_digits(v) for k, v in x.items()}
+    if isinstance(x, (list, tuple)):
+        return [six_digits(v) for v in x]
+    return x
+
+
+def short_line(line: dict) -> dict:
+    """The line for stdout: six digits a number, and of the further workloads their rates alone.  With all digits and every
+    workload's kernels it is 20 KB, more than a reader of a log's end keeps."""
+    further = {k: {n: v[n] for n in _FURTHER if n in v} for k, v in (line.get("per_workload") or {}).items()}
+    return six_digits({**line, **({"per_workload": further} if further else {})})
+
+
 def run_reference(args, rank, world):
     if rank != 0:
         return 0
@@ -960,7 +982,9 @@ def run_ours(args, rank, world, local_rank):
         if wl.name == "c2":
             line["baseline_note"] = ("vs_baseline divides by the pages' grouped-GEMM figure for this workload "
                                      "(13.14 ms fwd+bwd = 47.1 TFLOP/s on one A100): context, another machine")
-        print(json.dumps(line), flush=True)
+        if per_workload:
+            print(json.dumps({"per_workload": six_digits(per_workload)}), file=sys.stderr, flush=True)
+        print(json.dumps(short_line(line)), flush=True)
     return 0
 
 
