@@ -708,8 +708,8 @@ int moe_forward_few(moe_ctx* ctx, const void* X, long long ld_x, const void* W_r
 
 /*
  * moe_forward_few_e4m3 — the same on e4m3 weights: Wg_q, Wu_q [E,n,d], Wd_q [E,d,n] with wg_scale, wu_scale [E,n], wd_scale
- * [E,d] as moe_grouped_gemm_fwd_e4m3 takes them (moe_quantize_rows_e4m3).  The call quantizes X per token and A, rounded to
- * bf16, per pair by the rule of moe_quantize_rows_e4m3; the router takes X and W_r in bf16.
+ * [E,d] as moe_grouped_gemm_fwd_e4m3 takes them (moe_quantize_rows_e4m3), wd_scale 16-byte aligned.  The call quantizes X
+ * per token and A, rounded to bf16, per pair by the rule of moe_quantize_rows_e4m3; the router takes X and W_r in bf16.
  */
 int moe_forward_few_e4m3(moe_ctx* ctx, const void* X, long long ld_x, const void* W_r, const float* bias, const void* Wg_q,
                          const float* wg_scale, const void* Wu_q, const float* wu_scale, const void* Wd_q,

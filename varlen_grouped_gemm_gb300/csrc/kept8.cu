@@ -35,8 +35,9 @@ cudaError_t run_dx_store_f16s(int BN, const GemmParams& p, const Maps& m, int gr
 }
 
 // A matrix of bf16 values to codes and scales.  Four lanes have a block's 32 columns, 8 (16 bytes) each: loads and stores
-// are contiguous over the warp.  Rows are whole blocks, so the matrix is one run of them.  Bound by HBM and the launch:
-// 32768 x 1536 35 us with its events (154 MB, 4.4 TB/s), the way back 30.
+// are contiguous over the warp.  Rows are whole blocks, so the matrix is one run of them.  32768 x 1536 35 us with its
+// events (154 MB, 4.4 TB/s, two thirds of the copy rate), the way back 30: a thread has one load in flight, and two
+// exchanges and a division behind it before the next.
 __global__ void __launch_bounds__(256) keep_rows8_kernel(const __nv_bfloat16* __restrict__ M, long long n8,
                                                          uint8_t* __restrict__ q, __nv_bfloat16* __restrict__ scale) {
   const long long step = static_cast<long long>(gridDim.x) * blockDim.x;
