@@ -733,9 +733,9 @@ __device__ __forceinline__ void kept8_block32(const float (&v)[32], uint8_t* q, 
                    kept8_x4(v[j + 8], v[j + 9], v[j + 10], v[j + 11], inv),
                    kept8_x4(v[j + 12], v[j + 13], v[j + 14], v[j + 15], inv));
 }
-// The values of four codes: code times scale, rounded to bf16; as two bf16 pairs.  The codes of the largest numbers stand for
-// more than bf16 holds (0x7F7F: 127 times 2.6792e36 is 3.4026e38): its largest number then, which is nearer to what was kept.  A code c as a byte c + 128 under the
-// exponent of 2^23 is 2^23 + 128 + c.
+// The values of four codes: code times scale, rounded to bf16; as two bf16 pairs.  The codes of the largest numbers may stand
+// for more than bf16 holds (0x7F7F: 127 times 2.6792e36 is 3.4026e38): its largest number then, which is nearer to what was
+// kept.  A code c as a byte c + 128 under the exponent of 2^23 is 2^23 + 128 + c.
 __device__ __forceinline__ uint2 kept8_values4(uint32_t w, float scale) {
   const uint32_t x = w ^ 0x80808080u;
   float f[4];
